@@ -24,6 +24,12 @@
  *   pe_argmax          the LM head fused with a per-row greedy argmax.
  *   pe_verify_greedy   the target's greedy verification of the drafts, which
  *                      yields the next step's accepted counts and bonus tokens.
+ *   pe_verify_sampled  the same at a temperature: rejection sampling of the drafts
+ *                      against the target's probabilities, from given numbers.
+ *   pe_qkv_append, pe_chunk_attention
+ *                      the paged cache write (with per-head norms and RoPE) and
+ *                      attention over the pages for rows outside a draft step:
+ *                      prompts, chunks of prompts, the target's verify rows.
  *   pe_draft_autoregressive
  *                      the K-pass autoregressive drafting the parallel step
  *                      replaces, on the same kernels (the baseline).
@@ -88,10 +94,15 @@ extern "C" {
 #define PE_ST_TOKEN_RANGE 0x4u    /* token id outside [0, V): embedding row 0 is used */
 #define PE_ST_ROWS_RANGE 0x8u     /* pe_verify_greedy: qsl is not a non-decreasing run
                                      from 0 to T_in (each request is clamped to
-                                     the rows in range); pe_draft_step with
-                                     several layers: a request has more
-                                     non-rejected rows than the layers carry */
+                                     the rows in range); pe_verify_sampled and
+                                     pe_chunk_attention: from 0 to at most T;
+                                     pe_draft_step with several layers: a request
+                                     has more non-rejected rows than the layers
+                                     carry */
 #define PE_ST_TIMEOUT 0x10u       /* a bounded wait inside a kernel expired */
+#define PE_ST_SAMPLING 0x40u      /* pe_verify_sampled: a temperature that is negative
+                                     or NaN (read as 0), or a bonus token due from a
+                                     row without a distribution (bonus -1) */
 #define PE_ST_CAPACITY 0x20u      /* COD calls: a sequence length outside [0, S_max]
                                      (clamped), a mask larger than its row capacity
                                      or row stride (rows / columns past it are not
@@ -387,6 +398,138 @@ int pe_verify_greedy(int B, int T_in, const int32_t* qsl, const int32_t* tok,
                      const void* logits, int vocab, int dtype, int32_t* target_tok,
                      int32_t* accepted, int32_t* bonus, void* ws, size_t ws_bytes,
                      void* stream);
+
+/* Verification of greedy drafts by sampling: the temperature > 0 counterpart of
+ * pe_verify_greedy.  "Attention Drift", section 2 (preliminaries): the target
+ * applies rejection sampling against its own distribution and accepts the
+ * longest valid prefix.  The drafts of pe_argmax are greedy, so the draft
+ * distribution is a point mass and rejection sampling reads: draft x after row j
+ * is accepted with probability p_j(x), p_j = softmax(logits_j / temperature), and
+ * the token after the accepted prefix is drawn from p_a, without the draft that
+ * was rejected there.  Every random number is an input.  Needs no handle.
+ *   qsl[B+1], tok[T_in], logits[T_in][vocab], dtype: as for pe_verify_greedy,
+ *                  but qsl[B] may be below T_in (a padded batch): rows from
+ *                  qsl[B] on belong to no request and are neither used nor written
+ *   temperature[B] float, nullable (NULL: 1 for every request).  0: the request is
+ *                  greedy (pe_verify_greedy's rules; its numbers are not read).
+ *                  Negative or NaN: read as 0, PE_ST_SAMPLING
+ *   u[T_in]        float uniform numbers in [0, 1): u of row j >= 1 of a request
+ *                  decides its draft j (row 0's entry is not read)
+ *   gumbel[B][vocab] float standard Gumbel noise, -log(E) of exponential draws E
+ *   accepted[B]    out: a_r = the largest m <= n_r - 1 with u_j < p_{j-1}(tok_j) for
+ *                  every j = 1..m (rows j of the request)
+ *   bonus[B]       out: argmax over tokens v of logits_a[v] / temperature +
+ *                  gumbel[r][v], lowest index on ties, where v = the draft after
+ *                  row a_r does not compete if there is one; by the Gumbel-max
+ *                  property a draw from p_a, or from p_a without that draft.
+ *                  Scores are formed in fp32 and the best of each thread compared in
+ *                  64 bits: two scores within a few fp32 roundings may trade places
+ *   p_draft[T_in]  out, float, nullable: p_{j-1}(tok_j) of each row j >= 1 (for a
+ *                  greedy request 1 or 0), also past the accepted prefix; 1 for
+ *                  a request's row 0
+ *   ws             pe_verify_sampled_workspace_bytes(B, T_in, vocab) bytes or more,
+ *                  256-byte aligned; its first word is the status word
+ * A logit of -inf has probability 0.  A row with a NaN or a +inf logit, or with
+ * nothing but -inf, has no distribution: p_draft is 0 after it, the prefix ends
+ * there and, when the token would come from it, bonus is -1 and PE_ST_SAMPLING is
+ * set (greedy requests keep pe_verify_greedy's rule for such rows).  If the
+ * rejected draft held every finite logit, bonus is -1 too.  A draft outside [0,
+ * vocab) has probability 0 (PE_ST_TOKEN_RANGE).  A request with no rows gets
+ * accepted 0 and bonus -1.  A qsl that is not a non-decreasing run from 0 to at
+ * most T_in sets PE_ST_ROWS_RANGE; the results are then undefined (nothing outside
+ * the outputs is touched).  The call clears the status word first.  PE_ERR_ARG: negative sizes, null
+ * pointers, logits, u or gumbel not aligned to their element size, ws misaligned
+ * or too small, B = 0 with T_in > 0.  PE_ERR_UNSUPPORTED: B > 65535, or a dtype
+ * other than the two. */
+size_t pe_verify_sampled_workspace_bytes(int max_batch, int max_rows_in, int vocab);
+int pe_verify_sampled(int B, int T_in, const int32_t* qsl, const int32_t* tok, const void* logits,
+                      int vocab, int dtype, const float* temperature, const float* u,
+                      const float* gumbel, int32_t* accepted, int32_t* bonus, float* p_draft,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- paged attention calls
+ * The cache write and the attention of the draft step as calls of their own, for
+ * rows that pe_draft_step does not take: a prompt, a chunk of one, the target's
+ * verify rows.  "P-EAGLE: parallel speculative decoding in vLLM", KV cache and
+ * CUDA graphs: a paged cache addressed by slots, PADDING_SLOT_ID = -1 for rows that
+ * are not written.  The caches are those of pe_draft_step, one layer each:
+ * [num_blocks][G][block_size][hd]; slot s is offset s % block_size of block
+ * s / block_size (pe_meta.slot).  Both calls need no handle.
+ *
+ * A pe_attn_plan is a plain host struct without resources: the layer's shape and
+ * its RoPE frequencies.  pe_attn_plan_init fills it; copies are fine.  It may be
+ * used by several calls and streams at once. */
+typedef struct pe_attn_plan {
+  int32_t n_heads;    /* H */
+  int32_t n_kv_heads; /* G; query head h reads KV head h / (H/G) */
+  int32_t head_dim;   /* hd */
+  int32_t block_size; /* tokens per block */
+  int32_t dtype;      /* PE_DTYPE_F32 or PE_DTYPE_BF16 */
+  float eps;          /* epsilon of the q and k norms */
+  uint64_t rope_turn[64]; /* theta^(-2i/hd) / (2 pi) as a 64-bit fraction of a turn */
+} pe_attn_plan;
+
+/* PE_ERR_UNSUPPORTED: H not a multiple of G, H / G > 128, hd not a multiple of 8 or
+ * above 128 (bf16: 64 or 128), block_size < 1, eps negative or NaN, rope_theta not
+ * positive, another dtype.  PE_ERR_ARG: plan is NULL.  On an error *plan is zeroed
+ * and every call refuses it. */
+int pe_attn_plan_init(pe_attn_plan* plan, int n_heads, int n_kv_heads, int head_dim,
+                      int block_size, int dtype, float eps, float rope_theta);
+
+/* Norm, rotation and cache write of T rows in one pass.
+ *   qkv      [T][H + 2G][hd] in the plan's dtype: q heads, then k, then v heads
+ *            (the order of w_qkv); consecutive rows ld_qkv elements apart
+ *   gamma_q, gamma_k  [hd] gains of the per-head RMS norms, each nullable (NULL: no
+ *            norm): y = x * gamma / sqrt(mean(x^2) + eps), in fp32
+ *   pos[T]   int64 positions; the pair (y_i, y_{i+hd/2}) turns by
+ *            pos * theta^(-2i/hd) (q and k heads; v heads are copied)
+ *   slot[T]  int64 cache slots.  Negative: the row's k and v are not written (its q
+ *            is).  num_blocks * block_size or more: the same, and PE_ST_BLOCK_RANGE
+ *   q_out    [T][H][hd] dense, nullable (NULL: only the cache is written)
+ *   k_cache, v_cache  as above; slots that no row names keep their bytes
+ *   ws       256 bytes or more, 256-byte aligned: the status word, which this call
+ *            does not clear (zero it once; pe_read_status clears it)
+ * Each result is rounded once, from fp32, to the plan's dtype.  The slots >= 0 of a
+ * call must differ: where two rows name one slot, it is undefined which row's k and
+ * v vectors stay.  q_out, the caches and qkv must not overlap.  T = 0 is a no-op.
+ * PE_ERR_ARG: a plan pe_attn_plan_init did not fill, negative T or num_blocks, ld_qkv
+ * below (H + 2G) hd or not a multiple of 8 elements, null pointers, tensors not
+ * 16-byte aligned, pos or slot not 8-byte aligned, ws misaligned or too small. */
+int pe_qkv_append(const pe_attn_plan* plan, int T, const void* qkv, int64_t ld_qkv,
+                  const void* gamma_q, const void* gamma_k, const int64_t* pos,
+                  const int64_t* slot, int num_blocks, void* q_out, void* k_cache, void* v_cache,
+                  void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of each request's new rows over its pages.
+ *   qsl[B+1]    int32 row offsets: request r owns rows qsl[r] .. qsl[r+1]-1 (n_r >= 0
+ *               rows); qsl[0] = 0, qsl[B] <= T.  Rows from qsl[B] on are neither read
+ *               nor written
+ *   seq_len[B]  int32 cache positions of the request after this chunk: its row j is
+ *               at position seq_len[r] - n_r + j and sees every position up to its
+ *               own (from 0).  The caches already hold the chunk's keys and values
+ *   q           [T][H][hd] in the plan's dtype, rows ld_q elements apart
+ *   block_table [B][max_blocks], num_blocks: as for pe_draft_step
+ *   sink[H]     float, nullable: per-head sink logits (pe_weights.attn_sink)
+ *   out         [T][H][hd] in the plan's dtype, rows ld_out elements apart
+ *   ws          pe_chunk_attention_workspace_bytes(plan, B, T) bytes or more,
+ *               256-byte aligned; its first word is the status word (cleared first)
+ * Scores are scaled by 1/sqrt(hd); the softmax and its sums are fp32.  A row whose
+ * position is negative (seq_len[r] < n_r) or whose keys all lie in invalid blocks
+ * sees nothing and gets zeros.  What the caches hold at positions past seq_len[r],
+ * or in blocks that are skipped, is never used, NaN included.
+ * seq_len outside [0, max_blocks * block_size] is clamped, a block id outside [0,
+ * num_blocks) skips its keys: PE_ST_BLOCK_RANGE.  A qsl that is not a non-decreasing
+ * run from 0 to at most T sets PE_ST_ROWS_RANGE; the rows of out are then undefined
+ * (nothing outside them is touched).
+ * T = 0 or B = 0 writes no output.  PE_ERR_ARG: as for pe_qkv_append (strides at
+ * least H * hd and multiples of 8 elements; max_blocks < 1).  PE_ERR_UNSUPPORTED:
+ * B > 65535, or caches of 2^31 or more rows (num_blocks * G * block_size). */
+size_t pe_chunk_attention_workspace_bytes(const pe_attn_plan* plan, int max_batch, int max_rows);
+int pe_chunk_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qsl,
+                       const int32_t* seq_len, const void* q, int64_t ld_q, const void* k_cache,
+                       const void* v_cache, const int32_t* block_table, int max_blocks,
+                       int num_blocks, const float* sink, void* out, int64_t ld_out, void* ws,
+                       size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- COD training indices
  * "[RFC]: Add random anchor for p-eagle first position": the training-side

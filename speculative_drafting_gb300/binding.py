@@ -26,6 +26,7 @@ PE_ST_TOKEN_RANGE = 0x4
 PE_ST_ROWS_RANGE = 0x8
 PE_ST_TIMEOUT = 0x10
 PE_ST_CAPACITY = 0x20
+PE_ST_SAMPLING = 0x40
 PE_COD_MAX_DEPTH = 16
 PE_DTYPE_F32 = 0
 PE_DTYPE_BF16 = 1
@@ -70,6 +71,13 @@ META_FIELDS = ["out_qsl", "tok", "pos", "is_rejected", "is_masked", "hidden_src"
 
 class PeMeta(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in META_FIELDS]
+
+
+class PeAttnPlan(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("rope_turn", ctypes.c_uint64 * 64)]
 
 
 _lib = None
@@ -137,6 +145,22 @@ def load(path: str | None = None):
     lib.pe_cod_mask.argtypes = [_i32, _i32, _vp, _i32, _vp, _vp, _vp, ctypes.c_int64,
                                 ctypes.c_int64, ctypes.c_int64, _vp, _sz, _vp]
     lib.pe_cod_mask.restype = _i32
+    lib.pe_verify_sampled_workspace_bytes.argtypes = [_i32, _i32, _i32]
+    lib.pe_verify_sampled_workspace_bytes.restype = _sz
+    lib.pe_verify_sampled.argtypes = [_i32, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp,
+                                      _vp, _vp, _vp, _sz, _vp]
+    lib.pe_verify_sampled.restype = _i32
+    lib.pe_attn_plan_init.argtypes = [_vp, _i32, _i32, _i32, _i32, _i32, ctypes.c_float,
+                                      ctypes.c_float]
+    lib.pe_attn_plan_init.restype = _i32
+    lib.pe_qkv_append.argtypes = [_vp, _i32, _vp, ctypes.c_int64, _vp, _vp, _vp, _vp, _i32, _vp,
+                                  _vp, _vp, _vp, _sz, _vp]
+    lib.pe_qkv_append.restype = _i32
+    lib.pe_chunk_attention_workspace_bytes.argtypes = [_vp, _i32, _i32]
+    lib.pe_chunk_attention_workspace_bytes.restype = _sz
+    lib.pe_chunk_attention.argtypes = [_vp, _i32, _i32, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp,
+                                       _vp, _i32, _i32, _vp, _vp, ctypes.c_int64, _vp, _sz, _vp]
+    lib.pe_chunk_attention.restype = _i32
     _lib = lib
     return lib
 
@@ -161,6 +185,17 @@ def _stream(stream):
 
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _addr(t):
+    # a plain integer: ctypes converts it to the void* argument without an object
+    return None if t is None else t.data_ptr()
+
+
+def _stream_handle(stream):
+    import torch
+
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
 def _check(rc, what):
@@ -374,6 +409,83 @@ def read_status_ws(ws, clear=True, stream=None):
     if rc not in (PE_OK, PE_ERR_DEVICE_INPUT, PE_ERR_TIMEOUT):
         raise PeError(rc, "pe_read_status")
     return int(v.value), rc
+
+
+def verify_sampled_workspace(max_batch: int, max_rows_in: int, vocab: int, device="cuda"):
+    """A device workspace for pe_verify_sampled (torch allocates it 256-byte aligned)."""
+    import torch
+
+    n = int(load().pe_verify_sampled_workspace_bytes(int(max_batch), int(max_rows_in), int(vocab)))
+    if n == 0:
+        raise PeError(PE_ERR_ARG, "pe_verify_sampled_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def verify_sampled(B, T_in, qsl, tok, logits, vocab, dtype, temperature, u, gumbel, accepted, bonus,
+                   p_draft, ws, stream=None):
+    """pe_verify_sampled on device tensors; dtype is PE_DTYPE_F32 or PE_DTYPE_BF16;
+    temperature and p_draft may be None."""
+    rc = load().pe_verify_sampled(B, T_in, _addr(qsl), _addr(tok), _addr(logits), vocab, dtype,
+                                  _addr(temperature), _addr(u), _addr(gumbel), _addr(accepted),
+                                  _addr(bonus), _addr(p_draft), _addr(ws), ws.numel(),
+                                  _stream_handle(stream))
+    _check(rc, "pe_verify_sampled")
+
+
+# ----------------------------------------------------------------------------- paged attention calls
+
+
+class PagedAttention:
+    """The paged cache write and attention of one layer shape (a pe_attn_plan): rows
+    outside a draft step, such as prompts, chunks of prompts and verify rows.
+    dtype is "bf16" or "f32"; caches are [num_blocks][G][block_size][hd]."""
+
+    def __init__(self, n_heads, n_kv_heads, head_dim, block_size, dtype="bf16", eps=1e-6,
+                 rope_theta=10000.0):
+        self.lib = load()
+        self.c = PeAttnPlan()
+        self.addr = ctypes.addressof(self.c)
+        self.qkv_width = (n_heads + 2 * n_kv_heads) * head_dim
+        _check(self.lib.pe_attn_plan_init(self.addr, n_heads, n_kv_heads, head_dim, block_size,
+                                          PE_DTYPE_BF16 if dtype == "bf16" else PE_DTYPE_F32,
+                                          eps, rope_theta), "pe_attn_plan_init")
+
+    def append_workspace(self, device="cuda"):
+        """The status word of ``append`` (zeroed)."""
+        import torch
+
+        return torch.zeros(256, dtype=torch.uint8, device=device)
+
+    def workspace(self, max_batch: int, max_rows: int, device="cuda"):
+        """A device workspace for ``attend`` with at most max_batch requests and max_rows rows."""
+        import torch
+
+        n = int(self.lib.pe_chunk_attention_workspace_bytes(self.addr, int(max_batch),
+                                                            int(max_rows)))
+        if n == 0:
+            raise PeError(PE_ERR_ARG, "pe_chunk_attention_workspace_bytes")
+        return torch.zeros(n, dtype=torch.uint8, device=device)
+
+    def append(self, T, qkv, gamma_q, gamma_k, pos, slot, num_blocks, q_out, k_cache, v_cache, ws,
+               stream=None):
+        """pe_qkv_append: qkv [T][H + 2G][hd] (or [T][(H + 2G) hd]; its rows may be
+        strided), gains and q_out may be None."""
+        rc = self.lib.pe_qkv_append(self.addr, T, _addr(qkv), qkv.stride(0), _addr(gamma_q),
+                                    _addr(gamma_k), _addr(pos), _addr(slot), num_blocks,
+                                    _addr(q_out), _addr(k_cache), _addr(v_cache), _addr(ws),
+                                    ws.numel(), _stream_handle(stream))
+        _check(rc, "pe_qkv_append")
+
+    def attend(self, B, T, qsl, seq_len, q, k_cache, v_cache, block_table, num_blocks, out, ws,
+               sink=None, stream=None):
+        """pe_chunk_attention: q and out [T][H][hd] (or [T][H hd]; their rows may be
+        strided)."""
+        rc = self.lib.pe_chunk_attention(self.addr, B, T, _addr(qsl), _addr(seq_len), _addr(q),
+                                         q.stride(0), _addr(k_cache), _addr(v_cache),
+                                         _addr(block_table), block_table.shape[1], num_blocks,
+                                         _addr(sink), _addr(out), out.stride(0), _addr(ws),
+                                         ws.numel(), _stream_handle(stream))
+        _check(rc, "pe_chunk_attention")
 
 
 # ----------------------------------------------------------------------------- COD training indices

@@ -1,0 +1,42 @@
+// Host-side checks and launch interfaces of the paged attention calls.
+#pragma once
+
+#include "pe_internal.h"
+
+namespace pe {
+
+// Whether pe_attn_plan_init filled this plan (its shape fields are in range).
+bool plan_ok(const pe_attn_plan* p);
+
+// One call of pe_chunk_attention, as its kernels take it.
+struct ChunkArgs {
+  int B, T, H, G, hd, bs, max_blocks, num_blocks;
+  const int32_t* qsl;
+  const int32_t* seq_len;
+  const void* q;
+  int64_t ld_q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_table;
+  const float* sink;
+  void* out;
+  int64_t ld_out;
+  uint32_t* status;
+};
+
+// Rows [q0, q1) of request r, clamped to [0, T]; bad: qsl is not a
+// non-decreasing run from 0 to at most T.
+struct RowRange {
+  int q0, q1;
+  bool bad;
+};
+__device__ __forceinline__ RowRange request_rows(const int32_t* qsl, int r, int T) {
+  RowRange x;
+  const int a = qsl[r], b = qsl[r + 1];
+  x.bad = a < 0 || b > T || b < a || (r == 0 && a != 0);
+  x.q0 = min(max(a, 0), T);
+  x.q1 = min(max(b, x.q0), T);
+  return x;
+}
+
+}  // namespace pe
