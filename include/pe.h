@@ -512,7 +512,8 @@ int pe_qkv_append(const pe_attn_plan* plan, int T, const void* qkv, int64_t ld_q
  *   sink[H]     float, nullable: per-head sink logits (pe_weights.attn_sink)
  *   out         [T][H][hd] in the plan's dtype, rows ld_out elements apart
  *   ws          pe_chunk_attention_workspace_bytes(plan, B, T) bytes or more,
- *               256-byte aligned; its first word is the status word (cleared first)
+ *               256-byte aligned; its first word is the status word, which this call
+ *               does not clear (zero it once; pe_read_status clears it)
  * Scores are scaled by 1/sqrt(hd); the softmax and its sums are fp32.  A row whose
  * position is negative (seq_len[r] < n_r) or whose keys all lie in invalid blocks
  * sees nothing and gets zeros.  What the caches hold at positions past seq_len[r],
@@ -521,9 +522,10 @@ int pe_qkv_append(const pe_attn_plan* plan, int T, const void* qkv, int64_t ld_q
  * num_blocks) skips its keys: PE_ST_BLOCK_RANGE.  A qsl that is not a non-decreasing
  * run from 0 to at most T sets PE_ST_ROWS_RANGE; the rows of out are then undefined
  * (nothing outside them is touched).
- * T = 0 or B = 0 writes no output.  PE_ERR_ARG: as for pe_qkv_append (strides at
+ * T = 0 or B = 0 is a no-op.  PE_ERR_ARG: as for pe_qkv_append (strides at
  * least H * hd and multiples of 8 elements; max_blocks < 1).  PE_ERR_UNSUPPORTED:
- * B > 65535, or caches of 2^31 or more rows (num_blocks * G * block_size). */
+ * B > 65535, caches of 2^31 or more rows (num_blocks * G * block_size), T * H or
+ * max_blocks * block_size past 2^31 - 256. */
 size_t pe_chunk_attention_workspace_bytes(const pe_attn_plan* plan, int max_batch, int max_rows);
 int pe_chunk_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qsl,
                        const int32_t* seq_len, const void* q, int64_t ld_q, const void* k_cache,

@@ -107,7 +107,7 @@ using namespace pe;
 extern "C" size_t pe_chunk_attention_workspace_bytes(const pe_attn_plan* plan, int max_batch,
                                                      int max_rows) {
   if (!plan_ok(plan) || max_batch < 0 || max_rows < 0) return 0;
-  return 256;
+  return chunk_tc_takes(plan) ? chunk_tc_workspace(plan, max_rows) : 256;
 }
 
 extern "C" int pe_chunk_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qsl,
@@ -120,7 +120,9 @@ extern "C" int pe_chunk_attention(const pe_attn_plan* plan, int B, int T, const 
   if (!plan_ok(plan) || B < 0 || T < 0 || max_blocks < 1 || num_blocks < 0) return PE_ERR_ARG;
   const int64_t width = static_cast<int64_t>(plan->n_heads) * plan->head_dim;
   if (ld_q < width || ld_out < width || ld_q % 8 || ld_out % 8) return PE_ERR_ARG;
-  if (B > 65535) return PE_ERR_UNSUPPORTED;
+  if (B > 65535 || static_cast<int64_t>(T) * plan->n_heads > 0x7fffffff ||
+      static_cast<int64_t>(max_blocks) * plan->block_size > 0x7fffff00)
+    return PE_ERR_UNSUPPORTED;
   if (static_cast<double>(num_blocks) * plan->n_kv_heads * plan->block_size >= 2147483648.0)
     return PE_ERR_UNSUPPORTED;
   if (!ws || !aligned(ws, 256) || ws_bytes < pe_chunk_attention_workspace_bytes(plan, B, T))
@@ -133,7 +135,6 @@ extern "C" int pe_chunk_attention(const pe_attn_plan* plan, int B, int T, const 
     if (!aligned(qsl, 4) || !aligned(seq_len, 4) || !aligned(block_table, 4) || !aligned(sink, 4))
       return PE_ERR_ARG;
   }
-  if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return PE_ERR_CUDA;
   if (B == 0 || T == 0) return PE_OK;
   ChunkArgs a = {};
   a.B = B;
@@ -155,6 +156,7 @@ extern "C" int pe_chunk_attention(const pe_attn_plan* plan, int B, int T, const 
   a.out = out;
   a.ld_out = ld_out;
   a.status = static_cast<uint32_t*>(ws);
+  if (chunk_tc_takes(plan) && num_blocks > 0) return launch_chunk_tc(a, static_cast<char*>(ws), st);
   const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(plan->n_heads));
   const cudaError_t e = plan->dtype == PE_DTYPE_BF16
                             ? launch_pdl(chunk_simt_kernel<bf16>, grid, dim3(128), 0, st, a)

@@ -1,0 +1,897 @@
+// Attention of each request's new rows over its pages on the tensor cores (bf16,
+// head size 64 or 128, blocks of a multiple of 8 keys).
+//
+//   S = Q K^T, P = exp(S / sqrt(hd) - m), l = sum P, O = P V, out = O / l
+//
+// in one pass over 128-key tiles with a running maximum m per row; S, P and O live
+// in tensor memory, K and V come by TMA, page by page.
+//
+// The rows of a request that share a KV head (n_r tokens x H/G heads, token-major)
+// are cut into units of up to 256 rows.  One CTA works on one unit at a time with
+// two streams of 128 rows, each with its own softmax warpgroup (one thread per
+// row), so that one stream's products run while the other's exponentials do:
+//   wide unit   (129..256 rows): stream s holds rows 128 s ..; both read every tile;
+//   narrow unit (at most 128 rows: verify rows, single tokens): both streams hold
+//               the same rows and take the tiles in turn; their (m, l, O) join at
+//               the end through tensor memory.
+//
+// Work split.  The units of all KV heads form one line, each as long as its cost
+// (rows in use x keys, plus a constant); CTA c takes the c-th of equal pieces, cut
+// at tiles.  A unit cut between CTAs leaves unnormalised partials (m, l, O) in the
+// workspace, at most two per CTA, and a second kernel joins them.  Every CTA finds
+// its piece itself from qsl and seq_len, so the host needs no lengths.
+//
+// Warps: 0-3 softmax of stream 0, 4-7 of stream 1, 8 TMA and unit list, 9 MMA.
+#include "pe_paged.h"
+#include "pe_tmem.cuh"
+
+namespace pe {
+namespace {
+
+constexpr int kThreads = 384;  // three warpgroups; warps 10 and 11 only lend their registers
+constexpr int kTile = 128;        // keys per tile, rows per stream
+constexpr int kUnitRows = 256;
+constexpr int kItems = 4;         // unit descriptors in flight
+constexpr int kMasks = 16;        // tile masks in flight
+constexpr float kLog2e = 1.4426950408889634f;
+// The running maximum is raised only when a row's new one is more than 2^8 above
+// it: P stays below 2^8 (exact in the fp32 sums), and O is rarely rescaled.
+constexpr float kLazy = 8.f;
+
+template <int HD>
+struct Shape {
+  static constexpr int kHalves = HD / 64;             // 128-byte columns of a row
+  static constexpr int kTileBytes = kTile * HD * 2;   // K, V or Q tile
+  // ring slots (one K or V tile each): 160 KB for 64, 128 KB for 128
+  static constexpr int kSlots = HD == 64 ? 10 : 4;
+  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024;
+  // Steps whose S product may be issued before their P V: with head size 64, P has
+  // tensor memory of its own and S is free as soon as it is in registers; with 128
+  // P takes the place of S, which is free after P V.
+  static constexpr int kAhead = HD == 64 ? 4 : 2;
+  static constexpr uint32_t kS = 0, kP = HD == 64 ? 256 : 0, kPStride = HD == 64 ? 64 : 128;
+  static constexpr uint32_t kO = HD == 64 ? 384 : 256;
+};
+
+struct Req {
+  int q0, n, L, R, Q;
+  long long A;
+};
+
+// A place on the line of units: tile `tile` of unit `qt` of request r, KV head g.
+struct Place {
+  int g, r, qt, tile;
+};
+
+struct Unit {
+  int r, g, q0, n, L;   // request, KV head, first row, rows, keys
+  int row0, rows, wide; // first packed row, packed rows (1..256)
+  int tile0, tile1;     // key tiles of this CTA's part
+  int kend;             // keys any row of the unit sees
+  int whole;            // the part is the whole unit
+};
+
+// The TMA warp's walk over a unit's boxes, 32 at a time, one per lane: the window's
+// number, this lane's cache row (-1: none) and its block id in the next window.
+struct Window {
+  int n, row, next;
+};
+
+struct TcArgs {
+  ChunkArgs c;
+  int box;          // keys per TMA box
+  int grid;
+  int umin;         // least cost of a CTA's piece, in 128-key tiles of a narrow unit
+  int overhead;     // constant cost of a unit, in the same measure
+  float* part_o;    // [grid][2][part_rows][hd]
+  float* part_ml;   // [grid][2][part_rows][2]
+  int part_rows;
+  int* rec;         // [grid][8]: head code, then the tail: valid, q0, g, row0, rows
+};
+
+PE_DEV Req load_req(const ChunkArgs& a, int r, bool report) {
+  const RowRange x = request_rows(a.qsl, r, a.T);
+  Req q;
+  q.q0 = x.q0;
+  q.n = x.q1 - x.q0;
+  const long long Lmax = static_cast<long long>(a.max_blocks) * a.bs;
+  const int L = a.seq_len[r];
+  const bool over = L < 0 || L > Lmax;
+  q.L = over ? static_cast<int>(min(max(static_cast<long long>(L), 0ll), Lmax)) : L;
+  if (report && (x.bad || over))
+    set_status(a.status, (x.bad ? PE_ST_ROWS_RANGE : 0u) | (over ? PE_ST_BLOCK_RANGE : 0u));
+  const int HG = a.H / a.G;
+  q.R = q.n * HG;
+  q.Q = (q.R + kUnitRows - 1) / kUnitRows;
+  q.A = static_cast<long long>(max(q.L - q.n, 0)) * HG;
+  return q;
+}
+
+// keys that some row of unit i sees, and their tiles (at least one)
+PE_DEV int unit_kend(const Req& q, int i, int HG) {
+  const int last = (min((i + 1) * kUnitRows, q.R) - 1) / HG;
+  return min(max(q.L - q.n + last + 1, 0), q.L);
+}
+PE_DEV int unit_tiles(int kend) { return max(1, (kend + kTile - 1) / kTile); }
+
+// cost of unit i, and of the units before it (all but the last are wide)
+PE_DEV long long unit_cost(const Req& q, int i, long long ov) {
+  const int end = min((i + 1) * kUnitRows, q.R);
+  return (end - i * kUnitRows > kTile ? 2 : 1) * (q.A + end) + ov;
+}
+PE_DEV long long units_before(const Req& q, int i, long long ov) {
+  return i * (2 * q.A + ov) + 256ll * i * (i + 1);
+}
+PE_DEV long long req_cost(const Req& q, long long ov) {
+  return q.Q == 0 ? 0 : units_before(q, q.Q - 1, ov) + unit_cost(q, q.Q - 1, ov);
+}
+
+// the first request at or after r that has rows (B if none), by one whole warp
+PE_DEV int next_request(const ChunkArgs& a, int r, int lane) {
+  for (; r < a.B; r += 32) {
+    int n = 0;
+    if (r + lane < a.B) {
+      const RowRange x = request_rows(a.qsl, r + lane, a.T);
+      n = x.q1 - x.q0;
+    }
+    const unsigned any = __ballot_sync(0xffffffffu, n > 0);
+    if (any) return r + __ffs(any) - 1;
+  }
+  return a.B;
+}
+
+PE_DEV uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+PE_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_tc_kernel(const __grid_constant__ CUtensorMap kmap,
+                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TcArgs p) {
+  using S = Shape<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t kv_full[S::kSlots], kv_empty[S::kSlots];
+  __shared__ __align__(8) uint64_t it_full[kItems], it_empty[kItems];
+  __shared__ __align__(8) uint64_t q_full[2], s_full[2], s_free[2], p_full[2], pv_done[2], x_bar[2];
+  __shared__ __align__(8) uint64_t end_bar;
+  __shared__ Unit items[kItems];
+  __shared__ uint32_t mask_sh[kMasks];  // per tile: bit j = keys 8j..8j+7 were loaded
+  __shared__ float ml_sh[2][kTile][2];
+  __shared__ long long scan_sh[kThreads / 32];
+  __shared__ Place place_sh[2];
+  __shared__ uint32_t tmem_sh;
+  __shared__ int abort_sh;
+  const ChunkArgs& a = p.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* q_sm = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* ring = q_sm + 2 * S::kTileBytes;
+  const int HG = a.H / a.G;
+
+  if (tid == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&it_full[i], 1);
+      mbar_init(&it_empty[i], 2 * kTile + 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], kTile);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&s_free[s], kTile);
+      mbar_init(&p_full[s], kTile);
+      mbar_init(&pv_done[s], 1);
+      mbar_init(&x_bar[s], 2 * kTile);
+    }
+    mbar_init(&end_bar, 1);
+    abort_sh = 0;
+    fence_barrier_init();
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+  }
+  // tensor memory before the next kernel may start: a successor's CTA that held
+  // some of it while waiting for this grid would keep this one from starting
+  if (warp == 9) {
+    tmem_alloc(&tmem_sh, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  pdl_trigger();
+  pdl_wait();
+
+  // ---------------- this CTA's piece of the line
+  const long long ov = static_cast<long long>(p.overhead) * kTile * HG;
+  const int per = (a.B + kThreads - 1) / kThreads;  // requests per thread
+  const int r_lo = min(tid * per, a.B), r_hi = min(r_lo + per, a.B);
+  long long mine = 0;
+  for (int r = r_lo; r < r_hi; ++r) mine += req_cost(load_req(a, r, blockIdx.x == 0), ov);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) scan_sh[warp] = incl;
+  if (tid < 2) place_sh[tid] = Place{a.G, 0, 0, 0};  // the end of the line
+  __syncthreads();
+  long long before = incl - mine, Wg = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += scan_sh[w];
+    Wg += scan_sh[w];
+  }
+  const long long W = Wg * a.G;
+  const long long least = static_cast<long long>(p.umin) * kTile * HG + ov;
+  const int pieces = static_cast<int>(min(max(W / least, 1ll), static_cast<long long>(p.grid)));
+  const bool idle = W == 0 || static_cast<int>(blockIdx.x) >= pieces;
+  if (!idle) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int c = blockIdx.x + e;
+      // c W / pieces without leaving 64 bits
+      const long long w = c >= pieces ? W : W / pieces * c + W % pieces * c / pieces;
+      if (w >= W) continue;
+      const int g = static_cast<int>(w / Wg);
+      long long rem = w - g * Wg - before;
+      if (rem < 0 || rem >= mine) continue;
+      for (int r = r_lo; r < r_hi; ++r) {
+        const Req q = load_req(a, r, false);
+        const long long cost = req_cost(q, ov);
+        if (rem >= cost) {
+          rem -= cost;
+          continue;
+        }
+        int lo = 0, hi = q.Q;  // the last unit that starts at or before rem
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (units_before(q, mid, ov) <= rem) lo = mid; else hi = mid;
+        }
+        const long long off = rem - units_before(q, lo, ov);
+        const int kt = unit_tiles(unit_kend(q, lo, HG));
+        place_sh[e] = Place{g, r, lo, static_cast<int>(off * kt / unit_cost(q, lo, ov))};
+        break;
+      }
+    }
+  }
+  __syncthreads();
+
+  volatile int* abort_flag = &abort_sh;
+  auto fail = [&]() {
+    abort_sh = 1;
+    set_status(a.status, PE_ST_TIMEOUT);
+  };
+
+  // the whole warp goes on or gives up together (what follows is .aligned)
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
+  };
+
+  if (idle) {
+    if (tid == 0) p.rec[blockIdx.x * 8] = p.rec[blockIdx.x * 8 + 1] = 0;
+  } else if (warp < 8) {
+    // registers: 384 x 168 at launch = 2 x 128 x 216 + 128 x 72
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // ---------------- softmax warpgroups: one thread per row
+    const int s = warp >> 2, wq = warp & 3, i = tid & (kTile - 1);
+    const uint32_t tm = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t tS = tm + S::kS + s * 128, tP = tm + S::kP + s * S::kPStride;
+    const float sc = kLog2e / sqrtf(static_cast<float>(HD));
+    uint32_t n_items = 0, n_st = 0, loads = 0, tiles = 0, n_x = 0;
+    bool go = true;
+    while (go) {
+      const int slot = n_items % kItems;
+      if (!wait_warp(&it_full[slot], (n_items / kItems) & 1)) {
+        fail();
+        break;
+      }
+      const Unit u = items[slot];
+      mbar_arrive(&it_empty[slot]);
+      ++n_items;
+      if (u.r < 0) break;
+      const int nt = u.tile1 - u.tile0;
+      const int rel = u.wide ? s * kTile + i : i;  // row within the unit
+      const bool row_ok = rel < u.rows;
+      const bool live = (rel & ~31) < u.rows;      // some row of this warp exists
+      const int R = u.row0 + (row_ok ? rel : 0);
+      const int tok = R / HG, head = u.g * HG + R % HG;
+      const int lim = row_ok ? u.L - u.n + tok : -1;           // last key this row sees
+      const int lim0 = u.L - u.n + u.row0 / HG;                // ... the unit's first row
+      // Q: this row into shared memory, 128-byte swizzle
+      if (u.wide || s == 0) {
+        uint8_t* dst = q_sm + (u.wide ? s : 0) * S::kTileBytes + i * 128;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const bf16*>(a.q) + (u.q0 + tok) * a.ld_q + static_cast<long long>(head) * HD);
+        uint4 v[HD / 8];
+#pragma unroll
+        for (int ch = 0; ch < HD / 8; ++ch) v[ch] = row_ok ? src[ch] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int ch = 0; ch < HD / 8; ++ch)
+          *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kTile * 128) + (((ch & 7) ^ (i & 7)) << 4)) = v[ch];
+        fence_proxy_async();
+        mbar_arrive(&q_full[u.wide ? s : 0]);
+      }
+      const int ahead = u.wide ? S::kAhead / 2 : S::kAhead;
+      const int mysteps = u.wide ? nt : (nt - s + 1) >> 1;
+      float m = -INFINITY, l = 0.f;  // m: running maximum in units of log2
+      for (int k = 0; k < mysteps; ++k) {
+        const int j = u.wide ? k : 2 * k + s;
+        const int t0 = (u.tile0 + j) * kTile;
+        if (!wait_warp(&s_full[s], (n_st + k) & 1)) {
+          go = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t have = mask_sh[(tiles + j) % kMasks];
+        const bool inner = t0 + kTile - 1 <= lim0 && have == 0xffffu;
+        uint32_t x[kTile];
+        if (live) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) tmem_ld32_issue(tS + 32 * b, x + 32 * b);
+          tmem_wait_ld();
+#pragma unroll
+          for (int b = 0; b < 4; ++b) tmem_use32(x + 32 * b);
+        }
+        if (S::kAhead == 4) {
+          tc_fence_before();
+          mbar_arrive(&s_free[s]);
+        }
+        if (live) {
+          if (!inner) {
+#pragma unroll
+            for (int c = 0; c < kTile; ++c)
+              if (t0 + c > lim || !(have >> (c >> 3) & 1u)) x[c] = 0xff800000u;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < kTile; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+          // raise the maximum: at the first finite score, or when it climbed far
+          const bool raise = top > m + kLazy || (m == -INFINITY && top > m);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float mn = raise ? top : m;
+            const float f = (m == -INFINITY) ? 1.f : ex2(m - mn);
+            m = mn;
+            l *= f;
+            if (k > 0) {
+              if (!wait_warp(&pv_done[s], (n_st + k - 1) & 1)) {
+                go = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll
+              for (int b = 0; b < HD / 32; ++b) {
+                uint32_t o[32];
+                tmem_ld32_issue(tm + S::kO + s * HD + 32 * b, o);
+                tmem_wait_ld();
+                tmem_use32(o);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                tmem_st32_issue(tm + S::kO + s * HD + 32 * b, o);
+              }
+              tmem_wait_st();
+            }
+          }
+          const float off = m == -INFINITY ? 0.f : m;
+          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < kTile; c += 2) {
+            const float p0 = ex2(fmaf(__uint_as_float(x[c]), sc, -off));
+            const float p1 = ex2(fmaf(__uint_as_float(x[c + 1]), sc, -off));
+            ls[c & 3] += p0;
+            ls[(c & 3) + 1] += p1;
+            // P enters the product as bf16 (relative 2^-8 at most, the size of the
+            // result's own rounding); the sum l takes the unrounded weights
+            x[c >> 1] = pack_bf16x2(p0, p1);
+          }
+          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        }
+        // the last P V of this stream has read P
+        if (k > 0 && !wait_warp(&pv_done[s], (n_st + k - 1) & 1)) {
+          go = false;
+          break;
+        }
+        if (live) {
+          tc_fence_after();
+          tmem_st32_issue(tP, x);
+          tmem_st32_issue(tP + 32, x + 32);
+          tmem_wait_st();
+        }
+        // Keys that no row sees (past the unit's last, or of a skipped block) hold
+        // anything, NaN included: their V rows become 0 before the product
+        const bool cut = t0 + kTile > u.kend || have != 0xffffu;
+        if (cut && (s == 0 || !u.wide)) {
+          const uint32_t idx = loads + min(nt, ahead + j) + j;
+          if (!wait_warp(&kv_full[idx % S::kSlots], (idx / S::kSlots) & 1)) {
+            go = false;
+            break;
+          }
+          if (t0 + i >= u.kend || !(have >> (i >> 3) & 1u)) {
+            uint8_t* v = ring + (idx % S::kSlots) * S::kTileBytes + i * 128;
+#pragma unroll
+            for (int ch = 0; ch < HD / 8; ++ch)
+              *reinterpret_cast<uint4*>(v + (ch >> 3) * (kTile * 128) + ((ch & 7) << 4)) =
+                  make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+        }
+        tc_fence_before();
+        mbar_arrive(&p_full[s]);
+      }
+      if (go && mysteps > 0 && !wait_warp(&pv_done[s], (n_st + mysteps - 1) & 1)) go = false;
+      if (!go) {
+        fail();
+        break;
+      }
+      n_st += mysteps;
+      loads += 2 * nt;
+      tiles += nt;
+      tc_fence_after();
+      // ---------------- results
+      const float sk = u.whole && a.sink && row_ok ? a.sink[head] * kLog2e : -INFINITY;
+      const int slot_p = u.tile0 > 0 ? 0 : 1;
+      const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + slot_p) * p.part_rows + rel;
+      bf16* out = static_cast<bf16*>(a.out) + (u.q0 + tok) * a.ld_out + static_cast<long long>(head) * HD;
+      auto emit = [&](int col, uint32_t* o, float f) {  // 32 columns from col
+        if (!row_ok) return;
+        if (u.whole) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * f,
+                                 __uint_as_float(o[8 * c + 2 * e + 1]) * f);
+            reinterpret_cast<uint4*>(out + col)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          uint4* d = reinterpret_cast<uint4*>(p.part_o + prow * HD + col);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) d[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        }
+      };
+      // factor of the unnormalised O of a row with (M, den): a sink joins both
+      auto factor = [&](float M, float den) {
+        if (!u.whole) return 1.f;
+        const float top = fmaxf(M, sk);
+        if (top == -INFINITY || den == 0.f) return 0.f;
+        const float e = ex2(M - top);
+        return e / (den * e + (sk == -INFINITY ? 0.f : ex2(sk - top)));
+      };
+      if (u.wide) {
+        const float f = factor(m, l);
+        if (live) {
+#pragma unroll
+          for (int b = 0; b < HD / 32; ++b) {
+            uint32_t o[32];
+            tmem_ld32_issue(tm + S::kO + s * HD + 32 * b, o);
+            tmem_wait_ld();
+            tmem_use32(o);
+            emit(32 * b, o, f);
+          }
+        }
+        if (!u.whole && row_ok) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
+        tc_fence_before();
+      } else {
+        // the two streams' states of the same row join; each group writes half the columns
+        ml_sh[s][i][0] = m;
+        ml_sh[s][i][1] = l;
+        tc_fence_before();
+        mbar_arrive(&x_bar[0]);
+        if (!wait_warp(&x_bar[0], n_x & 1)) {
+          fail();
+          break;
+        }
+        tc_fence_after();
+        const float m0 = ml_sh[0][i][0], m1 = ml_sh[1][i][0];
+        const float M = fmaxf(m0, m1);
+        float w0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), w1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+        const float den = ml_sh[0][i][1] * w0 + ml_sh[1][i][1] * w1;
+        const float f = factor(M, den);
+        if (live) {
+#pragma unroll
+          for (int b = 0; b < HD / 64; ++b) {
+            const int col = s * (HD / 2) + 32 * b;
+            uint32_t o[32];
+            tmem_ld32_issue(tm + S::kO + col, o);
+            tmem_wait_ld();
+            tmem_use32(o);
+            if (nt > 1) {
+              uint32_t o1[32];
+              tmem_ld32_issue(tm + S::kO + HD + col, o1);
+              tmem_wait_ld();
+              tmem_use32(o1);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                o[c] = __float_as_uint(__uint_as_float(o[c]) * w0 + __uint_as_float(o1[c]) * w1);
+            }
+            emit(col, o, f);
+          }
+        }
+        if (!u.whole && row_ok && s == 0)
+          *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(M, den);
+        // the other group may still read this stream's O (and ml_sh)
+        tc_fence_before();
+        mbar_arrive(&x_bar[1]);
+        if (!wait_warp(&x_bar[1], n_x & 1)) {
+          fail();
+          break;
+        }
+        ++n_x;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8) {
+    // ---------------- TMA warp: lists the units of this CTA's piece and streams
+    // their tiles in the order in which the MMA warp consumes them
+    const Place first = place_sh[0], last = place_sh[1];
+    Place cur = first;
+    uint32_t loads = 0, n_items = 0, tiles = 0;
+    int head = 0, tail = 0, t_q0 = 0, t_g = 0, t_row0 = 0, t_rows = 0;
+    bool go = true;
+    const uint64_t once = policy_evict_first(), kept = policy_evict_normal();
+    const int gpt = kTile / p.box;  // boxes per tile
+    while (go) {
+      if (cur.g > last.g || (cur.g == last.g && (cur.r > last.r || (cur.r == last.r && cur.qt > last.qt))))
+        break;
+      const bool ends_here = cur.g == last.g && cur.r == last.r && cur.qt == last.qt;
+      if (ends_here && last.tile <= cur.tile) break;
+      if (cur.g >= a.G) break;
+      const Req q = load_req(a, cur.r, false);
+      Unit u;
+      u.r = cur.r;
+      u.g = cur.g;
+      u.q0 = q.q0;
+      u.n = q.n;
+      u.L = q.L;
+      u.row0 = cur.qt * kUnitRows;
+      u.rows = min(kUnitRows, q.R - u.row0);
+      u.wide = u.rows > kTile;
+      u.kend = unit_kend(q, cur.qt, HG);
+      const int kt = unit_tiles(u.kend);
+      u.tile0 = cur.tile;
+      u.tile1 = ends_here ? last.tile : kt;
+      u.whole = u.tile0 == 0 && u.tile1 == kt;
+      if (!u.whole) {
+        if (u.tile0 > 0) {
+          head = u.tile1 == kt ? 2 : 1;
+        } else {
+          tail = 1;
+          t_q0 = u.q0;
+          t_g = u.g;
+          t_row0 = u.row0;
+          t_rows = u.rows;
+        }
+      }
+      // hand the unit over
+      const int slot = n_items % kItems;
+      if (n_items >= kItems) {
+        int ok = lane == 0 ? mbar_wait(&it_empty[slot], (n_items / kItems - 1) & 1, abort_flag) : 1;
+        if (!__shfl_sync(0xffffffffu, ok, 0)) {
+          if (lane == 0) fail();
+          break;
+        }
+      }
+      if (lane == 0) {
+        items[slot] = u;
+        mbar_arrive(&it_full[slot]);
+      }
+      ++n_items;
+      // stream its tiles.  A window is 32 boxes (32 / gpt tiles), one per lane; K and V
+      // walk their own, and the block ids of the next window are read while the
+      // current one streams.
+      const int nt = u.tile1 - u.tile0;
+      const int steps = u.wide ? 2 * nt : nt;
+      auto block_of = [&](int wn) {
+        const long long key = (static_cast<long long>(wn) * 32 + lane) * p.box;
+        return key < u.kend ? a.block_table[static_cast<long long>(u.r) * a.max_blocks + key / a.bs]
+                            : -2;  // past the unit's keys
+      };
+      auto row_of = [&](int wn, int blk) {
+        if (blk >= 0 && blk < a.num_blocks)
+          return (blk * a.G + u.g) * a.bs + (wn * 32 + lane) * p.box % a.bs;
+        if (blk != -2 || (wn * 32 + lane) * p.box < u.kend) set_status(a.status, PE_ST_BLOCK_RANGE);
+        return -1;
+      };
+      Window kw, vw;
+      kw.n = u.tile0 * gpt / 32;
+      kw.row = row_of(kw.n, block_of(kw.n));
+      kw.next = block_of(kw.n + 1);
+      vw = kw;
+      auto load = [&](int j, bool is_v, Window& w) {  // tile j of the unit
+        const int t = u.tile0 + j;
+        if (t * gpt / 32 != w.n) {
+          ++w.n;
+          w.row = row_of(w.n, w.next);
+          w.next = block_of(w.n + 1);
+        }
+        const int b0 = t * gpt & 31;
+        const bool in = lane >= b0 && lane < b0 + gpt;
+        const unsigned have = __ballot_sync(0xffffffffu, in && w.row >= 0);
+        const int st = loads % S::kSlots;
+        int ok = 1;
+        if (lane == 0) {
+          if (loads >= S::kSlots) ok = mbar_wait(&kv_empty[st], (loads / S::kSlots - 1) & 1, abort_flag);
+          if (ok) {
+            if (!is_v) {
+              // the boxes' bits, widened to groups of 8 keys
+              uint32_t m = 0;
+              const int w8 = p.box / 8;
+              for (int b = 0; b < gpt; ++b)
+                if (have >> (b0 + b) & 1) m |= ((1u << w8) - 1u) << (b * w8);
+              mask_sh[tiles % kMasks] = m;
+            }
+            mbar_arrive_expect_tx(&kv_full[st], __popc(have) * p.box * HD * 2);
+          } else {
+            fail();
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!is_v) ++tiles;
+        if (!ok) {
+          go = false;
+          return;
+        }
+        if (in && w.row >= 0) {
+          uint8_t* dst = ring + st * S::kTileBytes + (lane - b0) * p.box * 128;
+          for (int h = 0; h < S::kHalves; ++h)
+            tma_load_2d(dst + h * (kTile * 128), is_v ? &vmap : &kmap, &kv_full[st], h * 64, w.row,
+                        u.wide ? kept : once);
+        }
+        __syncwarp();
+        ++loads;
+      };
+#pragma unroll 1
+      for (int i = -S::kAhead; i < steps && go; ++i) {
+        if (i >= 0 && (!u.wide || !(i & 1))) load(u.wide ? i >> 1 : i, true, vw);
+        const int n = i + S::kAhead;
+        if (go && n < steps && (!u.wide || !(n & 1))) load(u.wide ? n >> 1 : n, false, kw);
+      }
+      // the next unit
+      if (ends_here) break;
+      cur.tile = 0;
+      if (++cur.qt >= q.Q) {
+        cur.qt = 0;
+        cur.r = next_request(a, cur.r + 1, lane);
+        if (cur.r >= a.B) {
+          ++cur.g;
+          cur.r = next_request(a, 0, lane);
+        }
+      }
+    }
+    // the end of the list
+    if (lane == 0) {
+      const int slot = n_items % kItems;
+      if (n_items < kItems || mbar_wait(&it_empty[slot], (n_items / kItems - 1) & 1, abort_flag)) {
+        items[slot].r = -1;
+        mbar_arrive(&it_full[slot]);
+      }
+      int* rec = p.rec + blockIdx.x * 8;
+      rec[0] = head;
+      rec[1] = tail;
+      rec[2] = t_q0;
+      rec[3] = t_g;
+      rec[4] = t_row0;
+      rec[5] = t_rows;
+      // no copy may be in flight when the CTA leaves (after a timeout some may be)
+      int never = 0;
+      for (uint32_t i = loads > S::kSlots ? loads - S::kSlots : 0; i < loads; ++i)
+        mbar_wait(&kv_full[i % S::kSlots], (i / S::kSlots) & 1, &never);
+    }
+    __syncwarp();
+    } else if (warp == 9) {
+    // ---------------- MMA warp, one thread
+    if (lane == 0) {
+      uint32_t loads = 0, n_items = 0, q_a = 0, q_b = 0, st_a = 0, st_b = 0;
+      const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
+      const uint32_t idesc_o = idesc_bf16_f32(kTile, HD) | (1u << 16);  // V is MN-major
+      bool go = true;
+      while (go) {
+        const int slot = n_items % kItems;
+        if (!mbar_wait(&it_full[slot], (n_items / kItems) & 1, abort_flag)) {
+          fail();
+          break;
+        }
+        const Unit u = items[slot];
+        mbar_arrive(&it_empty[slot]);
+        ++n_items;
+        if (u.r < 0) break;
+        const int nt = u.tile1 - u.tile0;
+        const int steps = u.wide ? 2 * nt : nt;
+        const int ahead = u.wide ? S::kAhead / 2 : S::kAhead;  // K tiles before V tile 0
+        go = mbar_wait(&q_full[0], q_a++ & 1, abort_flag);
+        if (go && u.wide) go = mbar_wait(&q_full[1], q_b++ & 1, abort_flag);
+        tc_fence_after();
+        const uint32_t base = loads;
+        auto wait_load = [&](uint32_t idx, int& st) {
+          st = idx % S::kSlots;
+          if (mbar_wait(&kv_full[st], (idx / S::kSlots) & 1, abort_flag)) return true;
+          return false;
+        };
+        // step i: stream i & 1, tile i (narrow) or i / 2 (wide), the k-th of its stream
+        auto score = [&](int i) -> bool {
+          const int s = i & 1, j = u.wide ? i >> 1 : i, k = i >> 1;
+          int st;
+          if (!wait_load(base + j + max(0, j - ahead + 1), st)) return false;
+          if (k > 0) {
+            // S of this stream's previous step is out of the way
+            uint64_t* bar = S::kAhead == 4 ? &s_free[s] : &pv_done[s];
+            if (!mbar_wait(bar, ((s ? st_b : st_a) + k - 1) & 1, abort_flag)) return false;
+          }
+          tc_fence_after();
+          const uint64_t ad = sw128_kmajor_desc(
+              smem_u32(q_sm + (u.wide ? s : 0) * S::kTileBytes));
+          const uint64_t bd = sw128_kmajor_desc(smem_u32(ring + st * S::kTileBytes));
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * (kTile * 128 / 16) + (kk & 3) * 2;
+            umma_bf16(tmem + S::kS + s * 128, ad + o, bd + o, idesc_s, kk > 0);
+          }
+          umma_commit(&s_full[s]);
+          if (!u.wide || (i & 1)) umma_commit(&kv_empty[st]);
+          return true;
+        };
+        auto value = [&](int i) -> bool {
+          const int s = i & 1, j = u.wide ? i >> 1 : i, k = i >> 1;
+          int st;
+          if (!wait_load(base + min(nt, ahead + j) + j, st)) return false;
+          if (!mbar_wait(&p_full[s], ((s ? st_b : st_a) + k) & 1, abort_flag)) return false;
+          tc_fence_after();
+          const uint64_t bd = sw128_mnmajor_desc(smem_u32(ring + st * S::kTileBytes), kTile * 128);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            umma_bf16_ta(tmem + S::kO + s * HD, tmem + S::kP + s * S::kPStride + kk * 8,
+                         bd + kk * 128, idesc_o, k > 0 || kk > 0);
+          umma_commit(&pv_done[s]);
+          if (!u.wide || (i & 1)) umma_commit(&kv_empty[st]);
+          return true;
+        };
+#pragma unroll 1
+        for (int i = -S::kAhead; i < steps && go; ++i) {
+          if (i >= 0) go = value(i);
+          if (go && i + S::kAhead < steps) go = score(i + S::kAhead);
+        }
+        if (!go) fail();
+        loads += 2 * nt;
+        st_a += (steps + 1) >> 1;
+        st_b += steps >> 1;
+      }
+      // nothing of this thread is running when the CTA leaves
+      int never = 0;
+      umma_commit(&end_bar);
+      mbar_wait(&end_bar, 0, &never);
+    }
+    __syncwarp();
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partials of the units that were cut between CTAs.  CTA (c, y): the unit
+// whose first part is CTA c's last one, a slice of its rows; its other parts are the
+// first ones of the CTAs after c, up to the one that ends it.  One warp per row.
+template <int HD>
+__global__ void __launch_bounds__(128) chunk_join_kernel(const __grid_constant__ TcArgs p) {
+  constexpr int V = HD / 32;
+  pdl_trigger();
+  pdl_wait();
+  const ChunkArgs& a = p.c;
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int* rec = p.rec + c * 8;
+  if (!rec[1]) return;
+  const int q0 = rec[2], g = rec[3], row0 = rec[4], rows = rec[5];
+  const int HG = a.H / a.G;
+  for (int row = blockIdx.y * 4 + warp; row < rows; row += gridDim.y * 4) {
+    const int tok = (row0 + row) / HG, head = g * HG + (row0 + row) % HG;
+    float M = a.sink ? a.sink[head] * kLog2e : -INFINITY;
+    float den = M == -INFINITY ? 0.f : 1.f;
+    bool any = false;
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int k = c, part = 1;; part = 0) {
+      const size_t prow = (static_cast<size_t>(k) * 2 + part) * p.part_rows + row;
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + prow * 2);
+      float o[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = p.part_o[prow * HD + lane + 32 * i];
+      if (ml.y != 0.f) {  // some key of this part was seen (or is NaN)
+        any = true;
+        const float mn = fmaxf(M, ml.x);
+        const float f0 = M == -INFINITY ? 0.f : ex2(M - mn), f1 = ex2(ml.x - mn);
+        M = mn;
+        den = den * f0 + ml.y * f1;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = acc[i] * f0 + o[i] * f1;
+      }
+      // the next part
+      int code = 0;
+      if (!part && p.rec[k * 8] == 2) break;
+      for (++k; k < p.grid; ++k)
+        if ((code = p.rec[k * 8])) break;
+      if (!code) break;
+    }
+    const float inv = any ? 1.f / den : 0.f;
+    bf16* out = static_cast<bf16*>(a.out) + (q0 + tok) * a.ld_out + static_cast<long long>(head) * HD;
+#pragma unroll
+    for (int i = 0; i < V; ++i) out[lane + 32 * i] = __float2bfloat16_rn(acc[i] * inv);
+  }
+}
+
+constexpr int kMaxGrid = 152;
+
+size_t al256(size_t x) { return (x + 255) / 256 * 256; }
+
+int part_rows_of(int T, int HG) {
+  return static_cast<long long>(T) * HG > kTile ? kUnitRows : kTile;
+}
+
+// offsets past the 256-byte header: records, (m, l), O
+size_t rec_bytes() { return al256(kMaxGrid * 8 * sizeof(int)); }
+size_t ml_bytes(int part_rows) { return al256(size_t{kMaxGrid} * 2 * part_rows * 2 * sizeof(float)); }
+
+template <int HD>
+int launch(const TcArgs& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+  cudaFuncSetAttribute(chunk_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       Shape<HD>::kSmem);
+  if (launch_pdl(chunk_tc_kernel<HD>, dim3(p.grid), dim3(kThreads), Shape<HD>::kSmem, st, km, vm, p) !=
+      cudaSuccess)
+    return PE_ERR_CUDA;
+  return launch_pdl(chunk_join_kernel<HD>, dim3(p.grid, 8), dim3(128), 0, st, p) == cudaSuccess
+             ? PE_OK
+             : PE_ERR_CUDA;
+}
+
+}  // namespace
+
+bool chunk_tc_takes(const pe_attn_plan* plan) {
+  return plan->dtype == PE_DTYPE_BF16 && plan->block_size % 8 == 0;
+}
+
+size_t chunk_tc_workspace(const pe_attn_plan* plan, int max_rows) {
+  const int rows = part_rows_of(max_rows, plan->n_heads / plan->n_kv_heads);
+  return 256 + rec_bytes() + ml_bytes(rows) +
+         al256(size_t{kMaxGrid} * 2 * rows * plan->head_dim * sizeof(float));
+}
+
+int launch_chunk_tc(const ChunkArgs& a, char* ws, cudaStream_t st) {
+  TcArgs p = {};
+  p.c = a;
+  p.box = 8;
+  while (p.box < kTile && a.bs % (2 * p.box) == 0) p.box *= 2;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return PE_ERR_CUDA;
+  p.grid = sms < kMaxGrid ? sms : kMaxGrid;
+  p.umin = 2;
+  p.overhead = 1;
+  p.part_rows = part_rows_of(a.T, a.H / a.G);
+  p.rec = reinterpret_cast<int*>(ws + 256);
+  p.part_ml = reinterpret_cast<float*>(ws + 256 + rec_bytes());
+  p.part_o = reinterpret_cast<float*>(ws + 256 + rec_bytes() + ml_bytes(p.part_rows));
+  CUtensorMap km, vm;
+  const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.G * a.bs;
+  if (!encode_tmap_bf16(&km, a.k_cache, rows, a.hd, p.box) ||
+      !encode_tmap_bf16(&vm, a.v_cache, rows, a.hd, p.box))
+    return PE_ERR_CUDA;
+  return a.hd == 64 ? launch<64>(p, km, vm, st) : launch<128>(p, km, vm, st);
+}
+
+}  // namespace pe

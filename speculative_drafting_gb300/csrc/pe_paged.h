@@ -24,6 +24,11 @@ struct ChunkArgs {
   uint32_t* status;
 };
 
+// The tensor-core kernels of pe_chunk_attention (bf16, blocks of a multiple of 8 keys).
+bool chunk_tc_takes(const pe_attn_plan* plan);
+size_t chunk_tc_workspace(const pe_attn_plan* plan, int max_rows);
+int launch_chunk_tc(const ChunkArgs& a, char* ws, cudaStream_t st);
+
 // Rows [q0, q1) of request r, clamped to [0, T]; bad: qsl is not a
 // non-decreasing run from 0 to at most T.
 struct RowRange {
