@@ -7,8 +7,13 @@
 //   (y_i, y_{i+hd/2}) -> (y_i c - y_{i+hd/2} s, y_{i+hd/2} c + y_i s),
 //   c, s = cos, sin of pos * theta^(-2i/hd)              (q and k heads)
 //
-// One warp per (row, head).  Everything is fp32 until the one rounding of the
-// result.
+// Everything is fp32 until the one rounding of the result.
+//
+//   append_kernel       bf16 with head size 64 or 128 (and fp32 with the same): 16-byte
+//                       vectors.  A CTA takes one row; its first hd/2 threads form the
+//                       row's cos and sin once, in shared memory, while the CTA's
+//                       first loads are under way.
+//   append_any_kernel   every other head size: one warp per (row, head).
 #include <cmath>
 
 #include "pe_common.cuh"
@@ -17,7 +22,8 @@
 namespace pe {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;         // append_any_kernel
+constexpr int kRowThreads = 256;  // append_kernel
 
 struct AppendArgs {
   int T, H, G, hd, bs, num_blocks;
@@ -32,11 +38,113 @@ struct AppendArgs {
   void* k_cache;
   void* v_cache;
   uint32_t* status;
+  int head0, heads_per_cta;  // append_kernel: the first head, heads of a CTA's row
   uint64_t turn[64];
 };
 
+// Where head h of a row goes, or NULL: q rows without a q_out, rows without a slot.
 template <typename T>
-__global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_constant__ AppendArgs a) {
+PE_DEV T* head_dst(const AppendArgs& a, int64_t t, int64_t slot, int h) {
+  if (h < a.H) return a.q_out ? static_cast<T*>(a.q_out) + (t * a.H + h) * a.hd : nullptr;
+  if (slot < 0) return nullptr;
+  const int g = h < a.H + a.G ? h - a.H : h - a.H - a.G;
+  T* cache = static_cast<T*>(h < a.H + a.G ? a.k_cache : a.v_cache);
+  // 32-bit division where it is enough: a 64-bit one costs as much as the rotation
+  const bool small = slot <= 0xffffffffll;
+  const int64_t blk = small ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.bs) : slot / a.bs;
+  return cache + ((blk * a.G + g) * a.bs + (slot - blk * a.bs)) * a.hd;
+}
+
+// Threads of a head: hd / 2 / kVec, each with the kVec pairs (i, i + hd/2) of one
+// 16-byte vector from either half.  Every thread keeps its pairs for all the heads it
+// visits.
+template <typename T, int HD>
+__global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kVec = 16 / sizeof(T);
+  constexpr int kHalf = HD / 2;
+  constexpr int kLanes = kHalf / kVec;                // threads per head
+  constexpr int kHeads = kRowThreads / kLanes;        // heads per round
+  __shared__ float cs[kHalf], sn[kHalf];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  const int sub = tid % kLanes, h0 = a.head0 + blockIdx.y * a.heads_per_cta + tid / kLanes;
+  const int h_end = min(a.head0 + static_cast<int>(blockIdx.y + 1) * a.heads_per_cta, a.H + 2 * a.G);
+  const int64_t t = blockIdx.x;
+  const T* x = static_cast<const T*>(a.qkv) + t * a.ld_qkv;
+  const int64_t pos = a.pos[t];
+  int64_t slot = a.slot[t];
+  if (slot >= static_cast<int64_t>(a.num_blocks) * a.bs) {
+    if (tid == 0) set_status(a.status, PE_ST_BLOCK_RANGE);
+    slot = -1;
+  }
+  auto vec = [&](int h, int half) {
+    return *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(h) * HD + half * kHalf + sub * kVec);
+  };
+  uint4 lo, hi;
+  if (h0 < h_end) {
+    lo = vec(h0, 0);
+    hi = vec(h0, 1);
+  }
+  if (tid < kHalf) rope_cos_sin(pos, a.turn[tid], cs[tid], sn[tid]);
+  __syncthreads();
+  float c[kVec], s[kVec];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    c[i] = cs[sub * kVec + i];
+    s[i] = sn[sub * kVec + i];
+  }
+  for (int h = h0; h < h_end; h += kHeads) {
+    const uint4 l4 = lo, h4 = hi;
+    if (h + kHeads < h_end) {
+      lo = vec(h + kHeads, 0);
+      hi = vec(h + kHeads, 1);
+    }
+    T* dst = head_dst<T>(a, t, slot, h);
+    uint4 o0 = l4, o1 = h4;
+    if (h < a.H + a.G) {
+      float p[kVec], q[kVec];
+      unpack16<T>(l4, p);
+      unpack16<T>(h4, q);
+      const T* gain = static_cast<const T*>(h < a.H ? a.gamma_q : a.gamma_k);
+      if (gain) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          ss = fmaf(p[i], p[i], ss);
+          ss = fmaf(q[i], q[i], ss);
+        }
+        // the threads of a head are neighbours in one warp; all of them are here
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(__activemask(), ss, o);
+        const float inv = 1.0f / sqrtf(ss / static_cast<float>(HD) + a.eps);
+        float g0[kVec], g1[kVec];
+        unpack16<T>(*reinterpret_cast<const uint4*>(gain + sub * kVec), g0);
+        unpack16<T>(*reinterpret_cast<const uint4*>(gain + kHalf + sub * kVec), g1);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          p[i] *= inv * g0[i];
+          q[i] *= inv * g1[i];
+        }
+      }
+      float y[kVec], z[kVec];
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        y[i] = p[i] * c[i] - q[i] * s[i];
+        z[i] = q[i] * c[i] + p[i] * s[i];
+      }
+      o0 = pack16<T>(y);
+      o1 = pack16<T>(z);
+    }
+    if (dst) {
+      *reinterpret_cast<uint4*>(dst + sub * kVec) = o0;
+      *reinterpret_cast<uint4*>(dst + kHalf + sub * kVec) = o1;
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps) append_any_kernel(const __grid_constant__ AppendArgs a) {
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -46,21 +154,13 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
   if (t >= a.T) return;
   const int h = static_cast<int>(item - t * heads);
   const T* x = static_cast<const T*>(a.qkv) + t * a.ld_qkv + static_cast<int64_t>(h) * a.hd;
-  T* dst;
-  if (h < a.H) {
-    if (!a.q_out) return;
-    dst = static_cast<T*>(a.q_out) + (t * a.H + h) * a.hd;
-  } else {
-    const int64_t slot = a.slot[t];
-    if (slot >= static_cast<int64_t>(a.num_blocks) * a.bs) {
-      if (lane == 0) set_status(a.status, PE_ST_BLOCK_RANGE);
-      return;
-    }
-    if (slot < 0) return;
-    const int g = (h - a.H) % a.G;
-    T* cache = static_cast<T*>(h < a.H + a.G ? a.k_cache : a.v_cache);
-    dst = cache + (((slot / a.bs) * a.G + g) * a.bs + slot % a.bs) * a.hd;
+  int64_t slot = a.slot[t];
+  if (slot >= static_cast<int64_t>(a.num_blocks) * a.bs) {
+    if (lane == 0) set_status(a.status, PE_ST_BLOCK_RANGE);
+    slot = -1;
   }
+  T* dst = head_dst<T>(a, t, slot, h);
+  if (!dst) return;
   if (h >= a.H + a.G) {  // a value head: copied
     for (int i = lane; i < a.hd; i += 32) dst[i] = x[i];
     return;
@@ -172,14 +272,25 @@ extern "C" int pe_qkv_append(const pe_attn_plan* plan, int T, const void* qkv, i
   a.v_cache = v_cache;
   a.status = static_cast<uint32_t*>(ws);
   for (int i = 0; i < 64; ++i) a.turn[i] = plan->rope_turn[i];
-  const int64_t items = static_cast<int64_t>(T) * heads;
-  const int64_t grid = (items + kWarps - 1) / kWarps;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf = plan->dtype == PE_DTYPE_BF16;
+  if (a.hd == 64 || a.hd == 128) {
+    // Without q_out only the k and v heads are read.  A row is one CTA, or, while the
+    // rows leave SMs idle, up to four.
+    a.head0 = q_out ? 0 : a.H;
+    const int n = heads - a.head0;
+    const int cut = T >= 128 ? 1 : T >= 64 ? 2 : 4;
+    a.heads_per_cta = (n + cut - 1) / cut;
+    const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>((n + a.heads_per_cta - 1) / a.heads_per_cta));
+    auto* kernel = bf ? (a.hd == 64 ? append_kernel<bf16, 64> : append_kernel<bf16, 128>)
+                      : (a.hd == 64 ? append_kernel<float, 64> : append_kernel<float, 128>);
+    return launch_pdl(kernel, grid, dim3(kRowThreads), 0, st, a) == cudaSuccess ? PE_OK : PE_ERR_CUDA;
+  }
+  const int64_t grid = (static_cast<int64_t>(T) * heads + kWarps - 1) / kWarps;
   if (grid > 0x7fffffff) return PE_ERR_UNSUPPORTED;
-  const cudaError_t e =
-      plan->dtype == PE_DTYPE_BF16
-          ? launch_pdl(append_kernel<bf16>, dim3(static_cast<unsigned>(grid)), dim3(32 * kWarps), 0,
-                       static_cast<cudaStream_t>(stream), a)
-          : launch_pdl(append_kernel<float>, dim3(static_cast<unsigned>(grid)), dim3(32 * kWarps), 0,
-                       static_cast<cudaStream_t>(stream), a);
-  return e == cudaSuccess ? PE_OK : PE_ERR_CUDA;
+  // bf16 plans have head size 64 or 128
+  return launch_pdl(append_any_kernel<float>, dim3(static_cast<unsigned>(grid)), dim3(32 * kWarps), 0,
+                    st, a) == cudaSuccess
+             ? PE_OK
+             : PE_ERR_CUDA;
 }
