@@ -412,7 +412,8 @@ int pe_verify_greedy(int B, int T_in, const int32_t* qsl, const int32_t* tok,
  *                  qsl[B] on belong to no request and are neither used nor written
  *   temperature[B] float, nullable (NULL: 1 for every request).  0: the request is
  *                  greedy (pe_verify_greedy's rules; its numbers are not read).
- *                  Negative or NaN: read as 0, PE_ST_SAMPLING
+ *                  Negative or NaN: read as 0, PE_ST_SAMPLING.  Positive ones
+ *                  below 1e-30 are read as 1e-30
  *   u[T_in]        float uniform numbers in [0, 1): u of row j >= 1 of a request
  *                  decides its draft j (row 0's entry is not read)
  *   gumbel[B][vocab] float standard Gumbel noise, -log(E) of exponential draws E

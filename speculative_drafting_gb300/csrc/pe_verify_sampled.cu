@@ -8,10 +8,18 @@
 // x) is argmax_v(l_v / T + g_v) for standard Gumbel noise g (over v != x): the
 // normaliser of p does not enter, so only the acceptance tests need the row sums.
 //
-//   row kernel      one CTA per row: the largest logit m and the sum s of
-//                   exp((l - m) / T); for a greedy request (T = 0) the argmax key.
-//   request kernel  one CTA per request: the accepted prefix, then the race over
-//                   the one row the next token comes from.
+//   row kernel      CTA (row, chunk): the chunk's largest logit m and the sum s of
+//                   exp((l - m) / T); for a greedy request (T = 0) its argmax key.
+//                   Streams the logits once: HBM-bound.
+//   request kernel  CTA (request, chunk): joins the rows' chunks, walks the drafts
+//                   to the accepted prefix, then races over its chunk of the one
+//                   row that the next token comes from; the last CTA of a request
+//                   to finish takes the best of the chunks.
+//
+// The request kernel reads one row per request a second time (1 / n of the logits)
+// and its noise; racing in the row kernel instead would read the noise for every
+// row.
+#include <algorithm>
 #include <cmath>
 
 #include "pe_common.cuh"
@@ -21,7 +29,10 @@ namespace pe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWsHeader = 256;  // status word, then per row: (m, s) or the key
+constexpr int kUnroll = 4;            // 16-byte loads in flight per thread
+constexpr int kMaxChunkBytes = 32768; // of a row, per CTA of the row kernel
+constexpr int kRace = 8;              // logits per thread and round of the race
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct VerifyArgs {
   int B, T, V;
@@ -35,90 +46,162 @@ struct VerifyArgs {
   int32_t* bonus;
   float* p_draft;
   uint32_t* status;
-  uint64_t* rows;
+  int chunk, splits;    // row kernel
+  int rchunk, rsplits;  // request kernel
+  int vec;              // the race's rows are 16-byte aligned
+  uint64_t* rows;       // [T][splits]: (m, s) or the argmax key
+  uint32_t* done;       // [B] CTAs of the request kernel that finished
+  ulonglong2* best;     // [B][rsplits]: order of the score, token
 };
 
 PE_DEV float temperature_of(const VerifyArgs& a, int r) {
   const float t = a.temperature ? a.temperature[r] : 1.f;
-  return t > 0.f ? t : 0.f;
+  return t > 0.f ? fmaxf(t, 1e-30f) : 0.f;  // 1 / T stays finite, l / T for any real logit
+}
+
+PE_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+PE_DEV float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+PE_DEV uint4 ld_stream16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// The request of a row, by one warp: the last r with qsl[r] <= row (32 probes a
+// round).  -1: the row is behind the last request.
+PE_DEV int request_of(const VerifyArgs& a, int row, int lane) {
+  int lo = 0, hi = a.B;  // qsl[lo] <= row < qsl[hi], were qsl[B] past every row
+  if (a.qsl[a.B] <= row || a.qsl[0] > row) return -1;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, at < hi && a.qsl[min(at, a.B)] <= row);
+    const int k = 31 - __clz(le | 1u);
+    const int nlo = lo + k * step;
+    hi = min(hi, nlo + step);
+    lo = nlo;
+  }
+  return lo;
+}
+
+// Running maximum m and sum s of exp2((l - m) c).  A NaN logit makes m NaN, a +inf
+// one makes it +inf: neither row has a distribution.
+struct Stat {
+  float m, s;
+};
+PE_DEV Stat join(const Stat& x, const Stat& y, float c) {
+  Stat z;
+  z.m = max_nan(x.m, y.m);
+  const float off = z.m == -INFINITY ? 0.f : z.m;
+  z.s = x.s * ex2((x.m - off) * c) + y.s * ex2((y.m - off) * c);
+  return z;
 }
 
 template <typename T>
-PE_DEV float logit(const VerifyArgs& a, int64_t row, int v) {
-  return Elem<T>::to_f(static_cast<const T*>(a.logits)[row * a.V + v]);
-}
-
-// 1 / T, finite for every T > 0 (so that a difference of 0 stays 0)
-PE_DEV float inv_temperature(float temp) { return fminf(1.f / temp, 3.0e38f); }
-
-// probability of token v given a row's statistics (m: largest logit, s: sum of
-// exp((l - m) / T)), 0 for a row without a distribution.  64 bits: one value per
-// draft, and a draft is accepted by a comparison with it.
-template <typename T>
-PE_DEV float prob(const VerifyArgs& a, int64_t row, int v, float temp, float m, float s) {
-  if (!(fabsf(m) < INFINITY)) return 0.f;
-  const double d = static_cast<double>(logit<T>(a, row, v)) - static_cast<double>(m);
-  return static_cast<float>(exp(d / static_cast<double>(temp)) / static_cast<double>(s));
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) sampled_row_kernel(const VerifyArgs a) {
-  __shared__ float sm[kThreads / 32], ss[kThreads / 32];
-  __shared__ uint64_t sk[kThreads / 32];
-  __shared__ int req_sh;
+__global__ void __launch_bounds__(kThreads, 6) sampled_row_kernel(const VerifyArgs a) {
+  constexpr int kVec = 16 / sizeof(T);
+  __shared__ Stat st_sh[kThreads / 32];
+  __shared__ unsigned long long key_sh[kThreads / 32];
+  __shared__ float temp_sh;
   pdl_trigger();
   pdl_wait();
-  const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (row == 0 && tid == 0) *a.status = 0u;  // only the request kernel sets bits
-  if (tid == 0) req_sh = -1;
-  __syncthreads();
-  for (int r = tid; r < a.B; r += kThreads) {
-    const RowRange x = request_rows(a.qsl, r, a.T);
-    if (x.q0 <= row && row < x.q1) atomicMax(&req_sh, r);
+  const int row = blockIdx.x / a.splits, sp = blockIdx.x - row * a.splits;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (blockIdx.x == 0) {  // only the request kernel, after this one, uses these
+    if (tid == 0) *a.status = 0u;
+    for (int r = tid; r < a.B; r += kThreads) a.done[r] = 0u;
+  }
+  const int c0 = sp * a.chunk, c1 = min(a.V, c0 + a.chunk);
+  const T* base = static_cast<const T*>(a.logits) + static_cast<size_t>(row) * a.V;
+  // scalar head up to the first 16-byte boundary, vectors, scalar tail
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(base + c0);
+  const int head = min(static_cast<int>(((16u - (a0 & 15u)) & 15u) / sizeof(T)), c1 - c0);
+  const int v0 = c0 + head, nvec = (c1 - v0) / kVec, t0 = v0 + nvec * kVec;
+  const uint4* vp = reinterpret_cast<const uint4*>(base + v0);
+  const uint4 none = sizeof(T) == 2 ? make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u)
+                                    : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+  // the first vectors are on their way while the row's request is looked up
+  uint4 u[kUnroll];
+#pragma unroll
+  for (int x = 0; x < kUnroll; ++x)
+    u[x] = tid + x * kThreads < nvec ? ld_stream16(vp + tid + x * kThreads) : none;
+  if (warp == 0) {
+    const int r = request_of(a, row, lane);
+    if (lane == 0) temp_sh = r < 0 ? -1.f : temperature_of(a, r);
   }
   __syncthreads();
-  if (req_sh < 0) return;
-  const float temp = temperature_of(a, req_sh);
+  const float temp = temp_sh;
+  if (temp < 0.f) return;
   if (temp == 0.f) {
     unsigned long long k = 0ull;
-    for (int v = tid; v < a.V; v += kThreads)
-      k = max(k, argmax_key(logit<T>(a, row, v), static_cast<uint32_t>(v)));
+    auto look = [&](T x, int v) {
+      k = max(k, argmax_key(Elem<T>::to_f(x), static_cast<uint32_t>(v)));
+    };
+    if (tid < head) look(base[c0 + tid], c0 + tid);
+    if (t0 + tid < c1) look(base[t0 + tid], t0 + tid);
+    for (int j = tid; j < nvec; j += kThreads) {
+      float f[kVec];
+      unpack16<T>(ld_stream16(vp + j), f);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e)
+        k = max(k, argmax_key(f[e], static_cast<uint32_t>(v0 + j * kVec + e)));
+    }
     k = warp_max_u64(k);
-    if (lane == 0) sk[warp] = k;
+    if (lane == 0) key_sh[warp] = k;
     __syncthreads();
     if (tid == 0) {
-      for (int w = 1; w < kThreads / 32; ++w) k = max(k, static_cast<unsigned long long>(sk[w]));
-      a.rows[row] = k;
+      for (int w = 1; w < kThreads / 32; ++w) k = max(k, key_sh[w]);
+      a.rows[static_cast<size_t>(row) * a.splits + sp] = k;
     }
     return;
   }
-  const float it = inv_temperature(temp);
-  float m = -INFINITY, s = 0.f;
-  bool nan = false;
-  for (int v = tid; v < a.V; v += kThreads) {
-    const float x = logit<T>(a, row, v);
-    nan |= x != x;
-    if (x > m) {
-      s = m == -INFINITY ? 0.f : s * expf((m - x) * it);
-      m = x;
+  const float c = (1.f / temp) * kLog2e;
+  Stat st{-INFINITY, 0.f};
+  if (tid < head) st = join(st, Stat{Elem<T>::to_f(base[c0 + tid]), 1.f}, c);
+  if (t0 + tid < c1) st = join(st, Stat{Elem<T>::to_f(base[t0 + tid]), 1.f}, c);
+  for (int j = tid; j < nvec; j += kUnroll * kThreads) {
+    // one maximum and one rescaling for the kUnroll vectors
+    float f[kUnroll][kVec];
+    float m = st.m;
+#pragma unroll
+    for (int x = 0; x < kUnroll; ++x) {
+      unpack16<T>(u[x], f[x]);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) m = max_nan(m, f[x][e]);
     }
-    if (x != -INFINITY) s += expf((x - m) * it);
+    const int jn = j + kUnroll * kThreads;
+#pragma unroll
+    for (int x = 0; x < kUnroll; ++x)
+      u[x] = jn + x * kThreads < nvec ? ld_stream16(vp + jn + x * kThreads) : none;
+    const float off = m == -INFINITY ? 0.f : m;
+    st.s *= ex2((st.m - off) * c);
+    st.m = m;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int x = 0; x < kUnroll; ++x)
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) s[e & 3] += ex2((f[x][e] - off) * c);
+    st.s += (s[0] + s[1]) + (s[2] + s[3]);
   }
-  const float wm = __any_sync(0xffffffffu, nan) ? NAN : warp_max(m);
-  s = m == -INFINITY ? 0.f : s * expf((m - wm) * it);
-  s = warp_sum(s);
-  if (lane == 0) {
-    sm[warp] = wm;
-    ss[warp] = s;
-  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    st = join(st, Stat{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o)}, c);
+  if (lane == 0) st_sh[warp] = st;
   __syncthreads();
   if (tid == 0) {
-    float M = sm[0];
-    for (int w = 1; w < kThreads / 32; ++w) M = (sm[w] != sm[w] || M != M) ? NAN : fmaxf(M, sm[w]);
-    float S = 0.f;
-    for (int w = 0; w < kThreads / 32; ++w)
-      if (sm[w] != -INFINITY) S += ss[w] * expf((sm[w] - M) * it);
-    a.rows[row] = (static_cast<uint64_t>(__float_as_uint(M)) << 32) | __float_as_uint(S);
+    for (int w = 1; w < kThreads / 32; ++w) st = join(st, st_sh[w], c);
+    a.rows[static_cast<size_t>(row) * a.splits + sp] =
+        (static_cast<uint64_t>(__float_as_uint(st.m)) << 32) | __float_as_uint(st.s);
   }
 }
 
@@ -129,95 +212,224 @@ PE_DEV unsigned long long score_order(double x) {
   return (u >> 63) ? ~u : (u | (1ull << 63));
 }
 
+PE_DEV void warp_best(unsigned long long& k, int& v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const unsigned long long k2 = __shfl_xor_sync(0xffffffffu, k, o);
+    const int v2 = __shfl_xor_sync(0xffffffffu, v, o);
+    if (k2 > k || (k2 == k && v2 < v)) {
+      k = k2;
+      v = v2;
+    }
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyArgs a) {
-  __shared__ int bad_sh;
-  __shared__ unsigned long long key_sh[kThreads / 32];
-  __shared__ int idx_sh[kThreads / 32];
+  constexpr int kW = kThreads / 32;
+  __shared__ int bad_sh, last_sh;
+  __shared__ uint32_t st_sh;
+  __shared__ Stat row_sh[kW];
+  __shared__ unsigned long long key_sh[kW];
+  __shared__ int idx_sh[kW];
   pdl_trigger();
   pdl_wait();
-  const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = blockIdx.x / a.rsplits, sp = blockIdx.x - r * a.rsplits;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const RowRange x = request_rows(a.qsl, r, a.T);
   const int n = x.q1 - x.q0;
-  uint32_t st = x.bad ? PE_ST_ROWS_RANGE : 0u;
   const float t0 = a.temperature ? a.temperature[r] : 1.f;
-  if (!(t0 >= 0.f)) st |= PE_ST_SAMPLING;
   const float temp = temperature_of(a, r);
-  if (tid == 0) bad_sh = n;
-  __syncthreads();
-  // draft j follows row j - 1
-  for (int j = 1 + tid; j < n; j += kThreads) {
-    const int64_t row = x.q0 + j - 1;
-    const int v = a.tok[row + 1];
-    const uint64_t w = a.rows[row];
-    float p = 0.f;
-    if (v < 0 || v >= a.V) {
-      st |= PE_ST_TOKEN_RANGE;
-    } else if (temp == 0.f) {
-      p = static_cast<uint32_t>(v) == ~static_cast<uint32_t>(w) ? 1.f : 0.f;
-    } else {
-      p = prob<T>(a, row, v, temp, __uint_as_float(static_cast<uint32_t>(w >> 32)),
-                  __uint_as_float(static_cast<uint32_t>(w)));
-    }
-    if (a.p_draft) a.p_draft[row + 1] = p;
-    if (temp == 0.f ? p == 0.f : !(a.u[row + 1] < p)) atomicMin(&bad_sh, j - 1);
+  if (temp == 0.f && sp > 0) return;  // a greedy request has no race
+  uint32_t st = x.bad ? PE_ST_ROWS_RANGE : 0u;
+  if (!(t0 >= 0.f)) st |= PE_ST_SAMPLING;
+  if (tid == 0) {
+    bad_sh = n;
+    st_sh = 0u;
+    if (sp == 0 && n > 0 && a.p_draft) a.p_draft[x.q0] = 1.f;
   }
-  if (tid == 0 && n > 0 && a.p_draft) a.p_draft[x.q0] = 1.f;
   __syncthreads();
-  const int acc = n > 0 ? min(bad_sh, n - 1) : 0;
-  int bonus = -1;
-  if (n > 0) {
-    const int64_t row = x.q0 + acc;
-    const uint64_t w = a.rows[row];
-    if (temp == 0.f) {
-      bonus = static_cast<int>(~static_cast<uint32_t>(w));
-    } else {
-      const float m = __uint_as_float(static_cast<uint32_t>(w >> 32));
-      if (fabsf(m) < INFINITY) {
-        const int skip = acc + 1 < n ? a.tok[row + 1] : -1;
-        unsigned long long best = 0ull;
-        int bi = 0x7fffffff;
-        for (int v = tid; v < a.V; v += kThreads) {
-          const float l = logit<T>(a, row, v);
-          if (v == skip || l == -INFINITY) continue;
-          const double s = static_cast<double>(l) / temp + a.gumbel[static_cast<int64_t>(r) * a.V + v];
-          const unsigned long long k = score_order(s);
-          if (k > best) {
-            best = k;
-            bi = v;
-          }
-        }
-        for (int o = 16; o; o >>= 1) {
-          const unsigned long long k2 = __shfl_xor_sync(0xffffffffu, best, o);
-          const int b2 = __shfl_xor_sync(0xffffffffu, bi, o);
-          if (k2 > best || (k2 == best && b2 < bi)) {
-            best = k2;
-            bi = b2;
-          }
-        }
-        if (lane == 0) {
-          key_sh[warp] = best;
-          idx_sh[warp] = bi;
-        }
-        __syncthreads();
-        if (tid == 0)
-          for (int i = 1; i < kThreads / 32; ++i)
-            if (key_sh[i] > best || (key_sh[i] == best && idx_sh[i] < bi)) {
-              best = key_sh[i];
-              bi = idx_sh[i];
-            }
-        bonus = best ? bi : -1;
+  // One warp per row, in order: the row's statistics (or key), then the draft after
+  // it.  The first CTA goes through all rows (p_draft), the others stop behind the
+  // first rejection.
+  const float c = (1.f / temp) * kLog2e;
+  const size_t rs = static_cast<size_t>(x.q0) * a.splits;
+  auto row_stat = [&](int j) {
+    Stat s{-INFINITY, 0.f};
+    for (int i = lane; i < a.splits; i += 32) {
+      const uint64_t w = a.rows[rs + static_cast<size_t>(j) * a.splits + i];
+      s = join(s, Stat{__uint_as_float(static_cast<uint32_t>(w >> 32)),
+                       __uint_as_float(static_cast<uint32_t>(w))}, c);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+      s = join(s, Stat{__shfl_xor_sync(0xffffffffu, s.m, o), __shfl_xor_sync(0xffffffffu, s.s, o)}, c);
+    return s;
+  };
+  auto row_pick = [&](int j) {
+    unsigned long long k = 0ull;
+    for (int i = lane; i < a.splits; i += 32)
+      k = max(k, static_cast<unsigned long long>(a.rows[rs + static_cast<size_t>(j) * a.splits + i]));
+    return static_cast<int>(~static_cast<uint32_t>(warp_max_u64(k)));
+  };
+  for (int j0 = 0; j0 + 1 < n; j0 += kW) {
+    const int j = j0 + warp;
+    int rejected = 0;
+    if (j + 1 < n) {
+      const int64_t row = x.q0 + j;
+      const int v = a.tok[row + 1];
+      float p = 0.f;
+      const bool in = v >= 0 && v < a.V;
+      if (!in) st |= PE_ST_TOKEN_RANGE;
+      if (temp == 0.f) {
+        p = in && row_pick(j) == v ? 1.f : 0.f;
       } else {
-        st |= PE_ST_SAMPLING;
+        const float l = in ? Elem<T>::to_f(static_cast<const T*>(a.logits)[row * a.V + v]) : -INFINITY;
+        const Stat s = row_stat(j);
+        // 64 bits: one value per draft, and a comparison with it decides
+        if (fabsf(s.m) < INFINITY)
+          p = static_cast<float>(exp((static_cast<double>(l) - static_cast<double>(s.m)) /
+                                     static_cast<double>(temp)) / static_cast<double>(s.s));
+      }
+      if (lane == 0) {
+        if (sp == 0 && a.p_draft) a.p_draft[row + 1] = p;
+        rejected = temp == 0.f ? p == 0.f : !(a.u[row + 1] < p);
+        if (rejected) atomicMin(&bad_sh, j);
       }
     }
+    if (__syncthreads_or(rejected) && sp > 0) break;
   }
+  __syncthreads();
+  const int acc = n > 0 ? min(bad_sh, n - 1) : 0;
+  const int64_t row = x.q0 + acc;
+  int bonus = -1;
+  bool race = false;
+  if (n > 0) {
+    if (warp == 0) {
+      if (temp == 0.f) {
+        bonus = row_pick(acc);
+      } else {
+        const Stat s = row_stat(acc);
+        if (lane == 0) row_sh[0] = s;
+      }
+    }
+    __syncthreads();
+    if (temp != 0.f) {
+      race = fabsf(row_sh[0].m) < INFINITY;
+      if (!race) st |= PE_ST_SAMPLING;
+    }
+  }
+  if (sp == 0 && st) atomicOr(&st_sh, st);
+  unsigned long long best = 0ull;
+  int bi = 0x7fffffff;
+  if (race) {
+    const int skip = acc + 1 < n ? a.tok[row + 1] : -1;
+    const T* lp = static_cast<const T*>(a.logits) + row * a.V;
+    const float* gp = a.gumbel + static_cast<int64_t>(r) * a.V;
+    const int c0 = sp * a.rchunk, c1 = min(a.V, c0 + a.rchunk);
+    const float it = (1.f / temp);
+    float bs = -INFINITY, bl = 0.f, bg = 0.f;
+    for (int v = c0 + tid * kRace; v < c1; v += kThreads * kRace) {
+      float l[kRace], g[kRace];
+      if (a.vec && v + kRace <= c1) {
+        unpack16<float>(ld_stream16(gp + v), g);
+        unpack16<float>(ld_stream16(gp + v + 4), g + 4);
+        unpack16<T>(*reinterpret_cast<const uint4*>(lp + v), l);
+        if (sizeof(T) == 4) unpack16<T>(*reinterpret_cast<const uint4*>(lp + v + 4), l + 4);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kRace; ++e) {
+          l[e] = v + e < c1 ? Elem<T>::to_f(lp[v + e]) : -INFINITY;
+          g[e] = v + e < c1 ? gp[v + e] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kRace; ++e) {
+        const float s = v + e == skip || l[e] == -INFINITY ? -INFINITY : fmaf(l[e], it, g[e]);
+        if (s > bs) {
+          bs = s;
+          bl = l[e];
+          bg = g[e];
+          bi = v + e;
+        }
+      }
+    }
+    // a thread's best, again in 64 bits for the comparison with the others'
+    if (bs > -INFINITY) best = score_order(static_cast<double>(bl) / static_cast<double>(temp) + bg);
+    warp_best(best, bi);
+    if (lane == 0) {
+      key_sh[warp] = best;
+      idx_sh[warp] = bi;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      best = lane < kW ? key_sh[lane] : 0ull;
+      bi = lane < kW ? idx_sh[lane] : 0x7fffffff;
+      warp_best(best, bi);
+    }
+  }
+  __syncthreads();
   if (tid == 0) {
+    if (st_sh) set_status(a.status, st_sh);
+    last_sh = 1;
+    if (race) {
+      a.best[static_cast<size_t>(r) * a.rsplits + sp] =
+          make_ulonglong2(best, static_cast<unsigned long long>(bi));
+      __threadfence();
+      last_sh = atomicAdd(&a.done[r], 1u) == static_cast<uint32_t>(a.rsplits) - 1u;
+    } else if (sp > 0) {
+      last_sh = 0;
+    }
+  }
+  __syncthreads();
+  if (!last_sh || warp != 0) return;
+  if (race) {
+    __threadfence();
+    best = 0ull;
+    bi = 0x7fffffff;
+    for (int i = lane; i < a.rsplits; i += 32) {
+      const volatile ulonglong2* e = a.best + static_cast<size_t>(r) * a.rsplits + i;
+      const unsigned long long k = e->x;
+      const int v = static_cast<int>(e->y);
+      if (k > best || (k == best && v < bi)) {
+        best = k;
+        bi = v;
+      }
+    }
+    warp_best(best, bi);
+    bonus = best ? bi : -1;
+  }
+  if (lane == 0) {
     a.accepted[r] = acc;
     a.bonus[r] = bonus;
   }
-  if (st) set_status(a.status, st);
 }
+
+size_t al256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Chunks of a row: about one wave of CTAs (six per SM) over the batch, at least one
+// 16-byte vector per thread, at most 32 KB.  Chunks of the race: four CTAs per SM, at
+// least one round per thread.
+void plan(VerifyArgs& a, int esize, int num_sms) {
+  const int vec = 16 / esize;
+  const long long total = static_cast<long long>(a.T) * a.V;
+  long long chunk = (total + 6LL * num_sms - 1) / (6LL * num_sms);
+  chunk = std::max<long long>(chunk, static_cast<long long>(kThreads) * vec);
+  chunk = std::min<long long>(chunk, kMaxChunkBytes / esize);
+  chunk = (chunk + vec - 1) / vec * vec;
+  a.chunk = static_cast<int>(chunk);
+  a.splits = static_cast<int>((a.V + chunk - 1) / chunk);
+  const long long noise = static_cast<long long>(a.B) * a.V;
+  chunk = std::max<long long>((noise + 4LL * num_sms - 1) / (4LL * num_sms), kThreads * kRace);
+  chunk = (chunk + kRace - 1) / kRace * kRace;
+  a.rchunk = static_cast<int>(std::min<long long>(chunk, 0x7ffffff8));
+  a.rsplits = static_cast<int>((a.V + chunk - 1) / chunk);
+}
+
+// the most chunks a row (one fp32 vector per thread) and a race can have
+size_t max_splits(int V) { return (static_cast<size_t>(V) + kThreads * 4 - 1) / (kThreads * 4); }
+size_t max_rsplits(int V) { return (static_cast<size_t>(V) + kThreads * kRace - 1) / (kThreads * kRace); }
+constexpr int kWsHeader = 256;
 
 }  // namespace
 }  // namespace pe
@@ -226,7 +438,8 @@ using namespace pe;
 
 extern "C" size_t pe_verify_sampled_workspace_bytes(int max_batch, int max_rows_in, int vocab) {
   if (max_batch < 0 || max_rows_in < 0 || vocab < 1) return 0;
-  return static_cast<size_t>(kWsHeader) + static_cast<size_t>(max_rows_in) * 8;
+  return kWsHeader + al256(max_rows_in * max_splits(vocab) * sizeof(uint64_t)) +
+         al256(max_batch * sizeof(uint32_t)) + max_batch * max_rsplits(vocab) * sizeof(ulonglong2);
 }
 
 extern "C" int pe_verify_sampled(int B, int T_in, const int32_t* qsl, const int32_t* tok,
@@ -251,19 +464,45 @@ extern "C" int pe_verify_sampled(int B, int T_in, const int32_t* qsl, const int3
   if (reinterpret_cast<uintptr_t>(ws) % 256 != 0) return PE_ERR_ARG;
   if (ws_bytes < pe_verify_sampled_workspace_bytes(B, T_in, vocab)) return PE_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  VerifyArgs a = {B, T_in, vocab, qsl, tok, logits, temperature, u, gumbel, accepted, bonus, p_draft,
-                  static_cast<uint32_t*>(ws),
-                  reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + kWsHeader)};
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return PE_ERR_CUDA;
+  VerifyArgs a = {};
+  a.B = B;
+  a.T = T_in;
+  a.V = vocab;
+  a.qsl = qsl;
+  a.tok = tok;
+  a.logits = logits;
+  a.temperature = temperature;
+  a.u = u;
+  a.gumbel = gumbel;
+  a.accepted = accepted;
+  a.bonus = bonus;
+  a.p_draft = p_draft;
+  plan(a, esize, sms);
+  a.vec = vocab % 8 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0 &&
+          reinterpret_cast<uintptr_t>(gumbel) % 16 == 0;
+  if (static_cast<long long>(T_in) * a.splits > 0x7fffffffLL ||
+      static_cast<long long>(B) * a.rsplits > 0x7fffffffLL)
+    return PE_ERR_UNSUPPORTED;
+  char* w = static_cast<char*>(ws);
+  a.status = reinterpret_cast<uint32_t*>(w);
+  w += kWsHeader;
+  a.rows = reinterpret_cast<uint64_t*>(w);
+  w += al256(T_in * max_splits(vocab) * sizeof(uint64_t));
+  a.done = reinterpret_cast<uint32_t*>(w);
+  w += al256(B * sizeof(uint32_t));
+  a.best = reinterpret_cast<ulonglong2*>(w);
   const bool f32 = dtype == PE_DTYPE_F32;
   if (T_in > 0) {
-    if (launch_pdl(f32 ? sampled_row_kernel<float> : sampled_row_kernel<bf16>, dim3(T_in),
-                   dim3(kThreads), 0, st, a) != cudaSuccess)
+    if (launch_pdl(f32 ? sampled_row_kernel<float> : sampled_row_kernel<bf16>,
+                   dim3(static_cast<unsigned>(T_in) * a.splits), dim3(kThreads), 0, st, a) != cudaSuccess)
       return PE_ERR_CUDA;
   } else if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) {
     return PE_ERR_CUDA;
   }
-  return launch_pdl(f32 ? sampled_request_kernel<float> : sampled_request_kernel<bf16>, dim3(B),
-                    dim3(kThreads), 0, st, a) == cudaSuccess
+  return launch_pdl(f32 ? sampled_request_kernel<float> : sampled_request_kernel<bf16>,
+                    dim3(static_cast<unsigned>(B) * a.rsplits), dim3(kThreads), 0, st, a) == cudaSuccess
              ? PE_OK
              : PE_ERR_CUDA;
 }
