@@ -21,14 +21,15 @@
 // workspace, at most two per CTA, and a second kernel joins them.  Every CTA finds
 // its piece itself from qsl and seq_len, so the host needs no lengths.
 //
-// Warps: 0-3 softmax of stream 0, 4-7 of stream 1, 8 TMA and unit list, 9 MMA.
+// Warps: 0-3 softmax of stream 0, 4-7 of stream 1, 8 TMA and unit list, 9 and 10 the
+// products of either stream.
 #include "pe_paged.h"
 #include "pe_tmem.cuh"
 
 namespace pe {
 namespace {
 
-constexpr int kThreads = 384;  // three warpgroups; warps 10 and 11 only lend their registers
+constexpr int kThreads = 384;  // three warpgroups; warp 11 only lends its registers
 constexpr int kTile = 128;        // keys per tile, rows per stream
 constexpr int kUnitRows = 256;
 constexpr int kItems = 4;         // unit descriptors in flight
@@ -42,8 +43,8 @@ template <int HD>
 struct Shape {
   static constexpr int kHalves = HD / 64;             // 128-byte columns of a row
   static constexpr int kTileBytes = kTile * HD * 2;   // K, V or Q tile
-  // ring slots (one K or V tile each): 160 KB for 64, 128 KB for 128
-  static constexpr int kSlots = HD == 64 ? 10 : 4;
+  // ring slots (one K or V tile each): 128 KB
+  static constexpr int kSlots = HD == 64 ? 8 : 4;
   static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024;
   // Steps whose S product may be issued before their P V: with head size 64, P has
   // tensor memory of its own and S is free as soon as it is in registers; with 128
@@ -146,6 +147,44 @@ PE_DEV uint64_t policy_evict_normal() {
   return p;
 }
 
+PE_DEV float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Two fp32 values in one 64-bit register, for the paired fp32 instructions (half the
+// issue slots).
+PE_DEV uint64_t pack_f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+PE_DEV void unpack_f32x2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+PE_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+PE_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// One lane of a whole warp, the same one every time.
+PE_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 PE_DEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -160,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t kv_full[S::kSlots], kv_empty[S::kSlots];
   __shared__ __align__(8) uint64_t it_full[kItems], it_empty[kItems];
-  __shared__ __align__(8) uint64_t q_full[2], s_full[2], s_free[2], p_full[2], pv_done[2], x_bar[2];
+  __shared__ __align__(8) uint64_t q_full[kItems][2], s_full[2], s_free[2], p_full[2], pv_done[2], x_bar[2];
   __shared__ __align__(8) uint64_t end_bar;
   __shared__ Unit items[kItems];
   __shared__ uint32_t mask_sh[kMasks];  // per tile: bit j = keys 8j..8j+7 were loaded
@@ -179,21 +218,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], 2);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&it_full[i], 1);
-      mbar_init(&it_empty[i], 2 * kTile + 1);
+      mbar_init(&it_empty[i], 2 * kTile + 2);
+      mbar_init(&q_full[i][0], kTile);
+      mbar_init(&q_full[i][1], kTile);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&q_full[s], kTile);
       mbar_init(&s_full[s], 1);
       mbar_init(&s_free[s], kTile);
       mbar_init(&p_full[s], kTile);
       mbar_init(&pv_done[s], 1);
       mbar_init(&x_bar[s], 2 * kTile);
     }
-    mbar_init(&end_bar, 1);
+    mbar_init(&end_bar, 2);
     abort_sh = 0;
     fence_barrier_init();
     prefetch_tmap(&kmap);
@@ -297,8 +337,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       const Unit u = items[slot];
-      mbar_arrive(&it_empty[slot]);
-      ++n_items;
       if (u.r < 0) break;
       const int nt = u.tile1 - u.tile0;
       const int rel = u.wide ? s * kTile + i : i;  // row within the unit
@@ -320,8 +358,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ch = 0; ch < HD / 8; ++ch)
           *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kTile * 128) + (((ch & 7) ^ (i & 7)) << 4)) = v[ch];
         fence_proxy_async();
-        mbar_arrive(&q_full[u.wide ? s : 0]);
       }
+      // Both groups complete both Q barriers of the slot in every unit, before they let
+      // go of it: an MMA warp that skips units (none of their tiles is its stream's)
+      // finds the barriers in step.
+      mbar_arrive(&q_full[slot][s]);
+      mbar_arrive(&it_empty[slot]);
+      ++n_items;
       const int ahead = u.wide ? S::kAhead / 2 : S::kAhead;
       const int mysteps = u.wide ? nt : (nt - s + 1) >> 1;
       float m = -INFINITY, l = 0.f;  // m: running maximum in units of log2
@@ -355,7 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < kTile; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
+          for (int c = 0; c < kTile; c += 2)
+            mx[c / 2 & 3] = max3(mx[c / 2 & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
           // raise the maximum: at the first finite score, or when it climbed far
           const bool raise = top > m + kLazy || (m == -INFINITY && top > m);
@@ -384,18 +428,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float off = m == -INFINITY ? 0.f : m;
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t sc2 = pack_f32x2(sc, sc), off2 = pack_f32x2(-off, -off);
+          uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll
           for (int c = 0; c < kTile; c += 2) {
-            const float p0 = ex2(fmaf(__uint_as_float(x[c]), sc, -off));
-            const float p1 = ex2(fmaf(__uint_as_float(x[c + 1]), sc, -off));
-            ls[c & 3] += p0;
-            ls[(c & 3) + 1] += p1;
+            float p0, p1;
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, off2),
+                         p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            ls[c / 2 & 1] = add_f32x2(ls[c / 2 & 1], pack_f32x2(p0, p1));
             // P enters the product as bf16 (relative 2^-8 at most, the size of the
             // result's own rounding); the sum l takes the unrounded weights
             x[c >> 1] = pack_bf16x2(p0, p1);
           }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          float l0, l1;
+          unpack_f32x2(add_f32x2(ls[0], ls[1]), l0, l1);
+          l += l0 + l1;
         }
         // the last P V of this stream has read P
         if (k > 0 && !wait_warp(&pv_done[s], (n_st + k - 1) & 1)) {
@@ -411,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Keys that no row sees (past the unit's last, or of a skipped block) hold
         // anything, NaN included: their V rows become 0 before the product
         const bool cut = t0 + kTile > u.kend || have != 0xffffu;
-        if (cut && (s == 0 || !u.wide)) {
+        if (cut) {
           const uint32_t idx = loads + min(nt, ahead + j) + j;
           if (!wait_warp(&kv_full[idx % S::kSlots], (idx / S::kSlots) & 1)) {
             go = false;
@@ -691,88 +740,107 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&kv_full[i % S::kSlots], (i / S::kSlots) & 1, &never);
     }
     __syncwarp();
-    } else if (warp == 9) {
-    // ---------------- MMA warp, one thread
-    if (lane == 0) {
-      uint32_t loads = 0, n_items = 0, q_a = 0, q_b = 0, st_a = 0, st_b = 0;
-      const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
-      const uint32_t idesc_o = idesc_bf16_f32(kTile, HD) | (1u << 16);  // V is MN-major
-      bool go = true;
-      while (go) {
-        const int slot = n_items % kItems;
-        if (!mbar_wait(&it_full[slot], (n_items / kItems) & 1, abort_flag)) {
-          fail();
-          break;
+    } else if (warp <= 10) {
+    // ---------------- MMA warps, one per stream: the waits of one overlap the products
+    // of the other (a single warp for both took 1436 clocks a tile of head size 64, in
+    // which the tensor pipe worked 614).  All lanes follow the steps and an elected one
+    // issues: in a branch of one lane the operands' descriptors go through vector
+    // registers for every product (955 clocks a tile against 690 in isolation).
+    const int s = warp - 9;
+    uint32_t loads = 0, seen = 0, n_items = 0, n_st = 0;
+    const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
+    const uint32_t idesc_o = idesc_bf16_f32(kTile, HD) | (1u << 16);  // V is MN-major
+    const uint32_t dS = tmem + S::kS + s * 128, dP = tmem + S::kP + s * S::kPStride;
+    const uint32_t dO = tmem + S::kO + s * HD;
+    constexpr int kOwn = S::kAhead / 2;  // this stream's S products ahead of its P V
+    bool go = true;
+    while (go) {
+      const int slot = n_items % kItems;
+      if (!wait_warp(&it_full[slot], (n_items / kItems) & 1)) {
+        fail();
+        break;
+      }
+      const Unit u = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&it_empty[slot]);
+      ++n_items;
+      if (u.r < 0) break;
+      const int nt = u.tile1 - u.tile0;
+      const int steps = u.wide ? nt : (nt - s + 1) >> 1;     // of this stream
+      const int ahead = u.wide ? S::kAhead / 2 : S::kAhead;  // K tiles before V tile 0
+      const int qb = u.wide ? s : 0;
+      // (with no step here the other stream may run units ahead: nothing to wait for)
+      if (steps > 0) go = wait_warp(&q_full[slot][qb], ((n_items - 1) / kItems) & 1);
+      const uint64_t ad = sw128_kmajor_desc(smem_u32(q_sm + qb * S::kTileBytes));
+      // Both warps see every load in order, the other stream's too: a slot's barrier
+      // then never is a phase behind or ahead of the one that is waited for.  A slot is
+      // free when both have let go of it, its users once their products are done.
+      auto take = [&](uint32_t idx) {
+        for (; seen < idx; ++seen) {
+          if (!wait_warp(&kv_full[seen % S::kSlots], (seen / S::kSlots) & 1)) return false;
+          if (elect_one()) mbar_arrive(&kv_empty[seen % S::kSlots]);
         }
-        const Unit u = items[slot];
-        mbar_arrive(&it_empty[slot]);
-        ++n_items;
-        if (u.r < 0) break;
-        const int nt = u.tile1 - u.tile0;
-        const int steps = u.wide ? 2 * nt : nt;
-        const int ahead = u.wide ? S::kAhead / 2 : S::kAhead;  // K tiles before V tile 0
-        go = mbar_wait(&q_full[0], q_a++ & 1, abort_flag);
-        if (go && u.wide) go = mbar_wait(&q_full[1], q_b++ & 1, abort_flag);
-        tc_fence_after();
-        const uint32_t base = loads;
-        auto wait_load = [&](uint32_t idx, int& st) {
-          st = idx % S::kSlots;
-          if (mbar_wait(&kv_full[st], (idx / S::kSlots) & 1, abort_flag)) return true;
-          return false;
-        };
-        // step i: stream i & 1, tile i (narrow) or i / 2 (wide), the k-th of its stream
-        auto score = [&](int i) -> bool {
-          const int s = i & 1, j = u.wide ? i >> 1 : i, k = i >> 1;
-          int st;
-          if (!wait_load(base + j + max(0, j - ahead + 1), st)) return false;
-          if (k > 0) {
-            // S of this stream's previous step is out of the way
-            uint64_t* bar = S::kAhead == 4 ? &s_free[s] : &pv_done[s];
-            if (!mbar_wait(bar, ((s ? st_b : st_a) + k - 1) & 1, abort_flag)) return false;
-          }
-          tc_fence_after();
-          const uint64_t ad = sw128_kmajor_desc(
-              smem_u32(q_sm + (u.wide ? s : 0) * S::kTileBytes));
-          const uint64_t bd = sw128_kmajor_desc(smem_u32(ring + st * S::kTileBytes));
-#pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t o = (kk >> 2) * (kTile * 128 / 16) + (kk & 3) * 2;
-            umma_bf16(tmem + S::kS + s * 128, ad + o, bd + o, idesc_s, kk > 0);
-          }
-          umma_commit(&s_full[s]);
-          if (!u.wide || (i & 1)) umma_commit(&kv_empty[st]);
-          return true;
-        };
-        auto value = [&](int i) -> bool {
-          const int s = i & 1, j = u.wide ? i >> 1 : i, k = i >> 1;
-          int st;
-          if (!wait_load(base + min(nt, ahead + j) + j, st)) return false;
-          if (!mbar_wait(&p_full[s], ((s ? st_b : st_a) + k) & 1, abort_flag)) return false;
+        return true;
+      };
+      auto wait_load = [&](uint32_t idx) {
+        if (!take(idx)) return false;
+        ++seen;
+        return wait_warp(&kv_full[idx % S::kSlots], (idx / S::kSlots) & 1);
+      };
+#pragma unroll 1
+      for (int k = -kOwn; k < steps && go; ++k) {
+        if (k >= 0) {  // O += P V of step k
+          const int j = u.wide ? k : 2 * k + s;
+          const uint32_t idx = loads + min(nt, ahead + j) + j;
+          const int st = idx % S::kSlots;
+          go = wait_load(idx) && wait_warp(&p_full[s], (n_st + k) & 1);
+          if (!go) break;
           tc_fence_after();
           const uint64_t bd = sw128_mnmajor_desc(smem_u32(ring + st * S::kTileBytes), kTile * 128);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            umma_bf16_ta(tmem + S::kO + s * HD, tmem + S::kP + s * S::kPStride + kk * 8,
-                         bd + kk * 128, idesc_o, k > 0 || kk > 0);
-          umma_commit(&pv_done[s]);
-          if (!u.wide || (i & 1)) umma_commit(&kv_empty[st]);
-          return true;
-        };
-#pragma unroll 1
-        for (int i = -S::kAhead; i < steps && go; ++i) {
-          if (i >= 0) go = value(i);
-          if (go && i + S::kAhead < steps) go = score(i + S::kAhead);
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              umma_bf16_ta(dO, dP + kk * 8, bd + kk * 128, idesc_o, k > 0 || kk > 0);
+            umma_commit(&pv_done[s]);
+            umma_commit(&kv_empty[st]);
+          }
         }
-        if (!go) fail();
-        loads += 2 * nt;
-        st_a += (steps + 1) >> 1;
-        st_b += steps >> 1;
+        const int n = k + kOwn;
+        if (n < steps) {  // S = Q K^T of step n
+          const int j = u.wide ? n : 2 * n + s;
+          const uint32_t idx = loads + j + max(0, j - ahead + 1);
+          const int st = idx % S::kSlots;
+          go = wait_load(idx);
+          // S of the step before is out of the way: in registers (S::kAhead = 4; of the
+          // unit before it is), or P has been multiplied (of the unit before too: a
+          // narrow unit's Q comes from the other stream's group)
+          if (go && (n > 0 || (S::kAhead == 2 && n_st > 0)))
+            go = wait_warp(S::kAhead == 4 ? &s_free[s] : &pv_done[s], (n_st + n - 1) & 1);
+          if (!go) break;
+          tc_fence_after();
+          const uint64_t bd = sw128_kmajor_desc(smem_u32(ring + st * S::kTileBytes));
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk) {
+              const uint32_t o = (kk >> 2) * (kTile * 128 / 16) + (kk & 3) * 2;
+              umma_bf16(dS, ad + o, bd + o, idesc_s, kk > 0);
+            }
+            umma_commit(&s_full[s]);
+            umma_commit(&kv_empty[st]);
+          }
+        }
       }
-      // nothing of this thread is running when the CTA leaves
-      int never = 0;
-      umma_commit(&end_bar);
-      mbar_wait(&end_bar, 0, &never);
+      loads += 2 * nt;
+      if (!go || !take(loads)) {
+        fail();
+        break;
+      }
+      n_st += steps;
     }
+    // nothing of this warp is running when the CTA leaves
+    int never = 0;
+    if (elect_one()) umma_commit(&end_bar);
+    mbar_wait(&end_bar, 0, &never);
     __syncwarp();
     }
   }
