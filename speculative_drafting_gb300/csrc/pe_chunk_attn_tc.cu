@@ -82,6 +82,7 @@ struct TcArgs {
   ChunkArgs c;
   int box;          // keys per TMA box
   int grid;
+  int hg_shift;     // H / G = 1 << hg_shift, -1 if it is no power of two
   int umin;         // least cost of a CTA's piece, in 128-key tiles of a narrow unit
   int overhead;     // constant cost of a unit, in the same measure
   float* part_o;    // [grid][2][part_rows][hd]
@@ -147,6 +148,11 @@ PE_DEV uint64_t policy_evict_normal() {
   return p;
 }
 
+template <int N>
+struct Const {
+  static constexpr int value = N;
+};
+
 PE_DEV float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -199,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t kv_full[S::kSlots], kv_empty[S::kSlots];
   __shared__ __align__(8) uint64_t it_full[kItems], it_empty[kItems];
-  __shared__ __align__(8) uint64_t q_full[kItems][2], s_full[2], s_free[2], p_full[2], pv_done[2], x_bar[2];
+  __shared__ __align__(8) uint64_t q_full[kItems][2], s_full[2], s_free[2], p_full[2], pv_done[2], x_bar[2], lag_bar;
   __shared__ __align__(8) uint64_t end_bar;
   __shared__ Unit items[kItems];
   __shared__ uint32_t mask_sh[kMasks];  // per tile: bit j = keys 8j..8j+7 were loaded
@@ -233,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&pv_done[s], 1);
       mbar_init(&x_bar[s], 2 * kTile);
     }
+    mbar_init(&lag_bar, kTile);
     mbar_init(&end_bar, 2);
     abort_sh = 0;
     fence_barrier_init();
@@ -330,47 +337,100 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sc = kLog2e / sqrtf(static_cast<float>(HD));
     uint32_t n_items = 0, n_st = 0, loads = 0, tiles = 0, n_x = 0;
     bool go = true;
-    while (go) {
+    // Rows move between global and shared memory a whole row per HD / 8 lanes: each
+    // instruction covers kRpi full rows of this warp's 32 (a thread per row touched 32
+    // lines per instruction: a unit boundary cost 11000 clocks, of it 6000 the results).
+    constexpr int kLpr = HD / 8, kRpi = 32 / kLpr;
+    const int own = wq * 32;
+    auto tile_at = [&](int tile, int row, int ch) {  // 16-byte chunk ch of a row, 128-byte swizzle
+      return reinterpret_cast<uint4*>(q_sm + tile * S::kTileBytes + (ch >> 3) * (kTile * 128) +
+                                      row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+    };
+    auto split = [&](int R, int& tok, int& head) {  // packed row -> token, head in the group
+      tok = p.hg_shift >= 0 ? R >> p.hg_shift : R / HG;
+      head = R - tok * HG;
+    };
+    // This lane's Q row of a unit (element offset), or whether there is none.
+    auto q_row = [&](const Unit& u, long long& off) {
+      const int rel = u.wide ? s * kTile + i : i;
+      const bool ok = rel < u.rows && (u.wide || s == 0);
+      int tok, head;
+      split(u.row0 + (ok ? rel : 0), tok, head);
+      off = (u.q0 + tok) * a.ld_q + static_cast<long long>(u.g * HG + head) * HD;
+      return ok;
+    };
+    // A unit's description stays in its slot until the unit is done: what the results
+    // need of it is read again then, not held in registers through the steps.
+    int cur = -1;  // slot of the unit at hand, -1: none is left
+    // the next unit: its Q rows start on their way to L2
+    auto next_unit = [&]() {
       const int slot = n_items % kItems;
-      if (!wait_warp(&it_full[slot], (n_items / kItems) & 1)) {
-        fail();
-        break;
+      if (!wait_warp(&it_full[slot], (n_items / kItems) & 1)) return false;
+      ++n_items;
+      cur = items[slot].r < 0 ? -1 : slot;
+      long long off;
+      if (q_row(items[slot], off)) {
+        const bf16* q = static_cast<const bf16*>(a.q) + off;
+#pragma unroll
+        for (int h = 0; h < S::kHalves; ++h)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64 * h));
       }
-      const Unit u = items[slot];
-      if (u.r < 0) break;
-      const int nt = u.tile1 - u.tile0;
-      const int rel = u.wide ? s * kTile + i : i;  // row within the unit
-      const bool row_ok = rel < u.rows;
-      const bool live = (rel & ~31) < u.rows;      // some row of this warp exists
-      const int R = u.row0 + (row_ok ? rel : 0);
-      const int tok = R / HG, head = u.g * HG + R % HG;
-      const int lim = row_ok ? u.L - u.n + tok : -1;           // last key this row sees
-      const int lim0 = u.L - u.n + u.row0 / HG;                // ... the unit's first row
-      // Q: this row into shared memory, 128-byte swizzle
-      if (u.wide || s == 0) {
-        uint8_t* dst = q_sm + (u.wide ? s : 0) * S::kTileBytes + i * 128;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const bf16*>(a.q) + (u.q0 + tok) * a.ld_q + static_cast<long long>(head) * HD);
-        uint4 v[HD / 8];
+      return true;
+    };
+    // ... into registers, once the results of the unit before have left theirs
+    uint4 qv[kLpr];
+    auto fetch_q = [&]() {
 #pragma unroll
-        for (int ch = 0; ch < HD / 8; ++ch) v[ch] = row_ok ? src[ch] : make_uint4(0, 0, 0, 0);
+      for (int it = 0; it < kLpr; ++it) qv[it] = make_uint4(0, 0, 0, 0);
+      if (cur < 0) return;
+      long long off;
+      const unsigned oks = __ballot_sync(0xffffffffu, q_row(items[cur], off));
 #pragma unroll
-        for (int ch = 0; ch < HD / 8; ++ch)
-          *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kTile * 128) + (((ch & 7) ^ (i & 7)) << 4)) = v[ch];
+      for (int it = 0; it < kLpr; ++it) {
+        const int src = it * kRpi + lane / kLpr;
+        const long long o = __shfl_sync(0xffffffffu, off, src);
+        if (oks >> src & 1)
+          qv[it] = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + o + lane % kLpr * 8);
+      }
+    };
+    if (!next_unit()) {
+      fail();
+      cur = -1;
+    }
+    fetch_q();
+    while (cur >= 0) {
+      const int slot = cur;
+      const int nt = items[slot].tile1 - items[slot].tile0;
+      const bool wide = items[slot].wide;
+      const int rel = wide ? s * kTile + i : i;           // row within the unit
+      const bool row_ok = rel < items[slot].rows;
+      const bool live = (rel & ~31) < items[slot].rows;   // some row of this warp exists
+      const int kend = items[slot].kend, tile0 = items[slot].tile0;
+      int lim, lim0;  // the last key that this row sees, and the unit's first row
+      {
+        int tok, head;
+        split(items[slot].row0 + rel, tok, head);
+        const int p0 = items[slot].L - items[slot].n;
+        lim = row_ok ? p0 + tok : -1;
+        split(items[slot].row0, tok, head);
+        lim0 = p0 + tok;
+      }
+      if (wide || s == 0) {
+#pragma unroll
+        for (int it = 0; it < kLpr; ++it)
+          *tile_at(wide ? s : 0, own + it * kRpi + lane / kLpr, lane % kLpr) = qv[it];
         fence_proxy_async();
       }
       // Both groups complete both Q barriers of the slot in every unit, before they let
       // go of it: an MMA warp that skips units (none of their tiles is its stream's)
       // finds the barriers in step.
       mbar_arrive(&q_full[slot][s]);
-      mbar_arrive(&it_empty[slot]);
-      ++n_items;
-      const int ahead = u.wide ? S::kAhead / 2 : S::kAhead;
-      const int mysteps = u.wide ? nt : (nt - s + 1) >> 1;
+      const int ahead = wide ? S::kAhead / 2 : S::kAhead;
+      const int mysteps = wide ? nt : (nt - s + 1) >> 1;
       float m = -INFINITY, l = 0.f;  // m: running maximum in units of log2
       for (int k = 0; k < mysteps; ++k) {
-        const int j = u.wide ? k : 2 * k + s;
-        const int t0 = (u.tile0 + j) * kTile;
+        const int j = wide ? k : 2 * k + s;
+        const int t0 = (tile0 + j) * kTile;
         if (!wait_warp(&s_full[s], (n_st + k) & 1)) {
           go = false;
           break;
@@ -459,14 +519,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // Keys that no row sees (past the unit's last, or of a skipped block) hold
         // anything, NaN included: their V rows become 0 before the product
-        const bool cut = t0 + kTile > u.kend || have != 0xffffu;
+        const bool cut = t0 + kTile > kend || have != 0xffffu;
         if (cut) {
           const uint32_t idx = loads + min(nt, ahead + j) + j;
           if (!wait_warp(&kv_full[idx % S::kSlots], (idx / S::kSlots) & 1)) {
             go = false;
             break;
           }
-          if (t0 + i >= u.kend || !(have >> (i >> 3) & 1u)) {
+          if (t0 + i >= kend || !(have >> (i >> 3) & 1u)) {
             uint8_t* v = ring + (idx % S::kSlots) * S::kTileBytes + i * 128;
 #pragma unroll
             for (int ch = 0; ch < HD / 8; ++ch)
@@ -477,9 +537,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(&p_full[s]);
+        if (S::kAhead == 4 && wide && s == 0 && k == 0) mbar_arrive(&lag_bar);
       }
-      if (go && mysteps > 0 && !wait_warp(&pv_done[s], (n_st + mysteps - 1) & 1)) go = false;
       if (!go) {
+        fail();
+        break;
+      }
+      // the next unit's Q, then the last P V of this one
+      if (!next_unit() || (mysteps > 0 && !wait_warp(&pv_done[s], (n_st + mysteps - 1) & 1))) {
         fail();
         break;
       }
@@ -487,14 +552,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       loads += 2 * nt;
       tiles += nt;
       tc_fence_after();
-      // ---------------- results
-      const float sk = u.whole && a.sink && row_ok ? a.sink[head] * kLog2e : -INFINITY;
-      const int slot_p = u.tile0 > 0 ? 0 : 1;
-      const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + slot_p) * p.part_rows + rel;
-      bf16* out = static_cast<bf16*>(a.out) + (u.q0 + tok) * a.ld_out + static_cast<long long>(head) * HD;
+      const bool whole = items[slot].whole;
+      int tok, head;
+      split(items[slot].row0 + (row_ok ? rel : 0), tok, head);
+      head += items[slot].g * HG;
+      const long long out_off = (items[slot].q0 + tok) * a.ld_out + static_cast<long long>(head) * HD;
+      const size_t prow =
+          (static_cast<size_t>(blockIdx.x) * 2 + (tile0 > 0 ? 0 : 1)) * p.part_rows + rel;
+      const float sk = whole && a.sink && row_ok ? a.sink[head] * kLog2e : -INFINITY;
+      // ---------------- results: through this stream's Q tile (whole units), or as fp32
+      // partials straight to the workspace
       auto emit = [&](int col, uint32_t* o, float f) {  // 32 columns from col
-        if (!row_ok) return;
-        if (u.whole) {
+        if (whole) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t w[4];
@@ -502,23 +571,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 4; ++e)
               w[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * f,
                                  __uint_as_float(o[8 * c + 2 * e + 1]) * f);
-            reinterpret_cast<uint4*>(out + col)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+            *tile_at(s, i, col / 8 + c) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        } else {
+        } else if (row_ok) {
           uint4* d = reinterpret_cast<uint4*>(p.part_o + prow * HD + col);
 #pragma unroll
           for (int c = 0; c < 8; ++c) d[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
         }
       };
+      // chunks [c0, c0 + n) of this warp's rows out of the tile, n lanes a row
+      const unsigned oks = __ballot_sync(0xffffffffu, row_ok);
+      auto flush = [&](int c0, auto n_) {
+        constexpr int n = decltype(n_)::value, rpi = 32 / n;
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < n; ++it) {
+          const int src = it * rpi + lane / n;
+          const long long o = __shfl_sync(0xffffffffu, out_off, src);
+          if (oks >> src & 1)
+            *reinterpret_cast<uint4*>(static_cast<bf16*>(a.out) + o + (c0 + lane % n) * 8) =
+                *tile_at(s, own + src, c0 + lane % n);
+        }
+        __syncwarp();
+      };
       // factor of the unnormalised O of a row with (M, den): a sink joins both
       auto factor = [&](float M, float den) {
-        if (!u.whole) return 1.f;
+        if (!whole) return 1.f;
         const float top = fmaxf(M, sk);
         if (top == -INFINITY || den == 0.f) return 0.f;
         const float e = ex2(M - top);
         return e / (den * e + (sk == -INFINITY ? 0.f : ex2(sk - top)));
       };
-      if (u.wide) {
+      if (wide) {
         const float f = factor(m, l);
         if (live) {
 #pragma unroll
@@ -530,7 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             emit(32 * b, o, f);
           }
         }
-        if (!u.whole && row_ok) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
+        fetch_q();
+        if (live && whole) flush(0, Const<kLpr>{});
+        if (!whole && row_ok) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
         tc_fence_before();
       } else {
         // the two streams' states of the same row join; each group writes half the columns
@@ -545,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float m0 = ml_sh[0][i][0], m1 = ml_sh[1][i][0];
         const float M = fmaxf(m0, m1);
-        float w0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), w1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+        const float w0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), w1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
         const float den = ml_sh[0][i][1] * w0 + ml_sh[1][i][1] * w1;
         const float f = factor(M, den);
         if (live) {
@@ -568,7 +654,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             emit(col, o, f);
           }
         }
-        if (!u.whole && row_ok && s == 0)
+        fetch_q();
+        if (live && whole) flush(s * (kLpr / 2), Const<kLpr / 2>{});
+        if (!whole && row_ok && s == 0)
           *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(M, den);
         // the other group may still read this stream's O (and ml_sh)
         tc_fence_before();
@@ -579,6 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++n_x;
       }
+      mbar_arrive(&it_empty[slot]);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -592,13 +681,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool go = true;
     const uint64_t once = policy_evict_first(), kept = policy_evict_normal();
     const int gpt = kTile / p.box;  // boxes per tile
+    Req q;
+    int q_of = -1;
     while (go) {
       if (cur.g > last.g || (cur.g == last.g && (cur.r > last.r || (cur.r == last.r && cur.qt > last.qt))))
         break;
       const bool ends_here = cur.g == last.g && cur.r == last.r && cur.qt == last.qt;
       if (ends_here && last.tile <= cur.tile) break;
       if (cur.g >= a.G) break;
-      const Req q = load_req(a, cur.r, false);
+      if (cur.r != q_of) {
+        q = load_req(a, cur.r, false);
+        q_of = cur.r;
+      }
       Unit u;
       u.r = cur.r;
       u.g = cur.g;
@@ -725,6 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = n_items % kItems;
       if (n_items < kItems || mbar_wait(&it_empty[slot], (n_items / kItems - 1) & 1, abort_flag)) {
         items[slot].r = -1;
+        items[slot].rows = items[slot].wide = items[slot].row0 = 0;
         mbar_arrive(&it_full[slot]);
       }
       int* rec = p.rec + blockIdx.x * 8;
@@ -747,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // issues: in a branch of one lane the operands' descriptors go through vector
     // registers for every product (955 clocks a tile against 690 in isolation).
     const int s = warp - 9;
-    uint32_t loads = 0, seen = 0, n_items = 0, n_st = 0;
+    uint32_t loads = 0, seen = 0, n_items = 0, n_st = 0, n_wide = 0;
     const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
     const uint32_t idesc_o = idesc_bf16_f32(kTile, HD) | (1u << 16);  // V is MN-major
     const uint32_t dS = tmem + S::kS + s * 128, dP = tmem + S::kP + s * S::kPStride;
@@ -771,6 +866,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qb = u.wide ? s : 0;
       // (with no step here the other stream may run units ahead: nothing to wait for)
       if (steps > 0) go = wait_warp(&q_full[slot][qb], ((n_items - 1) / kItems) & 1);
+      // Stream 1 of a wide unit starts when stream 0 has its first weights: the two then
+      // stay out of step, one's exponentials beside the other's waits.
+      if (S::kAhead == 4 && go && s == 1 && u.wide) go = wait_warp(&lag_bar, n_wide++ & 1);
       const uint64_t ad = sw128_kmajor_desc(smem_u32(q_sm + qb * S::kTileBytes));
       // Both warps see every load in order, the other stream's too: a slot's barrier
       // then never is a phase behind or ahead of the one that is waited for.  A slot is
@@ -948,9 +1046,13 @@ int launch_chunk_tc(const ChunkArgs& a, char* ws, cudaStream_t st) {
   const int sms = num_sms_of_current_device();
   if (sms <= 0) return PE_ERR_CUDA;
   p.grid = sms < kMaxGrid ? sms : kMaxGrid;
+  const int HG = a.H / a.G;
+  p.hg_shift = -1;
+  for (int i = 0; i < 8; ++i)
+    if (HG == 1 << i) p.hg_shift = i;
   p.umin = 2;
   p.overhead = 1;
-  p.part_rows = part_rows_of(a.T, a.H / a.G);
+  p.part_rows = part_rows_of(a.T, HG);
   p.rec = reinterpret_cast<int*>(ws + 256);
   p.part_ml = reinterpret_cast<float*>(ws + 256 + rec_bytes());
   p.part_o = reinterpret_cast<float*>(ws + 256 + rec_bytes() + ml_bytes(p.part_rows));

@@ -32,7 +32,6 @@ constexpr int kThreads = 256;
 constexpr int kUnroll = 4;            // 16-byte loads in flight per thread
 constexpr int kMaxChunkBytes = 32768; // of a row, per CTA of the row kernel
 constexpr int kRace = 8;              // logits per thread and round of the race
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct VerifyArgs {
   int B, T, V;
@@ -94,8 +93,10 @@ PE_DEV int request_of(const VerifyArgs& a, int row, int lane) {
   return lo;
 }
 
-// Running maximum m and sum s of exp2((l - m) c).  A NaN logit makes m NaN, a +inf
-// one makes it +inf: neither row has a distribution.
+// Largest logit m seen and the sum s of 2^((l - m) c), c = log2(e) / T.  The difference
+// is formed first: it is exact near the largest logit, whatever its size.  A NaN logit
+// makes m NaN, a +inf one +inf: neither row has a distribution (nor has one of -inf
+// alone).
 struct Stat {
   float m, s;
 };
@@ -105,6 +106,32 @@ PE_DEV Stat join(const Stat& x, const Stat& y, float c) {
   const float off = z.m == -INFINITY ? 0.f : z.m;
   z.s = x.s * ex2((x.m - off) * c) + y.s * ex2((y.m - off) * c);
   return z;
+}
+
+// log2(e) / T rounded once (a division and a correction by its remainder)
+PE_DEV float scale_of(float temp) {
+  const float hi = 1.44269502162933349609375f, lo = 1.925963033500011e-8f;  // log2(e)
+  const float q = hi / temp;
+  return q + (fmaf(-q, temp, hi) + lo) / temp;
+}
+
+// Largest element of a 16-byte vector, NaN if it holds one.
+PE_DEV uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <typename T>
+PE_DEV float vec_max(const uint4& u);
+template <>
+PE_DEV float vec_max<float>(const uint4& u) {
+  return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)),
+                 max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
+}
+template <>
+PE_DEV float vec_max<bf16>(const uint4& u) {
+  const uint32_t p = max_nan_bf16x2(max_nan_bf16x2(u.x, u.y), max_nan_bf16x2(u.z, u.w));
+  return max_nan(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
 }
 
 template <typename T>
@@ -165,32 +192,28 @@ __global__ void __launch_bounds__(kThreads, 6) sampled_row_kernel(const VerifyAr
     }
     return;
   }
-  const float c = (1.f / temp) * kLog2e;
+  const float c = scale_of(temp);
   Stat st{-INFINITY, 0.f};
   if (tid < head) st = join(st, Stat{Elem<T>::to_f(base[c0 + tid]), 1.f}, c);
   if (t0 + tid < c1) st = join(st, Stat{Elem<T>::to_f(base[t0 + tid]), 1.f}, c);
   for (int j = tid; j < nvec; j += kUnroll * kThreads) {
     // one maximum and one rescaling for the kUnroll vectors
-    float f[kUnroll][kVec];
     float m = st.m;
 #pragma unroll
-    for (int x = 0; x < kUnroll; ++x) {
-      unpack16<T>(u[x], f[x]);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) m = max_nan(m, f[x][e]);
-    }
-    const int jn = j + kUnroll * kThreads;
-#pragma unroll
-    for (int x = 0; x < kUnroll; ++x)
-      u[x] = jn + x * kThreads < nvec ? ld_stream16(vp + jn + x * kThreads) : none;
+    for (int x = 0; x < kUnroll; ++x) m = max_nan(m, vec_max<T>(u[x]));
     const float off = m == -INFINITY ? 0.f : m;
     st.s *= ex2((st.m - off) * c);
     st.m = m;
+    const int jn = j + kUnroll * kThreads;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int x = 0; x < kUnroll; ++x)
+    for (int x = 0; x < kUnroll; ++x) {
+      float f[kVec];
+      unpack16<T>(u[x], f);
+      u[x] = jn + x * kThreads < nvec ? ld_stream16(vp + jn + x * kThreads) : none;
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) s[e & 3] += ex2((f[x][e] - off) * c);
+      for (int e = 0; e < kVec; ++e) s[e & 3] += ex2((f[e] - off) * c);
+    }
     st.s += (s[0] + s[1]) + (s[2] + s[3]);
   }
 #pragma unroll
@@ -198,10 +221,14 @@ __global__ void __launch_bounds__(kThreads, 6) sampled_row_kernel(const VerifyAr
     st = join(st, Stat{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o)}, c);
   if (lane == 0) st_sh[warp] = st;
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kThreads / 32; ++w) st = join(st, st_sh[w], c);
-    a.rows[static_cast<size_t>(row) * a.splits + sp] =
-        (static_cast<uint64_t>(__float_as_uint(st.m)) << 32) | __float_as_uint(st.s);
+  if (warp == 0) {
+    st = lane < kThreads / 32 ? st_sh[lane] : Stat{-INFINITY, 0.f};
+#pragma unroll
+    for (int o = 4; o; o >>= 1)
+      st = join(st, Stat{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o)}, c);
+    if (lane == 0)
+      a.rows[static_cast<size_t>(row) * a.splits + sp] =
+          (static_cast<uint64_t>(__float_as_uint(st.m)) << 32) | __float_as_uint(st.s);
   }
 }
 
@@ -229,7 +256,8 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
   constexpr int kW = kThreads / 32;
   __shared__ int bad_sh, last_sh;
   __shared__ uint32_t st_sh;
-  __shared__ Stat row_sh[kW];
+  __shared__ int pick_sh[kW];
+  __shared__ float top_sh[kW];
   __shared__ unsigned long long key_sh[kW];
   __shared__ int idx_sh[kW];
   pdl_trigger();
@@ -249,10 +277,12 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
     if (sp == 0 && n > 0 && a.p_draft) a.p_draft[x.q0] = 1.f;
   }
   __syncthreads();
+  int acc = 0, pick_acc = -1;
+  bool found = false;
   // One warp per row, in order: the row's statistics (or key), then the draft after
   // it.  The first CTA goes through all rows (p_draft), the others stop behind the
   // first rejection.
-  const float c = (1.f / temp) * kLog2e;
+  const float c = temp == 0.f ? 1.f : scale_of(temp);
   const size_t rs = static_cast<size_t>(x.q0) * a.splits;
   auto row_stat = [&](int j) {
     Stat s{-INFINITY, 0.f};
@@ -272,53 +302,50 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
       k = max(k, static_cast<unsigned long long>(a.rows[rs + static_cast<size_t>(j) * a.splits + i]));
     return static_cast<int>(~static_cast<uint32_t>(warp_max_u64(k)));
   };
-  for (int j0 = 0; j0 + 1 < n; j0 += kW) {
+  for (int j0 = 0; j0 < n; j0 += kW) {
     const int j = j0 + warp;
     int rejected = 0;
-    if (j + 1 < n) {
+    if (j < n) {
       const int64_t row = x.q0 + j;
-      const int v = a.tok[row + 1];
-      float p = 0.f;
+      const bool draft = j + 1 < n;
+      const int v = draft ? a.tok[row + 1] : -1;
       const bool in = v >= 0 && v < a.V;
-      if (!in) st |= PE_ST_TOKEN_RANGE;
+      float p = 0.f;
+      int pick = -1;
       if (temp == 0.f) {
-        p = in && row_pick(j) == v ? 1.f : 0.f;
+        pick = row_pick(j);
+        p = in && pick == v ? 1.f : 0.f;
       } else {
         const float l = in ? Elem<T>::to_f(static_cast<const T*>(a.logits)[row * a.V + v]) : -INFINITY;
+        const float u = draft ? a.u[row + 1] : 0.f;
         const Stat s = row_stat(j);
-        // 64 bits: one value per draft, and a comparison with it decides
-        if (fabsf(s.m) < INFINITY)
-          p = static_cast<float>(exp((static_cast<double>(l) - static_cast<double>(s.m)) /
-                                     static_cast<double>(temp)) / static_cast<double>(s.s));
+        pick = fabsf(s.m) < INFINITY ? 0 : -1;  // whether the row has a distribution
+        if (pick == 0) p = fminf(ex2((l - s.m) * c) / s.s, 1.f);
+        rejected = !(u < p);
       }
+      if (temp == 0.f) rejected = p == 0.f;
+      rejected &= draft;
+      if (draft && !in) st |= PE_ST_TOKEN_RANGE;
       if (lane == 0) {
-        if (sp == 0 && a.p_draft) a.p_draft[row + 1] = p;
-        rejected = temp == 0.f ? p == 0.f : !(a.u[row + 1] < p);
+        if (draft && sp == 0 && a.p_draft) a.p_draft[row + 1] = p;
         if (rejected) atomicMin(&bad_sh, j);
+        pick_sh[warp] = pick;
       }
     }
-    if (__syncthreads_or(rejected) && sp > 0) break;
-  }
-  __syncthreads();
-  const int acc = n > 0 ? min(bad_sh, n - 1) : 0;
-  const int64_t row = x.q0 + acc;
-  int bonus = -1;
-  bool race = false;
-  if (n > 0) {
-    if (warp == 0) {
-      if (temp == 0.f) {
-        bonus = row_pick(acc);
-      } else {
-        const Stat s = row_stat(acc);
-        if (lane == 0) row_sh[0] = s;
-      }
+    // the first rejection (or the last row) decides what the next token comes from
+    const bool any = __syncthreads_or(rejected);
+    if (!found && (any || j0 + kW >= n)) {
+      found = true;
+      acc = min(bad_sh, n - 1);
+      pick_acc = pick_sh[acc - j0];
     }
     __syncthreads();
-    if (temp != 0.f) {
-      race = fabsf(row_sh[0].m) < INFINITY;
-      if (!race) st |= PE_ST_SAMPLING;
-    }
+    if (found && sp > 0) break;
   }
+  const int64_t row = x.q0 + acc;
+  int bonus = temp == 0.f ? pick_acc : -1;
+  const bool race = n > 0 && temp != 0.f && pick_acc == 0;
+  if (n > 0 && temp != 0.f && !race) st |= PE_ST_SAMPLING;
   if (sp == 0 && st) atomicOr(&st_sh, st);
   unsigned long long best = 0ull;
   int bi = 0x7fffffff;
@@ -354,8 +381,18 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
         }
       }
     }
-    // a thread's best, again in 64 bits for the comparison with the others'
-    if (bs > -INFINITY) best = score_order(static_cast<double>(bl) / static_cast<double>(temp) + bg);
+    // The threads whose best is within reach of the CTA's compare in 64 bits (doubles are
+    // slow here: by then it is one or two of the 256).
+    float top = warp_max(bs);
+    if (lane == 0) top_sh[warp] = top;
+    __syncthreads();
+    top = top_sh[0];
+#pragma unroll
+    for (int w = 1; w < kW; ++w) top = fmaxf(top, top_sh[w]);
+    if (bs > -INFINITY && bs >= top - 1e-5f * fmaxf(fabsf(top), fabsf(bl * it)))
+      best = score_order(static_cast<double>(bl) / static_cast<double>(temp) + bg);
+    else
+      bi = 0x7fffffff;
     warp_best(best, bi);
     if (lane == 0) {
       key_sh[warp] = best;
