@@ -153,12 +153,6 @@ struct Const {
   static constexpr int value = N;
 };
 
-PE_DEV float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // Two fp32 values in one 64-bit register, for the paired fp32 instructions (half the
 // issue slots).
 PE_DEV uint64_t pack_f32x2(float a, float b) {
@@ -338,8 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n_items = 0, n_st = 0, loads = 0, tiles = 0, n_x = 0;
     bool go = true;
     // Rows move between global and shared memory a whole row per HD / 8 lanes: each
-    // instruction covers kRpi full rows of this warp's 32 (a thread per row touched 32
-    // lines per instruction: a unit boundary cost 11000 clocks, of it 6000 the results).
+    // instruction covers kRpi full rows of this warp's 32.  These loops, and those over
+    // the columns of O, stay rolled: a unit boundary runs cold code, and unrolled it
+    // cost 5000 (head size 64) to 12000 clocks (128) for its instruction fetches.
     constexpr int kLpr = HD / 8, kRpi = 32 / kLpr;
     const int own = wq * 32;
     auto tile_at = [&](int tile, int row, int ch) {  // 16-byte chunk ch of a row, 128-byte swizzle
@@ -377,27 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    // ... into registers, once the results of the unit before have left theirs
-    uint4 qv[kLpr];
-    auto fetch_q = [&]() {
-#pragma unroll
-      for (int it = 0; it < kLpr; ++it) qv[it] = make_uint4(0, 0, 0, 0);
-      if (cur < 0) return;
-      long long off;
-      const unsigned oks = __ballot_sync(0xffffffffu, q_row(items[cur], off));
-#pragma unroll
-      for (int it = 0; it < kLpr; ++it) {
-        const int src = it * kRpi + lane / kLpr;
-        const long long o = __shfl_sync(0xffffffffu, off, src);
-        if (oks >> src & 1)
-          qv[it] = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + o + lane % kLpr * 8);
-      }
-    };
     if (!next_unit()) {
       fail();
       cur = -1;
     }
-    fetch_q();
     while (cur >= 0) {
       const int slot = cur;
       const int nt = items[slot].tile1 - items[slot].tile0;
@@ -416,9 +394,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         lim0 = p0 + tok;
       }
       if (wide || s == 0) {
-#pragma unroll
-        for (int it = 0; it < kLpr; ++it)
-          *tile_at(wide ? s : 0, own + it * kRpi + lane / kLpr, lane % kLpr) = qv[it];
+        long long off;
+        const unsigned oks = __ballot_sync(0xffffffffu, q_row(items[slot], off));
+#pragma unroll 2
+        for (int it = 0; it < kLpr; ++it) {
+          const int src = it * kRpi + lane / kLpr, ch = lane % kLpr;
+          const long long o = __shfl_sync(0xffffffffu, off, src);
+          cp_async16(smem_u32(tile_at(wide ? s : 0, own + src, ch)),
+                     static_cast<const bf16*>(a.q) + o + ch * 8, oks >> src & 1);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
         fence_proxy_async();
       }
       // Both groups complete both Q barriers of the slot in every unit, before they let
@@ -439,28 +425,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t have = mask_sh[(tiles + j) % kMasks];
         const bool inner = t0 + kTile - 1 <= lim0 && have == 0xffffu;
         uint32_t x[kTile];
+        float best = -INFINITY;  // this row's largest score of the tile
         if (live) {
+          if (inner) {
+            uint32_t mx[4];
 #pragma unroll
-          for (int b = 0; b < 4; ++b) tmem_ld32_issue(tS + 32 * b, x + 32 * b);
-          tmem_wait_ld();
+            for (int b = 0; b < 4; ++b) tmem_ld32_max_issue(tS + 32 * b, x + 32 * b, mx[b]);
+            tmem_wait_ld();
 #pragma unroll
-          for (int b = 0; b < 4; ++b) tmem_use32(x + 32 * b);
+            for (int b = 0; b < 4; ++b) {
+              tmem_use32(x + 32 * b);
+              tmem_use(mx[b]);
+              best = fmaxf(best, __uint_as_float(mx[b]));
+            }
+          } else {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tmem_ld32_issue(tS + 32 * b, x + 32 * b);
+            tmem_wait_ld();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tmem_use32(x + 32 * b);
+#pragma unroll
+            for (int c = 0; c < kTile; ++c) {
+              if (t0 + c > lim || !(have >> (c >> 3) & 1u)) x[c] = 0xff800000u;
+              best = fmaxf(best, __uint_as_float(x[c]));
+            }
+          }
         }
         if (S::kAhead == 4) {
           tc_fence_before();
           mbar_arrive(&s_free[s]);
         }
         if (live) {
-          if (!inner) {
-#pragma unroll
-            for (int c = 0; c < kTile; ++c)
-              if (t0 + c > lim || !(have >> (c >> 3) & 1u)) x[c] = 0xff800000u;
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < kTile; c += 2)
-            mx[c / 2 & 3] = max3(mx[c / 2 & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+          const float top = best * sc;
           // raise the maximum: at the first finite score, or when it climbed far
           const bool raise = top > m + kLazy || (m == -INFINITY && top > m);
           if (__any_sync(0xffffffffu, raise)) {
@@ -474,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
               }
               tc_fence_after();
-#pragma unroll
+#pragma unroll 1
               for (int b = 0; b < HD / 32; ++b) {
                 uint32_t o[32];
                 tmem_ld32_issue(tm + S::kO + s * HD + 32 * b, o);
@@ -584,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto flush = [&](int c0, auto n_) {
         constexpr int n = decltype(n_)::value, rpi = 32 / n;
         __syncwarp();
-#pragma unroll
+#pragma unroll 2
         for (int it = 0; it < n; ++it) {
           const int src = it * rpi + lane / n;
           const long long o = __shfl_sync(0xffffffffu, out_off, src);
@@ -605,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (wide) {
         const float f = factor(m, l);
         if (live) {
-#pragma unroll
+#pragma unroll 1
           for (int b = 0; b < HD / 32; ++b) {
             uint32_t o[32];
             tmem_ld32_issue(tm + S::kO + s * HD + 32 * b, o);
@@ -614,7 +610,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             emit(32 * b, o, f);
           }
         }
-        fetch_q();
         if (live && whole) flush(0, Const<kLpr>{});
         if (!whole && row_ok) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
         tc_fence_before();
@@ -635,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float den = ml_sh[0][i][1] * w0 + ml_sh[1][i][1] * w1;
         const float f = factor(M, den);
         if (live) {
-#pragma unroll
+#pragma unroll 1
           for (int b = 0; b < HD / 64; ++b) {
             const int col = s * (HD / 2) + 32 * b;
             uint32_t o[32];
@@ -654,7 +649,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             emit(col, o, f);
           }
         }
-        fetch_q();
         if (live && whole) flush(s * (kLpr / 2), Const<kLpr / 2>{});
         if (!whole && row_ok && s == 0)
           *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(M, den);

@@ -25,6 +25,24 @@ PE_DEV void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
       : "memory");
 }
 
+// The same load, and the largest of the thread's 32 columns read as fp32 (NaN ignored,
+// as by fmaxf) in m.
+PE_DEV void tmem_ld32_max_issue(uint32_t taddr, uint32_t* r, uint32_t& m) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31 "
+      "}, %32, [%33];"
+      :
+        "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(m)
+      : "r"(taddr)
+      : "memory");
+}
+
 PE_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 PE_DEV void tmem_use32(uint32_t* r) {
@@ -38,6 +56,9 @@ PE_DEV void tmem_use32(uint32_t* r) {
                :
                : "memory");
 }
+
+// ... and the maximum of tmem_ld32_max_issue
+PE_DEV void tmem_use(uint32_t& m) { asm volatile("" : "+r"(m) : : "memory"); }
 
 PE_DEV void tmem_st32_issue(uint32_t taddr, const uint32_t* r) {
   asm volatile(
