@@ -43,6 +43,8 @@ template <int HD>
 struct Shape {
   static constexpr int kHalves = HD / 64;             // 128-byte columns of a row
   static constexpr int kTileBytes = kTile * HD * 2;   // K, V or Q tile
+  // bytes from one group of 8 keys of a K or V tile to the next (load_box)
+  static constexpr int kGroupBytes = 1024 * kHalves;
   // ring slots (one K or V tile each): 128 KB
   static constexpr int kSlots = HD == 64 ? 8 : 4;
   static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024;
@@ -146,6 +148,22 @@ PE_DEV uint64_t policy_evict_normal() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
+}
+
+// One box of keys: rows `row` .. of the cache.  Head size 64: [keys][128 bytes].  Head
+// size 128: both 128-byte halves of 8 keys at a time, [keys / 8][half][8][128 bytes], so
+// that one copy brings whole rows (a copy per half took twice the TMA's time).
+template <int HD>
+PE_DEV void load_box(void* dst, const CUtensorMap* map, uint64_t* bar, int row, uint64_t policy) {
+  if (HD == 64) {
+    tma_load_2d(dst, map, bar, 0, row, policy);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::"
+        "cache_hint [%0], [%1, {%3, %3, %3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(row >> 3), "l"(policy)
+        : "memory");
+  }
 }
 
 template <int N>
@@ -523,11 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           if (t0 + i >= kend || !(have >> (i >> 3) & 1u)) {
-            uint8_t* v = ring + (idx % S::kSlots) * S::kTileBytes + i * 128;
+            uint8_t* v = ring + (idx % S::kSlots) * S::kTileBytes + (i >> 3) * S::kGroupBytes + (i & 7) * 128;
 #pragma unroll
             for (int ch = 0; ch < HD / 8; ++ch)
-              *reinterpret_cast<uint4*>(v + (ch >> 3) * (kTile * 128) + ((ch & 7) << 4)) =
-                  make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(v + (ch >> 3) * 1024 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async();
         }
@@ -748,46 +765,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       kw.next = block_of(kw.n + 1);
       vw = kw;
       auto load = [&](int j, bool is_v, Window& w) {  // tile j of the unit
-        const int t = u.tile0 + j;
-        if (t * gpt / 32 != w.n) {
+        const int box0 = (u.tile0 + j) * gpt;
+        if (box0 >> 5 != w.n) {
           ++w.n;
           w.row = row_of(w.n, w.next);
           w.next = block_of(w.n + 1);
         }
-        const int b0 = t * gpt & 31;
-        const bool in = lane >= b0 && lane < b0 + gpt;
-        const unsigned have = __ballot_sync(0xffffffffu, in && w.row >= 0);
+        const int b0 = box0 & 31;
+        const bool mine = lane >= b0 && lane < b0 + gpt && w.row >= 0;
+        const unsigned have = __ballot_sync(0xffffffffu, mine);
         const int st = loads % S::kSlots;
-        int ok = 1;
-        if (lane == 0) {
-          if (loads >= S::kSlots) ok = mbar_wait(&kv_empty[st], (loads / S::kSlots - 1) & 1, abort_flag);
-          if (ok) {
-            if (!is_v) {
-              // the boxes' bits, widened to groups of 8 keys
-              uint32_t m = 0;
-              const int w8 = p.box / 8;
-              for (int b = 0; b < gpt; ++b)
-                if (have >> (b0 + b) & 1) m |= ((1u << w8) - 1u) << (b * w8);
-              mask_sh[tiles % kMasks] = m;
-            }
-            mbar_arrive_expect_tx(&kv_full[st], __popc(have) * p.box * HD * 2);
-          } else {
-            fail();
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!is_v) ++tiles;
-        if (!ok) {
+        if (loads >= S::kSlots && !wait_warp(&kv_empty[st], (loads / S::kSlots - 1) & 1)) {
+          fail();
           go = false;
           return;
         }
-        if (in && w.row >= 0) {
-          uint8_t* dst = ring + st * S::kTileBytes + (lane - b0) * p.box * 128;
-          for (int h = 0; h < S::kHalves; ++h)
-            tma_load_2d(dst + h * (kTile * 128), is_v ? &vmap : &kmap, &kv_full[st], h * 64, w.row,
-                        u.wide ? kept : once);
+        const int n = __popc(have);
+        if (lane == 0) {
+          if (!is_v) {
+            uint32_t m = 0xffffu;  // the boxes' bits, widened to groups of 8 keys
+            if (n < gpt) {
+              m = 0;
+              const int w8 = p.box / 8;
+              for (int b = 0; b < gpt; ++b)
+                if (have >> (b0 + b) & 1) m |= ((1u << w8) - 1u) << (b * w8);
+            }
+            mask_sh[tiles % kMasks] = m;
+          }
+          mbar_arrive_expect_tx(&kv_full[st], n * p.box * HD * 2);
         }
+        tiles += !is_v;
         __syncwarp();
+        if (mine)
+          load_box<HD>(ring + st * S::kTileBytes + (lane - b0) * p.box * HD * 2, is_v ? &vmap : &kmap,
+                       &kv_full[st], w.row, u.wide ? kept : once);
         ++loads;
       };
 #pragma unroll 1
@@ -841,6 +852,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc_o = idesc_bf16_f32(kTile, HD) | (1u << 16);  // V is MN-major
     const uint32_t dS = tmem + S::kS + s * 128, dP = tmem + S::kP + s * S::kPStride;
     const uint32_t dO = tmem + S::kO + s * HD;
+    // the stride between groups of 8 keys, past the 1024 bytes of the descriptors' default
+    constexpr uint64_t kWider = static_cast<uint64_t>((S::kGroupBytes - 1024) / 16) << 32;
     constexpr int kOwn = S::kAhead / 2;  // this stream's S products ahead of its P V
     bool go = true;
     while (go) {
@@ -888,11 +901,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           go = wait_load(idx) && wait_warp(&p_full[s], (n_st + k) & 1);
           if (!go) break;
           tc_fence_after();
-          const uint64_t bd = sw128_mnmajor_desc(smem_u32(ring + st * S::kTileBytes), kTile * 128);
+          // column blocks of 64 lie 1024 bytes apart, groups of 8 keys kGroupBytes
+          const uint64_t bd = sw128_mnmajor_desc(smem_u32(ring + st * S::kTileBytes), 1024) + kWider;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
-              umma_bf16_ta(dO, dP + kk * 8, bd + kk * 128, idesc_o, k > 0 || kk > 0);
+              umma_bf16_ta(dO, dP + kk * 8, bd + kk * (2 * S::kGroupBytes / 16), idesc_o, k > 0 || kk > 0);
             umma_commit(&pv_done[s]);
             umma_commit(&kv_empty[st]);
           }
@@ -910,12 +924,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             go = wait_warp(S::kAhead == 4 ? &s_free[s] : &pv_done[s], (n_st + n - 1) & 1);
           if (!go) break;
           tc_fence_after();
-          const uint64_t bd = sw128_kmajor_desc(smem_u32(ring + st * S::kTileBytes));
+          const uint64_t bd = sw128_kmajor_desc(smem_u32(ring + st * S::kTileBytes)) + kWider;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
-              const uint32_t o = (kk >> 2) * (kTile * 128 / 16) + (kk & 3) * 2;
-              umma_bf16(dS, ad + o, bd + o, idesc_s, kk > 0);
+              const uint32_t in = (kk & 3) * 2, half = kk >> 2;
+              umma_bf16(dS, ad + half * (kTile * 128 / 16) + in, bd + half * (1024 / 16) + in,
+                        idesc_s, kk > 0);
             }
             umma_commit(&s_full[s]);
             umma_commit(&kv_empty[st]);
@@ -1052,8 +1067,8 @@ int launch_chunk_tc(const ChunkArgs& a, char* ws, cudaStream_t st) {
   p.part_o = reinterpret_cast<float*>(ws + 256 + rec_bytes() + ml_bytes(p.part_rows));
   CUtensorMap km, vm;
   const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.G * a.bs;
-  if (!encode_tmap_bf16(&km, a.k_cache, rows, a.hd, p.box) ||
-      !encode_tmap_bf16(&vm, a.v_cache, rows, a.hd, p.box))
+  auto* encode = a.hd == 64 ? encode_tmap_bf16 : encode_tmap_bf16_rows128;
+  if (!encode(&km, a.k_cache, rows, a.hd, p.box) || !encode(&vm, a.v_cache, rows, a.hd, p.box))
     return PE_ERR_CUDA;
   return a.hd == 64 ? launch<64>(p, km, vm, st) : launch<128>(p, km, vm, st);
 }

@@ -1093,6 +1093,20 @@ bool encode_tmap_bf16(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_bf16_rows128(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols,
+                              uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || !ptr || rows == 0 || rows % 8 || cols != 128 || box_rows % 8) return false;
+  if ((reinterpret_cast<uintptr_t>(ptr) & 15u) != 0) return false;
+  const cuuint64_t dims[4] = {64, 8, 2, rows / 8};
+  const cuuint64_t strides[3] = {256, 128, 2048};
+  const cuuint32_t box[4] = {64u, 8u, 2u, box_rows / 8};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ------------------------------------------------------------------ tile-packed weights
 
 size_t packed_weight_bytes(int M, int K) {

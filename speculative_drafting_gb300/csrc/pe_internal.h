@@ -103,6 +103,11 @@ int launch_gemm_f32(const float* W, const float* W2, const float* X, int M, int 
 bool encode_tmap_bf16(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols,
                       uint32_t box_rows);
 
+// A matrix of 128-element rows as [rows / 8][2 halves][8 rows][64]: a box of box_rows rows
+// (a multiple of 8) brings both 128-byte halves of 8 rows at a time.  cols is 128.
+bool encode_tmap_bf16_rows128(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols,
+                              uint32_t box_rows);
+
 // ------------------------------------------------------------------ tile-packed weights
 // A weight W [M][K] (bf16, row-major) copied into the order the GEMM reads it:
 // tile (m, a) = rows 128m..128m+127 x columns 64a..64a+63 is one contiguous
