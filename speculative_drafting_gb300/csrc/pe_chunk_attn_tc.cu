@@ -21,15 +21,15 @@
 // workspace, at most two per CTA, and a second kernel joins them.  Every CTA finds
 // its piece itself from qsl and seq_len, so the host needs no lengths.
 //
-// Warps: 0-3 softmax of stream 0, 4-7 of stream 1, 8 TMA and unit list, 9 and 10 the
-// products of either stream.
+// Warps: 0-3 softmax of stream 0, 4-7 of stream 1, 8 K tiles and the unit list, 9 and 10
+// the products of either stream, 11 V tiles.
 #include "pe_paged.h"
 #include "pe_tmem.cuh"
 
 namespace pe {
 namespace {
 
-constexpr int kThreads = 384;  // three warpgroups; warp 11 only lends its registers
+constexpr int kThreads = 384;  // three warpgroups
 constexpr int kTile = 128;        // keys per tile, rows per stream
 constexpr int kUnitRows = 256;
 constexpr int kItems = 4;         // unit descriptors in flight
@@ -45,9 +45,9 @@ struct Shape {
   static constexpr int kTileBytes = kTile * HD * 2;   // K, V or Q tile
   // bytes from one group of 8 keys of a K or V tile to the next (load_box)
   static constexpr int kGroupBytes = 1024 * kHalves;
-  // ring slots (one K or V tile each): 128 KB
-  static constexpr int kSlots = HD == 64 ? 8 : 4;
-  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024;
+  // slots of the K ring, and of the V ring: 128 KB in all
+  static constexpr int kSlots = HD == 64 ? 4 : 2;
+  static constexpr int kSmem = (2 + 2 * kSlots) * kTileBytes + 1024;
   // Steps whose S product may be issued before their P V: with head size 64, P has
   // tensor memory of its own and S is free as soon as it is in registers; with 128
   // P takes the place of S, which is free after P V.
@@ -72,12 +72,6 @@ struct Unit {
   int tile0, tile1;     // key tiles of this CTA's part
   int kend;             // keys any row of the unit sees
   int whole;            // the part is the whole unit
-};
-
-// The TMA warp's walk over a unit's boxes, 32 at a time, one per lane: the window's
-// number, this lane's cache row (-1: none) and its block id in the next window.
-struct Window {
-  int n, row, next;
 };
 
 struct TcArgs {
@@ -215,7 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TcArgs p) {
   using S = Shape<HD>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t kv_full[S::kSlots], kv_empty[S::kSlots];
+  __shared__ __align__(8) uint64_t k_full[S::kSlots], k_empty[S::kSlots];
+  __shared__ __align__(8) uint64_t v_full[S::kSlots], v_empty[S::kSlots];
   __shared__ __align__(8) uint64_t it_full[kItems], it_empty[kItems];
   __shared__ __align__(8) uint64_t q_full[kItems][2], s_full[2], s_free[2], p_full[2], pv_done[2], x_bar[2], lag_bar;
   __shared__ __align__(8) uint64_t end_bar;
@@ -230,17 +225,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* q_sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* ring = q_sm + 2 * S::kTileBytes;
+  uint8_t* k_ring = q_sm + 2 * S::kTileBytes;
+  uint8_t* v_ring = k_ring + S::kSlots * S::kTileBytes;
   const int HG = a.H / a.G;
 
   if (tid == 0) {
     for (int i = 0; i < S::kSlots; ++i) {
-      mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 2);
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 2);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 2);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&it_full[i], 1);
-      mbar_init(&it_empty[i], 2 * kTile + 2);
+      mbar_init(&it_empty[i], 2 * kTile + 3);
       mbar_init(&q_full[i][0], kTile);
       mbar_init(&q_full[i][1], kTile);
     }
@@ -337,6 +335,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
   };
 
+  // The tiles of a unit's part into a ring, by one whole warp.  A window is 32 boxes (32 /
+  // gpt tiles), one per lane; the block ids of the next window are read while the
+  // current one streams.
+  auto stream_tiles = [&](const Unit& u, bool is_v, uint8_t* ring, const CUtensorMap* map, uint64_t* full,
+                          uint64_t* empty, uint32_t& loads) {
+    const uint64_t policy = u.wide ? policy_evict_normal() : policy_evict_first();
+    const int gpt = kTile / p.box;  // boxes per tile
+    auto block_of = [&](int wn) {
+      const long long key = (static_cast<long long>(wn) * 32 + lane) * p.box;
+      return key < u.kend ? a.block_table[static_cast<long long>(u.r) * a.max_blocks + key / a.bs]
+                          : -2;  // past the unit's keys
+    };
+    auto row_of = [&](int wn, int blk) {
+      if (blk >= 0 && blk < a.num_blocks)
+        return (blk * a.G + u.g) * a.bs + (wn * 32 + lane) * p.box % a.bs;
+      if (blk != -2 || (wn * 32 + lane) * p.box < u.kend) set_status(a.status, PE_ST_BLOCK_RANGE);
+      return -1;
+    };
+    int wn = u.tile0 * gpt >> 5;
+    int row = row_of(wn, block_of(wn)), next = block_of(wn + 1);
+#pragma unroll 1
+    for (int t = u.tile0; t < u.tile1; ++t, ++loads) {
+      if (t * gpt >> 5 != wn) {
+        ++wn;
+        row = row_of(wn, next);
+        next = block_of(wn + 1);
+      }
+      const int b0 = t * gpt & 31;
+      const bool mine = lane >= b0 && lane < b0 + gpt && row >= 0;
+      const unsigned have = __ballot_sync(0xffffffffu, mine);
+      const int st = loads % S::kSlots;
+      if (loads >= S::kSlots && !wait_warp(&empty[st], (loads / S::kSlots - 1) & 1)) return false;
+      const int n = __popc(have);
+      if (lane == 0) {
+        if (!is_v) {
+          uint32_t m = 0xffffu;  // the boxes' bits, widened to groups of 8 keys
+          if (n < gpt) {
+            m = 0;
+            const int w8 = p.box / 8;
+            for (int b = 0; b < gpt; ++b)
+              if (have >> (b0 + b) & 1) m |= ((1u << w8) - 1u) << (b * w8);
+          }
+          mask_sh[loads % kMasks] = m;
+        }
+        mbar_arrive_expect_tx(&full[st], n * p.box * HD * 2);
+      }
+      __syncwarp();
+      if (mine)
+        load_box<HD>(ring + st * S::kTileBytes + (lane - b0) * p.box * HD * 2, map, &full[st], row, policy);
+    }
+    return true;
+  };
+  // no copy may be in flight when the CTA leaves (after a timeout some may be)
+  auto drain = [&](uint64_t* full, uint32_t loads) {
+    int never = 0;
+    for (uint32_t i = loads > S::kSlots ? loads - S::kSlots : 0; i < loads; ++i)
+      mbar_wait(&full[i % S::kSlots], (i / S::kSlots) & 1, &never);
+  };
+
   if (idle) {
     if (tid == 0) p.rec[blockIdx.x * 8] = p.rec[blockIdx.x * 8 + 1] = 0;
   } else if (warp < 8) {
@@ -347,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t tS = tm + S::kS + s * 128, tP = tm + S::kP + s * S::kPStride;
     const float sc = kLog2e / sqrtf(static_cast<float>(HD));
-    uint32_t n_items = 0, n_st = 0, loads = 0, tiles = 0, n_x = 0;
+    uint32_t n_items = 0, n_st = 0, tiles = 0, n_x = 0;
     bool go = true;
     // Rows move between global and shared memory a whole row per HD / 8 lanes: each
     // instruction covers kRpi full rows of this warp's 32.  These loops, and those over
@@ -429,7 +486,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // go of it: an MMA warp that skips units (none of their tiles is its stream's)
       // finds the barriers in step.
       mbar_arrive(&q_full[slot][s]);
-      const int ahead = wide ? S::kAhead / 2 : S::kAhead;
       const int mysteps = wide ? nt : (nt - s + 1) >> 1;
       float m = -INFINITY, l = 0.f;  // m: running maximum in units of log2
       for (int k = 0; k < mysteps; ++k) {
@@ -535,13 +591,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // anything, NaN included: their V rows become 0 before the product
         const bool cut = t0 + kTile > kend || have != 0xffffu;
         if (cut) {
-          const uint32_t idx = loads + min(nt, ahead + j) + j;
-          if (!wait_warp(&kv_full[idx % S::kSlots], (idx / S::kSlots) & 1)) {
+          const uint32_t idx = tiles + j;
+          if (!wait_warp(&v_full[idx % S::kSlots], (idx / S::kSlots) & 1)) {
             go = false;
             break;
           }
           if (t0 + i >= kend || !(have >> (i >> 3) & 1u)) {
-            uint8_t* v = ring + (idx % S::kSlots) * S::kTileBytes + (i >> 3) * S::kGroupBytes + (i & 7) * 128;
+            uint8_t* v = v_ring + (idx % S::kSlots) * S::kTileBytes + (i >> 3) * S::kGroupBytes + (i & 7) * 128;
 #pragma unroll
             for (int ch = 0; ch < HD / 8; ++ch)
               *reinterpret_cast<uint4*>(v + (ch >> 3) * 1024 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -562,7 +618,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       n_st += mysteps;
-      loads += 2 * nt;
       tiles += nt;
       tc_fence_after();
       const bool whole = items[slot].whole;
@@ -683,15 +738,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 8) {
-    // ---------------- TMA warp: lists the units of this CTA's piece and streams
-    // their tiles in the order in which the MMA warp consumes them
+    // ---------------- K warp: lists the units of this CTA's piece and streams their K
+    // tiles (the V warp, below, their V tiles: one warp issues a 2 KB box every 90 ns,
+    // half of what an SM's share of DRAM needs at head size 64)
     const Place first = place_sh[0], last = place_sh[1];
     Place cur = first;
-    uint32_t loads = 0, n_items = 0, tiles = 0;
+    uint32_t loads = 0, n_items = 0;
     int head = 0, tail = 0, t_q0 = 0, t_g = 0, t_row0 = 0, t_rows = 0;
     bool go = true;
-    const uint64_t once = policy_evict_first(), kept = policy_evict_normal();
-    const int gpt = kTile / p.box;  // boxes per tile
     Req q;
     int q_of = -1;
     while (go) {
@@ -743,69 +797,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&it_full[slot]);
       }
       ++n_items;
-      // stream its tiles.  A window is 32 boxes (32 / gpt tiles), one per lane; K and V
-      // walk their own, and the block ids of the next window are read while the
-      // current one streams.
-      const int nt = u.tile1 - u.tile0;
-      const int steps = u.wide ? 2 * nt : nt;
-      auto block_of = [&](int wn) {
-        const long long key = (static_cast<long long>(wn) * 32 + lane) * p.box;
-        return key < u.kend ? a.block_table[static_cast<long long>(u.r) * a.max_blocks + key / a.bs]
-                            : -2;  // past the unit's keys
-      };
-      auto row_of = [&](int wn, int blk) {
-        if (blk >= 0 && blk < a.num_blocks)
-          return (blk * a.G + u.g) * a.bs + (wn * 32 + lane) * p.box % a.bs;
-        if (blk != -2 || (wn * 32 + lane) * p.box < u.kend) set_status(a.status, PE_ST_BLOCK_RANGE);
-        return -1;
-      };
-      Window kw, vw;
-      kw.n = u.tile0 * gpt / 32;
-      kw.row = row_of(kw.n, block_of(kw.n));
-      kw.next = block_of(kw.n + 1);
-      vw = kw;
-      auto load = [&](int j, bool is_v, Window& w) {  // tile j of the unit
-        const int box0 = (u.tile0 + j) * gpt;
-        if (box0 >> 5 != w.n) {
-          ++w.n;
-          w.row = row_of(w.n, w.next);
-          w.next = block_of(w.n + 1);
-        }
-        const int b0 = box0 & 31;
-        const bool mine = lane >= b0 && lane < b0 + gpt && w.row >= 0;
-        const unsigned have = __ballot_sync(0xffffffffu, mine);
-        const int st = loads % S::kSlots;
-        if (loads >= S::kSlots && !wait_warp(&kv_empty[st], (loads / S::kSlots - 1) & 1)) {
-          fail();
-          go = false;
-          return;
-        }
-        const int n = __popc(have);
-        if (lane == 0) {
-          if (!is_v) {
-            uint32_t m = 0xffffu;  // the boxes' bits, widened to groups of 8 keys
-            if (n < gpt) {
-              m = 0;
-              const int w8 = p.box / 8;
-              for (int b = 0; b < gpt; ++b)
-                if (have >> (b0 + b) & 1) m |= ((1u << w8) - 1u) << (b * w8);
-            }
-            mask_sh[tiles % kMasks] = m;
-          }
-          mbar_arrive_expect_tx(&kv_full[st], n * p.box * HD * 2);
-        }
-        tiles += !is_v;
-        __syncwarp();
-        if (mine)
-          load_box<HD>(ring + st * S::kTileBytes + (lane - b0) * p.box * HD * 2, is_v ? &vmap : &kmap,
-                       &kv_full[st], w.row, u.wide ? kept : once);
-        ++loads;
-      };
-#pragma unroll 1
-      for (int i = -S::kAhead; i < steps && go; ++i) {
-        if (i >= 0 && (!u.wide || !(i & 1))) load(u.wide ? i >> 1 : i, true, vw);
-        const int n = i + S::kAhead;
-        if (go && n < steps && (!u.wide || !(n & 1))) load(u.wide ? n >> 1 : n, false, kw);
+      if (!stream_tiles(u, false, k_ring, &kmap, k_full, k_empty, loads)) {
+        fail();
+        go = false;
       }
       // the next unit
       if (ends_here) break;
@@ -834,20 +828,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       rec[3] = t_g;
       rec[4] = t_row0;
       rec[5] = t_rows;
-      // no copy may be in flight when the CTA leaves (after a timeout some may be)
-      int never = 0;
-      for (uint32_t i = loads > S::kSlots ? loads - S::kSlots : 0; i < loads; ++i)
-        mbar_wait(&kv_full[i % S::kSlots], (i / S::kSlots) & 1, &never);
     }
+    drain(k_full, loads);
     __syncwarp();
-    } else if (warp <= 10) {
+    } else if (warp == 11) {
+    // ---------------- V warp
+    uint32_t loads = 0;
+    for (uint32_t n_items = 0;; ++n_items) {
+      const int slot = n_items % kItems;
+      if (!wait_warp(&it_full[slot], (n_items / kItems) & 1)) {
+        fail();
+        break;
+      }
+      const Unit u = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&it_empty[slot]);
+      if (u.r < 0) break;
+      if (!stream_tiles(u, true, v_ring, &vmap, v_full, v_empty, loads)) {
+        fail();
+        break;
+      }
+    }
+    drain(v_full, loads);
+    __syncwarp();
+    } else {
     // ---------------- MMA warps, one per stream: the waits of one overlap the products
     // of the other (a single warp for both took 1436 clocks a tile of head size 64, in
     // which the tensor pipe worked 614).  All lanes follow the steps and an elected one
     // issues: in a branch of one lane the operands' descriptors go through vector
     // registers for every product (955 clocks a tile against 690 in isolation).
     const int s = warp - 9;
-    uint32_t loads = 0, seen = 0, n_items = 0, n_st = 0, n_wide = 0;
+    uint32_t tiles = 0, seen_k = 0, seen_v = 0, n_items = 0, n_st = 0, n_wide = 0;
     const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
     const uint32_t idesc_o = idesc_bf16_f32(kTile, HD) | (1u << 16);  // V is MN-major
     const uint32_t dS = tmem + S::kS + s * 128, dP = tmem + S::kP + s * S::kPStride;
@@ -869,7 +880,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u.r < 0) break;
       const int nt = u.tile1 - u.tile0;
       const int steps = u.wide ? nt : (nt - s + 1) >> 1;     // of this stream
-      const int ahead = u.wide ? S::kAhead / 2 : S::kAhead;  // K tiles before V tile 0
       const int qb = u.wide ? s : 0;
       // (with no step here the other stream may run units ahead: nothing to wait for)
       if (steps > 0) go = wait_warp(&q_full[slot][qb], ((n_items - 1) / kItems) & 1);
@@ -877,46 +887,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       // stay out of step, one's exponentials beside the other's waits.
       if (S::kAhead == 4 && go && s == 1 && u.wide) go = wait_warp(&lag_bar, n_wide++ & 1);
       const uint64_t ad = sw128_kmajor_desc(smem_u32(q_sm + qb * S::kTileBytes));
-      // Both warps see every load in order, the other stream's too: a slot's barrier
-      // then never is a phase behind or ahead of the one that is waited for.  A slot is
-      // free when both have let go of it, its users once their products are done.
-      auto take = [&](uint32_t idx) {
-        for (; seen < idx; ++seen) {
-          if (!wait_warp(&kv_full[seen % S::kSlots], (seen / S::kSlots) & 1)) return false;
-          if (elect_one()) mbar_arrive(&kv_empty[seen % S::kSlots]);
+      // Both warps see every load of both rings in order, the other stream's too: a
+      // slot's barrier then never is a phase behind or ahead of the one that is waited
+      // for.  A slot is free when both have let go of it, its users once their products
+      // are done.
+      auto take = [&](uint64_t* full, uint64_t* empty, uint32_t& seen, uint32_t to) {
+        for (; seen < to; ++seen) {
+          if (!wait_warp(&full[seen % S::kSlots], (seen / S::kSlots) & 1)) return false;
+          if (elect_one()) mbar_arrive(&empty[seen % S::kSlots]);
         }
         return true;
       };
-      auto wait_load = [&](uint32_t idx) {
-        if (!take(idx)) return false;
+      auto wait_load = [&](uint64_t* full, uint64_t* empty, uint32_t& seen, uint32_t idx) {
+        if (!take(full, empty, seen, idx)) return false;
         ++seen;
-        return wait_warp(&kv_full[idx % S::kSlots], (idx / S::kSlots) & 1);
+        return wait_warp(&full[idx % S::kSlots], (idx / S::kSlots) & 1);
       };
 #pragma unroll 1
       for (int k = -kOwn; k < steps && go; ++k) {
         if (k >= 0) {  // O += P V of step k
           const int j = u.wide ? k : 2 * k + s;
-          const uint32_t idx = loads + min(nt, ahead + j) + j;
+          const uint32_t idx = tiles + j;
           const int st = idx % S::kSlots;
-          go = wait_load(idx) && wait_warp(&p_full[s], (n_st + k) & 1);
+          go = wait_load(v_full, v_empty, seen_v, idx) && wait_warp(&p_full[s], (n_st + k) & 1);
           if (!go) break;
           tc_fence_after();
           // column blocks of 64 lie 1024 bytes apart, groups of 8 keys kGroupBytes
-          const uint64_t bd = sw128_mnmajor_desc(smem_u32(ring + st * S::kTileBytes), 1024) + kWider;
+          const uint64_t bd = sw128_mnmajor_desc(smem_u32(v_ring + st * S::kTileBytes), 1024) + kWider;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
               umma_bf16_ta(dO, dP + kk * 8, bd + kk * (2 * S::kGroupBytes / 16), idesc_o, k > 0 || kk > 0);
             umma_commit(&pv_done[s]);
-            umma_commit(&kv_empty[st]);
+            umma_commit(&v_empty[st]);
           }
         }
         const int n = k + kOwn;
         if (n < steps) {  // S = Q K^T of step n
           const int j = u.wide ? n : 2 * n + s;
-          const uint32_t idx = loads + j + max(0, j - ahead + 1);
+          const uint32_t idx = tiles + j;
           const int st = idx % S::kSlots;
-          go = wait_load(idx);
+          go = wait_load(k_full, k_empty, seen_k, idx);
           // S of the step before is out of the way: in registers (S::kAhead = 4; of the
           // unit before it is), or P has been multiplied (of the unit before too: a
           // narrow unit's Q comes from the other stream's group)
@@ -924,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             go = wait_warp(S::kAhead == 4 ? &s_free[s] : &pv_done[s], (n_st + n - 1) & 1);
           if (!go) break;
           tc_fence_after();
-          const uint64_t bd = sw128_kmajor_desc(smem_u32(ring + st * S::kTileBytes)) + kWider;
+          const uint64_t bd = sw128_kmajor_desc(smem_u32(k_ring + st * S::kTileBytes)) + kWider;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
@@ -933,12 +944,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         idesc_s, kk > 0);
             }
             umma_commit(&s_full[s]);
-            umma_commit(&kv_empty[st]);
+            umma_commit(&k_empty[st]);
           }
         }
       }
-      loads += 2 * nt;
-      if (!go || !take(loads)) {
+      tiles += nt;
+      if (!go || !take(k_full, k_empty, seen_k, tiles) || !take(v_full, v_empty, seen_v, tiles)) {
         fail();
         break;
       }
