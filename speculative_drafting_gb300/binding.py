@@ -192,10 +192,20 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_handle(stream):
-    import torch
+_raw_stream = None
 
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+def _stream_handle(stream, t):
+    """The cudaStream_t of `stream`, or of the current stream on tensor t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+
+        # what torch.cuda.current_stream wraps in an object, 3 us a call
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+    return _raw_stream(t.get_device())
 
 
 def _check(rc, what):
@@ -428,7 +438,7 @@ def verify_sampled(B, T_in, qsl, tok, logits, vocab, dtype, temperature, u, gumb
     rc = load().pe_verify_sampled(B, T_in, _addr(qsl), _addr(tok), _addr(logits), vocab, dtype,
                                   _addr(temperature), _addr(u), _addr(gumbel), _addr(accepted),
                                   _addr(bonus), _addr(p_draft), _addr(ws), ws.numel(),
-                                  _stream_handle(stream))
+                                  _stream_handle(stream, ws))
     _check(rc, "pe_verify_sampled")
 
 
@@ -473,7 +483,7 @@ class PagedAttention:
         rc = self.lib.pe_qkv_append(self.addr, T, _addr(qkv), qkv.stride(0), _addr(gamma_q),
                                     _addr(gamma_k), _addr(pos), _addr(slot), num_blocks,
                                     _addr(q_out), _addr(k_cache), _addr(v_cache), _addr(ws),
-                                    ws.numel(), _stream_handle(stream))
+                                    ws.numel(), _stream_handle(stream, ws))
         _check(rc, "pe_qkv_append")
 
     def attend(self, B, T, qsl, seq_len, q, k_cache, v_cache, block_table, num_blocks, out, ws,
@@ -484,7 +494,7 @@ class PagedAttention:
                                          q.stride(0), _addr(k_cache), _addr(v_cache),
                                          _addr(block_table), block_table.shape[1], num_blocks,
                                          _addr(sink), _addr(out), out.stride(0), _addr(ws),
-                                         ws.numel(), _stream_handle(stream))
+                                         ws.numel(), _stream_handle(stream, ws))
         _check(rc, "pe_chunk_attention")
 
 

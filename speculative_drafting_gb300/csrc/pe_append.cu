@@ -284,12 +284,12 @@ extern "C" int pe_qkv_append(const pe_attn_plan* plan, int T, const void* qkv, i
     const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>((n + a.heads_per_cta - 1) / a.heads_per_cta));
     auto* kernel = bf ? (a.hd == 64 ? append_kernel<bf16, 64> : append_kernel<bf16, 128>)
                       : (a.hd == 64 ? append_kernel<float, 64> : append_kernel<float, 128>);
-    return launch_pdl(kernel, grid, dim3(kRowThreads), 0, st, a) == cudaSuccess ? PE_OK : PE_ERR_CUDA;
+    return launch_chained(kernel, grid, dim3(kRowThreads), 0, st, a) == cudaSuccess ? PE_OK : PE_ERR_CUDA;
   }
   const int64_t grid = (static_cast<int64_t>(T) * heads + kWarps - 1) / kWarps;
   if (grid > 0x7fffffff) return PE_ERR_UNSUPPORTED;
   // bf16 plans have head size 64 or 128
-  return launch_pdl(append_any_kernel<float>, dim3(static_cast<unsigned>(grid)), dim3(32 * kWarps), 0,
+  return launch_chained(append_any_kernel<float>, dim3(static_cast<unsigned>(grid)), dim3(32 * kWarps), 0,
                     st, a) == cudaSuccess
              ? PE_OK
              : PE_ERR_CUDA;

@@ -159,7 +159,7 @@ extern "C" int pe_chunk_attention(const pe_attn_plan* plan, int B, int T, const 
   if (chunk_tc_takes(plan) && num_blocks > 0) return launch_chunk_tc(a, static_cast<char*>(ws), st);
   const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(plan->n_heads));
   const cudaError_t e = plan->dtype == PE_DTYPE_BF16
-                            ? launch_pdl(chunk_simt_kernel<bf16>, grid, dim3(128), 0, st, a)
-                            : launch_pdl(chunk_simt_kernel<float>, grid, dim3(128), 0, st, a);
+                            ? launch_chained(chunk_simt_kernel<bf16>, grid, dim3(128), 0, st, a)
+                            : launch_chained(chunk_simt_kernel<float>, grid, dim3(128), 0, st, a);
   return e == cudaSuccess ? PE_OK : PE_ERR_CUDA;
 }

@@ -23,6 +23,8 @@
 //
 // Warps: 0-3 softmax of stream 0, 4-7 of stream 1, 8 K tiles and the unit list, 9 and 10
 // the products of either stream, 11 V tiles.
+#include <atomic>
+
 #include "pe_paged.h"
 #include "pe_tmem.cuh"
 
@@ -289,18 +291,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (w < warp) before += scan_sh[w];
     Wg += scan_sh[w];
   }
+  // Where the pieces begin is a matter of balance: fp32 serves (64-bit divisions cost a
+  // small call a microsecond), so long as neighbours find the same place.
   const long long W = Wg * a.G;
-  const long long least = static_cast<long long>(p.umin) * kTile * HG + ov;
-  const int pieces = static_cast<int>(min(max(W / least, 1ll), static_cast<long long>(p.grid)));
+  const float least = static_cast<float>(p.umin * kTile * HG + static_cast<int>(ov));
+  const int pieces = static_cast<int>(fminf(fmaxf(static_cast<float>(W) / least, 1.f), static_cast<float>(p.grid)));
+  auto piece = [&](int c) {  // never past W, and no less for a larger c
+    return c >= pieces ? W : min(W, static_cast<long long>(static_cast<float>(W) * (static_cast<float>(c) / static_cast<float>(pieces))));
+  };
   const bool idle = W == 0 || static_cast<int>(blockIdx.x) >= pieces;
   if (!idle) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int c = blockIdx.x + e;
-      // c W / pieces without leaving 64 bits
-      const long long w = c >= pieces ? W : W / pieces * c + W % pieces * c / pieces;
+      const long long w = piece(blockIdx.x + e);
       if (w >= W) continue;
-      const int g = static_cast<int>(w / Wg);
+      int g = min(a.G - 1, static_cast<int>(static_cast<float>(w) / static_cast<float>(Wg)));
+      while (w < g * Wg) --g;
+      while (w >= (g + 1) * Wg) ++g;
       long long rem = w - g * Wg - before;
       if (rem < 0 || rem >= mine) continue;
       for (int r = r_lo; r < r_hi; ++r) {
@@ -317,7 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const long long off = rem - units_before(q, lo, ov);
         const int kt = unit_tiles(unit_kend(q, lo, HG));
-        place_sh[e] = Place{g, r, lo, static_cast<int>(off * kt / unit_cost(q, lo, ov))};
+        const float part = static_cast<float>(off) / static_cast<float>(unit_cost(q, lo, ov));
+        place_sh[e] = Place{g, r, lo, min(kt - 1, static_cast<int>(part * static_cast<float>(kt)))};
         break;
       }
     }
@@ -987,33 +995,57 @@ __global__ void __launch_bounds__(128) chunk_join_kernel(const __grid_constant__
   const int HG = a.H / a.G;
   for (int row = blockIdx.y * 4 + warp; row < rows; row += gridDim.y * 4) {
     const int tok = (row0 + row) / HG, head = g * HG + (row0 + row) % HG;
-    float M = a.sink ? a.sink[head] * kLog2e : -INFINITY;
+    float M = a.sink ? a.sink[head] * kLog2e : -INFINITY;  // the sink: one more part, O = 0
     float den = M == -INFINITY ? 0.f : 1.f;
     bool any = false;
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    for (int k = c, part = 1;; part = 0) {
-      const size_t prow = (static_cast<size_t>(k) * 2 + part) * p.part_rows + row;
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + prow * 2);
-      float o[V];
+    // 32 CTAs at a time, a lane each: which of them hold a part, and its (m, l)
+    bool more = true;
+    for (int k0 = c; more; k0 += 32) {
+      const int k = k0 + lane;
+      const int code = k >= p.grid ? 0 : k == c ? 1 : p.rec[k * 8];
+      const unsigned ends = __ballot_sync(0xffffffffu, code == 2 || k >= p.grid);
+      const int last = ends ? __ffs(ends) - 1 : 31;  // of this window
+      more = !ends;
+      const bool part = code != 0 && lane <= last;
+      const size_t prow = (static_cast<size_t>(k) * 2 + (k == c)) * p.part_rows + row;
+      const float2 ml = part ? *reinterpret_cast<const float2*>(p.part_ml + prow * 2)
+                             : make_float2(-INFINITY, 0.f);
+      // (l = 0: no key of the part was seen; NaN counts as seen)
+      const bool seen = ml.y != 0.f;
+      any |= __any_sync(0xffffffffu, seen);
+      const float mn = fmaxf(M, warp_max(ml.x));
+      const float keep = M == -INFINITY ? 0.f : ex2(M - mn);
+      const float w = !seen ? 0.f : ml.x == -INFINITY ? ml.y : ex2(ml.x - mn);
+      M = mn;
+      den = den * keep + warp_sum(w * ml.y);
 #pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = p.part_o[prow * HD + lane + 32 * i];
-      if (ml.y != 0.f) {  // some key of this part was seen (or is NaN)
-        any = true;
-        const float mn = fmaxf(M, ml.x);
-        const float f0 = M == -INFINITY ? 0.f : ex2(M - mn), f1 = ex2(ml.x - mn);
-        M = mn;
-        den = den * f0 + ml.y * f1;
+      for (int i = 0; i < V; ++i) acc[i] *= keep;
+      unsigned todo = __ballot_sync(0xffffffffu, part && seen);
+      while (todo) {
+        // four parts' loads in flight, added in order
+        float o[4][V], wj[4];
+        int n = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = acc[i] * f0 + o[i] * f1;
+        for (int x = 0; x < 4; ++x) {
+          const int j = todo ? __ffs(todo) - 1 : 0;
+          wj[x] = __shfl_sync(0xffffffffu, w, j);
+          const bool ok = todo != 0;
+          todo &= todo - 1;
+          n += ok;
+          const float* src =
+              p.part_o + ((static_cast<size_t>(k0 + j) * 2 + (k0 + j == c)) * p.part_rows + row) * HD;
+#pragma unroll
+          for (int i = 0; i < V; ++i) o[x][i] = ok ? src[lane + 32 * i] : 0.f;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (x < n)
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] += wj[x] * o[x][i];
       }
-      // the next part
-      int code = 0;
-      if (!part && p.rec[k * 8] == 2) break;
-      for (++k; k < p.grid; ++k)
-        if ((code = p.rec[k * 8])) break;
-      if (!code) break;
     }
     const float inv = any ? 1.f / den : 0.f;
     bf16* out = static_cast<bf16*>(a.out) + (q0 + tok) * a.ld_out + static_cast<long long>(head) * HD;
@@ -1036,12 +1068,21 @@ size_t ml_bytes(int part_rows) { return al256(size_t{kMaxGrid} * 2 * part_rows *
 
 template <int HD>
 int launch(const TcArgs& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
-  cudaFuncSetAttribute(chunk_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       Shape<HD>::kSmem);
-  if (launch_pdl(chunk_tc_kernel<HD>, dim3(p.grid), dim3(kThreads), Shape<HD>::kSmem, st, km, vm, p) !=
+  // the function's shared-memory limit, once per device (a bit each; past 63 every time)
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PE_ERR_CUDA;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (!(set.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(chunk_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Shape<HD>::kSmem) != cudaSuccess)
+      return PE_ERR_CUDA;
+    set.fetch_or(bit, std::memory_order_release);
+  }
+  if (launch_chained(chunk_tc_kernel<HD>, dim3(p.grid), dim3(kThreads), Shape<HD>::kSmem, st, km, vm, p) !=
       cudaSuccess)
     return PE_ERR_CUDA;
-  return launch_pdl(chunk_join_kernel<HD>, dim3(p.grid, 8), dim3(128), 0, st, p) == cudaSuccess
+  return launch_chained(chunk_join_kernel<HD>, dim3(p.grid, 8), dim3(128), 0, st, p) == cudaSuccess
              ? PE_OK
              : PE_ERR_CUDA;
 }

@@ -532,13 +532,13 @@ extern "C" int pe_verify_sampled(int B, int T_in, const int32_t* qsl, const int3
   a.best = reinterpret_cast<ulonglong2*>(w);
   const bool f32 = dtype == PE_DTYPE_F32;
   if (T_in > 0) {
-    if (launch_pdl(f32 ? sampled_row_kernel<float> : sampled_row_kernel<bf16>,
+    if (launch_chained(f32 ? sampled_row_kernel<float> : sampled_row_kernel<bf16>,
                    dim3(static_cast<unsigned>(T_in) * a.splits), dim3(kThreads), 0, st, a) != cudaSuccess)
       return PE_ERR_CUDA;
   } else if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) {
     return PE_ERR_CUDA;
   }
-  return launch_pdl(f32 ? sampled_request_kernel<float> : sampled_request_kernel<bf16>,
+  return launch_chained(f32 ? sampled_request_kernel<float> : sampled_request_kernel<bf16>,
                     dim3(static_cast<unsigned>(B) * a.rsplits), dim3(kThreads), 0, st, a) == cudaSuccess
              ? PE_OK
              : PE_ERR_CUDA;
