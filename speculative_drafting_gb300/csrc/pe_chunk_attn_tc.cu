@@ -23,6 +23,7 @@
 //
 // Warps: 0-3 softmax of stream 0, 4-7 of stream 1, 8 K tiles and the unit list, 9 and 10
 // the products of either stream, 11 V tiles.
+#include <algorithm>
 #include <atomic>
 
 #include "pe_paged.h"
@@ -276,7 +277,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per = (a.B + kThreads - 1) / kThreads;  // requests per thread
   const int r_lo = min(tid * per, a.B), r_hi = min(r_lo + per, a.B);
   long long mine = 0;
-  for (int r = r_lo; r < r_hi; ++r) mine += req_cost(load_req(a, r, blockIdx.x == 0), ov);
+  Req req0;  // of this thread's first request (with up to kThreads requests, its only one)
+  for (int r = r_lo; r < r_hi; ++r) {
+    const Req q = load_req(a, r, blockIdx.x == 0);
+    if (r == r_lo) req0 = q;
+    mine += req_cost(q, ov);
+  }
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -292,26 +298,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     Wg += scan_sh[w];
   }
   // Where the pieces begin is a matter of balance: fp32 serves (64-bit divisions cost a
-  // small call a microsecond), so long as neighbours find the same place.
+  // small call a microsecond), so long as neighbours find the same place.  Every KV head
+  // has the same line, so a whole number of pieces each, unless that idles more than one
+  // CTA in 16.
   const long long W = Wg * a.G;
-  const float least = static_cast<float>(p.umin * kTile * HG + static_cast<int>(ov));
-  const int pieces = static_cast<int>(fminf(fmaxf(static_cast<float>(W) / least, 1.f), static_cast<float>(p.grid)));
-  auto piece = [&](int c) {  // never past W, and no less for a larger c
-    return c >= pieces ? W : min(W, static_cast<long long>(static_cast<float>(W) * (static_cast<float>(c) / static_cast<float>(pieces))));
+  const float least = static_cast<float>(p.umin * kTile * HG);
+  int pieces = static_cast<int>(fminf(fmaxf(static_cast<float>(W) / least, 1.f), static_cast<float>(p.grid)));
+  const int per_head = pieces / a.G;
+  const bool even = per_head > 0 && (pieces - per_head * a.G) * 16 <= pieces;
+  if (even) pieces = per_head * a.G;
+  // the first cost of piece c on its head's line: never past the line, no less for a
+  // larger c
+  auto piece = [&](int c, int& g) {
+    if (even) {
+      g = c / per_head;
+      return static_cast<long long>(static_cast<float>(Wg) *
+                                    (static_cast<float>(c - g * per_head) / static_cast<float>(per_head)));
+    }
+    long long w = static_cast<long long>(static_cast<float>(W) * (static_cast<float>(c) / static_cast<float>(pieces)));
+    w = min(w, W - 1);
+    g = min(a.G - 1, static_cast<int>(static_cast<float>(w) / static_cast<float>(Wg)));
+    while (w < g * Wg) --g;
+    while (w >= (g + 1) * Wg) ++g;
+    return w - g * Wg;
   };
   const bool idle = W == 0 || static_cast<int>(blockIdx.x) >= pieces;
   if (!idle) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const long long w = piece(blockIdx.x + e);
-      if (w >= W) continue;
-      int g = min(a.G - 1, static_cast<int>(static_cast<float>(w) / static_cast<float>(Wg)));
-      while (w < g * Wg) --g;
-      while (w >= (g + 1) * Wg) ++g;
-      long long rem = w - g * Wg - before;
+      const int c = blockIdx.x + e;
+      if (c >= pieces) continue;  // the end of the line
+      int g;
+      long long rem = min(piece(c, g), Wg - 1) - before;
       if (rem < 0 || rem >= mine) continue;
       for (int r = r_lo; r < r_hi; ++r) {
-        const Req q = load_req(a, r, false);
+        const Req q = r == r_lo ? req0 : load_req(a, r, false);
         const long long cost = req_cost(q, ov);
         if (rem >= cost) {
           rem -= cost;
@@ -324,8 +345,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const long long off = rem - units_before(q, lo, ov);
         const int kt = unit_tiles(unit_kend(q, lo, HG));
-        const float part = static_cast<float>(off) / static_cast<float>(unit_cost(q, lo, ov));
-        place_sh[e] = Place{g, r, lo, min(kt - 1, static_cast<int>(part * static_cast<float>(kt)))};
+        // A cut near a unit's end or start moves there: a part costs a CTA some tiles of
+        // time whatever its length.
+        const float cost_u = static_cast<float>(unit_cost(q, lo, ov));
+        const float len = static_cast<float>(W) / static_cast<float>(pieces) * static_cast<float>(kt) / cost_u;
+        const int snap = min(4, static_cast<int>(0.25f * len));
+        int tile = min(kt - 1, static_cast<int>(static_cast<float>(off) / cost_u * static_cast<float>(kt)));
+        if (tile <= snap && 2 * tile < kt)
+          tile = 0;
+        else if (kt - tile <= snap)
+          tile = kt;  // (no tile of this unit)
+        place_sh[e] = Place{g, r, lo, tile};
         break;
       }
     }
@@ -778,9 +808,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       u.kend = unit_kend(q, cur.qt, HG);
       const int kt = unit_tiles(u.kend);
       u.tile0 = cur.tile;
-      u.tile1 = ends_here ? last.tile : kt;
+      u.tile1 = ends_here ? min(last.tile, kt) : kt;
+      const bool some = u.tile0 < u.tile1;
       u.whole = u.tile0 == 0 && u.tile1 == kt;
-      if (!u.whole) {
+      if (some && !u.whole) {
         if (u.tile0 > 0) {
           head = u.tile1 == kt ? 2 : 1;
         } else {
@@ -791,12 +822,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           t_rows = u.rows;
         }
       }
+      if (some) {
       // hand the unit over
       const int slot = n_items % kItems;
       if (n_items >= kItems) {
         int ok = lane == 0 ? mbar_wait(&it_empty[slot], (n_items / kItems - 1) & 1, abort_flag) : 1;
         if (!__shfl_sync(0xffffffffu, ok, 0)) {
           if (lane == 0) fail();
+          go = false;
           break;
         }
       }
@@ -808,6 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!stream_tiles(u, false, k_ring, &kmap, k_full, k_empty, loads)) {
         fail();
         go = false;
+      }
       }
       // the next unit
       if (ends_here) break;
@@ -1082,7 +1116,10 @@ int launch(const TcArgs& p, const CUtensorMap& km, const CUtensorMap& vm, cudaSt
   if (launch_chained(chunk_tc_kernel<HD>, dim3(p.grid), dim3(kThreads), Shape<HD>::kSmem, st, km, vm, p) !=
       cudaSuccess)
     return PE_ERR_CUDA;
-  return launch_chained(chunk_join_kernel<HD>, dim3(p.grid, 8), dim3(128), 0, st, p) == cudaSuccess
+  // a warp takes eight of a unit's rows
+  const int join = std::max(1, std::min(8, static_cast<int>(
+      std::min<long long>(static_cast<long long>(p.c.T) * (p.c.H / p.c.G), p.part_rows) + 31) / 32));
+  return launch_chained(chunk_join_kernel<HD>, dim3(p.grid, join), dim3(128), 0, st, p) == cudaSuccess
              ? PE_OK
              : PE_ERR_CUDA;
 }
