@@ -30,8 +30,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;            // 16-byte loads in flight per thread
-constexpr int kMaxChunkBytes = 32768; // of a row, per CTA of the row kernel
+constexpr int kMaxChunkBytes = 65536; // of a row, per CTA of the row kernel
 constexpr int kRace = 8;              // logits per thread and round of the race
+constexpr int kRaceRounds = 2;        // rounds whose loads are in flight together
 
 struct VerifyArgs {
   int B, T, V;
@@ -62,6 +63,25 @@ PE_DEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// two fp32 values in one 64-bit register, for the paired instructions
+PE_DEV uint64_t pack_f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+PE_DEV void unpack_f32x2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+PE_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+PE_DEV uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 PE_DEV float max_nan(float a, float b) {
   float r;
@@ -106,6 +126,14 @@ PE_DEV Stat join(const Stat& x, const Stat& y, float c) {
   const float off = z.m == -INFINITY ? 0.f : z.m;
   z.s = x.s * ex2((x.m - off) * c) + y.s * ex2((y.m - off) * c);
   return z;
+}
+
+// ... of all the lanes of a warp: one maximum, one rescaling each
+PE_DEV Stat warp_join(Stat x, float c) {
+  float m = x.m;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return Stat{m, warp_sum(x.s * ex2((x.m - (m == -INFINITY ? 0.f : m)) * c))};
 }
 
 // log2(e) / T rounded once (a division and a correction by its remainder)
@@ -170,19 +198,37 @@ __global__ void __launch_bounds__(kThreads, 6) sampled_row_kernel(const VerifyAr
   const float temp = temp_sh;
   if (temp < 0.f) return;
   if (temp == 0.f) {
+    // the first vector that holds this thread's greatest value stays in registers (a NaN
+    // counts as the greatest); its lowest index with the value is found at the end
     unsigned long long k = 0ull;
-    auto look = [&](T x, int v) {
-      k = max(k, argmax_key(Elem<T>::to_f(x), static_cast<uint32_t>(v)));
-    };
-    if (tid < head) look(base[c0 + tid], c0 + tid);
-    if (t0 + tid < c1) look(base[t0 + tid], t0 + tid);
-    for (int j = tid; j < nvec; j += kThreads) {
-      float f[kVec];
-      unpack16<T>(ld_stream16(vp + j), f);
+    if (tid < head) k = argmax_key(Elem<T>::to_f(base[c0 + tid]), static_cast<uint32_t>(c0 + tid));
+    float best = -INFINITY;
+    int bj = -1;
+    uint4 bv = none;
+    for (int j = tid; j < nvec; j += kUnroll * kThreads) {
 #pragma unroll
-      for (int e = 0; e < kVec; ++e)
-        k = max(k, argmax_key(f[e], static_cast<uint32_t>(v0 + j * kVec + e)));
+      for (int x = 0; x < kUnroll; ++x) {
+        const float m = vec_max<T>(u[x]);
+        const int jx = j + x * kThreads, jn = jx + kUnroll * kThreads;
+        if (jx < nvec && (bj < 0 || (!(m <= best) && best == best))) {
+          best = m;
+          bj = jx;
+          bv = u[x];
+        }
+        if (jn < nvec) u[x] = ld_stream16(vp + jn);
+      }
     }
+    if (bj >= 0) {
+      float f[kVec];
+      unpack16<T>(bv, f);
+      int e = kVec - 1;
+#pragma unroll
+      for (int i = kVec - 1; i >= 0; --i)
+        if (best != best ? f[i] != f[i] : f[i] == best) e = i;
+      k = max(k, argmax_key(best, static_cast<uint32_t>(v0 + bj * kVec + e)));
+    }
+    if (t0 + tid < c1)
+      k = max(k, argmax_key(Elem<T>::to_f(base[t0 + tid]), static_cast<uint32_t>(t0 + tid)));
     k = warp_max_u64(k);
     if (lane == 0) key_sh[warp] = k;
     __syncthreads();
@@ -193,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 6) sampled_row_kernel(const VerifyAr
     return;
   }
   const float c = scale_of(temp);
+  const uint64_t c2 = pack_f32x2(c, c);
   Stat st{-INFINITY, 0.f};
   if (tid < head) st = join(st, Stat{Elem<T>::to_f(base[c0 + tid]), 1.f}, c);
   if (t0 + tid < c1) st = join(st, Stat{Elem<T>::to_f(base[t0 + tid]), 1.f}, c);
@@ -205,27 +252,32 @@ __global__ void __launch_bounds__(kThreads, 6) sampled_row_kernel(const VerifyAr
     st.s *= ex2((st.m - off) * c);
     st.m = m;
     const int jn = j + kUnroll * kThreads;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint64_t off2 = pack_f32x2(-off, -off);
+    uint64_t s[2] = {0ull, 0ull};
 #pragma unroll
     for (int x = 0; x < kUnroll; ++x) {
       float f[kVec];
       unpack16<T>(u[x], f);
-      u[x] = jn + x * kThreads < nvec ? ld_stream16(vp + jn + x * kThreads) : none;
+      if (jn + x * kThreads < nvec)
+        u[x] = ld_stream16(vp + jn + x * kThreads);
+      else
+        u[x] = none;
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) s[e & 3] += ex2((f[e] - off) * c);
+      for (int e = 0; e < kVec; e += 2) {
+        float p, q;
+        unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(f[e], f[e + 1]), off2), c2), p, q);
+        s[e / 2 & 1] = add_f32x2(s[e / 2 & 1], pack_f32x2(ex2(p), ex2(q)));
+      }
     }
-    st.s += (s[0] + s[1]) + (s[2] + s[3]);
+    float s0, s1;
+    unpack_f32x2(add_f32x2(s[0], s[1]), s0, s1);
+    st.s += s0 + s1;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1)
-    st = join(st, Stat{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o)}, c);
+  st = warp_join(st, c);
   if (lane == 0) st_sh[warp] = st;
   __syncthreads();
   if (warp == 0) {
-    st = lane < kThreads / 32 ? st_sh[lane] : Stat{-INFINITY, 0.f};
-#pragma unroll
-    for (int o = 4; o; o >>= 1)
-      st = join(st, Stat{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o)}, c);
+    st = warp_join(lane < kThreads / 32 ? st_sh[lane] : Stat{-INFINITY, 0.f}, c);
     if (lane == 0)
       a.rows[static_cast<size_t>(row) * a.splits + sp] =
           (static_cast<uint64_t>(__float_as_uint(st.m)) << 32) | __float_as_uint(st.s);
@@ -291,10 +343,7 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
       s = join(s, Stat{__uint_as_float(static_cast<uint32_t>(w >> 32)),
                        __uint_as_float(static_cast<uint32_t>(w))}, c);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-      s = join(s, Stat{__shfl_xor_sync(0xffffffffu, s.m, o), __shfl_xor_sync(0xffffffffu, s.s, o)}, c);
-    return s;
+    return warp_join(s, c);
   };
   auto row_pick = [&](int j) {
     unsigned long long k = 0ull;
@@ -356,29 +405,54 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
     const int c0 = sp * a.rchunk, c1 = min(a.V, c0 + a.rchunk);
     const float it = (1.f / temp);
     float bs = -INFINITY, bl = 0.f, bg = 0.f;
-    for (int v = c0 + tid * kRace; v < c1; v += kThreads * kRace) {
-      float l[kRace], g[kRace];
-      if (a.vec && v + kRace <= c1) {
-        unpack16<float>(ld_stream16(gp + v), g);
-        unpack16<float>(ld_stream16(gp + v + 4), g + 4);
-        unpack16<T>(*reinterpret_cast<const uint4*>(lp + v), l);
-        if (sizeof(T) == 4) unpack16<T>(*reinterpret_cast<const uint4*>(lp + v + 4), l + 4);
-      } else {
+    auto look = [&](float l, float g, int v) {
+      const float x = v == skip || l == -INFINITY ? -INFINITY : fmaf(l, it, g);
+      if (x > bs) {
+        bs = x;
+        bl = l;
+        bg = g;
+        bi = v;
+      }
+    };
+    constexpr int kVecs = sizeof(T) == 2 ? 1 : 2;  // 16-byte vectors of kRace logits
+    constexpr int kStep = kThreads * kRace;
+    int v = c0 + tid * kRace;
+    if (a.vec) {
+      for (; v + kRace <= c1; v += kRaceRounds * kStep) {
+        // all the rounds' loads first
+        uint4 lv[kRaceRounds][kVecs], gv[kRaceRounds][2];
+#pragma unroll
+        for (int x = 0; x < kRaceRounds; ++x)
+          if (v + x * kStep + kRace <= c1) {
+#pragma unroll
+            for (int y = 0; y < kVecs; ++y)
+              lv[x][y] = *reinterpret_cast<const uint4*>(lp + v + x * kStep + y * (kRace / kVecs));
+            gv[x][0] = ld_stream16(gp + v + x * kStep);
+            gv[x][1] = ld_stream16(gp + v + x * kStep + 4);
+          }
+#pragma unroll
+        for (int x = 0; x < kRaceRounds; ++x)
+          if (v + x * kStep + kRace <= c1) {
+            float l[kRace], g[kRace];
+#pragma unroll
+            for (int y = 0; y < kVecs; ++y) unpack16<T>(lv[x][y], l + y * (kRace / kVecs));
+            unpack16<float>(gv[x][0], g);
+            unpack16<float>(gv[x][1], g + 4);
+#pragma unroll
+            for (int e = 0; e < kRace; ++e) look(l[e], g[e], v + x * kStep + e);
+          }
+      }
+    } else {
+      for (v = c0 + tid; v < c1; v += kRace * kThreads) {
+        float l[kRace], g[kRace];
 #pragma unroll
         for (int e = 0; e < kRace; ++e) {
-          l[e] = v + e < c1 ? Elem<T>::to_f(lp[v + e]) : -INFINITY;
-          g[e] = v + e < c1 ? gp[v + e] : 0.f;
+          const int w = v + e * kThreads;
+          l[e] = w < c1 ? Elem<T>::to_f(lp[w]) : -INFINITY;
+          g[e] = w < c1 ? gp[w] : 0.f;
         }
-      }
 #pragma unroll
-      for (int e = 0; e < kRace; ++e) {
-        const float s = v + e == skip || l[e] == -INFINITY ? -INFINITY : fmaf(l[e], it, g[e]);
-        if (s > bs) {
-          bs = s;
-          bl = l[e];
-          bg = g[e];
-          bi = v + e;
-        }
+        for (int e = 0; e < kRace; ++e) look(l[e], g[e], v + e * kThreads);
       }
     }
     // The threads whose best is within reach of the CTA's compare in 64 bits (doubles are
