@@ -8,8 +8,8 @@
 //
 // The rows of a request that share a KV head (n_r tokens x H/G heads, token-major)
 // are cut into units of up to 256 rows.  One CTA works on one unit at a time with
-// two streams of 128 rows, each with its own softmax warpgroup (one thread per
-// row), so that one stream's products run while the other's exponentials do:
+// two streams of 128 rows, each with softmax warps of its own, so that one stream's
+// products run while the other's exponentials do:
 //   wide unit   (129..256 rows): stream s holds rows 128 s ..; both read every tile;
 //   narrow unit (at most 128 rows: verify rows, single tokens): both streams hold
 //               the same rows and take the tiles in turn; their (m, l, O) join at
@@ -21,8 +21,9 @@
 // workspace, at most two per CTA, and a second kernel joins them.  Every CTA finds
 // its piece itself from qsl and seq_len, so the host needs no lengths.
 //
-// Warps: 0-3 softmax of stream 0, 4-7 of stream 1, 8 K tiles and the unit list, 9 and 10
-// the products of either stream, 11 V tiles.
+// Warps: 0-7 softmax of stream 0 (two warps to 32 rows, half the keys of a tile each),
+// 8-15 of stream 1, 16 K tiles and the unit list, 17 and 18 the products of either stream,
+// 19 V tiles.
 #include <algorithm>
 #include <atomic>
 
@@ -32,7 +33,7 @@
 namespace pe {
 namespace {
 
-constexpr int kThreads = 384;  // three warpgroups
+constexpr int kThreads = 640;     // four softmax warpgroups, one of K, V and product warps
 constexpr int kTile = 128;        // keys per tile, rows per stream
 constexpr int kUnitRows = 256;
 constexpr int kItems = 4;         // unit descriptors in flight
@@ -163,11 +164,6 @@ PE_DEV void load_box(void* dst, const CUtensorMap* map, uint64_t* bar, int row, 
   }
 }
 
-template <int N>
-struct Const {
-  static constexpr int value = N;
-};
-
 // Two fp32 values in one 64-bit register, for the paired fp32 instructions (half the
 // issue slots).
 PE_DEV uint64_t pack_f32x2(float a, float b) {
@@ -215,17 +211,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t k_full[S::kSlots], k_empty[S::kSlots];
   __shared__ __align__(8) uint64_t v_full[S::kSlots], v_empty[S::kSlots];
   __shared__ __align__(8) uint64_t it_full[kItems], it_empty[kItems];
-  __shared__ __align__(8) uint64_t q_full[kItems][2], s_full[2], s_free[2], p_full[2], pv_done[2], x_bar[2], lag_bar;
+  __shared__ __align__(8) uint64_t q_full[kItems][2], s_full[2], s_free[2], p_full[2], pv_done[2], x_bar[2], pair_bar[2][4], lag_bar;
   __shared__ __align__(8) uint64_t end_bar;
   __shared__ Unit items[kItems];
   __shared__ uint32_t mask_sh[kMasks];  // per tile: bit j = keys 8j..8j+7 were loaded
   __shared__ float ml_sh[2][kTile][2];
+  __shared__ float pair_sh[2][2][2][kTile];  // [stream][half][buffer][row]
   __shared__ long long scan_sh[kThreads / 32];
   __shared__ Place place_sh[2];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   const ChunkArgs& a = p.c;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (values that are the same across a warp go through a shuffle: the compiler then
+  // keeps them in the warp's uniform registers)
+  auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   uint8_t* q_sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* k_ring = q_sm + 2 * S::kTileBytes;
@@ -241,18 +241,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&it_full[i], 1);
-      mbar_init(&it_empty[i], 2 * kTile + 3);
-      mbar_init(&q_full[i][0], kTile);
-      mbar_init(&q_full[i][1], kTile);
+      mbar_init(&it_empty[i], 4 * kTile + 3);
+      mbar_init(&q_full[i][0], 2 * kTile);
+      mbar_init(&q_full[i][1], 2 * kTile);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&s_free[s], kTile);
-      mbar_init(&p_full[s], kTile);
+      mbar_init(&s_free[s], 2 * kTile);
+      mbar_init(&p_full[s], 2 * kTile);
       mbar_init(&pv_done[s], 1);
-      mbar_init(&x_bar[s], 2 * kTile);
+      mbar_init(&x_bar[s], 4 * kTile);
+      for (int w = 0; w < 4; ++w) mbar_init(&pair_bar[s][w], 64);
     }
-    mbar_init(&lag_bar, kTile);
+    mbar_init(&lag_bar, 2 * kTile);
     mbar_init(&end_bar, 2);
     abort_sh = 0;
     fence_barrier_init();
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // tensor memory before the next kernel may start: a successor's CTA that held
   // some of it while waiting for this grid would keep this one from starting
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(&tmem_sh, 512);
     tmem_relinquish();
   }
@@ -434,25 +435,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (idle) {
     if (tid == 0) p.rec[blockIdx.x * 8] = p.rec[blockIdx.x * 8 + 1] = 0;
-  } else if (warp < 8) {
-    // registers: 384 x 168 at launch = 2 x 128 x 216 + 128 x 72
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    // ---------------- softmax warpgroups: one thread per row
-    const int s = warp >> 2, wq = warp & 3, i = tid & (kTile - 1);
+  } else if (warp < 16) {
+    // registers: 640 x 96 at launch = 4 x 128 x 104 + 128 x 64
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // ---------------- softmax warpgroups: two threads per row, of two warps that share
+    // the tensor-memory lanes; thread hf has keys 64 hf .. of a tile and half the columns
+    // of O.  (One thread per row left a scheduler two warps, in which the waits of a step
+    // took longer than its exponentials.)
+    const int s = warp >> 3, hf = warp >> 2 & 1, wq = warp & 3, i = wq * 32 + lane;
     const uint32_t tm = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-    const uint32_t tS = tm + S::kS + s * 128, tP = tm + S::kP + s * S::kPStride;
+    const uint32_t tS = tm + S::kS + s * 128 + 64 * hf, tP = tm + S::kP + s * S::kPStride + 32 * hf;
+    const uint32_t tO = tm + S::kO + (HD / 2) * hf;  // of stream 0; stream 1's HD columns on
     const float sc = kLog2e / sqrtf(static_cast<float>(HD));
-    uint32_t n_items = 0, n_st = 0, tiles = 0, n_x = 0;
+    uint32_t n_items = 0, n_st = 0, tiles = 0, n_x = 0, n_pair = 0;
     bool go = true;
-    // Rows move between global and shared memory a whole row per HD / 8 lanes: each
-    // instruction covers kRpi full rows of this warp's 32.  These loops, and those over
+    // Half rows move between global and shared memory kLpr lanes to a row: each
+    // instruction covers kRpi rows of this warp's 32.  These loops, and those over
     // the columns of O, stay rolled: a unit boundary runs cold code, and unrolled it
     // cost 5000 (head size 64) to 12000 clocks (128) for its instruction fetches.
-    constexpr int kLpr = HD / 8, kRpi = 32 / kLpr;
+    constexpr int kLpr = HD / 16, kRpi = 32 / kLpr;
     const int own = wq * 32;
     auto tile_at = [&](int tile, int row, int ch) {  // 16-byte chunk ch of a row, 128-byte swizzle
       return reinterpret_cast<uint4*>(q_sm + tile * S::kTileBytes + (ch >> 3) * (kTile * 128) +
                                       row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+    };
+    // A value of this row from the thread with its other half.
+    auto partner = [&](float v, float& other) {
+      const int buf = n_pair & 1;
+      pair_sh[s][hf][buf][i] = v;
+      mbar_arrive(&pair_bar[s][wq]);
+      if (!wait_warp(&pair_bar[s][wq], n_pair & 1)) return false;
+      other = pair_sh[s][hf ^ 1][buf][i];
+      ++n_pair;
+      return true;
     };
     auto split = [&](int R, int& tok, int& head) {  // packed row -> token, head in the group
       tok = p.hg_shift >= 0 ? R >> p.hg_shift : R / HG;
@@ -475,13 +490,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = n_items % kItems;
       if (!wait_warp(&it_full[slot], (n_items / kItems) & 1)) return false;
       ++n_items;
-      cur = items[slot].r < 0 ? -1 : slot;
+      cur = uniform(items[slot].r < 0 ? -1 : slot);
       long long off;
       if (q_row(items[slot], off)) {
-        const bf16* q = static_cast<const bf16*>(a.q) + off;
-#pragma unroll
-        for (int h = 0; h < S::kHalves; ++h)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64 * h));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const bf16*>(a.q) + off + HD / 2 * hf));
       }
       return true;
     };
@@ -491,12 +503,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     while (cur >= 0) {
       const int slot = cur;
-      const int nt = items[slot].tile1 - items[slot].tile0;
-      const bool wide = items[slot].wide;
+      const int nt = uniform(items[slot].tile1 - items[slot].tile0);
+      const bool wide = uniform(items[slot].wide);
       const int rel = wide ? s * kTile + i : i;           // row within the unit
       const bool row_ok = rel < items[slot].rows;
-      const bool live = (rel & ~31) < items[slot].rows;   // some row of this warp exists
-      const int kend = items[slot].kend, tile0 = items[slot].tile0;
+      const bool live = uniform((rel & ~31) < items[slot].rows);  // some row of this warp exists
+      const int kend = uniform(items[slot].kend), tile0 = uniform(items[slot].tile0);
       int lim, lim0;  // the last key that this row sees, and the unit's first row
       {
         int tok, head;
@@ -504,14 +516,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int p0 = items[slot].L - items[slot].n;
         lim = row_ok ? p0 + tok : -1;
         split(items[slot].row0, tok, head);
-        lim0 = p0 + tok;
+        lim0 = uniform(p0 + tok);
       }
       if (wide || s == 0) {
         long long off;
         const unsigned oks = __ballot_sync(0xffffffffu, q_row(items[slot], off));
 #pragma unroll 2
         for (int it = 0; it < kLpr; ++it) {
-          const int src = it * kRpi + lane / kLpr, ch = lane % kLpr;
+          const int src = it * kRpi + lane / kLpr, ch = hf * kLpr + lane % kLpr;
           const long long o = __shfl_sync(0xffffffffu, off, src);
           cp_async16(smem_u32(tile_at(wide ? s : 0, own + src, ch)),
                      static_cast<const bf16*>(a.q) + o + ch * 8, oks >> src & 1);
@@ -534,31 +546,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t have = mask_sh[(tiles + j) % kMasks];
+        const uint32_t have = uniform(mask_sh[(tiles + j) % kMasks]);
         const bool inner = t0 + kTile - 1 <= lim0 && have == 0xffffu;
-        uint32_t x[kTile];
+        uint32_t x[64];
+        const int c0 = t0 + 64 * hf;  // this thread's keys
         float best = -INFINITY;  // this row's largest score of the tile
         if (live) {
           if (inner) {
-            uint32_t mx[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) tmem_ld32_max_issue(tS + 32 * b, x + 32 * b, mx[b]);
+            uint32_t m0, m1;
+            tmem_ld32_max_issue(tS, x, m0);
+            tmem_ld32_max_issue(tS + 32, x + 32, m1);
             tmem_wait_ld();
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              tmem_use32(x + 32 * b);
-              tmem_use(mx[b]);
-              best = fmaxf(best, __uint_as_float(mx[b]));
-            }
+            tmem_use32(x);
+            tmem_use32(x + 32);
+            tmem_use(m0);
+            tmem_use(m1);
+            best = fmaxf(__uint_as_float(m0), __uint_as_float(m1));
           } else {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) tmem_ld32_issue(tS + 32 * b, x + 32 * b);
+            tmem_ld32_issue(tS, x);
+            tmem_ld32_issue(tS + 32, x + 32);
             tmem_wait_ld();
+            tmem_use32(x);
+            tmem_use32(x + 32);
+            const uint32_t mine = have >> (8 * hf);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) tmem_use32(x + 32 * b);
-#pragma unroll
-            for (int c = 0; c < kTile; ++c) {
-              if (t0 + c > lim || !(have >> (c >> 3) & 1u)) x[c] = 0xff800000u;
+            for (int c = 0; c < 64; ++c) {
+              if (c0 + c > lim || !(mine >> (c >> 3) & 1u)) x[c] = 0xff800000u;
               best = fmaxf(best, __uint_as_float(x[c]));
             }
           }
@@ -568,7 +581,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&s_free[s]);
         }
         if (live) {
-          const float top = best * sc;
+          float other;
+          if (!partner(best, other)) {
+            go = false;
+            break;
+          }
+          const float top = fmaxf(best, other) * sc;
           // raise the maximum: at the first finite score, or when it climbed far
           const bool raise = top > m + kLazy || (m == -INFINITY && top > m);
           if (__any_sync(0xffffffffu, raise)) {
@@ -584,13 +602,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
 #pragma unroll 1
               for (int b = 0; b < HD / 32; ++b) {
-                uint32_t o[32];
-                tmem_ld32_issue(tm + S::kO + s * HD + 32 * b, o);
+                uint32_t o[16];
+                tmem_ld16_issue(tO + s * HD + 16 * b, o);
                 tmem_wait_ld();
-                tmem_use32(o);
+                tmem_use16(o);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-                tmem_st32_issue(tm + S::kO + s * HD + 32 * b, o);
+                for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                tmem_st16_issue(tO + s * HD + 16 * b, o);
               }
               tmem_wait_st();
             }
@@ -599,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t sc2 = pack_f32x2(sc, sc), off2 = pack_f32x2(-off, -off);
           uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll
-          for (int c = 0; c < kTile; c += 2) {
+          for (int c = 0; c < 64; c += 2) {
             float p0, p1;
             unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, off2),
                          p0, p1);
@@ -622,7 +640,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live) {
           tc_fence_after();
           tmem_st32_issue(tP, x);
-          tmem_st32_issue(tP + 32, x + 32);
           tmem_wait_st();
         }
         // Keys that no row sees (past the unit's last, or of a skipped block) hold
@@ -637,8 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t0 + i >= kend || !(have >> (i >> 3) & 1u)) {
             uint8_t* v = v_ring + (idx % S::kSlots) * S::kTileBytes + (i >> 3) * S::kGroupBytes + (i & 7) * 128;
 #pragma unroll
-            for (int ch = 0; ch < HD / 8; ++ch)
+            for (int c = 0; c < kLpr; ++c) {
+              const int ch = hf * kLpr + c;
               *reinterpret_cast<uint4*>(v + (ch >> 3) * 1024 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
+            }
           }
           fence_proxy_async();
         }
@@ -658,6 +677,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       n_st += mysteps;
       tiles += nt;
       tc_fence_after();
+      if (live) {
+        float other;
+        if (!partner(l, other)) {
+          fail();
+          break;
+        }
+        l += other;
+      }
       const bool whole = items[slot].whole;
       int tok, head;
       split(items[slot].row0 + (row_ok ? rel : 0), tok, head);
@@ -668,10 +695,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float sk = whole && a.sink && row_ok ? a.sink[head] * kLog2e : -INFINITY;
       // ---------------- results: through this stream's Q tile (whole units), or as fp32
       // partials straight to the workspace
-      auto emit = [&](int col, uint32_t* o, float f) {  // 32 columns from col
+      auto emit = [&](int col, uint32_t* o, float f) {  // 16 columns from col
         if (whole) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -682,21 +709,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (row_ok) {
           uint4* d = reinterpret_cast<uint4*>(p.part_o + prow * HD + col);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) d[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          for (int c = 0; c < 4; ++c) d[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
         }
       };
-      // chunks [c0, c0 + n) of this warp's rows out of the tile, n lanes a row
+      // this half of this warp's rows, out of the tile
       const unsigned oks = __ballot_sync(0xffffffffu, row_ok);
-      auto flush = [&](int c0, auto n_) {
-        constexpr int n = decltype(n_)::value, rpi = 32 / n;
+      auto flush = [&]() {
         __syncwarp();
 #pragma unroll 2
-        for (int it = 0; it < n; ++it) {
-          const int src = it * rpi + lane / n;
+        for (int it = 0; it < kLpr; ++it) {
+          const int src = it * kRpi + lane / kLpr, ch = hf * kLpr + lane % kLpr;
           const long long o = __shfl_sync(0xffffffffu, out_off, src);
           if (oks >> src & 1)
-            *reinterpret_cast<uint4*>(static_cast<bf16*>(a.out) + o + (c0 + lane % n) * 8) =
-                *tile_at(s, own + src, c0 + lane % n);
+            *reinterpret_cast<uint4*>(static_cast<bf16*>(a.out) + o + ch * 8) = *tile_at(s, own + src, ch);
         }
         __syncwarp();
       };
@@ -713,20 +738,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live) {
 #pragma unroll 1
           for (int b = 0; b < HD / 32; ++b) {
-            uint32_t o[32];
-            tmem_ld32_issue(tm + S::kO + s * HD + 32 * b, o);
+            uint32_t o[16];
+            tmem_ld16_issue(tO + s * HD + 16 * b, o);
             tmem_wait_ld();
-            tmem_use32(o);
-            emit(32 * b, o, f);
+            tmem_use16(o);
+            emit(HD / 2 * hf + 16 * b, o, f);
           }
         }
-        if (live && whole) flush(0, Const<kLpr>{});
-        if (!whole && row_ok) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
+        if (live && whole) flush();
+        if (!whole && row_ok && hf == 0)
+          *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
         tc_fence_before();
       } else {
-        // the two streams' states of the same row join; each group writes half the columns
-        ml_sh[s][i][0] = m;
-        ml_sh[s][i][1] = l;
+        // the two streams' states of the same row join; stream 0's groups write the row
+        if (hf == 0) {
+          ml_sh[s][i][0] = m;
+          ml_sh[s][i][1] = l;
+        }
         tc_fence_before();
         mbar_arrive(&x_bar[0]);
         if (!wait_warp(&x_bar[0], n_x & 1)) {
@@ -734,35 +762,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const float m0 = ml_sh[0][i][0], m1 = ml_sh[1][i][0];
-        const float M = fmaxf(m0, m1);
-        const float w0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), w1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-        const float den = ml_sh[0][i][1] * w0 + ml_sh[1][i][1] * w1;
-        const float f = factor(M, den);
-        if (live) {
+        if (live && s == 0) {
+          const float m0 = ml_sh[0][i][0], m1 = ml_sh[1][i][0];
+          const float M = fmaxf(m0, m1);
+          const float w0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), w1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+          const float den = ml_sh[0][i][1] * w0 + ml_sh[1][i][1] * w1;
+          const float f = factor(M, den);
 #pragma unroll 1
-          for (int b = 0; b < HD / 64; ++b) {
-            const int col = s * (HD / 2) + 32 * b;
-            uint32_t o[32];
-            tmem_ld32_issue(tm + S::kO + col, o);
+          for (int b = 0; b < HD / 32; ++b) {
+            uint32_t o[16];
+            tmem_ld16_issue(tO + 16 * b, o);
             tmem_wait_ld();
-            tmem_use32(o);
+            tmem_use16(o);
             if (nt > 1) {
-              uint32_t o1[32];
-              tmem_ld32_issue(tm + S::kO + HD + col, o1);
+              uint32_t o1[16];
+              tmem_ld16_issue(tO + HD + 16 * b, o1);
               tmem_wait_ld();
-              tmem_use32(o1);
+              tmem_use16(o1);
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
+              for (int c = 0; c < 16; ++c)
                 o[c] = __float_as_uint(__uint_as_float(o[c]) * w0 + __uint_as_float(o1[c]) * w1);
             }
-            emit(col, o, f);
+            emit(HD / 2 * hf + 16 * b, o, f);
           }
+          if (whole) flush();
+          if (!whole && row_ok && hf == 0)
+            *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(M, den);
         }
-        if (live && whole) flush(s * (kLpr / 2), Const<kLpr / 2>{});
-        if (!whole && row_ok && s == 0)
-          *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(M, den);
-        // the other group may still read this stream's O (and ml_sh)
+        // stream 1's O and ml_sh have been read
         tc_fence_before();
         mbar_arrive(&x_bar[1]);
         if (!wait_warp(&x_bar[1], n_x & 1)) {
@@ -774,8 +801,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&it_empty[slot]);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 16) {
     // ---------------- K warp: lists the units of this CTA's piece and streams their K
     // tiles (the V warp, below, their V tiles: one warp issues a 2 KB box every 90 ns,
     // half of what an SM's share of DRAM needs at head size 64)
@@ -873,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     drain(k_full, loads);
     __syncwarp();
-    } else if (warp == 11) {
+    } else if (warp == 19) {
     // ---------------- V warp
     uint32_t loads = 0;
     for (uint32_t n_items = 0;; ++n_items) {
@@ -899,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // which the tensor pipe worked 614).  All lanes follow the steps and an elected one
     // issues: in a branch of one lane the operands' descriptors go through vector
     // registers for every product (955 clocks a tile against 690 in isolation).
-    const int s = warp - 9;
+    const int s = warp - 17;
     uint32_t tiles = 0, seen_k = 0, seen_v = 0, n_items = 0, n_st = 0, n_wide = 0;
     const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
     const uint32_t idesc_o = idesc_bf16_f32(kTile, HD) | (1u << 16);  // V is MN-major
@@ -1007,7 +1034,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
