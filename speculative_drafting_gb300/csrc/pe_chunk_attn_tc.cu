@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t k_full[S::kSlots], k_empty[S::kSlots];
   __shared__ __align__(8) uint64_t v_full[S::kSlots], v_empty[S::kSlots];
   __shared__ __align__(8) uint64_t it_full[kItems], it_empty[kItems];
-  __shared__ __align__(8) uint64_t q_full[kItems][2], s_full[2], s_free[2], p_full[2], pv_done[2], x_bar[2], pair_bar[2][4], lag_bar;
+  __shared__ __align__(8) uint64_t q_full[kItems][2], s_full[2], s_free[2], p_full[2], pv_done[2], x_bar[2], pair_bar[2][4];
   __shared__ __align__(8) uint64_t end_bar;
   __shared__ Unit items[kItems];
   __shared__ uint32_t mask_sh[kMasks];  // per tile: bit j = keys 8j..8j+7 were loaded
@@ -253,7 +253,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&x_bar[s], 4 * kTile);
       for (int w = 0; w < 4; ++w) mbar_init(&pair_bar[s][w], 64);
     }
-    mbar_init(&lag_bar, 2 * kTile);
     mbar_init(&end_bar, 2);
     abort_sh = 0;
     fence_barrier_init();
@@ -663,7 +662,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(&p_full[s]);
-        if (S::kAhead == 4 && wide && s == 0 && k == 0) mbar_arrive(&lag_bar);
       }
       if (!go) {
         fail();
@@ -927,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // issues: in a branch of one lane the operands' descriptors go through vector
     // registers for every product (955 clocks a tile against 690 in isolation).
     const int s = warp - 17;
-    uint32_t tiles = 0, seen_k = 0, seen_v = 0, n_items = 0, n_st = 0, n_wide = 0;
+    uint32_t tiles = 0, seen_k = 0, seen_v = 0, n_items = 0, n_st = 0;
     const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
     const uint32_t idesc_o = idesc_bf16_f32(kTile, HD) | (1u << 16);  // V is MN-major
     const uint32_t dS = tmem + S::kS + s * 128, dP = tmem + S::kP + s * S::kPStride;
@@ -952,9 +950,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qb = u.wide ? s : 0;
       // (with no step here the other stream may run units ahead: nothing to wait for)
       if (steps > 0) go = wait_warp(&q_full[slot][qb], ((n_items - 1) / kItems) & 1);
-      // Stream 1 of a wide unit starts when stream 0 has its first weights: the two then
-      // stay out of step, one's exponentials beside the other's waits.
-      if (S::kAhead == 4 && go && s == 1 && u.wide) go = wait_warp(&lag_bar, n_wide++ & 1);
       const uint64_t ad = sw128_kmajor_desc(smem_u32(q_sm + qb * S::kTileBytes));
       // Both warps see every load of both rings in order, the other stream's too: a
       // slot's barrier then never is a phase behind or ahead of the one that is waited
@@ -1175,8 +1170,8 @@ int launch_chunk_tc(const ChunkArgs& a, char* ws, cudaStream_t st) {
   p.hg_shift = -1;
   for (int i = 0; i < 8; ++i)
     if (HG == 1 << i) p.hg_shift = i;
-  p.umin = 2;
-  p.overhead = 1;
+  p.umin = 4;
+  p.overhead = 9;
   p.part_rows = part_rows_of(a.T, HG);
   p.rec = reinterpret_cast<int*>(ws + 256);
   p.part_ml = reinterpret_cast<float*>(ws + 256 + rec_bytes());
