@@ -3,8 +3,8 @@
 //
 //   S = Q K^T, P = exp(S / sqrt(hd) - m), l = sum P, O = P V, out = O / l
 //
-// in one pass over 128-key tiles with a running maximum m per row; S, P and O live
-// in tensor memory, K and V come by TMA, page by page.
+// in one pass over tiles of 128 keys (head size 64) or 64 (128) with a running maximum m
+// per row; S, P and O live in tensor memory, K and V come by TMA, page by page.
 //
 // The rows of a request that share a KV head (n_r tokens x H/G heads, token-major)
 // are cut into units of up to 256 rows.  One CTA works on one unit at a time with
@@ -21,20 +21,27 @@
 // workspace, at most two per CTA, and a second kernel joins them.  Every CTA finds
 // its piece itself from qsl and seq_len, so the host needs no lengths.
 //
+// Infinities and NaN.  A key that some rows of a unit see and others do not has weight 0
+// in the others' product, and 0 times what is not finite is NaN.  Rows whose result is
+// not finite though their l is a number, and which do not see all of their unit's keys,
+// are computed again by the second kernel from the keys that they do see.
+//
 // Warps: 0-7 softmax of stream 0 (two warps to 32 rows, half the keys of a tile each),
 // 8-15 of stream 1, 16 K tiles and the unit list, 17 and 18 the products of either stream,
 // 19 V tiles.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
+#include <climits>
 
-#include "pe_paged.h"
+#include "pe_attn_row.cuh"
 #include "pe_tmem.cuh"
 
 namespace pe {
 namespace {
 
 constexpr int kThreads = 640;     // four softmax warpgroups, one of K, V and product warps
-constexpr int kTile = 128;        // keys per tile, rows per stream
+constexpr int kRows = 128;        // rows per stream
 constexpr int kUnitRows = 256;
 constexpr int kItems = 4;         // unit descriptors in flight
 constexpr int kMasks = 16;        // tile masks in flight
@@ -46,17 +53,22 @@ constexpr float kLazy = 8.f;
 template <int HD>
 struct Shape {
   static constexpr int kHalves = HD / 64;             // 128-byte columns of a row
-  static constexpr int kTileBytes = kTile * HD * 2;   // K, V or Q tile
+  static constexpr int kTile = HD == 64 ? 128 : 64;   // keys per tile
+  static constexpr int kTileBytes = kTile * HD * 2;   // a K or V tile
+  static constexpr int kQBytes = kRows * HD * 2;      // a Q tile
   // bytes from one group of 8 keys of a K or V tile to the next (load_box)
   static constexpr int kGroupBytes = 1024 * kHalves;
   // slots of the K ring, and of the V ring: 128 KB in all
-  static constexpr int kSlots = HD == 64 ? 4 : 2;
-  static constexpr int kSmem = (2 + 2 * kSlots) * kTileBytes + 1024;
-  // Steps whose S product may be issued before their P V: with head size 64, P has
-  // tensor memory of its own and S is free as soon as it is in registers; with 128
-  // P takes the place of S, which is free after P V.
-  static constexpr int kAhead = HD == 64 ? 4 : 2;
-  static constexpr uint32_t kS = 0, kP = HD == 64 ? 256 : 0, kPStride = HD == 64 ? 64 : 128;
+  static constexpr int kSlots = 4;
+  static constexpr int kSmem = 2 * kQBytes + 2 * kSlots * kTileBytes + 1024;
+  // Tensor memory, 512 columns: S, P and O of two streams.  Head size 64: 128 + 64 + 64
+  // columns each; S is free again once it is in registers.  Head size 128 leaves 128 for S
+  // and P: two S buffers of a 64-key tile that the steps take in turn, with P in the
+  // place of its S, free after P V.  (With one S of 128 keys, the next product waiting for
+  // P V, the softmax warps waited for S two fifths of their time: mixed chunks 534 us,
+  // 486 like this.)
+  static constexpr bool kOverlay = HD == 128;
+  static constexpr uint32_t kS = 0, kP = kOverlay ? 0 : 256, kPStride = kOverlay ? 128 : 64;
   static constexpr uint32_t kO = HD == 64 ? 384 : 256;
 };
 
@@ -76,6 +88,17 @@ struct Unit {
   int tile0, tile1;     // key tiles of this CTA's part
   int kend;             // keys any row of the unit sees
   int whole;            // the part is the whole unit
+  int index;            // in this CTA's list
+};
+
+// What a CTA leaves for the second kernel.
+struct Rec {
+  int head;                  // its first unit began elsewhere: 1, and ends there too: 2
+  int tail;                  // its last unit goes on in the next CTA: that unit's
+  int q0, g, row0, rows, r;  // first row, KV head, packed rows, request
+  int bad0, bad1;            // range of its whole units with rows to compute again
+  int u_g, u_r, u_qt;        // where its list of units starts
+  int pad[4];
 };
 
 struct TcArgs {
@@ -88,7 +111,7 @@ struct TcArgs {
   float* part_o;    // [grid][2][part_rows][hd]
   float* part_ml;   // [grid][2][part_rows][2]
   int part_rows;
-  int* rec;         // [grid][8]: head code, then the tail: valid, q0, g, row0, rows
+  Rec* rec;         // [grid]
 };
 
 PE_DEV Req load_req(const ChunkArgs& a, int r, bool report) {
@@ -114,12 +137,15 @@ PE_DEV int unit_kend(const Req& q, int i, int HG) {
   const int last = (min((i + 1) * kUnitRows, q.R) - 1) / HG;
   return min(max(q.L - q.n + last + 1, 0), q.L);
 }
-PE_DEV int unit_tiles(int kend) { return max(1, (kend + kTile - 1) / kTile); }
+template <int HD>
+PE_DEV int unit_tiles(int kend) {
+  return max(1, (kend + Shape<HD>::kTile - 1) / Shape<HD>::kTile);
+}
 
 // cost of unit i, and of the units before it (all but the last are wide)
 PE_DEV long long unit_cost(const Req& q, int i, long long ov) {
   const int end = min((i + 1) * kUnitRows, q.R);
-  return (end - i * kUnitRows > kTile ? 2 : 1) * (q.A + end) + ov;
+  return (end - i * kUnitRows > kRows ? 2 : 1) * (q.A + end) + ov;
 }
 PE_DEV long long units_before(const Req& q, int i, long long ov) {
   return i * (2 * q.A + ov) + 256ll * i * (i + 1);
@@ -202,6 +228,37 @@ PE_DEV float ex2(float x) {
   return y;
 }
 
+// `zero`, with NaN in it if one of the eight values is not finite
+PE_DEV __nv_bfloat162 not_finite(const uint4& v, __nv_bfloat162 zero) {
+  const __nv_bfloat162 none = __float2bfloat162_rn(0.f);
+  zero = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.x), none, zero);
+  zero = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.y), none, zero);
+  zero = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.z), none, zero);
+  return __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.w), none, zero);
+}
+
+
+template <int HD>
+__device__ __noinline__ bool flush_rows(bf16* out, long long out_off, bool row_ok, float l, const uint8_t* tile, int hf, int own) {
+  constexpr int kLpr = HD / 16, kRpi = 32 / kLpr;
+  const int lane = threadIdx.x & 31;
+  const unsigned oks = __ballot_sync(0xffffffffu, row_ok), nums = __ballot_sync(0xffffffffu, l == l);
+  __nv_bfloat162 zero = __float2bfloat162_rn(0.f);  // NaN once a value is not finite
+  __syncwarp();
+#pragma unroll 2
+  for (int it = 0; it < kLpr; ++it) {
+    const int src = it * kRpi + lane / kLpr, ch = hf * kLpr + lane % kLpr;
+    const long long o = __shfl_sync(0xffffffffu, out_off, src);
+    if (oks >> src & 1) {
+      const int row = own + src;
+      const uint4 v = *reinterpret_cast<const uint4*>(tile + (ch >> 3) * (kRows * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+      *reinterpret_cast<uint4*>(out + o + ch * 8) = v;
+      if (nums >> src & 1) zero = not_finite(v, zero);
+    }
+  }
+  return __any_sync(0xffffffffu, __hisnan(zero.x) || __hisnan(zero.y));
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_tc_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -211,16 +268,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t k_full[S::kSlots], k_empty[S::kSlots];
   __shared__ __align__(8) uint64_t v_full[S::kSlots], v_empty[S::kSlots];
   __shared__ __align__(8) uint64_t it_full[kItems], it_empty[kItems];
-  __shared__ __align__(8) uint64_t q_full[kItems][2], s_full[2], s_free[2], p_full[2], pv_done[2], x_bar[2], pair_bar[2][4];
+  __shared__ __align__(8) uint64_t q_full[kItems][2], s_full[2][2], s_free[2], p_full[2], pv_done[2];
+  __shared__ __align__(8) uint64_t x_bar[2], pair_bar[2][4];
   __shared__ __align__(8) uint64_t end_bar;
   __shared__ Unit items[kItems];
   __shared__ uint32_t mask_sh[kMasks];  // per tile: bit j = keys 8j..8j+7 were loaded
-  __shared__ float ml_sh[2][kTile][2];
-  __shared__ float pair_sh[2][2][2][kTile];  // [stream][half][buffer][row]
+  __shared__ float ml_sh[2][kRows][2];
+  __shared__ float pair_sh[2][2][2][kRows];  // [stream][half][buffer][row]
   __shared__ long long scan_sh[kThreads / 32];
   __shared__ Place place_sh[2];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
+  __shared__ Rec rec_sh;
+  __shared__ int bad_sh[2];  // first and last unit of the list with rows to compute again
+  constexpr uint32_t kAll = (1u << S::kTile / 8) - 1;  // every group of 8 keys of a tile
   const ChunkArgs& a = p.c;
   // (values that are the same across a warp go through a shuffle: the compiler then
   // keeps them in the warp's uniform registers)
@@ -228,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   uint8_t* q_sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* k_ring = q_sm + 2 * S::kTileBytes;
+  uint8_t* k_ring = q_sm + 2 * S::kQBytes;
   uint8_t* v_ring = k_ring + S::kSlots * S::kTileBytes;
   const int HG = a.H / a.G;
 
@@ -241,20 +302,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&it_full[i], 1);
-      mbar_init(&it_empty[i], 4 * kTile + 3);
-      mbar_init(&q_full[i][0], 2 * kTile);
-      mbar_init(&q_full[i][1], 2 * kTile);
+      mbar_init(&it_empty[i], 4 * kRows + 3);
+      mbar_init(&q_full[i][0], 2 * kRows);
+      mbar_init(&q_full[i][1], 2 * kRows);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&s_full[s], 1);
-      mbar_init(&s_free[s], 2 * kTile);
-      mbar_init(&p_full[s], 2 * kTile);
+      mbar_init(&s_full[s][0], 1);
+      mbar_init(&s_full[s][1], 1);
+      mbar_init(&s_free[s], 2 * kRows);
+      mbar_init(&p_full[s], 2 * kRows);
       mbar_init(&pv_done[s], 1);
-      mbar_init(&x_bar[s], 4 * kTile);
+      mbar_init(&x_bar[s], 4 * kRows);
       for (int w = 0; w < 4; ++w) mbar_init(&pair_bar[s][w], 64);
     }
     mbar_init(&end_bar, 2);
     abort_sh = 0;
+    rec_sh.head = rec_sh.tail = 0;
+    rec_sh.bad1 = -1;
+    bad_sh[0] = INT_MAX;
+    bad_sh[1] = -1;
     fence_barrier_init();
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
@@ -273,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
 
   // ---------------- this CTA's piece of the line
-  const long long ov = static_cast<long long>(p.overhead) * kTile * HG;
+  const long long ov = static_cast<long long>(p.overhead) * 128 * HG;
   const int per = (a.B + kThreads - 1) / kThreads;  // requests per thread
   const int r_lo = min(tid * per, a.B), r_hi = min(r_lo + per, a.B);
   long long mine = 0;
@@ -302,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // has the same line, so a whole number of pieces each, unless that idles more than one
   // CTA in 16.
   const long long W = Wg * a.G;
-  const float least = static_cast<float>(p.umin * kTile * HG);
+  const float least = static_cast<float>(p.umin * 128 * HG);
   int pieces = static_cast<int>(fminf(fmaxf(static_cast<float>(W) / least, 1.f), static_cast<float>(p.grid)));
   const int per_head = pieces / a.G;
   const bool even = per_head > 0 && (pieces - per_head * a.G) * 16 <= pieces;
@@ -344,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (units_before(q, mid, ov) <= rem) lo = mid; else hi = mid;
         }
         const long long off = rem - units_before(q, lo, ov);
-        const int kt = unit_tiles(unit_kend(q, lo, HG));
+        const int kt = unit_tiles<HD>(unit_kend(q, lo, HG));
         // A cut near a unit's end or start moves there: a part costs a CTA some tiles of
         // time whatever its length.
         const float cost_u = static_cast<float>(unit_cost(q, lo, ov));
@@ -361,6 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
+
+  // columns from the first S (and P) to those of a stream's n-th step
+  auto buffer = [](uint32_t n) { return S::kOverlay ? (n & 1) * S::kTile : 0u; };
 
   volatile int* abort_flag = &abort_sh;
   auto fail = [&]() {
@@ -379,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto stream_tiles = [&](const Unit& u, bool is_v, uint8_t* ring, const CUtensorMap* map, uint64_t* full,
                           uint64_t* empty, uint32_t& loads) {
     const uint64_t policy = u.wide ? policy_evict_normal() : policy_evict_first();
-    const int gpt = kTile / p.box;  // boxes per tile
+    const int gpt = S::kTile / p.box;  // boxes per tile
     auto block_of = [&](int wn) {
       const long long key = (static_cast<long long>(wn) * 32 + lane) * p.box;
       return key < u.kend ? a.block_table[static_cast<long long>(u.r) * a.max_blocks + key / a.bs]
@@ -408,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = __popc(have);
       if (lane == 0) {
         if (!is_v) {
-          uint32_t m = 0xffffu;  // the boxes' bits, widened to groups of 8 keys
+          uint32_t m = kAll;  // the boxes' bits, widened to groups of 8 keys
           if (n < gpt) {
             m = 0;
             const int w8 = p.box / 8;
@@ -433,17 +502,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (idle) {
-    if (tid == 0) p.rec[blockIdx.x * 8] = p.rec[blockIdx.x * 8 + 1] = 0;
+    if (tid == 0) {
+      p.rec[blockIdx.x].head = p.rec[blockIdx.x].tail = 0;
+      p.rec[blockIdx.x].bad1 = -1;
+    }
   } else if (warp < 16) {
     // registers: 640 x 96 at launch = 4 x 128 x 104 + 128 x 64
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ---------------- softmax warpgroups: two threads per row, of two warps that share
-    // the tensor-memory lanes; thread hf has keys 64 hf .. of a tile and half the columns
+    // the tensor-memory lanes; thread hf has half hf of a tile's keys and half the columns
     // of O.  (One thread per row left a scheduler two warps, in which the waits of a step
     // took longer than its exponentials.)
     const int s = warp >> 3, hf = warp >> 2 & 1, wq = warp & 3, i = wq * 32 + lane;
     const uint32_t tm = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-    const uint32_t tS = tm + S::kS + s * 128 + 64 * hf, tP = tm + S::kP + s * S::kPStride + 32 * hf;
+    constexpr int kKeys = S::kTile / 2;  // this thread's of a tile
+    const uint32_t tS0 = tm + S::kS + s * 128 + kKeys * hf, tP0 = tm + S::kP + s * S::kPStride + kKeys / 2 * hf;
     const uint32_t tO = tm + S::kO + (HD / 2) * hf;  // of stream 0; stream 1's HD columns on
     const float sc = kLog2e / sqrtf(static_cast<float>(HD));
     uint32_t n_items = 0, n_st = 0, tiles = 0, n_x = 0, n_pair = 0;
@@ -455,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kLpr = HD / 16, kRpi = 32 / kLpr;
     const int own = wq * 32;
     auto tile_at = [&](int tile, int row, int ch) {  // 16-byte chunk ch of a row, 128-byte swizzle
-      return reinterpret_cast<uint4*>(q_sm + tile * S::kTileBytes + (ch >> 3) * (kTile * 128) +
+      return reinterpret_cast<uint4*>(q_sm + tile * S::kQBytes + (ch >> 3) * (kRows * 128) +
                                       row * 128 + (((ch & 7) ^ (row & 7)) << 4));
     };
     // A value of this row from the thread with its other half.
@@ -474,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // This lane's Q row of a unit (element offset), or whether there is none.
     auto q_row = [&](const Unit& u, long long& off) {
-      const int rel = u.wide ? s * kTile + i : i;
+      const int rel = u.wide ? s * kRows + i : i;
       const bool ok = rel < u.rows && (u.wide || s == 0);
       int tok, head;
       split(u.row0 + (ok ? rel : 0), tok, head);
@@ -504,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = cur;
       const int nt = uniform(items[slot].tile1 - items[slot].tile0);
       const bool wide = uniform(items[slot].wide);
-      const int rel = wide ? s * kTile + i : i;           // row within the unit
+      const int rel = wide ? s * kRows + i : i;           // row within the unit
       const bool row_ok = rel < items[slot].rows;
       const bool live = uniform((rel & ~31) < items[slot].rows);  // some row of this warp exists
       const int kend = uniform(items[slot].kend), tile0 = uniform(items[slot].tile0);
@@ -539,43 +612,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;  // m: running maximum in units of log2
       for (int k = 0; k < mysteps; ++k) {
         const int j = wide ? k : 2 * k + s;
-        const int t0 = (tile0 + j) * kTile;
-        if (!wait_warp(&s_full[s], (n_st + k) & 1)) {
+        const int t0 = (tile0 + j) * S::kTile;
+        // (two S products of the overlay may be done before the first is looked at: a
+        // barrier for either buffer)
+        const uint32_t n = n_st + k;
+        if (!wait_warp(&s_full[s][S::kOverlay ? n & 1 : 0], (S::kOverlay ? n >> 1 : n) & 1)) {
           go = false;
           break;
         }
         tc_fence_after();
         const uint32_t have = uniform(mask_sh[(tiles + j) % kMasks]);
-        const bool inner = t0 + kTile - 1 <= lim0 && have == 0xffffu;
-        uint32_t x[64];
-        const int c0 = t0 + 64 * hf;  // this thread's keys
+        const bool inner = t0 + S::kTile - 1 <= lim0 && have == kAll;
+        uint32_t x[kKeys];
+        const int c0 = t0 + kKeys * hf;
+        const uint32_t tS = tS0 + buffer(n), tP = tP0 + buffer(n);
         float best = -INFINITY;  // this row's largest score of the tile
         if (live) {
           if (inner) {
-            uint32_t m0, m1;
-            tmem_ld32_max_issue(tS, x, m0);
-            tmem_ld32_max_issue(tS + 32, x + 32, m1);
-            tmem_wait_ld();
-            tmem_use32(x);
-            tmem_use32(x + 32);
-            tmem_use(m0);
-            tmem_use(m1);
-            best = fmaxf(__uint_as_float(m0), __uint_as_float(m1));
-          } else {
-            tmem_ld32_issue(tS, x);
-            tmem_ld32_issue(tS + 32, x + 32);
-            tmem_wait_ld();
-            tmem_use32(x);
-            tmem_use32(x + 32);
-            const uint32_t mine = have >> (8 * hf);
+            uint32_t mx[kKeys / 32];
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
+            for (int b = 0; b < kKeys / 32; ++b) tmem_ld32_max_issue(tS + 32 * b, x + 32 * b, mx[b]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int b = 0; b < kKeys / 32; ++b) {
+              tmem_use32(x + 32 * b);
+              tmem_use(mx[b]);
+              best = fmaxf(best, __uint_as_float(mx[b]));
+            }
+          } else {
+#pragma unroll
+            for (int b = 0; b < kKeys / 32; ++b) tmem_ld32_issue(tS + 32 * b, x + 32 * b);
+            tmem_wait_ld();
+#pragma unroll
+            for (int b = 0; b < kKeys / 32; ++b) tmem_use32(x + 32 * b);
+            const uint32_t mine = have >> (kKeys / 8 * hf);
+#pragma unroll
+            for (int c = 0; c < kKeys; ++c) {
               if (c0 + c > lim || !(mine >> (c >> 3) & 1u)) x[c] = 0xff800000u;
               best = fmaxf(best, __uint_as_float(x[c]));
             }
           }
         }
-        if (S::kAhead == 4) {
+        if (!S::kOverlay) {
           tc_fence_before();
           mbar_arrive(&s_free[s]);
         }
@@ -616,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t sc2 = pack_f32x2(sc, sc), off2 = pack_f32x2(-off, -off);
           uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
+          for (int c = 0; c < kKeys; c += 2) {
             float p0, p1;
             unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, off2),
                          p0, p1);
@@ -631,26 +709,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           unpack_f32x2(add_f32x2(ls[0], ls[1]), l0, l1);
           l += l0 + l1;
         }
-        // the last P V of this stream has read P
+        // the last P V of this stream has read P (and, with the overlay, the product warp
+        // has taken the p_full before this one)
         if (k > 0 && !wait_warp(&pv_done[s], (n_st + k - 1) & 1)) {
           go = false;
           break;
         }
         if (live) {
           tc_fence_after();
-          tmem_st32_issue(tP, x);
+          if constexpr (kKeys == 64)
+            tmem_st32_issue(tP, x);
+          else
+            tmem_st16_issue(tP, x);
           tmem_wait_st();
         }
         // Keys that no row sees (past the unit's last, or of a skipped block) hold
         // anything, NaN included: their V rows become 0 before the product
-        const bool cut = t0 + kTile > kend || have != 0xffffu;
+        const bool cut = t0 + S::kTile > kend || have != kAll;
         if (cut) {
           const uint32_t idx = tiles + j;
           if (!wait_warp(&v_full[idx % S::kSlots], (idx / S::kSlots) & 1)) {
             go = false;
             break;
           }
-          if (t0 + i >= kend || !(have >> (i >> 3) & 1u)) {
+          if (i < S::kTile && (t0 + i >= kend || !(have >> (i >> 3) & 1u))) {
             uint8_t* v = v_ring + (idx % S::kSlots) * S::kTileBytes + (i >> 3) * S::kGroupBytes + (i & 7) * 128;
 #pragma unroll
             for (int c = 0; c < kLpr; ++c) {
@@ -684,13 +766,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += other;
       }
       const bool whole = items[slot].whole;
-      int tok, head;
-      split(items[slot].row0 + (row_ok ? rel : 0), tok, head);
-      head += items[slot].g * HG;
-      const long long out_off = (items[slot].q0 + tok) * a.ld_out + static_cast<long long>(head) * HD;
-      const size_t prow =
-          (static_cast<size_t>(blockIdx.x) * 2 + (tile0 > 0 ? 0 : 1)) * p.part_rows + rel;
-      const float sk = whole && a.sink && row_ok ? a.sink[head] * kLog2e : -INFINITY;
+      const int prow = (static_cast<int>(blockIdx.x) * 2 + (tile0 > 0 ? 0 : 1)) * p.part_rows + rel;
+      float sk = -INFINITY;
+      if (whole && a.sink && row_ok) {
+        int tok, head;
+        split(items[slot].row0 + rel, tok, head);
+        sk = a.sink[items[slot].g * HG + head] * kLog2e;
+      }
       // ---------------- results: through this stream's Q tile (whole units), or as fp32
       // partials straight to the workspace
       auto emit = [&](int col, uint32_t* o, float f) {  // 16 columns from col
@@ -705,23 +787,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             *tile_at(s, i, col / 8 + c) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else if (row_ok) {
-          uint4* d = reinterpret_cast<uint4*>(p.part_o + prow * HD + col);
+          uint4* d = reinterpret_cast<uint4*>(p.part_o + static_cast<size_t>(prow) * HD + col);
 #pragma unroll
           for (int c = 0; c < 4; ++c) d[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
         }
-      };
-      // this half of this warp's rows, out of the tile
-      const unsigned oks = __ballot_sync(0xffffffffu, row_ok);
-      auto flush = [&]() {
-        __syncwarp();
-#pragma unroll 2
-        for (int it = 0; it < kLpr; ++it) {
-          const int src = it * kRpi + lane / kLpr, ch = hf * kLpr + lane % kLpr;
-          const long long o = __shfl_sync(0xffffffffu, out_off, src);
-          if (oks >> src & 1)
-            *reinterpret_cast<uint4*>(static_cast<bf16*>(a.out) + o + ch * 8) = *tile_at(s, own + src, ch);
-        }
-        __syncwarp();
       };
       // factor of the unnormalised O of a row with (M, den): a sink joins both
       auto factor = [&](float M, float den) {
@@ -743,9 +812,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             emit(HD / 2 * hf + 16 * b, o, f);
           }
         }
-        if (live && whole) flush();
         if (!whole && row_ok && hf == 0)
-          *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
+          *reinterpret_cast<float2*>(p.part_ml + static_cast<size_t>(prow) * 2) = make_float2(m, l);
         tc_fence_before();
       } else {
         // the two streams' states of the same row join; stream 0's groups write the row
@@ -764,8 +832,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m0 = ml_sh[0][i][0], m1 = ml_sh[1][i][0];
           const float M = fmaxf(m0, m1);
           const float w0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), w1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-          const float den = ml_sh[0][i][1] * w0 + ml_sh[1][i][1] * w1;
-          const float f = factor(M, den);
+          l = ml_sh[0][i][1] * w0 + ml_sh[1][i][1] * w1;
+          const float f = factor(M, l);
 #pragma unroll 1
           for (int b = 0; b < HD / 32; ++b) {
             uint32_t o[16];
@@ -783,9 +851,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             emit(HD / 2 * hf + 16 * b, o, f);
           }
-          if (whole) flush();
           if (!whole && row_ok && hf == 0)
-            *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(M, den);
+            *reinterpret_cast<float2*>(p.part_ml + static_cast<size_t>(prow) * 2) = make_float2(M, l);
         }
         // stream 1's O and ml_sh have been read
         tc_fence_before();
@@ -795,6 +862,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         ++n_x;
+      }
+      // This half of this warp's rows, out of the tile.  The unit is noted if a value is not
+      // finite though its row's l is a number.
+      if (live && whole && (wide || s == 0)) {
+        int tok, head;
+        split(items[slot].row0 + (row_ok ? rel : 0), tok, head);
+        head += items[slot].g * HG;
+        const bool bad = flush_rows<HD>(static_cast<bf16*>(a.out), (items[slot].q0 + tok) * a.ld_out + static_cast<long long>(head) * HD, row_ok, l, q_sm + s * S::kQBytes, hf, own);
+        if (bad && lane == 0) {
+          atomicMin(&bad_sh[0], items[slot].index);
+          atomicMax(&bad_sh[1], items[slot].index);
+        }
+        __syncwarp();
       }
       mbar_arrive(&it_empty[slot]);
     }
@@ -807,7 +887,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Place first = place_sh[0], last = place_sh[1];
     Place cur = first;
     uint32_t loads = 0, n_items = 0;
-    int head = 0, tail = 0, t_q0 = 0, t_g = 0, t_row0 = 0, t_rows = 0;
     bool go = true;
     Req q;
     int q_of = -1;
@@ -829,22 +908,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       u.L = q.L;
       u.row0 = cur.qt * kUnitRows;
       u.rows = min(kUnitRows, q.R - u.row0);
-      u.wide = u.rows > kTile;
+      u.wide = u.rows > kRows;
       u.kend = unit_kend(q, cur.qt, HG);
-      const int kt = unit_tiles(u.kend);
+      const int kt = unit_tiles<HD>(u.kend);
       u.tile0 = cur.tile;
       u.tile1 = ends_here ? min(last.tile, kt) : kt;
+      u.index = static_cast<int>(n_items);
       const bool some = u.tile0 < u.tile1;
       u.whole = u.tile0 == 0 && u.tile1 == kt;
-      if (some && !u.whole) {
+      if (some && !u.whole && lane == 0) {
         if (u.tile0 > 0) {
-          head = u.tile1 == kt ? 2 : 1;
+          rec_sh.head = u.tile1 == kt ? 2 : 1;
         } else {
-          tail = 1;
-          t_q0 = u.q0;
-          t_g = u.g;
-          t_row0 = u.row0;
-          t_rows = u.rows;
+          rec_sh.tail = 1;
+          rec_sh.q0 = u.q0;
+          rec_sh.g = u.g;
+          rec_sh.row0 = u.row0;
+          rec_sh.rows = u.rows;
+          rec_sh.r = u.r;
         }
       }
       if (some) {
@@ -861,6 +942,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         items[slot] = u;
         mbar_arrive(&it_full[slot]);
+      }
+      if (n_items == 0 && lane == 0) {
+        rec_sh.u_g = u.g;
+        rec_sh.u_r = u.r;
+        rec_sh.u_qt = cur.qt;
       }
       ++n_items;
       if (!stream_tiles(u, false, k_ring, &kmap, k_full, k_empty, loads)) {
@@ -888,13 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         items[slot].rows = items[slot].wide = items[slot].row0 = 0;
         mbar_arrive(&it_full[slot]);
       }
-      int* rec = p.rec + blockIdx.x * 8;
-      rec[0] = head;
-      rec[1] = tail;
-      rec[2] = t_q0;
-      rec[3] = t_g;
-      rec[4] = t_row0;
-      rec[5] = t_rows;
+      p.rec[blockIdx.x] = rec_sh;
     }
     drain(k_full, loads);
     __syncwarp();
@@ -926,13 +1006,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // registers for every product (955 clocks a tile against 690 in isolation).
     const int s = warp - 17;
     uint32_t tiles = 0, seen_k = 0, seen_v = 0, n_items = 0, n_st = 0;
-    const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
-    const uint32_t idesc_o = idesc_bf16_f32(kTile, HD) | (1u << 16);  // V is MN-major
+    const uint32_t idesc_s = idesc_bf16_f32(kRows, S::kTile);
+    const uint32_t idesc_o = idesc_bf16_f32(kRows, HD) | (1u << 16);  // V is MN-major
     const uint32_t dS = tmem + S::kS + s * 128, dP = tmem + S::kP + s * S::kPStride;
     const uint32_t dO = tmem + S::kO + s * HD;
     // the stride between groups of 8 keys, past the 1024 bytes of the descriptors' default
     constexpr uint64_t kWider = static_cast<uint64_t>((S::kGroupBytes - 1024) / 16) << 32;
-    constexpr int kOwn = S::kAhead / 2;  // this stream's S products ahead of its P V
+    constexpr int kOwn = 2;  // this stream's S products ahead of its P V
     bool go = true;
     while (go) {
       const int slot = n_items % kItems;
@@ -950,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qb = u.wide ? s : 0;
       // (with no step here the other stream may run units ahead: nothing to wait for)
       if (steps > 0) go = wait_warp(&q_full[slot][qb], ((n_items - 1) / kItems) & 1);
-      const uint64_t ad = sw128_kmajor_desc(smem_u32(q_sm + qb * S::kTileBytes));
+      const uint64_t ad = sw128_kmajor_desc(smem_u32(q_sm + qb * S::kQBytes));
       // Both warps see every load of both rings in order, the other stream's too: a
       // slot's barrier then never is a phase behind or ahead of the one that is waited
       // for.  A slot is free when both have let go of it, its users once their products
@@ -980,11 +1060,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t bd = sw128_mnmajor_desc(smem_u32(v_ring + st * S::kTileBytes), 1024) + kWider;
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              umma_bf16_ta(dO, dP + kk * 8, bd + kk * (2 * S::kGroupBytes / 16), idesc_o, k > 0 || kk > 0);
+            for (int kk = 0; kk < S::kTile / 16; ++kk)
+              umma_bf16_ta(dO, dP + buffer(n_st + k) + kk * 8, bd + kk * (2 * S::kGroupBytes / 16), idesc_o,
+                           k > 0 || kk > 0);
             umma_commit(&pv_done[s]);
             umma_commit(&v_empty[st]);
           }
+          // with the overlay P's place is that of the next S but one (or of the next unit's
+          // second S, whose Q may come from the other stream's warps)
+          if (S::kOverlay) go = wait_warp(&pv_done[s], (n_st + k) & 1);
+          if (!go) break;
         }
         const int n = k + kOwn;
         if (n < steps) {  // S = Q K^T of step n
@@ -992,11 +1077,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t idx = tiles + j;
           const int st = idx % S::kSlots;
           go = wait_load(k_full, k_empty, seen_k, idx);
-          // S of the step before is out of the way: in registers (S::kAhead = 4; of the
-          // unit before it is), or P has been multiplied (of the unit before too: a
-          // narrow unit's Q comes from the other stream's group)
-          if (go && (n > 0 || (S::kAhead == 2 && n_st > 0)))
-            go = wait_warp(S::kAhead == 4 ? &s_free[s] : &pv_done[s], (n_st + n - 1) & 1);
+          // the S of the step before is in registers (the unit before's is)
+          if (go && !S::kOverlay && n > 0) go = wait_warp(&s_free[s], (n_st + n - 1) & 1);
           if (!go) break;
           tc_fence_after();
           const uint64_t bd = sw128_kmajor_desc(smem_u32(k_ring + st * S::kTileBytes)) + kWider;
@@ -1004,10 +1086,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
               const uint32_t in = (kk & 3) * 2, half = kk >> 2;
-              umma_bf16(dS, ad + half * (kTile * 128 / 16) + in, bd + half * (1024 / 16) + in,
-                        idesc_s, kk > 0);
+              umma_bf16(dS + buffer(n_st + n), ad + half * (kRows * 128 / 16) + in,
+                        bd + half * (1024 / 16) + in, idesc_s, kk > 0);
             }
-            umma_commit(&s_full[s]);
+            umma_commit(&s_full[s][S::kOverlay ? (n_st + n) & 1 : 0]);
             umma_commit(&k_empty[st]);
           }
         }
@@ -1029,26 +1111,102 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && bad_sh[1] >= 0) {
+    p.rec[blockIdx.x].bad0 = bad_sh[0];
+    p.rec[blockIdx.x].bad1 = bad_sh[1];
+  }
   if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
+PE_DEV bool finite(float v) { return fabsf(v) <= FLT_MAX; }
+
+// By a whole warp: notes a row of the unit at hand to be computed again.
+PE_DEV bool mark(uint32_t* again, bool bad, int row) {
+  bad = __any_sync(0xffffffffu, bad);
+  if (bad && (threadIdx.x & 31) == 0) atomicOr(&again[row >> 5], 1u << (row & 31));
+  return bad;
+}
+
+// The rows noted of the unit at packed row row0, so far as a key of the unit is past them.
+// (This and the next one are calls, not inlined: their registers would be the join's.)
+__device__ __noinline__ void redo_unit(const TcArgs& p, int r, int g, int row0, uint32_t* again,
+                                       RowScratch& scratch) {
+  const ChunkArgs& a = p.c;
+  const int HG = a.H / a.G;
+  __syncthreads();
+  const Req q = load_req(a, r, false);
+  const int kend = unit_kend(q, row0 / kUnitRows, HG);
+  for (int row = 0; row < kUnitRows; ++row) {
+    const int tok = (row0 + row) / HG, head = g * HG + (row0 + row) % HG, lim = q.L - q.n + tok;
+    if (!(again[row >> 5] >> (row & 31) & 1) || lim >= kend - 1) continue;
+    row_query<bf16>(a, q.q0 + tok, head, scratch);
+    __syncthreads();
+    attend_row<bf16>(a, r, q.q0 + tok, head, lim, scratch);
+    __syncthreads();
+  }
+  __syncthreads();
+  if (threadIdx.x < kUnitRows / 32) again[threadIdx.x] = 0;
+  __syncthreads();
+}
+
+// The whole units of this CTA's list up to the last that was noted, as the K warp of the
+// first kernel went through them.
+template <int HD>
+__device__ __noinline__ void redo_list(const TcArgs& p, uint32_t* again, RowScratch& scratch) {
+  const ChunkArgs& a = p.c;
+  const Rec& rec = p.rec[blockIdx.x];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, HG = a.H / a.G;
+  const int bad0 = rec.bad0, bad1 = rec.bad1;
+  int g = rec.u_g, r = rec.u_r, qt = rec.u_qt;
+  for (int unit = 0; unit <= bad1; ++unit) {
+    const Req q = load_req(a, r, false);
+    if (unit >= bad0) {
+      const int n = min(kUnitRows, q.R - qt * kUnitRows);
+      for (int row = blockIdx.y * 4 + warp; row < n; row += gridDim.y * 4) {
+        const int tok = (qt * kUnitRows + row) / HG, head = g * HG + (qt * kUnitRows + row) % HG;
+        const bf16* o = static_cast<const bf16*>(a.out) + (q.q0 + tok) * a.ld_out + static_cast<long long>(head) * HD;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < HD / 32; ++i) bad |= !finite(__bfloat162float(o[lane + 32 * i]));
+        mark(again, bad, row);
+      }
+      redo_unit(p, r, g, qt * kUnitRows, again, scratch);
+    }
+    if (++qt >= q.Q) {
+      qt = 0;
+      r = next_request(a, r + 1, lane);
+      if (r >= a.B) {
+        ++g;
+        r = next_request(a, 0, lane);
+      }
+    }
+  }
+}
+
 // Joins the partials of the units that were cut between CTAs.  CTA (c, y): the unit
 // whose first part is CTA c's last one, a slice of its rows; its other parts are the
-// first ones of the CTAs after c, up to the one that ends it.  One warp per row.
+// first ones of the CTAs after c, up to the one that ends it.  One warp per row.  Then the
+// rows to compute again: of that unit, and of CTA c's whole units that have some.
 template <int HD>
-__global__ void __launch_bounds__(128) chunk_join_kernel(const __grid_constant__ TcArgs p) {
+__global__ void __launch_bounds__(32 * kRowWarps) chunk_join_kernel(const __grid_constant__ TcArgs p) {
   constexpr int V = HD / 32;
+  __shared__ RowScratch scratch;
+  __shared__ uint32_t again_sh[kUnitRows / 32];  // the unit's rows to compute again
   pdl_trigger();
+  if (threadIdx.x < kUnitRows / 32) again_sh[threadIdx.x] = 0;
+  __syncthreads();
   pdl_wait();
   const ChunkArgs& a = p.c;
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int* rec = p.rec + c * 8;
-  if (!rec[1]) return;
-  const int q0 = rec[2], g = rec[3], row0 = rec[4], rows = rec[5];
+  const Rec& rec = p.rec[c];
+  const int bad1 = rec.bad1;
+  if (!rec.tail && bad1 < 0) return;
   const int HG = a.H / a.G;
+  bool some = false;
+  const int q0 = rec.q0, g = rec.g, row0 = rec.row0, rows = rec.tail ? rec.rows : 0;
   for (int row = blockIdx.y * 4 + warp; row < rows; row += gridDim.y * 4) {
     const int tok = (row0 + row) / HG, head = g * HG + (row0 + row) % HG;
     float M = a.sink ? a.sink[head] * kLog2e : -INFINITY;  // the sink: one more part, O = 0
@@ -1061,13 +1219,13 @@ __global__ void __launch_bounds__(128) chunk_join_kernel(const __grid_constant__
     bool more = true;
     for (int k0 = c; more; k0 += 32) {
       const int k = k0 + lane;
-      const int code = k >= p.grid ? 0 : k == c ? 1 : p.rec[k * 8];
+      const int code = k >= p.grid ? 0 : k == c ? 1 : p.rec[k].head;
       const unsigned ends = __ballot_sync(0xffffffffu, code == 2 || k >= p.grid);
       const int last = ends ? __ffs(ends) - 1 : 31;  // of this window
       more = !ends;
       const bool part = code != 0 && lane <= last;
       const size_t prow = (static_cast<size_t>(k) * 2 + (k == c)) * p.part_rows + row;
-      const float2 ml = part ? *reinterpret_cast<const float2*>(p.part_ml + prow * 2)
+      const float2 ml = part ? *reinterpret_cast<const float2*>(p.part_ml + static_cast<size_t>(prow) * 2)
                              : make_float2(-INFINITY, 0.f);
       // (l = 0: no key of the part was seen; NaN counts as seen)
       const bool seen = ml.y != 0.f;
@@ -1107,7 +1265,13 @@ __global__ void __launch_bounds__(128) chunk_join_kernel(const __grid_constant__
     bf16* out = static_cast<bf16*>(a.out) + (q0 + tok) * a.ld_out + static_cast<long long>(head) * HD;
 #pragma unroll
     for (int i = 0; i < V; ++i) out[lane + 32 * i] = __float2bfloat16_rn(acc[i] * inv);
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) bad |= !finite(acc[i]);
+    some |= mark(again_sh, bad && den == den, row);
   }
+  if (__syncthreads_or(some)) redo_unit(p, rec.r, g, row0, again_sh, scratch);
+  if (bad1 >= 0) redo_list<HD>(p, again_sh, scratch);
 }
 
 constexpr int kMaxGrid = 152;
@@ -1115,11 +1279,11 @@ constexpr int kMaxGrid = 152;
 size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
 int part_rows_of(int T, int HG) {
-  return static_cast<long long>(T) * HG > kTile ? kUnitRows : kTile;
+  return static_cast<long long>(T) * HG > kRows ? kUnitRows : kRows;
 }
 
 // offsets past the 256-byte header: records, (m, l), O
-size_t rec_bytes() { return al256(kMaxGrid * 8 * sizeof(int)); }
+size_t rec_bytes() { return al256(kMaxGrid * sizeof(Rec)); }
 size_t ml_bytes(int part_rows) { return al256(size_t{kMaxGrid} * 2 * part_rows * 2 * sizeof(float)); }
 
 template <int HD>
@@ -1162,7 +1326,8 @@ int launch_chunk_tc(const ChunkArgs& a, char* ws, cudaStream_t st) {
   TcArgs p = {};
   p.c = a;
   p.box = 8;
-  while (p.box < kTile && a.bs % (2 * p.box) == 0) p.box *= 2;
+  const int tile = a.hd == 64 ? Shape<64>::kTile : Shape<128>::kTile;
+  while (p.box < tile && a.bs % (2 * p.box) == 0) p.box *= 2;
   const int sms = num_sms_of_current_device();
   if (sms <= 0) return PE_ERR_CUDA;
   p.grid = sms < kMaxGrid ? sms : kMaxGrid;
@@ -1173,7 +1338,7 @@ int launch_chunk_tc(const ChunkArgs& a, char* ws, cudaStream_t st) {
   p.umin = 4;
   p.overhead = 9;
   p.part_rows = part_rows_of(a.T, HG);
-  p.rec = reinterpret_cast<int*>(ws + 256);
+  p.rec = reinterpret_cast<Rec*>(ws + 256);
   p.part_ml = reinterpret_cast<float*>(ws + 256 + rec_bytes());
   p.part_o = reinterpret_cast<float*>(ws + 256 + rec_bytes() + ml_bytes(p.part_rows));
   CUtensorMap km, vm;

@@ -373,3 +373,41 @@ def test_attend_zero_rows():
     t = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
     plan.attend(2, 0, t, t, z, z, z, t, 0, z, ws)
     assert binding.read_status_ws(ws)[0] == 0
+
+
+@pytest.mark.parametrize("dtype,H,G,hd,bs", [("bf16", 64, 8, 64, 16), ("bf16", 28, 4, 128, 16),
+                                             ("bf16", 6, 2, 64, 5), ("f32", 4, 2, 16, 4)])
+@pytest.mark.parametrize("ns,Ls", [((9,), (9,)), ((300,), (300,)), ((8,), (3000,)), ((100, 5), (2100, 3)),
+                                   ((40, 1, 8, 33), (41, 70, 500, 33))])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_attend_infinities_and_nan_at_later_positions(dtype, H, G, hd, bs, ns, Ls, sinks):
+    """What a row does not see does not enter it, be it infinite or NaN in the value or the
+    key, although later rows of the same request do see it: those follow the formula."""
+    c = _chunk(dtype, H, G, hd, bs, ns, Ls, sinks=sinks, extra=2, seed=31)
+    rng = np.random.default_rng(5)
+    kc, vc = O.decode(c["kc"], dtype), O.decode(c["vc"], dtype)
+    for r, (n, L) in enumerate(zip(ns, Ls)):
+        for t in range(max(L - n, 0) + 1, L, max(n // 5, 2)):  # visible from its own row on
+            at = c["table"][r][t // bs], slice(None), t % bs
+            vc[at][:, rng.integers(hd)] = rng.choice([np.nan, np.inf, -np.inf])
+            if t > L - 2:
+                kc[at][0] = np.nan
+    c["kc"], c["vc"] = _store(kc, dtype), _store(vc, dtype)
+    kc, vc = O.decode(c["kc"], dtype), O.decode(c["vc"], dtype)
+    got, st = _attend(c)
+    assert st == 0
+    val = _value(got, dtype).reshape(c["T"], H, hd)
+    assert (val[sum(ns):] == 3.0).all()
+    q = O.decode(c["q"], dtype)[:, :H * hd].reshape(c["T"], H, hd)
+    half, w = (2.0 ** -8, 2.0 ** -8 + 1e-4) if dtype == "bf16" else (2.0 ** -24, 2e-5)
+    for r, (n, L) in enumerate(zip(ns, Ls)):
+        for j in range(n):
+            # one row as a request of its own, over the positions up to its own
+            row = c["qsl"][r] + j
+            with np.errstate(invalid="ignore"):
+                ref, spread = P.chunk_attention([0, 1], [L - n + j + 1], q[row:row + 1], kc, vc,
+                                                c["table"][r:r + 1], c["sink"])
+            fin = np.isfinite(ref[0])
+            np.testing.assert_array_equal(val[row][~fin], ref[0][~fin])
+            err = np.abs(val[row] - np.where(fin, ref[0], 0))[fin]
+            assert (err <= (half * np.abs(ref[0]) + w * spread[0])[fin] + 1e-30).all(), (r, j)
