@@ -438,9 +438,9 @@ int pe_verify_greedy(int B, int T_in, const int32_t* qsl, const int32_t* tok,
  * vocab) has probability 0 (PE_ST_TOKEN_RANGE).  A request with no rows gets
  * accepted 0 and bonus -1.  A qsl that is not a non-decreasing run from 0 to at
  * most T_in sets PE_ST_ROWS_RANGE; the results are then undefined (nothing outside
- * the outputs is touched).  The call clears the status word first.  PE_ERR_ARG: negative sizes, null
- * pointers, logits, u or gumbel not aligned to their element size, ws misaligned
- * or too small, B = 0 with T_in > 0.  PE_ERR_UNSUPPORTED: B > 65535, or a dtype
+ * the outputs is touched).  The call clears the status word first.  PE_ERR_ARG:
+ * negative sizes, null pointers, logits, u or gumbel not aligned to their element
+ * size, ws misaligned or too small, B = 0 with T_in > 0.  PE_ERR_UNSUPPORTED: B > 65535, or a dtype
  * other than the two. */
 size_t pe_verify_sampled_workspace_bytes(int max_batch, int max_rows_in, int vocab);
 int pe_verify_sampled(int B, int T_in, const int32_t* qsl, const int32_t* tok, const void* logits,
@@ -517,8 +517,10 @@ int pe_qkv_append(const pe_attn_plan* plan, int T, const void* qkv, int64_t ld_q
  *               does not clear (zero it once; pe_read_status clears it)
  * Scores are scaled by 1/sqrt(hd); the softmax and its sums are fp32.  A row whose
  * position is negative (seq_len[r] < n_r) or whose keys all lie in invalid blocks
- * sees nothing and gets zeros.  What the caches hold at positions past seq_len[r],
- * or in blocks that are skipped, is never used, NaN included.
+ * sees nothing and gets zeros.  What the caches hold at positions that a row does not
+ * see, or in blocks that are skipped, does not enter the row, NaN and infinities
+ * included (bf16 rows are computed a second time, slowly, where a later position of
+ * the chunk holds one in its value).
  * seq_len outside [0, max_blocks * block_size] is clamped, a block id outside [0,
  * num_blocks) skips its keys: PE_ST_BLOCK_RANGE.  A qsl that is not a non-decreasing
  * run from 0 to at most T sets PE_ST_ROWS_RANGE; the rows of out are then undefined

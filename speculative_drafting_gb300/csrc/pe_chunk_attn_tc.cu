@@ -238,25 +238,44 @@ PE_DEV __nv_bfloat162 not_finite(const uint4& v, __nv_bfloat162 zero) {
 }
 
 
+// packed row -> token, head in the group
+PE_DEV void split_row(const TcArgs& p, int row, int& tok, int& head) {
+  const int HG = p.c.H / p.c.G;
+  tok = p.hg_shift >= 0 ? row >> p.hg_shift : row / HG;
+  head = row - tok * HG;
+}
+
+// A warp's 32 rows from `own` of a stream's tile, half hf of them, to where they belong;
+// rel is this lane's row within the unit, l its sum.  The unit is noted in bad if a value
+// is not finite though its row's l is a number.  (A call, not inlined: what it needs would
+// stay in registers through the steps.)
 template <int HD>
-__device__ __noinline__ bool flush_rows(bf16* out, long long out_off, bool row_ok, float l, const uint8_t* tile, int hf, int own) {
+__device__ __noinline__ void write_rows(const TcArgs& p, const Unit& u, int* bad, int rel, float l,
+                                        const uint8_t* tile, int hf, int own) {
   constexpr int kLpr = HD / 16, kRpi = 32 / kLpr;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, HG = p.c.H / p.c.G;
+  const bool row_ok = rel < u.rows;
+  int tok, head;
+  split_row(p, u.row0 + (row_ok ? rel : 0), tok, head);
+  const long long off = (u.q0 + tok) * p.c.ld_out + static_cast<long long>(u.g * HG + head) * HD;
+  bf16* out = static_cast<bf16*>(p.c.out);
   const unsigned oks = __ballot_sync(0xffffffffu, row_ok), nums = __ballot_sync(0xffffffffu, l == l);
   __nv_bfloat162 zero = __float2bfloat162_rn(0.f);  // NaN once a value is not finite
-  __syncwarp();
 #pragma unroll 2
   for (int it = 0; it < kLpr; ++it) {
-    const int src = it * kRpi + lane / kLpr, ch = hf * kLpr + lane % kLpr;
-    const long long o = __shfl_sync(0xffffffffu, out_off, src);
+    const int src = it * kRpi + lane / kLpr, ch = hf * kLpr + lane % kLpr, row = own + src;
+    const long long o = __shfl_sync(0xffffffffu, off, src);
     if (oks >> src & 1) {
-      const int row = own + src;
-      const uint4 v = *reinterpret_cast<const uint4*>(tile + (ch >> 3) * (kRows * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+      const uint4 v = *reinterpret_cast<const uint4*>(tile + (ch >> 3) * (kRows * 128) + row * 128 +
+                                                      (((ch & 7) ^ (row & 7)) << 4));
       *reinterpret_cast<uint4*>(out + o + ch * 8) = v;
       if (nums >> src & 1) zero = not_finite(v, zero);
     }
   }
-  return __any_sync(0xffffffffu, __hisnan(zero.x) || __hisnan(zero.y));
+  if (__any_sync(0xffffffffu, __hisnan(zero.x) || __hisnan(zero.y)) && lane == 0) {
+    atomicMin(&bad[0], u.index);
+    atomicMax(&bad[1], u.index);
+  }
 }
 
 template <int HD>
@@ -381,7 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       return static_cast<long long>(static_cast<float>(Wg) *
                                     (static_cast<float>(c - g * per_head) / static_cast<float>(per_head)));
     }
-    long long w = static_cast<long long>(static_cast<float>(W) * (static_cast<float>(c) / static_cast<float>(pieces)));
+    long long w =
+        static_cast<long long>(static_cast<float>(W) * (static_cast<float>(c) / static_cast<float>(pieces)));
     w = min(w, W - 1);
     g = min(a.G - 1, static_cast<int>(static_cast<float>(w) / static_cast<float>(Wg)));
     while (w < g * Wg) --g;
@@ -541,16 +561,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++n_pair;
       return true;
     };
-    auto split = [&](int R, int& tok, int& head) {  // packed row -> token, head in the group
-      tok = p.hg_shift >= 0 ? R >> p.hg_shift : R / HG;
-      head = R - tok * HG;
-    };
     // This lane's Q row of a unit (element offset), or whether there is none.
     auto q_row = [&](const Unit& u, long long& off) {
       const int rel = u.wide ? s * kRows + i : i;
       const bool ok = rel < u.rows && (u.wide || s == 0);
       int tok, head;
-      split(u.row0 + (ok ? rel : 0), tok, head);
+      split_row(p, u.row0 + (ok ? rel : 0), tok, head);
       off = (u.q0 + tok) * a.ld_q + static_cast<long long>(u.g * HG + head) * HD;
       return ok;
     };
@@ -584,10 +600,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int lim, lim0;  // the last key that this row sees, and the unit's first row
       {
         int tok, head;
-        split(items[slot].row0 + rel, tok, head);
+        split_row(p, items[slot].row0 + rel, tok, head);
         const int p0 = items[slot].L - items[slot].n;
         lim = row_ok ? p0 + tok : -1;
-        split(items[slot].row0, tok, head);
+        split_row(p, items[slot].row0, tok, head);
         lim0 = uniform(p0 + tok);
       }
       if (wide || s == 0) {
@@ -692,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float off = m == -INFINITY ? 0.f : m;
           const uint64_t sc2 = pack_f32x2(sc, sc), off2 = pack_f32x2(-off, -off);
-          uint64_t ls[2] = {0ull, 0ull};
+          uint64_t ls = 0ull;
 #pragma unroll
           for (int c = 0; c < kKeys; c += 2) {
             float p0, p1;
@@ -700,13 +716,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                          p0, p1);
             p0 = ex2(p0);
             p1 = ex2(p1);
-            ls[c / 2 & 1] = add_f32x2(ls[c / 2 & 1], pack_f32x2(p0, p1));
+            ls = add_f32x2(ls, pack_f32x2(p0, p1));
             // P enters the product as bf16 (relative 2^-8 at most, the size of the
             // result's own rounding); the sum l takes the unrounded weights
             x[c >> 1] = pack_bf16x2(p0, p1);
           }
           float l0, l1;
-          unpack_f32x2(add_f32x2(ls[0], ls[1]), l0, l1);
+          unpack_f32x2(ls, l0, l1);
           l += l0 + l1;
         }
         // the last P V of this stream has read P (and, with the overlay, the product warp
@@ -770,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sk = -INFINITY;
       if (whole && a.sink && row_ok) {
         int tok, head;
-        split(items[slot].row0 + rel, tok, head);
+        split_row(p, items[slot].row0 + rel, tok, head);
         sk = a.sink[items[slot].g * HG + head] * kLog2e;
       }
       // ---------------- results: through this stream's Q tile (whole units), or as fp32
@@ -863,17 +879,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++n_x;
       }
-      // This half of this warp's rows, out of the tile.  The unit is noted if a value is not
-      // finite though its row's l is a number.
       if (live && whole && (wide || s == 0)) {
-        int tok, head;
-        split(items[slot].row0 + (row_ok ? rel : 0), tok, head);
-        head += items[slot].g * HG;
-        const bool bad = flush_rows<HD>(static_cast<bf16*>(a.out), (items[slot].q0 + tok) * a.ld_out + static_cast<long long>(head) * HD, row_ok, l, q_sm + s * S::kQBytes, hf, own);
-        if (bad && lane == 0) {
-          atomicMin(&bad_sh[0], items[slot].index);
-          atomicMax(&bad_sh[1], items[slot].index);
-        }
+        __syncwarp();
+        write_rows<HD>(p, items[slot], bad_sh, rel, l, q_sm + s * S::kQBytes, hf, own);
         __syncwarp();
       }
       mbar_arrive(&it_empty[slot]);
@@ -1123,39 +1131,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 PE_DEV bool finite(float v) { return fabsf(v) <= FLT_MAX; }
 
-// By a whole warp: notes a row of the unit at hand to be computed again.
-PE_DEV bool mark(uint32_t* again, bool bad, int row) {
-  bad = __any_sync(0xffffffffu, bad);
-  if (bad && (threadIdx.x & 31) == 0) atomicOr(&again[row >> 5], 1u << (row & 31));
-  return bad;
-}
+// The i-th row of a unit for this warp of the join (its slice: blockIdx.y)
+PE_DEV int join_row(int i, int warp) { return (blockIdx.y + i * gridDim.y) * kRowWarps + warp; }
 
-// The rows noted of the unit at packed row row0, so far as a key of the unit is past them.
-// (This and the next one are calls, not inlined: their registers would be the join's.)
-__device__ __noinline__ void redo_unit(const TcArgs& p, int r, int g, int row0, uint32_t* again,
+// Of the unit at packed row row0, the rows noted (bit i of a warp's `again`: its i-th row),
+// so far as a key of the unit is past them.  (This and the next one are calls, not inlined:
+// their registers would be the join's.)
+__device__ __noinline__ void redo_unit(const TcArgs& p, int r, int g, int row0, uint32_t again,
                                        RowScratch& scratch) {
+  __shared__ uint32_t again_sh[kRowWarps];
   const ChunkArgs& a = p.c;
   const int HG = a.H / a.G;
+  if ((threadIdx.x & 31) == 0) again_sh[threadIdx.x >> 5] = again;
   __syncthreads();
   const Req q = load_req(a, r, false);
   const int kend = unit_kend(q, row0 / kUnitRows, HG);
-  for (int row = 0; row < kUnitRows; ++row) {
-    const int tok = (row0 + row) / HG, head = g * HG + (row0 + row) % HG, lim = q.L - q.n + tok;
-    if (!(again[row >> 5] >> (row & 31) & 1) || lim >= kend - 1) continue;
-    row_query<bf16>(a, q.q0 + tok, head, scratch);
-    __syncthreads();
-    attend_row<bf16>(a, r, q.q0 + tok, head, lim, scratch);
-    __syncthreads();
-  }
-  __syncthreads();
-  if (threadIdx.x < kUnitRows / 32) again[threadIdx.x] = 0;
+  for (int w = 0; w < kRowWarps; ++w)
+    for (uint32_t todo = again_sh[w]; todo; todo &= todo - 1) {
+      const int row = row0 + join_row(__ffs(todo) - 1, w);
+      const int tok = row / HG, head = g * HG + row % HG, lim = q.L - q.n + tok;
+      if (lim >= kend - 1) continue;
+      row_query<bf16>(a, q.q0 + tok, head, scratch);
+      __syncthreads();
+      attend_row<bf16>(a, r, q.q0 + tok, head, lim, scratch);
+      __syncthreads();
+    }
   __syncthreads();
 }
 
 // The whole units of this CTA's list up to the last that was noted, as the K warp of the
 // first kernel went through them.
 template <int HD>
-__device__ __noinline__ void redo_list(const TcArgs& p, uint32_t* again, RowScratch& scratch) {
+__device__ __noinline__ void redo_list(const TcArgs& p, RowScratch& scratch) {
   const ChunkArgs& a = p.c;
   const Rec& rec = p.rec[blockIdx.x];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, HG = a.H / a.G;
@@ -1165,13 +1172,15 @@ __device__ __noinline__ void redo_list(const TcArgs& p, uint32_t* again, RowScra
     const Req q = load_req(a, r, false);
     if (unit >= bad0) {
       const int n = min(kUnitRows, q.R - qt * kUnitRows);
-      for (int row = blockIdx.y * 4 + warp; row < n; row += gridDim.y * 4) {
+      uint32_t again = 0;
+      for (int at = 0, row; (row = join_row(at, warp)) < n; ++at) {
         const int tok = (qt * kUnitRows + row) / HG, head = g * HG + (qt * kUnitRows + row) % HG;
-        const bf16* o = static_cast<const bf16*>(a.out) + (q.q0 + tok) * a.ld_out + static_cast<long long>(head) * HD;
+        const bf16* o =
+            static_cast<const bf16*>(a.out) + (q.q0 + tok) * a.ld_out + static_cast<long long>(head) * HD;
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < HD / 32; ++i) bad |= !finite(__bfloat162float(o[lane + 32 * i]));
-        mark(again, bad, row);
+        again |= static_cast<uint32_t>(__any_sync(0xffffffffu, bad)) << at;
       }
       redo_unit(p, r, g, qt * kUnitRows, again, scratch);
     }
@@ -1194,10 +1203,7 @@ template <int HD>
 __global__ void __launch_bounds__(32 * kRowWarps) chunk_join_kernel(const __grid_constant__ TcArgs p) {
   constexpr int V = HD / 32;
   __shared__ RowScratch scratch;
-  __shared__ uint32_t again_sh[kUnitRows / 32];  // the unit's rows to compute again
   pdl_trigger();
-  if (threadIdx.x < kUnitRows / 32) again_sh[threadIdx.x] = 0;
-  __syncthreads();
   pdl_wait();
   const ChunkArgs& a = p.c;
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1205,9 +1211,9 @@ __global__ void __launch_bounds__(32 * kRowWarps) chunk_join_kernel(const __grid
   const int bad1 = rec.bad1;
   if (!rec.tail && bad1 < 0) return;
   const int HG = a.H / a.G;
-  bool some = false;
+  uint32_t again = 0;  // the rows of this warp to compute again
   const int q0 = rec.q0, g = rec.g, row0 = rec.row0, rows = rec.tail ? rec.rows : 0;
-  for (int row = blockIdx.y * 4 + warp; row < rows; row += gridDim.y * 4) {
+  for (int at = 0, row; (row = join_row(at, warp)) < rows; ++at) {
     const int tok = (row0 + row) / HG, head = g * HG + (row0 + row) % HG;
     float M = a.sink ? a.sink[head] * kLog2e : -INFINITY;  // the sink: one more part, O = 0
     float den = M == -INFINITY ? 0.f : 1.f;
@@ -1268,10 +1274,10 @@ __global__ void __launch_bounds__(32 * kRowWarps) chunk_join_kernel(const __grid
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) bad |= !finite(acc[i]);
-    some |= mark(again_sh, bad && den == den, row);
+    again |= static_cast<uint32_t>(__any_sync(0xffffffffu, bad && den == den)) << at;
   }
-  if (__syncthreads_or(some)) redo_unit(p, rec.r, g, row0, again_sh, scratch);
-  if (bad1 >= 0) redo_list<HD>(p, again_sh, scratch);
+  if (__syncthreads_or(again)) redo_unit(p, rec.r, g, row0, again, scratch);
+  if (bad1 >= 0) redo_list<HD>(p, scratch);
 }
 
 constexpr int kMaxGrid = 152;
@@ -1302,7 +1308,7 @@ int launch(const TcArgs& p, const CUtensorMap& km, const CUtensorMap& vm, cudaSt
   if (launch_chained(chunk_tc_kernel<HD>, dim3(p.grid), dim3(kThreads), Shape<HD>::kSmem, st, km, vm, p) !=
       cudaSuccess)
     return PE_ERR_CUDA;
-  // a warp takes eight of a unit's rows
+  // a warp takes at most eight of a unit's rows (the join notes them in 32 bits)
   const int join = std::max(1, std::min(8, static_cast<int>(
       std::min<long long>(static_cast<long long>(p.c.T) * (p.c.H / p.c.G), p.part_rows) + 31) / 32));
   return launch_chained(chunk_join_kernel<HD>, dim3(p.grid, join), dim3(128), 0, st, p) == cudaSuccess
