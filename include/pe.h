@@ -413,10 +413,11 @@ int pe_verify_greedy(int B, int T_in, const int32_t* qsl, const int32_t* tok,
  *   temperature[B] float, nullable (NULL: 1 for every request).  0: the request is
  *                  greedy (pe_verify_greedy's rules; its numbers are not read).
  *                  Negative or NaN: read as 0, PE_ST_SAMPLING.  Positive ones
- *                  below 1e-30 are read as 1e-30
+ *                  below 1e-30 are read as 1e-30, those above 1e30 as 1e30
  *   u[T_in]        float uniform numbers in [0, 1): u of row j >= 1 of a request
  *                  decides its draft j (row 0's entry is not read)
- *   gumbel[B][vocab] float standard Gumbel noise, -log(E) of exponential draws E
+ *   gumbel[B][vocab] float standard Gumbel noise, -log(E) of exponential draws E (E = 0
+ *                  gives +inf: such a token wins unless its logit is -inf)
  *   accepted[B]    out: a_r = the largest m <= n_r - 1 with u_j < p_{j-1}(tok_j) for
  *                  every j = 1..m (rows j of the request)
  *   bonus[B]       out: argmax over tokens v of logits_a[v] / temperature +
@@ -440,8 +441,8 @@ int pe_verify_greedy(int B, int T_in, const int32_t* qsl, const int32_t* tok,
  * most T_in sets PE_ST_ROWS_RANGE; the results are then undefined (nothing outside
  * the outputs is touched).  The call clears the status word first.  PE_ERR_ARG:
  * negative sizes, null pointers, logits, u or gumbel not aligned to their element
- * size, ws misaligned or too small, B = 0 with T_in > 0.  PE_ERR_UNSUPPORTED: B > 65535, or a dtype
- * other than the two. */
+ * size, ws misaligned or too small, B = 0 with T_in > 0.  PE_ERR_UNSUPPORTED: B > 65535,
+ * vocab > 2^30, or a dtype other than the two. */
 size_t pe_verify_sampled_workspace_bytes(int max_batch, int max_rows_in, int vocab);
 int pe_verify_sampled(int B, int T_in, const int32_t* qsl, const int32_t* tok, const void* logits,
                       int vocab, int dtype, const float* temperature, const float* u,
@@ -470,10 +471,10 @@ typedef struct pe_attn_plan {
   uint64_t rope_turn[64]; /* theta^(-2i/hd) / (2 pi) as a 64-bit fraction of a turn */
 } pe_attn_plan;
 
-/* PE_ERR_UNSUPPORTED: H not a multiple of G, H / G > 128, hd not a multiple of 8 or
- * above 128 (bf16: 64 or 128), block_size < 1, eps negative or NaN, rope_theta not
- * positive, another dtype.  PE_ERR_ARG: plan is NULL.  On an error *plan is zeroed
- * and every call refuses it. */
+/* PE_ERR_UNSUPPORTED: H not a multiple of G, H / G > 128, H > 65535, hd not a multiple
+ * of 8 or above 128 (bf16: 64 or 128), block_size < 1, eps negative or not finite,
+ * rope_theta not positive or not finite, another dtype.  PE_ERR_ARG: plan is NULL.  On
+ * an error *plan is zeroed and every call refuses it. */
 int pe_attn_plan_init(pe_attn_plan* plan, int n_heads, int n_kv_heads, int head_dim,
                       int block_size, int dtype, float eps, float rope_theta);
 

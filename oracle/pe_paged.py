@@ -98,6 +98,7 @@ def verify_sampled(qsl, tok, logits, temperature, u, gumbel):
     for r in range(B):
         lo, hi = int(qsl[r]), int(qsl[r + 1])
         n, temp = hi - lo, float(temperature[r])
+        temp = min(max(temp, 1e-30), 1e30) if temp > 0 else temp
         if n == 0:
             continue
         p[lo] = 1.0

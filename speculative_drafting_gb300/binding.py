@@ -193,19 +193,23 @@ def _addr(t):
 
 
 _raw_stream = None
+_current_device = None
 
 
 def _stream_handle(stream, t):
-    """The cudaStream_t of `stream`, or of the current stream on tensor t's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    global _raw_stream
+    """The cudaStream_t of `stream`, or the current one; a tensor t of another device than
+    the current one is refused (the launch would go to the current one)."""
+    global _raw_stream, _current_device
     if _raw_stream is None:
         import torch
 
-        # what torch.cuda.current_stream wraps in an object, 3 us a call
+        # what torch.cuda.current_stream and current_device wrap, 3 us a call
         _raw_stream = torch._C._cuda_getCurrentRawStream
-    return _raw_stream(t.get_device())
+        _current_device = torch._C._cuda_getDevice
+    dev = t.get_device()
+    if dev != _current_device():
+        raise ValueError(f"tensors on device {dev}, the current device is {_current_device()}")
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _check(rc, what):
@@ -456,9 +460,9 @@ class PagedAttention:
         self.c = PeAttnPlan()
         self.addr = ctypes.addressof(self.c)
         self.qkv_width = (n_heads + 2 * n_kv_heads) * head_dim
+        code = {"bf16": PE_DTYPE_BF16, "f32": PE_DTYPE_F32}.get(dtype, -1)
         _check(self.lib.pe_attn_plan_init(self.addr, n_heads, n_kv_heads, head_dim, block_size,
-                                          PE_DTYPE_BF16 if dtype == "bf16" else PE_DTYPE_F32,
-                                          eps, rope_theta), "pe_attn_plan_init")
+                                          code, eps, rope_theta), "pe_attn_plan_init")
 
     def append_workspace(self, device="cuda"):
         """The status word of ``append`` (zeroed)."""

@@ -224,7 +224,7 @@ bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % 
 }  // namespace
 
 bool plan_ok(const pe_attn_plan* p) {
-  if (!p || p->n_heads < 1 || p->n_kv_heads < 1 || p->n_heads % p->n_kv_heads ||
+  if (!p || p->n_heads < 1 || p->n_heads > 65535 || p->n_kv_heads < 1 || p->n_heads % p->n_kv_heads ||
       p->n_heads / p->n_kv_heads > 128 || p->head_dim < 8 || p->head_dim % 8 ||
       p->head_dim > 128 || p->block_size < 1 || !(p->eps >= 0.f))
     return false;

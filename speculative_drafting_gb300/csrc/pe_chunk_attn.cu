@@ -68,7 +68,7 @@ extern "C" int pe_chunk_attention(const pe_attn_plan* plan, int B, int T, const 
   if (!plan_ok(plan) || B < 0 || T < 0 || max_blocks < 1 || num_blocks < 0) return PE_ERR_ARG;
   const int64_t width = static_cast<int64_t>(plan->n_heads) * plan->head_dim;
   if (ld_q < width || ld_out < width || ld_q % 8 || ld_out % 8) return PE_ERR_ARG;
-  if (B > 65535 || static_cast<int64_t>(T) * plan->n_heads > 0x7fffffff ||
+  if (B > 65535 || static_cast<int64_t>(T) * plan->n_heads > 0x7fffff00 ||
       static_cast<int64_t>(max_blocks) * plan->block_size > 0x7fffff00)
     return PE_ERR_UNSUPPORTED;
   if (static_cast<double>(num_blocks) * plan->n_kv_heads * plan->block_size >= 2147483648.0)

@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto row_of = [&](int wn, int blk) {
       if (blk >= 0 && blk < a.num_blocks)
         return (blk * a.G + u.g) * a.bs + (wn * 32 + lane) * p.box % a.bs;
-      if (blk != -2 || (wn * 32 + lane) * p.box < u.kend) set_status(a.status, PE_ST_BLOCK_RANGE);
+      if (blk != -2 || (wn * 32ll + lane) * p.box < u.kend) set_status(a.status, PE_ST_BLOCK_RANGE);
       return -1;
     };
     int wn = u.tile0 * gpt >> 5;

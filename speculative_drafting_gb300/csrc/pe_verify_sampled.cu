@@ -56,7 +56,7 @@ struct VerifyArgs {
 
 PE_DEV float temperature_of(const VerifyArgs& a, int r) {
   const float t = a.temperature ? a.temperature[r] : 1.f;
-  return t > 0.f ? fmaxf(t, 1e-30f) : 0.f;  // 1 / T stays finite, l / T for any real logit
+  return t > 0.f ? fminf(fmaxf(t, 1e-30f), 1e30f) : 0.f;  // 1 / T stays finite and above 0
 }
 
 PE_DEV float ex2(float x) {
@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
   __shared__ int bad_sh, last_sh;
   __shared__ uint32_t st_sh;
   __shared__ int pick_sh[kW];
+  __shared__ float max_sh[kW];
   __shared__ float top_sh[kW];
   __shared__ unsigned long long key_sh[kW];
   __shared__ int idx_sh[kW];
@@ -330,6 +331,7 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
   }
   __syncthreads();
   int acc = 0, pick_acc = -1;
+  float max_acc = 0.f;
   bool found = false;
   // One warp per row, in order: the row's statistics (or key), then the draft after
   // it.  The first CTA goes through all rows (p_draft), the others stop behind the
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
       const bool draft = j + 1 < n;
       const int v = draft ? a.tok[row + 1] : -1;
       const bool in = v >= 0 && v < a.V;
-      float p = 0.f;
+      float p = 0.f, top = 0.f;
       int pick = -1;
       if (temp == 0.f) {
         pick = row_pick(j);
@@ -368,6 +370,7 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
         const float l = in ? Elem<T>::to_f(static_cast<const T*>(a.logits)[row * a.V + v]) : -INFINITY;
         const float u = draft ? a.u[row + 1] : 0.f;
         const Stat s = row_stat(j);
+        top = s.m;
         pick = fabsf(s.m) < INFINITY ? 0 : -1;  // whether the row has a distribution
         if (pick == 0) p = fminf(ex2((l - s.m) * c) / s.s, 1.f);
         rejected = !(u < p);
@@ -379,6 +382,7 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
         if (draft && sp == 0 && a.p_draft) a.p_draft[row + 1] = p;
         if (rejected) atomicMin(&bad_sh, j);
         pick_sh[warp] = pick;
+        max_sh[warp] = top;
       }
     }
     // the first rejection (or the last row) decides what the next token comes from
@@ -387,6 +391,7 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
       found = true;
       acc = min(bad_sh, n - 1);
       pick_acc = pick_sh[acc - j0];
+      max_acc = max_sh[acc - j0];
     }
     __syncthreads();
     if (found && sp > 0) break;
@@ -405,8 +410,10 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
     const int c0 = sp * a.rchunk, c1 = min(a.V, c0 + a.rchunk);
     const float it = (1.f / temp);
     float bs = -INFINITY, bl = 0.f, bg = 0.f;
+    // The score counts from the row's largest logit: the difference is exact near it, and
+    // no quotient passes fp32's range upwards.
     auto look = [&](float l, float g, int v) {
-      const float x = v == skip || l == -INFINITY ? -INFINITY : fmaf(l, it, g);
+      const float x = v == skip || l == -INFINITY ? -INFINITY : fmaf(l - max_acc, it, g);
       if (x > bs) {
         bs = x;
         bl = l;
@@ -463,8 +470,8 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
     top = top_sh[0];
 #pragma unroll
     for (int w = 1; w < kW; ++w) top = fmaxf(top, top_sh[w]);
-    if (bs > -INFINITY && bs >= top - 1e-5f * fmaxf(fabsf(top), fabsf(bl * it)))
-      best = score_order(static_cast<double>(bl) / static_cast<double>(temp) + bg);
+    if (bs > -INFINITY && (bs == top || bs >= top - 1e-5f * fmaxf(fabsf(top), fabsf((bl - max_acc) * it))))
+      best = score_order((static_cast<double>(bl) - static_cast<double>(max_acc)) / static_cast<double>(temp) + bg);
     else
       bi = 0x7fffffff;
     warp_best(best, bi);
@@ -519,7 +526,7 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
 size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Chunks of a row: about one wave of CTAs (six per SM) over the batch, at least one
-// 16-byte vector per thread, at most 32 KB.  Chunks of the race: four CTAs per SM, at
+// 16-byte vector per thread, at most 64 KB.  Chunks of the race: four CTAs per SM, at
 // least one round per thread.
 void plan(VerifyArgs& a, int esize, int num_sms) {
   const int vec = 16 / esize;
@@ -562,7 +569,7 @@ extern "C" int pe_verify_sampled(int B, int T_in, const int32_t* qsl, const int3
   if (B < 0 || T_in < 0 || vocab < 1) return PE_ERR_ARG;
   if (dtype != PE_DTYPE_F32 && dtype != PE_DTYPE_BF16) return PE_ERR_UNSUPPORTED;
   if (B == 0) return T_in == 0 ? PE_OK : PE_ERR_ARG;
-  if (B > 65535) return PE_ERR_UNSUPPORTED;
+  if (B > 65535 || vocab > 1 << 30) return PE_ERR_UNSUPPORTED;
   if (!qsl || !accepted || !bonus || !ws) return PE_ERR_ARG;
   if (T_in > 0 && (!tok || !logits || !u || !gumbel)) return PE_ERR_ARG;
   const int esize = dtype == PE_DTYPE_F32 ? 4 : 2;
@@ -607,13 +614,13 @@ extern "C" int pe_verify_sampled(int B, int T_in, const int32_t* qsl, const int3
   const bool f32 = dtype == PE_DTYPE_F32;
   if (T_in > 0) {
     if (launch_chained(f32 ? sampled_row_kernel<float> : sampled_row_kernel<bf16>,
-                   dim3(static_cast<unsigned>(T_in) * a.splits), dim3(kThreads), 0, st, a) != cudaSuccess)
+                       dim3(static_cast<unsigned>(T_in) * a.splits), dim3(kThreads), 0, st, a) != cudaSuccess)
       return PE_ERR_CUDA;
   } else if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) {
     return PE_ERR_CUDA;
   }
   return launch_chained(f32 ? sampled_request_kernel<float> : sampled_request_kernel<bf16>,
-                    dim3(static_cast<unsigned>(B) * a.rsplits), dim3(kThreads), 0, st, a) == cudaSuccess
+                        dim3(static_cast<unsigned>(B) * a.rsplits), dim3(kThreads), 0, st, a) == cudaSuccess
              ? PE_OK
              : PE_ERR_CUDA;
 }

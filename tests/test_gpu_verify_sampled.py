@@ -210,3 +210,41 @@ def test_replays_in_a_graph_and_shares_a_workspace():
             torch.cuda.synchronize()
             for t, x in zip(o, w):
                 np.testing.assert_array_equal(host(t), x)
+
+
+@pytest.mark.parametrize("temp", [1e30, 3e38, np.inf])
+def test_high_temperatures_draw_from_the_allowed_tokens_alike(temp):
+    c = _case((4, 1, 7), 1500, "f32", temps=temp, seed=15)
+    acc, bon = _check(c, least_clear=0.6)
+    # every score is the noise alone, of the tokens with a logit above -inf
+    row = c["qsl"][1]
+    assert bon[1] == np.argmax(np.where(np.isneginf(c["logits"][row]), -np.inf, c["gumbel"][1]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [40, 5003])
+def test_infinite_noise(dtype, V):
+    """-log(0) among the noise: that token wins, unless it has no probability or is the
+    rejected draft."""
+    c = _case((1, 1, 2), V, dtype, temps=1.0, seed=16, barred=0.0)
+    c["u"][:] = 0.999999  # the draft of request 2 is rejected
+    c["gumbel"][0, 11] = np.inf
+    lg = O.decode(c["logits"], dtype).astype(np.float32)
+    lg[1, 7] = -np.inf
+    c["logits"] = W.f32_to_bf16_bits(lg) if dtype == "bf16" else lg
+    c["gumbel"][1, 7] = c["gumbel"][1, 23] = np.inf
+    draft = int(c["tok"][3])
+    c["gumbel"][2, draft] = c["gumbel"][2, (draft + 5) % V] = np.inf
+    c["gumbel"][2, (draft + 9) % V] = -np.inf
+    acc, bon, _, st = _run(c)
+    assert st == 0 and acc.tolist() == [0, 0, 0] and bon.tolist() == [11, 23, (draft + 5) % V]
+
+
+def test_large_logits_at_low_temperatures():
+    """Quotients far past fp32's range: the largest logit wins, wherever it stands."""
+    c = _case((1, 1, 1), 3000, "f32", temps=1e-6, seed=17, barred=0.0)
+    c["logits"] *= np.float32(1e36)
+    acc, bon, _, st = _run(c)
+    assert st == 0 and bon.tolist() == c["logits"].argmax(1).tolist()
+    c["logits"] -= np.float32(2e37)  # all below zero
+    assert _run(c)[1].tolist() == c["logits"].argmax(1).tolist()

@@ -127,3 +127,38 @@ def test_verify_sampled_refusals(lib):
     assert ws(1, 8, 0) == 0 and ws(-1, 8, 10) == 0 and ws(1, -8, 10) == 0 and ws(0, 0, 1) >= 256
     sizes = [ws(b, t, v) for b, t, v in ((1, 8, 1000), (1, 64, 1000), (64, 64, 1000), (64, 64, 200000))]
     assert sizes == sorted(sizes)
+
+
+def test_sizes_past_the_indexes_are_refused(lib):
+    assert lib.pe_verify_sampled(*dict(VERIFY, V=(1 << 30) + 1).values()) == UNSUP
+    rc, plan = _plan(lib, H=64, G=8)
+    at = dict(ATTEND, plan=ctypes.addressof(plan))
+    assert lib.pe_chunk_attention(*dict(at, T=(1 << 25) - 2).values()) == UNSUP  # T * H past 2^31 - 256
+    assert lib.pe_chunk_attention(*dict(at, mb=1 << 27).values()) == UNSUP
+    assert _plan(lib, H=65536, G=1024)[0] == UNSUP and _plan(lib, H=65535, G=65535)[0] == OK
+
+
+def test_unknown_dtypes_are_refused(lib):
+    for name in ("fp16", "BF16", None, "bfloat16"):
+        with pytest.raises(binding.PeError):
+            binding.PagedAttention(8, 2, 64, 16, dtype=name)
+
+
+def test_workspaces_of_another_device_are_refused(lib, monkeypatch):
+    """The launch goes to the current device: tensors of another one are not for it."""
+    import torch
+
+    class Other:
+        def get_device(self):
+            return 1
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 64 + d, raising=False)
+    monkeypatch.setattr(binding, "_raw_stream", None)
+    monkeypatch.setattr(binding, "_current_device", None)
+    with pytest.raises(ValueError, match="device"):
+        binding._stream_handle(None, Other())
+    monkeypatch.setattr(Other, "get_device", lambda self: 0)
+    assert binding._stream_handle(None, Other()) == 64
+    # what the test's stand-ins left is not kept
+    binding._raw_stream = binding._current_device = None
