@@ -60,7 +60,10 @@ struct Shape {
   static constexpr int kGroupBytes = 1024 * kHalves;
   // slots of the K ring, and of the V ring: 128 KB in all
   static constexpr int kSlots = 4;
-  static constexpr int kSmem = 2 * kQBytes + 2 * kSlots * kTileBytes + 1024;
+  // Q of a unit, and where its results pass through; with a second one the next unit's Q
+  // and first S are on their way while this one's results are written
+  static constexpr int kQBufs = HD == 64 ? 2 : 1;
+  static constexpr int kSmem = 2 * kQBufs * kQBytes + 2 * kSlots * kTileBytes + 1024;
   // Tensor memory, 512 columns: S, P and O of two streams.  Head size 64: 128 + 64 + 64
   // columns each; S is free again once it is in registers.  Head size 128 leaves 128 for S
   // and P: two S buffers of a 64-key tile that the steps take in turn, with P in the
@@ -245,37 +248,158 @@ PE_DEV void split_row(const TcArgs& p, int row, int& tok, int& head) {
   head = row - tok * HG;
 }
 
-// A warp's 32 rows from `own` of a stream's tile, half hf of them, to where they belong;
-// rel is this lane's row within the unit, l its sum.  The unit is noted in bad if a value
-// is not finite though its row's l is a number.  (A call, not inlined: what it needs would
-// stay in registers through the steps.)
+// Places of a softmax thread: stream s, half hf of the keys and columns, rows 32 wq ..
+struct Seat {
+  int lane, s, hf, wq, i;
+};
+PE_DEV Seat seat_of(int tid) {
+  Seat t;
+  t.lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  t.s = warp >> 3;
+  t.hf = warp >> 2 & 1;
+  t.wq = warp & 3;
+  t.i = t.wq * 32 + t.lane;
+  return t;
+}
+// 16-byte chunk ch of a row of a Q tile, 128-byte swizzle
+PE_DEV uint4* tile_at(uint8_t* tile, int row, int ch) {
+  return reinterpret_cast<uint4*>(tile + (ch >> 3) * (kRows * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+}
 template <int HD>
-__device__ __noinline__ void write_rows(const TcArgs& p, const Unit& u, int* bad, int rel, float l,
-                                        const uint8_t* tile, int hf, int own) {
-  constexpr int kLpr = HD / 16, kRpi = 32 / kLpr;
-  const int lane = threadIdx.x & 31, HG = p.c.H / p.c.G;
+PE_DEV uint8_t* q_tile(uint8_t* q_sm, const Unit& u, int tile) {
+  return q_sm + ((Shape<HD>::kQBufs == 2 ? (u.index & 1) * 2 : 0) + tile) * Shape<HD>::kQBytes;
+}
+// Half rows move between global and shared memory kLpr lanes to a row: each instruction
+// covers kRpi rows of a warp's 32.
+template <int HD>
+struct Lines {
+  static constexpr int kLpr = HD / 16, kRpi = 32 / kLpr;
+};
+
+// What softmax warps do between units is in calls that are not inlined, with rolled loops:
+// it is cold code (unrolled, its instruction fetches cost 5000 clocks a unit at head size
+// 64, 12000 at 128), and inlined, what it needs stays in registers through the steps and
+// pushes others out of them (prompt of 8192: 695 us, 64 x 8 rows 125 us).
+
+// A unit's Q on its way to shared memory, or to L2.
+template <int HD>
+PE_DEV void load_q(const TcArgs& p, const Unit& u, uint8_t* q_sm, bool to_l2) {
+  constexpr int kLpr = Lines<HD>::kLpr, kRpi = Lines<HD>::kRpi;
+  const Seat t = seat_of(threadIdx.x);
+  if (!u.wide && t.s != 0) return;
+  const int HG = p.c.H / p.c.G, rel = u.wide ? t.s * kRows + t.i : t.i;
+  const bool ok = rel < u.rows;
+  int tok, head;
+  split_row(p, u.row0 + (ok ? rel : 0), tok, head);
+  const long long off = (u.q0 + tok) * p.c.ld_q + static_cast<long long>(u.g * HG + head) * HD;
+  if (to_l2) {
+    if (ok) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const bf16*>(p.c.q) + off + HD / 2 * t.hf));
+    return;
+  }
+  const unsigned oks = __ballot_sync(0xffffffffu, ok);
+  uint8_t* tile = q_tile<HD>(q_sm, u, u.wide ? t.s : 0);
+#pragma unroll 2
+  for (int it = 0; it < kLpr; ++it) {
+    const int src = it * kRpi + t.lane / kLpr, ch = t.hf * kLpr + t.lane % kLpr;
+    const long long o = __shfl_sync(0xffffffffu, off, src);
+    cp_async16(smem_u32(tile_at(tile, t.wq * 32 + src, ch)), static_cast<const bf16*>(p.c.q) + o + ch * 8,
+               oks >> src & 1);
+  }
+  cp_async_commit();
+}
+
+// A unit's results: through its Q tiles (whole units), or as fp32 partials straight to the
+// workspace.  m and l are this thread's row's; those of a narrow unit's two streams join
+// here, in stream 0's warps.  A whole unit is noted in bad if a value is not finite though
+// its row's l is a number.
+template <int HD>
+__device__ __noinline__ void finish_unit(const TcArgs& p, const Unit& u, int* bad, uint8_t* q_sm, uint32_t tmem,
+                                         const float (*ml)[kRows][2], float m, float l) {
+  constexpr int kLpr = Lines<HD>::kLpr, kRpi = Lines<HD>::kRpi;
+  const ChunkArgs& a = p.c;
+  const Seat t = seat_of(threadIdx.x);
+  const bool wide = u.wide, whole = u.whole;
+  const int rel = wide ? t.s * kRows + t.i : t.i;
+  // (a whole warp's answer, and known as such: what follows is .aligned)
+  if (__shfl_sync(0xffffffffu, (!wide && t.s != 0) || (rel & ~31) >= u.rows, 0)) return;
   const bool row_ok = rel < u.rows;
   int tok, head;
   split_row(p, u.row0 + (row_ok ? rel : 0), tok, head);
-  const long long off = (u.q0 + tok) * p.c.ld_out + static_cast<long long>(u.g * HG + head) * HD;
-  bf16* out = static_cast<bf16*>(p.c.out);
+  head += u.g * (a.H / a.G);
+  const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + (u.tile0 > 0 ? 0 : 1)) * p.part_rows + rel;
+  float w0 = 1.f, w1 = 0.f;
+  if (!wide) {
+    const float m0 = ml[0][t.i][0], m1 = ml[1][t.i][0];
+    m = fmaxf(m0, m1);
+    w0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
+    w1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+    l = ml[0][t.i][1] * w0 + ml[1][t.i][1] * w1;
+  }
+  if (!whole && row_ok && t.hf == 0) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
+  // factor of the unnormalised O of a whole unit: a sink joins m and l
+  float f = 1.f;
+  if (whole) {
+    const float sk = a.sink && row_ok ? a.sink[head] * kLog2e : -INFINITY;
+    const float top = fmaxf(m, sk);
+    const float e = ex2(m - top);
+    f = top == -INFINITY || l == 0.f ? 0.f : e / (l * e + (sk == -INFINITY ? 0.f : ex2(sk - top)));
+  }
+  const uint32_t tO = tmem + (static_cast<uint32_t>(t.wq * 32) << 16) + Shape<HD>::kO + (HD / 2) * t.hf;
+  uint8_t* tile = q_tile<HD>(q_sm, u, t.s);
+  const bool both = !wide && u.tile1 - u.tile0 > 1;
+#pragma unroll 1
+  for (int b = 0; b < HD / 32; ++b) {
+    uint32_t o[16];
+    tmem_ld16_issue(tO + (wide ? t.s * HD : 0) + 16 * b, o);
+    tmem_wait_ld();
+    tmem_use16(o);
+    if (both) {
+      uint32_t o1[16];
+      tmem_ld16_issue(tO + HD + 16 * b, o1);
+      tmem_wait_ld();
+      tmem_use16(o1);
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        o[c] = __float_as_uint(__uint_as_float(o[c]) * w0 + __uint_as_float(o1[c]) * w1);
+    }
+    const int col = HD / 2 * t.hf + 16 * b;
+    if (whole) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * f, __uint_as_float(o[8 * c + 2 * e + 1]) * f);
+        *tile_at(tile, t.i, col / 8 + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else if (row_ok) {
+      uint4* d = reinterpret_cast<uint4*>(p.part_o + prow * HD + col);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) d[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+    }
+  }
+  if (!whole) return;
+  __syncwarp();
+  const long long off = (u.q0 + tok) * a.ld_out + static_cast<long long>(head) * HD;
+  bf16* out = static_cast<bf16*>(a.out);
   const unsigned oks = __ballot_sync(0xffffffffu, row_ok), nums = __ballot_sync(0xffffffffu, l == l);
   __nv_bfloat162 zero = __float2bfloat162_rn(0.f);  // NaN once a value is not finite
 #pragma unroll 2
   for (int it = 0; it < kLpr; ++it) {
-    const int src = it * kRpi + lane / kLpr, ch = hf * kLpr + lane % kLpr, row = own + src;
+    const int src = it * kRpi + t.lane / kLpr, ch = t.hf * kLpr + t.lane % kLpr;
     const long long o = __shfl_sync(0xffffffffu, off, src);
     if (oks >> src & 1) {
-      const uint4 v = *reinterpret_cast<const uint4*>(tile + (ch >> 3) * (kRows * 128) + row * 128 +
-                                                      (((ch & 7) ^ (row & 7)) << 4));
+      const uint4 v = *tile_at(tile, t.wq * 32 + src, ch);
       *reinterpret_cast<uint4*>(out + o + ch * 8) = v;
       if (nums >> src & 1) zero = not_finite(v, zero);
     }
   }
-  if (__any_sync(0xffffffffu, __hisnan(zero.x) || __hisnan(zero.y)) && lane == 0) {
+  if (__any_sync(0xffffffffu, __hisnan(zero.x) || __hisnan(zero.y)) && t.lane == 0) {
     atomicMin(&bad[0], u.index);
     atomicMax(&bad[1], u.index);
   }
+  __syncwarp();
 }
 
 template <int HD>
@@ -308,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   uint8_t* q_sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* k_ring = q_sm + 2 * S::kQBytes;
+  uint8_t* k_ring = q_sm + 2 * S::kQBufs * S::kQBytes;
   uint8_t* v_ring = k_ring + S::kSlots * S::kTileBytes;
   const int HG = a.H / a.G;
 
@@ -541,16 +665,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sc = kLog2e / sqrtf(static_cast<float>(HD));
     uint32_t n_items = 0, n_st = 0, tiles = 0, n_x = 0, n_pair = 0;
     bool go = true;
-    // Half rows move between global and shared memory kLpr lanes to a row: each
-    // instruction covers kRpi rows of this warp's 32.  These loops, and those over
-    // the columns of O, stay rolled: a unit boundary runs cold code, and unrolled it
-    // cost 5000 (head size 64) to 12000 clocks (128) for its instruction fetches.
-    constexpr int kLpr = HD / 16, kRpi = 32 / kLpr;
-    const int own = wq * 32;
-    auto tile_at = [&](int tile, int row, int ch) {  // 16-byte chunk ch of a row, 128-byte swizzle
-      return reinterpret_cast<uint4*>(q_sm + tile * S::kQBytes + (ch >> 3) * (kRows * 128) +
-                                      row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-    };
     // A value of this row from the thread with its other half.
     auto partner = [&](float v, float& other) {
       const int buf = n_pair & 1;
@@ -561,28 +675,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++n_pair;
       return true;
     };
-    // This lane's Q row of a unit (element offset), or whether there is none.
-    auto q_row = [&](const Unit& u, long long& off) {
-      const int rel = u.wide ? s * kRows + i : i;
-      const bool ok = rel < u.rows && (u.wide || s == 0);
-      int tok, head;
-      split_row(p, u.row0 + (ok ? rel : 0), tok, head);
-      off = (u.q0 + tok) * a.ld_q + static_cast<long long>(u.g * HG + head) * HD;
-      return ok;
-    };
     // A unit's description stays in its slot until the unit is done: what the results
     // need of it is read again then, not held in registers through the steps.
     int cur = -1;  // slot of the unit at hand, -1: none is left
-    // the next unit: its Q rows start on their way to L2
+    // A unit's Q is there.  Both groups complete both Q barriers of the slot in every unit, before
+    // they let go of it: an MMA warp that skips units (none of their tiles is its stream's)
+    // finds the barriers in step.
+    auto q_there = [&](int slot) {
+      cp_async_wait<0>();
+      fence_proxy_async();
+      mbar_arrive(&q_full[slot][s]);
+    };
+    // the next unit
     auto next_unit = [&]() {
       const int slot = n_items % kItems;
       if (!wait_warp(&it_full[slot], (n_items / kItems) & 1)) return false;
       ++n_items;
       cur = uniform(items[slot].r < 0 ? -1 : slot);
-      long long off;
-      if (q_row(items[slot], off)) {
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const bf16*>(a.q) + off + HD / 2 * hf));
-      }
       return true;
     };
     if (!next_unit()) {
@@ -606,24 +715,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         split_row(p, items[slot].row0, tok, head);
         lim0 = uniform(p0 + tok);
       }
-      if (wide || s == 0) {
-        long long off;
-        const unsigned oks = __ballot_sync(0xffffffffu, q_row(items[slot], off));
-#pragma unroll 2
-        for (int it = 0; it < kLpr; ++it) {
-          const int src = it * kRpi + lane / kLpr, ch = hf * kLpr + lane % kLpr;
-          const long long o = __shfl_sync(0xffffffffu, off, src);
-          cp_async16(smem_u32(tile_at(wide ? s : 0, own + src, ch)),
-                     static_cast<const bf16*>(a.q) + o + ch * 8, oks >> src & 1);
-        }
-        cp_async_commit();
-        cp_async_wait<0>();
-        fence_proxy_async();
+      if (S::kQBufs == 1 || items[slot].index == 0) {
+        load_q<HD>(p, items[slot], q_sm, false);
+        q_there(slot);
       }
-      // Both groups complete both Q barriers of the slot in every unit, before they let
-      // go of it: an MMA warp that skips units (none of their tiles is its stream's)
-      // finds the barriers in step.
-      mbar_arrive(&q_full[slot][s]);
       const int mysteps = wide ? nt : (nt - s + 1) >> 1;
       float m = -INFINITY, l = 0.f;  // m: running maximum in units of log2
       for (int k = 0; k < mysteps; ++k) {
@@ -751,8 +846,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i < S::kTile && (t0 + i >= kend || !(have >> (i >> 3) & 1u))) {
             uint8_t* v = v_ring + (idx % S::kSlots) * S::kTileBytes + (i >> 3) * S::kGroupBytes + (i & 7) * 128;
 #pragma unroll
-            for (int c = 0; c < kLpr; ++c) {
-              const int ch = hf * kLpr + c;
+            for (int c = 0; c < HD / 16; ++c) {
+              const int ch = hf * (HD / 16) + c;
               *reinterpret_cast<uint4*>(v + (ch >> 3) * 1024 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
             }
           }
@@ -766,10 +861,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       // the next unit's Q, then the last P V of this one
-      if (!next_unit() || (mysteps > 0 && !wait_warp(&pv_done[s], (n_st + mysteps - 1) & 1))) {
+      bool on = next_unit();
+      if (on && cur >= 0) load_q<HD>(p, items[cur], q_sm, S::kQBufs == 1);
+      if (!on || (mysteps > 0 && !wait_warp(&pv_done[s], (n_st + mysteps - 1) & 1))) {
         fail();
         break;
       }
+      if (S::kQBufs == 2 && cur >= 0) q_there(cur);
       n_st += mysteps;
       tiles += nt;
       tc_fence_after();
@@ -781,58 +879,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         l += other;
       }
-      const bool whole = items[slot].whole;
-      const int prow = (static_cast<int>(blockIdx.x) * 2 + (tile0 > 0 ? 0 : 1)) * p.part_rows + rel;
-      float sk = -INFINITY;
-      if (whole && a.sink && row_ok) {
-        int tok, head;
-        split_row(p, items[slot].row0 + rel, tok, head);
-        sk = a.sink[items[slot].g * HG + head] * kLog2e;
-      }
-      // ---------------- results: through this stream's Q tile (whole units), or as fp32
-      // partials straight to the workspace
-      auto emit = [&](int col, uint32_t* o, float f) {  // 16 columns from col
-        if (whole) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * f,
-                                 __uint_as_float(o[8 * c + 2 * e + 1]) * f);
-            *tile_at(s, i, col / 8 + c) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else if (row_ok) {
-          uint4* d = reinterpret_cast<uint4*>(p.part_o + static_cast<size_t>(prow) * HD + col);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) d[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-        }
-      };
-      // factor of the unnormalised O of a row with (M, den): a sink joins both
-      auto factor = [&](float M, float den) {
-        if (!whole) return 1.f;
-        const float top = fmaxf(M, sk);
-        if (top == -INFINITY || den == 0.f) return 0.f;
-        const float e = ex2(M - top);
-        return e / (den * e + (sk == -INFINITY ? 0.f : ex2(sk - top)));
-      };
-      if (wide) {
-        const float f = factor(m, l);
-        if (live) {
-#pragma unroll 1
-          for (int b = 0; b < HD / 32; ++b) {
-            uint32_t o[16];
-            tmem_ld16_issue(tO + s * HD + 16 * b, o);
-            tmem_wait_ld();
-            tmem_use16(o);
-            emit(HD / 2 * hf + 16 * b, o, f);
-          }
-        }
-        if (!whole && row_ok && hf == 0)
-          *reinterpret_cast<float2*>(p.part_ml + static_cast<size_t>(prow) * 2) = make_float2(m, l);
-        tc_fence_before();
-      } else {
-        // the two streams' states of the same row join; stream 0's groups write the row
+      // the two streams' states of a narrow unit's rows join in stream 0's warps
+      if (!wide) {
         if (hf == 0) {
           ml_sh[s][i][0] = m;
           ml_sh[s][i][1] = l;
@@ -844,45 +892,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        if (live && s == 0) {
-          const float m0 = ml_sh[0][i][0], m1 = ml_sh[1][i][0];
-          const float M = fmaxf(m0, m1);
-          const float w0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), w1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-          l = ml_sh[0][i][1] * w0 + ml_sh[1][i][1] * w1;
-          const float f = factor(M, l);
-#pragma unroll 1
-          for (int b = 0; b < HD / 32; ++b) {
-            uint32_t o[16];
-            tmem_ld16_issue(tO + 16 * b, o);
-            tmem_wait_ld();
-            tmem_use16(o);
-            if (nt > 1) {
-              uint32_t o1[16];
-              tmem_ld16_issue(tO + HD + 16 * b, o1);
-              tmem_wait_ld();
-              tmem_use16(o1);
-#pragma unroll
-              for (int c = 0; c < 16; ++c)
-                o[c] = __float_as_uint(__uint_as_float(o[c]) * w0 + __uint_as_float(o1[c]) * w1);
-            }
-            emit(HD / 2 * hf + 16 * b, o, f);
-          }
-          if (!whole && row_ok && hf == 0)
-            *reinterpret_cast<float2*>(p.part_ml + static_cast<size_t>(prow) * 2) = make_float2(M, l);
-        }
+      }
+      finish_unit<HD>(p, items[slot], bad_sh, q_sm, tmem, ml_sh, m, l);
+      tc_fence_before();
+      if (!wide) {
         // stream 1's O and ml_sh have been read
-        tc_fence_before();
         mbar_arrive(&x_bar[1]);
         if (!wait_warp(&x_bar[1], n_x & 1)) {
           fail();
           break;
         }
         ++n_x;
-      }
-      if (live && whole && (wide || s == 0)) {
-        __syncwarp();
-        write_rows<HD>(p, items[slot], bad_sh, rel, l, q_sm + s * S::kQBytes, hf, own);
-        __syncwarp();
       }
       mbar_arrive(&it_empty[slot]);
     }
@@ -1035,10 +1055,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u.r < 0) break;
       const int nt = u.tile1 - u.tile0;
       const int steps = u.wide ? nt : (nt - s + 1) >> 1;     // of this stream
-      const int qb = u.wide ? s : 0;
+      const int qb = u.wide ? s : 0, q_at = S::kQBufs == 2 ? (u.index & 1) * 2 + qb : qb;
       // (with no step here the other stream may run units ahead: nothing to wait for)
       if (steps > 0) go = wait_warp(&q_full[slot][qb], ((n_items - 1) / kItems) & 1);
-      const uint64_t ad = sw128_kmajor_desc(smem_u32(q_sm + qb * S::kQBytes));
+      const uint64_t ad = sw128_kmajor_desc(smem_u32(q_sm + q_at * S::kQBytes));
       // Both warps see every load of both rings in order, the other stream's too: a
       // slot's barrier then never is a phase behind or ahead of the one that is waited
       // for.  A slot is free when both have let go of it, its users once their products
