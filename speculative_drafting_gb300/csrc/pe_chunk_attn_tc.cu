@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t v_full[S::kSlots], v_empty[S::kSlots];
   __shared__ __align__(8) uint64_t it_full[kItems], it_empty[kItems];
   __shared__ __align__(8) uint64_t q_full[kItems][2], s_full[2][2], s_free[2], p_full[2], pv_done[2];
-  __shared__ __align__(8) uint64_t x_bar[2], pair_bar[2][4];
+  __shared__ __align__(8) uint64_t x_bar[2];
   __shared__ __align__(8) uint64_t end_bar;
   __shared__ Unit items[kItems];
   __shared__ uint32_t mask_sh[kMasks];  // per tile: bit j = keys 8j..8j+7 were loaded
@@ -445,18 +445,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&it_full[i], 1);
-      mbar_init(&it_empty[i], 4 * kRows + 3);
-      mbar_init(&q_full[i][0], 2 * kRows);
-      mbar_init(&q_full[i][1], 2 * kRows);
+      mbar_init(&it_empty[i], 16 + 3);
+      mbar_init(&q_full[i][0], 8);
+      mbar_init(&q_full[i][1], 8);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s][0], 1);
       mbar_init(&s_full[s][1], 1);
-      mbar_init(&s_free[s], 2 * kRows);
-      mbar_init(&p_full[s], 2 * kRows);
+      mbar_init(&s_free[s], 8);
+      mbar_init(&p_full[s], 8);
       mbar_init(&pv_done[s], 1);
-      mbar_init(&x_bar[s], 4 * kRows);
-      for (int w = 0; w < 4; ++w) mbar_init(&pair_bar[s][w], 64);
+      mbar_init(&x_bar[s], 16);
     }
     mbar_init(&end_bar, 2);
     abort_sh = 0;
@@ -664,16 +663,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tm + S::kO + (HD / 2) * hf;  // of stream 0; stream 1's HD columns on
     const float sc = kLog2e / sqrtf(static_cast<float>(HD));
     uint32_t n_items = 0, n_st = 0, tiles = 0, n_x = 0, n_pair = 0;
-    bool go = true;
-    // A value of this row from the thread with its other half.
-    auto partner = [&](float v, float& other) {
-      const int buf = n_pair & 1;
+    bool failed = false;
+    // One arrival for the warp, of all that its lanes did before.
+    auto warp_arrive = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    // The two warps of a row meet at named barriers: a vote, and a value of this row from
+    // the thread with its other half.  These have no time limit, so each warp comes to every
+    // one that the other comes to: a warp whose wait gave up (`failed`) goes on without
+    // waits to the end of the unit, where the two leave together.
+    const int pair = 1 + s * 4 + wq;
+    auto vote = [&](bool v) {
+      uint32_t r;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\t"
+          "setp.ne.u32 p, %1, 0;\n\t"
+          "barrier.cta.red.or.pred.aligned q, %2, 64, p;\n\t"
+          "selp.u32 %0, 1, 0, q;\n\t}\n"
+          : "=r"(r)
+          : "r"(static_cast<uint32_t>(v)), "r"(pair)
+          : "memory");
+      return __any_sync(0xffffffffu, r) != 0;  // (known to be the whole warp's)
+    };
+    auto partner = [&](float v) {
+      const int buf = n_pair++ & 1;
       pair_sh[s][hf][buf][i] = v;
-      mbar_arrive(&pair_bar[s][wq]);
-      if (!wait_warp(&pair_bar[s][wq], n_pair & 1)) return false;
-      other = pair_sh[s][hf ^ 1][buf][i];
-      ++n_pair;
-      return true;
+      asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(pair) : "memory");
+      return pair_sh[s][hf ^ 1][buf][i];
     };
     // A unit's description stays in its slot until the unit is done: what the results
     // need of it is read again then, not held in registers through the steps.
@@ -684,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto q_there = [&](int slot) {
       cp_async_wait<0>();
       fence_proxy_async();
-      mbar_arrive(&q_full[slot][s]);
+      warp_arrive(&q_full[slot][s]);
     };
     // the next unit
     auto next_unit = [&]() {
@@ -694,8 +711,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       cur = uniform(items[slot].r < 0 ? -1 : slot);
       return true;
     };
-    if (!next_unit()) {
-      fail();
+    failed = !next_unit();
+    if (vote(failed)) {
+      if (failed) fail();
       cur = -1;
     }
     while (cur >= 0) {
@@ -727,10 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (two S products of the overlay may be done before the first is looked at: a
         // barrier for either buffer)
         const uint32_t n = n_st + k;
-        if (!wait_warp(&s_full[s][S::kOverlay ? n & 1 : 0], (S::kOverlay ? n >> 1 : n) & 1)) {
-          go = false;
-          break;
-        }
+        failed = failed || !wait_warp(&s_full[s][S::kOverlay ? n & 1 : 0], (S::kOverlay ? n >> 1 : n) & 1);
         tc_fence_after();
         const uint32_t have = uniform(mask_sh[(tiles + j) % kMasks]);
         const bool inner = t0 + S::kTile - 1 <= lim0 && have == kAll;
@@ -766,27 +781,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!S::kOverlay) {
           tc_fence_before();
-          mbar_arrive(&s_free[s]);
+          warp_arrive(&s_free[s]);
         }
         if (live) {
-          float other;
-          if (!partner(best, other)) {
-            go = false;
-            break;
-          }
-          const float top = fmaxf(best, other) * sc;
           // raise the maximum: at the first finite score, or when it climbed far
-          const bool raise = top > m + kLazy || (m == -INFINITY && top > m);
-          if (__any_sync(0xffffffffu, raise)) {
+          best *= sc;
+          if (vote(best > m + kLazy || (m == -INFINITY && best > m))) {
+            const float top = fmaxf(best, partner(best));
+            const bool raise = top > m + kLazy || (m == -INFINITY && top > m);
             const float mn = raise ? top : m;
             const float f = (m == -INFINITY) ? 1.f : ex2(m - mn);
             m = mn;
             l *= f;
             if (k > 0) {
-              if (!wait_warp(&pv_done[s], (n_st + k - 1) & 1)) {
-                go = false;
-                break;
-              }
+              failed = failed || !wait_warp(&pv_done[s], (n_st + k - 1) & 1);
               tc_fence_after();
 #pragma unroll 1
               for (int b = 0; b < HD / 32; ++b) {
@@ -822,10 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the last P V of this stream has read P (and, with the overlay, the product warp
         // has taken the p_full before this one)
-        if (k > 0 && !wait_warp(&pv_done[s], (n_st + k - 1) & 1)) {
-          go = false;
-          break;
-        }
+        if (k > 0) failed = failed || !wait_warp(&pv_done[s], (n_st + k - 1) & 1);
         if (live) {
           tc_fence_after();
           if constexpr (kKeys == 64)
@@ -839,11 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool cut = t0 + S::kTile > kend || have != kAll;
         if (cut) {
           const uint32_t idx = tiles + j;
-          if (!wait_warp(&v_full[idx % S::kSlots], (idx / S::kSlots) & 1)) {
-            go = false;
-            break;
-          }
-          if (i < S::kTile && (t0 + i >= kend || !(have >> (i >> 3) & 1u))) {
+          failed = failed || !wait_warp(&v_full[idx % S::kSlots], (idx / S::kSlots) & 1);
+          if (!failed && i < S::kTile && (t0 + i >= kend || !(have >> (i >> 3) & 1u))) {
             uint8_t* v = v_ring + (idx % S::kSlots) * S::kTileBytes + (i >> 3) * S::kGroupBytes + (i & 7) * 128;
 #pragma unroll
             for (int c = 0; c < HD / 16; ++c) {
@@ -854,31 +856,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async();
         }
         tc_fence_before();
-        mbar_arrive(&p_full[s]);
-      }
-      if (!go) {
-        fail();
-        break;
+        warp_arrive(&p_full[s]);
       }
       // the next unit's Q, then the last P V of this one
-      bool on = next_unit();
-      if (on && cur >= 0) load_q<HD>(p, items[cur], q_sm, S::kQBufs == 1);
-      if (!on || (mysteps > 0 && !wait_warp(&pv_done[s], (n_st + mysteps - 1) & 1))) {
-        fail();
-        break;
-      }
-      if (S::kQBufs == 2 && cur >= 0) q_there(cur);
+      failed = failed || !next_unit();
+      if (!failed && cur >= 0) load_q<HD>(p, items[cur], q_sm, S::kQBufs == 1);
+      if (mysteps > 0) failed = failed || !wait_warp(&pv_done[s], (n_st + mysteps - 1) & 1);
+      if (S::kQBufs == 2 && !failed && cur >= 0) q_there(cur);
       n_st += mysteps;
       tiles += nt;
       tc_fence_after();
-      if (live) {
-        float other;
-        if (!partner(l, other)) {
-          fail();
-          break;
-        }
-        l += other;
-      }
+      if (live) l += partner(l);
       // the two streams' states of a narrow unit's rows join in stream 0's warps
       if (!wide) {
         if (hf == 0) {
@@ -886,25 +874,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           ml_sh[s][i][1] = l;
         }
         tc_fence_before();
-        mbar_arrive(&x_bar[0]);
-        if (!wait_warp(&x_bar[0], n_x & 1)) {
-          fail();
-          break;
-        }
+        warp_arrive(&x_bar[0]);
+        failed = failed || !wait_warp(&x_bar[0], n_x & 1);
         tc_fence_after();
       }
-      finish_unit<HD>(p, items[slot], bad_sh, q_sm, tmem, ml_sh, m, l);
+      if (!failed) finish_unit<HD>(p, items[slot], bad_sh, q_sm, tmem, ml_sh, m, l);
       tc_fence_before();
       if (!wide) {
         // stream 1's O and ml_sh have been read
-        mbar_arrive(&x_bar[1]);
-        if (!wait_warp(&x_bar[1], n_x & 1)) {
-          fail();
-          break;
-        }
+        warp_arrive(&x_bar[1]);
+        failed = failed || !wait_warp(&x_bar[1], n_x & 1);
         ++n_x;
       }
-      mbar_arrive(&it_empty[slot]);
+      if (vote(failed)) {
+        if (failed) fail();
+        break;
+      }
+      warp_arrive(&it_empty[slot]);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
