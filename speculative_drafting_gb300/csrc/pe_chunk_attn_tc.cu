@@ -507,13 +507,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // Where the pieces begin is a matter of balance: fp32 serves (64-bit divisions cost a
   // small call a microsecond), so long as neighbours find the same place.  Every KV head
-  // has the same line, so a whole number of pieces each, unless that idles more than one
-  // CTA in 16.
+  // has the same line, so a whole number of pieces each: the nearest one where there are
+  // CTAs to spare (one token over 2048 keys of 8 KV heads: 19 us, 22 us with pieces across
+  // heads), else the next below unless that idles more than one CTA in 16.
   const long long W = Wg * a.G;
   const float least = static_cast<float>(p.umin * 128 * HG);
   int pieces = static_cast<int>(fminf(fmaxf(static_cast<float>(W) / least, 1.f), static_cast<float>(p.grid)));
-  const int per_head = pieces / a.G;
-  const bool even = per_head > 0 && (pieces - per_head * a.G) * 16 <= pieces;
+  const bool spare = pieces < p.grid;
+  const int per_head = spare ? min((pieces + a.G / 2) / a.G, p.grid / a.G) : pieces / a.G;
+  const bool even = per_head > 0 && (spare || (pieces - per_head * a.G) * 16 <= pieces);
   if (even) pieces = per_head * a.G;
   // the first cost of piece c on its head's line: never past the line, no less for a
   // larger c
@@ -1347,12 +1349,13 @@ int launch_chunk_tc(const ChunkArgs& a, char* ws, cudaStream_t st) {
   p.hg_shift = -1;
   for (int i = 0; i < 8; ++i)
     if (HG == 1 << i) p.hg_shift = i;
-  // A piece of fewer than four tiles takes a CTA no less time (one token over 2048 keys:
-  // 17 us with 4, 18 with 2 or 8).  A unit costs a CTA as long as nine tiles beside its own
-  // (Q, the first tile's way through the pipeline, its results): with 4 a prompt of 8192
-  // takes 768 us, with 9 620, with 16 640.
-  p.umin = 4;
-  p.overhead = 9;
+  // The least piece: one token over 2048 keys of 8 KV heads takes 20.0 us with 3 tiles,
+  // 19.6 with 4, 18.7 with 5, 19.1 with 6.  A unit costs a CTA the time of ten tiles
+  // beside its own (Q, the first tile's way through the pipeline, its results): a prompt
+  // of 8192 takes 642 us with 6, 604 with 8, 571 with 10, 568 with 12; 64 x 8 rows 108 to
+  // 109 us up to 10, 111 above.
+  p.umin = 5;
+  p.overhead = 10;
   p.part_rows = part_rows_of(a.T, HG);
   p.rec = reinterpret_cast<Rec*>(ws + 256);
   p.part_ml = reinterpret_cast<float*>(ws + 256 + rec_bytes());
