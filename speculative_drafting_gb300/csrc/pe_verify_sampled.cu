@@ -83,6 +83,11 @@ PE_DEV uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+PE_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 PE_DEV float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -409,16 +414,20 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
     const float* gp = a.gumbel + static_cast<int64_t>(r) * a.V;
     const int c0 = sp * a.rchunk, c1 = min(a.V, c0 + a.rchunk);
     const float it = (1.f / temp);
-    float bs = -INFINITY, bl = 0.f, bg = 0.f;
+    float bs = -INFINITY;
     // The score counts from the row's largest logit: the difference is exact near it, and
-    // no quotient passes fp32's range upwards.
-    auto look = [&](float l, float g, int v) {
-      const float x = v == skip || l == -INFINITY ? -INFINITY : fmaf(l - max_acc, it, g);
-      if (x > bs) {
-        bs = x;
-        bl = l;
-        bg = g;
-        bi = v;
+    // no quotient passes fp32's range upwards.  A logit of -inf gives -inf, or NaN with
+    // infinite noise: neither is greater than anything.
+    const uint64_t it2 = pack_f32x2(it, it), off2 = pack_f32x2(-max_acc, -max_acc);
+    auto scores = [&](const float* l, const float* g, int v, float* x) {  // of kRace tokens from v
+#pragma unroll
+      for (int e = 0; e < kRace; e += 2)
+        unpack_f32x2(fma_f32x2(add_f32x2(pack_f32x2(l[e], l[e + 1]), off2), it2, pack_f32x2(g[e], g[e + 1])),
+                     x[e], x[e + 1]);
+      if (static_cast<unsigned>(skip - v) < kRace) {
+#pragma unroll
+        for (int e = 0; e < kRace; ++e)
+          if (v + e == skip) x[e] = -INFINITY;
       }
     };
     constexpr int kVecs = sizeof(T) == 2 ? 1 : 2;  // 16-byte vectors of kRace logits
@@ -445,8 +454,15 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
             for (int y = 0; y < kVecs; ++y) unpack16<T>(lv[x][y], l + y * (kRace / kVecs));
             unpack16<float>(gv[x][0], g);
             unpack16<float>(gv[x][1], g + 4);
+            float sc[kRace];
+            scores(l, g, v + x * kStep, sc);
+            float m = sc[0];
 #pragma unroll
-            for (int e = 0; e < kRace; ++e) look(l[e], g[e], v + x * kStep + e);
+            for (int e = 1; e < kRace; ++e) m = fmaxf(m, sc[e]);
+            if (m > bs) {
+              bs = m;
+              bi = v + x * kStep;  // the first vector with the best score
+            }
           }
       }
     } else {
@@ -459,21 +475,52 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
           g[e] = w < c1 ? gp[w] : 0.f;
         }
 #pragma unroll
-        for (int e = 0; e < kRace; ++e) look(l[e], g[e], v + e * kThreads);
+        for (int e = 0; e < kRace; ++e) {
+          const int w = v + e * kThreads;
+          const float x = w == skip ? -INFINITY : fmaf(l[e] - max_acc, it, g[e]);
+          if (x > bs) {
+            bs = x;
+            bi = w;
+          }
+        }
       }
     }
-    // The threads whose best is within reach of the CTA's compare in 64 bits (doubles are
-    // slow here: by then it is one or two of the 256).
+    // The threads whose best is within reach of the CTA's (a score's rounding is 2^-23 of
+    // its two terms; noise past 128 is infinite) compare in 64 bits: doubles are slow here,
+    // and by then it is one or two of the 256.
     float top = warp_max(bs);
     if (lane == 0) top_sh[warp] = top;
     __syncthreads();
     top = top_sh[0];
 #pragma unroll
     for (int w = 1; w < kW; ++w) top = fmaxf(top, top_sh[w]);
-    if (bs > -INFINITY && (bs == top || bs >= top - 1e-5f * fmaxf(fabsf(top), fabsf((bl - max_acc) * it))))
+    if (bs > -INFINITY && (bs == top || bs >= top - 1e-6f * (fabsf(top) + fabsf(bs) + 128.f))) {
+      float l[kRace], g[kRace], sc[kRace];
+      float bl = 0.f, bg = 0.f;
+      if (a.vec) {  // the first token of the vector with that score
+#pragma unroll
+        for (int e = 0; e < kRace; ++e) {
+          l[e] = Elem<T>::to_f(lp[bi + e]);
+          g[e] = gp[bi + e];
+        }
+        scores(l, g, bi, sc);
+        int first = 0;
+#pragma unroll
+        for (int e = kRace - 1; e >= 0; --e)
+          if (sc[e] == bs) {
+            first = e;
+            bl = l[e];
+            bg = g[e];
+          }
+        bi += first;
+      } else {
+        bl = Elem<T>::to_f(lp[bi]);
+        bg = gp[bi];
+      }
       best = score_order((static_cast<double>(bl) - static_cast<double>(max_acc)) / static_cast<double>(temp) + bg);
-    else
+    } else {
       bi = 0x7fffffff;
+    }
     warp_best(best, bi);
     if (lane == 0) {
       key_sh[warp] = best;
