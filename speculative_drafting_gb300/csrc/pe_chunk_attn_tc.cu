@@ -240,7 +240,6 @@ PE_DEV __nv_bfloat162 not_finite(const uint4& v, __nv_bfloat162 zero) {
   return __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.w), none, zero);
 }
 
-
 // packed row -> token, head in the group
 PE_DEV void split_row(const TcArgs& p, int row, int& tok, int& head) {
   const int HG = p.c.H / p.c.G;
@@ -697,9 +696,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A unit's description stays in its slot until the unit is done: what the results
     // need of it is read again then, not held in registers through the steps.
     int cur = -1;  // slot of the unit at hand, -1: none is left
-    // A unit's Q is there.  Both groups complete both Q barriers of the slot in every unit, before
-    // they let go of it: an MMA warp that skips units (none of their tiles is its stream's)
-    // finds the barriers in step.
+    // A unit's Q is there.  Both groups complete both Q barriers of the slot in every unit,
+    // before they let go of it: an MMA warp that skips units (none of their tiles is its
+    // stream's) finds the barriers in step.
     auto q_there = [&](int slot) {
       cp_async_wait<0>();
       fence_proxy_async();
@@ -890,6 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (vote(failed)) {
         if (failed) fail();
+        cp_async_wait<0>();  // no copy of Q is in flight when the CTA leaves
         break;
       }
       warp_arrive(&it_empty[slot]);
