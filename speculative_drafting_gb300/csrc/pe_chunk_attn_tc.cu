@@ -1223,7 +1223,19 @@ __global__ void __launch_bounds__(32 * kRowWarps) chunk_join_kernel(const __grid
   // (the same for every row)
   const int code0 = c + lane >= p.grid ? 0 : lane == 0 ? 1 : p.rec[c + lane].head;
   const int q0 = rec.q0, g = rec.g, row0 = rec.row0, rows = rec.tail ? rec.rows : 0;
+  // (m, l) of a row in the part of CTA k, its `head` being code
+  auto load_ml = [&](int k, int code, bool part, int row) {
+    const size_t prow = (static_cast<size_t>(k) * 2 + (k == c)) * p.part_rows + row;
+    return part && code != 0 && row < rows ? *reinterpret_cast<const float2*>(p.part_ml + prow * 2)
+                                           : make_float2(-INFINITY, 0.f);
+  };
+  // the next row's, of the first 32 CTAs, is on its way while a row is joined
+  const unsigned ends0 = __ballot_sync(0xffffffffu, code0 == 2 || c + lane >= p.grid);
+  const bool in0 = lane <= (ends0 ? __ffs(ends0) - 1 : 31);
+  float2 ahead = load_ml(c + lane, code0, in0, join_row(0, warp));
   for (int at = 0, row; (row = join_row(at, warp)) < rows; ++at) {
+    const float2 ml0 = ahead;
+    ahead = load_ml(c + lane, code0, in0, join_row(at + 1, warp));
     const int tok = (row0 + row) / HG, head = g * HG + (row0 + row) % HG;
     float M = a.sink ? a.sink[head] * kLog2e : -INFINITY;  // the sink: one more part, O = 0
     float den = M == -INFINITY ? 0.f : 1.f;
@@ -1240,9 +1252,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) chunk_join_kernel(const __grid
       const int last = ends ? __ffs(ends) - 1 : 31;  // of this window
       more = !ends;
       const bool part = code != 0 && lane <= last;
-      const size_t prow = (static_cast<size_t>(k) * 2 + (k == c)) * p.part_rows + row;
-      const float2 ml = part ? *reinterpret_cast<const float2*>(p.part_ml + static_cast<size_t>(prow) * 2)
-                             : make_float2(-INFINITY, 0.f);
+      const float2 ml = k0 == c ? ml0 : load_ml(k, code, part, row);
       // (l = 0: no key of the part was seen; NaN counts as seen)
       const bool seen = ml.y != 0.f;
       any |= __any_sync(0xffffffffu, seen);
