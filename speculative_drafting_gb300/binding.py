@@ -212,6 +212,15 @@ def _stream_handle(stream, t):
     return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
+def _row_stride(t, hd):
+    """Elements from one row of [T][heads][hd] (or [T][heads hd]) to the next; the rows
+    themselves have to be dense."""
+    s = t.stride()
+    if s[-1] != 1 or (len(s) == 3 and s[1] != hd and t.shape[1] != 1):
+        raise ValueError(f"rows of shape {tuple(t.shape[1:])} with strides {s}: a row has to be dense")
+    return s[0]
+
+
 def _check(rc, what):
     if rc != PE_OK:
         raise PeError(rc, what)
@@ -437,8 +446,11 @@ def verify_sampled_workspace(max_batch: int, max_rows_in: int, vocab: int, devic
 
 def verify_sampled(B, T_in, qsl, tok, logits, vocab, dtype, temperature, u, gumbel, accepted, bonus,
                    p_draft, ws, stream=None):
-    """pe_verify_sampled on device tensors; dtype is PE_DTYPE_F32 or PE_DTYPE_BF16;
-    temperature and p_draft may be None."""
+    """pe_verify_sampled on device tensors, dense ones; dtype is PE_DTYPE_F32 or
+    PE_DTYPE_BF16; temperature and p_draft may be None."""
+    for t in (logits, gumbel):
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"logits and gumbel have to be dense, not with strides {t.stride()}")
     rc = load().pe_verify_sampled(B, T_in, _addr(qsl), _addr(tok), _addr(logits), vocab, dtype,
                                   _addr(temperature), _addr(u), _addr(gumbel), _addr(accepted),
                                   _addr(bonus), _addr(p_draft), _addr(ws), ws.numel(),
@@ -456,13 +468,21 @@ class PagedAttention:
 
     def __init__(self, n_heads, n_kv_heads, head_dim, block_size, dtype="bf16", eps=1e-6,
                  rope_theta=10000.0):
+        import torch
+
         self.lib = load()
         self.c = PeAttnPlan()
         self.addr = ctypes.addressof(self.c)
+        self.hd = head_dim
+        self.dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
         self.qkv_width = (n_heads + 2 * n_kv_heads) * head_dim
         code = {"bf16": PE_DTYPE_BF16, "f32": PE_DTYPE_F32}.get(dtype, -1)
         _check(self.lib.pe_attn_plan_init(self.addr, n_heads, n_kv_heads, head_dim, block_size,
                                           code, eps, rope_theta), "pe_attn_plan_init")
+
+    def _refuse(self, *tensors):
+        got = ", ".join(f"{t.dtype} {tuple(t.shape)} strides {t.stride()}" for t in tensors if t is not None)
+        raise ValueError(f"the plan's type is {self.dtype}; caches, q_out and block_table are dense: got {got}")
 
     def append_workspace(self, device="cuda"):
         """The status word of ``append`` (zeroed)."""
@@ -484,9 +504,16 @@ class PagedAttention:
                stream=None):
         """pe_qkv_append: qkv [T][H + 2G][hd] (or [T][(H + 2G) hd]; its rows may be
         strided), gains and q_out may be None."""
-        rc = self.lib.pe_qkv_append(self.addr, T, _addr(qkv), qkv.stride(0), _addr(gamma_q),
-                                    _addr(gamma_k), _addr(pos), _addr(slot), num_blocks,
-                                    _addr(q_out), _addr(k_cache), _addr(v_cache), _addr(ws),
+        # (a call of a few rows is bound by its host time: data_ptr without _addr and checks
+        # in line save 0.3 us of 5.4)
+        d = self.dtype
+        if not (qkv.dtype is d and k_cache.dtype is d and v_cache.dtype is d
+                and k_cache.is_contiguous() and v_cache.is_contiguous()
+                and (q_out is None or (q_out.dtype is d and q_out.is_contiguous()))):
+            self._refuse(qkv, k_cache, v_cache, q_out)
+        rc = self.lib.pe_qkv_append(self.addr, T, qkv.data_ptr(), _row_stride(qkv, self.hd), _addr(gamma_q),
+                                    _addr(gamma_k), pos.data_ptr(), slot.data_ptr(), num_blocks,
+                                    _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(),
                                     ws.numel(), _stream_handle(stream, ws))
         _check(rc, "pe_qkv_append")
 
@@ -494,10 +521,14 @@ class PagedAttention:
                sink=None, stream=None):
         """pe_chunk_attention: q and out [T][H][hd] (or [T][H hd]; their rows may be
         strided)."""
-        rc = self.lib.pe_chunk_attention(self.addr, B, T, _addr(qsl), _addr(seq_len), _addr(q),
-                                         q.stride(0), _addr(k_cache), _addr(v_cache),
-                                         _addr(block_table), block_table.shape[1], num_blocks,
-                                         _addr(sink), _addr(out), out.stride(0), _addr(ws),
+        d = self.dtype
+        if not (q.dtype is d and k_cache.dtype is d and v_cache.dtype is d and out.dtype is d
+                and k_cache.is_contiguous() and v_cache.is_contiguous() and block_table.is_contiguous()):
+            self._refuse(q, k_cache, v_cache, out, block_table)
+        rc = self.lib.pe_chunk_attention(self.addr, B, T, qsl.data_ptr(), seq_len.data_ptr(), q.data_ptr(),
+                                         _row_stride(q, self.hd), k_cache.data_ptr(), v_cache.data_ptr(),
+                                         block_table.data_ptr(), block_table.shape[1], num_blocks,
+                                         _addr(sink), out.data_ptr(), _row_stride(out, self.hd), ws.data_ptr(),
                                          ws.numel(), _stream_handle(stream, ws))
         _check(rc, "pe_chunk_attention")
 

@@ -162,3 +162,36 @@ def test_workspaces_of_another_device_are_refused(lib, monkeypatch):
     assert binding._stream_handle(None, Other()) == 64
     # what the test's stand-ins left is not kept
     binding._raw_stream = binding._current_device = None
+
+
+def test_views_that_are_not_dense_are_refused(lib):
+    """Only rows may be strided: other views would be read as if they were dense."""
+    import torch
+
+    plan = binding.PagedAttention(4, 2, 64, 16)
+    bf = dict(dtype=torch.bfloat16)
+    pair = torch.zeros(3, 2, 2, 16, 64, **bf)  # keys and values of a block side by side
+    k, v = torch.zeros(2, 3, 2, 16, 64, **bf)
+    q, out = torch.zeros(2, 5, 4, 64, **bf)
+    table, ints, ws = torch.zeros(1, 8, dtype=torch.int32), torch.zeros(8, dtype=torch.int32), torch.zeros(256)
+
+    def attend(q=q, k=k, v=v, table=table, out=out):
+        plan.attend(1, 5, ints, ints, q, k, v, table, 3, out, ws)
+
+    def append(qkv, k=k, v=v, q_out=q):
+        plan.append(5, qkv, None, None, ints, ints, 3, q_out, k, v, ws)
+
+    qkv = torch.zeros(5, 8 * 64, **bf)
+    wide = torch.zeros(2, 16, dtype=torch.int32)
+    for call in (lambda: attend(k=pair[:, 0]), lambda: attend(v=pair[:, 1]), lambda: attend(table=wide[:, :8]),
+                 lambda: attend(q=q.transpose(1, 2).contiguous().transpose(1, 2)),
+                 lambda: attend(out=torch.zeros(5, 4, 128, **bf)[:, :, ::2]),
+                 lambda: attend(out=torch.zeros(5, 4, 128, **bf)[:, :, :64]),
+                 lambda: attend(q=q.float()), lambda: attend(out=out.half()), lambda: attend(k=k.float()),
+                 lambda: append(qkv, k=pair[:, 0]), lambda: append(qkv, v=pair[:, 0]),
+                 lambda: append(qkv, q_out=torch.zeros(5, 8, 64, **bf)[:, :4]), lambda: append(qkv[:, ::2]),
+                 lambda: append(qkv.float()), lambda: append(qkv, q_out=q.float()),
+                 lambda: binding.verify_sampled(1, 4, ints, ints, torch.zeros(4, 32)[:, :16], 16, F32, None, ints,
+                                                torch.zeros(1, 16), ints, ints, None, ws)):
+        with pytest.raises(ValueError, match="dense|type"):
+            call()
