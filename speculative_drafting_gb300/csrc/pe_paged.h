@@ -55,13 +55,15 @@ struct RowRange {
   int q0, q1;
   bool bad;
 };
-__device__ __forceinline__ RowRange request_rows(const int32_t* qsl, int r, int T) {
+__device__ __forceinline__ RowRange row_range(int a, int b, int r, int T) {  // a, b: qsl[r], qsl[r + 1]
   RowRange x;
-  const int a = qsl[r], b = qsl[r + 1];
   x.bad = a < 0 || b > T || b < a || (r == 0 && a != 0);
   x.q0 = min(max(a, 0), T);
   x.q1 = min(max(b, x.q0), T);
   return x;
+}
+__device__ __forceinline__ RowRange request_rows(const int32_t* qsl, int r, int T) {
+  return row_range(qsl[r], qsl[r + 1], r, T);
 }
 
 }  // namespace pe

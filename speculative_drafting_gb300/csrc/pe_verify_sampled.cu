@@ -54,8 +54,11 @@ struct VerifyArgs {
   ulonglong2* best;     // [B][rsplits]: order of the score, token
 };
 
-PE_DEV float temperature_of(const VerifyArgs& a, int r) {
-  const float t = a.temperature ? a.temperature[r] : 1.f;
+// as given (NULL: 1), and as used
+PE_DEV float given_temperature(const VerifyArgs& a, int r) {
+  return a.temperature ? __ldcg(a.temperature + r) : 1.f;
+}
+PE_DEV float temperature_of(float t) {
   return t > 0.f ? fminf(fmaxf(t, 1e-30f), 1e30f) : 0.f;  // 1 / T stays finite and above 0
 }
 
@@ -173,8 +176,10 @@ __global__ void __launch_bounds__(kThreads, 6) sampled_row_kernel(const VerifyAr
   __shared__ Stat st_sh[kThreads / 32];
   __shared__ unsigned long long key_sh[kThreads / 32];
   __shared__ float temp_sh;
-  pdl_trigger();
+  // (in this order: when the request kernel starts, what came before this one is done, and
+  // the inputs may be read)
   pdl_wait();
+  pdl_trigger();
   const int row = blockIdx.x / a.splits, sp = blockIdx.x - row * a.splits;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (blockIdx.x == 0) {  // only the request kernel, after this one, uses these
@@ -197,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 6) sampled_row_kernel(const VerifyAr
     u[x] = tid + x * kThreads < nvec ? ld_stream16(vp + tid + x * kThreads) : none;
   if (warp == 0) {
     const int r = request_of(a, row, lane);
-    if (lane == 0) temp_sh = r < 0 ? -1.f : temperature_of(a, r);
+    if (lane == 0) temp_sh = r < 0 ? -1.f : temperature_of(given_temperature(a, r));
   }
   __syncthreads();
   const float temp = temp_sh;
@@ -319,13 +324,33 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
   __shared__ unsigned long long key_sh[kW];
   __shared__ int idx_sh[kW];
   pdl_trigger();
-  pdl_wait();
   const int r = blockIdx.x / a.rsplits, sp = blockIdx.x - r * a.rsplits;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const RowRange x = request_rows(a.qsl, r, a.T);
+  // The inputs are read while the row kernel ends (from L2: this kernel has waited for
+  // nothing yet): the request, and of the row that this warp looks at first the draft, its
+  // logit and its number (8 fp32 rows 11.4 -> 10.8 us).
+  const RowRange x = row_range(__ldcg(a.qsl + r), __ldcg(a.qsl + r + 1), r, a.T);
   const int n = x.q1 - x.q0;
-  const float t0 = a.temperature ? a.temperature[r] : 1.f;
-  const float temp = temperature_of(a, r);
+  const float t0 = given_temperature(a, r);
+  const float temp = temperature_of(t0);
+  struct Draft {
+    int v;       // the draft after the row, -1: none
+    float l, u;  // its logit in the row and its number
+  };
+  auto draft_of = [&](int j) {
+    Draft d{-1, -INFINITY, 0.f};
+    const int64_t row = x.q0 + j;
+    if (j + 1 < n) {
+      d.v = __ldcg(a.tok + row + 1);
+      if (temp != 0.f) {
+        d.u = __ldcg(a.u + row + 1);
+        if (d.v >= 0 && d.v < a.V) d.l = Elem<T>::to_f(__ldcg(static_cast<const T*>(a.logits) + row * a.V + d.v));
+      }
+    }
+    return d;
+  };
+  const Draft first = draft_of(warp);
+  pdl_wait();
   if (temp == 0.f && sp > 0) return;  // a greedy request has no race
   uint32_t st = x.bad ? PE_ST_ROWS_RANGE : 0u;
   if (!(t0 >= 0.f)) st |= PE_ST_SAMPLING;
@@ -364,7 +389,8 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
     if (j < n) {
       const int64_t row = x.q0 + j;
       const bool draft = j + 1 < n;
-      const int v = draft ? a.tok[row + 1] : -1;
+      const Draft d = j0 == 0 ? first : draft_of(j);
+      const int v = d.v;
       const bool in = v >= 0 && v < a.V;
       float p = 0.f, top = 0.f;
       int pick = -1;
@@ -372,13 +398,11 @@ __global__ void __launch_bounds__(kThreads) sampled_request_kernel(const VerifyA
         pick = row_pick(j);
         p = in && pick == v ? 1.f : 0.f;
       } else {
-        const float l = in ? Elem<T>::to_f(static_cast<const T*>(a.logits)[row * a.V + v]) : -INFINITY;
-        const float u = draft ? a.u[row + 1] : 0.f;
         const Stat s = row_stat(j);
         top = s.m;
         pick = fabsf(s.m) < INFINITY ? 0 : -1;  // whether the row has a distribution
-        if (pick == 0) p = fminf(ex2((l - s.m) * c) / s.s, 1.f);
-        rejected = !(u < p);
+        if (pick == 0) p = fminf(ex2((d.l - s.m) * c) / s.s, 1.f);
+        rejected = !(d.u < p);
       }
       if (temp == 0.f) rejected = p == 0.f;
       rejected &= draft;
