@@ -23,8 +23,8 @@
 //
 // Infinities and NaN.  A key that some rows of a unit see and others do not has weight 0
 // in the others' product, and 0 times what is not finite is NaN.  Rows whose result is
-// not finite though their l is a number, and which do not see all of their unit's keys,
-// are computed again by the second kernel from the keys that they do see.
+// not finite though their l is a number, in units with a value that is not finite past
+// some row's last key, are computed again by the second kernel from the keys that they see.
 //
 // Warps: 0-7 softmax of stream 0 (two warps to 32 rows, half the keys of a tile each),
 // 8-15 of stream 1, 16 K tiles and the unit list, 17 and 18 the products of either stream,
@@ -1154,6 +1154,18 @@ __device__ __noinline__ void redo_unit(const TcArgs& p, int r, int g, int row0, 
   __syncthreads();
   const Req q = load_req(a, r, false);
   const int kend = unit_kend(q, row0 / kUnitRows, HG);
+  // Only where a value that some row does not see (at most the unit's tokens) is not finite:
+  // what all of its rows see reached them rightly.
+  const int t0 = max(q.L - q.n + row0 / HG + 1, 0), chunks = a.hd / 8;
+  __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+  for (int i = threadIdx.x; i < (kend - t0) * chunks; i += 32 * kRowWarps) {
+    const int t = t0 + i / chunks;
+    const int blk = a.block_table[static_cast<long long>(r) * a.max_blocks + t / a.bs];
+    if (blk < 0 || blk >= a.num_blocks) continue;
+    const long long key = (static_cast<long long>(blk) * a.G + g) * a.bs + t % a.bs;
+    zero = not_finite(reinterpret_cast<const uint4*>(a.v_cache)[key * chunks + i % chunks], zero);
+  }
+  if (!__syncthreads_or(__hisnan(zero.x) || __hisnan(zero.y))) return;
   for (int w = 0; w < kRowWarps; ++w)
     for (uint32_t todo = again_sh[w]; todo; todo &= todo - 1) {
       const int row = row0 + join_row(__ffs(todo) - 1, w);

@@ -411,3 +411,34 @@ def test_attend_infinities_and_nan_at_later_positions(dtype, H, G, hd, bs, ns, L
             np.testing.assert_array_equal(val[row][~fin], ref[0][~fin])
             err = np.abs(val[row] - np.where(fin, ref[0], 0))[fin]
             assert (err <= (half * np.abs(ref[0]) + w * spread[0])[fin] + 1e-30).all(), (r, j)
+
+
+@pytest.mark.parametrize("H,G,hd", [(64, 8, 64), (28, 4, 128)])
+@pytest.mark.parametrize("n,L", [(300, 300), (70, 2500), (8, 90)])
+@pytest.mark.parametrize("late", [False, True])
+def test_attend_infinities_and_nan_that_all_rows_see(H, G, hd, n, L, late):
+    """A value that every row sees reaches every row, in its column and KV head alone; with
+    one more that only the last row sees, beside it."""
+    c = _chunk("bf16", H, G, hd, 16, (n,), (L,), seed=33)
+    vc = O.decode(c["vc"], "bf16")
+    clean = vc.copy()
+    vc[c["table"][0][0], 0, 0, 5] = np.nan
+    vc[c["table"][0][0], 1, 0, 9] = -np.inf
+    if late:
+        vc[c["table"][0][(L - 1) // 16], 0, (L - 1) % 16, 11] = np.inf
+    c["vc"] = _store(vc, "bf16")
+    got, st = _attend(c)
+    assert st == 0
+    val = _value(got, "bf16").reshape(n, H, hd)
+    c["vc"] = _store(clean, "bf16")
+    ref, spread = P.chunk_attention(c["qsl"], c["seq"], O.decode(c["q"], "bf16").reshape(n, H, hd),
+                                    O.decode(c["kc"], "bf16"), clean, c["table"])
+    want = ref.copy()
+    hg = H // G
+    want[:, :hg, 5] = np.nan
+    want[:, hg:2 * hg, 9] = -np.inf
+    if late:
+        want[n - 1, :hg, 11] = np.inf
+    fin = np.isfinite(want)
+    np.testing.assert_array_equal(val[~fin], want[~fin])
+    assert (np.abs(val - ref)[fin] <= (2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 1e-4) * spread)[fin] + 1e-30).all()
