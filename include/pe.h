@@ -481,8 +481,8 @@ int pe_attn_plan_init(pe_attn_plan* plan, int n_heads, int n_kv_heads, int head_
 /* Norm, rotation and cache write of T rows in one pass.
  *   qkv      [T][H + 2G][hd] in the plan's dtype: q heads, then k, then v heads
  *            (the order of w_qkv); consecutive rows ld_qkv elements apart
- *   gamma_q, gamma_k  [hd] gains of the per-head RMS norms, each nullable (NULL: no
- *            norm): y = x * gamma / sqrt(mean(x^2) + eps), in fp32
+ *   gamma_q, gamma_k  [hd] gains of the per-head RMS norms in the plan's dtype, each
+ *            nullable (NULL: no norm): y = x * gamma / sqrt(mean(x^2) + eps), in fp32
  *   pos[T]   int64 positions; the pair (y_i, y_{i+hd/2}) turns by
  *            pos * theta^(-2i/hd) (q and k heads; v heads are copied)
  *   slot[T]  int64 cache slots.  Negative: the row's k and v are not written (its q

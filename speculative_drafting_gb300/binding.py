@@ -482,7 +482,16 @@ class PagedAttention:
 
     def _refuse(self, *tensors):
         got = ", ".join(f"{t.dtype} {tuple(t.shape)} strides {t.stride()}" for t in tensors if t is not None)
-        raise ValueError(f"the plan's type is {self.dtype}; caches, q_out and block_table are dense: got {got}")
+        raise ValueError(f"the plan's type is {self.dtype}; caches, q_out, gains (of head_dim elements) and "
+                         f"block_table are dense: got {got}")
+
+    def _gain(self, t):
+        # nullable, of the plan's type: other bytes would be read as if they were
+        if t is None:
+            return None
+        if not (t.dtype is self.dtype and t.numel() == self.hd and t.is_contiguous()):
+            self._refuse(t)
+        return t.data_ptr()
 
     def append_workspace(self, device="cuda"):
         """The status word of ``append`` (zeroed)."""
@@ -503,7 +512,7 @@ class PagedAttention:
     def append(self, T, qkv, gamma_q, gamma_k, pos, slot, num_blocks, q_out, k_cache, v_cache, ws,
                stream=None):
         """pe_qkv_append: qkv [T][H + 2G][hd] (or [T][(H + 2G) hd]; its rows may be
-        strided), gains and q_out may be None."""
+        strided), gains and q_out may be None; the gains have the plan's type."""
         # (a call of a few rows is bound by its host time: data_ptr without _addr and checks
         # in line save 0.3 us of 5.4)
         d = self.dtype
@@ -511,8 +520,8 @@ class PagedAttention:
                 and k_cache.is_contiguous() and v_cache.is_contiguous()
                 and (q_out is None or (q_out.dtype is d and q_out.is_contiguous()))):
             self._refuse(qkv, k_cache, v_cache, q_out)
-        rc = self.lib.pe_qkv_append(self.addr, T, qkv.data_ptr(), _row_stride(qkv, self.hd), _addr(gamma_q),
-                                    _addr(gamma_k), pos.data_ptr(), slot.data_ptr(), num_blocks,
+        rc = self.lib.pe_qkv_append(self.addr, T, qkv.data_ptr(), _row_stride(qkv, self.hd), self._gain(gamma_q),
+                                    self._gain(gamma_k), pos.data_ptr(), slot.data_ptr(), num_blocks,
                                     _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(),
                                     ws.numel(), _stream_handle(stream, ws))
         _check(rc, "pe_qkv_append")

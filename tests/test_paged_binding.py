@@ -1,0 +1,72 @@
+"""What the binding of the paged calls and of sampled verification hands to the library:
+tensors of another type, size or device than the call reads are refused before it (no GPU
+needed: the library's calls are stand-ins that note their arguments)."""
+
+import os
+import shutil
+
+import pytest
+
+from speculative_drafting_gb300 import binding, build
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.skipif(shutil.which("nvcc") is None and not os.path.exists(
+    "/usr/local/cuda/bin/nvcc"), reason="needs nvcc to build libpe.so")
+
+H, G, HD, BS, T, NB = 4, 2, 64, 16, 5, 3
+BF = torch.bfloat16
+
+
+class Calls:
+    """The library's compute calls, noted instead of made; host-only calls go through."""
+
+    def __init__(self, lib):
+        self.lib, self.made = lib, []
+
+    def __getattr__(self, name):
+        if name in ("pe_qkv_append", "pe_chunk_attention", "pe_verify_sampled"):
+            return lambda *a: self.made.append((name, a)) or binding.PE_OK
+        return getattr(self.lib, name)
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    build.build()
+    c = Calls(binding.load())
+    monkeypatch.setattr(binding, "_lib", c)
+    # CPU tensors are on device -1
+    monkeypatch.setattr(binding, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(binding, "_current_device", lambda: -1)
+    return c
+
+
+def plan():
+    return binding.PagedAttention(H, G, HD, BS)
+
+
+def append(**kw):
+    a = dict(T=T, qkv=torch.zeros(T, (H + 2 * G) * HD, dtype=BF), gamma_q=torch.ones(HD, dtype=BF),
+             gamma_k=torch.ones(HD, dtype=BF), pos=torch.arange(T), slot=torch.arange(T), num_blocks=NB,
+             q_out=torch.zeros(T, H, HD, dtype=BF), k_cache=torch.zeros(NB, G, BS, HD, dtype=BF),
+             v_cache=torch.zeros(NB, G, BS, HD, dtype=BF), ws=torch.zeros(256, dtype=torch.uint8))
+    a.update(kw)
+    plan().append(**a)
+
+
+def refused(calls, make, *cases):
+    """The call as it should be goes through, once; each of the others is refused."""
+    make()
+    assert len(calls.made) == 1
+    for kw in cases:
+        with pytest.raises(ValueError):
+            make(**kw)
+        assert len(calls.made) == 1, {k: getattr(v, "dtype", v) for k, v in kw.items()}
+
+
+def test_gains_of_another_type_or_size_are_refused(calls):
+    append(gamma_q=None, gamma_k=None)
+    calls.made.clear()
+    refused(calls, append, dict(gamma_q=torch.ones(HD)), dict(gamma_k=torch.ones(HD)),
+            dict(gamma_k=torch.ones(HD, dtype=torch.half)), dict(gamma_q=torch.ones(HD // 2, dtype=BF)),
+            dict(gamma_q=torch.ones(H, HD, dtype=BF)), dict(gamma_k=torch.ones(2 * HD, dtype=BF)[::2]))
