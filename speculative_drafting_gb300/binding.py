@@ -474,6 +474,7 @@ class PagedAttention:
         self.c = PeAttnPlan()
         self.addr = ctypes.addressof(self.c)
         self.hd = head_dim
+        self.i32, self.i64, self.f32 = torch.int32, torch.int64, torch.float32
         self.dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
         self.qkv_width = (n_heads + 2 * n_kv_heads) * head_dim
         code = {"bf16": PE_DTYPE_BF16, "f32": PE_DTYPE_F32}.get(dtype, -1)
@@ -484,6 +485,10 @@ class PagedAttention:
         got = ", ".join(f"{t.dtype} {tuple(t.shape)} strides {t.stride()}" for t in tensors if t is not None)
         raise ValueError(f"the plan's type is {self.dtype}; caches, q_out, gains (of head_dim elements) and "
                          f"block_table are dense: got {got}")
+
+    def _refuse_ints(self, what, *tensors):
+        got = ", ".join(f"{t.dtype} strides {t.stride()}" for t in tensors)
+        raise ValueError(f"{what}, all dense: got {got}")
 
     def _gain(self, t):
         # nullable, of the plan's type: other bytes would be read as if they were
@@ -520,6 +525,9 @@ class PagedAttention:
                 and k_cache.is_contiguous() and v_cache.is_contiguous()
                 and (q_out is None or (q_out.dtype is d and q_out.is_contiguous()))):
             self._refuse(qkv, k_cache, v_cache, q_out)
+        i64 = self.i64
+        if not (pos.dtype is i64 and slot.dtype is i64 and pos.is_contiguous() and slot.is_contiguous()):
+            self._refuse_ints("pos and slot have the type int64", pos, slot)
         rc = self.lib.pe_qkv_append(self.addr, T, qkv.data_ptr(), _row_stride(qkv, self.hd), self._gain(gamma_q),
                                     self._gain(gamma_k), pos.data_ptr(), slot.data_ptr(), num_blocks,
                                     _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(),
@@ -534,6 +542,12 @@ class PagedAttention:
         if not (q.dtype is d and k_cache.dtype is d and v_cache.dtype is d and out.dtype is d
                 and k_cache.is_contiguous() and v_cache.is_contiguous() and block_table.is_contiguous()):
             self._refuse(q, k_cache, v_cache, out, block_table)
+        i32 = self.i32
+        if not (qsl.dtype is i32 and seq_len.dtype is i32 and block_table.dtype is i32
+                and qsl.is_contiguous() and seq_len.is_contiguous()):
+            self._refuse_ints("qsl, seq_len and block_table have the type int32", qsl, seq_len, block_table)
+        if sink is not None and not (sink.dtype is self.f32 and sink.is_contiguous()):
+            self._refuse_ints("sink has the type float32", sink)
         rc = self.lib.pe_chunk_attention(self.addr, B, T, qsl.data_ptr(), seq_len.data_ptr(), q.data_ptr(),
                                          _row_stride(q, self.hd), k_cache.data_ptr(), v_cache.data_ptr(),
                                          block_table.data_ptr(), block_table.shape[1], num_blocks,

@@ -54,6 +54,18 @@ def append(**kw):
     plan().append(**a)
 
 
+def attend(**kw):
+    i32 = dict(dtype=torch.int32)
+    a = dict(B=1, T=T, qsl=torch.tensor([0, T], **i32), seq_len=torch.tensor([T], **i32),
+             q=torch.zeros(T, H, HD, dtype=BF), k_cache=torch.zeros(NB, G, BS, HD, dtype=BF),
+             v_cache=torch.zeros(NB, G, BS, HD, dtype=BF), block_table=torch.zeros(1, 2, **i32), num_blocks=NB,
+             out=torch.zeros(T, H * HD, dtype=BF), ws=None, sink=torch.zeros(H))
+    a.update(kw)
+    p = plan()
+    a["ws"] = p.workspace(1, T, device="cpu") if a["ws"] is None else a["ws"]
+    p.attend(**a)
+
+
 def refused(calls, make, *cases):
     """The call as it should be goes through, once; each of the others is refused."""
     make()
@@ -70,3 +82,18 @@ def test_gains_of_another_type_or_size_are_refused(calls):
     refused(calls, append, dict(gamma_q=torch.ones(HD)), dict(gamma_k=torch.ones(HD)),
             dict(gamma_k=torch.ones(HD, dtype=torch.half)), dict(gamma_q=torch.ones(HD // 2, dtype=BF)),
             dict(gamma_q=torch.ones(H, HD, dtype=BF)), dict(gamma_k=torch.ones(2 * HD, dtype=BF)[::2]))
+
+
+def test_append_indexes_of_another_type_are_refused(calls):
+    i = torch.arange(T)
+    refused(calls, append, dict(pos=i.int()), dict(slot=i.int()), dict(pos=i.double()),
+            dict(slot=torch.arange(2 * T)[::2]), dict(pos=torch.arange(2 * T)[::2]))
+
+
+def test_attend_indexes_and_sinks_of_another_type_are_refused(calls):
+    attend(sink=None)
+    calls.made.clear()
+    refused(calls, attend, dict(qsl=torch.tensor([0, T])), dict(seq_len=torch.tensor([T])),
+            dict(block_table=torch.zeros(1, 2, dtype=torch.int64)), dict(sink=torch.zeros(H, dtype=BF)),
+            dict(sink=torch.zeros(H, dtype=torch.float64)), dict(sink=torch.zeros(2 * H)[::2]),
+            dict(qsl=torch.tensor([0, 9, T, 9], dtype=torch.int32)[::2]))
