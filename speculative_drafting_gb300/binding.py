@@ -434,6 +434,18 @@ def read_status_ws(ws, clear=True, stream=None):
     return int(v.value), rc
 
 
+_torch_types = None
+
+
+def _types():
+    global _torch_types
+    if _torch_types is None:
+        import torch
+
+        _torch_types = torch.float32, torch.bfloat16, torch.int32
+    return _torch_types
+
+
 def verify_sampled_workspace(max_batch: int, max_rows_in: int, vocab: int, device="cuda"):
     """A device workspace for pe_verify_sampled (torch allocates it 256-byte aligned)."""
     import torch
@@ -447,10 +459,16 @@ def verify_sampled_workspace(max_batch: int, max_rows_in: int, vocab: int, devic
 def verify_sampled(B, T_in, qsl, tok, logits, vocab, dtype, temperature, u, gumbel, accepted, bonus,
                    p_draft, ws, stream=None):
     """pe_verify_sampled on device tensors, dense ones; dtype is PE_DTYPE_F32 or
-    PE_DTYPE_BF16; temperature and p_draft may be None."""
-    for t in (logits, gumbel):
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"logits and gumbel have to be dense, not with strides {t.stride()}")
+    PE_DTYPE_BF16 and the type of logits; qsl, tok, accepted and bonus are int32, the other
+    tensors float32; temperature and p_draft may be None."""
+    f32, bf16, i32 = _types()
+    floats = [t for t in (u, gumbel, temperature, p_draft) if t is not None]
+    if not (logits.dtype is (bf16 if dtype == PE_DTYPE_BF16 else f32) and logits.is_contiguous()
+            and all([t.dtype is f32 and t.is_contiguous() for t in floats])
+            and all([t.dtype is i32 and t.is_contiguous() for t in (qsl, tok, accepted, bonus)])):
+        got = ", ".join(f"{t.dtype} strides {t.stride()}" for t in (logits, qsl, tok, accepted, bonus, *floats))
+        raise ValueError("logits have the type of dtype, qsl, tok, accepted and bonus int32, u, gumbel, "
+                         f"temperature and p_draft float32, all dense: got {got}")
     rc = load().pe_verify_sampled(B, T_in, _addr(qsl), _addr(tok), _addr(logits), vocab, dtype,
                                   _addr(temperature), _addr(u), _addr(gumbel), _addr(accepted),
                                   _addr(bonus), _addr(p_draft), _addr(ws), ws.numel(),

@@ -66,6 +66,19 @@ def attend(**kw):
     p.attend(**a)
 
 
+V = 40
+
+
+def verify(**kw):
+    i32 = dict(dtype=torch.int32)
+    a = dict(B=2, T_in=T, qsl=torch.tensor([0, 3, T], **i32), tok=torch.zeros(T, **i32), logits=torch.zeros(T, V),
+             vocab=V, dtype=binding.PE_DTYPE_F32, temperature=torch.ones(2), u=torch.zeros(T),
+             gumbel=torch.zeros(2, V), accepted=torch.zeros(2, **i32), bonus=torch.zeros(2, **i32),
+             p_draft=torch.zeros(T), ws=binding.verify_sampled_workspace(2, T, V, device="cpu"))
+    a.update(kw)
+    binding.verify_sampled(**a)
+
+
 def refused(calls, make, *cases):
     """The call as it should be goes through, once; each of the others is refused."""
     make()
@@ -97,3 +110,17 @@ def test_attend_indexes_and_sinks_of_another_type_are_refused(calls):
             dict(block_table=torch.zeros(1, 2, dtype=torch.int64)), dict(sink=torch.zeros(H, dtype=BF)),
             dict(sink=torch.zeros(H, dtype=torch.float64)), dict(sink=torch.zeros(2 * H)[::2]),
             dict(qsl=torch.tensor([0, 9, T, 9], dtype=torch.int32)[::2]))
+
+
+def test_verify_sampled_tensors_of_another_type_are_refused(calls):
+    verify(temperature=None, p_draft=None)
+    verify(logits=torch.zeros(T, V, dtype=BF), dtype=binding.PE_DTYPE_BF16)
+    calls.made.clear()
+    every = [torch.zeros(2 * T)[::2], torch.zeros(T, dtype=torch.float64), torch.zeros(T, dtype=BF)]
+    refused(calls, verify, dict(logits=torch.zeros(T, V, dtype=BF)), dict(dtype=binding.PE_DTYPE_BF16),
+            dict(logits=torch.zeros(T, V, dtype=torch.half)), dict(logits=torch.zeros(T, 2 * V)[:, :V]),
+            dict(tok=torch.zeros(T, dtype=torch.int64)), dict(tok=torch.zeros(2 * T, dtype=torch.int32)[::2]),
+            dict(qsl=torch.tensor([0, 3, T])), dict(accepted=torch.zeros(2, dtype=torch.int64)),
+            dict(bonus=torch.zeros(2, dtype=torch.int64)), dict(gumbel=torch.zeros(2, V, dtype=torch.float64)),
+            dict(gumbel=torch.zeros(2, 2 * V)[:, :V]),
+            *(dict([(k, t)]) for k in ("temperature", "u", "p_draft") for t in every))
