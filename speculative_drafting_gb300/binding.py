@@ -212,12 +212,20 @@ def _stream_handle(stream, t):
     return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _row_stride(t, hd):
+def _row_stride(t, T, heads, hd):
     """Elements from one row of [T][heads][hd] (or [T][heads hd]) to the next; the rows
-    themselves have to be dense."""
-    s = t.stride()
-    if s[-1] != 1 or (len(s) == 3 and s[1] != hd and t.shape[1] != 1):
-        raise ValueError(f"rows of shape {tuple(t.shape[1:])} with strides {s}: a row has to be dense")
+    themselves have to be dense, and there."""
+    n, s = t.shape, t.stride()
+    if len(s) == 3:
+        dense, width = s[2] == 1 and (s[1] == hd or n[1] == 1), n[1] * n[2]
+    elif len(s) == 2:
+        dense, width = s[1] == 1, n[1]
+    else:
+        raise ValueError(f"a tensor of shape {tuple(n)}: rows of {heads} heads have two or three dimensions, dense")
+    if not dense:
+        raise ValueError(f"rows of shape {tuple(n[1:])} with strides {s}: a row has to be dense")
+    if n[0] < T or width < heads * hd:
+        raise ValueError(f"{T} rows of {heads} heads of {hd} do not fit the shape {tuple(n)}")
     return s[0]
 
 
@@ -462,13 +470,14 @@ def verify_sampled(B, T_in, qsl, tok, logits, vocab, dtype, temperature, u, gumb
     PE_DTYPE_BF16 and the type of logits; qsl, tok, accepted and bonus are int32, the other
     tensors float32; temperature and p_draft may be None."""
     f32, bf16, i32 = _types()
-    floats = [t for t in (u, gumbel, temperature, p_draft) if t is not None]
-    if not (logits.dtype is (bf16 if dtype == PE_DTYPE_BF16 else f32) and logits.is_contiguous()
-            and all([t.dtype is f32 and t.is_contiguous() for t in floats])
-            and all([t.dtype is i32 and t.is_contiguous() for t in (qsl, tok, accepted, bonus)])):
-        got = ", ".join(f"{t.dtype} strides {t.stride()}" for t in (logits, qsl, tok, accepted, bonus, *floats))
-        raise ValueError("logits have the type of dtype, qsl, tok, accepted and bonus int32, u, gumbel, "
-                         f"temperature and p_draft float32, all dense: got {got}")
+    for name, t, ty, n in (("logits", logits, bf16 if dtype == PE_DTYPE_BF16 else f32, T_in * vocab),
+                           ("qsl", qsl, i32, B and B + 1), ("tok", tok, i32, T_in), ("u", u, f32, T_in),
+                           ("temperature", temperature, f32, B), ("gumbel", gumbel, f32, B * vocab),
+                           ("accepted", accepted, i32, B), ("bonus", bonus, i32, B),
+                           ("p_draft", p_draft, f32, T_in)):
+        if t is not None and not (t.dtype is ty and t.numel() >= n and t.is_contiguous()):
+            raise ValueError(f"{name}: {n} dense elements of the type {ty} are read or written, "
+                             f"got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
     rc = load().pe_verify_sampled(B, T_in, _addr(qsl), _addr(tok), _addr(logits), vocab, dtype,
                                   _addr(temperature), _addr(u), _addr(gumbel), _addr(accepted),
                                   _addr(bonus), _addr(p_draft), _addr(ws), ws.numel(),
@@ -494,7 +503,9 @@ class PagedAttention:
         self.hd = head_dim
         self.i32, self.i64, self.f32 = torch.int32, torch.int64, torch.float32
         self.dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
-        self.qkv_width = (n_heads + 2 * n_kv_heads) * head_dim
+        self.heads, self.qkv_heads = n_heads, n_heads + 2 * n_kv_heads
+        self.width = n_heads * head_dim
+        self.block = n_kv_heads * block_size * head_dim  # elements of a cache's block
         code = {"bf16": PE_DTYPE_BF16, "f32": PE_DTYPE_F32}.get(dtype, -1)
         _check(self.lib.pe_attn_plan_init(self.addr, n_heads, n_kv_heads, head_dim, block_size,
                                           code, eps, rope_theta), "pe_attn_plan_init")
@@ -507,6 +518,10 @@ class PagedAttention:
     def _refuse_ints(self, what, *tensors):
         got = ", ".join(f"{t.dtype} strides {t.stride()}" for t in tensors)
         raise ValueError(f"{what}, all dense: got {got}")
+
+    def _too_small(self, what, *tensors):
+        raise ValueError(f"{what} of {self.heads} heads do not fit the shapes "
+                         f"{[tuple(t.shape) for t in tensors if t is not None]}")
 
     def _gain(self, t):
         # nullable, of the plan's type: other bytes would be read as if they were
@@ -546,7 +561,10 @@ class PagedAttention:
         i64 = self.i64
         if not (pos.dtype is i64 and slot.dtype is i64 and pos.is_contiguous() and slot.is_contiguous()):
             self._refuse_ints("pos and slot have the type int64", pos, slot)
-        rc = self.lib.pe_qkv_append(self.addr, T, qkv.data_ptr(), _row_stride(qkv, self.hd), self._gain(gamma_q),
+        if (pos.numel() < T or slot.numel() < T or (q_out is not None and q_out.numel() < T * self.width)
+                or k_cache.numel() < num_blocks * self.block or v_cache.numel() < num_blocks * self.block):
+            self._too_small(f"{T} rows, {num_blocks} blocks", pos, slot, q_out, k_cache, v_cache)
+        rc = self.lib.pe_qkv_append(self.addr, T, qkv.data_ptr(), _row_stride(qkv, T, self.qkv_heads, self.hd), self._gain(gamma_q),
                                     self._gain(gamma_k), pos.data_ptr(), slot.data_ptr(), num_blocks,
                                     _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(),
                                     ws.numel(), _stream_handle(stream, ws))
@@ -566,10 +584,15 @@ class PagedAttention:
             self._refuse_ints("qsl, seq_len and block_table have the type int32", qsl, seq_len, block_table)
         if sink is not None and not (sink.dtype is self.f32 and sink.is_contiguous()):
             self._refuse_ints("sink has the type float32", sink)
+        if T > 0 and B > 0 and (
+                qsl.numel() <= B or seq_len.numel() < B or block_table.shape[0] < B
+                or (sink is not None and sink.numel() < self.heads)
+                or k_cache.numel() < num_blocks * self.block or v_cache.numel() < num_blocks * self.block):
+            self._too_small(f"{B} requests, {num_blocks} blocks", qsl, seq_len, block_table, sink, k_cache, v_cache)
         rc = self.lib.pe_chunk_attention(self.addr, B, T, qsl.data_ptr(), seq_len.data_ptr(), q.data_ptr(),
-                                         _row_stride(q, self.hd), k_cache.data_ptr(), v_cache.data_ptr(),
+                                         _row_stride(q, T, self.heads, self.hd), k_cache.data_ptr(), v_cache.data_ptr(),
                                          block_table.data_ptr(), block_table.shape[1], num_blocks,
-                                         _addr(sink), out.data_ptr(), _row_stride(out, self.hd), ws.data_ptr(),
+                                         _addr(sink), out.data_ptr(), _row_stride(out, T, self.heads, self.hd), ws.data_ptr(),
                                          ws.numel(), _stream_handle(stream, ws))
         _check(rc, "pe_chunk_attention")
 

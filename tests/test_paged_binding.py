@@ -124,3 +124,45 @@ def test_verify_sampled_tensors_of_another_type_are_refused(calls):
             dict(bonus=torch.zeros(2, dtype=torch.int64)), dict(gumbel=torch.zeros(2, V, dtype=torch.float64)),
             dict(gumbel=torch.zeros(2, 2 * V)[:, :V]),
             *(dict([(k, t)]) for k in ("temperature", "u", "p_draft") for t in every))
+
+
+def test_append_tensors_too_small_for_the_call_are_refused(calls):
+    bf = dict(dtype=BF)
+    append(qkv=torch.zeros(T, H + 2 * G, HD, **bf))
+    append(qkv=torch.zeros(T + 2, (H + 2 * G) * HD + 64, **bf), pos=torch.arange(9), slot=torch.arange(9), q_out=None)
+    append(T=0, qkv=torch.zeros(0, (H + 2 * G) * HD, **bf))
+    append(qkv=torch.zeros(T, 1, (H + 2 * G) * HD, **bf))
+    calls.made.clear()
+    refused(calls, append, dict(T=T + 1), dict(pos=torch.arange(T - 1)), dict(slot=torch.arange(T - 1)),
+            dict(qkv=torch.zeros(T - 1, (H + 2 * G) * HD, **bf)), dict(qkv=torch.zeros(T, (H + 2 * G) * HD - 8, **bf)),
+            dict(qkv=torch.zeros(T, H + G, HD, **bf)), dict(qkv=torch.zeros((H + 2 * G) * HD, **bf)),
+            dict(q_out=torch.zeros(T - 1, H, HD, **bf)), dict(q_out=torch.zeros(T, H - 1, HD, **bf)),
+            dict(num_blocks=NB + 1), dict(k_cache=torch.zeros(NB, G, BS - 1, HD, **bf)),
+            dict(v_cache=torch.zeros(NB - 1, G, BS, HD, **bf)))
+
+
+def test_attend_tensors_too_small_for_the_call_are_refused(calls):
+    bf, i32 = dict(dtype=BF), dict(dtype=torch.int32)
+    attend(q=torch.zeros(T + 1, H * HD + 64, **bf), out=torch.zeros(T, H, HD, **bf))
+    none, two = torch.zeros(0, H * HD, **bf), torch.zeros(2, 1, **i32)
+    attend(B=2, T=0, q=none, out=none, qsl=two, seq_len=two, block_table=two)  # nothing to do: nothing is read
+    calls.made.clear()
+    refused(calls, attend, dict(T=T + 1), dict(B=2), dict(qsl=torch.zeros(1, **i32)), dict(seq_len=torch.zeros(0, **i32)),
+            dict(block_table=torch.zeros(0, 2, **i32)), dict(sink=torch.zeros(H - 1)),
+            dict(q=torch.zeros(T - 1, H, HD, **bf)), dict(q=torch.zeros(T, H * HD - 8, **bf)),
+            dict(out=torch.zeros(T - 1, H * HD, **bf)), dict(out=torch.zeros(T, H - 1, HD, **bf)),
+            dict(out=torch.zeros(H * HD, **bf)), dict(num_blocks=NB + 1),
+            dict(k_cache=torch.zeros(NB, G, BS - 1, HD, **bf)), dict(v_cache=torch.zeros(NB - 1, G, BS, HD, **bf)))
+
+
+def test_verify_sampled_tensors_too_small_for_the_call_are_refused(calls):
+    i32 = dict(dtype=torch.int32)
+    verify(logits=torch.zeros(T * V + 7), p_draft=torch.zeros(T + 1), temperature=torch.ones(5))
+    verify(T_in=0, logits=torch.zeros(0, V), tok=torch.zeros(0, **i32), u=torch.zeros(0))
+    verify(T_in=0, logits=None, tok=None, u=None, gumbel=None, p_draft=None)
+    verify(B=0, T_in=0, qsl=None, logits=None, tok=None, u=None, gumbel=None, accepted=None, bonus=None, p_draft=None)
+    calls.made.clear()
+    refused(calls, verify, dict(B=3), dict(T_in=T + 1), dict(vocab=V + 1), dict(qsl=torch.zeros(2, **i32)),
+            dict(tok=torch.zeros(T - 1, **i32)), dict(u=torch.zeros(T - 1)), dict(logits=torch.zeros(T - 1, V)),
+            dict(gumbel=torch.zeros(1, V)), dict(gumbel=torch.zeros(2, V - 1)), dict(temperature=torch.ones(1)),
+            dict(accepted=torch.zeros(1, **i32)), dict(bonus=torch.zeros(1, **i32)), dict(p_draft=torch.zeros(T - 1)))
