@@ -470,12 +470,17 @@ def verify_sampled(B, T_in, qsl, tok, logits, vocab, dtype, temperature, u, gumb
     PE_DTYPE_BF16 and the type of logits; qsl, tok, accepted and bonus are int32, the other
     tensors float32; temperature and p_draft may be None."""
     f32, bf16, i32 = _types()
+    dev = ws.get_device()
     for name, t, ty, n in (("logits", logits, bf16 if dtype == PE_DTYPE_BF16 else f32, T_in * vocab),
                            ("qsl", qsl, i32, B and B + 1), ("tok", tok, i32, T_in), ("u", u, f32, T_in),
                            ("temperature", temperature, f32, B), ("gumbel", gumbel, f32, B * vocab),
                            ("accepted", accepted, i32, B), ("bonus", bonus, i32, B),
                            ("p_draft", p_draft, f32, T_in)):
-        if t is not None and not (t.dtype is ty and t.numel() >= n and t.is_contiguous()):
+        if t is None:
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on device {t.get_device()}, ws on {dev}")
+        if not (t.dtype is ty and t.numel() >= n and t.is_contiguous()):
             raise ValueError(f"{name}: {n} dense elements of the type {ty} are read or written, "
                              f"got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
     rc = load().pe_verify_sampled(B, T_in, _addr(qsl), _addr(tok), _addr(logits), vocab, dtype,
@@ -523,6 +528,10 @@ class PagedAttention:
         raise ValueError(f"{what} of {self.heads} heads do not fit the shapes "
                          f"{[tuple(t.shape) for t in tensors if t is not None]}")
 
+    def _apart(self, *tensors):
+        raise ValueError(f"tensors on devices {[t.get_device() for t in tensors if t is not None]}: "
+                         "all have to be on the workspace's")
+
     def _gain(self, t):
         # nullable, of the plan's type: other bytes would be read as if they were
         if t is None:
@@ -564,6 +573,11 @@ class PagedAttention:
         if (pos.numel() < T or slot.numel() < T or (q_out is not None and q_out.numel() < T * self.width)
                 or k_cache.numel() < num_blocks * self.block or v_cache.numel() < num_blocks * self.block):
             self._too_small(f"{T} rows, {num_blocks} blocks", pos, slot, q_out, k_cache, v_cache)
+        if not (ws.get_device() == qkv.get_device() == pos.get_device() == slot.get_device()
+                == k_cache.get_device() == v_cache.get_device()
+                == (ws if q_out is None else q_out).get_device() == (ws if gamma_q is None else gamma_q).get_device()
+                == (ws if gamma_k is None else gamma_k).get_device()):
+            self._apart(ws, qkv, pos, slot, k_cache, v_cache, q_out, gamma_q, gamma_k)
         rc = self.lib.pe_qkv_append(self.addr, T, qkv.data_ptr(), _row_stride(qkv, T, self.qkv_heads, self.hd), self._gain(gamma_q),
                                     self._gain(gamma_k), pos.data_ptr(), slot.data_ptr(), num_blocks,
                                     _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(),
@@ -589,6 +603,10 @@ class PagedAttention:
                 or (sink is not None and sink.numel() < self.heads)
                 or k_cache.numel() < num_blocks * self.block or v_cache.numel() < num_blocks * self.block):
             self._too_small(f"{B} requests, {num_blocks} blocks", qsl, seq_len, block_table, sink, k_cache, v_cache)
+        if not (ws.get_device() == qsl.get_device() == seq_len.get_device() == q.get_device() == k_cache.get_device()
+                == v_cache.get_device() == block_table.get_device() == out.get_device()
+                == (ws if sink is None else sink).get_device()):
+            self._apart(ws, qsl, seq_len, q, k_cache, v_cache, block_table, out, sink)
         rc = self.lib.pe_chunk_attention(self.addr, B, T, qsl.data_ptr(), seq_len.data_ptr(), q.data_ptr(),
                                          _row_stride(q, T, self.heads, self.hd), k_cache.data_ptr(), v_cache.data_ptr(),
                                          block_table.data_ptr(), block_table.shape[1], num_blocks,

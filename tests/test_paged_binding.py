@@ -166,3 +166,25 @@ def test_verify_sampled_tensors_too_small_for_the_call_are_refused(calls):
             dict(tok=torch.zeros(T - 1, **i32)), dict(u=torch.zeros(T - 1)), dict(logits=torch.zeros(T - 1, V)),
             dict(gumbel=torch.zeros(1, V)), dict(gumbel=torch.zeros(2, V - 1)), dict(temperature=torch.ones(1)),
             dict(accepted=torch.zeros(1, **i32)), dict(bonus=torch.zeros(1, **i32)), dict(p_draft=torch.zeros(T - 1)))
+
+
+class Elsewhere(torch.Tensor):
+    def get_device(self):
+        return 1
+
+
+@pytest.mark.parametrize("make", [append, attend, verify])
+def test_tensors_of_another_device_than_the_workspace_are_refused(calls, monkeypatch, make):
+    """Each tensor in turn: the launch goes to the current device, where its address is
+    another's or nobody's."""
+    sent = {}
+    name = {append: "append", attend: "attend"}.get(make, "verify_sampled")
+    owner = binding if make is verify else binding.PagedAttention
+    real = getattr(owner, name)
+    monkeypatch.setattr(owner, name, lambda *a, **kw: (sent.update(kw), real(*a, **kw))[1])
+    make()
+    given = dict(sent)
+    tensors = [k for k, t in given.items() if isinstance(t, torch.Tensor)]
+    assert len(tensors) >= 9
+    refused(calls, lambda **kw: make(**{**given, **kw}) if kw else None,
+            *(dict([(k, given[k].as_subclass(Elsewhere))]) for k in tensors))
