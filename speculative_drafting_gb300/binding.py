@@ -533,9 +533,7 @@ class PagedAttention:
                          "all have to be on the workspace's")
 
     def _gain(self, t):
-        # nullable, of the plan's type: other bytes would be read as if they were
-        if t is None:
-            return None
+        # of the plan's type: other bytes would be read as if they were
         if not (t.dtype is self.dtype and t.numel() == self.hd and t.is_contiguous()):
             self._refuse(t)
         return t.data_ptr()
@@ -560,27 +558,30 @@ class PagedAttention:
                stream=None):
         """pe_qkv_append: qkv [T][H + 2G][hd] (or [T][(H + 2G) hd]; its rows may be
         strided), gains and q_out may be None; the gains have the plan's type."""
-        # (a call of a few rows is bound by its host time: data_ptr without _addr and checks
-        # in line save 0.3 us of 5.4)
-        d = self.dtype
+        # (a call of a few rows is bound by its host time: the checks stand in line and cost
+        # 1.1 us of 6.5)
+        d, i64, n = self.dtype, self.i64, num_blocks * self.block
         if not (qkv.dtype is d and k_cache.dtype is d and v_cache.dtype is d
                 and k_cache.is_contiguous() and v_cache.is_contiguous()
                 and (q_out is None or (q_out.dtype is d and q_out.is_contiguous()))):
             self._refuse(qkv, k_cache, v_cache, q_out)
-        i64 = self.i64
         if not (pos.dtype is i64 and slot.dtype is i64 and pos.is_contiguous() and slot.is_contiguous()):
             self._refuse_ints("pos and slot have the type int64", pos, slot)
         if (pos.numel() < T or slot.numel() < T or (q_out is not None and q_out.numel() < T * self.width)
-                or k_cache.numel() < num_blocks * self.block or v_cache.numel() < num_blocks * self.block):
+                or k_cache.numel() < n or v_cache.numel() < n):
             self._too_small(f"{T} rows, {num_blocks} blocks", pos, slot, q_out, k_cache, v_cache)
-        if not (ws.get_device() == qkv.get_device() == pos.get_device() == slot.get_device()
-                == k_cache.get_device() == v_cache.get_device()
-                == (ws if q_out is None else q_out).get_device() == (ws if gamma_q is None else gamma_q).get_device()
-                == (ws if gamma_k is None else gamma_k).get_device()):
+        dev = ws.get_device()
+        if not (dev == qkv.get_device() == pos.get_device() == slot.get_device()
+                == k_cache.get_device() == v_cache.get_device() and (q_out is None or q_out.get_device() == dev)
+                and (gamma_q is None or gamma_q.get_device() == dev)
+                and (gamma_k is None or gamma_k.get_device() == dev)):
             self._apart(ws, qkv, pos, slot, k_cache, v_cache, q_out, gamma_q, gamma_k)
-        rc = self.lib.pe_qkv_append(self.addr, T, qkv.data_ptr(), _row_stride(qkv, T, self.qkv_heads, self.hd), self._gain(gamma_q),
-                                    self._gain(gamma_k), pos.data_ptr(), slot.data_ptr(), num_blocks,
-                                    _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(),
+        rc = self.lib.pe_qkv_append(self.addr, T, qkv.data_ptr(), _row_stride(qkv, T, self.qkv_heads, self.hd),
+                                    None if gamma_q is None else self._gain(gamma_q),
+                                    None if gamma_k is None else self._gain(gamma_k),
+                                    pos.data_ptr(), slot.data_ptr(), num_blocks,
+                                    None if q_out is None else q_out.data_ptr(),
+                                    k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(),
                                     ws.numel(), _stream_handle(stream, ws))
         _check(rc, "pe_qkv_append")
 
