@@ -24,7 +24,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, 10) chunk_simt_kernel(const Ch
   const int row = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
   // the request of this row: the last one that starts at or before it
   if (tid == 0) req_sh = -1;
-  row_query<T>(a, row, h, sh);
+  // (rows behind the last request are not read: they may not be written yet)
+  if (row < a.qsl[a.B]) row_query<T>(a, row, h, sh);
   __syncthreads();
   for (int r = tid; r < a.B; r += 32 * kRowWarps) {
     const RowRange x = request_rows(a.qsl, r, a.T);
