@@ -27,9 +27,12 @@ __global__ void __launch_bounds__(32 * kRowWarps, 10) chunk_simt_kernel(const Ch
   // (rows behind the last request are not read: they may not be written yet)
   if (row < a.qsl[a.B]) row_query<T>(a, row, h, sh);
   __syncthreads();
+  const int64_t Lmax = static_cast<int64_t>(a.max_blocks) * a.bs;
   for (int r = tid; r < a.B; r += 32 * kRowWarps) {
     const RowRange x = request_rows(a.qsl, r, a.T);
     if (x.bad) set_status(a.status, PE_ST_ROWS_RANGE);
+    // (of every request, those without rows too)
+    if (row == 0 && h == 0 && (a.seq_len[r] < 0 || a.seq_len[r] > Lmax)) set_status(a.status, PE_ST_BLOCK_RANGE);
     if (x.q0 <= row && row < x.q1) atomicMax(&req_sh, r);
   }
   __syncthreads();
@@ -37,12 +40,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 10) chunk_simt_kernel(const Ch
   if (r < 0) return;  // behind the last request
   const RowRange rr = request_rows(a.qsl, r, a.T);
   const int n = rr.q1 - rr.q0, j = row - rr.q0;
-  const int64_t Lmax = static_cast<int64_t>(a.max_blocks) * a.bs;
-  int L = a.seq_len[r];
-  if (L < 0 || L > Lmax) {
-    if (tid == 0) set_status(a.status, PE_ST_BLOCK_RANGE);
-    L = static_cast<int>(min(max(static_cast<int64_t>(L), int64_t{0}), Lmax));
-  }
+  const int L = static_cast<int>(min(max(static_cast<int64_t>(a.seq_len[r]), int64_t{0}), Lmax));
   const int lim = L - n + j;  // the row's own position
   attend_row<T>(a, r, row, h, lim, sh);
 }
