@@ -60,6 +60,20 @@ int pe_test_projection(pe_handle* h, int which, const void* X, int n_rows, void*
  * word first (pe_read_status with clear set). */
 int pe_test_bounded_wait(void* ws, size_t ws_bytes, void* stream);
 
+/* The same for the tensor-core kernel of pe_chunk_attention (a bf16 plan with blocks of
+ * a multiple of 8 keys): the barrier of one slot of a CTA's key ring (slot 0..3) or value
+ * ring (4..7) expects one arrival more than is made, so the wait for the tile in that
+ * slot runs out (2 s).  Every warp leaves at its next wait or at the end of its unit,
+ * after the copies and products in flight, and PE_ST_TIMEOUT is set; out is then
+ * undefined.  A CTA whose part has fewer tiles than the slot's number does not stall.
+ * The other arguments are those of pe_chunk_attention. */
+int pe_test_chunk_attention_stall(const pe_attn_plan* plan, int slot, int B, int T, const int32_t* qsl,
+                                  const int32_t* seq_len, const void* q, int64_t ld_q,
+                                  const void* k_cache, const void* v_cache,
+                                  const int32_t* block_table, int max_blocks, int num_blocks,
+                                  const float* sink, void* out, int64_t ld_out, void* ws,
+                                  size_t ws_bytes, void* stream);
+
 /* Failure-detection check of the persistent decode layer (a bf16 one-layer step
  * of at most 16 rows): the byte of the step workspace that holds the count of
  * the layer's first kernel's completed launches within the step (uint32, zeroed

@@ -161,6 +161,9 @@ def load(path: str | None = None):
     lib.pe_chunk_attention.argtypes = [_vp, _i32, _i32, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp,
                                        _vp, _i32, _i32, _vp, _vp, ctypes.c_int64, _vp, _sz, _vp]
     lib.pe_chunk_attention.restype = _i32
+    args = lib.pe_chunk_attention.argtypes
+    lib.pe_test_chunk_attention_stall.argtypes = [args[0], _i32, *args[1:]]
+    lib.pe_test_chunk_attention_stall.restype = _i32
     _lib = lib
     return lib
 

@@ -10,6 +10,7 @@
 // (pe_chunk_attn_tc.cu) do not take: fp32 plans, and blocks that are no multiple of 8
 // keys.  One CTA per (row, query head).
 #include "pe_attn_row.cuh"
+#include "pe_testing.h"
 
 namespace pe {
 namespace {
@@ -58,13 +59,12 @@ extern "C" size_t pe_chunk_attention_workspace_bytes(const pe_attn_plan* plan, i
   return chunk_tc_takes(plan) ? chunk_tc_workspace(plan, max_rows) : 256;
 }
 
-extern "C" int pe_chunk_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qsl,
-                                  const int32_t* seq_len, const void* q, int64_t ld_q,
-                                  const void* k_cache, const void* v_cache,
-                                  const int32_t* block_table, int max_blocks, int num_blocks,
-                                  const float* sink, void* out, int64_t ld_out, void* ws,
-                                  size_t ws_bytes, void* stream) {
-  NvtxRange nvtx("pe_chunk_attention");
+namespace {
+
+int chunk_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qsl, const int32_t* seq_len,
+                    const void* q, int64_t ld_q, const void* k_cache, const void* v_cache,
+                    const int32_t* block_table, int max_blocks, int num_blocks, const float* sink, void* out,
+                    int64_t ld_out, void* ws, size_t ws_bytes, void* stream, int stall) {
   if (!plan_ok(plan) || B < 0 || T < 0 || max_blocks < 1 || num_blocks < 0) return PE_ERR_ARG;
   const int64_t width = static_cast<int64_t>(plan->n_heads) * plan->head_dim;
   if (ld_q < width || ld_out < width || ld_q % 8 || ld_out % 8) return PE_ERR_ARG;
@@ -104,10 +104,35 @@ extern "C" int pe_chunk_attention(const pe_attn_plan* plan, int B, int T, const 
   a.out = out;
   a.ld_out = ld_out;
   a.status = static_cast<uint32_t*>(ws);
+  a.stall = stall;
   if (chunk_tc_takes(plan) && num_blocks > 0) return launch_chunk_tc(a, static_cast<char*>(ws), st);
   const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(plan->n_heads));
   const cudaError_t e = plan->dtype == PE_DTYPE_BF16
                             ? launch_chained(chunk_simt_kernel<bf16>, grid, dim3(32 * kRowWarps), 0, st, a)
                             : launch_chained(chunk_simt_kernel<float>, grid, dim3(32 * kRowWarps), 0, st, a);
   return e == cudaSuccess ? PE_OK : PE_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" int pe_chunk_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qsl,
+                                  const int32_t* seq_len, const void* q, int64_t ld_q,
+                                  const void* k_cache, const void* v_cache,
+                                  const int32_t* block_table, int max_blocks, int num_blocks,
+                                  const float* sink, void* out, int64_t ld_out, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  NvtxRange nvtx("pe_chunk_attention");
+  return chunk_attention(plan, B, T, qsl, seq_len, q, ld_q, k_cache, v_cache, block_table, max_blocks,
+                         num_blocks, sink, out, ld_out, ws, ws_bytes, stream, 0);
+}
+
+extern "C" int pe_test_chunk_attention_stall(const pe_attn_plan* plan, int slot, int B, int T, const int32_t* qsl,
+                                             const int32_t* seq_len, const void* q, int64_t ld_q,
+                                             const void* k_cache, const void* v_cache,
+                                             const int32_t* block_table, int max_blocks, int num_blocks,
+                                             const float* sink, void* out, int64_t ld_out, void* ws,
+                                             size_t ws_bytes, void* stream) {
+  if (slot < 0 || slot > 7) return PE_ERR_ARG;
+  return chunk_attention(plan, B, T, qsl, seq_len, q, ld_q, k_cache, v_cache, block_table, max_blocks,
+                         num_blocks, sink, out, ld_out, ws, ws_bytes, stream, 1 + slot);
 }

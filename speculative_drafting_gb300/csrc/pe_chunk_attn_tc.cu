@@ -436,10 +436,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int HG = a.H / a.G;
 
   if (tid == 0) {
+    // (a stalled slot's barrier expects an arrival that no one makes)
     for (int i = 0; i < S::kSlots; ++i) {
-      mbar_init(&k_full[i], 1);
+      mbar_init(&k_full[i], a.stall == 1 + i ? 2 : 1);
       mbar_init(&k_empty[i], 2);
-      mbar_init(&v_full[i], 1);
+      mbar_init(&v_full[i], a.stall == 1 + S::kSlots + i ? 2 : 1);
       mbar_init(&v_empty[i], 2);
     }
     for (int i = 0; i < kItems; ++i) {

@@ -42,6 +42,7 @@ struct ChunkArgs {
   void* out;
   int64_t ld_out;
   uint32_t* status;
+  int stall;  // pe_test_chunk_attention_stall's, else 0
 };
 
 // The tensor-core kernels of pe_chunk_attention (bf16, blocks of a multiple of 8 keys).
