@@ -11,6 +11,7 @@ from oracle import pe_paged as P
 from parity import built, cuda_or_skip, host
 from speculative_drafting_gb300 import binding, runner, workloads as W
 from test_gpu_paged import _append, _attend, _check, _chunk, _store
+from test_gpu_verify_sampled import _run as _verify
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +62,109 @@ def test_attend_wait_runs_out_and_the_context_survives(H, G, hd, ns, Ls, slot):
     got, st = _attend(c, plan=plan, ws=ws)
     assert st == 0
     _check(c, got=got)
+
+
+# ------------------------------------------------------------------ long contexts and chunks
+
+
+@pytest.mark.parametrize("H,G,hd", [(8, 2, 64), (7, 1, 128), (4, 4, 64)])
+@pytest.mark.parametrize("n", [1, 8])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_attend_units_cut_into_more_parts_than_a_warp_has_lanes(H, G, hd, n, sinks):
+    """One request over 32K keys with few KV heads: 38 to 53 parts a unit by the split's
+    arithmetic, joined 32 at a time."""
+    _check(_chunk("bf16", H, G, hd, 16, (n,), (32768 + 5,), sinks=sinks, seed=60 + n, wide=2))
+
+
+@pytest.mark.parametrize("H,G,hd", [(8, 2, 64), (7, 1, 128)])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_attend_first_parts_without_keys(H, G, hd, sinks):
+    """The blocks of the first 24,000 of 32,768 keys are invalid: the first window of 32 parts
+    sees nothing, and its maximum stays at -inf."""
+
+    def edit(table, nb):
+        table[0, :1500] = -1
+
+    c = _chunk("bf16", H, G, hd, 16, (8,), (32768,), sinks=sinks, table_edit=edit, seed=62)
+    _check(c, expect_status=binding.PE_ST_BLOCK_RANGE)
+    # and nothing at all is there
+    c["table"][:] = -1
+    got, st = _attend(c)
+    assert st == binding.PE_ST_BLOCK_RANGE and (got == 0).all()
+
+
+@pytest.mark.parametrize("H,G,hd", [(8, 2, 64), (7, 1, 128)])
+def test_attend_infinities_over_many_parts(H, G, hd):
+    """A NaN value that only the last rows see, in a unit of many parts: the rows before it are
+    computed again over all their keys."""
+    n, L = 8, 32768
+    c = _chunk("bf16", H, G, hd, 16, (n,), (L,), seed=63)
+    clean = O.decode(c["vc"], "bf16")
+    vc = clean.copy()
+    vc[c["table"][0][(L - 2) // 16], :, (L - 2) % 16, 3] = np.nan  # seen by the last two rows
+    ref, spread = P.chunk_attention(c["qsl"], c["seq"], O.decode(c["q"], "bf16").reshape(n, H, hd),
+                                    O.decode(c["kc"], "bf16"), clean, c["table"])
+    c["vc"] = _store(vc, "bf16")
+    got, st = _attend(c)
+    assert st == 0
+    val = O.decode(host(got), "bf16").reshape(n, H, hd)
+    want = ref.copy()
+    want[n - 2:, :, 3] = np.nan
+    fin = np.isfinite(want)
+    np.testing.assert_array_equal(val[~fin], want[~fin])
+    assert (np.abs(val - ref)[fin] <= (2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 1e-4) * spread)[fin] + 1e-30).all()
+
+
+@pytest.mark.parametrize("dtype,H,G,hd,bs", [("bf16", 8, 2, 64, 16), ("bf16", 7, 1, 128, 32), ("bf16", 4, 2, 64, 5),
+                                             ("f32", 4, 2, 16, 4)])
+def test_attend_long_chunks_over_long_contexts(dtype, H, G, hd, bs):
+    _check(_chunk(dtype, H, G, hd, bs, (1100, 0, 601), (6000, 17, 5003), sinks=True, extra=3, seed=64))
+
+
+@pytest.mark.parametrize("dtype,H,G,hd,bs,T,norm", [("bf16", 64, 8, 64, 16, 2500, True), ("bf16", 32, 8, 128, 16, 1300, False),
+                                                    ("f32", 4, 2, 16, 4, 3001, True), ("f32", 6, 3, 40, 5, 2000, True)])
+def test_append_many_rows_without_q_out(dtype, H, G, hd, bs, T, norm):
+    """Rows past one walk of the CTAs, with the cache alone written."""
+    _append(T, H, G, hd, bs, dtype, norm, pos0=10 ** 5, want_q=False, seed=65)
+
+
+# ------------------------------------------------------------------ sampled verification
+
+
+@pytest.mark.parametrize("V,apart", [(5000, 1), (5000, 2048), (20000, 4096), (5003, 256), (5003, 1)])
+@pytest.mark.parametrize("lead", [2e-5, -2e-5, 0.0])
+def test_close_scores_of_one_thread_beside_a_rejected_largest_logit(V, apart, lead):
+    """The row's largest logit is the rejected draft's, and the two best of the others are read
+    by the same thread, `apart` tokens from each other, with scores 2e-5 apart or equal.  The
+    scores' terms are below 16: three fp32 roundings of 2^-24 * 16 each, 3e-6 at most."""
+    cuda_or_skip()
+    built()
+    lg = np.full((2, V), -np.inf, np.float32)
+    temp, draft, at = 0.05, 9, 1024
+    lg[0, draft] = 3.0
+    lg[0, at] = lg[0, at + apart] = 3.0 - 0.0625  # scores -1.25 beside the draft's 0: p(draft) = 0.64
+    gumbel = np.full((1, V), -50.0, np.float32)
+    gumbel[0, at], gumbel[0, at + apart], gumbel[0, draft] = 5.0, 5.0 + lead, 40.0
+    c = dict(qsl=np.array([0, 2], np.int32), tok=np.array([1, draft], np.int32), dtype="f32", V=V, logits=lg,
+             temp=np.array([temp], np.float32), u=np.array([0.0, 0.9], np.float32), gumbel=gumbel)
+    acc, bon, p, st = _verify(c)
+    assert st == 0 and acc.tolist() == [0] and abs(p[1] - 1 / (1 + 2 * np.exp(-1.25))) < 1e-6
+    assert bon.tolist() == [at + apart if lead > 0 else at]
+
+
+def test_infinite_noise_on_a_token_masked_with_the_types_lowest_value():
+    """Only a logit of -inf keeps a token with infinite noise from winning: a mask of the
+    type's lowest value does not, although (logit - max) / T is below fp32's range (the sum is
+    rounded once)."""
+    cuda_or_skip()
+    built()
+    for V in (64, 63):  # rows on and off the 16-byte grid
+        lg = np.zeros((1, V), np.float32)
+        lg[0, 7] = np.finfo(np.float32).min
+        gumbel = np.zeros((1, V), np.float32)
+        gumbel[0, 7], gumbel[0, 30] = np.inf, 1.0
+        c = dict(qsl=np.array([0, 1], np.int32), tok=np.array([0], np.int32), dtype="f32", V=V, logits=lg,
+                 temp=np.array([0.5], np.float32), u=np.zeros(1, np.float32), gumbel=gumbel)
+        assert _verify(c)[1].tolist() == [7]
+        gumbel[0, 7] = 100.0  # the largest finite noise does not lift it
+        assert _verify(c)[1].tolist() == [30]
