@@ -429,6 +429,8 @@ int pe_verify_greedy(int B, int T_in, const int32_t* qsl, const int32_t* tok,
  *   p_draft[T_in]  out, float, nullable: p_{j-1}(tok_j) of each row j >= 1 (for a
  *                  greedy request 1 or 0), also past the accepted prefix; 1 for
  *                  a request's row 0
+ *                  (p is formed in fp32, from fp32 exponentials and sums: off by less
+ *                  than 1e-5 p + 1e-7, and a u that near to it may fall on either side)
  *   ws             pe_verify_sampled_workspace_bytes(B, T_in, vocab) bytes or more,
  *                  256-byte aligned; its first word is the status word
  * A logit of -inf has probability 0.  A row with a NaN or a +inf logit, or with
