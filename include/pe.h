@@ -513,8 +513,10 @@ int pe_qkv_append(const pe_attn_plan* plan, int T, const void* qkv, int64_t ld_q
  *               own (from 0).  The caches already hold the chunk's keys and values
  *   q           [T][H][hd] in the plan's dtype, rows ld_q elements apart
  *   block_table [B][max_blocks], num_blocks: as for pe_draft_step
- *   sink[H]     float, nullable: per-head sink logits (pe_weights.attn_sink)
- *   out         [T][H][hd] in the plan's dtype, rows ld_out elements apart
+ *   sink[H]     float, nullable: per-head sink logits (pe_weights.attn_sink), finite or
+ *               -inf (no sink for that head); +inf and NaN give NaN where a row sees a key
+ *   out         [T][H][hd] in the plan's dtype, rows ld_out elements apart; must not
+ *               overlap an input (parts of a row's heads are read after others are written)
  *   ws          pe_chunk_attention_workspace_bytes(plan, B, T) bytes or more,
  *               256-byte aligned; its first word is the status word, which this call
  *               does not clear (zero it once; pe_read_status clears it)
@@ -524,6 +526,9 @@ int pe_qkv_append(const pe_attn_plan* plan, int T, const void* qkv, int64_t ld_q
  * see, or in blocks that are skipped, does not enter the row, NaN and infinities
  * included (bf16 rows are computed a second time, slowly, where a later position of
  * the chunk holds one in its value).
+ * The weighted sums of the values are formed before they are divided by the sum of the
+ * weights, the largest of which is at most 2^8: a finite value above 3.4e38 / (2^8 * keys)
+ * may give an infinite result.
  * seq_len outside [0, max_blocks * block_size] is clamped, a block id outside [0,
  * num_blocks) skips its keys: PE_ST_BLOCK_RANGE.  A qsl that is not a non-decreasing
  * run from 0 to at most T sets PE_ST_ROWS_RANGE; the rows of out are then undefined

@@ -47,7 +47,8 @@ constexpr int kItems = 4;         // unit descriptors in flight
 constexpr int kMasks = 16;        // tile masks in flight
 constexpr float kLog2e = 1.4426950408889634f;
 // The running maximum is raised only when a row's new one is more than 2^8 above
-// it: P stays below 2^8 (exact in the fp32 sums), and O is rarely rescaled.
+// it: O is rarely rescaled.  P is at most 2^8, so O of values below 2^120 / keys stays
+// finite; the sums round relatively, whatever the scale.
 constexpr float kLazy = 8.f;
 
 template <int HD>

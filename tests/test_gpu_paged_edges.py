@@ -121,6 +121,46 @@ def test_attend_long_chunks_over_long_contexts(dtype, H, G, hd, bs):
     _check(_chunk(dtype, H, G, hd, bs, (1100, 0, 601), (6000, 17, 5003), sinks=True, extra=3, seed=64))
 
 
+CALLS = [("bf16", 8, 2, 64, 16), ("bf16", 7, 1, 128, 16), ("bf16", 4, 2, 64, 5), ("f32", 4, 2, 16, 4)]
+
+
+@pytest.mark.parametrize("dtype,H,G,hd,bs", CALLS)
+def test_attend_large_values(dtype, H, G, hd, bs):
+    """Values up to the size that the header allows, 3.4e38 / (2^8 * keys), and scores that
+    climb by nearly 2^8 in weight before the running maximum follows."""
+    L = 700
+    c = _chunk(dtype, H, G, hd, bs, (5, 1), (L, 40), seed=66)
+    q, k, v = (O.decode(c[x], dtype) for x in ("q", "kc", "vc"))
+    q[:] = 1.0
+    t = np.arange(L)
+    at = c["table"][0][t // bs], slice(None), t % bs
+    k[at] = (np.minimum(t / 256.0, 1.0) * 5.4 / np.sqrt(hd))[:, None, None]  # s from 0 to 5.4 = 7.8 in log2
+    v *= 0.9 * 3.4e38 / (2.0 ** 8 * L) / np.abs(v).max()
+    c["q"], c["kc"], c["vc"] = _store(q, dtype), _store(k, dtype), _store(v, dtype)
+    assert np.abs(O.decode(c["vc"], dtype)).max() > 1e33
+    _check(c)
+
+
+@pytest.mark.parametrize("dtype,H,G,hd,bs", CALLS)
+def test_attend_sinks_that_are_not_finite(dtype, H, G, hd, bs):
+    """-inf: no sink for that head; +inf and NaN: NaN where a row sees a key, zeros where it
+    sees none.  A request in one part and one in several."""
+    ns, Ls = (3, 6, 8), (1, 90, 3000)  # the first two rows see nothing
+    c = _chunk(dtype, H, G, hd, bs, ns, Ls, sinks=True, seed=67)
+    c["sink"][0], c["sink"][1], c["sink"][2] = -np.inf, np.inf, np.nan
+    got, st = _attend(c)
+    assert st == 0
+    val = O.decode(host(got), dtype).reshape(c["T"], H, hd)
+    assert (val[:2] == 0).all() and np.isnan(val[2:, 1:3]).all()
+    q = O.decode(c["q"], dtype)[:, :H * hd].reshape(c["T"], H, hd)
+    sink = np.where(np.arange(H) < 3, -np.inf, c["sink"])
+    ref, spread = P.chunk_attention(c["qsl"], c["seq"], q, O.decode(c["kc"], dtype), O.decode(c["vc"], dtype),
+                                    c["table"], sink)
+    half, w = (2.0 ** -8, 2.0 ** -8 + 1e-4) if dtype == "bf16" else (2.0 ** -24, 2e-5)
+    ok = np.abs(val - ref) <= half * np.abs(ref) + w * spread + 1e-30
+    assert ok[:, 0].all() and ok[:, 3:].all()
+
+
 @pytest.mark.parametrize("dtype,H,G,hd,bs,T,norm", [("bf16", 64, 8, 64, 16, 2500, True), ("bf16", 32, 8, 128, 16, 1300, False),
                                                     ("f32", 4, 2, 16, 4, 3001, True), ("f32", 6, 3, 40, 5, 2000, True)])
 def test_append_many_rows_without_q_out(dtype, H, G, hd, bs, T, norm):
