@@ -520,7 +520,10 @@ int pe_qkv_append(const pe_attn_plan* plan, int T, const void* qkv, int64_t ld_q
  *   ws          pe_chunk_attention_workspace_bytes(plan, B, T) bytes or more,
  *               256-byte aligned; its first word is the status word, which this call
  *               does not clear (zero it once; pe_read_status clears it)
- * Scores are scaled by 1/sqrt(hd); the softmax and its sums are fp32.  A row whose
+ * Scores are scaled by 1/sqrt(hd); the softmax and its sums are fp32.  A bf16 plan with
+ * blocks of a multiple of 8 keys rounds each weight to bf16 (relative 2^-8 at most) before
+ * its product with the value, so a result is off by up to 2^-8 of sum p |v| beside its own
+ * rounding (pe_draft_step's attention carries its weights in two bf16 parts).  A row whose
  * position is negative (seq_len[r] < n_r) or whose keys all lie in invalid blocks
  * sees nothing and gets zeros.  What the caches hold at positions that a row does not
  * see, or in blocks that are skipped, does not enter the row, NaN and infinities

@@ -824,7 +824,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             p1 = ex2(p1);
             ls = add_f32x2(ls, pack_f32x2(p0, p1));
             // P enters the product as bf16 (relative 2^-8 at most, the size of the
-            // result's own rounding); the sum l takes the unrounded weights
+            // result's own rounding); the sum l takes the unrounded weights.  (Low parts in a
+            // second product, in units of at most 128 rows only: error against 64 bits 0.0023
+            // -> 0.0017, 64 x 8 rows 110 -> 187 us, one token 17.2 -> 19.4, 32K 610 -> 642.
+            // Tensor memory is full at head size 64: the low parts take S's place.)
             x[c >> 1] = pack_bf16x2(p0, p1);
           }
           float l0, l1;
