@@ -70,7 +70,7 @@ struct Shape {
   // and P: two S buffers of a 64-key tile that the steps take in turn, with P in the
   // place of its S, free after P V.  (With one S of 128 keys, the next product waiting for
   // P V, the softmax warps waited for S two fifths of their time: mixed chunks 534 us,
-  // 486 like this.)
+  // 478 like this.)
   static constexpr bool kOverlay = HD == 128;
   static constexpr uint32_t kS = 0, kP = kOverlay ? 0 : 256, kPStride = kOverlay ? 128 : 64;
   static constexpr uint32_t kO = HD == 64 ? 384 : 256;
