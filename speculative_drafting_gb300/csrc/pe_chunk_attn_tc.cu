@@ -194,27 +194,6 @@ PE_DEV void load_box(void* dst, const CUtensorMap* map, uint64_t* bar, int row, 
   }
 }
 
-// Two fp32 values in one 64-bit register, for the paired fp32 instructions (half the
-// issue slots).
-PE_DEV uint64_t pack_f32x2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-PE_DEV void unpack_f32x2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-PE_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-PE_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // One lane of a whole warp, the same one every time.
 PE_DEV bool elect_one() {
   uint32_t p;
@@ -224,12 +203,6 @@ PE_DEV bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(p));
   return p != 0;
-}
-
-PE_DEV float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // `zero`, with NaN in it if one of the eight values is not finite
