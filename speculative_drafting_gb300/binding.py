@@ -223,8 +223,11 @@ def _row_stride(t, T, heads, hd):
         dense, width = s[2] == 1 and (s[1] == hd or n[1] == 1), n[1] * n[2]
     elif len(s) == 2:
         dense, width = s[1] == 1, n[1]
-    else:
-        raise ValueError(f"a tensor of shape {tuple(n)}: rows of {heads} heads have two or three dimensions, dense")
+    else:  # [T][G][H/G][hd] and the like
+        dense, width = True, 1
+        for size, stride in zip(reversed(n[1:]), reversed(s[1:])):
+            dense = dense and (stride == width or size == 1)
+            width *= size
     if not dense:
         raise ValueError(f"rows of shape {tuple(n[1:])} with strides {s}: a row has to be dense")
     if n[0] < T or width < heads * hd:

@@ -188,3 +188,16 @@ def test_tensors_of_another_device_than_the_workspace_are_refused(calls, monkeyp
     assert len(tensors) >= 9
     refused(calls, lambda **kw: make(**{**given, **kw}) if kw else None,
             *(dict([(k, given[k].as_subclass(Elsewhere))]) for k in tensors))
+
+
+def test_rows_of_more_dimensions_are_taken_where_they_are_dense(calls):
+    """Heads by KV head, as a model may hold them: [T][G][H/G][hd]."""
+    bf = dict(dtype=BF)
+    attend(q=torch.zeros(T, G, H // G, HD, **bf), out=torch.zeros(T + 1, G, H // G, HD, **bf)[:T])
+    append(qkv=torch.zeros(T, (H + 2 * G) // 2, 2, HD, **bf), q_out=torch.zeros(T, G, H // G, HD, **bf))
+    assert [a[1][6] for a in calls.made[:1]] == [H * HD] and calls.made[1][1][3] == (H + 2 * G) * HD
+    calls.made.clear()
+    wide = torch.zeros(T, G, H // G, 2 * HD, **bf)
+    refused(calls, attend, dict(q=wide[..., :HD]), dict(q=wide[..., ::2]), dict(out=wide[..., :HD]),
+            dict(q=torch.zeros(T, H // G, G, HD, **bf).transpose(1, 2)), dict(q=torch.zeros(T, 1, G, HD, **bf)),
+            dict(q=torch.zeros(T - 1, G, H // G, HD, **bf)))
