@@ -30,6 +30,12 @@
  *                      the paged cache write (with per-head norms and RoPE) and
  *                      attention over the pages for rows outside a draft step:
  *                      prompts, chunks of prompts, the target's verify rows.
+ *   pe_tree_layout, pe_tree_attention, pe_sample, pe_tree_accept, pe_cache_compact
+ *                      verification of a tree of drafts: masks and positions, attention,
+ *                      the target's tokens (temperature, top-k, top-p, min-p), the walk
+ *                      along them, and the accepted nodes moved behind their context.
+ *   pe_pages_reserve, pe_pages_fork, pe_pages_free, pe_cache_copy
+ *                      the cache's pages: given to requests, shared, given back, copied.
  *   pe_draft_autoregressive
  *                      the K-pass autoregressive drafting the parallel step
  *                      replaces, on the same kernels (the baseline).
@@ -102,7 +108,15 @@ extern "C" {
 #define PE_ST_TIMEOUT 0x10u       /* a bounded wait inside a kernel expired */
 #define PE_ST_SAMPLING 0x40u      /* pe_verify_sampled: a temperature that is negative
                                      or NaN (read as 0), or a bonus token due from a
-                                     row without a distribution (bonus -1) */
+                                     row without a distribution (bonus -1); pe_sample:
+                                     the same, and a top_p or min_p that is NaN */
+#define PE_ST_TREE 0x80u          /* tree calls: a parent that is no earlier node (read as
+                                     -1), more nodes than the masks have bits or than
+                                     PE_TREE_MAX_NODES, a path that does not ascend
+                                     (nothing of the request is moved) */
+#define PE_ST_PAGES 0x100u        /* page calls: an entry that is refused (its row or length
+                                     out of range, named twice, not empty, not there), no
+                                     free page left, a page given back that was free */
 #define PE_ST_CAPACITY 0x20u      /* COD calls: a sequence length outside [0, S_max]
                                      (clamped), a mask larger than its row capacity
                                      or row stride (rows / columns past it are not
@@ -546,6 +560,175 @@ int pe_chunk_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qs
                        const void* v_cache, const int32_t* block_table, int max_blocks,
                        int num_blocks, const float* sink, void* out, int64_t ld_out, void* ws,
                        size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- trees of drafts
+ * Verification of several candidates a position: the rows of a request in the verify batch
+ * are the nodes of a tree.  Row 0 is the root, the last committed token; parent[j] is the
+ * row, within the request, that node j follows: an earlier one, or -1 for a node right
+ * behind the context (the root's).  With ctx = seq_len - n positions in the cache before
+ * them, node j stands at position ctx + its depth and its keys and values lie at cache
+ * position ctx + j (siblings share a position, not a slot).  A round:
+ *   pe_tree_layout -> (per layer) pe_qkv_append, pe_tree_attention -> pe_sample or the
+ *   greedy token of each row -> pe_tree_accept -> pe_cache_compact
+ * A chain of drafts (parent[j] = j - 1) gives what the calls without a tree give.  With
+ * pe_sample's tokens as targets the walk is rejection sampling of greedy drafts: a node's
+ * child is accepted with its probability, and the token after the path is drawn from what
+ * the rejected children leave. */
+#define PE_TREE_MAX_NODES 1024
+
+/* Masks, positions and slots of the nodes, once per verify batch.
+ *   qsl[B+1], seq_len[B], block_table[B][max_blocks], num_blocks: as for
+ *               pe_chunk_attention (seq_len counts all nodes)
+ *   parent[T]   int32
+ *   mask        out [T][words] uint32: bit i of a row's words (bit i % 32 of word i / 32)
+ *               is set if node i is the row's own or one of its ancestors; 1 <= words <=
+ *               PE_TREE_MAX_NODES / 32
+ *   pos[T]      out, int64, nullable: ctx + depth
+ *   slot[T]     out, int64, nullable: the slot of cache position ctx + j; -1 and
+ *               PE_ST_BLOCK_RANGE where the block table has no valid block for it
+ *   ws          256 bytes or more, 256-byte aligned: the status word, which this call does
+ *               not clear (zero it once; pe_read_status clears it)
+ * Nodes from 32 * words on (PE_ST_TREE) get an empty mask, depth 0 and slot -1.  Rows from
+ * qsl[B] on are not written.  PE_ST_ROWS_RANGE as for pe_chunk_attention.  PE_ERR_ARG:
+ * negative sizes, words, max_blocks or block_size out of range, null or misaligned
+ * pointers, ws too small, B = 0 with T > 0.  PE_ERR_UNSUPPORTED: B > 65535. */
+int pe_tree_layout(int B, int T, const int32_t* qsl, const int32_t* seq_len, const int32_t* parent,
+                   const int32_t* block_table, int max_blocks, int num_blocks, int block_size,
+                   uint32_t* mask, int words, int64_t* pos, int64_t* slot, void* ws, size_t ws_bytes,
+                   void* stream);
+
+/* pe_chunk_attention for nodes: row j of request r sees every cache position before
+ * seq_len[r] - n_r, and of the request's own rows i, at position seq_len[r] - n_r + i,
+ * those whose bit is set in its row of mask (any set of them, not a tree's alone; its own
+ * is not implied).  Rows i >= 32 * words are seen by none (PE_ST_TREE).  Every other
+ * argument, result and error is pe_chunk_attention's, and so is the workspace.  PE_ERR_ARG
+ * also: words out of range, mask null or misaligned. */
+int pe_tree_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qsl,
+                      const int32_t* seq_len, const void* q, int64_t ld_q, const void* k_cache,
+                      const void* v_cache, const int32_t* block_table, int max_blocks,
+                      int num_blocks, const uint32_t* mask, int words, const float* sink, void* out,
+                      int64_t ld_out, void* ws, size_t ws_bytes, void* stream);
+
+/* The walk: from row 0 of a request on to the first child (lowest row) whose token is the
+ * target's token after the node, until there is none.
+ *   tok[T], target[T]  int32: each row's own token, and the target's after it (a negative
+ *                one is no token: the walk ends there)
+ *   accepted[B]  out: nodes accepted behind the root
+ *   path[T]      out: row qsl[r] + d holds the d-th node of the path (d = 0: the root, row
+ *                0), d <= accepted[r]; -1 behind it
+ *   bonus[B]     out: the target's token after the path's last node
+ *   ws           as for pe_tree_layout
+ * A request with no rows gets accepted 0 and bonus -1.  Rows from PE_TREE_MAX_NODES on are
+ * not walked to (PE_ST_TREE).  Errors as for pe_tree_layout. */
+int pe_tree_accept(int B, int T, const int32_t* qsl, const int32_t* parent, const int32_t* tok,
+                   const int32_t* target, int32_t* accepted, int32_t* path, int32_t* bonus,
+                   void* ws, size_t ws_bytes, void* stream);
+
+/* The accepted nodes' keys and values moved to the cache positions right behind the context:
+ * of each request, cache position ctx + path[d] to ctx + d for d = 1..accepted, in order, in
+ * every layer (the keys keep the rotation of their position, which is ctx + d).
+ *   accepted[B], path[T]: of pe_tree_accept.  accepted outside [0, n_r - 1] is clamped
+ *               (PE_ST_ACCEPTED_RANGE); a request whose path does not ascend from above 0
+ *               to below n_r is left as it is (PE_ST_TREE)
+ *   k_cache, v_cache  [n_layers][num_blocks][G][block_size][hd], as for pe_draft_step
+ *   ws          as for pe_qkv_append
+ * A position without a valid block is not moved and not written (PE_ST_BLOCK_RANGE).  No
+ * page may be in two requests at the positions of their nodes: what it holds then is
+ * undefined.  Every other byte of the caches stays.  PE_ERR_ARG: a plan that
+ * pe_attn_plan_init did not fill, n_layers < 1, else as for pe_chunk_attention. */
+int pe_cache_compact(const pe_attn_plan* plan, int n_layers, int B, int T, const int32_t* qsl,
+                     const int32_t* seq_len, const int32_t* accepted, const int32_t* path,
+                     const int32_t* block_table, int max_blocks, int num_blocks, void* k_cache,
+                     void* v_cache, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- sampling
+ * The target's token after each row, from given random numbers.  Needs no handle.
+ *   qsl[B+1], dtype, temperature[B]: as for pe_verify_sampled; row t of request r takes the
+ *               request's settings
+ *   logits      [T][vocab] in dtype, consecutive rows ld_logits elements apart; rows need no
+ *               particular alignment beyond the element size
+ *   top_k[B]    int32, nullable: the number of tokens kept; 0, negative or vocab and more: all
+ *   top_p[B]    float, nullable: 1 and more: all; 0 and less: the first token; NaN: all,
+ *               PE_ST_SAMPLING
+ *   min_p[B]    float, nullable: 0 and less: all; NaN: all, PE_ST_SAMPLING
+ *   gumbel      [T][vocab] float standard Gumbel noise, rows ld_gumbel elements apart.  Only
+ *               the noise of kept tokens is looked at
+ *   token[T]    out
+ *   ws          pe_sample_workspace_bytes(B, T, vocab) bytes or more, 256-byte aligned; its
+ *               first word is the status word, which this call does not clear (zero it
+ *               once; pe_read_status clears it)
+ * In the order of the logits, largest first, the lower index first among equal ones, with
+ * weights w = exp((logit - largest) / temperature):
+ *   - the first top_k tokens are kept;
+ *   - of those, the ones with less than top_p times their sum of w before them (the first
+ *     one always);
+ *   - of those, the ones with w >= min_p (of the first: always).
+ * token = argmax over the kept ones of (logit - largest) / temperature + gumbel, the lowest
+ * index on ties: a draw from the kept tokens' probabilities.  Temperature 0: the largest
+ * logit's, by pe_verify_greedy's rules.  Sums and weights are formed in fp32 or more: a
+ * token whose sum before it, or w, is within 1e-6 of the bound may fall on either side;
+ * two scores within a few fp32 roundings may trade places.
+ * A logit of -inf is never kept.  A row with a NaN or +inf logit, with nothing but -inf, or
+ * whose kept tokens all have noise of -inf or NaN gets token -1 and PE_ST_SAMPLING (at
+ * temperature 0 pe_verify_greedy's rules hold for such rows).  Rows from qsl[B] on are neither
+ * used nor written; PE_ST_ROWS_RANGE as for pe_verify_sampled.  PE_ERR_ARG: negative
+ * sizes, vocab < 1, strides below vocab, null pointers, tensors not aligned to their element
+ * size, ws misaligned or too small, B = 0 with T > 0.  PE_ERR_UNSUPPORTED: B > 65535,
+ * vocab > 2^24, a dtype other than the two. */
+size_t pe_sample_workspace_bytes(int max_batch, int max_rows, int vocab);
+int pe_sample(int B, int T, const int32_t* qsl, const void* logits, int64_t ld_logits, int vocab,
+              int dtype, const float* temperature, const int32_t* top_k, const float* top_p,
+              const float* min_p, const float* gumbel, int64_t ld_gumbel, int32_t* token, void* ws,
+              size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- pages
+ * A pool of pages on the device.  block_table [rows][max_blocks] int32 holds each row's pages,
+ * in order, negative where it has none; refs[num_blocks] int32 counts the entries that name a
+ * page, 0: it is free.  The host sets them up (all entries -1, all counts 0, or its own
+ * state); from then on the calls below change both, in the order of the stream, so a
+ * captured loop may grow, share and drop requests.  Free pages are handed out in ascending order to the
+ * entries of a call in order: the outcome does not depend on the run.
+ *   ws          pe_pages_workspace_bytes(n, num_blocks) bytes or more, 256-byte aligned,
+ *               zeroed once; its first word is the status word, which the calls do not clear
+ * An entry that is refused changes nothing and sets PE_ST_PAGES. */
+size_t pe_pages_workspace_bytes(int max_entries, int num_blocks);
+
+/* Pages for n rows: row[i] of the table gets one for every negative entry among its first
+ * ceil(length[i] / block_size).  Refused: a row out of range or named twice, a length below 0
+ * or above max_blocks * block_size.  Rows are served in order; the first whose pages are not
+ * there, and all later ones that need some, are refused.  PE_ERR_ARG: negative n, rows or
+ * num_blocks, max_blocks or block_size < 1, null or misaligned pointers, ws. */
+int pe_pages_reserve(int n, const int32_t* row, const int32_t* length, int32_t* block_table,
+                     int rows, int max_blocks, int num_blocks, int block_size, int32_t* refs,
+                     void* ws, size_t ws_bytes, void* stream);
+
+/* n rows that share the first length[i] positions of another: row child[i] gets the pages of
+ * row parent[i] that those fill, counted once more, and where length[i] is no multiple of
+ * block_size a page of its own with a copy of the rest (the first length[i] % block_size
+ * positions of the parent's page, in every layer, keys and values).  Refused: a row out of
+ * range, a child that is not empty, is named twice or is some entry's parent, a length as for
+ * pe_pages_reserve, a parent without valid, counted pages for it; for want of a free page as
+ * there.  PE_ERR_ARG as there, and a plan that pe_attn_plan_init did not fill, n_layers < 1,
+ * caches null or not 16-byte aligned.  PE_ERR_UNSUPPORTED: n > 65535. */
+int pe_pages_fork(const pe_attn_plan* plan, int n_layers, int n, const int32_t* parent,
+                  const int32_t* child, const int32_t* length, int32_t* block_table, int rows,
+                  int max_blocks, int num_blocks, int32_t* refs, void* k_cache, void* v_cache,
+                  void* ws, size_t ws_bytes, void* stream);
+
+/* n rows give their pages back: every entry of the row becomes -1 and its page's count falls by
+ * one (a row named twice gives them back once).  A row out of range is refused; an entry
+ * outside [0, num_blocks) is dropped (PE_ST_BLOCK_RANGE), and a page whose count is 0 keeps it
+ * (PE_ST_PAGES).  ws: 256 bytes or more serve.  PE_ERR_ARG as for pe_pages_reserve. */
+int pe_pages_free(int n, const int32_t* row, int32_t* block_table, int rows, int max_blocks,
+                  int num_blocks, int32_t* refs, void* ws, size_t ws_bytes, void* stream);
+
+/* Pages copied: page src[i] to page dst[i] in every layer, keys and values.  The pages of dst
+ * must differ from one another and from those of src: what such a page holds is undefined
+ * (src[i] = dst[i] does nothing).  An entry outside [0, num_blocks) is skipped
+ * (PE_ST_BLOCK_RANGE).  ws as for pe_qkv_append.  PE_ERR_ARG as for pe_pages_fork. */
+int pe_cache_copy(const pe_attn_plan* plan, int n_layers, int n, const int32_t* src,
+                  const int32_t* dst, int num_blocks, void* k_cache, void* v_cache, void* ws,
+                  size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- COD training indices
  * "[RFC]: Add random anchor for p-eagle first position": the training-side

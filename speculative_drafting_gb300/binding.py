@@ -27,6 +27,9 @@ PE_ST_ROWS_RANGE = 0x8
 PE_ST_TIMEOUT = 0x10
 PE_ST_CAPACITY = 0x20
 PE_ST_SAMPLING = 0x40
+PE_ST_TREE = 0x80
+PE_ST_PAGES = 0x100
+PE_TREE_MAX_NODES = 1024
 PE_COD_MAX_DEPTH = 16
 PE_DTYPE_F32 = 0
 PE_DTYPE_BF16 = 1
@@ -164,6 +167,31 @@ def load(path: str | None = None):
     args = lib.pe_chunk_attention.argtypes
     lib.pe_test_chunk_attention_stall.argtypes = [args[0], _i32, *args[1:]]
     lib.pe_test_chunk_attention_stall.restype = _i32
+    lib.pe_tree_layout.argtypes = [_i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp,
+                                   _vp, _vp, _sz, _vp]
+    lib.pe_tree_layout.restype = _i32
+    lib.pe_tree_attention.argtypes = [*args[:12], _vp, _i32, *args[12:]]
+    lib.pe_tree_attention.restype = _i32
+    lib.pe_tree_accept.argtypes = [_i32, _i32, *[_vp] * 8, _sz, _vp]
+    lib.pe_tree_accept.restype = _i32
+    lib.pe_sample_workspace_bytes.argtypes = [_i32, _i32, _i32]
+    lib.pe_sample_workspace_bytes.restype = _sz
+    lib.pe_sample.argtypes = [_i32, _i32, _vp, _vp, ctypes.c_int64, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
+                              ctypes.c_int64, _vp, _vp, _sz, _vp]
+    lib.pe_sample.restype = _i32
+    lib.pe_cache_compact.argtypes = [_vp, _i32, _i32, _i32, *[_vp] * 5, _i32, _i32, _vp, _vp, _vp, _sz, _vp]
+    lib.pe_cache_compact.restype = _i32
+    lib.pe_cache_copy.argtypes = [_vp, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _sz, _vp]
+    lib.pe_cache_copy.restype = _i32
+    lib.pe_pages_workspace_bytes.argtypes = [_i32, _i32]
+    lib.pe_pages_workspace_bytes.restype = _sz
+    lib.pe_pages_reserve.argtypes = [_i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _sz, _vp]
+    lib.pe_pages_reserve.restype = _i32
+    lib.pe_pages_fork.argtypes = [_vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                                  _sz, _vp]
+    lib.pe_pages_fork.restype = _i32
+    lib.pe_pages_free.argtypes = [_i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _sz, _vp]
+    lib.pe_pages_free.restype = _i32
     _lib = lib
     return lib
 
@@ -496,6 +524,129 @@ def verify_sampled(B, T_in, qsl, tok, logits, vocab, dtype, temperature, u, gumb
     _check(rc, "pe_verify_sampled")
 
 
+def _dense(ws, what, n, t, ty):
+    """`what` with at least n dense elements of the type ty, on the workspace's device."""
+    if t.get_device() != ws.get_device():
+        raise ValueError(f"{what} is on device {t.get_device()}, ws on {ws.get_device()}")
+    if not (t.dtype is ty and t.numel() >= n and t.is_contiguous()):
+        raise ValueError(f"{what}: {n} dense elements of the type {ty} are read or written, "
+                         f"got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _table(ws, t, rows, i32):
+    """A block table [rows or more][max_blocks]."""
+    if t.dim() != 2 or t.shape[0] < rows:
+        raise ValueError(f"block_table has the shape {tuple(t.shape)}, {rows} rows are read")
+    return _dense(ws, "block_table", t.numel(), t, i32)
+
+
+def _rows_of(ws, what, t, T, width, ty):
+    """Elements from one of T rows of `width` dense elements of the type ty to the next."""
+    if t.get_device() != ws.get_device():
+        raise ValueError(f"{what} is on device {t.get_device()}, ws on {ws.get_device()}")
+    if not (t.dtype is ty and t.dim() == 2 and t.shape[0] >= T and t.shape[1] >= width
+            and (t.stride(1) == 1 or width == 1)):
+        raise ValueError(f"{what}: {T} rows of {width} elements of the type {ty} are read, got {t.dtype} "
+                         f"{tuple(t.shape)} strides {t.stride()}")
+    return max(t.stride(0), width) if T <= 1 else t.stride(0)
+
+
+def sample_workspace(max_batch: int, max_rows: int, vocab: int, device="cuda"):
+    """A device workspace for pe_sample (zeroed; torch allocates it 256-byte aligned)."""
+    import torch
+
+    n = int(load().pe_sample_workspace_bytes(int(max_batch), int(max_rows), int(vocab)))
+    if n == 0:
+        raise PeError(PE_ERR_ARG, "pe_sample_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def sample(B, T, qsl, logits, vocab, temperature, top_k, top_p, min_p, gumbel, token, ws, stream=None):
+    """pe_sample on device tensors: logits [T][vocab] float32 or bfloat16 and gumbel [T][vocab]
+    float32, whose rows may be strided; qsl, top_k and token are int32, the settings float32, one
+    each a request; temperature, top_k, top_p and min_p may be None."""
+    f32, bf16, i32 = _types()
+    ld = _rows_of(ws, "logits", logits, T, vocab, bf16 if logits.dtype is bf16 else f32)
+    ldg = _rows_of(ws, "gumbel", gumbel, T, vocab, f32)
+    rc = load().pe_sample(
+        B, T, _dense(ws, "qsl", B and B + 1, qsl, i32), logits.data_ptr(), ld, vocab,
+        PE_DTYPE_BF16 if logits.dtype is bf16 else PE_DTYPE_F32,
+        None if temperature is None else _dense(ws, "temperature", B, temperature, f32),
+        None if top_k is None else _dense(ws, "top_k", B, top_k, i32),
+        None if top_p is None else _dense(ws, "top_p", B, top_p, f32),
+        None if min_p is None else _dense(ws, "min_p", B, min_p, f32), gumbel.data_ptr(), ldg,
+        _dense(ws, "token", T, token, i32), ws.data_ptr(), ws.numel(), _stream_handle(stream, ws))
+    _check(rc, "pe_sample")
+
+
+# ----------------------------------------------------------------------------- trees of drafts
+
+
+def tree_layout(B, T, qsl, seq_len, parent, block_table, num_blocks, block_size, mask, pos, slot, ws,
+                stream=None):
+    """pe_tree_layout: mask [T][words] int32 (the bits of uint32 words); pos and slot int64, each
+    may be None; the others int32.  ws: any zeroed workspace of 256 bytes or more."""
+    import torch
+
+    i32, i64 = torch.int32, torch.int64
+    if mask.dim() != 2 or mask.shape[0] < T:
+        raise ValueError(f"mask has the shape {tuple(mask.shape)}, {T} rows are written")
+    rc = load().pe_tree_layout(
+        B, T, _dense(ws, "qsl", B and B + 1, qsl, i32), _dense(ws, "seq_len", B, seq_len, i32),
+        _dense(ws, "parent", T, parent, i32), _table(ws, block_table, B, i32), block_table.shape[1], num_blocks,
+        block_size, _dense(ws, "mask", mask.numel(), mask, i32), mask.shape[1],
+        None if pos is None else _dense(ws, "pos", T, pos, i64),
+        None if slot is None else _dense(ws, "slot", T, slot, i64), ws.data_ptr(), ws.numel(),
+        _stream_handle(stream, ws))
+    _check(rc, "pe_tree_layout")
+
+
+def tree_accept(B, T, qsl, parent, tok, target, accepted, path, bonus, ws, stream=None):
+    """pe_tree_accept on int32 tensors.  ws: any zeroed workspace of 256 bytes or more."""
+    i32 = _types()[2]
+    rc = load().pe_tree_accept(
+        B, T, _dense(ws, "qsl", B and B + 1, qsl, i32), _dense(ws, "parent", T, parent, i32),
+        _dense(ws, "tok", T, tok, i32), _dense(ws, "target", T, target, i32),
+        _dense(ws, "accepted", B, accepted, i32), _dense(ws, "path", T, path, i32),
+        _dense(ws, "bonus", B, bonus, i32), ws.data_ptr(), ws.numel(), _stream_handle(stream, ws))
+    _check(rc, "pe_tree_accept")
+
+
+# ----------------------------------------------------------------------------- pages of a cache
+
+
+def pages_workspace(max_entries: int, num_blocks: int, device="cuda"):
+    """A device workspace for the page calls (zeroed): at most max_entries entries a call."""
+    import torch
+
+    n = int(load().pe_pages_workspace_bytes(int(max_entries), int(num_blocks)))
+    if n == 0:
+        raise PeError(PE_ERR_ARG, "pe_pages_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def pages_reserve(n, row, length, block_table, refs, block_size, ws, stream=None):
+    """pe_pages_reserve: rows row[i] of block_table get pages for length[i] positions; refs counts
+    the uses of each page (num_blocks of them).  All int32."""
+    i32 = _types()[2]
+    rc = load().pe_pages_reserve(
+        n, _dense(ws, "row", n, row, i32), _dense(ws, "length", n, length, i32),
+        _table(ws, block_table, 0, i32), block_table.shape[0], block_table.shape[1], refs.numel(), block_size,
+        _dense(ws, "refs", 0, refs, i32), ws.data_ptr(), ws.numel(), _stream_handle(stream, ws))
+    _check(rc, "pe_pages_reserve")
+
+
+def pages_free(n, row, block_table, refs, ws, stream=None):
+    """pe_pages_free: rows row[i] of block_table give their pages back.  All int32."""
+    i32 = _types()[2]
+    rc = load().pe_pages_free(
+        n, _dense(ws, "row", n, row, i32), _table(ws, block_table, 0, i32), block_table.shape[0],
+        block_table.shape[1], refs.numel(), _dense(ws, "refs", 0, refs, i32), ws.data_ptr(), ws.numel(),
+        _stream_handle(stream, ws))
+    _check(rc, "pe_pages_free")
+
+
 # ----------------------------------------------------------------------------- paged attention calls
 
 
@@ -595,6 +746,30 @@ class PagedAttention:
                sink=None, stream=None):
         """pe_chunk_attention: q and out [T][H][hd] (or [T][H hd]; their rows may be
         strided)."""
+        self._attend_checks(B, T, qsl, seq_len, q, k_cache, v_cache, block_table, num_blocks, out, ws, sink)
+        rc = self.lib.pe_chunk_attention(self.addr, B, T, qsl.data_ptr(), seq_len.data_ptr(), q.data_ptr(),
+                                         _row_stride(q, T, self.heads, self.hd), k_cache.data_ptr(), v_cache.data_ptr(),
+                                         block_table.data_ptr(), block_table.shape[1], num_blocks,
+                                         _addr(sink), out.data_ptr(), _row_stride(out, T, self.heads, self.hd), ws.data_ptr(),
+                                         ws.numel(), _stream_handle(stream, ws))
+        _check(rc, "pe_chunk_attention")
+
+    def attend_tree(self, B, T, qsl, seq_len, q, k_cache, v_cache, block_table, num_blocks, mask, out, ws,
+                    sink=None, stream=None):
+        """pe_tree_attention: as ``attend`` for rows that are nodes, with their masks [T][words]
+        int32 (of ``tree_layout``)."""
+        self._attend_checks(B, T, qsl, seq_len, q, k_cache, v_cache, block_table, num_blocks, out, ws, sink)
+        if mask.dim() != 2 or mask.shape[0] < T:
+            raise ValueError(f"mask has the shape {tuple(mask.shape)}, {T} rows are read")
+        rc = self.lib.pe_tree_attention(self.addr, B, T, qsl.data_ptr(), seq_len.data_ptr(), q.data_ptr(),
+                                        _row_stride(q, T, self.heads, self.hd), k_cache.data_ptr(), v_cache.data_ptr(),
+                                        block_table.data_ptr(), block_table.shape[1], num_blocks,
+                                        _dense(ws, "mask", mask.numel(), mask, self.i32), mask.shape[1],
+                                        _addr(sink), out.data_ptr(), _row_stride(out, T, self.heads, self.hd), ws.data_ptr(),
+                                        ws.numel(), _stream_handle(stream, ws))
+        _check(rc, "pe_tree_attention")
+
+    def _attend_checks(self, B, T, qsl, seq_len, q, k_cache, v_cache, block_table, num_blocks, out, ws, sink):
         d = self.dtype
         if not (q.dtype is d and k_cache.dtype is d and v_cache.dtype is d and out.dtype is d
                 and k_cache.is_contiguous() and v_cache.is_contiguous() and block_table.is_contiguous()):
@@ -614,12 +789,41 @@ class PagedAttention:
                 == v_cache.get_device() == block_table.get_device() == out.get_device()
                 == (ws if sink is None else sink).get_device()):
             self._apart(ws, qsl, seq_len, q, k_cache, v_cache, block_table, out, sink)
-        rc = self.lib.pe_chunk_attention(self.addr, B, T, qsl.data_ptr(), seq_len.data_ptr(), q.data_ptr(),
-                                         _row_stride(q, T, self.heads, self.hd), k_cache.data_ptr(), v_cache.data_ptr(),
-                                         block_table.data_ptr(), block_table.shape[1], num_blocks,
-                                         _addr(sink), out.data_ptr(), _row_stride(out, T, self.heads, self.hd), ws.data_ptr(),
-                                         ws.numel(), _stream_handle(stream, ws))
-        _check(rc, "pe_chunk_attention")
+    def _layers(self, n_layers, num_blocks, ws, *caches):
+        """Caches of n_layers layers, back to back."""
+        return [_dense(ws, "a cache", n_layers * num_blocks * self.block, c, self.dtype) for c in caches]
+
+    def compact(self, n_layers, B, T, qsl, seq_len, accepted, path, block_table, num_blocks, k_cache, v_cache,
+                ws, stream=None):
+        """pe_cache_compact: caches [n_layers][num_blocks][G][block_size][hd]; the others int32."""
+        i32 = self.i32
+        k, v = self._layers(n_layers, num_blocks, ws, k_cache, v_cache)
+        rc = self.lib.pe_cache_compact(
+            self.addr, n_layers, B, T, _dense(ws, "qsl", B and B + 1, qsl, i32),
+            _dense(ws, "seq_len", B, seq_len, i32), _dense(ws, "accepted", B, accepted, i32),
+            _dense(ws, "path", T, path, i32), _table(ws, block_table, B, i32), block_table.shape[1], num_blocks, k,
+            v, ws.data_ptr(), ws.numel(), _stream_handle(stream, ws))
+        _check(rc, "pe_cache_compact")
+
+    def copy_pages(self, n_layers, n, src, dst, num_blocks, k_cache, v_cache, ws, stream=None):
+        """pe_cache_copy: pages src[i] to dst[i] (int32) of every layer."""
+        k, v = self._layers(n_layers, num_blocks, ws, k_cache, v_cache)
+        rc = self.lib.pe_cache_copy(self.addr, n_layers, n, _dense(ws, "src", n, src, self.i32),
+                                    _dense(ws, "dst", n, dst, self.i32), num_blocks, k, v, ws.data_ptr(), ws.numel(),
+                                    _stream_handle(stream, ws))
+        _check(rc, "pe_cache_copy")
+
+    def fork(self, n_layers, n, parent, child, length, block_table, refs, k_cache, v_cache, ws, stream=None):
+        """pe_pages_fork: rows child[i] of block_table share the first length[i] positions of rows
+        parent[i]; refs counts the uses of each page (num_blocks of them).  All int32."""
+        i32, num_blocks = self.i32, refs.numel()
+        k, v = self._layers(n_layers, num_blocks, ws, k_cache, v_cache)
+        rc = self.lib.pe_pages_fork(
+            self.addr, n_layers, n, _dense(ws, "parent", n, parent, i32), _dense(ws, "child", n, child, i32),
+            _dense(ws, "length", n, length, i32), _table(ws, block_table, 0, i32), block_table.shape[0],
+            block_table.shape[1], num_blocks, _dense(ws, "refs", 0, refs, i32), k, v, ws.data_ptr(), ws.numel(),
+            _stream_handle(stream, ws))
+        _check(rc, "pe_pages_fork")
 
 
 # ----------------------------------------------------------------------------- COD training indices

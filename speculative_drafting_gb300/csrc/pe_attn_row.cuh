@@ -34,9 +34,20 @@ PE_DEV void row_query(const ChunkArgs& a, int row, int h, RowScratch& sh) {
   if (tid < a.hd) sh.q[tid] = Elem<T>::to_f(q[tid]) / sqrtf(static_cast<float>(a.hd));
 }
 
-// Keys 0 .. lim of request r for its row `row` (of all), head h.
-template <typename T>
-PE_DEV void attend_row(const ChunkArgs& a, int r, int row, int h, int lim, RowScratch& sh) {
+// Bits s .. s + 31 of a mask row of `words` words; those before bit 0 are set, those behind
+// the last word are not.
+PE_DEV uint32_t mask_bits(const uint32_t* bits, int words, int64_t s) {
+  if (s <= -32) return 0xffffffffu;
+  if (s >= 32ll * words) return 0u;
+  const int w = static_cast<int>(s >> 5), sh = static_cast<int>(s & 31);  // w: -1 and on
+  const uint32_t lo = w < 0 ? 0xffffffffu : bits[w], hi = w + 1 < words ? bits[w + 1] : 0u;
+  return __funnelshift_r(lo, hi, sh);
+}
+
+// Keys 0 .. lim of request r for its row `row` (of all), head h; of a tree (kTree), of the keys
+// from `first` on those whose bit is set in the row's mask.
+template <typename T, bool kTree>
+PE_DEV void attend_row(const ChunkArgs& a, int r, int row, int h, int lim, int first, RowScratch& sh) {
   constexpr int kVec = 16 / sizeof(T);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = h / (a.H / a.G);
@@ -49,7 +60,10 @@ PE_DEV void attend_row(const ChunkArgs& a, int r, int row, int h, int lim, RowSc
     const int t = static_cast<int>(t0) + lane;
     int64_t base = -1;
     float s = -INFINITY;
-    if (t0 + lane <= lim) {
+    bool seen = t0 + lane <= lim;
+    if (kTree && t0 + 31 >= first)
+      seen = seen && mask_bits(a.mask + static_cast<int64_t>(row) * a.words, a.words, t0 - first) >> lane & 1u;
+    if (seen) {
       const int blk = a.block_table[static_cast<int64_t>(r) * a.max_blocks + t / a.bs];
       if (blk < 0 || blk >= a.num_blocks) {
         set_status(a.status, PE_ST_BLOCK_RANGE);

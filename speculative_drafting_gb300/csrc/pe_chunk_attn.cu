@@ -1,10 +1,12 @@
-// Attention of each request's new rows over its pages (pe_chunk_attention).
+// Attention of each request's new rows over its pages (pe_chunk_attention, pe_tree_attention).
 //
 // Row j of request r stands at position L_r - n_r + j and sees every cache
 // position up to its own:
 //   o = sum_t p_t v_t,  p_t = exp(s_t - m) / (sum_t exp(s_t - m) + exp(sink - m)),
 //   s_t = q . k_t / sqrt(hd),
-// computed in one pass over the keys with a running maximum and sum.
+// computed in one pass over the keys with a running maximum and sum.  Rows that are the nodes
+// of a tree see the context's positions, those before L_r - n_r, and of the nodes' own the ones
+// in their mask.
 //
 // This file: the entry point, and the kernel of the shapes that the tensor-core kernels
 // (pe_chunk_attn_tc.cu) do not take: fp32 plans, and blocks that are no multiple of 8
@@ -16,7 +18,7 @@ namespace pe {
 namespace {
 
 // (48 registers: with 56 a small fp32 call takes 17 us, with 48 13 us, with 40 16 us)
-template <typename T>
+template <typename T, bool kTree>
 __global__ void __launch_bounds__(32 * kRowWarps, 10) chunk_simt_kernel(const ChunkArgs a) {
   __shared__ RowScratch sh;
   __shared__ int req_sh;
@@ -32,6 +34,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 10) chunk_simt_kernel(const Ch
   for (int r = tid; r < a.B; r += 32 * kRowWarps) {
     const RowRange x = request_rows(a.qsl, r, a.T);
     if (x.bad) set_status(a.status, PE_ST_ROWS_RANGE);
+    if (kTree && x.q1 - x.q0 > 32 * a.words) set_status(a.status, PE_ST_TREE);
     // (of every request, those without rows too)
     if (row == 0 && h == 0 && (a.seq_len[r] < 0 || a.seq_len[r] > Lmax)) set_status(a.status, PE_ST_BLOCK_RANGE);
     if (x.q0 <= row && row < x.q1) atomicMax(&req_sh, r);
@@ -42,8 +45,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, 10) chunk_simt_kernel(const Ch
   const RowRange rr = request_rows(a.qsl, r, a.T);
   const int n = rr.q1 - rr.q0, j = row - rr.q0;
   const int L = static_cast<int>(min(max(static_cast<int64_t>(a.seq_len[r]), int64_t{0}), Lmax));
-  const int lim = L - n + j;  // the row's own position
-  attend_row<T>(a, r, row, h, lim, sh);
+  const int lim = kTree ? L - 1 : L - n + j;  // the row's own position
+  attend_row<T, kTree>(a, r, row, h, lim, L - n, sh);
 }
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -64,7 +67,8 @@ namespace {
 int chunk_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qsl, const int32_t* seq_len,
                     const void* q, int64_t ld_q, const void* k_cache, const void* v_cache,
                     const int32_t* block_table, int max_blocks, int num_blocks, const float* sink, void* out,
-                    int64_t ld_out, void* ws, size_t ws_bytes, void* stream, int stall) {
+                    int64_t ld_out, void* ws, size_t ws_bytes, void* stream, int stall, bool tree = false,
+                    const uint32_t* mask = nullptr, int words = 0) {
   if (!plan_ok(plan) || B < 0 || T < 0 || max_blocks < 1 || num_blocks < 0) return PE_ERR_ARG;
   const int64_t width = static_cast<int64_t>(plan->n_heads) * plan->head_dim;
   if (ld_q < width || ld_out < width || ld_q % 8 || ld_out % 8) return PE_ERR_ARG;
@@ -82,6 +86,7 @@ int chunk_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qsl, 
       if (!aligned(p, 16)) return PE_ERR_ARG;
     if (!aligned(qsl, 4) || !aligned(seq_len, 4) || !aligned(block_table, 4) || !aligned(sink, 4))
       return PE_ERR_ARG;
+    if (tree && (!mask || !aligned(mask, 4))) return PE_ERR_ARG;
   }
   if (B == 0 || T == 0) return PE_OK;
   ChunkArgs a = {};
@@ -105,11 +110,14 @@ int chunk_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qsl, 
   a.ld_out = ld_out;
   a.status = static_cast<uint32_t*>(ws);
   a.stall = stall;
+  a.mask = mask;
+  a.words = words;
   if (chunk_tc_takes(plan) && num_blocks > 0) return launch_chunk_tc(a, static_cast<char*>(ws), st);
   const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(plan->n_heads));
-  const cudaError_t e = plan->dtype == PE_DTYPE_BF16
-                            ? launch_chained(chunk_simt_kernel<bf16>, grid, dim3(32 * kRowWarps), 0, st, a)
-                            : launch_chained(chunk_simt_kernel<float>, grid, dim3(32 * kRowWarps), 0, st, a);
+  const bool b = plan->dtype == PE_DTYPE_BF16;
+  void (*kernel)(ChunkArgs) = tree ? (b ? chunk_simt_kernel<bf16, true> : chunk_simt_kernel<float, true>)
+                                   : (b ? chunk_simt_kernel<bf16, false> : chunk_simt_kernel<float, false>);
+  const cudaError_t e = launch_chained(kernel, grid, dim3(32 * kRowWarps), 0, st, a);
   return e == cudaSuccess ? PE_OK : PE_ERR_CUDA;
 }
 
@@ -124,6 +132,17 @@ extern "C" int pe_chunk_attention(const pe_attn_plan* plan, int B, int T, const 
   NvtxRange nvtx("pe_chunk_attention");
   return chunk_attention(plan, B, T, qsl, seq_len, q, ld_q, k_cache, v_cache, block_table, max_blocks,
                          num_blocks, sink, out, ld_out, ws, ws_bytes, stream, 0);
+}
+
+extern "C" int pe_tree_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qsl, const int32_t* seq_len,
+                                 const void* q, int64_t ld_q, const void* k_cache, const void* v_cache,
+                                 const int32_t* block_table, int max_blocks, int num_blocks, const uint32_t* mask,
+                                 int words, const float* sink, void* out, int64_t ld_out, void* ws, size_t ws_bytes,
+                                 void* stream) {
+  NvtxRange nvtx("pe_tree_attention");
+  if (words < 1 || words > PE_TREE_MAX_NODES / 32) return PE_ERR_ARG;
+  return chunk_attention(plan, B, T, qsl, seq_len, q, ld_q, k_cache, v_cache, block_table, max_blocks, num_blocks, sink,
+                         out, ld_out, ws, ws_bytes, stream, 0, true, mask, words);
 }
 
 extern "C" int pe_test_chunk_attention_stall(const pe_attn_plan* plan, int slot, int B, int T, const int32_t* qsl,

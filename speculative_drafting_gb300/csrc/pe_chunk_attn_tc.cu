@@ -118,6 +118,7 @@ struct TcArgs {
   Rec* rec;         // [grid]
 };
 
+template <bool kTree>
 PE_DEV Req load_req(const ChunkArgs& a, int r, bool report) {
   const RowRange x = request_rows(a.qsl, r, a.T);
   Req q;
@@ -129,15 +130,18 @@ PE_DEV Req load_req(const ChunkArgs& a, int r, bool report) {
   q.L = over ? static_cast<int>(min(max(static_cast<long long>(L), 0ll), Lmax)) : L;
   if (report && (x.bad || over))
     set_status(a.status, (x.bad ? PE_ST_ROWS_RANGE : 0u) | (over ? PE_ST_BLOCK_RANGE : 0u));
+  if (kTree && report && q.n > 32 * a.words) set_status(a.status, PE_ST_TREE);
   const int HG = a.H / a.G;
   q.R = q.n * HG;
   q.Q = (q.R + kUnitRows - 1) / kUnitRows;
-  q.A = static_cast<long long>(max(q.L - q.n, 0)) * HG;
+  q.A = static_cast<long long>(kTree ? q.L : max(q.L - q.n, 0)) * HG;
   return q;
 }
 
-// keys that some row of unit i sees, and their tiles (at least one)
+// keys that some row of unit i sees (of a tree: may see), and their tiles (at least one)
+template <bool kTree>
 PE_DEV int unit_kend(const Req& q, int i, int HG) {
+  if (kTree) return q.L;
   const int last = (min((i + 1) * kUnitRows, q.R) - 1) / HG;
   return min(max(q.L - q.n + last + 1, 0), q.L);
 }
@@ -146,16 +150,20 @@ PE_DEV int unit_tiles(int kend) {
   return max(1, (kend + Shape<HD>::kTile - 1) / Shape<HD>::kTile);
 }
 
-// cost of unit i, and of the units before it (all but the last are wide)
+// cost of unit i, and of the units before it (all but the last are wide; every row of a tree
+// goes over all keys)
+template <bool kTree>
 PE_DEV long long unit_cost(const Req& q, int i, long long ov) {
   const int end = min((i + 1) * kUnitRows, q.R);
-  return (end - i * kUnitRows > kRows ? 2 : 1) * (q.A + end) + ov;
+  return (end - i * kUnitRows > kRows ? 2 : 1) * (q.A + (kTree ? 0 : end)) + ov;
 }
+template <bool kTree>
 PE_DEV long long units_before(const Req& q, int i, long long ov) {
-  return i * (2 * q.A + ov) + 256ll * i * (i + 1);
+  return i * (2 * q.A + ov) + (kTree ? 0 : 256ll * i * (i + 1));
 }
+template <bool kTree>
 PE_DEV long long req_cost(const Req& q, long long ov) {
-  return q.Q == 0 ? 0 : units_before(q, q.Q - 1, ov) + unit_cost(q, q.Q - 1, ov);
+  return q.Q == 0 ? 0 : units_before<kTree>(q, q.Q - 1, ov) + unit_cost<kTree>(q, q.Q - 1, ov);
 }
 
 // the first request at or after r that has rows (B if none), by one whole warp
@@ -375,7 +383,7 @@ __device__ __noinline__ void finish_unit(const TcArgs& p, const Unit& u, int* ba
   __syncwarp();
 }
 
-template <int HD>
+template <int HD, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TcArgs p) {
@@ -461,9 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long mine = 0;
   Req req0;  // of this thread's first request (with up to kThreads requests, its only one)
   for (int r = r_lo; r < r_hi; ++r) {
-    const Req q = load_req(a, r, blockIdx.x == 0);
+    const Req q = load_req<kTree>(a, r, blockIdx.x == 0);
     if (r == r_lo) req0 = q;
-    mine += req_cost(q, ov);
+    mine += req_cost<kTree>(q, ov);
   }
   long long incl = mine;
 #pragma unroll
@@ -517,8 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       long long rem = min(piece(c, g), Wg - 1) - before;
       if (rem < 0 || rem >= mine) continue;
       for (int r = r_lo; r < r_hi; ++r) {
-        const Req q = r == r_lo ? req0 : load_req(a, r, false);
-        const long long cost = req_cost(q, ov);
+        const Req q = r == r_lo ? req0 : load_req<kTree>(a, r, false);
+        const long long cost = req_cost<kTree>(q, ov);
         if (rem >= cost) {
           rem -= cost;
           continue;
@@ -526,13 +534,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         int lo = 0, hi = q.Q;  // the last unit that starts at or before rem
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
-          if (units_before(q, mid, ov) <= rem) lo = mid; else hi = mid;
+          if (units_before<kTree>(q, mid, ov) <= rem) lo = mid; else hi = mid;
         }
-        const long long off = rem - units_before(q, lo, ov);
-        const int kt = unit_tiles<HD>(unit_kend(q, lo, HG));
+        const long long off = rem - units_before<kTree>(q, lo, ov);
+        const int kt = unit_tiles<HD>(unit_kend<kTree>(q, lo, HG));
         // A cut near a unit's end or start moves there: a part costs a CTA some tiles of
         // time whatever its length.
-        const float cost_u = static_cast<float>(unit_cost(q, lo, ov));
+        const float cost_u = static_cast<float>(unit_cost<kTree>(q, lo, ov));
         const float len = static_cast<float>(W) / static_cast<float>(pieces) * static_cast<float>(kt) / cost_u;
         const int snap = min(4, static_cast<int>(0.25f * len));
         int tile = min(kt - 1, static_cast<int>(static_cast<float>(off) / cost_u * static_cast<float>(kt)));
@@ -700,14 +708,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_ok = rel < items[slot].rows;
       const bool live = uniform((rel & ~31) < items[slot].rows);  // some row of this warp exists
       const int kend = uniform(items[slot].kend), tile0 = uniform(items[slot].tile0);
-      int lim, lim0;  // the last key that this row sees, and the unit's first row
+      // the last key that this row sees, and the unit's first row (of a tree: its row of the
+      // mask, and the context's last key)
+      int lim, lim0;
       {
         int tok, head;
         split_row(p, items[slot].row0 + rel, tok, head);
         const int p0 = items[slot].L - items[slot].n;
-        lim = row_ok ? p0 + tok : -1;
-        split_row(p, items[slot].row0, tok, head);
-        lim0 = uniform(p0 + tok);
+        if constexpr (kTree) {
+          lim = row_ok ? items[slot].q0 + tok : -1;
+          lim0 = uniform(p0 - 1);
+        } else {
+          lim = row_ok ? p0 + tok : -1;
+          split_row(p, items[slot].row0, tok, head);
+          lim0 = uniform(p0 + tok);
+        }
       }
       if (S::kQBufs == 1 || items[slot].index == 0) {
         load_q<HD>(p, items[slot], q_sm, false);
@@ -721,6 +736,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (two S products of the overlay may be done before the first is looked at: a
         // barrier for either buffer)
         const uint32_t n = n_st + k;
+        // (on their way while the product runs)
+        uint32_t tree[kTree ? kKeys / 32 : 1];
+        if constexpr (kTree) {
+          if (t0 + S::kTile - 1 > lim0) {
+#pragma unroll
+            for (int b = 0; b < kKeys / 32; ++b)
+              tree[b] = lim < 0 ? 0u
+                                : mask_bits(a.mask + static_cast<int64_t>(lim) * a.words, a.words,
+                                            t0 + kKeys * hf + 32 * b - static_cast<int64_t>(lim0 + 1));
+          } else {
+#pragma unroll
+            for (int b = 0; b < kKeys / 32; ++b) tree[b] = lim < 0 ? 0u : 0xffffffffu;
+          }
+        }
         failed = failed || !wait_warp(&s_full[s][S::kOverlay ? n & 1 : 0], (S::kOverlay ? n >> 1 : n) & 1);
         tc_fence_after();
         const uint32_t have = uniform(mask_sh[(tiles + j) % kMasks]);
@@ -748,10 +777,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int b = 0; b < kKeys / 32; ++b) tmem_use32(x + 32 * b);
             const uint32_t mine = have >> (kKeys / 8 * hf);
+            if constexpr (kTree) {
 #pragma unroll
-            for (int c = 0; c < kKeys; ++c) {
-              if (c0 + c > lim || !(mine >> (c >> 3) & 1u)) x[c] = 0xff800000u;
-              best = fmaxf(best, __uint_as_float(x[c]));
+              for (int b = 0; b < kKeys / 32; ++b) {
+                // this row's keys of 32: in its mask, there, before the request's end
+                uint32_t see = tree[b];
+                const int left = kend - c0 - 32 * b;
+                if (left < 32) see &= left <= 0 ? 0u : (1u << left) - 1u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (!(mine >> (4 * b + e) & 1u)) see &= ~(0xffu << 8 * e);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                  if (!(see >> c & 1u)) x[32 * b + c] = 0xff800000u;
+                  best = fmaxf(best, __uint_as_float(x[32 * b + c]));
+                }
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < kKeys; ++c) {
+                if (c0 + c > lim || !(mine >> (c >> 3) & 1u)) x[c] = 0xff800000u;
+                best = fmaxf(best, __uint_as_float(x[c]));
+              }
             }
           }
         }
@@ -891,7 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ends_here && last.tile <= cur.tile) break;
       if (cur.g >= a.G) break;
       if (cur.r != q_of) {
-        q = load_req(a, cur.r, false);
+        q = load_req<kTree>(a, cur.r, false);
         q_of = cur.r;
       }
       Unit u;
@@ -903,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       u.row0 = cur.qt * kUnitRows;
       u.rows = min(kUnitRows, q.R - u.row0);
       u.wide = u.rows > kRows;
-      u.kend = unit_kend(q, cur.qt, HG);
+      u.kend = unit_kend<kTree>(q, cur.qt, HG);
       const int kt = unit_tiles<HD>(u.kend);
       u.tile0 = cur.tile;
       u.tile1 = ends_here ? min(last.tile, kt) : kt;
@@ -1123,6 +1170,7 @@ PE_DEV int join_row(int i, int warp) { return (blockIdx.y + i * gridDim.y) * kRo
 // Of the unit at packed row row0, the rows noted (bit i of a warp's `again`: its i-th row),
 // so far as a key of the unit is past them.  (This and the next one are calls, not inlined:
 // their registers would be the join's.)
+template <bool kTree>
 __device__ __noinline__ void redo_unit(const TcArgs& p, int r, int g, int row0, uint32_t again,
                                        RowScratch& scratch) {
   __shared__ uint32_t again_sh[kRowWarps];
@@ -1130,11 +1178,11 @@ __device__ __noinline__ void redo_unit(const TcArgs& p, int r, int g, int row0, 
   const int HG = a.H / a.G;
   if ((threadIdx.x & 31) == 0) again_sh[threadIdx.x >> 5] = again;
   __syncthreads();
-  const Req q = load_req(a, r, false);
-  const int kend = unit_kend(q, row0 / kUnitRows, HG);
+  const Req q = load_req<kTree>(a, r, false);
+  const int kend = unit_kend<kTree>(q, row0 / kUnitRows, HG);
   // Only where a value that some row does not see (at most the unit's tokens) is not finite:
   // what all of its rows see reached them rightly.
-  const int t0 = max(q.L - q.n + row0 / HG + 1, 0), chunks = a.hd / 8;
+  const int t0 = max(kTree ? q.L - q.n : q.L - q.n + row0 / HG + 1, 0), chunks = a.hd / 8;
   __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
   for (int i = threadIdx.x; i < (kend - t0) * chunks; i += 32 * kRowWarps) {
     const int t = t0 + i / chunks;
@@ -1147,11 +1195,11 @@ __device__ __noinline__ void redo_unit(const TcArgs& p, int r, int g, int row0, 
   for (int w = 0; w < kRowWarps; ++w)
     for (uint32_t todo = again_sh[w]; todo; todo &= todo - 1) {
       const int row = row0 + join_row(__ffs(todo) - 1, w);
-      const int tok = row / HG, head = g * HG + row % HG, lim = q.L - q.n + tok;
-      if (lim >= kend - 1) continue;
+      const int tok = row / HG, head = g * HG + row % HG, lim = kTree ? q.L - 1 : q.L - q.n + tok;
+      if (!kTree && lim >= kend - 1) continue;
       row_query<bf16>(a, q.q0 + tok, head, scratch);
       __syncthreads();
-      attend_row<bf16>(a, r, q.q0 + tok, head, lim, scratch);
+      attend_row<bf16, kTree>(a, r, q.q0 + tok, head, lim, q.L - q.n, scratch);
       __syncthreads();
     }
   __syncthreads();
@@ -1159,7 +1207,7 @@ __device__ __noinline__ void redo_unit(const TcArgs& p, int r, int g, int row0, 
 
 // The whole units of this CTA's list up to the last that was noted, as the K warp of the
 // first kernel went through them.
-template <int HD>
+template <int HD, bool kTree>
 __device__ __noinline__ void redo_list(const TcArgs& p, RowScratch& scratch) {
   const ChunkArgs& a = p.c;
   const Rec& rec = p.rec[blockIdx.x];
@@ -1167,7 +1215,7 @@ __device__ __noinline__ void redo_list(const TcArgs& p, RowScratch& scratch) {
   const int bad0 = rec.bad0, bad1 = rec.bad1;
   int g = rec.u_g, r = rec.u_r, qt = rec.u_qt;
   for (int unit = 0; unit <= bad1; ++unit) {
-    const Req q = load_req(a, r, false);
+    const Req q = load_req<kTree>(a, r, false);
     if (unit >= bad0) {
       const int n = min(kUnitRows, q.R - qt * kUnitRows);
       uint32_t again = 0;
@@ -1180,7 +1228,7 @@ __device__ __noinline__ void redo_list(const TcArgs& p, RowScratch& scratch) {
         for (int i = 0; i < HD / 32; ++i) bad |= !finite(__bfloat162float(o[lane + 32 * i]));
         again |= static_cast<uint32_t>(__any_sync(0xffffffffu, bad)) << at;
       }
-      redo_unit(p, r, g, qt * kUnitRows, again, scratch);
+      redo_unit<kTree>(p, r, g, qt * kUnitRows, again, scratch);
     }
     if (++qt >= q.Q) {
       qt = 0;
@@ -1197,7 +1245,7 @@ __device__ __noinline__ void redo_list(const TcArgs& p, RowScratch& scratch) {
 // whose first part is CTA c's last one, a slice of its rows; its other parts are the
 // first ones of the CTAs after c, up to the one that ends it.  One warp per row.  Then the
 // rows to compute again: of that unit, and of CTA c's whole units that have some.
-template <int HD>
+template <int HD, bool kTree>
 __global__ void __launch_bounds__(32 * kRowWarps) chunk_join_kernel(const __grid_constant__ TcArgs p) {
   constexpr int V = HD / 32;
   __shared__ RowScratch scratch;
@@ -1286,8 +1334,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) chunk_join_kernel(const __grid
     for (int i = 0; i < V; ++i) bad |= !finite(acc[i]);
     again |= static_cast<uint32_t>(__any_sync(0xffffffffu, bad && den == den)) << at;
   }
-  if (__syncthreads_or(again)) redo_unit(p, rec.r, g, row0, again, scratch);
-  if (bad1 >= 0) redo_list<HD>(p, scratch);
+  if (__syncthreads_or(again)) redo_unit<kTree>(p, rec.r, g, row0, again, scratch);
+  if (bad1 >= 0) redo_list<HD, kTree>(p, scratch);
 }
 
 constexpr int kMaxGrid = 152;
@@ -1302,7 +1350,7 @@ int part_rows_of(int T, int HG) {
 size_t rec_bytes() { return al256(kMaxGrid * sizeof(Rec)); }
 size_t ml_bytes(int part_rows) { return al256(size_t{kMaxGrid} * 2 * part_rows * 2 * sizeof(float)); }
 
-template <int HD>
+template <int HD, bool kTree>
 int launch(const TcArgs& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
   // the function's shared-memory limit, once per device (a bit each; past 63 every time)
   static std::atomic<uint64_t> set{0};
@@ -1310,12 +1358,12 @@ int launch(const TcArgs& p, const CUtensorMap& km, const CUtensorMap& vm, cudaSt
   if (cudaGetDevice(&dev) != cudaSuccess) return PE_ERR_CUDA;
   const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
   if (!(set.load(std::memory_order_acquire) & bit)) {
-    if (cudaFuncSetAttribute(chunk_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(chunk_tc_kernel<HD, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Shape<HD>::kSmem) != cudaSuccess)
       return PE_ERR_CUDA;
     set.fetch_or(bit, std::memory_order_release);
   }
-  if (launch_chained(chunk_tc_kernel<HD>, dim3(p.grid), dim3(kThreads), Shape<HD>::kSmem, st, km, vm, p) !=
+  if (launch_chained(chunk_tc_kernel<HD, kTree>, dim3(p.grid), dim3(kThreads), Shape<HD>::kSmem, st, km, vm, p) !=
       cudaSuccess)
     return PE_ERR_CUDA;
   // Rows of a unit per warp of the join (it notes them in 32 bits): one where there are few
@@ -1323,7 +1371,7 @@ int launch(const TcArgs& p, const CUtensorMap& km, const CUtensorMap& vm, cudaSt
   const int rows = static_cast<int>(
       std::min<long long>(static_cast<long long>(p.c.T) * (p.c.H / p.c.G), p.part_rows));
   const int join = rows <= 32 ? (rows + 3) / 4 : (rows + 31) / 32;
-  return launch_chained(chunk_join_kernel<HD>, dim3(p.grid, join), dim3(128), 0, st, p) == cudaSuccess
+  return launch_chained(chunk_join_kernel<HD, kTree>, dim3(p.grid, join), dim3(128), 0, st, p) == cudaSuccess
              ? PE_OK
              : PE_ERR_CUDA;
 }
@@ -1369,7 +1417,8 @@ int launch_chunk_tc(const ChunkArgs& a, char* ws, cudaStream_t st) {
   auto* encode = a.hd == 64 ? encode_tmap_bf16 : encode_tmap_bf16_rows128;
   if (!encode(&km, a.k_cache, rows, a.hd, p.box) || !encode(&vm, a.v_cache, rows, a.hd, p.box))
     return PE_ERR_CUDA;
-  return a.hd == 64 ? launch<64>(p, km, vm, st) : launch<128>(p, km, vm, st);
+  if (a.mask) return a.hd == 64 ? launch<64, true>(p, km, vm, st) : launch<128, true>(p, km, vm, st);
+  return a.hd == 64 ? launch<64, false>(p, km, vm, st) : launch<128, false>(p, km, vm, st);
 }
 
 }  // namespace pe

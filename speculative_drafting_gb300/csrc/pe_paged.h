@@ -28,7 +28,7 @@ inline cudaError_t launch_chained(void (*kernel)(Exp...), dim3 grid, dim3 block,
 // Whether pe_attn_plan_init filled this plan (its shape fields are in range).
 bool plan_ok(const pe_attn_plan* p);
 
-// One call of pe_chunk_attention, as its kernels take it.
+// One call of pe_chunk_attention or pe_tree_attention, as their kernels take it.
 struct ChunkArgs {
   int B, T, H, G, hd, bs, max_blocks, num_blocks;
   const int32_t* qsl;
@@ -42,10 +42,12 @@ struct ChunkArgs {
   void* out;
   int64_t ld_out;
   uint32_t* status;
+  const uint32_t* mask;  // pe_tree_attention: [T][words], else null
+  int words;
   int stall;  // pe_test_chunk_attention_stall's, else 0
 };
 
-// The tensor-core kernels of pe_chunk_attention (bf16, blocks of a multiple of 8 keys).
+// The tensor-core kernels of the two (bf16, blocks of a multiple of 8 keys).
 bool chunk_tc_takes(const pe_attn_plan* plan);
 size_t chunk_tc_workspace(const pe_attn_plan* plan, int max_rows);
 int launch_chunk_tc(const ChunkArgs& a, char* ws, cudaStream_t st);
