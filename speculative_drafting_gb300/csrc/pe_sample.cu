@@ -5,21 +5,27 @@
 // as all three settings allow, so a row's answer needs the place of the cut in that order and
 // then the best of (l - max) / T + g over the tokens before it.  Nothing is sorted as a whole.
 //
-// One cluster of CTAs per row, each with a slice of the row in shared memory: the logits are
-// read once.
-//   1. Largest logit of the row; each thread's largest one of its share of the slice.
-//   2. A bound from below for the cut: the threads' largest values are tokens of the row, so
-//      the value at which k of them (for top-p: enough of them to weigh p of the whole) are
-//      reached cannot lie above the cut.  They go into kBins bins, a bin of the range that they
-//      span each.
-//   3. The tokens from the bound on, some more than are kept, go to the first CTA with their
-//      noise: rank and weight before each by comparing all pairs, the cut, the best score.
-// Where that does not do (a flat row that keeps thousands, a large k, many equal logits),
-// the cut is found digit by digit: histograms of counts and weights over 8 bits of the
-// logits' order at a time, weights as 31-bit integers (their sums do not depend on the
-// order), then all CTAs race over their slices.
+//   row kernel   CTA (row, part) streams its part of the logits once: the largest logit, the
+//                sum of weights (top-p), the first largest token (greedy) or the best score
+//                (nothing is cut: the noise is streamed along).  For rows with a cut it also
+//                leaves the largest logit of each group of some hundred tokens.
+//   cut kernel   a CTA per row joins the parts.  For a row with a cut:
+//                  - a bound from below for it.  The groups' largest logits are tokens of the
+//                    row, so the value at which k of them (for top-p: enough of them to weigh
+//                    p of the whole) are reached cannot lie above the cut;
+//                  - the tokens from the bound on, read again from the few groups that have
+//                    one: rank and weight before each by comparing all pairs, the cut, the
+//                    best score.
+//   wide kernel  takes the rows for which that does not do (flat rows that keep thousands of
+//                tokens, a large k, many equal logits), a cluster of CTAs a row with a slice
+//                each in shared memory: histograms of counts and weights over the distance from the
+//                largest logit, finer ones inside the bin of the cut, then a race over the
+//                slices.  Weights are 31-bit integers there: their sums do not depend on the
+//                order of the atomics.
 //
-// Rows without cuts (and greedy ones) need neither 2 nor 3.
+// The first kernel is bound by the logits' bytes.  (Every row by a cluster with the row in
+// shared memory: 512 bf16 rows of 201,088 with top-k 162 us; the barriers of a row are waited
+// for with its 400 KB held.)
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -30,13 +36,31 @@
 namespace pe {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;         // row kernel
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
-constexpr int kBins = 64;
-constexpr int kList = 512;   // candidates of a row that the first CTA compares
-constexpr int kUnroll = 4;   // 16-byte loads in flight per thread
-constexpr int kDigits = 256;
+constexpr int kUnroll = 4;            // 16-byte loads in flight per thread
+constexpr int kRaceUnroll = 2;        // ... where the noise is streamed too
+constexpr int kMaxPartBytes = 65536;  // of a row, per CTA
+constexpr int kGroups = 4096;         // of a row, at most
+constexpr int kBins = 256;
+constexpr int kList = 512;            // candidates of a row whose pairs are compared
+constexpr int kGroupList = 1024;      // groups that are read again
+
+constexpr int kWideThreads = 512;     // wide kernel
+constexpr int kWideWarps = kWideThreads / 32;
+constexpr int kCluster = 8;
+
+// What a CTA of the row kernel leaves of its part.
+struct __align__(16) Part {
+  float m;        // largest logit (NaN if there is one)
+  float s;        // sum of weights relative to it
+  float x, g;     // of the best score: logit and noise
+  int idx;        // ... and token, -1: there is none
+  int pad;
+  unsigned long long key;  // greedy: argmax_key of the first largest logit
+};
+
+struct Settings;
 
 struct SampleArgs {
   int B, T, V;
@@ -51,80 +75,46 @@ struct SampleArgs {
   int64_t ld_g;
   int32_t* token;
   uint32_t* status;
-  int ctas;      // of a row
-  int resident;  // slices stay in shared memory
+  int part, parts;   // 16-byte vectors of a part, parts of a row
+  int gshift;        // threads of a group: 1 << gshift
+  Part* stat;        // [T][parts]
+  float* top;        // [T][parts][kThreads >> gshift]
+  Settings* set;  // [T] of each row
+  uint32_t* todo_n;  // rows for the wide kernel
+  int32_t* todo;     // [T]
+  int resident;      // the wide kernel's slices fit in shared memory
 };
 
-// What a CTA of the cluster tells the others, in their shared memory.
-struct FromCta {
-  float m, lo;     // largest logit; least finite of the threads' largest
-  int cand;        // candidates
-  double z;        // sum of weights
-  uint32_t cnt[kBins], least[kBins];  // threads' largest values per bin; order of their least
-  unsigned long long mass[kBins];     // their weights, 2^-40
+struct Settings {
+  float temp, p, mp;  // temperature (negative: a row of no request); top-p, 1: off; min-p, 0: off
+  int k;              // 0: off
 };
-
-struct Entry {
-  unsigned long long key;  // order of the logit, then of the index: larger comes first
-  float g;
-};
-
-struct Best {
-  unsigned long long order;
-  int idx;
-};
-
-union Scratch {
-  FromCta from[kMaxCluster];
-  // [two levels in turn][digit]: count, and the sums of three parts of the weights' bits
-  uint32_t digits[2][kDigits][4];
-};
-
-PE_DEV uint32_t cluster_addr(const void* local, uint32_t rank) {
-  uint32_t remote;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
-  return remote;
-}
-PE_DEV void put32(const void* local, uint32_t rank, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(local, rank)), "r"(v) : "memory");
-}
-PE_DEV void put64(const void* local, uint32_t rank, unsigned long long v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_addr(local, rank)), "l"(v) : "memory");
-}
-PE_DEV uint32_t get32(const void* local, uint32_t rank) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(local, rank)) : "memory");
-  return v;
-}
-PE_DEV uint32_t add32(const void* local, uint32_t rank, uint32_t v) {
-  uint32_t old;
-  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
-               : "=r"(old)
-               : "r"(cluster_addr(local, rank)), "r"(v)
-               : "memory");
-  return old;
+PE_DEV Settings settings_of(const SampleArgs& a, int r, uint32_t& status) {
+  Settings s;
+  const float t = a.temperature ? a.temperature[r] : 1.f;
+  const int k = a.top_k ? a.top_k[r] : 0;
+  const float p = a.top_p ? a.top_p[r] : 1.f, mp = a.min_p ? a.min_p[r] : 0.f;
+  if (!(t >= 0.f) || p != p || mp != mp) status |= PE_ST_SAMPLING;
+  s.temp = temperature_of(t);
+  s.k = k <= 0 || k >= a.V ? 0 : k;
+  s.p = p < 1.f ? p : 1.f;     // (NaN: 1)
+  s.mp = mp > 0.f ? mp : 0.f;  // (NaN: 0)
+  return s;
 }
 
-// (all threads of all CTAs of the row)
-PE_DEV void row_sync() {
-  __syncwarp();
-  cluster_sync_all();
-}
-
-// The logit of an order (argmax_order), and one that is in none of its values
-PE_DEV float logit_of(uint32_t order) {
-  return __uint_as_float(order & 0x80000000u ? order & 0x7fffffffu : ~order);
-}
-
-// A CTA's part of a row, in 16-byte vectors on the grid of the addresses: vector v holds the
-// tokens v * kVec - shift and on, those outside the row as -inf.
+// A row in 16-byte vectors on the grid of the addresses: vector v holds the tokens
+// v * kVec - shift and on, those outside the row as -inf.
 template <typename T>
-struct Slice {
+struct Row {
   static constexpr int kVec = 16 / sizeof(T);
   const T* row;
-  int V, shift, v0, v1;
-  const uint4* held;  // of v0 and on, in shared memory, or null
-
+  int V, shift;
+  PE_DEV Row(const SampleArgs& a, int r) {
+    row = static_cast<const T*>(a.logits) + r * a.ld;
+    V = a.V;
+    shift = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+  }
+  PE_DEV int vectors() const { return (V + shift + kVec - 1) / kVec; }
   PE_DEV int token(int v) const { return v * kVec - shift; }
   PE_DEV uint4 load(int v) const {
     const int e = token(v);
@@ -134,10 +124,71 @@ struct Slice {
     for (int i = 0; i < kVec; ++i) f[i] = e + i >= 0 && e + i < V ? Elem<T>::to_f(row[e + i]) : -INFINITY;
     return pack16<T>(f);
   }
-  PE_DEV uint4 get(int v) const { return held ? held[v - v0] : load(v); }
+};
+template <typename T>
+PE_DEV uint4 no_tokens() {
+  return sizeof(T) == 2 ? make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u)
+                        : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+}
+
+// The noise of a row beside a vector of its logits; zeros outside the row.
+template <typename T>
+struct Noise {
+  static constexpr int kVec = 16 / sizeof(T);
+  const float* g;
+  bool wide;  // vectors of noise lie on the 16-byte grid too
+  PE_DEV Noise(const SampleArgs& a, int r, int shift) {
+    g = a.gumbel + r * a.ld_g;
+    wide = !((reinterpret_cast<uintptr_t>(g) - shift * 4u) & 15u);
+  }
+  PE_DEV void load(int t0, int V, float* x) const {
+    if (wide && t0 >= 0 && t0 + kVec <= V) {
+#pragma unroll
+      for (int e = 0; e < kVec; e += 4) unpack16<float>(ld_stream16(g + t0 + e), x + e);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) x[e] = t0 + e >= 0 && t0 + e < V ? g[t0 + e] : 0.f;
+    }
+  }
 };
 
+PE_DEV unsigned long long exact_score(float x, float g, float M, float temp) {
+  return score_order((static_cast<double>(x) - static_cast<double>(M)) / static_cast<double>(temp) + g);
+}
+
+// The logit of an order (argmax_order)
+PE_DEV float logit_of(uint32_t order) {
+  return __uint_as_float(order & 0x80000000u ? order & 0x7fffffffu : ~order);
+}
+
+// Best (order, index) of the CTA; all threads get it.
+template <int W>
+PE_DEV void cta_best(unsigned long long& k, int& i, unsigned long long* ks, int* is) {
+  warp_best(k, i);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) {
+    ks[threadIdx.x >> 5] = k;
+    is[threadIdx.x >> 5] = i;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  k = lane < W ? ks[lane] : 0ull;
+  i = lane < W ? is[lane] : 0x7fffffff;
+  warp_best(k, i);
+}
+template <int W>
+PE_DEV float cta_max(float v, float* warps) {  // NaN if there is one
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = warps[0];
+  for (int w = 1; w < W; ++w) v = max_nan(v, warps[w]);
+  return v;
+}
 // Sum over the CTA, in a fixed order; all threads get it.
+template <int W>
 PE_DEV double cta_sum(double v, double* warps) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -145,574 +196,980 @@ PE_DEV double cta_sum(double v, double* warps) {
   if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
   __syncthreads();
   double s = 0.;
-  for (int w = 0; w < kWarps; ++w) s += warps[w];
+  for (int w = 0; w < W; ++w) s += warps[w];
   return s;
 }
 
-struct Cut {
-  uint32_t key;   // order of the last kept token's logit
-  int ties;       // kept ones with that logit, the first by index
-  int all;        // all of them are kept
-  double mass;    // weight of the kept ones
-};
-
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArgs a) {
   constexpr int kVec = 16 / sizeof(T);
-  extern __shared__ uint4 held[];
-  __shared__ Scratch sh;
-  __shared__ Entry list[kList];     // on rank 0: the row's candidates
-  __shared__ int mine_i[kList];     // this CTA's
-  __shared__ float mine_x[kList];
-  __shared__ uint32_t n_list, n_mine;
-  __shared__ Best best_of[kMaxCluster];
-  __shared__ uint32_t h_cnt[kBins], h_least[kBins];
-  __shared__ unsigned long long h_mass[kBins];
+  __shared__ float warp_m[kWarps];
   __shared__ double warp_d[kWarps];
-  __shared__ float warp_m[kWarps], warp_lo[kWarps];
   __shared__ unsigned long long warp_k[kWarps];
   __shared__ int warp_i[kWarps];
-  __shared__ float set_sh[4];
-  __shared__ int req_sh;
-  __shared__ uint32_t cut_sh[2];
-  __shared__ int cut_count_sh, cut_n_sh;
+  __shared__ Settings set_sh;
   pdl_trigger();
-  // (every CTA of the cluster has to have begun before another one writes to it)
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
-  const int row = blockIdx.x / a.ctas, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = blockIdx.x - row * a.ctas, nr = a.ctas;
-  Slice<T> s;
-  s.row = static_cast<const T*>(a.logits) + row * a.ld;
-  s.V = a.V;
-  s.shift = static_cast<int>((reinterpret_cast<uintptr_t>(s.row) & 15u) / sizeof(T));
-  {
-    const int nvec = (a.V + s.shift + kVec - 1) / kVec, per = (nvec + nr - 1) / nr;
-    s.v0 = min(static_cast<int>(rank) * per, nvec);
-    s.v1 = min(s.v0 + per, nvec);
-    s.held = nullptr;
-  }
-  // ---------------- settings
+  const int row = blockIdx.x / a.parts, part = blockIdx.x - row * a.parts;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Row<T> s(a, row);
+  const int v0 = part * a.part, n = min(a.part, s.vectors() - v0);  // (n <= 0: nothing is left for this part)
+  // the first vectors are on their way while the row's request is looked up
+  uint4 u[kUnroll];
+#pragma unroll
+  for (int x = 0; x < kUnroll; ++x) u[x] = tid + x * kThreads < n ? s.load(v0 + tid + x * kThreads) : no_tokens<T>();
   if (warp == 0) {
     const int r = request_of(a.qsl, a.B, row, lane);
     if (lane == 0) {
-      req_sh = r;
-      uint32_t st = 0;
+      uint32_t status = 0;
+      Settings x{-1.f, 1.f, 0.f, 0};
       if (r >= 0) {
-        if (request_rows(a.qsl, r, a.T).bad) st |= PE_ST_ROWS_RANGE;
-        const float t = a.temperature ? a.temperature[r] : 1.f;
-        if (!(t >= 0.f)) st |= PE_ST_SAMPLING;
-        const int k = a.top_k ? a.top_k[r] : 0;
-        const float p = a.top_p ? a.top_p[r] : 1.f, mp = a.min_p ? a.min_p[r] : 0.f;
-        if (p != p || mp != mp) st |= PE_ST_SAMPLING;
-        set_sh[0] = temperature_of(t);
-        set_sh[1] = __int_as_float(k <= 0 || k >= a.V ? 0 : k);
-        set_sh[2] = p < 1.f ? p : 1.f;   // (NaN: 1)
-        set_sh[3] = mp > 0.f ? mp : 0.f;  // (NaN: 0)
+        x = settings_of(a, r, status);
+        if (request_rows(a.qsl, r, a.T).bad) status |= PE_ST_ROWS_RANGE;
       }
-      if (rank == 0 && st) set_status(a.status, st);
+      set_sh = x;
+      if (part == 0) {
+        a.set[row] = x;
+        if (status) set_status(a.status, status);
+        if (row == 0) *a.todo_n = 0u;
+      }
     }
   }
-  if (tid < kBins) {
-    h_cnt[tid] = 0;
-    h_least[tid] = 0xffffffffu;
-    h_mass[tid] = 0;
-  }
-  if (tid == 0) n_list = n_mine = 0;
-  // ---------------- the slice, its largest logit
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   __syncthreads();
-  if (req_sh < 0) return;  // (the whole cluster)
+  const Settings st = set_sh;
+  if (st.temp < 0.f) return;
+  Part out{-INFINITY, 0.f, 0.f, 0.f, -1, 0, 0ull};
+  const bool free = st.k == 0 && st.p >= 1.f && st.mp == 0.f;
   float m = -INFINITY;
-  for (int v = s.v0 + tid; v < s.v1; v += kUnroll * kThreads) {
-    uint4 u[kUnroll];
+  if (st.temp == 0.f) {
+    // the first vector that holds this thread's greatest value stays in registers (a NaN
+    // counts as the greatest); its lowest index with the value is found at the end
+    int bj = -1;
+    uint4 bv = no_tokens<T>();
+    for (int j = tid; j < n; j += kUnroll * kThreads) {
 #pragma unroll
-    for (int x = 0; x < kUnroll; ++x)
-      if (v + x * kThreads < s.v1) u[x] = s.load(v + x * kThreads);
+      for (int x = 0; x < kUnroll; ++x) {
+        const float vm = vec_max<T>(u[x]);
+        const int jx = j + x * kThreads, jn = jx + kUnroll * kThreads;
+        if (jx < n && (bj < 0 || (!(vm <= m) && m == m))) {
+          m = vm;
+          bj = jx;
+          bv = u[x];
+        }
+        if (jn < n) u[x] = s.load(v0 + jn);
+      }
+    }
+    unsigned long long k = 0ull;
+    if (bj >= 0) {
+      float f[kVec];
+      unpack16<T>(bv, f);
+      const int t0 = s.token(v0 + bj);
 #pragma unroll
-    for (int x = 0; x < kUnroll; ++x)
-      if (v + x * kThreads < s.v1) {
+      for (int e = kVec - 1; e >= 0; --e)
+        if (t0 + e >= 0 && t0 + e < a.V && (m != m ? f[e] != f[e] : f[e] == m))
+          k = argmax_key(m, static_cast<uint32_t>(t0 + e));
+    }
+    k = warp_max_u64(k);
+    if (lane == 0) warp_k[warp] = k;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) k = max(k, warp_k[w]);
+    out.key = k;
+  } else if (free) {
+    // (l - m) / T + g with the thread's largest logit so far: exact near it, and no quotient
+    // passes fp32's range upwards
+    const Noise<T> noise(a, row, s.shift);
+    const float it = 1.f / st.temp;
+    float bs = -INFINITY;
+    int bv = -1;
+    for (int j = tid; j < n; j += kRaceUnroll * kThreads) {
+      if (j != tid) {
+#pragma unroll
+        for (int x = 0; x < kRaceUnroll; ++x)
+          u[x] = j + x * kThreads < n ? s.load(v0 + j + x * kThreads) : no_tokens<T>();
+      }
+      float g[kRaceUnroll][kVec];
+#pragma unroll
+      for (int x = 0; x < kRaceUnroll; ++x)
+        if (j + x * kThreads < n) noise.load(s.token(v0 + j + x * kThreads), a.V, g[x]);
+      float mn = m;
+#pragma unroll
+      for (int x = 0; x < kRaceUnroll; ++x) mn = max_nan(mn, vec_max<T>(u[x]));
+      const float off = mn == -INFINITY ? 0.f : mn;
+      if (mn > m && bs < INFINITY) bs = fmaf(m - mn, it, bs);
+      m = mn;
+#pragma unroll
+      for (int x = 0; x < kRaceUnroll; ++x) {
+        if (j + x * kThreads >= n) continue;
+        float f[kVec], best = -INFINITY;
+        unpack16<T>(u[x], f);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) best = fmaxf(best, fmaf(f[e] - off, it, g[x][e]));
+        if (best > bs || bv < 0) {
+          bs = fmaxf(bs, best);
+          bv = j + x * kThreads;
+        }
+      }
+    }
+    out.m = cta_max<kWarps>(m, warp_m);
+    // The threads whose best is within reach of the CTA's (a score's rounding is 2^-23 of its
+    // terms; noise past 128 is infinite) compare in 64 bits, token by token.
+    const float far = m == out.m ? 0.f : (m - out.m) * it;
+    if (bs < INFINITY) bs += far;
+    float top = warp_max(bs);
+    __syncthreads();
+    if (lane == 0) warp_m[warp] = top;
+    __syncthreads();
+    top = warp_m[0];
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, warp_m[w]);
+    unsigned long long k = 0ull;
+    int bi = 0x7fffffff;
+    float bx = 0.f, bg = 0.f;
+    if (bv >= 0 && fabsf(out.m) < INFINITY &&
+        (bs >= top || bs >= top - 1e-6f * (fabsf(top) + fabsf(bs) + fabsf(far) + 128.f))) {
+      float f[kVec], g[kVec];
+      unpack16<T>(s.load(v0 + bv), f);
+      const int t0 = s.token(v0 + bv);
+      noise.load(t0, a.V, g);
+      for (int e = 0; e < kVec; ++e) {
+        const unsigned long long o = f[e] == -INFINITY ? 0ull : exact_score(f[e], g[e], out.m, st.temp);
+        if (o > k) {
+          k = o;
+          bi = t0 + e;
+          bx = f[e];
+          bg = g[e];
+        }
+      }
+    }
+    unsigned long long best = k;
+    int winner = bi;
+    cta_best<kWarps>(best, winner, warp_k, warp_i);
+    out.idx = best ? winner : -1;
+    // (its thread writes the part)
+    if (best ? bi == winner : tid == 0) {
+      out.x = bx;
+      out.g = bg;
+      a.stat[static_cast<size_t>(row) * a.parts + part] = out;
+    }
+  } else if (st.k > 0 || st.p >= 1.f) {
+    for (int j = tid; j < n; j += kUnroll * kThreads) {
+#pragma unroll
+      for (int x = 0; x < kUnroll; ++x) {
         m = max_nan(m, vec_max<T>(u[x]));
-        if (a.resident) held[v + x * kThreads - s.v0] = u[x];
+        const int jn = j + (x + kUnroll) * kThreads;
+        u[x] = jn < n ? s.load(v0 + jn) : no_tokens<T>();
       }
-  }
-  if (a.resident) s.held = held;
-  {
-    float wm = m, lo = m > -INFINITY ? m : INFINITY;
+    }
+  } else {
+    // sum of 2^((l - m) c), c = log2(e) / T: the difference is exact near the largest logit
+    const float c = scale_of(st.temp);
+    const uint64_t c2 = pack_f32x2(c, c);
+    float sum = 0.f;
+    for (int j = tid; j < n; j += kUnroll * kThreads) {
+      // one maximum and one rescaling for the kUnroll vectors
+      float mn = m;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      wm = max_nan(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    }
-    if (lane == 0) {
-      warp_m[warp] = wm;
-      warp_lo[warp] = lo;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      wm = lane < kWarps ? warp_m[lane] : -INFINITY;
-      lo = lane < kWarps ? warp_lo[lane] : INFINITY;
+      for (int x = 0; x < kUnroll; ++x) mn = max_nan(mn, vec_max<T>(u[x]));
+      const float off = mn == -INFINITY ? 0.f : mn;
+      sum *= ex2((m - off) * c);
+      m = mn;
+      const uint64_t off2 = pack_f32x2(-off, -off);
+      uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        wm = max_nan(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      for (int x = 0; x < kUnroll; ++x) {
+        float f[kVec];
+        unpack16<T>(u[x], f);
+        const int jn = j + (x + kUnroll) * kThreads;
+        u[x] = jn < n ? s.load(v0 + jn) : no_tokens<T>();
+#pragma unroll
+        for (int e = 0; e < kVec; e += 2) {
+          float p, q;
+          unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(f[e], f[e + 1]), off2), c2), p, q);
+          acc[e / 2 & 1] = add_f32x2(acc[e / 2 & 1], pack_f32x2(ex2(p), ex2(q)));
+        }
       }
-      if (lane < nr) {
-        put32(&sh.from[rank].m, lane, __float_as_uint(wm));
-        put32(&sh.from[rank].lo, lane, __float_as_uint(lo));
-      }
+      float s0, s1;
+      unpack_f32x2(add_f32x2(acc[0], acc[1]), s0, s1);
+      sum += s0 + s1;
     }
+    out.m = cta_max<kWarps>(m, warp_m);
+    out.s = static_cast<float>(
+        cta_sum<kWarps>(m > -INFINITY ? sum * ex2((m - out.m) * c) : 0.f, warp_d));
   }
-  row_sync();
-  float M = -INFINITY, lo = INFINITY;
-  for (uint32_t i = 0; i < nr; ++i) {
-    M = max_nan(M, sh.from[i].m);
-    lo = fminf(lo, sh.from[i].lo);
+  if (!free && st.temp != 0.f) {
+    if (st.k > 0 || st.p >= 1.f) out.m = cta_max<kWarps>(m, warp_m);
+    float t = m;
+    for (int o = 1; o < 1 << a.gshift; o <<= 1) t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, o));
+    if ((lane & ((1 << a.gshift) - 1)) == 0)
+      a.top[(static_cast<size_t>(row) * a.parts + part) * (kThreads >> a.gshift) + (tid >> a.gshift)] = t;
   }
-  const float temp = set_sh[0], top_p = set_sh[2], min_p = set_sh[3];
-  const int top_k = __float_as_int(set_sh[1]);
+  if ((!free || st.temp == 0.f) && tid == 0) a.stat[static_cast<size_t>(row) * a.parts + part] = out;
+}
 
-  // The CTA's best (order, index), and of the cluster; rank 0 writes the token.
-  auto finish = [&](unsigned long long k, int i, bool cluster) {
-    warp_best(k, i);
-    if (lane == 0) {
-      warp_k[warp] = k;
-      warp_i[warp] = i;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      k = lane < kWarps ? warp_k[lane] : 0ull;
-      i = lane < kWarps ? warp_i[lane] : 0x7fffffff;
-      warp_best(k, i);
-      if (cluster && lane == 0) {
-        put64(&best_of[rank].order, 0, k);
-        put32(&best_of[rank].idx, 0, i);
-      }
-    }
-    if (cluster) {
-      row_sync();
-      if (rank == 0 && warp == 0) {
-        k = lane < nr ? best_of[lane].order : 0ull;
-        i = lane < nr ? best_of[lane].idx : 0x7fffffff;
-        warp_best(k, i);
-      }
-    }
-    if (rank == 0 && tid == 0) {
+// Candidates of a row, all tokens that come before some place in its order, and what comes
+// before them (weights 2^-40): which are kept, and the best score.
+struct Cands {
+  unsigned long long key[kList];  // argmax_key: larger comes first
+  unsigned long long q[kList];    // weight
+  float g[kList];
+};
+constexpr float kOne = 0x1p40f;
+
+// Shared memory of the cut kernel.
+struct __align__(16) CutShared {
+  float m[kWarps];
+  double d[kWarps];
+  unsigned long long k[kWarps];
+  int i[kWarps];
+  int n, n_groups, enough;
+  uint32_t bound;
+  float top[kGroups];
+  union {
+    struct {
+      uint32_t cnt[kBins], least[kBins];  // of the groups' largest logits; order of the least
+      unsigned long long mass[kBins];
+    } h;
+    Cands c;
+  };
+  uint16_t group[kGroupList];
+};
+
+// The answer of a row from its parts.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) sample_cut_kernel(const SampleArgs a) {
+  constexpr int kVec = 16 / sizeof(T);
+  __shared__ CutShared sh;
+  pdl_trigger();
+  pdl_wait();
+  const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Settings st = a.set[row];
+  if (st.temp < 0.f) return;
+  const Part* stat = a.stat + static_cast<size_t>(row) * a.parts;
+  auto answer = [&](unsigned long long k, int i) {
+    cta_best<kWarps>(k, i, sh.k, sh.i);
+    if (tid == 0) {
       a.token[row] = k ? i : -1;
       if (!k) set_status(a.status, PE_ST_SAMPLING);
     }
   };
-
-  // ---------------- greedy: the first token with the largest logit
-  if (temp == 0.f) {
-    int first = 0x7fffffff;
-    if (m == M || M != M) {
-      for (int v = s.v0 + tid; v < s.v1 && first == 0x7fffffff; v += kThreads) {
-        float f[kVec];
-        unpack16<T>(s.get(v), f);
-#pragma unroll
-        for (int e = kVec - 1; e >= 0; --e) {
-          const int t = s.token(v) + e;
-          if ((M != M ? f[e] != f[e] : f[e] == M) && t >= 0 && t < a.V) first = t;
-        }
-      }
-    }
-    finish(first < 0x7fffffff ? 1ull : 0ull, first, true);
-    return;
-  }
-  if (!(fabsf(M) < INFINITY)) {  // no distribution
-    if (rank == 0 && tid == 0) {
-      a.token[row] = -1;
-      set_status(a.status, PE_ST_SAMPLING);
-    }
-    return;
-  }
-  const float c = scale_of(temp), it = 1.f / temp;
-  const float* noise = a.gumbel + row * a.ld_g;
-  auto exact_score = [&](float x, float g) {
-    return score_order((static_cast<double>(x) - static_cast<double>(M)) / static_cast<double>(temp) + g);
-  };
-
-  // Race over the slice's tokens that come no later than the cut (key 0: over all), with a
-  // weight of at least min_p.  A thread keeps its best score in fp32; the threads whose best
-  // is within reach of the CTA's (a score's rounding is 2^-23 of its two terms; noise past 128
-  // is infinite) compare in 64 bits.
-  auto race = [&](uint32_t key, bool all, int ties) {
-    const bool wide = !((reinterpret_cast<uintptr_t>(noise) - s.shift * 4u) & 15u);
-    float bs = -INFINITY, bx = 0.f, bg = 0.f;
-    int bi = 0x7fffffff, seen = 0;  // seen: tokens at the cut before this trip's
-    for (int vb = s.v0; vb < s.v1; vb += kThreads) {
-      const int v = vb + tid;
-      float f[kVec], g[kVec];
-      int eq = 0;
-      const int t0 = s.token(v);
-      if (v < s.v1) {
-        unpack16<T>(s.get(v), f);
-        bool any = false;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          const uint32_t o = argmax_order(f[e]);
-          if (!all && o == key) ++eq;
-          if (o < key || (min_p > 0.f && f[e] != M && ex2((f[e] - M) * c) < min_p)) f[e] = -INFINITY;
-          any |= f[e] > -INFINITY;
-        }
-        if (any) {
-          if (wide && t0 >= 0 && t0 + kVec <= a.V) {
-#pragma unroll
-            for (int e = 0; e < kVec; e += 4) unpack16<float>(ld_stream16(noise + t0 + e), g + e);
-          } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) g[e] = f[e] > -INFINITY ? noise[t0 + e] : 0.f;
-          }
-        }
-      }
-      int place = 0;
-      if (!all) {  // which of the equal ones are the first
-        int incl = eq;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        __syncthreads();
-        if (lane == 31) warp_i[warp] = incl;
-        __syncthreads();
-        place = seen + incl - eq;
-        for (int w = 0; w < kWarps; ++w) {
-          if (w < warp) place += warp_i[w];
-          seen += warp_i[w];
-        }
-      }
-      if (v < s.v1) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          if (!all && argmax_order(f[e]) == key && place++ >= ties) continue;
-          const float sc = f[e] > -INFINITY ? fmaf(f[e] - M, it, g[e]) : -INFINITY;
-          if (sc > bs) {
-            bs = sc;
-            bi = t0 + e;
-            bx = f[e];
-            bg = g[e];
-          }
-        }
-      }
-    }
-    __syncthreads();
-    const float wt = warp_max(bs);
-    if (lane == 0) warp_m[warp] = wt;
-    __syncthreads();
-    float top = warp_m[0];
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, warp_m[w]);
+  if (st.temp == 0.f) {
     unsigned long long k = 0ull;
-    if (bs > -INFINITY && (bs == top || bs >= top - 1e-6f * (fabsf(top) + fabsf(bs) + 128.f)))
-      k = exact_score(bx, bg);
-    else
-      bi = 0x7fffffff;
-    finish(k, bi, true);
-  };
-
-  const bool cut_k = top_k > 0, cut_p = top_p < 1.f;
-  if (!cut_k && !cut_p && min_p == 0.f) {
-    race(0u, true, 0);
+    for (int i = tid; i < a.parts; i += kThreads) k = max(k, __ldcg(&stat[i].key));
+    answer(k, static_cast<int>(~static_cast<uint32_t>(k)));
     return;
   }
-
-  // ---------------- a bound from below for the cut
-  const float span = M - lo;
-  const float scale = span > 0.f && span < INFINITY ? fminf(kBins / span, 1e30f) : 0.f;
-  float bound = -INFINITY;
-  double z_row = 0.;  // the weight of the whole row, where no top-k is set
-  bool have_bound = false;
-  if (cut_k || cut_p) {
-    double z = 0.;
-    if (!cut_k) {  // the weight of the whole row
-      float z32 = 0.f;
-      for (int v = s.v0 + tid; v < s.v1; v += kThreads) {
-        float f[kVec], w = 0.f;
-        unpack16<T>(s.get(v), f);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) w += ex2((f[e] - M) * c);
-        z32 += w;
+  float M = -INFINITY;
+  for (int i = tid; i < a.parts; i += kThreads) M = max_nan(M, __ldcg(&stat[i].m));
+  M = cta_max<kWarps>(M, sh.m);
+  if (!(fabsf(M) < INFINITY)) {  // no distribution
+    answer(0ull, -1);
+    return;
+  }
+  const bool cut_k = st.k > 0, cut_p = st.p < 1.f;
+  if (!cut_k && !cut_p && st.mp == 0.f) {
+    unsigned long long k = 0ull;
+    int best = 0x7fffffff;
+    for (int i = tid; i < a.parts; i += kThreads) {
+      const int t = __ldcg(&stat[i].idx);
+      const unsigned long long o = t < 0 ? 0ull : exact_score(__ldcg(&stat[i].x), __ldcg(&stat[i].g), M, st.temp);
+      if (o > k || (o == k && t < best)) {
+        k = o;
+        best = t;
       }
-      z = cta_sum(z32, warp_d);
     }
-    if (m > -INFINITY) {
-      const int b = min(kBins - 1, static_cast<int>((M - m) * scale));
-      atomicAdd(&h_cnt[b], 1u);
-      atomicMin(&h_least[b], argmax_order(m));
-      if (!cut_k) atomicAdd(&h_mass[b], static_cast<unsigned long long>(ex2((m - M) * c) * 0x1p40f));
+    answer(k, best);
+    return;
+  }
+  const float c = scale_of(st.temp);
+  double z = 0.;  // the weight of the whole row
+  if (cut_p && !cut_k) {
+    for (int i = tid; i < a.parts; i += kThreads) {
+      const float m = __ldcg(&stat[i].m);
+      if (m > -INFINITY) z += static_cast<double>(__ldcg(&stat[i].s) * ex2((m - M) * c));
+    }
+    z = cta_sum<kWarps>(z, sh.d);
+  }
+  // ---------------- a bound from below for the cut
+  const int gpp = kThreads >> a.gshift, groups = a.parts * gpp;  // groups of a part, of the row
+  const float* top = a.top + static_cast<size_t>(row) * groups;
+  float lo = INFINITY;
+  for (int i = tid; i < groups; i += kThreads) {
+    const float t = __ldcg(top + i);
+    sh.top[i] = t;
+    if (t > -INFINITY) lo = fminf(lo, t);
+  }
+  for (int b = tid; b < kBins; b += kThreads) {
+    sh.h.cnt[b] = 0;
+    sh.h.least[b] = 0xffffffffu;
+    sh.h.mass[b] = 0;
+  }
+  if (tid == 0) {
+    sh.n = sh.n_groups = 0;
+    sh.enough = 0;
+  }
+  lo = -cta_max<kWarps>(-lo, sh.m);
+  float bound = -INFINITY;
+  if (cut_k || cut_p) {
+    // bins of the range that the groups' largest logits span
+    const float span = M - lo;
+    const float scale = span > 0.f && span < INFINITY ? fminf(kBins / span, 1e30f) : 0.f;
+    for (int i = tid; i < groups; i += kThreads) {
+      const float t = sh.top[i];
+      if (t > -INFINITY) {
+        const int b = min(kBins - 1, static_cast<int>((M - t) * scale));
+        atomicAdd(&sh.h.cnt[b], 1u);
+        atomicMin(&sh.h.least[b], argmax_order(t));
+        if (!cut_k) atomicAdd(&sh.h.mass[b], static_cast<unsigned long long>(ex2((t - M) * c) * kOne));
+      }
     }
     __syncthreads();
-    for (uint32_t i = tid; i < kBins * nr; i += kThreads) {
-      const uint32_t b = i % kBins, to = i / kBins;
-      put32(&sh.from[rank].cnt[b], to, h_cnt[b]);
-      put32(&sh.from[rank].least[b], to, h_least[b]);
-      put64(&sh.from[rank].mass[b], to, h_mass[b]);
-    }
-    if (tid < nr) put64(&sh.from[rank].z, tid, __double_as_longlong(z));
-    row_sync();
-    for (uint32_t i = 0; i < nr; ++i) z_row += sh.from[i].z;
     if (warp == 0) {
-      // (a margin for the roundings of the sums)
-      const double need = cut_k ? static_cast<double>(top_k) : z_row * fmaxf(top_p, 0.f) * 1.000001;
-      // two bins a lane
-      double have[2];
-      uint32_t least[2];
+      // The first bin with which there are k, or p of the weight; for want of the latter as many
+      // as can be compared (their weight tells, below).
+      constexpr int kPer = kBins / 32;
+      double have[kPer], mine = 0.;
+      uint32_t count = 0;
+      const double need = cut_k ? static_cast<double>(st.k) : z * fmaxf(st.p, 0.f) * 1.000001 * kOne;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        unsigned long long q = 0;
-        least[e] = 0xffffffffu;
-        for (uint32_t i = 0; i < nr; ++i) {
-          q += cut_k ? sh.from[i].cnt[2 * lane + e] : sh.from[i].mass[2 * lane + e];
-          least[e] = min(least[e], sh.from[i].least[2 * lane + e]);
-        }
-        have[e] = cut_k ? static_cast<double>(q) : static_cast<double>(q) * 0x1p-40;
+      for (int e = 0; e < kPer; ++e) {
+        const int b = lane * kPer + e;
+        have[e] = cut_k ? static_cast<double>(sh.h.cnt[b]) : static_cast<double>(sh.h.mass[b]);
+        mine += have[e];
+        count += sh.h.cnt[b];
       }
-      double before = have[0] + have[1];
+      double before = mine;
+      uint32_t n_before = count;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const double y = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += y;
+        const uint32_t n = __shfl_up_sync(0xffffffffu, n_before, o);
+        if (lane >= o) {
+          before += y;
+          n_before += n;
+        }
       }
-      before -= have[0] + have[1];
-      // the first bin with which there is enough
-      const bool at0 = before + have[0] >= need, at1 = before + have[0] + have[1] >= need;
-      const unsigned hit = __ballot_sync(0xffffffffu, at1);
-      const int last = hit ? __ffs(hit) - 1 : 32;
+      before -= mine;
+      n_before -= count;
+      int last = kBins, most = -1;  // the bin; the last one with few enough groups before its end
+#pragma unroll
+      for (int e = kPer - 1; e >= 0; --e) {
+        double upto = before;
+        uint32_t n = n_before;
+        for (int f = 0; f <= e; ++f) {
+          upto += have[f];
+          n += sh.h.cnt[lane * kPer + f];
+        }
+        if (upto >= need) last = lane * kPer + e;
+        if (n <= kList / 2 && most < 0) most = lane * kPer + e;
+      }
+      last = __reduce_min_sync(0xffffffffu, last);
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (last == kBins && !cut_k) last = most;
       uint32_t o = 0xffffffffu;
-      if (lane < last) o = min(least[0], least[1]);
-      if (lane == last) o = at0 ? least[0] : min(least[0], least[1]);
+      for (int e = 0; e < kPer; ++e)
+        if (lane * kPer + e <= last) o = min(o, sh.h.least[lane * kPer + e]);
       o = __reduce_min_sync(0xffffffffu, o);
       if (lane == 0) {
-        cut_sh[0] = hit != 0 && o != 0xffffffffu;
-        cut_sh[1] = o;
+        sh.bound = o;
+        sh.enough = last < kBins && last >= 0 && o != 0xffffffffu;
       }
     }
     __syncthreads();
-    have_bound = cut_sh[0];
-    if (have_bound) bound = logit_of(cut_sh[1]);
-  } else {
-    have_bound = true;  // min-p alone: the weights say it
+    if (sh.enough) bound = logit_of(sh.bound);
+  } else if (tid == 0) {
+    sh.enough = 1;  // min-p alone: the weights say it
   }
-
-  // ---------------- the candidates
-  if (have_bound) {
+  __syncthreads();
+  bool done = sh.enough;
+  if (done) {
+    // ---------------- the groups that have a token from the bound on, and those tokens
     const bool by_w = !cut_k && !cut_p;
-    for (int v = s.v0 + tid; v < s.v1; v += kThreads) {
-      const uint4 u = s.get(v);
-      const float vm = vec_max<T>(u);
-      if (by_w ? ex2((vm - M) * c) < min_p && vm != M : vm < bound) continue;
-      float f[kVec];
-      unpack16<T>(u, f);
+    auto in = [&](float x) { return by_w ? x == M || ex2((x - M) * c) >= st.mp : x >= bound; };
+    for (int i = tid; i < groups; i += kThreads)
+      if (sh.top[i] > -INFINITY && in(sh.top[i])) {
+        const int at = atomicAdd(&sh.n_groups, 1);
+        if (at < kGroupList) sh.group[at] = static_cast<uint16_t>(i);
+      }
+    __syncthreads();
+    const Row<T> s(a, row);
+    const int nv = s.vectors(), n_groups = sh.n_groups;
+    if (n_groups <= kGroupList) {
+      // a group's vectors: of each trip over the part, as many as it has threads
+      const int trips = (a.part + kThreads - 1) / kThreads, per = trips << a.gshift;
+      for (int i = tid; i < n_groups * per; i += kThreads) {
+        const int g = sh.group[i / per], j = i % per;
+        const int at = (j >> a.gshift) * kThreads + ((g % gpp) << a.gshift) + (j & ((1 << a.gshift) - 1));
+        const int v = g / gpp * a.part + at;
+        if (at >= a.part || v >= nv) continue;
+        const uint4 u = s.load(v);
+        if (!in(vec_max<T>(u))) continue;
+        float f[kVec];
+        unpack16<T>(u, f);
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const bool in = by_w ? f[e] == M || ex2((f[e] - M) * c) >= min_p : f[e] >= bound;
-        if (in && f[e] > -INFINITY) {
-          const uint32_t at = atomicAdd(&n_mine, 1u);
-          if (at < kList) {
-            mine_i[at] = s.token(v) + e;
-            mine_x[at] = f[e];
+        for (int e = 0; e < kVec; ++e)
+          if (f[e] > -INFINITY && in(f[e])) {
+            const int at2 = atomicAdd(&sh.n, 1);
+            if (at2 < kList) sh.c.key[at2] = argmax_key(f[e], static_cast<uint32_t>(s.token(v) + e));
+          }
+      }
+    }
+    __syncthreads();
+    const int n = sh.n;
+    done = n_groups <= kGroupList && n <= kList;
+    if (done) {
+      // ---------------- rank and weight before each
+      constexpr int kPer = kList / kThreads;
+      const float* noise = a.gumbel + row * a.ld_g;
+      unsigned long long key[kPer], before[kPer];
+      float g[kPer];
+      int place[kPer];
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) {
+        const int i = tid + x * kThreads;
+        key[x] = before[x] = 0ull;
+        place[x] = 0;
+        g[x] = 0.f;
+        if (i < n) {
+          key[x] = sh.c.key[i];
+          g[x] = noise[~static_cast<uint32_t>(key[x])];
+          sh.c.q[i] = static_cast<unsigned long long>(ex2((logit_of(static_cast<uint32_t>(key[x] >> 32)) - M) * c) * kOne);
+        }
+      }
+      __syncthreads();
+      if ((tid & ~31) < n) {
+        for (int j = 0; j < n; ++j) {
+          const unsigned long long kj = sh.c.key[j], qj = sh.c.q[j];
+#pragma unroll
+          for (int x = 0; x < kPer; ++x)
+            if (kj > key[x]) {
+              ++place[x];
+              before[x] += qj;
+            }
+        }
+      }
+      double sum = z * kOne;  // what top-p is a share of
+      if (cut_p) {
+        double mine = 0.;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x)
+          if (tid + x * kThreads < n && (!cut_k || place[x] < st.k)) mine += static_cast<double>(sh.c.q[tid + x * kThreads]);
+        mine = cta_sum<kWarps>(mine, sh.d);
+        if (cut_k)
+          sum = mine;
+        else
+          done = mine >= sum * fmaxf(st.p, 0.f) * 1.000001;  // (else the cut lies behind them)
+      }
+      if (done) {
+        unsigned long long best = 0ull;
+        int bi = 0x7fffffff;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+          const int i = tid + x * kThreads;
+          if (i >= n) continue;
+          const float l = logit_of(static_cast<uint32_t>(key[x] >> 32));
+          const bool first = place[x] == 0;
+          if ((cut_k && place[x] >= st.k) ||
+              (cut_p && !first && static_cast<double>(before[x]) >= static_cast<double>(st.p) * sum) ||
+              (!first && ex2((l - M) * c) < st.mp))
+            continue;
+          const unsigned long long o = exact_score(l, g[x], M, st.temp);
+          const int t = static_cast<int>(~static_cast<uint32_t>(key[x]));
+          if (o > best || (o == best && t < bi)) {
+            best = o;
+            bi = t;
           }
         }
+        answer(best, bi);
       }
-    }
-    __syncthreads();
-    const uint32_t n = n_mine;
-    if (tid < nr) put32(&sh.from[rank].cand, tid, n);
-    if (n <= kList) {
-      __shared__ uint32_t start_sh;
-      if (tid == 0) start_sh = n ? add32(&n_list, 0, n) : 0u;
-      __syncthreads();
-      const uint32_t at = start_sh + tid;
-      if (tid < n && at < kList) {
-        const int t = mine_i[tid];
-        put64(&list[at].key, 0, argmax_key(mine_x[tid], static_cast<uint32_t>(t)));
-        put32(&list[at].g, 0, __float_as_uint(noise[t]));
-      }
-    }
-    row_sync();
-    uint32_t total = 0;
-    for (uint32_t i = 0; i < nr; ++i) total += min(static_cast<uint32_t>(sh.from[i].cand), kList + 1u);
-    if (total <= kList) {
-      if (rank != 0) return;
-      // ---------------- rank and weight before each candidate
-      unsigned long long key = 0ull, before = 0ull;
-      int place = 0;
-      float x = -INFINITY, w = 0.f, g = 0.f;
-      if (tid < total) {
-        key = list[tid].key;
-        g = list[tid].g;
-        x = logit_of(static_cast<uint32_t>(key >> 32));
-        w = ex2((x - M) * c);
-      }
-      __shared__ unsigned long long q_sh[kList];
-      const unsigned long long q = static_cast<unsigned long long>(w * 0x1p40f);
-      q_sh[tid] = q;
-      __syncthreads();
-      if ((tid & ~31) < total) {
-        for (uint32_t j = 0; j < total; ++j) {
-          const bool ahead = list[j].key > key;
-          place += ahead;
-          before += ahead ? q_sh[j] : 0ull;
-        }
-      }
-      bool keep = tid < total && (!cut_k || place < top_k);
-      if (cut_p) {
-        const double sum = cut_k ? cta_sum(keep ? static_cast<double>(q) : 0., warp_d) : z_row * 0x1p40;
-        keep = keep && (place == 0 || static_cast<double>(before) < static_cast<double>(top_p) * sum);
-      }
-      keep = keep && (place == 0 || w >= min_p);
-      finish(keep ? exact_score(x, g) : 0ull, static_cast<int>(~static_cast<uint32_t>(key)), false);
-      return;
     }
   }
-
-  // ---------------- the cut digit by digit
-  // By all CTAs of the row alike: among the tokens whose order starts with the digits found so
-  // far, counts and weights per next digit; the cut lies in the last digit with a kept token,
-  // that is one with less than k tokens and less than `most` of weight before it.
-  auto weight_bits = [&](float x) { return static_cast<uint32_t>(ex2((x - M) * c) * 0x1p31f); };
-  auto descend = [&](int k, double frac, double z, int& my_ties) {
-    uint32_t prefix = 0;
-    unsigned long long count = 0, mass = 0;  // before the prefix
-    unsigned long long n_eq = 0;
-    double most = INFINITY;
-    for (int level = 0; level < 4; ++level) {
-      const int lshift = 24 - 8 * level;
-      uint32_t (*h)[4] = sh.digits[level & 1];
-      __syncthreads();
-      for (int i = tid; i < kDigits * 4; i += kThreads) (&h[0][0])[i] = 0;
-      __syncthreads();
-      for (int v = s.v0 + tid; v < s.v1; v += kThreads) {
-        float f[kVec];
-        unpack16<T>(s.get(v), f);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          const uint32_t o = argmax_order(f[e]);
-          if (f[e] == -INFINITY || (level > 0 && o >> (lshift + 8) != prefix >> (lshift + 8))) continue;
-          const uint32_t d = o >> lshift & 0xffu, q = weight_bits(f[e]);
-          atomicAdd(&h[d][0], 1u);
-          atomicAdd(&h[d][1], q & 0x7ffu);
-          atomicAdd(&h[d][2], q >> 11 & 0x3ffu);
-          atomicAdd(&h[d][3], q >> 21);
-        }
-      }
-      row_sync();
-      // the row's sums, from the largest digit down; thread t has digit 255 - t
-      unsigned long long n_d = 0, m_d = 0;
-      uint32_t own = 0;
-      if (tid < kDigits) {
-        const int d = kDigits - 1 - tid;
-        own = h[d][0];
-        for (uint32_t i = 0; i < nr; ++i) {
-          n_d += get32(&h[d][0], i);
-          m_d += get32(&h[d][1], i) + (static_cast<unsigned long long>(get32(&h[d][2], i)) << 11) +
-                 (static_cast<unsigned long long>(get32(&h[d][3], i)) << 21);
-        }
-      }
-      unsigned long long ni = n_d, mi = m_d;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y0 = __shfl_up_sync(0xffffffffu, ni, o), y1 = __shfl_up_sync(0xffffffffu, mi, o);
-        if (lane >= o) {
-          ni += y0;
-          mi += y1;
-        }
-      }
-      __shared__ unsigned long long scan_n[kWarps], scan_m[kWarps];
-      if (lane == 31) {
-        scan_n[warp] = ni;
-        scan_m[warp] = mi;
-      }
-      if (tid == 0) cut_n_sh = -1;
-      __syncthreads();
-      unsigned long long cb = count + ni - n_d, mb = mass + mi - m_d, m_all = 0;
-      for (int w = 0; w < kDigits / 32; ++w) {
-        if (w < warp) {
-          cb += scan_n[w];
-          mb += scan_m[w];
-        }
-        m_all += scan_m[w];
-      }
-      // (the first token is kept whatever top_p is: nothing is before it)
-      if (level == 0) most = frac >= 1. ? INFINITY : fmax(frac * (z >= 0. ? z : static_cast<double>(m_all)), 0.5);
-      const bool in = tid < kDigits && n_d > 0 && cb < static_cast<unsigned long long>(k) && static_cast<double>(mb) < most;
-      if (in) atomicMax(&cut_n_sh, tid);
-      __syncthreads();
-      if (tid == cut_n_sh) {
-        cut_sh[0] = static_cast<uint32_t>(kDigits - 1 - tid);
-        cut_sh[1] = own;
-        scan_n[0] = cb;
-        scan_m[0] = mb;
-        scan_n[1] = n_d;
-      }
-      __syncthreads();
-      prefix |= cut_sh[0] << lshift;
-      my_ties = static_cast<int>(cut_sh[1]);
-      count = scan_n[0];
-      mass = scan_m[0];
-      n_eq = scan_n[1];
-    }
-    Cut cut;
-    cut.key = prefix;
-    const uint32_t q = weight_bits(logit_of(prefix));
-    double t = static_cast<double>(n_eq);
-    t = fmin(t, static_cast<double>(k) - static_cast<double>(count));
-    if (most < INFINITY && q > 0) t = fmin(t, ceil((most - static_cast<double>(mass)) / q));
-    t = fmax(t, 1.);
-    cut.ties = static_cast<int>(t);
-    cut.all = t >= static_cast<double>(n_eq);
-    cut.mass = static_cast<double>(mass) + t * q;
-    return cut;
-  };
-  int ties = 0;
-  Cut cut{0u, 0, 1, 0.};
-  if (cut_k || cut_p) {
-    const int k = cut_k ? top_k : 0x7fffffff;
-    // top-p of what top-k leaves: the weight of that first
-    double z = -1.;
-    if (cut_k) {
-      cut = descend(k, 1., -1., ties);
-      z = cut.mass;
-    }
-    if (cut_p) cut = descend(k, static_cast<double>(top_p), z, ties);
-    if (!cut.all) {
-      // the CTAs' shares of the equal ones
-      __syncthreads();
-      if (tid == 0) cut_count_sh = ties;
-      row_sync();
-      int before = 0;
-      for (uint32_t i = 0; i < rank; ++i) before += static_cast<int>(get32(&cut_count_sh, i));
-      cut.ties = max(0, cut.ties - before);
-    }
-  }
-  race(cut.key, cut.all, cut.ties);
-  // (race ends behind a barrier of the cluster: no CTA reads another's memory after it)
+  if (!done && tid == 0) a.todo[atomicAdd(a.todo_n, 1u)] = row;
 }
 
-// CTAs of a row, and whether its slices fit in their shared memory: few CTAs, as long as
-// two of them fit on an SM, and more of them where the rows are too few for the SMs.
-constexpr int kSliceTwo = 80 * 1024, kSliceOne = 176 * 1024;
+// ------------------------------------------------------------------ wide kernel
 
-struct Split {
-  int ctas, resident;
-  size_t smem;
+PE_DEV uint32_t row_addr(const void* local, uint32_t rank) {
+  uint32_t remote;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+  return remote;
+}
+PE_DEV void put32(const void* local, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(row_addr(local, rank)), "r"(v) : "memory");
+}
+PE_DEV void put64(const void* local, uint32_t rank, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(row_addr(local, rank)), "l"(v) : "memory");
+}
+PE_DEV uint4 get128(const void* local, uint32_t rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(row_addr(local, rank))
+               : "memory");
+  return v;
+}
+// (all threads of all CTAs of the row)
+PE_DEV void row_sync() {
+  __syncwarp();
+  cluster_sync_all();
+}
+
+// The last kept token of a row: those whose argmax_key is no less are kept.
+struct Cut {
+  unsigned long long key;
+  double mass;  // weight of the kept ones, 2^-31
 };
-Split split_of(int T, int V, int esize, int num_sms) {
-  const int64_t bytes = static_cast<int64_t>(V) * esize + 32;
-  int64_t n = std::min<int64_t>((bytes + kSliceTwo - 1) / kSliceTwo, kMaxCluster);
-  while (n < kMaxCluster && static_cast<int64_t>(T) * (n + 1) <= 2 * num_sms && bytes / (n + 1) >= 8192) ++n;
-  Split s;
-  s.ctas = static_cast<int>(n);
-  const int64_t vecs = (bytes / 16 + 1 + n - 1) / n;
-  s.resident = vecs * 16 <= kSliceOne;
-  s.smem = s.resident ? static_cast<size_t>(vecs * 16) : 0;
-  return s;
+
+// Shared memory of a CTA of the wide kernel.  What the others of the row write or read there is
+// held twice and taken in turn: whoever writes a place again has met all of them at a barrier
+// since the last one read it.
+struct __align__(16) WideShared {
+  uint4 bins[2][kBins];  // count, sums of two or three parts of the weights' bits
+  float m[kCluster], lo[kCluster];               // of every CTA: largest and least finite logit
+  uint32_t least[2][kCluster], most[2][kCluster];  // ... orders of the cut's bin of the level before
+  unsigned long long best[kCluster];
+  int best_i[kCluster];
+  Cands c;               // the tokens of the cut's bin, of all CTAs
+  int tie;
+  // this CTA's own
+  unsigned long long scan_n[kWideWarps], scan_m[kWideWarps], k[kWideWarps];
+  float wm[kWideWarps], wl[kWideWarps];
+  uint32_t u[kWideWarps], v[kWideWarps];
+  int i[kWideWarps];
+  int digit, n_list;
+  unsigned long long count, mass, n_in;
+  uint32_t own, start;
+};
+
+// Sum over the CTA before this thread (wide kernel), and of all.
+PE_DEV int wide_before(int v, int* warps, int& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();
+  if (lane == 31) warps[warp] = incl;
+  __syncthreads();
+  int before = incl - v;
+  all = 0;
+  for (int w = 0; w < kWideWarps; ++w) {
+    if (w < warp) before += warps[w];
+    all += warps[w];
+  }
+  return before;
 }
 
 template <typename T>
-cudaError_t launch(const SampleArgs& a, size_t smem, cudaStream_t st) {
+__global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const SampleArgs a) {
+  constexpr int kVec = 16 / sizeof(T);
+  extern __shared__ uint4 held[];
+  __shared__ WideShared sh;
+  pdl_trigger();
+  // (every CTA of the cluster has to have begun before another one writes to it)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  pdl_wait();
+  const uint32_t rank = blockIdx.x % kCluster;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rows = static_cast<int>(__ldcg(a.todo_n)), step = gridDim.x / kCluster;
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  uint32_t turn = 0;
+  for (int item = blockIdx.x / kCluster; item < rows; item += step) {
+    const int row = __ldcg(a.todo + item);
+    const Settings st = a.set[row];
+    const Row<T> s(a, row);
+    const int nv = s.vectors(), per = (nv + kCluster - 1) / kCluster;
+    const int v0 = min(static_cast<int>(rank) * per, nv), v1 = min(v0 + per, nv);
+    auto get = [&](int v) { return a.resident ? held[v - v0] : s.load(v); };
+    // two parts of a weight's 31 bits do where a bin of a slice has at most 2^16 tokens
+    const bool small = per * kVec <= 65536;
+    __syncthreads();
+    // ---------------- the slice, its largest and least logit
+    float m = -INFINITY, lo = INFINITY;
+    for (int v = v0 + tid; v < v1; v += kUnroll * kWideThreads) {
+      uint4 u[kUnroll];
+#pragma unroll
+      for (int x = 0; x < kUnroll; ++x)
+        if (v + x * kWideThreads < v1) u[x] = s.load(v + x * kWideThreads);
+#pragma unroll
+      for (int x = 0; x < kUnroll; ++x)
+        if (v + x * kWideThreads < v1) {
+          if (a.resident) held[v + x * kWideThreads - v0] = u[x];
+          float f[kVec];
+          unpack16<T>(u[x], f);
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) {
+            m = fmaxf(m, f[e]);
+            if (f[e] > -INFINITY) lo = fminf(lo, f[e]);
+          }
+        }
+    }
+    m = warp_max(m);
+    lo = -warp_max(-lo);
+    if (lane == 0) {
+      sh.wm[warp] = m;
+      sh.wl[warp] = lo;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      m = warp_max(lane < kWideWarps ? sh.wm[lane] : -INFINITY);
+      lo = -warp_max(lane < kWideWarps ? -sh.wl[lane] : -INFINITY);
+      if (lane < kCluster) {
+        put32(&sh.m[rank], lane, __float_as_uint(m));
+        put32(&sh.lo[rank], lane, __float_as_uint(lo));
+      }
+    }
+    row_sync();
+    float M = -INFINITY;
+    lo = INFINITY;
+    for (int i = 0; i < kCluster; ++i) {
+      M = fmaxf(M, sh.m[i]);
+      lo = fminf(lo, sh.lo[i]);
+    }
+    const float c = scale_of(st.temp), it = 1.f / st.temp;
+    auto weight_bits = [&](float x) { return static_cast<uint32_t>(ex2((x - M) * c) * 0x1p31f); };
+
+    // ---------------- the cut: k tokens, and a share of the weight z (negative: of the row's)
+    auto find = [&](int k, double share, double z) {
+      Cut cut;
+      // Digits, small ones first in the order: of the distance from the largest logit in bins
+      // (an eighth of a factor 2 of weight each, or the row's range in kBins, whichever is finer:
+      // the last takes all that is farther) and finer ones inside the last level's; if the cut's
+      // bin stays too full without all in it being equal, of the bits of the logits' order.
+      const float span = M - lo;
+      float scale = span > 0.f && span < INFINITY ? fminf(kBins / span, 1e30f) : 0.f;
+      if (share < 1.) scale = fmaxf(scale, fminf(8.f * c, 1e30f));
+      double most = INFINITY;
+      for (int bits = 0; bits < 2; ++bits) {
+        int b0 = 0, b1 = 0;
+        uint32_t prefix = 0;
+        unsigned long long count = 0, mass = 0, n_in = ~0ull;
+        uint32_t own = 0, start = 0;
+        // the digit of a logit at this level, -1: it is not in the bins found so far
+        auto digit = [&](float x, int level) {
+          if (bits) {
+            const uint32_t o = argmax_order(x);
+            if (level > 0 && o >> (32 - 8 * level) != prefix >> (32 - 8 * level)) return -1;
+            return static_cast<int>(255u - (o >> (24 - 8 * level) & 255u));
+          }
+          float t = (M - x) * scale;
+          int b = min(kBins - 1, static_cast<int>(t));
+          if (level > 0) {
+            if (b != b0) return -1;
+            t = (t - static_cast<float>(b)) * kBins;
+            b = min(kBins - 1, static_cast<int>(t));
+          }
+          if (level > 1) {
+            if (b != b1) return -1;
+            t = (t - static_cast<float>(b)) * kBins;
+            b = min(kBins - 1, static_cast<int>(t));
+          }
+          return b;
+        };
+        for (int level = 0; level < (bits ? 5 : 4); ++level) {
+          // Counts and weights per digit (of the level behind the last: only whether all are equal)
+          const bool last = level == (bits ? 4 : 3);
+          uint4* bins = sh.bins[turn & 1];
+          uint32_t (*word)[4] = reinterpret_cast<uint32_t (*)[4]>(bins);
+          __syncthreads();
+          for (int i = tid; i < kBins; i += kWideThreads) bins[i] = make_uint4(0, 0, 0, 0);
+          __syncthreads();
+          uint32_t least = 0xffffffffu, greatest = 0;
+          for (int v = v0 + tid; v < v1; v += kWideThreads) {
+            float f[kVec];
+            unpack16<T>(get(v), f);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+              if (f[e] == -INFINITY) continue;
+              const int d = last ? (digit(f[e], level - 1) == (bits ? 255 - static_cast<int>(prefix & 255u) : sh.digit) ? 0 : -1)
+                                 : digit(f[e], level);
+              if (d < 0) continue;
+              if (level > 0) {
+                const uint32_t o = argmax_order(f[e]);
+                least = min(least, o);
+                greatest = max(greatest, o);
+              }
+              if (last) continue;
+              const uint32_t q = weight_bits(f[e]);
+              atomicAdd(&word[d][0], 1u);
+              if (small) {
+                atomicAdd(&word[d][1], q & 0xffffu);
+                atomicAdd(&word[d][2], q >> 16);
+              } else {
+                atomicAdd(&word[d][1], q & 0x7ffu);
+                atomicAdd(&word[d][2], q >> 11 & 0x3ffu);
+                atomicAdd(&word[d][3], q >> 21);
+              }
+            }
+          }
+          if (level > 0) {
+            least = __reduce_min_sync(0xffffffffu, least);
+            greatest = __reduce_max_sync(0xffffffffu, greatest);
+            if (lane == 0) {
+              sh.u[warp] = least;
+              sh.v[warp] = greatest;
+            }
+            __syncthreads();
+            if (warp == 0) {
+              least = __reduce_min_sync(0xffffffffu, lane < kWideWarps ? sh.u[lane] : 0xffffffffu);
+              greatest = __reduce_max_sync(0xffffffffu, lane < kWideWarps ? sh.v[lane] : 0u);
+              if (lane < kCluster) {
+                put32(&sh.least[turn & 1][rank], lane, least);
+                put32(&sh.most[turn & 1][rank], lane, greatest);
+              }
+            }
+          }
+          row_sync();
+          if (level > 0) {
+            least = 0xffffffffu;
+            greatest = 0;
+            for (int i = 0; i < kCluster; ++i) {
+              least = min(least, sh.least[turn & 1][i]);
+              greatest = max(greatest, sh.most[turn & 1][i]);
+            }
+            if (least == greatest) {
+              // ---------------- all in the cut's bin are equal: the first of them by index
+              ++turn;
+              const uint32_t q = weight_bits(logit_of(least));
+              double t = fmin(static_cast<double>(n_in), static_cast<double>(k) - static_cast<double>(count));
+              if (most < INFINITY && q > 0) t = fmin(t, ceil((most - static_cast<double>(mass)) / q));
+              t = fmax(t, 1.);
+              cut.key = static_cast<unsigned long long>(least) << 32;
+              cut.mass = static_cast<double>(mass) + t * q;
+              if (t >= static_cast<double>(n_in)) return cut;
+              const int want = static_cast<int>(t) - static_cast<int>(start);  // the want-th of this CTA's
+              if (want >= 1 && want <= static_cast<int>(own)) {
+                int seen = 0;
+                for (int vb = v0; vb < v1; vb += kWideThreads) {
+                  const int v = vb + tid;
+                  float f[kVec];
+                  int eq = 0, all;
+                  if (v < v1) {
+                    unpack16<T>(get(v), f);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) eq += argmax_order(f[e]) == least;
+                  }
+                  int place = seen + wide_before(eq, sh.i, all);
+                  seen += all;
+                  if (v < v1 && place < want && place + eq >= want) {
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e)
+                      if (argmax_order(f[e]) == least && ++place == want)
+                        for (int i = 0; i < kCluster; ++i) put32(&sh.tie, i, static_cast<uint32_t>(s.token(v) + e));
+                  }
+                }
+              }
+              row_sync();
+              cut.key |= ~static_cast<uint32_t>(sh.tie);
+              return cut;
+            }
+          }
+          ++turn;
+          if (last) break;
+          // the row's sums per digit, and before it; thread t has digit t
+          unsigned long long n_d = 0, m_d = 0;
+          uint32_t mine = 0, before_me = 0;
+          if (tid < kBins) {
+            for (uint32_t i = 0; i < kCluster; ++i) {
+              const uint4 w = get128(&bins[tid], i);
+              n_d += w.x;
+              m_d += small ? w.y + (static_cast<unsigned long long>(w.z) << 16)
+                           : w.y + (static_cast<unsigned long long>(w.z) << 11) + (static_cast<unsigned long long>(w.w) << 21);
+              if (i < rank) before_me += w.x;
+              if (i == rank) mine = w.x;
+            }
+          }
+          unsigned long long ni = n_d, mi = m_d;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long y0 = __shfl_up_sync(0xffffffffu, ni, o), y1 = __shfl_up_sync(0xffffffffu, mi, o);
+            if (lane >= o) {
+              ni += y0;
+              mi += y1;
+            }
+          }
+          if (lane == 31) {
+            sh.scan_n[warp] = ni;
+            sh.scan_m[warp] = mi;
+          }
+          if (tid == 0) sh.digit = -1;
+          __syncthreads();
+          unsigned long long cb = count + ni - n_d, mb = mass + mi - m_d, m_all = 0;
+          for (int w = 0; w < kBins / 32; ++w) {
+            if (w < warp) {
+              cb += sh.scan_n[w];
+              mb += sh.scan_m[w];
+            }
+            m_all += sh.scan_m[w];
+          }
+          // (the first token is kept whatever top_p is: nothing is before it)
+          if (level == 0) most = share >= 1. ? INFINITY : fmax(share * (z >= 0. ? z : static_cast<double>(m_all)), 0.5);
+          if (tid < kBins && n_d > 0 && cb < static_cast<unsigned long long>(k) && static_cast<double>(mb) < most)
+            atomicMax(&sh.digit, tid);
+          __syncthreads();
+          if (tid == sh.digit) {
+            sh.count = cb;
+            sh.mass = mb;
+            sh.n_in = n_d;
+            sh.own = mine;
+            sh.start = before_me;
+            sh.n_list = 0;
+          }
+          __syncthreads();
+          const int b = sh.digit;
+          count = sh.count;
+          mass = sh.mass;
+          n_in = sh.n_in;
+          own = sh.own;
+          start = sh.start;
+          if (n_in <= kList) {
+            // ---------------- few: all of them to every CTA, their pairs compared
+            for (int v = v0 + tid; v < v1; v += kWideThreads) {
+              float f[kVec];
+              unpack16<T>(get(v), f);
+#pragma unroll
+              for (int e = 0; e < kVec; ++e) {
+                if (f[e] == -INFINITY || digit(f[e], level) != b) continue;
+                const uint32_t at = start + atomicAdd(&sh.n_list, 1);
+                const unsigned long long key = argmax_key(f[e], static_cast<uint32_t>(s.token(v) + e));
+                const unsigned long long q = weight_bits(f[e]);
+                for (int i = 0; i < kCluster; ++i) {
+                  put64(&sh.c.key[at], i, key);
+                  put64(&sh.c.q[at], i, q);
+                }
+              }
+            }
+            row_sync();
+            const int n = static_cast<int>(n_in);
+            unsigned long long key = 0, before = 0;
+            int place = 0;
+            if (tid < n) key = sh.c.key[tid];
+            if ((tid & ~31) < n) {
+              for (int j = 0; j < n; ++j)
+                if (sh.c.key[j] > key) {
+                  ++place;
+                  before += sh.c.q[j];
+                }
+            }
+            // the last that is kept
+            const bool keep = tid < n && count + place < static_cast<unsigned long long>(k) &&
+                              (place == 0 || static_cast<double>(mass + before) < most);
+            const int kept = __syncthreads_count(keep);
+            if (keep && place == kept - 1) {
+              sh.count = key;
+              sh.mass = mass + before + sh.c.q[tid];
+            }
+            __syncthreads();
+            cut.key = sh.count;
+            cut.mass = static_cast<double>(sh.mass);
+            __syncthreads();
+            return cut;
+          }
+          if (bits)
+            prefix |= static_cast<uint32_t>(255 - b) << (24 - 8 * level);
+          else if (level == 0)
+            b0 = b;
+          else if (level == 1)
+            b1 = b;
+        }
+      }
+      return cut;  // (not reached: tokens with the same four digits are equal)
+    };
+
+    const bool cut_k = st.k > 0, cut_p = st.p < 1.f;
+    Cut cut{0ull, -1.};
+    if (cut_k) cut = find(st.k, 1., -1.);
+    if (cut_p) cut = find(cut_k ? st.k : 0x7fffffff, static_cast<double>(st.p), cut.mass);
+
+    // ---------------- race over the slice's kept tokens
+    const Noise<T> noise(a, row, s.shift);
+    float bs = -INFINITY, bx = 0.f, bg = 0.f;
+    int bi = 0x7fffffff;
+    for (int v = v0 + tid; v < v1; v += kWideThreads) {
+      float f[kVec], g[kVec];
+      unpack16<T>(get(v), f);
+      const int t0 = s.token(v);
+      bool any = false;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        if (argmax_key(f[e], static_cast<uint32_t>(t0 + e)) < cut.key ||
+            (st.mp > 0.f && f[e] != M && ex2((f[e] - M) * c) < st.mp))
+          f[e] = -INFINITY;
+        any |= f[e] > -INFINITY;
+      }
+      if (!any) continue;
+      noise.load(t0, a.V, g);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const float sc = f[e] > -INFINITY ? fmaf(f[e] - M, it, g[e]) : -INFINITY;
+        if (sc > bs) {
+          bs = sc;
+          bi = t0 + e;
+          bx = f[e];
+          bg = g[e];
+        }
+      }
+    }
+    // (as in the row kernel: within reach, in 64 bits)
+    const float wt = warp_max(bs);
+    __syncthreads();
+    if (lane == 0) sh.wm[warp] = wt;
+    __syncthreads();
+    float top = sh.wm[0];
+    for (int w = 1; w < kWideWarps; ++w) top = fmaxf(top, sh.wm[w]);
+    unsigned long long best = 0ull;
+    if (bs > -INFINITY && (bs >= top || bs >= top - 1e-6f * (fabsf(top) + fabsf(bs) + 128.f)))
+      best = exact_score(bx, bg, M, st.temp);
+    else
+      bi = 0x7fffffff;
+    cta_best<kWideWarps>(best, bi, sh.k, sh.i);
+    if (tid == 0) {
+      put64(&sh.best[rank], 0, best);
+      put32(&sh.best_i[rank], 0, static_cast<uint32_t>(bi));
+    }
+    row_sync();
+    if (rank == 0 && warp == 0) {
+      best = lane < kCluster ? sh.best[lane] : 0ull;
+      bi = lane < kCluster ? sh.best_i[lane] : 0x7fffffff;
+      warp_best(best, bi);
+      if (lane == 0) {
+        a.token[row] = best ? bi : -1;
+        if (!best) set_status(a.status, PE_ST_SAMPLING);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+size_t al256(size_t x) { return (x + 255) / 256 * 256; }
+
+constexpr int kSlice = 176 * 1024;   // of a row, in a CTA of the wide kernel
+constexpr int kMaxParts = kGroups / (kThreads >> 5);
+
+// Parts of a row: one wave of CTAs (four an SM) where the rows are few, at most 64 KB and at
+// least a vector per thread each.
+void plan(SampleArgs& a, int esize, int num_sms) {
+  const int vec = 16 / esize;
+  const int nvec = (a.V + 2 * (vec - 1)) / vec;  // whatever the row's place on the grid
+  int parts = a.T <= 4 * num_sms ? 4 * num_sms / std::max(a.T, 1) : 1;
+  parts = std::max(parts, (nvec * 16 + kMaxPartBytes - 1) / kMaxPartBytes);
+  parts = std::min(parts, (nvec + kThreads - 1) / kThreads);
+  parts = std::max(1, std::min(parts, kMaxParts));
+  a.part = (nvec + parts - 1) / parts;
+  a.parts = (nvec + a.part - 1) / a.part;
+  a.gshift = 0;
+  while (a.parts * (kThreads >> a.gshift) > kGroups) ++a.gshift;
+}
+
+// the most parts and groups of a row for any number of rows
+size_t max_parts(int V) {
+  return std::min<size_t>((static_cast<size_t>(V) + 6) / (4 * kThreads) + 1, kMaxParts);
+}
+
+template <typename T>
+cudaError_t launch(const SampleArgs& a, int num_sms, cudaStream_t st) {
   // the function's shared-memory limit, once per device (a bit each; past 63 every time)
   static std::atomic<uint64_t> set{0};
   int dev = 0;
@@ -720,14 +1177,19 @@ cudaError_t launch(const SampleArgs& a, size_t smem, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
   if (!(set.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSliceOne);
+    e = cudaFuncSetAttribute(sample_wide_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlice);
     if (e != cudaSuccess) return e;
     set.fetch_or(bit, std::memory_order_release);
   }
+  e = launch_chained(sample_row_kernel<T>, dim3(static_cast<unsigned>(a.T) * a.parts), dim3(kThreads), 0, st, a);
+  if (e != cudaSuccess) return e;
+  e = launch_chained(sample_cut_kernel<T>, dim3(a.T), dim3(kThreads), 0, st, a);
+  if (e != cudaSuccess) return e;
+  const int64_t slice = ((a.V + 7ll) * sizeof(T) / 16 + kCluster) / kCluster * 16 + 16;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.T) * a.ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(kCluster * std::min(a.T, std::max(num_sms / kCluster, 1)));
+  cfg.blockDim = dim3(kWideThreads);
+  cfg.dynamicSmemBytes = a.resident ? static_cast<size_t>(slice) : 0;
   cfg.stream = st;
   cudaLaunchAttribute attr[3];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -735,12 +1197,12 @@ cudaError_t launch(const SampleArgs& a, size_t smem, cudaStream_t st) {
   attr[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
   attr[1].val.sharedMemCarveout = cudaSharedmemCarveoutMaxShared;
   attr[2].id = cudaLaunchAttributeClusterDimension;
-  attr[2].val.clusterDim.x = a.ctas;
+  attr[2].val.clusterDim.x = kCluster;
   attr[2].val.clusterDim.y = 1;
   attr[2].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 3;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a);
+  return cudaLaunchKernelEx(&cfg, sample_wide_kernel<T>, a);
 }
 
 }  // namespace
@@ -749,7 +1211,10 @@ cudaError_t launch(const SampleArgs& a, size_t smem, cudaStream_t st) {
 using namespace pe;
 
 extern "C" size_t pe_sample_workspace_bytes(int max_batch, int max_rows, int vocab) {
-  return max_batch < 0 || max_rows < 0 || vocab < 1 ? 0 : 256;
+  if (max_batch < 0 || max_rows < 0 || vocab < 1 || vocab > 1 << 24) return 0;
+  const size_t T = max_rows, parts = max_parts(vocab);
+  return 256 + al256(T * sizeof(Settings)) + al256(T * sizeof(int32_t)) + al256(T * parts * sizeof(Part)) +
+         al256(T * std::min<size_t>(parts * kThreads, kGroups) * sizeof(float));
 }
 
 extern "C" int pe_sample(int B, int T, const int32_t* qsl, const void* logits, int64_t ld_logits, int vocab, int dtype,
@@ -760,8 +1225,10 @@ extern "C" int pe_sample(int B, int T, const int32_t* qsl, const void* logits, i
   if (B < 0 || T < 0 || vocab < 1 || ld_logits < vocab || ld_gumbel < vocab) return PE_ERR_ARG;
   if (dtype != PE_DTYPE_F32 && dtype != PE_DTYPE_BF16) return PE_ERR_UNSUPPORTED;
   if (B == 0) return T == 0 ? PE_OK : PE_ERR_ARG;
-  if (B > 65535 || vocab > 1 << 24 || T > 0x7fffffff / kMaxCluster) return PE_ERR_UNSUPPORTED;
-  if (!qsl || !ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < 256) return PE_ERR_ARG;
+  if (B > 65535 || vocab > 1 << 24) return PE_ERR_UNSUPPORTED;
+  if (!qsl || !ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 ||
+      ws_bytes < pe_sample_workspace_bytes(B, T, vocab))
+    return PE_ERR_ARG;
   const int esize = dtype == PE_DTYPE_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(logits) % esize != 0) return PE_ERR_ARG;
   for (const void* p : {static_cast<const void*>(qsl), static_cast<const void*>(temperature),
@@ -787,11 +1254,21 @@ extern "C" int pe_sample(int B, int T, const int32_t* qsl, const void* logits, i
   a.gumbel = gumbel;
   a.ld_g = ld_gumbel;
   a.token = token;
-  a.status = static_cast<uint32_t*>(ws);
-  const Split s = split_of(T, vocab, esize, sms);
-  a.ctas = s.ctas;
-  a.resident = s.resident;
+  plan(a, esize, sms);
+  if (static_cast<int64_t>(T) * a.parts > 0x7fffffff) return PE_ERR_UNSUPPORTED;
+  a.resident = (static_cast<int64_t>(vocab) + 7) * esize / 16 + kCluster <= static_cast<int64_t>(kSlice) / 16 * kCluster - kCluster;
+  char* w = static_cast<char*>(ws);
+  a.status = reinterpret_cast<uint32_t*>(w);
+  a.todo_n = reinterpret_cast<uint32_t*>(w + 128);
+  w += 256;
+  a.set = reinterpret_cast<Settings*>(w);
+  w += al256(T * sizeof(Settings));
+  a.todo = reinterpret_cast<int32_t*>(w);
+  w += al256(T * sizeof(int32_t));
+  a.stat = reinterpret_cast<Part*>(w);
+  w += al256(static_cast<size_t>(T) * a.parts * sizeof(Part));
+  a.top = reinterpret_cast<float*>(w);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == PE_DTYPE_F32 ? launch<float>(a, s.smem, st) : launch<bf16>(a, s.smem, st);
+  const cudaError_t e = dtype == PE_DTYPE_F32 ? launch<float>(a, sms, st) : launch<bf16>(a, sms, st);
   return e == cudaSuccess ? PE_OK : PE_ERR_CUDA;
 }

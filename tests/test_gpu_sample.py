@@ -183,6 +183,29 @@ def test_odd_settings():
     check(c, least_clear=0.5)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_cuts_behind_many_tokens(dtype):
+    """Cuts that thousands come before: in ranges that bins split badly (one far logit, a span that overflows, all
+    tokens within a few roundings), with ties around them, with both settings."""
+    V = 9001
+    ks = [(1.0, 3000, 1.0, 0.0), (1.0, 2500, 0.7, 0.0), (1.0, 0, 0.8, 0.0), (5.0, 8999, 0.999, 1e-9), (0.01, 4000, 1.0, 0.0)]
+    for i, kind in enumerate(("flat", "ties", "peaked", "flat", "equal")):
+        c = case((1,) * 5, V, dtype, kind, settings=ks, seed=i)
+        x = O.decode(c["logits"], dtype).copy()
+        if i == 1:
+            x[:, 100] = 3e38
+            x[:, 200] = -3e38
+        if i == 3:
+            x = 1.0 + x * 1e-6
+            x[:, 50] = 2e4
+        c["logits"] = _bits(x, dtype)
+        check(c, least_clear=0.5)
+
+
+def _bits(x, dtype):
+    return W.f32_to_bf16_bits(x.astype(np.float32)) if dtype == "bf16" else x.astype(np.float32)
+
+
 @pytest.mark.parametrize("qsl", [(0, 5, 3), (0, -2, 4), (1, 2, 3), (0, 3, 60)])
 def test_bad_offsets_are_reported(qsl):
     c = dict(case((2, 2), 300, "f32"), qsl=np.array(qsl, np.int32))
