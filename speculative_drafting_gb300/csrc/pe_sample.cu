@@ -14,14 +14,14 @@
 //                    row, so the value at which k of them (for top-p: enough of them to weigh
 //                    p of the whole) are reached cannot lie above the cut;
 //                  - the tokens from the bound on, read again from the few groups that have
-//                    one: rank and weight before each by comparing all pairs, the cut, the
-//                    best score.
+//                    one, in order; sums of their weights, the cut, the best score.
 //   wide kernel  takes the rows for which that does not do (flat rows that keep thousands of
 //                tokens, a large k, many equal logits), a cluster of CTAs a row with a slice
-//                each in shared memory: histograms of counts and weights over the distance from the
-//                largest logit, finer ones inside the bin of the cut, then a race over the
-//                slices.  Weights are 31-bit integers there: their sums do not depend on the
-//                order of the atomics.
+//                each in shared memory.  Top-p: all tokens race, and the weight before the
+//                winner tells whether it is kept (if not, the tokens before it race again).
+//                Top-k: a histogram of counts over the distance from the largest logit, finer
+//                ones inside the bin of the cut, then the race.  Weights are 31-bit integers there: their
+//                sums do not depend on an order.
 //
 // The first kernel is bound by the logits' bytes.  (Every row by a cluster with the row in
 // shared memory: 512 bf16 rows of 201,088 with top-k 162 us; the barriers of a row are waited
@@ -36,19 +36,24 @@
 namespace pe {
 namespace {
 
-constexpr int kThreads = 256;         // row kernel
+constexpr int kThreads = 256;         // row kernel (the cut kernel counts on 2^8)
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;            // 16-byte loads in flight per thread
 constexpr int kRaceUnroll = 2;        // ... where the noise is streamed too
 constexpr int kMaxPartBytes = 65536;  // of a row, per CTA
 constexpr int kGroups = 4096;         // of a row, at most
-constexpr int kBins = 256;
-constexpr int kList = 512;            // candidates of a row whose pairs are compared
-constexpr int kGroupList = 1024;      // groups that are read again
+
+constexpr int kCutThreads = 512;      // cut kernel
+constexpr int kCutWarps = kCutThreads / 32;
+constexpr int kCutBins = kCutThreads;  // of the groups' largest logits
+constexpr int kList = kCutThreads;    // candidates of a row that are put in order
+constexpr int kGroupList = 1024;      // groups that are read again, and vectors of theirs that matter
 
 constexpr int kWideThreads = 512;     // wide kernel
 constexpr int kWideWarps = kWideThreads / 32;
 constexpr int kCluster = 8;
+constexpr int kBins = 1024;           // two per thread
+constexpr int kTries = 6;
 
 // What a CTA of the row kernel leaves of its part.
 struct __align__(16) Part {
@@ -152,8 +157,22 @@ struct Noise {
   }
 };
 
+// element e of a vector, as the bits of a float
+template <typename T>
+PE_DEV uint32_t element(const uint4& u, int e) {
+  if (sizeof(T) == 4) return e == 0 ? u.x : e == 1 ? u.y : e == 2 ? u.z : u.w;
+  const uint32_t w = e < 2 ? u.x : e < 4 ? u.y : e < 6 ? u.z : u.w;
+  return e & 1 ? w & 0xffff0000u : w << 16;
+}
+
 PE_DEV unsigned long long exact_score(float x, float g, float M, float temp) {
   return score_order((static_cast<double>(x) - static_cast<double>(M)) / static_cast<double>(temp) + g);
+}
+
+// Whether a score may be the best one that rounds to `top` in fp32 (a score's rounding is 2^-23
+// of its terms; noise past 128 is infinite).
+PE_DEV bool within_reach(float score, float top, float term = 0.f) {
+  return score > -INFINITY && (score >= top || score >= top - 1e-6f * (fabsf(top) + fabsf(score) + fabsf(term) + 128.f));
 }
 
 // The logit of an order (argmax_order)
@@ -188,23 +207,29 @@ PE_DEV float cta_max(float v, float* warps) {  // NaN if there is one
   return v;
 }
 // Sum over the CTA, in a fixed order; all threads get it.
-template <int W>
-PE_DEV double cta_sum(double v, double* warps) {
+template <int W, typename X>
+PE_DEV X cta_sum(X v, X* warps) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
   __syncthreads();
-  double s = 0.;
+  X s = 0;
   for (int w = 0; w < W; ++w) s += warps[w];
   return s;
+}
+
+// The least whole number that is not below share * sum, share in [0, 1): what is below the one
+// is below the other.  (Doubles are slow here, two a clock and SM.)
+PE_DEV unsigned long long share_of(float share, unsigned long long sum) {
+  const unsigned long long p = static_cast<unsigned long long>(fmaxf(share, 0.f) * 0x1p64f);
+  return __umul64hi(p, sum) + (p * sum != 0ull);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArgs a) {
   constexpr int kVec = 16 / sizeof(T);
   __shared__ float warp_m[kWarps];
-  __shared__ double warp_d[kWarps];
   __shared__ unsigned long long warp_k[kWarps];
   __shared__ int warp_i[kWarps];
   __shared__ Settings set_sh;
@@ -281,16 +306,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
     const float it = 1.f / st.temp;
     float bs = -INFINITY;
     int bv = -1;
-    for (int j = tid; j < n; j += kRaceUnroll * kThreads) {
-      if (j != tid) {
-#pragma unroll
-        for (int x = 0; x < kRaceUnroll; ++x)
-          u[x] = j + x * kThreads < n ? s.load(v0 + j + x * kThreads) : no_tokens<T>();
-      }
-      float g[kRaceUnroll][kVec];
+    float g[kRaceUnroll][kVec];
+    auto load_noise = [&](int j) {
 #pragma unroll
       for (int x = 0; x < kRaceUnroll; ++x)
         if (j + x * kThreads < n) noise.load(s.token(v0 + j + x * kThreads), a.V, g[x]);
+    };
+    load_noise(tid);
+    for (int j = tid; j < n; j += kRaceUnroll * kThreads) {
       float mn = m;
 #pragma unroll
       for (int x = 0; x < kRaceUnroll; ++x) mn = max_nan(mn, vec_max<T>(u[x]));
@@ -299,20 +322,26 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
       m = mn;
 #pragma unroll
       for (int x = 0; x < kRaceUnroll; ++x) {
-        if (j + x * kThreads >= n) continue;
         float f[kVec], best = -INFINITY;
         unpack16<T>(u[x], f);
 #pragma unroll
         for (int e = 0; e < kVec; ++e) best = fmaxf(best, fmaf(f[e] - off, it, g[x][e]));
-        if (best > bs || bv < 0) {
+        if (j + x * kThreads < n && (best > bs || bv < 0)) {
           bs = fmaxf(bs, best);
           bv = j + x * kThreads;
+        }
+        // the next trip's are on their way (the first two trips' logits were loaded above)
+        static_assert(kUnroll == 2 * kRaceUnroll, "");
+        u[x] = j == tid ? u[x + kRaceUnroll] : no_tokens<T>();
+        const int jn = j + (x + kRaceUnroll) * kThreads;
+        if (jn < n) {
+          if (j != tid) u[x] = s.load(v0 + jn);
+          noise.load(s.token(v0 + jn), a.V, g[x]);
         }
       }
     }
     out.m = cta_max<kWarps>(m, warp_m);
-    // The threads whose best is within reach of the CTA's (a score's rounding is 2^-23 of its
-    // terms; noise past 128 is infinite) compare in 64 bits, token by token.
+    // The threads whose best is within reach of the CTA's compare in 64 bits.
     const float far = m == out.m ? 0.f : (m - out.m) * it;
     if (bs < INFINITY) bs += far;
     float top = warp_max(bs);
@@ -324,14 +353,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
     unsigned long long k = 0ull;
     int bi = 0x7fffffff;
     float bx = 0.f, bg = 0.f;
-    if (bv >= 0 && fabsf(out.m) < INFINITY &&
-        (bs >= top || bs >= top - 1e-6f * (fabsf(top) + fabsf(bs) + fabsf(far) + 128.f))) {
+    if (bv >= 0 && fabsf(out.m) < INFINITY && within_reach(bs, top, far)) {
       float f[kVec], g[kVec];
       unpack16<T>(s.load(v0 + bv), f);
       const int t0 = s.token(v0 + bv);
       noise.load(t0, a.V, g);
       for (int e = 0; e < kVec; ++e) {
-        const unsigned long long o = f[e] == -INFINITY ? 0ull : exact_score(f[e], g[e], out.m, st.temp);
+        if (!within_reach(fmaf(f[e] - m, it, g[e]) + far, top, far)) continue;
+        const unsigned long long o = exact_score(f[e], g[e], out.m, st.temp);
         if (o > k) {
           k = o;
           bi = t0 + e;
@@ -392,8 +421,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
       sum += s0 + s1;
     }
     out.m = cta_max<kWarps>(m, warp_m);
-    out.s = static_cast<float>(
-        cta_sum<kWarps>(m > -INFINITY ? sum * ex2((m - out.m) * c) : 0.f, warp_d));
+    out.s = cta_sum<kWarps>(m > -INFINITY ? sum * ex2((m - out.m) * c) : 0.f, warp_m);
   }
   if (!free && st.temp != 0.f) {
     if (st.k > 0 || st.p >= 1.f) out.m = cta_max<kWarps>(m, warp_m);
@@ -405,284 +433,289 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
   if ((!free || st.temp == 0.f) && tid == 0) a.stat[static_cast<size_t>(row) * a.parts + part] = out;
 }
 
-// Candidates of a row, all tokens that come before some place in its order, and what comes
-// before them (weights 2^-40): which are kept, and the best score.
-struct Cands {
-  unsigned long long key[kList];  // argmax_key: larger comes first
-  unsigned long long q[kList];    // weight
-  float g[kList];
-};
-constexpr float kOne = 0x1p40f;
+// ------------------------------------------------------------------ cut kernel
+
+// weights as integers: 2^38, so that 2^24 of them have a sum (in two parts: 2^20, 2^18)
+constexpr float kOne = 0x1p38f;
 
 // Shared memory of the cut kernel.
 struct __align__(16) CutShared {
-  float m[kWarps];
-  double d[kWarps];
-  unsigned long long k[kWarps];
-  int i[kWarps];
-  int n, n_groups, enough;
+  float m[kCutWarps];
+  unsigned long long k[kCutWarps], scan[kCutWarps];
+  int i[kCutWarps], scan_n[kCutWarps];
+  int n, n_groups, n_vec, last, most, near;
   uint32_t bound;
+  unsigned long long sum;
   float top[kGroups];
   union {
     struct {
-      uint32_t cnt[kBins], least[kBins];  // of the groups' largest logits; order of the least
-      unsigned long long mass[kBins];
+      uint32_t cnt[kCutBins], least[kCutBins];  // of the groups' largest logits; order of the least
+      uint32_t low[kCutBins], high[kCutBins];   // sums of their weights' lower 18 bits, and of the rest
     } h;
-    Cands c;
+    struct {  // the candidates, and in order
+      unsigned long long key[kList], sorted[kList];  // argmax_key: larger comes first
+    } l;
   };
   uint16_t group[kGroupList];
+  int vec[kGroupList];
 };
+
+// Sums over the CTA up to and with this thread (cut kernel); no barrier after the last read.
+template <typename T>
+PE_DEV T sum_upto(T v, T* warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  if (lane == 31) warps[warp] = v;
+  __syncthreads();
+  T before = 0;
+  for (int w = 0; w < kCutWarps; ++w)
+    if (w < warp) before += warps[w];
+  return v + before;
+}
+
+// (for the rounding of a sum that is compared with another)
+PE_DEV unsigned long long with_margin(unsigned long long x) { return x + (x >> 20); }
 
 // The answer of a row from its parts.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) sample_cut_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const SampleArgs a) {
   constexpr int kVec = 16 / sizeof(T);
   __shared__ CutShared sh;
   pdl_trigger();
   pdl_wait();
-  const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   const Settings st = a.set[row];
-  if (st.temp < 0.f) return;
   const Part* stat = a.stat + static_cast<size_t>(row) * a.parts;
+  // (what only some rows need is asked for with the settings; no more parts than threads)
+  const int gpp = kThreads >> a.gshift, groups = a.parts * gpp;  // groups of a part, of the row
+  const float* top = a.top + static_cast<size_t>(row) * groups;
+  float part_m = -INFINITY, part_s = 0.f, top_m[kGroups / kCutThreads];
+  if (tid < a.parts) {
+    part_m = __ldcg(&stat[tid].m);
+    part_s = __ldcg(&stat[tid].s);
+  }
+#pragma unroll
+  for (int x = 0; x < kGroups / kCutThreads; ++x)
+    top_m[x] = tid + x * kCutThreads < groups ? __ldcg(top + tid + x * kCutThreads) : -INFINITY;
   auto answer = [&](unsigned long long k, int i) {
-    cta_best<kWarps>(k, i, sh.k, sh.i);
+    cta_best<kCutWarps>(k, i, sh.k, sh.i);
     if (tid == 0) {
       a.token[row] = k ? i : -1;
       if (!k) set_status(a.status, PE_ST_SAMPLING);
     }
   };
+  if (st.temp < 0.f) return;
   if (st.temp == 0.f) {
     unsigned long long k = 0ull;
-    for (int i = tid; i < a.parts; i += kThreads) k = max(k, __ldcg(&stat[i].key));
+    for (int i = tid; i < a.parts; i += kCutThreads) k = max(k, __ldcg(&stat[i].key));
     answer(k, static_cast<int>(~static_cast<uint32_t>(k)));
     return;
   }
-  float M = -INFINITY;
-  for (int i = tid; i < a.parts; i += kThreads) M = max_nan(M, __ldcg(&stat[i].m));
-  M = cta_max<kWarps>(M, sh.m);
+  const bool cut_k = st.k > 0, cut_p = st.p < 1.f, cut = cut_k || cut_p || st.mp > 0.f;
+  float lo = INFINITY;
+  if (cut) {
+#pragma unroll
+    for (int x = 0; x < kGroups / kCutThreads; ++x) {
+      if (tid + x * kCutThreads < groups) sh.top[tid + x * kCutThreads] = top_m[x];
+      if (top_m[x] > -INFINITY) lo = fminf(lo, top_m[x]);
+    }
+    sh.h.cnt[tid] = 0;
+    sh.h.least[tid] = 0xffffffffu;
+    sh.h.low[tid] = sh.h.high[tid] = 0;
+    if (tid == 0) {
+      sh.n = sh.n_groups = sh.n_vec = 0;
+      sh.last = kCutBins;
+      sh.most = -1;
+      sh.bound = 0xffffffffu;
+    }
+  }
+  const float M = cta_max<kCutWarps>(part_m, sh.m);
   if (!(fabsf(M) < INFINITY)) {  // no distribution
     answer(0ull, -1);
     return;
   }
-  const bool cut_k = st.k > 0, cut_p = st.p < 1.f;
-  if (!cut_k && !cut_p && st.mp == 0.f) {
-    unsigned long long k = 0ull;
-    int best = 0x7fffffff;
-    for (int i = tid; i < a.parts; i += kThreads) {
-      const int t = __ldcg(&stat[i].idx);
-      const unsigned long long o = t < 0 ? 0ull : exact_score(__ldcg(&stat[i].x), __ldcg(&stat[i].g), M, st.temp);
-      if (o > k || (o == k && t < best)) {
-        k = o;
-        best = t;
-      }
-    }
-    answer(k, best);
+  if (!cut) {
+    const int t = tid < a.parts ? __ldcg(&stat[tid].idx) : -1;
+    answer(t < 0 ? 0ull : exact_score(__ldcg(&stat[tid].x), __ldcg(&stat[tid].g), M, st.temp), t < 0 ? 0x7fffffff : t);
     return;
   }
   const float c = scale_of(st.temp);
-  double z = 0.;  // the weight of the whole row
-  if (cut_p && !cut_k) {
-    for (int i = tid; i < a.parts; i += kThreads) {
-      const float m = __ldcg(&stat[i].m);
-      if (m > -INFINITY) z += static_cast<double>(__ldcg(&stat[i].s) * ex2((m - M) * c));
-    }
-    z = cta_sum<kWarps>(z, sh.d);
-  }
   // ---------------- a bound from below for the cut
-  const int gpp = kThreads >> a.gshift, groups = a.parts * gpp;  // groups of a part, of the row
-  const float* top = a.top + static_cast<size_t>(row) * groups;
-  float lo = INFINITY;
-  for (int i = tid; i < groups; i += kThreads) {
-    const float t = __ldcg(top + i);
-    sh.top[i] = t;
-    if (t > -INFINITY) lo = fminf(lo, t);
-  }
-  for (int b = tid; b < kBins; b += kThreads) {
-    sh.h.cnt[b] = 0;
-    sh.h.least[b] = 0xffffffffu;
-    sh.h.mass[b] = 0;
-  }
-  if (tid == 0) {
-    sh.n = sh.n_groups = 0;
-    sh.enough = 0;
-  }
-  lo = -cta_max<kWarps>(-lo, sh.m);
   float bound = -INFINITY;
+  unsigned long long z = 0;  // the weight of the whole row, where top-p alone asks for it
   if (cut_k || cut_p) {
+    if (!cut_k)
+      z = cta_sum<kCutWarps>(
+          part_m > -INFINITY ? static_cast<unsigned long long>(part_s * ex2((part_m - M) * c) * kOne) : 0ull, sh.k);
     // bins of the range that the groups' largest logits span
+    lo = -cta_max<kCutWarps>(-lo, sh.m);
     const float span = M - lo;
-    const float scale = span > 0.f && span < INFINITY ? fminf(kBins / span, 1e30f) : 0.f;
-    for (int i = tid; i < groups; i += kThreads) {
-      const float t = sh.top[i];
-      if (t > -INFINITY) {
-        const int b = min(kBins - 1, static_cast<int>((M - t) * scale));
+    const float scale = span > 0.f && span < INFINITY ? fminf(kCutBins / span, 1e30f) : 0.f;
+    for (int i = tid; i < groups; i += kCutThreads) {
+      const float t = sh.top[i], w = ex2((t - M) * c) * 0x1p20f;
+      const uint32_t high = static_cast<uint32_t>(w);
+      // (top-p alone: those that weigh next to nothing are left out, as many fall into one bin)
+      if (t > -INFINITY && (cut_k || high > 0)) {
+        const int b = min(kCutBins - 1, static_cast<int>((M - t) * scale));
         atomicAdd(&sh.h.cnt[b], 1u);
         atomicMin(&sh.h.least[b], argmax_order(t));
-        if (!cut_k) atomicAdd(&sh.h.mass[b], static_cast<unsigned long long>(ex2((t - M) * c) * kOne));
+        if (!cut_k) {
+          atomicAdd(&sh.h.high[b], high);
+          atomicAdd(&sh.h.low[b], static_cast<uint32_t>((w - static_cast<float>(high)) * 0x1p18f));
+        }
       }
     }
     __syncthreads();
-    if (warp == 0) {
-      // The first bin with which there are k, or p of the weight; for want of the latter as many
-      // as can be compared (their weight tells, below).
-      constexpr int kPer = kBins / 32;
-      double have[kPer], mine = 0.;
-      uint32_t count = 0;
-      const double need = cut_k ? static_cast<double>(st.k) : z * fmaxf(st.p, 0.f) * 1.000001 * kOne;
+    // The first bin with which there are k, or p of the weight (a margin for the rounding of
+    // the sum); for want of the latter as many as are put in order: their weight tells, below.
+    const uint32_t least = sh.h.least[tid];
+    const int count = sum_upto<int>(sh.h.cnt[tid], sh.scan_n);
+    bool enough = count >= st.k;
+    if (!cut_k) {
+      const unsigned long long mass = sum_upto<unsigned long long>(
+          sh.h.low[tid] + (static_cast<unsigned long long>(sh.h.high[tid]) << 18), sh.scan);
+      const unsigned long long need = with_margin(share_of(st.p, z));
+      enough = mass >= need;
+      if (tid == kCutThreads - 1) sh.near = mass >= need - (need >> 2);
+      const int most = __reduce_max_sync(0xffffffffu, count <= kList / 2 ? tid : -1);
+      if (lane == 0) atomicMax(&sh.most, most);
+    }
+    const int last = __reduce_min_sync(0xffffffffu, enough ? tid : kCutBins);
+    if (lane == 0) atomicMin(&sh.last, last);
+    __syncthreads();
+    const int bin = sh.last < kCutBins || cut_k ? sh.last : sh.most;
+    const uint32_t o = __reduce_min_sync(0xffffffffu, tid <= bin ? least : 0xffffffffu);
+    if (lane == 0) atomicMin(&sh.bound, o);
+    __syncthreads();
+    // (where all groups' largest are far from enough, the tokens behind them weigh as much)
+    if (bin < 0 || bin == kCutBins || sh.bound == 0xffffffffu || (sh.last == kCutBins && !sh.near)) {
+      if (tid == 0) a.todo[atomicAdd(a.todo_n, 1u)] = row;
+      return;
+    }
+    bound = logit_of(sh.bound);
+  } else {
+    // min-p alone: the logit that its weight stands for, a little less for the roundings
+    bound = fminf(M + (log2f(fminf(st.mp, 1.f)) * 1.00001f - 1e-5f) / c, M);
+  }
+  // ---------------- the groups that have a token from the bound on, and those tokens
+  for (int i = tid; i < groups; i += kCutThreads)
+    if (sh.top[i] > -INFINITY && sh.top[i] >= bound) {
+      const int at = atomicAdd(&sh.n_groups, 1);
+      if (at < kGroupList) sh.group[at] = static_cast<uint16_t>(i);
+    }
+  __syncthreads();
+  const Row<T> s(a, row);
+  const int nv = s.vectors(), n_groups = sh.n_groups;
+  if (n_groups <= kGroupList) {
+    // A warp to a group: which of its vectors (of each trip over the part, as many as it has
+    // threads) reach the bound.  Then a thread to a vector: its tokens.
+    const int warp = tid >> 5, per = ((a.part + kThreads - 1) / kThreads) << a.gshift;
+    for (int j = lane; j < (per + 31 & ~31); j += 32) {
+      const int in_part = (j >> a.gshift) * kThreads + (j & ((1 << a.gshift) - 1));
+      for (int i0 = warp; i0 < n_groups; i0 += kUnroll * kCutWarps) {
+        uint4 u[kUnroll];
+        int v[kUnroll];
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const int b = lane * kPer + e;
-        have[e] = cut_k ? static_cast<double>(sh.h.cnt[b]) : static_cast<double>(sh.h.mass[b]);
-        mine += have[e];
-        count += sh.h.cnt[b];
+        for (int x = 0; x < kUnroll; ++x) {
+          const int g = sh.group[min(i0 + x * kCutWarps, n_groups - 1)];
+          const int at = in_part + ((g & (gpp - 1)) << a.gshift);
+          v[x] = (g >> (8 - a.gshift)) * a.part + at;
+          if (j >= per || at >= a.part || v[x] >= nv || i0 + x * kCutWarps >= n_groups) v[x] = -1;
+          u[x] = v[x] >= 0 ? s.load(v[x]) : no_tokens<T>();
+        }
+        unsigned hit[kUnroll];
+        int hits = 0;
+#pragma unroll
+        for (int x = 0; x < kUnroll; ++x) {
+          hit[x] = __ballot_sync(0xffffffffu, v[x] >= 0 && vec_max<T>(u[x]) >= bound);
+          hits += __popc(hit[x]);
+        }
+        int at = 0;
+        if (lane == 0 && hits) at = atomicAdd(&sh.n_vec, hits);
+        at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+        for (int x = 0; x < kUnroll; ++x) {
+          const int mine = at + __popc(hit[x] & ((1u << lane) - 1u));
+          if ((hit[x] >> lane & 1u) && mine < kGroupList) sh.vec[mine] = v[x];
+          at += __popc(hit[x]);
+        }
       }
-      double before = mine;
-      uint32_t n_before = count;
+    }
+    __syncthreads();
+    const int n_vec = sh.n_vec;
+    for (int i0 = 0; i0 < min(n_vec, kGroupList); i0 += kCutThreads) {
+      const int v = i0 + tid < min(n_vec, kGroupList) ? sh.vec[i0 + tid] : -1;
+      const uint4 u = v >= 0 ? s.load(v) : no_tokens<T>();
+      float f[kVec];
+      unpack16<T>(u, f);
+      unsigned some = 0;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) some |= (f[e] >= bound && f[e] > -INFINITY) << e;
+      int upto = __popc(some);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, before, o);
-        const uint32_t n = __shfl_up_sync(0xffffffffu, n_before, o);
-        if (lane >= o) {
-          before += y;
-          n_before += n;
-        }
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
       }
-      before -= mine;
-      n_before -= count;
-      int last = kBins, most = -1;  // the bin; the last one with few enough groups before its end
-#pragma unroll
-      for (int e = kPer - 1; e >= 0; --e) {
-        double upto = before;
-        uint32_t n = n_before;
-        for (int f = 0; f <= e; ++f) {
-          upto += have[f];
-          n += sh.h.cnt[lane * kPer + f];
+      int at = 0;
+      if (lane == 31 && upto) at = atomicAdd(&sh.n, upto);
+      at = __shfl_sync(0xffffffffu, at, 31) + upto - __popc(some);
+      for (; some; some &= some - 1, ++at) {
+        const int e = __ffs(some) - 1, t = s.token(v) + e;
+        if (at < kList) {
+          sh.l.key[at] = argmax_key(__uint_as_float(element<T>(u, e)), static_cast<uint32_t>(t));
+          // (its noise is asked for below)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(a.gumbel + row * a.ld_g + t));
         }
-        if (upto >= need) last = lane * kPer + e;
-        if (n <= kList / 2 && most < 0) most = lane * kPer + e;
-      }
-      last = __reduce_min_sync(0xffffffffu, last);
-      most = __reduce_max_sync(0xffffffffu, most);
-      if (last == kBins && !cut_k) last = most;
-      uint32_t o = 0xffffffffu;
-      for (int e = 0; e < kPer; ++e)
-        if (lane * kPer + e <= last) o = min(o, sh.h.least[lane * kPer + e]);
-      o = __reduce_min_sync(0xffffffffu, o);
-      if (lane == 0) {
-        sh.bound = o;
-        sh.enough = last < kBins && last >= 0 && o != 0xffffffffu;
       }
     }
-    __syncthreads();
-    if (sh.enough) bound = logit_of(sh.bound);
-  } else if (tid == 0) {
-    sh.enough = 1;  // min-p alone: the weights say it
   }
   __syncthreads();
-  bool done = sh.enough;
+  const int n = sh.n;
+  bool done = n_groups <= kGroupList && sh.n_vec <= kGroupList && n <= kList;
   if (done) {
-    // ---------------- the groups that have a token from the bound on, and those tokens
-    const bool by_w = !cut_k && !cut_p;
-    auto in = [&](float x) { return by_w ? x == M || ex2((x - M) * c) >= st.mp : x >= bound; };
-    for (int i = tid; i < groups; i += kThreads)
-      if (sh.top[i] > -INFINITY && in(sh.top[i])) {
-        const int at = atomicAdd(&sh.n_groups, 1);
-        if (at < kGroupList) sh.group[at] = static_cast<uint16_t>(i);
+    // ---------------- in order: each counts those before it; then thread i has the i-th
+    {
+      const unsigned long long mine = tid < n ? sh.l.key[tid] : 0ull;
+      int place = 0;
+      if ((tid & ~31) < n) {
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) place += sh.l.key[j] > mine;
       }
-    __syncthreads();
-    const Row<T> s(a, row);
-    const int nv = s.vectors(), n_groups = sh.n_groups;
-    if (n_groups <= kGroupList) {
-      // a group's vectors: of each trip over the part, as many as it has threads
-      const int trips = (a.part + kThreads - 1) / kThreads, per = trips << a.gshift;
-      for (int i = tid; i < n_groups * per; i += kThreads) {
-        const int g = sh.group[i / per], j = i % per;
-        const int at = (j >> a.gshift) * kThreads + ((g % gpp) << a.gshift) + (j & ((1 << a.gshift) - 1));
-        const int v = g / gpp * a.part + at;
-        if (at >= a.part || v >= nv) continue;
-        const uint4 u = s.load(v);
-        if (!in(vec_max<T>(u))) continue;
-        float f[kVec];
-        unpack16<T>(u, f);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e)
-          if (f[e] > -INFINITY && in(f[e])) {
-            const int at2 = atomicAdd(&sh.n, 1);
-            if (at2 < kList) sh.c.key[at2] = argmax_key(f[e], static_cast<uint32_t>(s.token(v) + e));
-          }
-      }
+      if (tid < n) sh.l.sorted[place] = mine;
     }
     __syncthreads();
-    const int n = sh.n;
-    done = n_groups <= kGroupList && n <= kList;
-    if (done) {
-      // ---------------- rank and weight before each
-      constexpr int kPer = kList / kThreads;
-      const float* noise = a.gumbel + row * a.ld_g;
-      unsigned long long key[kPer], before[kPer];
-      float g[kPer];
-      int place[kPer];
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) {
-        const int i = tid + x * kThreads;
-        key[x] = before[x] = 0ull;
-        place[x] = 0;
-        g[x] = 0.f;
-        if (i < n) {
-          key[x] = sh.c.key[i];
-          g[x] = noise[~static_cast<uint32_t>(key[x])];
-          sh.c.q[i] = static_cast<unsigned long long>(ex2((logit_of(static_cast<uint32_t>(key[x] >> 32)) - M) * c) * kOne);
-        }
-      }
+    const unsigned long long key = tid < n ? sh.l.sorted[tid] : 0ull;
+    const int t = static_cast<int>(~static_cast<uint32_t>(key));
+    const bool there = tid < n && (!cut_k || tid < st.k);
+    const float g = there ? a.gumbel[row * a.ld_g + t] : 0.f;
+    const float l = logit_of(static_cast<uint32_t>(key >> 32));
+    const float w = ex2((l - M) * c);
+    bool keep = there;
+    if (cut_p) {
+      const unsigned long long q = there ? static_cast<unsigned long long>(w * kOne) : 0ull;
+      const unsigned long long upto = sum_upto<unsigned long long>(q, sh.scan);
+      if (tid == kCutThreads - 1) sh.sum = upto;
       __syncthreads();
-      if ((tid & ~31) < n) {
-        for (int j = 0; j < n; ++j) {
-          const unsigned long long kj = sh.c.key[j], qj = sh.c.q[j];
-#pragma unroll
-          for (int x = 0; x < kPer; ++x)
-            if (kj > key[x]) {
-              ++place[x];
-              before[x] += qj;
-            }
-        }
-      }
-      double sum = z * kOne;  // what top-p is a share of
-      if (cut_p) {
-        double mine = 0.;
-#pragma unroll
-        for (int x = 0; x < kPer; ++x)
-          if (tid + x * kThreads < n && (!cut_k || place[x] < st.k)) mine += static_cast<double>(sh.c.q[tid + x * kThreads]);
-        mine = cta_sum<kWarps>(mine, sh.d);
-        if (cut_k)
-          sum = mine;
-        else
-          done = mine >= sum * fmaxf(st.p, 0.f) * 1.000001;  // (else the cut lies behind them)
-      }
-      if (done) {
-        unsigned long long best = 0ull;
-        int bi = 0x7fffffff;
-#pragma unroll
-        for (int x = 0; x < kPer; ++x) {
-          const int i = tid + x * kThreads;
-          if (i >= n) continue;
-          const float l = logit_of(static_cast<uint32_t>(key[x] >> 32));
-          const bool first = place[x] == 0;
-          if ((cut_k && place[x] >= st.k) ||
-              (cut_p && !first && static_cast<double>(before[x]) >= static_cast<double>(st.p) * sum) ||
-              (!first && ex2((l - M) * c) < st.mp))
-            continue;
-          const unsigned long long o = exact_score(l, g[x], M, st.temp);
-          const int t = static_cast<int>(~static_cast<uint32_t>(key[x]));
-          if (o > best || (o == best && t < bi)) {
-            best = o;
-            bi = t;
-          }
-        }
-        answer(best, bi);
-      }
+      // (top-p alone: of all tokens, and if these do not weigh enough the cut lies behind them)
+      const unsigned long long most = share_of(st.p, cut_k ? sh.sum : z);
+      done = cut_k || sh.sum >= with_margin(most);
+      keep = there && (tid == 0 || upto - q < most);
+    }
+    if (done) {
+      keep = keep && (tid == 0 || w >= st.mp);
+      // in fp32, then those within reach of the best in 64 bits
+      const float score = keep ? fmaf(l - M, 1.f / st.temp, g) : -INFINITY;
+      const float best = cta_max<kCutWarps>(score == score ? score : -INFINITY, sh.m);
+      answer(keep && within_reach(score, best) ? exact_score(l, g, M, st.temp) : 0ull, t);
+      return;
     }
   }
-  if (!done && tid == 0) a.todo[atomicAdd(a.todo_n, 1u)] = row;
+  if (tid == 0) a.todo[atomicAdd(a.todo_n, 1u)] = row;
 }
 
 // ------------------------------------------------------------------ wide kernel
@@ -706,37 +739,35 @@ PE_DEV uint4 get128(const void* local, uint32_t rank) {
                : "memory");
   return v;
 }
+PE_DEV void put128(const void* local, uint32_t rank, uint4 v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row_addr(local, rank)), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
 // (all threads of all CTAs of the row)
 PE_DEV void row_sync() {
   __syncwarp();
   cluster_sync_all();
 }
 
-// The last kept token of a row: those whose argmax_key is no less are kept.
-struct Cut {
-  unsigned long long key;
-  double mass;  // weight of the kept ones, 2^-31
-};
-
 // Shared memory of a CTA of the wide kernel.  What the others of the row write or read there is
 // held twice and taken in turn: whoever writes a place again has met all of them at a barrier
 // since the last one read it.
 struct __align__(16) WideShared {
-  uint4 bins[2][kBins];  // count, sums of two or three parts of the weights' bits
-  float m[kCluster], lo[kCluster];               // of every CTA: largest and least finite logit
-  uint32_t least[2][kCluster], most[2][kCluster];  // ... orders of the cut's bin of the level before
-  unsigned long long best[kCluster];
-  int best_i[kCluster];
-  Cands c;               // the tokens of the cut's bin, of all CTAs
+  uint2 bins[2][kBins];  // counts; or sums of weights' lower and upper bits
+  float m[kCluster], lo[kCluster];  // of every CTA: largest and least finite logit
+  uint4 in[2][kCluster];  // ... of the cut's bin: tokens, least and greatest order
+  unsigned long long best[2][kCluster], best_key[2][kCluster];  // ... of its best score, and which token
+  unsigned long long key[kList];  // the tokens of the cut's bin, of all CTAs
   int tie;
   // this CTA's own
-  unsigned long long scan_n[kWideWarps], scan_m[kWideWarps], k[kWideWarps];
+  unsigned long long scan[kWideWarps], k[kWideWarps], mine[kList];
   float wm[kWideWarps], wl[kWideWarps];
   uint32_t u[kWideWarps], v[kWideWarps];
   int i[kWideWarps];
-  int digit, n_list;
-  unsigned long long count, mass, n_in;
-  uint32_t own, start;
+  int digit;
+  uint32_t n_list;
+  unsigned long long before;
 };
 
 // Sum over the CTA before this thread (wide kernel), and of all.
@@ -762,7 +793,7 @@ PE_DEV int wide_before(int v, int* warps, int& all) {
 
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const SampleArgs a) {
-  constexpr int kVec = 16 / sizeof(T);
+  constexpr int kVec = 16 / sizeof(T), kWideRace = 16 / kVec;  // (16 tokens a thread and trip)
   extern __shared__ uint4 held[];
   __shared__ WideShared sh;
   pdl_trigger();
@@ -782,8 +813,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
     const int nv = s.vectors(), per = (nv + kCluster - 1) / kCluster;
     const int v0 = min(static_cast<int>(rank) * per, nv), v1 = min(v0 + per, nv);
     auto get = [&](int v) { return a.resident ? held[v - v0] : s.load(v); };
-    // two parts of a weight's 31 bits do where a bin of a slice has at most 2^16 tokens
-    const bool small = per * kVec <= 65536;
     __syncthreads();
     // ---------------- the slice, its largest and least logit
     float m = -INFINITY, lo = INFINITY;
@@ -829,77 +858,220 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
     }
     const float c = scale_of(st.temp), it = 1.f / st.temp;
     auto weight_bits = [&](float x) { return static_cast<uint32_t>(ex2((x - M) * c) * 0x1p31f); };
+    // bits of a weight in a bin's lower sum: a slice of up to 2^16 tokens, or 2^21
+    const int low = per * kVec <= 65536 ? 16 : 11;
 
-    // ---------------- the cut: k tokens, and a share of the weight z (negative: of the row's)
-    auto find = [&](int k, double share, double z) {
-      Cut cut;
-      // Digits, small ones first in the order: of the distance from the largest logit in bins
-      // (an eighth of a factor 2 of weight each, or the row's range in kBins, whichever is finer:
-      // the last takes all that is farther) and finer ones inside the last level's; if the cut's
-      // bin stays too full without all in it being equal, of the bits of the logits' order.
+    const Noise<T> noise(a, row, s.shift);
+    // whether a token comes no later than a key (argmax_key), or before it
+    auto from = [&](float l, int t, unsigned long long key) {
+      const float x = key ? logit_of(static_cast<uint32_t>(key >> 32)) : -INFINITY;
+      return l > x || (l == x && static_cast<uint32_t>(t) <= ~static_cast<uint32_t>(key));
+    };
+    auto comes_before = [&](float l, int t, unsigned long long key) {
+      const float x = logit_of(static_cast<uint32_t>(key >> 32));
+      return l > x || (l == x && static_cast<uint32_t>(t) < ~static_cast<uint32_t>(key));
+    };
+    // The key of the best score among the tokens from a cut on, 0 if there is none.
+    auto race = [&](unsigned long long cut) {
+      auto kept = [&](float l, int t) {
+        return from(l, t, cut) && !(st.mp > 0.f && l != M && ex2((l - M) * c) < st.mp);
+      };
+      float bs = -INFINITY;
+      int bv = -1;  // the vector with this thread's
+      for (int v = v0 + tid; v < v1; v += kWideRace * kWideThreads) {
+        float f[kWideRace][kVec], g[kWideRace][kVec];
+#pragma unroll
+        for (int x = 0; x < kWideRace; ++x) {
+          const int vx = v + x * kWideThreads, t0 = s.token(vx);
+          unpack16<T>(vx < v1 ? get(vx) : no_tokens<T>(), f[x]);
+          bool any = false;
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) {
+            if (!kept(f[x][e], t0 + e)) f[x][e] = -INFINITY;
+            any |= f[x][e] > -INFINITY;
+          }
+          if (any) noise.load(t0, a.V, g[x]);
+        }
+#pragma unroll
+        for (int x = 0; x < kWideRace; ++x) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < kVec; ++e)
+            top = fmaxf(top, f[x][e] > -INFINITY ? fmaf(f[x][e] - M, it, g[x][e]) : -INFINITY);
+          if (top > bs) {
+            bs = top;
+            bv = v + x * kWideThreads;
+          }
+        }
+      }
+      // (as in the row kernel)
+      const float wt = warp_max(bs);
+      __syncthreads();
+      if (lane == 0) sh.wm[warp] = wt;
+      __syncthreads();
+      float top = sh.wm[0];
+      for (int w = 1; w < kWideWarps; ++w) top = fmaxf(top, sh.wm[w]);
+      unsigned long long best = 0ull, key = 0ull;
+      int bi = 0x7fffffff;
+      if (bv >= 0 && within_reach(bs, top)) {
+        const uint4 u = get(bv);
+        for (int e = 0; e < kVec; ++e) {
+          const float l = __uint_as_float(element<T>(u, e));
+          const int t = s.token(bv) + e;
+          if (!(l > -INFINITY) || !kept(l, t) || !within_reach(fmaf(l - M, it, noise.g[t]), top)) continue;
+          const unsigned long long o = exact_score(l, noise.g[t], M, st.temp);
+          if (o > best) {
+            best = o;
+            bi = t;
+            key = argmax_key(l, static_cast<uint32_t>(t));
+          }
+        }
+      }
+      unsigned long long k = best;
+      int i = bi;
+      cta_best<kWideWarps>(k, i, sh.k, sh.i);
+      // (its thread, or the first where none has one, tells the others)
+      if (k ? bi == i && best == k : tid == 0)
+        for (int to = 0; to < kCluster; ++to) {
+          put64(&sh.best[turn & 1][rank], to, k);
+          put64(&sh.best_key[turn & 1][rank], to, key);
+        }
+      row_sync();
+      k = 0ull;
+      key = 0ull;
+      for (int from_cta = 0; from_cta < kCluster; ++from_cta) {
+        const unsigned long long o = sh.best[turn & 1][from_cta], x = sh.best_key[turn & 1][from_cta];
+        // (equal scores: the lowest index)
+        if (o > k || (o == k && o && static_cast<uint32_t>(x) > static_cast<uint32_t>(key))) {
+          k = o;
+          key = x;
+        }
+      }
+      ++turn;
+      return key;
+    };
+    // Sum over the row; all threads get it.
+    auto wide_sum = [&](unsigned long long x) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      __syncthreads();
+      if (lane == 0) sh.scan[warp] = x;
+      __syncthreads();
+      if (warp == 0) {
+        x = lane < kWideWarps ? sh.scan[lane] : 0ull;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane < kCluster) put64(&sh.best[turn & 1][rank], lane, x);
+      }
+      row_sync();
+      x = 0ull;
+      for (int i = 0; i < kCluster; ++i) x += sh.best[turn & 1][i];
+      ++turn;
+      return x;
+    };
+
+    // ---------------- The cut: the last token with less than `most` tokens, or weight, before it.
+    // Returns its argmax_key.
+    auto find = [&](unsigned long long most, bool by_w) {
+      // Digits, small ones first in the order: of the distance from the largest logit in bins (a
+      // 32nd of a factor 2 of weight each, or the row's range in kBins, whichever is finer: the
+      // last takes all that is farther) and finer ones inside the cut's; if that stays too full
+      // without all in it being equal, ten bits of the logits' order at a time.
+      constexpr float kTop = kBins - 1;
+      // (0 .. kTop to the nearest integer: an addition that leaves it in the low bits)
+      auto linear = [](float t) { return __float_as_int(t + 8388608.f) & (kBins - 1); };
       const float span = M - lo;
       float scale = span > 0.f && span < INFINITY ? fminf(kBins / span, 1e30f) : 0.f;
-      if (share < 1.) scale = fmaxf(scale, fminf(8.f * c, 1e30f));
-      double most = INFINITY;
+      if (by_w) scale = fmaxf(scale, fminf(32.f * c, 1e30f));
       for (int bits = 0; bits < 2; ++bits) {
-        int b0 = 0, b1 = 0;
-        uint32_t prefix = 0;
-        unsigned long long count = 0, mass = 0, n_in = ~0ull;
-        uint32_t own = 0, start = 0;
-        // the digit of a logit at this level, -1: it is not in the bins found so far
+        int b0 = 0, b1 = 0, b2 = 0, b3 = 0;
+        unsigned long long before = 0;  // tokens, or weight, before the cut's bin
+        // the bin of a logit at this level, -1: it is not in the bins found so far
         auto digit = [&](float x, int level) {
           if (bits) {
-            const uint32_t o = argmax_order(x);
-            if (level > 0 && o >> (32 - 8 * level) != prefix >> (32 - 8 * level)) return -1;
-            return static_cast<int>(255u - (o >> (24 - 8 * level) & 255u));
+            const uint32_t o = ~argmax_order(x);
+            if ((level > 0 && static_cast<int>(o >> 22) != b0) || (level > 1 && static_cast<int>(o >> 12 & 1023u) != b1) ||
+                (level > 2 && static_cast<int>(o >> 2 & 1023u) != b2) || (level > 3 && static_cast<int>(o & 3u) != b3))
+              return -1;
+            return static_cast<int>(level == 0 ? o >> 22 : level == 1 ? o >> 12 & 1023u : level == 2 ? o >> 2 & 1023u : o & 3u);
           }
-          float t = (M - x) * scale;
-          int b = min(kBins - 1, static_cast<int>(t));
-          if (level > 0) {
-            if (b != b0) return -1;
-            t = (t - static_cast<float>(b)) * kBins;
-            b = min(kBins - 1, static_cast<int>(t));
-          }
+          const float t0 = fminf((M - x) * scale, kTop);
+          int b = linear(t0);
+          if (level == 0) return b;
+          if (b != b0) return -1;
+          float t = (t0 - static_cast<float>(b) + 0.5f) * kTop;
+          b = linear(t);
           if (level > 1) {
             if (b != b1) return -1;
-            t = (t - static_cast<float>(b)) * kBins;
-            b = min(kBins - 1, static_cast<int>(t));
+            t = (t - static_cast<float>(b) + 0.5f) * kTop;
+            b = linear(t);
           }
+          if (level > 2 && b != b2) return -1;
           return b;
         };
-        for (int level = 0; level < (bits ? 5 : 4); ++level) {
-          // Counts and weights per digit (of the level behind the last: only whether all are equal)
-          const bool last = level == (bits ? 4 : 3);
-          uint4* bins = sh.bins[turn & 1];
-          uint32_t (*word)[4] = reinterpret_cast<uint32_t (*)[4]>(bins);
+        const int levels = bits ? 4 : 3;
+        for (int level = 0; level <= levels; ++level) {
+          // Of the cut's bin of the level before: how many tokens, whether they differ, and the
+          // first of them in a list; and the bins of this level.
+          uint2* bins = sh.bins[turn & 1];
           __syncthreads();
-          for (int i = tid; i < kBins; i += kWideThreads) bins[i] = make_uint4(0, 0, 0, 0);
+          for (int i = tid; i < kBins; i += kWideThreads) bins[i] = make_uint2(0, 0);
+          if (tid == 0) {
+            sh.n_list = 0;
+            sh.digit = -1;
+          }
           __syncthreads();
           uint32_t least = 0xffffffffu, greatest = 0;
-          for (int v = v0 + tid; v < v1; v += kWideThreads) {
-            float f[kVec];
-            unpack16<T>(get(v), f);
+          if (level == 0 && !bits) {
+            // (every token, without a branch)
+            for (int v = v0 + tid; v < v1; v += kWideThreads) {
+              float f[kVec];
+              unpack16<T>(get(v), f);
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-              if (f[e] == -INFINITY) continue;
-              const int d = last ? (digit(f[e], level - 1) == (bits ? 255 - static_cast<int>(prefix & 255u) : sh.digit) ? 0 : -1)
-                                 : digit(f[e], level);
-              if (d < 0) continue;
-              if (level > 0) {
-                const uint32_t o = argmax_order(f[e]);
-                least = min(least, o);
-                greatest = max(greatest, o);
+              for (int e = 0; e < kVec; ++e) {
+                const int d = linear(fminf((M - f[e]) * scale, kTop));
+                if (by_w) {
+                  const uint32_t q = weight_bits(f[e]), lower = q & ((1u << low) - 1u);
+                  if (lower) atomicAdd(&bins[d].x, lower);
+                  if (q >> low) atomicAdd(&bins[d].y, q >> low);
+                } else if (f[e] > -INFINITY) {
+                  atomicAdd(&bins[d].x, 1u);
+                }
               }
-              if (last) continue;
-              const uint32_t q = weight_bits(f[e]);
-              atomicAdd(&word[d][0], 1u);
-              if (small) {
-                atomicAdd(&word[d][1], q & 0xffffu);
-                atomicAdd(&word[d][2], q >> 16);
-              } else {
-                atomicAdd(&word[d][1], q & 0x7ffu);
-                atomicAdd(&word[d][2], q >> 11 & 0x3ffu);
-                atomicAdd(&word[d][3], q >> 21);
+            }
+          } else {
+            for (int v = v0 + tid; v < v1; v += kWideThreads) {
+              float f[kVec];
+              unpack16<T>(get(v), f);
+              // which may be in the bins found so far: few are
+              unsigned some = 0;
+#pragma unroll
+              for (int e = 0; e < kVec; ++e)
+                some |= (f[e] > -INFINITY && (bits || fabsf(fminf((M - f[e]) * scale, kTop) - static_cast<float>(b0)) <= 0.5f))
+                        << e;
+              if (!some) continue;
+#pragma unroll 1
+              for (int e = 0; e < kVec; ++e) {
+                if (!(some >> e & 1u)) continue;
+                const uint32_t x = element<T>(get(v), e);
+                const float l = __uint_as_float(x);
+                const int d = digit(l, level);
+                if (d < 0) continue;
+                if (level > 0) {
+                  const uint32_t o = argmax_order(l);
+                  least = min(least, o);
+                  greatest = max(greatest, o);
+                  const uint32_t at = atomicAdd(&sh.n_list, 1u);
+                  if (at < kList) sh.mine[at] = argmax_key(l, static_cast<uint32_t>(s.token(v) + e));
+                }
+                if (level == levels) continue;
+                if (by_w) {
+                  const uint32_t q = weight_bits(l);
+                  atomicAdd(&bins[d].x, q & ((1u << low) - 1u));
+                  atomicAdd(&bins[d].y, q >> low);
+                } else {
+                  atomicAdd(&bins[d].x, 1u);
+                }
               }
             }
           }
@@ -914,31 +1086,30 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
             if (warp == 0) {
               least = __reduce_min_sync(0xffffffffu, lane < kWideWarps ? sh.u[lane] : 0xffffffffu);
               greatest = __reduce_max_sync(0xffffffffu, lane < kWideWarps ? sh.v[lane] : 0u);
-              if (lane < kCluster) {
-                put32(&sh.least[turn & 1][rank], lane, least);
-                put32(&sh.most[turn & 1][rank], lane, greatest);
-              }
+              if (lane < kCluster) put128(&sh.in[turn & 1][rank], lane, make_uint4(sh.n_list, least, greatest, 0u));
             }
           }
           row_sync();
           if (level > 0) {
+            uint32_t n_in = 0, start = 0;
             least = 0xffffffffu;
             greatest = 0;
-            for (int i = 0; i < kCluster; ++i) {
-              least = min(least, sh.least[turn & 1][i]);
-              greatest = max(greatest, sh.most[turn & 1][i]);
+            for (uint32_t i = 0; i < kCluster; ++i) {
+              const uint4 x = sh.in[turn & 1][i];
+              if (i < rank) start += x.x;
+              n_in += x.x;
+              least = min(least, x.y);
+              greatest = max(greatest, x.z);
             }
+            const uint32_t own = sh.in[turn & 1][rank].x;
             if (least == greatest) {
-              // ---------------- all in the cut's bin are equal: the first of them by index
+              // ---------------- all are equal: the first ones by index
               ++turn;
-              const uint32_t q = weight_bits(logit_of(least));
-              double t = fmin(static_cast<double>(n_in), static_cast<double>(k) - static_cast<double>(count));
-              if (most < INFINITY && q > 0) t = fmin(t, ceil((most - static_cast<double>(mass)) / q));
-              t = fmax(t, 1.);
-              cut.key = static_cast<unsigned long long>(least) << 32;
-              cut.mass = static_cast<double>(mass) + t * q;
-              if (t >= static_cast<double>(n_in)) return cut;
-              const int want = static_cast<int>(t) - static_cast<int>(start);  // the want-th of this CTA's
+              const uint32_t q = by_w ? weight_bits(logit_of(least)) : 1u;
+              const unsigned long long t = q > 0 ? (most - before + q - 1) / q : n_in;  // (before < most)
+              const unsigned long long key = static_cast<unsigned long long>(least) << 32;
+              if (t >= n_in) return key;
+              const int want = static_cast<int>(t) - static_cast<int>(start);  // of this CTA's
               if (want >= 1 && want <= static_cast<int>(own)) {
                 int seen = 0;
                 for (int vb = v0; vb < v1; vb += kWideThreads) {
@@ -961,182 +1132,103 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
                 }
               }
               row_sync();
-              cut.key |= ~static_cast<uint32_t>(sh.tie);
-              return cut;
+              return key | ~static_cast<uint32_t>(sh.tie);
             }
+            if (n_in <= kList) {
+              // ---------------- few: to every CTA, their pairs compared
+              ++turn;
+              for (uint32_t i = tid; i < own * kCluster; i += kWideThreads)
+                put64(&sh.key[start + i / kCluster], i % kCluster, sh.mine[i / kCluster]);
+              row_sync();
+              const unsigned long long key = tid < n_in ? sh.key[tid] : 0ull;
+              unsigned long long ahead = before;
+              sh.mine[tid] = by_w ? weight_bits(logit_of(static_cast<uint32_t>(key >> 32))) : 1u;
+              __syncthreads();
+              if ((tid & ~31) < n_in) {
+                for (uint32_t j = 0; j < n_in; ++j)
+                  if (sh.key[j] > key) ahead += sh.mine[j];
+              }
+              // the last that is kept (the first one always is)
+              const bool keep = tid < n_in && ahead < most;
+              unsigned long long last = keep ? ~key : 0ull;
+#pragma unroll
+              for (int o = 16; o; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
+              __syncthreads();
+              if (lane == 0) sh.k[warp] = last;
+              __syncthreads();
+              for (int w = 0; w < kWideWarps; ++w) last = max(last, sh.k[w]);
+              return ~last;
+            }
+          }
+          if (level == levels) {
+            ++turn;
+            break;
+          }
+          // the row's sums per bin, and before it; thread t has bins 2 t and 2 t + 1
+          unsigned long long x0 = 0, x1 = 0;
+          uint4 w[kCluster];
+#pragma unroll
+          for (uint32_t i = 0; i < kCluster; ++i) w[i] = get128(&bins[2 * tid], i);
+#pragma unroll
+          for (uint32_t i = 0; i < kCluster; ++i) {
+            x0 += w[i].x + (static_cast<unsigned long long>(w[i].y) << low);
+            x1 += w[i].z + (static_cast<unsigned long long>(w[i].w) << low);
           }
           ++turn;
-          if (last) break;
-          // the row's sums per digit, and before it; thread t has digit t
-          unsigned long long n_d = 0, m_d = 0;
-          uint32_t mine = 0, before_me = 0;
-          if (tid < kBins) {
-            for (uint32_t i = 0; i < kCluster; ++i) {
-              const uint4 w = get128(&bins[tid], i);
-              n_d += w.x;
-              m_d += small ? w.y + (static_cast<unsigned long long>(w.z) << 16)
-                           : w.y + (static_cast<unsigned long long>(w.z) << 11) + (static_cast<unsigned long long>(w.w) << 21);
-              if (i < rank) before_me += w.x;
-              if (i == rank) mine = w.x;
-            }
-          }
-          unsigned long long ni = n_d, mi = m_d;
+          unsigned long long upto = x0 + x1;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long y0 = __shfl_up_sync(0xffffffffu, ni, o), y1 = __shfl_up_sync(0xffffffffu, mi, o);
-            if (lane >= o) {
-              ni += y0;
-              mi += y1;
-            }
+            const unsigned long long y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
           }
-          if (lane == 31) {
-            sh.scan_n[warp] = ni;
-            sh.scan_m[warp] = mi;
-          }
-          if (tid == 0) sh.digit = -1;
+          if (lane == 31) sh.scan[warp] = upto;
           __syncthreads();
-          unsigned long long cb = count + ni - n_d, mb = mass + mi - m_d, m_all = 0;
-          for (int w = 0; w < kBins / 32; ++w) {
-            if (w < warp) {
-              cb += sh.scan_n[w];
-              mb += sh.scan_m[w];
-            }
-            m_all += sh.scan_m[w];
-          }
-          // (the first token is kept whatever top_p is: nothing is before it)
-          if (level == 0) most = share >= 1. ? INFINITY : fmax(share * (z >= 0. ? z : static_cast<double>(m_all)), 0.5);
-          if (tid < kBins && n_d > 0 && cb < static_cast<unsigned long long>(k) && static_cast<double>(mb) < most)
-            atomicMax(&sh.digit, tid);
+          unsigned long long first = before + upto - x0 - x1;
+          for (int w = 0; w < warp; ++w) first += sh.scan[w];
+          // the last bin that is not empty and has a kept token
+          const int b = x1 > 0 && first + x0 < most ? 2 * tid + 1 : x0 > 0 && first < most ? 2 * tid : -1;
+          if (b >= 0) atomicMax(&sh.digit, b);
           __syncthreads();
-          if (tid == sh.digit) {
-            sh.count = cb;
-            sh.mass = mb;
-            sh.n_in = n_d;
-            sh.own = mine;
-            sh.start = before_me;
-            sh.n_list = 0;
-          }
+          if (b >= 0 && b == sh.digit) sh.before = b & 1 ? first + x0 : first;
           __syncthreads();
-          const int b = sh.digit;
-          count = sh.count;
-          mass = sh.mass;
-          n_in = sh.n_in;
-          own = sh.own;
-          start = sh.start;
-          if (n_in <= kList) {
-            // ---------------- few: all of them to every CTA, their pairs compared
-            for (int v = v0 + tid; v < v1; v += kWideThreads) {
-              float f[kVec];
-              unpack16<T>(get(v), f);
-#pragma unroll
-              for (int e = 0; e < kVec; ++e) {
-                if (f[e] == -INFINITY || digit(f[e], level) != b) continue;
-                const uint32_t at = start + atomicAdd(&sh.n_list, 1);
-                const unsigned long long key = argmax_key(f[e], static_cast<uint32_t>(s.token(v) + e));
-                const unsigned long long q = weight_bits(f[e]);
-                for (int i = 0; i < kCluster; ++i) {
-                  put64(&sh.c.key[at], i, key);
-                  put64(&sh.c.q[at], i, q);
-                }
-              }
-            }
-            row_sync();
-            const int n = static_cast<int>(n_in);
-            unsigned long long key = 0, before = 0;
-            int place = 0;
-            if (tid < n) key = sh.c.key[tid];
-            if ((tid & ~31) < n) {
-              for (int j = 0; j < n; ++j)
-                if (sh.c.key[j] > key) {
-                  ++place;
-                  before += sh.c.q[j];
-                }
-            }
-            // the last that is kept
-            const bool keep = tid < n && count + place < static_cast<unsigned long long>(k) &&
-                              (place == 0 || static_cast<double>(mass + before) < most);
-            const int kept = __syncthreads_count(keep);
-            if (keep && place == kept - 1) {
-              sh.count = key;
-              sh.mass = mass + before + sh.c.q[tid];
-            }
-            __syncthreads();
-            cut.key = sh.count;
-            cut.mass = static_cast<double>(sh.mass);
-            __syncthreads();
-            return cut;
-          }
-          if (bits)
-            prefix |= static_cast<uint32_t>(255 - b) << (24 - 8 * level);
-          else if (level == 0)
-            b0 = b;
-          else if (level == 1)
-            b1 = b;
+          before = sh.before;
+          (level == 0 ? b0 : level == 1 ? b1 : level == 2 ? b2 : b3) = sh.digit;
         }
       }
-      return cut;  // (not reached: tokens with the same four digits are equal)
+      return 0ull;  // (not reached: tokens of the same order are equal)
     };
 
+    // ---------------- The best score among the tokens from a cut on (all CTAs get its key, 0: there
+    // is none); for top-p, is that token kept?  If it is not, none behind it is: the tokens before
+    // it race again.  Few are rejected, by the noise of a Gumbel draw; after kTries the cut is
+    // looked for.
     const bool cut_k = st.k > 0, cut_p = st.p < 1.f;
-    Cut cut{0ull, -1.};
-    if (cut_k) cut = find(st.k, 1., -1.);
-    if (cut_p) cut = find(cut_k ? st.k : 0x7fffffff, static_cast<double>(st.p), cut.mass);
-
-    // ---------------- race over the slice's kept tokens
-    const Noise<T> noise(a, row, s.shift);
-    float bs = -INFINITY, bx = 0.f, bg = 0.f;
-    int bi = 0x7fffffff;
-    for (int v = v0 + tid; v < v1; v += kWideThreads) {
-      float f[kVec], g[kVec];
-      unpack16<T>(get(v), f);
-      const int t0 = s.token(v);
-      bool any = false;
+    unsigned long long cut = cut_k ? find(st.k, false) : 0ull, won = 0ull, most = 0ull;
+    for (int attempt = 0;; ++attempt) {
+      won = race(cut);
+      if (!cut_p || won == 0ull || attempt > kTries) break;
+      // the weight before it, and (once) of all that top-p is a share of
+      unsigned long long before = 0ull, all = 0ull;
+      for (int v = v0 + tid; v < v1; v += kWideThreads) {
+        float f[kVec];
+        unpack16<T>(get(v), f);
+        const int t0 = s.token(v);
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        if (argmax_key(f[e], static_cast<uint32_t>(t0 + e)) < cut.key ||
-            (st.mp > 0.f && f[e] != M && ex2((f[e] - M) * c) < st.mp))
-          f[e] = -INFINITY;
-        any |= f[e] > -INFINITY;
-      }
-      if (!any) continue;
-      noise.load(t0, a.V, g);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const float sc = f[e] > -INFINITY ? fmaf(f[e] - M, it, g[e]) : -INFINITY;
-        if (sc > bs) {
-          bs = sc;
-          bi = t0 + e;
-          bx = f[e];
-          bg = g[e];
+        for (int e = 0; e < kVec; ++e) {
+          const uint32_t q = weight_bits(f[e]);
+          before += comes_before(f[e], t0 + e, won) ? q : 0u;
+          if (attempt == 0) all += from(f[e], t0 + e, cut) ? q : 0u;
         }
       }
+      before = wide_sum(before);
+      // (the first token is kept whatever top_p is: nothing is before it)
+      if (attempt == 0) most = max(share_of(st.p, wide_sum(all)), 1ull);
+      if (before < most) break;
+      cut = attempt == kTries ? find(most, true) : won + 1ull;
     }
-    // (as in the row kernel: within reach, in 64 bits)
-    const float wt = warp_max(bs);
-    __syncthreads();
-    if (lane == 0) sh.wm[warp] = wt;
-    __syncthreads();
-    float top = sh.wm[0];
-    for (int w = 1; w < kWideWarps; ++w) top = fmaxf(top, sh.wm[w]);
-    unsigned long long best = 0ull;
-    if (bs > -INFINITY && (bs >= top || bs >= top - 1e-6f * (fabsf(top) + fabsf(bs) + 128.f)))
-      best = exact_score(bx, bg, M, st.temp);
-    else
-      bi = 0x7fffffff;
-    cta_best<kWideWarps>(best, bi, sh.k, sh.i);
-    if (tid == 0) {
-      put64(&sh.best[rank], 0, best);
-      put32(&sh.best_i[rank], 0, static_cast<uint32_t>(bi));
-    }
-    row_sync();
-    if (rank == 0 && warp == 0) {
-      best = lane < kCluster ? sh.best[lane] : 0ull;
-      bi = lane < kCluster ? sh.best_i[lane] : 0x7fffffff;
-      warp_best(best, bi);
-      if (lane == 0) {
-        a.token[row] = best ? bi : -1;
-        if (!best) set_status(a.status, PE_ST_SAMPLING);
-      }
+    if (rank == 0 && tid == 0) {
+      a.token[row] = won ? static_cast<int>(~static_cast<uint32_t>(won)) : -1;
+      if (!won) set_status(a.status, PE_ST_SAMPLING);
     }
   }
 }
@@ -1147,13 +1239,14 @@ size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
 constexpr int kSlice = 176 * 1024;   // of a row, in a CTA of the wide kernel
 constexpr int kMaxParts = kGroups / (kThreads >> 5);
+constexpr int kWave = 4;  // CTAs of the row kernel per SM
 
 // Parts of a row: one wave of CTAs (four an SM) where the rows are few, at most 64 KB and at
 // least a vector per thread each.
 void plan(SampleArgs& a, int esize, int num_sms) {
   const int vec = 16 / esize;
   const int nvec = (a.V + 2 * (vec - 1)) / vec;  // whatever the row's place on the grid
-  int parts = a.T <= 4 * num_sms ? 4 * num_sms / std::max(a.T, 1) : 1;
+  int parts = a.T <= kWave * num_sms ? kWave * num_sms / std::max(a.T, 1) : 1;
   parts = std::max(parts, (nvec * 16 + kMaxPartBytes - 1) / kMaxPartBytes);
   parts = std::min(parts, (nvec + kThreads - 1) / kThreads);
   parts = std::max(1, std::min(parts, kMaxParts));
@@ -1183,8 +1276,8 @@ cudaError_t launch(const SampleArgs& a, int num_sms, cudaStream_t st) {
   }
   e = launch_chained(sample_row_kernel<T>, dim3(static_cast<unsigned>(a.T) * a.parts), dim3(kThreads), 0, st, a);
   if (e != cudaSuccess) return e;
-  e = launch_chained(sample_cut_kernel<T>, dim3(a.T), dim3(kThreads), 0, st, a);
-  if (e != cudaSuccess) return e;
+  e = launch_chained(sample_cut_kernel<T>, dim3(a.T), dim3(kCutThreads), 0, st, a);
+  if (e != cudaSuccess || !(a.top_k || a.top_p || a.min_p)) return e;
   const int64_t slice = ((a.V + 7ll) * sizeof(T) / 16 + kCluster) / kCluster * 16 + 16;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCluster * std::min(a.T, std::max(num_sms / kCluster, 1)));
