@@ -674,7 +674,7 @@ int pe_cache_compact(const pe_attn_plan* plan, int n_layers, int B, int T, const
  * used nor written; PE_ST_ROWS_RANGE as for pe_verify_sampled.  PE_ERR_ARG: negative
  * sizes, vocab < 1, strides below vocab, null pointers, tensors not aligned to their element
  * size, ws misaligned or too small, B = 0 with T > 0.  PE_ERR_UNSUPPORTED: B > 65535,
- * vocab > 2^24, a dtype other than the two. */
+ * vocab > 2^20, a dtype other than the two. */
 size_t pe_sample_workspace_bytes(int max_batch, int max_rows, int vocab);
 int pe_sample(int B, int T, const int32_t* qsl, const void* logits, int64_t ld_logits, int vocab,
               int dtype, const float* temperature, const int32_t* top_k, const float* top_p,

@@ -477,6 +477,7 @@ def read_status_ws(ws, clear=True, stream=None):
 
 
 _torch_types = None
+_torch_int64 = None
 
 
 def _types():
@@ -486,6 +487,15 @@ def _types():
 
         _torch_types = torch.float32, torch.bfloat16, torch.int32
     return _torch_types
+
+
+def _int64():
+    global _torch_int64
+    if _torch_int64 is None:
+        import torch
+
+        _torch_int64 = torch.int64
+    return _torch_int64
 
 
 def verify_sampled_workspace(max_batch: int, max_rows_in: int, vocab: int, device="cuda"):
@@ -524,32 +534,32 @@ def verify_sampled(B, T_in, qsl, tok, logits, vocab, dtype, temperature, u, gumb
     _check(rc, "pe_verify_sampled")
 
 
-def _dense(ws, what, n, t, ty):
-    """`what` with at least n dense elements of the type ty, on the workspace's device."""
-    if t.get_device() != ws.get_device():
-        raise ValueError(f"{what} is on device {t.get_device()}, ws on {ws.get_device()}")
-    if not (t.dtype is ty and t.numel() >= n and t.is_contiguous()):
-        raise ValueError(f"{what}: {n} dense elements of the type {ty} are read or written, "
-                         f"got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
-    return t.data_ptr()
+def _refuse_tensors(ws, *given):
+    """Which of (name, tensor, type, elements) the call cannot take, and why."""
+    for name, t, ty, n in given:
+        if t is None:
+            continue
+        if t.get_device() != ws.get_device():
+            raise ValueError(f"{name} is on device {t.get_device()}, ws on {ws.get_device()}")
+        if not (t.dtype is ty and t.numel() >= n and t.is_contiguous()):
+            raise ValueError(f"{name}: {n} dense elements of the type {ty} are read or written, "
+                             f"got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
+    raise ValueError("tensors that the call cannot take")
 
 
-def _table(ws, t, rows, i32):
-    """A block table [rows or more][max_blocks]."""
-    if t.dim() != 2 or t.shape[0] < rows:
-        raise ValueError(f"block_table has the shape {tuple(t.shape)}, {rows} rows are read")
-    return _dense(ws, "block_table", t.numel(), t, i32)
+def _refuse_rows(name, rows, t):
+    raise ValueError(f"{name} has the shape {tuple(t.shape)}, {rows} rows are read or written")
 
 
 def _rows_of(ws, what, t, T, width, ty):
     """Elements from one of T rows of `width` dense elements of the type ty to the next."""
     if t.get_device() != ws.get_device():
         raise ValueError(f"{what} is on device {t.get_device()}, ws on {ws.get_device()}")
-    if not (t.dtype is ty and t.dim() == 2 and t.shape[0] >= T and t.shape[1] >= width
-            and (t.stride(1) == 1 or width == 1)):
+    n, s = t.shape, t.stride()
+    if not (t.dtype is ty and len(n) == 2 and n[0] >= T and n[1] >= width and (s[1] == 1 or width == 1)):
         raise ValueError(f"{what}: {T} rows of {width} elements of the type {ty} are read, got {t.dtype} "
-                         f"{tuple(t.shape)} strides {t.stride()}")
-    return max(t.stride(0), width) if T <= 1 else t.stride(0)
+                         f"{tuple(n)} strides {s}")
+    return max(s[0], width) if T <= 1 else s[0]
 
 
 def sample_workspace(max_batch: int, max_rows: int, vocab: int, device="cuda"):
@@ -567,16 +577,21 @@ def sample(B, T, qsl, logits, vocab, temperature, top_k, top_p, min_p, gumbel, t
     float32, whose rows may be strided; qsl, top_k and token are int32, the settings float32, one
     each a request; temperature, top_k, top_p and min_p may be None."""
     f32, bf16, i32 = _types()
-    ld = _rows_of(ws, "logits", logits, T, vocab, bf16 if logits.dtype is bf16 else f32)
+    is_bf16 = logits.dtype is bf16
+    ld = _rows_of(ws, "logits", logits, T, vocab, bf16 if is_bf16 else f32)
     ldg = _rows_of(ws, "gumbel", gumbel, T, vocab, f32)
-    rc = load().pe_sample(
-        B, T, _dense(ws, "qsl", B and B + 1, qsl, i32), logits.data_ptr(), ld, vocab,
-        PE_DTYPE_BF16 if logits.dtype is bf16 else PE_DTYPE_F32,
-        None if temperature is None else _dense(ws, "temperature", B, temperature, f32),
-        None if top_k is None else _dense(ws, "top_k", B, top_k, i32),
-        None if top_p is None else _dense(ws, "top_p", B, top_p, f32),
-        None if min_p is None else _dense(ws, "min_p", B, min_p, f32), gumbel.data_ptr(), ldg,
-        _dense(ws, "token", T, token, i32), ws.data_ptr(), ws.numel(), _stream_handle(stream, ws))
+    dev = ws.get_device()
+    if not (qsl.dtype is i32 and token.dtype is i32 and qsl.is_contiguous() and token.is_contiguous()
+            and (qsl.numel() > B or B == 0) and token.numel() >= T and qsl.get_device() == dev == token.get_device()):
+        _refuse_tensors(ws, ("qsl", qsl, i32, B and B + 1), ("token", token, i32, T))
+    for t, ty in ((temperature, f32), (top_k, i32), (top_p, f32), (min_p, f32)):
+        if t is not None and not (t.dtype is ty and t.numel() >= B and t.is_contiguous() and t.get_device() == dev):
+            _refuse_tensors(ws, ("temperature", temperature, f32, B), ("top_k", top_k, i32, B),
+                            ("top_p", top_p, f32, B), ("min_p", min_p, f32, B))
+    rc = load().pe_sample(B, T, qsl.data_ptr(), logits.data_ptr(), ld, vocab,
+                          PE_DTYPE_BF16 if is_bf16 else PE_DTYPE_F32, _addr(temperature), _addr(top_k), _addr(top_p),
+                          _addr(min_p), gumbel.data_ptr(), ldg, token.data_ptr(), ws.data_ptr(), ws.numel(),
+                          _stream_handle(stream, ws))
     _check(rc, "pe_sample")
 
 
@@ -587,29 +602,47 @@ def tree_layout(B, T, qsl, seq_len, parent, block_table, num_blocks, block_size,
                 stream=None):
     """pe_tree_layout: mask [T][words] int32 (the bits of uint32 words); pos and slot int64, each
     may be None; the others int32.  ws: any zeroed workspace of 256 bytes or more."""
-    import torch
-
-    i32, i64 = torch.int32, torch.int64
-    if mask.dim() != 2 or mask.shape[0] < T:
-        raise ValueError(f"mask has the shape {tuple(mask.shape)}, {T} rows are written")
-    rc = load().pe_tree_layout(
-        B, T, _dense(ws, "qsl", B and B + 1, qsl, i32), _dense(ws, "seq_len", B, seq_len, i32),
-        _dense(ws, "parent", T, parent, i32), _table(ws, block_table, B, i32), block_table.shape[1], num_blocks,
-        block_size, _dense(ws, "mask", mask.numel(), mask, i32), mask.shape[1],
-        None if pos is None else _dense(ws, "pos", T, pos, i64),
-        None if slot is None else _dense(ws, "slot", T, slot, i64), ws.data_ptr(), ws.numel(),
-        _stream_handle(stream, ws))
+    # (the checks stand in line: calls of this size are bound by their host time)
+    i32, i64, dev = _types()[2], _int64(), ws.get_device()
+    if not (qsl.dtype is i32 and seq_len.dtype is i32 and parent.dtype is i32 and block_table.dtype is i32
+            and mask.dtype is i32 and qsl.is_contiguous() and seq_len.is_contiguous() and parent.is_contiguous()
+            and block_table.is_contiguous() and mask.is_contiguous() and (qsl.numel() > B or B == 0)
+            and seq_len.numel() >= B and parent.numel() >= T
+            and dev == qsl.get_device() == seq_len.get_device() == parent.get_device() == block_table.get_device()
+            == mask.get_device()):
+        _refuse_tensors(ws, ("qsl", qsl, i32, B and B + 1), ("seq_len", seq_len, i32, B), ("parent", parent, i32, T),
+                        ("block_table", block_table, i32, 0), ("mask", mask, i32, 0))
+    for t in (pos, slot):
+        if t is not None and not (t.dtype is i64 and t.numel() >= T and t.is_contiguous() and t.get_device() == dev):
+            _refuse_tensors(ws, ("pos", pos, i64, T), ("slot", slot, i64, T))
+    table, words = block_table.shape, mask.shape
+    if len(table) != 2 or table[0] < B:
+        _refuse_rows("block_table", B, block_table)
+    if len(words) != 2 or words[0] < T:
+        _refuse_rows("mask", T, mask)
+    rc = load().pe_tree_layout(B, T, qsl.data_ptr(), seq_len.data_ptr(), parent.data_ptr(), block_table.data_ptr(),
+                               table[1], num_blocks, block_size, mask.data_ptr(), words[1], _addr(pos), _addr(slot),
+                               ws.data_ptr(), ws.numel(), _stream_handle(stream, ws))
     _check(rc, "pe_tree_layout")
 
 
 def tree_accept(B, T, qsl, parent, tok, target, accepted, path, bonus, ws, stream=None):
     """pe_tree_accept on int32 tensors.  ws: any zeroed workspace of 256 bytes or more."""
     i32 = _types()[2]
-    rc = load().pe_tree_accept(
-        B, T, _dense(ws, "qsl", B and B + 1, qsl, i32), _dense(ws, "parent", T, parent, i32),
-        _dense(ws, "tok", T, tok, i32), _dense(ws, "target", T, target, i32),
-        _dense(ws, "accepted", B, accepted, i32), _dense(ws, "path", T, path, i32),
-        _dense(ws, "bonus", B, bonus, i32), ws.data_ptr(), ws.numel(), _stream_handle(stream, ws))
+    if not (qsl.dtype is i32 and parent.dtype is i32 and tok.dtype is i32 and target.dtype is i32
+            and accepted.dtype is i32 and path.dtype is i32 and bonus.dtype is i32
+            and qsl.is_contiguous() and parent.is_contiguous() and tok.is_contiguous() and target.is_contiguous()
+            and accepted.is_contiguous() and path.is_contiguous() and bonus.is_contiguous()
+            and (qsl.numel() > B or B == 0) and parent.numel() >= T and tok.numel() >= T and target.numel() >= T
+            and accepted.numel() >= B and path.numel() >= T and bonus.numel() >= B
+            and ws.get_device() == qsl.get_device() == parent.get_device() == tok.get_device() == target.get_device()
+            == accepted.get_device() == path.get_device() == bonus.get_device()):
+        _refuse_tensors(ws, ("qsl", qsl, i32, B and B + 1), ("parent", parent, i32, T), ("tok", tok, i32, T),
+                        ("target", target, i32, T), ("accepted", accepted, i32, B), ("path", path, i32, T),
+                        ("bonus", bonus, i32, B))
+    rc = load().pe_tree_accept(B, T, qsl.data_ptr(), parent.data_ptr(), tok.data_ptr(), target.data_ptr(),
+                               accepted.data_ptr(), path.data_ptr(), bonus.data_ptr(), ws.data_ptr(), ws.numel(),
+                               _stream_handle(stream, ws))
     _check(rc, "pe_tree_accept")
 
 
@@ -626,24 +659,36 @@ def pages_workspace(max_entries: int, num_blocks: int, device="cuda"):
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
+def _pool(ws, n, block_table, refs, **entries):
+    """Checks of a page call: entries (n int32 each), the table, the counts."""
+    i32, dev = _types()[2], ws.get_device()
+    ok = (block_table.dtype is i32 and refs.dtype is i32 and block_table.is_contiguous() and refs.is_contiguous()
+          and dev == block_table.get_device() == refs.get_device())
+    for t in entries.values():
+        ok = ok and t.dtype is i32 and t.numel() >= n and t.is_contiguous() and t.get_device() == dev
+    if not ok:
+        _refuse_tensors(ws, ("block_table", block_table, i32, 0), ("refs", refs, i32, 0),
+                        *((k, t, i32, n) for k, t in entries.items()))
+    if block_table.dim() != 2:
+        _refuse_rows("block_table", "its", block_table)
+    return block_table.shape
+
+
 def pages_reserve(n, row, length, block_table, refs, block_size, ws, stream=None):
     """pe_pages_reserve: rows row[i] of block_table get pages for length[i] positions; refs counts
     the uses of each page (num_blocks of them).  All int32."""
-    i32 = _types()[2]
-    rc = load().pe_pages_reserve(
-        n, _dense(ws, "row", n, row, i32), _dense(ws, "length", n, length, i32),
-        _table(ws, block_table, 0, i32), block_table.shape[0], block_table.shape[1], refs.numel(), block_size,
-        _dense(ws, "refs", 0, refs, i32), ws.data_ptr(), ws.numel(), _stream_handle(stream, ws))
+    rows, max_blocks = _pool(ws, n, block_table, refs, row=row, length=length)
+    rc = load().pe_pages_reserve(n, row.data_ptr(), length.data_ptr(), block_table.data_ptr(), rows, max_blocks,
+                                 refs.numel(), block_size, refs.data_ptr(), ws.data_ptr(), ws.numel(),
+                                 _stream_handle(stream, ws))
     _check(rc, "pe_pages_reserve")
 
 
 def pages_free(n, row, block_table, refs, ws, stream=None):
     """pe_pages_free: rows row[i] of block_table give their pages back.  All int32."""
-    i32 = _types()[2]
-    rc = load().pe_pages_free(
-        n, _dense(ws, "row", n, row, i32), _table(ws, block_table, 0, i32), block_table.shape[0],
-        block_table.shape[1], refs.numel(), _dense(ws, "refs", 0, refs, i32), ws.data_ptr(), ws.numel(),
-        _stream_handle(stream, ws))
+    rows, max_blocks = _pool(ws, n, block_table, refs, row=row)
+    rc = load().pe_pages_free(n, row.data_ptr(), block_table.data_ptr(), rows, max_blocks, refs.numel(),
+                              refs.data_ptr(), ws.data_ptr(), ws.numel(), _stream_handle(stream, ws))
     _check(rc, "pe_pages_free")
 
 
@@ -759,12 +804,17 @@ class PagedAttention:
         """pe_tree_attention: as ``attend`` for rows that are nodes, with their masks [T][words]
         int32 (of ``tree_layout``)."""
         self._attend_checks(B, T, qsl, seq_len, q, k_cache, v_cache, block_table, num_blocks, out, ws, sink)
-        if mask.dim() != 2 or mask.shape[0] < T:
-            raise ValueError(f"mask has the shape {tuple(mask.shape)}, {T} rows are read")
+        words = mask.shape
+        if not (mask.dtype is self.i32 and mask.is_contiguous() and mask.get_device() == ws.get_device()):
+            _refuse_tensors(ws, ("mask", mask, self.i32, 0))
+        if len(words) != 2 or words[0] < T:
+            _refuse_rows("mask", T, mask)
+        if block_table.dim() != 2:
+            _refuse_rows("block_table", B, block_table)
         rc = self.lib.pe_tree_attention(self.addr, B, T, qsl.data_ptr(), seq_len.data_ptr(), q.data_ptr(),
                                         _row_stride(q, T, self.heads, self.hd), k_cache.data_ptr(), v_cache.data_ptr(),
                                         block_table.data_ptr(), block_table.shape[1], num_blocks,
-                                        _dense(ws, "mask", mask.numel(), mask, self.i32), mask.shape[1],
+                                        mask.data_ptr(), words[1],
                                         _addr(sink), out.data_ptr(), _row_stride(out, T, self.heads, self.hd), ws.data_ptr(),
                                         ws.numel(), _stream_handle(stream, ws))
         _check(rc, "pe_tree_attention")
@@ -789,40 +839,58 @@ class PagedAttention:
                 == v_cache.get_device() == block_table.get_device() == out.get_device()
                 == (ws if sink is None else sink).get_device()):
             self._apart(ws, qsl, seq_len, q, k_cache, v_cache, block_table, out, sink)
-    def _layers(self, n_layers, num_blocks, ws, *caches):
+    def _layers(self, n_layers, num_blocks, k_cache, v_cache, ws):
         """Caches of n_layers layers, back to back."""
-        return [_dense(ws, "a cache", n_layers * num_blocks * self.block, c, self.dtype) for c in caches]
+        d, n = self.dtype, n_layers * num_blocks * self.block
+        if not (k_cache.dtype is d and v_cache.dtype is d and k_cache.is_contiguous() and v_cache.is_contiguous()
+                and k_cache.numel() >= n and v_cache.numel() >= n
+                and ws.get_device() == k_cache.get_device() == v_cache.get_device()):
+            _refuse_tensors(ws, ("k_cache", k_cache, d, n), ("v_cache", v_cache, d, n))
 
     def compact(self, n_layers, B, T, qsl, seq_len, accepted, path, block_table, num_blocks, k_cache, v_cache,
                 ws, stream=None):
         """pe_cache_compact: caches [n_layers][num_blocks][G][block_size][hd]; the others int32."""
         i32 = self.i32
-        k, v = self._layers(n_layers, num_blocks, ws, k_cache, v_cache)
-        rc = self.lib.pe_cache_compact(
-            self.addr, n_layers, B, T, _dense(ws, "qsl", B and B + 1, qsl, i32),
-            _dense(ws, "seq_len", B, seq_len, i32), _dense(ws, "accepted", B, accepted, i32),
-            _dense(ws, "path", T, path, i32), _table(ws, block_table, B, i32), block_table.shape[1], num_blocks, k,
-            v, ws.data_ptr(), ws.numel(), _stream_handle(stream, ws))
+        self._layers(n_layers, num_blocks, k_cache, v_cache, ws)
+        if not (qsl.dtype is i32 and seq_len.dtype is i32 and accepted.dtype is i32 and path.dtype is i32
+                and block_table.dtype is i32 and qsl.is_contiguous() and seq_len.is_contiguous()
+                and accepted.is_contiguous() and path.is_contiguous() and block_table.is_contiguous()
+                and (qsl.numel() > B or B == 0) and seq_len.numel() >= B and accepted.numel() >= B
+                and path.numel() >= T and ws.get_device() == qsl.get_device() == seq_len.get_device()
+                == accepted.get_device() == path.get_device() == block_table.get_device()):
+            _refuse_tensors(ws, ("qsl", qsl, i32, B and B + 1), ("seq_len", seq_len, i32, B),
+                            ("accepted", accepted, i32, B), ("path", path, i32, T), ("block_table", block_table, i32, 0))
+        table = block_table.shape
+        if len(table) != 2 or table[0] < B:
+            _refuse_rows("block_table", B, block_table)
+        rc = self.lib.pe_cache_compact(self.addr, n_layers, B, T, qsl.data_ptr(), seq_len.data_ptr(),
+                                       accepted.data_ptr(), path.data_ptr(), block_table.data_ptr(), table[1],
+                                       num_blocks, k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(), ws.numel(),
+                                       _stream_handle(stream, ws))
         _check(rc, "pe_cache_compact")
 
     def copy_pages(self, n_layers, n, src, dst, num_blocks, k_cache, v_cache, ws, stream=None):
         """pe_cache_copy: pages src[i] to dst[i] (int32) of every layer."""
-        k, v = self._layers(n_layers, num_blocks, ws, k_cache, v_cache)
-        rc = self.lib.pe_cache_copy(self.addr, n_layers, n, _dense(ws, "src", n, src, self.i32),
-                                    _dense(ws, "dst", n, dst, self.i32), num_blocks, k, v, ws.data_ptr(), ws.numel(),
+        i32 = self.i32
+        self._layers(n_layers, num_blocks, k_cache, v_cache, ws)
+        if not (src.dtype is i32 and dst.dtype is i32 and src.is_contiguous() and dst.is_contiguous()
+                and src.numel() >= n and dst.numel() >= n and ws.get_device() == src.get_device() == dst.get_device()):
+            _refuse_tensors(ws, ("src", src, i32, n), ("dst", dst, i32, n))
+        rc = self.lib.pe_cache_copy(self.addr, n_layers, n, src.data_ptr(), dst.data_ptr(), num_blocks,
+                                    k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(), ws.numel(),
                                     _stream_handle(stream, ws))
         _check(rc, "pe_cache_copy")
 
     def fork(self, n_layers, n, parent, child, length, block_table, refs, k_cache, v_cache, ws, stream=None):
         """pe_pages_fork: rows child[i] of block_table share the first length[i] positions of rows
         parent[i]; refs counts the uses of each page (num_blocks of them).  All int32."""
-        i32, num_blocks = self.i32, refs.numel()
-        k, v = self._layers(n_layers, num_blocks, ws, k_cache, v_cache)
-        rc = self.lib.pe_pages_fork(
-            self.addr, n_layers, n, _dense(ws, "parent", n, parent, i32), _dense(ws, "child", n, child, i32),
-            _dense(ws, "length", n, length, i32), _table(ws, block_table, 0, i32), block_table.shape[0],
-            block_table.shape[1], num_blocks, _dense(ws, "refs", 0, refs, i32), k, v, ws.data_ptr(), ws.numel(),
-            _stream_handle(stream, ws))
+        num_blocks = refs.numel()
+        self._layers(n_layers, num_blocks, k_cache, v_cache, ws)
+        rows, max_blocks = _pool(ws, n, block_table, refs, parent=parent, child=child, length=length)
+        rc = self.lib.pe_pages_fork(self.addr, n_layers, n, parent.data_ptr(), child.data_ptr(), length.data_ptr(),
+                                    block_table.data_ptr(), rows, max_blocks, num_blocks, refs.data_ptr(),
+                                    k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(), ws.numel(),
+                                    _stream_handle(stream, ws))
         _check(rc, "pe_pages_fork")
 
 

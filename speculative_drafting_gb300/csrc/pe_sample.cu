@@ -8,7 +8,8 @@
 //   row kernel   CTA (row, part) streams its part of the logits once: the largest logit, the
 //                sum of weights (top-p), the first largest token (greedy) or the best score
 //                (nothing is cut: the noise is streamed along).  For rows with a cut it also
-//                leaves the largest logit of each group of some hundred tokens.
+//                leaves the largest logit of each group of some dozens of tokens: what a few
+//                neighbouring threads load in one trip, so that a group lies in few pieces.
 //   cut kernel   a CTA per row joins the parts.  For a row with a cut:
 //                  - a bound from below for it.  The groups' largest logits are tokens of the
 //                    row, so the value at which k of them (for top-p: enough of them to weigh
@@ -81,9 +82,10 @@ struct SampleArgs {
   int32_t* token;
   uint32_t* status;
   int part, parts;   // 16-byte vectors of a part, parts of a row
+  int trips;         // of a part's CTA
   int gshift;        // threads of a group: 1 << gshift
   Part* stat;        // [T][parts]
-  float* top;        // [T][parts][kThreads >> gshift]
+  float* top;        // [T][parts][trips][kThreads >> gshift]
   Settings* set;  // [T] of each row
   uint32_t* todo_n;  // rows for the wide kernel
   int32_t* todo;     // [T]
@@ -379,27 +381,20 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
       out.g = bg;
       a.stat[static_cast<size_t>(row) * a.parts + part] = out;
     }
-  } else if (st.k > 0 || st.p >= 1.f) {
-    for (int j = tid; j < n; j += kUnroll * kThreads) {
-#pragma unroll
-      for (int x = 0; x < kUnroll; ++x) {
-        m = max_nan(m, vec_max<T>(u[x]));
-        const int jn = j + (x + kUnroll) * kThreads;
-        u[x] = jn < n ? s.load(v0 + jn) : no_tokens<T>();
-      }
-    }
   } else {
-    // sum of 2^((l - m) c), c = log2(e) / T: the difference is exact near the largest logit
+    // sum of 2^((l - m) c), c = log2(e) / T, for top-p alone: the difference is exact near the
+    // largest logit
+    const bool weigh = st.k == 0 && st.p < 1.f;
     const float c = scale_of(st.temp);
     const uint64_t c2 = pack_f32x2(c, c);
     float sum = 0.f;
-    for (int j = tid; j < n; j += kUnroll * kThreads) {
-      // one maximum and one rescaling for the kUnroll vectors
-      float mn = m;
+    float* top = a.top + (static_cast<size_t>(row) * a.parts + part) * a.trips * (kThreads >> a.gshift);
+    for (int trip = 0; trip < a.trips; ++trip) {
+      float of_trip = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < kUnroll; ++x) mn = max_nan(mn, vec_max<T>(u[x]));
-      const float off = mn == -INFINITY ? 0.f : mn;
-      sum *= ex2((m - off) * c);
+      for (int x = 0; x < kUnroll; ++x) of_trip = max_nan(of_trip, vec_max<T>(u[x]));
+      const float mn = max_nan(m, of_trip), off = mn == -INFINITY ? 0.f : mn;
+      if (weigh) sum *= ex2((m - off) * c);  // one rescaling for the kUnroll vectors
       m = mn;
       const uint64_t off2 = pack_f32x2(-off, -off);
       uint64_t acc[2] = {0ull, 0ull};
@@ -407,35 +402,32 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
       for (int x = 0; x < kUnroll; ++x) {
         float f[kVec];
         unpack16<T>(u[x], f);
-        const int jn = j + (x + kUnroll) * kThreads;
+        const int jn = tid + ((trip + 1) * kUnroll + x) * kThreads;
         u[x] = jn < n ? s.load(v0 + jn) : no_tokens<T>();
+        if (weigh) {
 #pragma unroll
-        for (int e = 0; e < kVec; e += 2) {
-          float p, q;
-          unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(f[e], f[e + 1]), off2), c2), p, q);
-          acc[e / 2 & 1] = add_f32x2(acc[e / 2 & 1], pack_f32x2(ex2(p), ex2(q)));
+          for (int e = 0; e < kVec; e += 2) {
+            float p, q;
+            unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(f[e], f[e + 1]), off2), c2), p, q);
+            acc[e / 2 & 1] = add_f32x2(acc[e / 2 & 1], pack_f32x2(ex2(p), ex2(q)));
+          }
         }
       }
       float s0, s1;
       unpack_f32x2(add_f32x2(acc[0], acc[1]), s0, s1);
       sum += s0 + s1;
+      for (int o = 1; o < 1 << a.gshift; o <<= 1) of_trip = max_nan(of_trip, __shfl_xor_sync(0xffffffffu, of_trip, o));
+      if ((lane & ((1 << a.gshift) - 1)) == 0) top[trip * (kThreads >> a.gshift) + (tid >> a.gshift)] = of_trip;
     }
     out.m = cta_max<kWarps>(m, warp_m);
-    out.s = cta_sum<kWarps>(m > -INFINITY ? sum * ex2((m - out.m) * c) : 0.f, warp_m);
-  }
-  if (!free && st.temp != 0.f) {
-    if (st.k > 0 || st.p >= 1.f) out.m = cta_max<kWarps>(m, warp_m);
-    float t = m;
-    for (int o = 1; o < 1 << a.gshift; o <<= 1) t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, o));
-    if ((lane & ((1 << a.gshift) - 1)) == 0)
-      a.top[(static_cast<size_t>(row) * a.parts + part) * (kThreads >> a.gshift) + (tid >> a.gshift)] = t;
+    if (weigh) out.s = cta_sum<kWarps>(m > -INFINITY ? sum * ex2((m - out.m) * c) : 0.f, warp_m);
   }
   if ((!free || st.temp == 0.f) && tid == 0) a.stat[static_cast<size_t>(row) * a.parts + part] = out;
 }
 
 // ------------------------------------------------------------------ cut kernel
 
-// weights as integers: 2^38, so that 2^24 of them have a sum (in two parts: 2^20, 2^18)
+// weights as integers: 2^38, so that 2^20 of them have a sum (in two parts: 2^20, 2^18)
 constexpr float kOne = 0x1p38f;
 
 // Shared memory of the cut kernel.
@@ -491,7 +483,7 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
   const Settings st = a.set[row];
   const Part* stat = a.stat + static_cast<size_t>(row) * a.parts;
   // (what only some rows need is asked for with the settings; no more parts than threads)
-  const int gpp = kThreads >> a.gshift, groups = a.parts * gpp;  // groups of a part, of the row
+  const int gpt = 8 - a.gshift, groups = a.parts * a.trips << gpt;  // log2 of a trip's groups; the row's
   const float* top = a.top + static_cast<size_t>(row) * groups;
   float part_m = -INFINITY, part_s = 0.f, top_m[kGroups / kCutThreads];
   if (tid < a.parts) {
@@ -611,38 +603,39 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
   const Row<T> s(a, row);
   const int nv = s.vectors(), n_groups = sh.n_groups;
   if (n_groups <= kGroupList) {
-    // A warp to a group: which of its vectors (of each trip over the part, as many as it has
-    // threads) reach the bound.  Then a thread to a vector: its tokens.
-    const int warp = tid >> 5, per = ((a.part + kThreads - 1) / kThreads) << a.gshift;
-    for (int j = lane; j < (per + 31 & ~31); j += 32) {
-      const int in_part = (j >> a.gshift) * kThreads + (j & ((1 << a.gshift) - 1));
-      for (int i0 = warp; i0 < n_groups; i0 += kUnroll * kCutWarps) {
-        uint4 u[kUnroll];
-        int v[kUnroll];
+    // Which of their vectors reach the bound (a group has those of its threads in each of a trip's
+    // loads), a thread to a vector.  Then those vectors' tokens.
+    const int per = 2 + a.gshift, items = n_groups << per;  // log2 of a group's vectors
+    static_assert(kUnroll == 4 && kThreads == 256, "");
+    for (int i0 = tid & ~31; i0 < items; i0 += kUnroll * kCutThreads) {
+      uint4 u[kUnroll];
+      int v[kUnroll];
 #pragma unroll
-        for (int x = 0; x < kUnroll; ++x) {
-          const int g = sh.group[min(i0 + x * kCutWarps, n_groups - 1)];
-          const int at = in_part + ((g & (gpp - 1)) << a.gshift);
-          v[x] = (g >> (8 - a.gshift)) * a.part + at;
-          if (j >= per || at >= a.part || v[x] >= nv || i0 + x * kCutWarps >= n_groups) v[x] = -1;
-          u[x] = v[x] >= 0 ? s.load(v[x]) : no_tokens<T>();
-        }
-        unsigned hit[kUnroll];
-        int hits = 0;
+      for (int x = 0; x < kUnroll; ++x) {
+        const int i = i0 + x * kCutThreads + lane;
+        const int g = sh.group[min(i, items - 1) >> per], j = i & ((1 << per) - 1);
+        const int trip = g >> gpt, part = trip / a.trips;
+        const int at = (trip - part * a.trips) * kUnroll * kThreads + (j >> a.gshift) * kThreads +
+                       ((g & ((1 << gpt) - 1)) << a.gshift) + (j & ((1 << a.gshift) - 1));
+        v[x] = part * a.part + at;
+        if (i >= items || at >= a.part || v[x] >= nv) v[x] = -1;
+        u[x] = v[x] >= 0 ? s.load(v[x]) : no_tokens<T>();
+      }
+      unsigned hit[kUnroll];
+      int hits = 0;
 #pragma unroll
-        for (int x = 0; x < kUnroll; ++x) {
-          hit[x] = __ballot_sync(0xffffffffu, v[x] >= 0 && vec_max<T>(u[x]) >= bound);
-          hits += __popc(hit[x]);
-        }
-        int at = 0;
-        if (lane == 0 && hits) at = atomicAdd(&sh.n_vec, hits);
-        at = __shfl_sync(0xffffffffu, at, 0);
+      for (int x = 0; x < kUnroll; ++x) {
+        hit[x] = __ballot_sync(0xffffffffu, v[x] >= 0 && vec_max<T>(u[x]) >= bound);
+        hits += __popc(hit[x]);
+      }
+      int at = 0;
+      if (lane == 0 && hits) at = atomicAdd(&sh.n_vec, hits);
+      at = __shfl_sync(0xffffffffu, at, 0);
 #pragma unroll
-        for (int x = 0; x < kUnroll; ++x) {
-          const int mine = at + __popc(hit[x] & ((1u << lane) - 1u));
-          if ((hit[x] >> lane & 1u) && mine < kGroupList) sh.vec[mine] = v[x];
-          at += __popc(hit[x]);
-        }
+      for (int x = 0; x < kUnroll; ++x) {
+        const int mine = at + __popc(hit[x] & ((1u << lane) - 1u));
+        if ((hit[x] >> lane & 1u) && mine < kGroupList) sh.vec[mine] = v[x];
+        at += __popc(hit[x]);
       }
     }
     __syncthreads();
@@ -792,6 +785,7 @@ PE_DEV int wide_before(int v, int* warps, int& all) {
 }
 
 template <typename T>
+// (two CTAs an SM: 512 flat rows 850 us instead of 1170, 8 of them 66 instead of 52)
 __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const SampleArgs a) {
   constexpr int kVec = 16 / sizeof(T), kWideRace = 16 / kVec;  // (16 tokens a thread and trip)
   extern __shared__ uint4 held[];
@@ -950,24 +944,39 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
       ++turn;
       return key;
     };
-    // Sum over the row; all threads get it.
-    auto wide_sum = [&](unsigned long long x) {
+    // Sums of two over the row; all threads get them.
+    auto wide_sums = [&](unsigned long long& x, unsigned long long& y) {
 #pragma unroll
-      for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      for (int o = 16; o; o >>= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+        y += __shfl_xor_sync(0xffffffffu, y, o);
+      }
       __syncthreads();
-      if (lane == 0) sh.scan[warp] = x;
+      if (lane == 0) {
+        sh.scan[warp] = x;
+        sh.k[warp] = y;
+      }
       __syncthreads();
       if (warp == 0) {
         x = lane < kWideWarps ? sh.scan[lane] : 0ull;
+        y = lane < kWideWarps ? sh.k[lane] : 0ull;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane < kCluster) put64(&sh.best[turn & 1][rank], lane, x);
+        for (int o = 16; o; o >>= 1) {
+          x += __shfl_xor_sync(0xffffffffu, x, o);
+          y += __shfl_xor_sync(0xffffffffu, y, o);
+        }
+        if (lane < kCluster) {
+          put64(&sh.best[turn & 1][rank], lane, x);
+          put64(&sh.best_key[turn & 1][rank], lane, y);
+        }
       }
       row_sync();
-      x = 0ull;
-      for (int i = 0; i < kCluster; ++i) x += sh.best[turn & 1][i];
+      x = y = 0ull;
+      for (int i = 0; i < kCluster; ++i) {
+        x += sh.best[turn & 1][i];
+        y += sh.best_key[turn & 1][i];
+      }
       ++turn;
-      return x;
     };
 
     // ---------------- The cut: the last token with less than `most` tokens, or weight, before it.
@@ -1220,9 +1229,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
           if (attempt == 0) all += from(f[e], t0 + e, cut) ? q : 0u;
         }
       }
-      before = wide_sum(before);
+      wide_sums(before, all);
       // (the first token is kept whatever top_p is: nothing is before it)
-      if (attempt == 0) most = max(share_of(st.p, wide_sum(all)), 1ull);
+      if (attempt == 0) most = max(share_of(st.p, all), 1ull);
       if (before < most) break;
       cut = attempt == kTries ? find(most, true) : won + 1ull;
     }
@@ -1238,7 +1247,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
 size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
 constexpr int kSlice = 176 * 1024;   // of a row, in a CTA of the wide kernel
-constexpr int kMaxParts = kGroups / (kThreads >> 5);
+constexpr int kMaxParts = kGroups / (kThreads >> 5);  // (and trips, in all of a row's parts)
+constexpr int kMaxVocab = 1 << 20;
 constexpr int kWave = 4;  // CTAs of the row kernel per SM
 
 // Parts of a row: one wave of CTAs (four an SM) where the rows are few, at most 64 KB and at
@@ -1250,10 +1260,15 @@ void plan(SampleArgs& a, int esize, int num_sms) {
   parts = std::max(parts, (nvec * 16 + kMaxPartBytes - 1) / kMaxPartBytes);
   parts = std::min(parts, (nvec + kThreads - 1) / kThreads);
   parts = std::max(1, std::min(parts, kMaxParts));
+  // (no more than kMaxParts trips, which are 2^21 logits: parts of whole ones where that matters)
+  const int trip = kUnroll * kThreads;
   a.part = (nvec + parts - 1) / parts;
+  if (static_cast<int64_t>((nvec + a.part - 1) / a.part) * ((a.part + trip - 1) / trip) > kMaxParts)
+    a.part = (a.part + trip - 1) / trip * trip;
   a.parts = (nvec + a.part - 1) / a.part;
+  a.trips = (a.part + kUnroll * kThreads - 1) / (kUnroll * kThreads);
   a.gshift = 0;
-  while (a.parts * (kThreads >> a.gshift) > kGroups) ++a.gshift;
+  while (a.gshift < 5 && a.parts * a.trips * (kThreads >> a.gshift) > kGroups) ++a.gshift;
 }
 
 // the most parts and groups of a row for any number of rows
@@ -1304,7 +1319,7 @@ cudaError_t launch(const SampleArgs& a, int num_sms, cudaStream_t st) {
 using namespace pe;
 
 extern "C" size_t pe_sample_workspace_bytes(int max_batch, int max_rows, int vocab) {
-  if (max_batch < 0 || max_rows < 0 || vocab < 1 || vocab > 1 << 24) return 0;
+  if (max_batch < 0 || max_rows < 0 || vocab < 1 || vocab > kMaxVocab) return 0;
   const size_t T = max_rows, parts = max_parts(vocab);
   return 256 + al256(T * sizeof(Settings)) + al256(T * sizeof(int32_t)) + al256(T * parts * sizeof(Part)) +
          al256(T * std::min<size_t>(parts * kThreads, kGroups) * sizeof(float));
@@ -1318,7 +1333,7 @@ extern "C" int pe_sample(int B, int T, const int32_t* qsl, const void* logits, i
   if (B < 0 || T < 0 || vocab < 1 || ld_logits < vocab || ld_gumbel < vocab) return PE_ERR_ARG;
   if (dtype != PE_DTYPE_F32 && dtype != PE_DTYPE_BF16) return PE_ERR_UNSUPPORTED;
   if (B == 0) return T == 0 ? PE_OK : PE_ERR_ARG;
-  if (B > 65535 || vocab > 1 << 24) return PE_ERR_UNSUPPORTED;
+  if (B > 65535 || vocab > kMaxVocab) return PE_ERR_UNSUPPORTED;
   if (!qsl || !ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 ||
       ws_bytes < pe_sample_workspace_bytes(B, T, vocab))
     return PE_ERR_ARG;
