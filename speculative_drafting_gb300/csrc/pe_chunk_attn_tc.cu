@@ -1366,11 +1366,16 @@ int launch(const TcArgs& p, const CUtensorMap& km, const CUtensorMap& vm, cudaSt
   if (launch_chained(chunk_tc_kernel<HD, kTree>, dim3(p.grid), dim3(kThreads), Shape<HD>::kSmem, st, km, vm, p) !=
       cudaSuccess)
     return PE_ERR_CUDA;
-  // Rows of a unit per warp of the join (it notes them in 32 bits): one where there are few
-  // (one token 18.6 -> 16.9 us), else eight (64 x 8 rows 109 us, 117 with one).
+  // Rows of a unit per warp of the join (it notes them in 32 bits): one where a unit has few
+  // (one token 18.6 -> 16.9 us); else the fewer rows there are in all, the fewer for each, whose
+  // reads wait for one another (16 nodes of one request over 2048 keys: 37.1 us with eight, 29.8
+  // with four, 27.1 with two, 27.5 with one; 8 x 16 nodes 41.8, 40.4, 41.3, 44.7; 64 x 8 rows
+  // 113, 114, 130, 121; graph replays).
   const int rows = static_cast<int>(
       std::min<long long>(static_cast<long long>(p.c.T) * (p.c.H / p.c.G), p.part_rows));
-  const int join = rows <= 32 ? (rows + 3) / 4 : (rows + 31) / 32;
+  const long long all = static_cast<long long>(p.c.T) * p.c.H;
+  const int per_warp = rows <= 32 ? 1 : all <= 4096 ? 2 : all <= 8192 ? 4 : 8;
+  const int join = (rows + 4 * per_warp - 1) / (4 * per_warp);
   return launch_chained(chunk_join_kernel<HD, kTree>, dim3(p.grid, join), dim3(128), 0, st, p) == cudaSuccess
              ? PE_OK
              : PE_ERR_CUDA;
