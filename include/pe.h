@@ -697,7 +697,8 @@ size_t pe_pages_workspace_bytes(int max_entries, int num_blocks);
  * ceil(length[i] / block_size).  Refused: a row out of range or named twice, a length below 0
  * or above max_blocks * block_size.  Rows are served in order; the first whose pages are not
  * there, and all later ones that need some, are refused.  PE_ERR_ARG: negative n, rows or
- * num_blocks, max_blocks or block_size < 1, null or misaligned pointers, ws. */
+ * num_blocks, max_blocks or block_size < 1, null or misaligned pointers, ws.
+ * PE_ERR_UNSUPPORTED: n > 65535. */
 int pe_pages_reserve(int n, const int32_t* row, const int32_t* length, int32_t* block_table,
                      int rows, int max_blocks, int num_blocks, int block_size, int32_t* refs,
                      void* ws, size_t ws_bytes, void* stream);

@@ -318,6 +318,12 @@ PE_DEV bool last_cta(const PoolArgs& a) {
   return last_sh;
 }
 
+// The k-th free page; -1 where there is none (in a workspace that was not zeroed anything may stand).
+PE_DEV int listed(const PoolArgs& a, int k) {
+  const int page = k >= 0 && k < a.num_blocks ? a.list[k] : -1;
+  return page < a.num_blocks ? page : -1;
+}
+
 // The entries of a row of the table that a length needs, -1: it does not fit in a row.
 PE_DEV int entries_of(const PoolArgs& a, int len) {
   const int e = len < 0 ? -1 : len / a.bs + (len % a.bs != 0);
@@ -360,9 +366,11 @@ __global__ void __launch_bounds__(kScanThreads) reserve_fill_kernel(const PoolAr
     int all;
     const int k = at + scan_before(missing, warps, all);
     if (missing) {
-      const int page = a.list[k];
-      row[b] = page;
-      a.refs[page] = 1;
+      const int page = listed(a, k);
+      if (page >= 0) {
+        row[b] = page;
+        a.refs[page] = 1;
+      }
     }
     at += all;
   }
@@ -408,7 +416,8 @@ __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const PoolArgs a, 
   const int len = a.length[i], full = len / a.bs, part = len % a.bs;
   int32_t* to = a.table + static_cast<int64_t>(a.row[i]) * a.max_blocks;
   const int32_t* from = a.table + static_cast<int64_t>(a.parent[i]) * a.max_blocks;
-  const int page = need ? a.list[a.start[i]] : -1;
+  const int page = need ? listed(a, a.start[i]) : -1;
+  if (need && page < 0) return;
   if (blockIdx.x == 0) {
     for (int b = tid; b < full; b += kThreads) {
       to[b] = from[b];
@@ -600,6 +609,7 @@ extern "C" int pe_pages_reserve(int n, const int32_t* row, const int32_t* length
   if (n < 0 || rows < 0 || max_blocks < 1 || num_blocks < 0 || block_size < 1 ||
       !ws_ok(ws, ws_bytes, pe_pages_workspace_bytes(n, num_blocks)))
     return PE_ERR_ARG;
+  if (n > 65535) return PE_ERR_UNSUPPORTED;
   if (n == 0) return PE_OK;
   PoolArgs a = {};
   if (pool_args(a, n, row, rows, length, block_table, max_blocks, num_blocks, block_size, refs, ws) != PE_OK)

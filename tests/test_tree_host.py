@@ -152,7 +152,7 @@ def test_pages(lib, plan):
                                           *pointers("parent", "child", "length", "table", "refs"),
                                           *pointers("k", "v", align=16)])
     assert lib.pe_pages_fork(*fork(plan, n=65536)) == UNSUP
-    assert lib.pe_pages_reserve(*reserve(n=0)) == OK
+    assert lib.pe_pages_reserve(*reserve(n=0)) == OK and lib.pe_pages_reserve(*reserve(n=65536)) == UNSUP
     check(lib.pe_pages_reserve, reserve, [dict(n=-1), dict(rows=-1), dict(mb=0), dict(nb=-1), dict(bs=0), dict(wsb=need - 1),
                                           dict(ws=None), *pointers("row", "length", "table", "refs")])
     assert lib.pe_pages_free(*free(n=0)) == OK
