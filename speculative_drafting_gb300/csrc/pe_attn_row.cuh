@@ -47,7 +47,8 @@ PE_DEV uint32_t mask_bits(const uint32_t* bits, int words, int64_t s) {
 // Keys 0 .. lim of request r for its row `row` (of all), head h; of a tree (kTree), of the keys
 // from `first` on those whose bit is set in the row's mask.
 template <typename T, bool kTree>
-PE_DEV void attend_row(const ChunkArgs& a, int r, int row, int h, int lim, int first, RowScratch& sh) {
+PE_DEV void attend_row(const ChunkArgs& a, const TreeMask& mask, int r, int row, int h, int lim, int first,
+                       RowScratch& sh) {
   constexpr int kVec = 16 / sizeof(T);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = h / (a.H / a.G);
@@ -60,10 +61,8 @@ PE_DEV void attend_row(const ChunkArgs& a, int r, int row, int h, int lim, int f
     const int t = static_cast<int>(t0) + lane;
     int64_t base = -1;
     float s = -INFINITY;
-    bool seen = t0 + lane <= lim;
-    if (kTree && t0 + 31 >= first)
-      seen = seen && mask_bits(a.mask + static_cast<int64_t>(row) * a.words, a.words, t0 - first) >> lane & 1u;
-    if (seen) {
+    if (t0 + lane <= lim && (!kTree || t0 + 31 < first ||
+                             (mask_bits(mask.bits + static_cast<int64_t>(row) * mask.words, mask.words, t0 - first) >> lane & 1u))) {
       const int blk = a.block_table[static_cast<int64_t>(r) * a.max_blocks + t / a.bs];
       if (blk < 0 || blk >= a.num_blocks) {
         set_status(a.status, PE_ST_BLOCK_RANGE);

@@ -17,9 +17,8 @@
 namespace pe {
 namespace {
 
-// (48 registers: with 56 a small fp32 call takes 17 us, with 48 13 us, with 40 16 us)
 template <typename T, bool kTree>
-__global__ void __launch_bounds__(32 * kRowWarps, 10) chunk_simt_kernel(const ChunkArgs a) {
+PE_DEV void chunk_simt(const ChunkArgs& a, const TreeMask& mask) {
   __shared__ RowScratch sh;
   __shared__ int req_sh;
   pdl_trigger();
@@ -34,7 +33,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 10) chunk_simt_kernel(const Ch
   for (int r = tid; r < a.B; r += 32 * kRowWarps) {
     const RowRange x = request_rows(a.qsl, r, a.T);
     if (x.bad) set_status(a.status, PE_ST_ROWS_RANGE);
-    if (kTree && x.q1 - x.q0 > 32 * a.words) set_status(a.status, PE_ST_TREE);
+    if (kTree && x.q1 - x.q0 > 32 * mask.words) set_status(a.status, PE_ST_TREE);
     // (of every request, those without rows too)
     if (row == 0 && h == 0 && (a.seq_len[r] < 0 || a.seq_len[r] > Lmax)) set_status(a.status, PE_ST_BLOCK_RANGE);
     if (x.q0 <= row && row < x.q1) atomicMax(&req_sh, r);
@@ -46,7 +45,16 @@ __global__ void __launch_bounds__(32 * kRowWarps, 10) chunk_simt_kernel(const Ch
   const int n = rr.q1 - rr.q0, j = row - rr.q0;
   const int L = static_cast<int>(min(max(static_cast<int64_t>(a.seq_len[r]), int64_t{0}), Lmax));
   const int lim = kTree ? L - 1 : L - n + j;  // the row's own position
-  attend_row<T, kTree>(a, r, row, h, lim, L - n, sh);
+  attend_row<T, kTree>(a, mask, r, row, h, lim, kTree ? L - n : 0, sh);
+}
+// (48 registers: with 56 a small fp32 call takes 17 us, with 48 13 us, with 40 16 us)
+template <typename T>
+__global__ void __launch_bounds__(32 * kRowWarps, 10) chunk_simt_kernel(const ChunkArgs a) {
+  chunk_simt<T, false>(a, TreeMask{});
+}
+template <typename T>
+__global__ void __launch_bounds__(32 * kRowWarps, 10) tree_simt_kernel(const ChunkArgs a, const TreeMask mask) {
+  chunk_simt<T, true>(a, mask);
 }
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -68,7 +76,7 @@ int chunk_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qsl, 
                     const void* q, int64_t ld_q, const void* k_cache, const void* v_cache,
                     const int32_t* block_table, int max_blocks, int num_blocks, const float* sink, void* out,
                     int64_t ld_out, void* ws, size_t ws_bytes, void* stream, int stall, bool tree = false,
-                    const uint32_t* mask = nullptr, int words = 0) {
+                    TreeMask mask = {}) {
   if (!plan_ok(plan) || B < 0 || T < 0 || max_blocks < 1 || num_blocks < 0) return PE_ERR_ARG;
   const int64_t width = static_cast<int64_t>(plan->n_heads) * plan->head_dim;
   if (ld_q < width || ld_out < width || ld_q % 8 || ld_out % 8) return PE_ERR_ARG;
@@ -86,7 +94,7 @@ int chunk_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qsl, 
       if (!aligned(p, 16)) return PE_ERR_ARG;
     if (!aligned(qsl, 4) || !aligned(seq_len, 4) || !aligned(block_table, 4) || !aligned(sink, 4))
       return PE_ERR_ARG;
-    if (tree && (!mask || !aligned(mask, 4))) return PE_ERR_ARG;
+    if (tree && (!mask.bits || !aligned(mask.bits, 4))) return PE_ERR_ARG;
   }
   if (B == 0 || T == 0) return PE_OK;
   ChunkArgs a = {};
@@ -110,14 +118,13 @@ int chunk_attention(const pe_attn_plan* plan, int B, int T, const int32_t* qsl, 
   a.ld_out = ld_out;
   a.status = static_cast<uint32_t*>(ws);
   a.stall = stall;
-  a.mask = mask;
-  a.words = words;
-  if (chunk_tc_takes(plan) && num_blocks > 0) return launch_chunk_tc(a, static_cast<char*>(ws), st);
+  if (chunk_tc_takes(plan) && num_blocks > 0) return launch_chunk_tc(a, mask, static_cast<char*>(ws), st);
   const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(plan->n_heads));
   const bool b = plan->dtype == PE_DTYPE_BF16;
-  void (*kernel)(ChunkArgs) = tree ? (b ? chunk_simt_kernel<bf16, true> : chunk_simt_kernel<float, true>)
-                                   : (b ? chunk_simt_kernel<bf16, false> : chunk_simt_kernel<float, false>);
-  const cudaError_t e = launch_chained(kernel, grid, dim3(32 * kRowWarps), 0, st, a);
+  const dim3 block(32 * kRowWarps);
+  const cudaError_t e =
+      tree ? launch_chained(b ? tree_simt_kernel<bf16> : tree_simt_kernel<float>, grid, block, 0, st, a, mask)
+           : launch_chained(b ? chunk_simt_kernel<bf16> : chunk_simt_kernel<float>, grid, block, 0, st, a);
   return e == cudaSuccess ? PE_OK : PE_ERR_CUDA;
 }
 
@@ -142,7 +149,7 @@ extern "C" int pe_tree_attention(const pe_attn_plan* plan, int B, int T, const i
   NvtxRange nvtx("pe_tree_attention");
   if (words < 1 || words > PE_TREE_MAX_NODES / 32) return PE_ERR_ARG;
   return chunk_attention(plan, B, T, qsl, seq_len, q, ld_q, k_cache, v_cache, block_table, max_blocks, num_blocks, sink,
-                         out, ld_out, ws, ws_bytes, stream, 0, true, mask, words);
+                         out, ld_out, ws, ws_bytes, stream, 0, true, TreeMask{mask, words});
 }
 
 extern "C" int pe_test_chunk_attention_stall(const pe_attn_plan* plan, int slot, int B, int T, const int32_t* qsl,

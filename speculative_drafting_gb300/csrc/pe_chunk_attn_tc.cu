@@ -33,6 +33,7 @@
 #include <atomic>
 #include <cfloat>
 #include <climits>
+#include <type_traits>
 
 #include "pe_attn_row.cuh"
 #include "pe_tmem.cuh"
@@ -117,6 +118,16 @@ struct TcArgs {
   int part_rows;
   Rec* rec;         // [grid]
 };
+struct TcTreeArgs : TcArgs {
+  TreeMask mask;
+};
+template <bool kTree>
+using Args = std::conditional_t<kTree, TcTreeArgs, TcArgs>;
+template <bool kTree>
+PE_DEV TreeMask mask_of(const Args<kTree>& p) {
+  if constexpr (kTree) return p.mask;
+  return TreeMask{};
+}
 
 template <bool kTree>
 PE_DEV Req load_req(const ChunkArgs& a, int r, bool report) {
@@ -130,7 +141,6 @@ PE_DEV Req load_req(const ChunkArgs& a, int r, bool report) {
   q.L = over ? static_cast<int>(min(max(static_cast<long long>(L), 0ll), Lmax)) : L;
   if (report && (x.bad || over))
     set_status(a.status, (x.bad ? PE_ST_ROWS_RANGE : 0u) | (over ? PE_ST_BLOCK_RANGE : 0u));
-  if (kTree && report && q.n > 32 * a.words) set_status(a.status, PE_ST_TREE);
   const int HG = a.H / a.G;
   q.R = q.n * HG;
   q.Q = (q.R + kUnitRows - 1) / kUnitRows;
@@ -386,7 +396,7 @@ __device__ __noinline__ void finish_unit(const TcArgs& p, const Unit& u, int* ba
 template <int HD, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_tc_kernel(const __grid_constant__ CUtensorMap kmap,
-                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TcArgs p) {
+                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args<kTree> p) {
   using S = Shape<HD>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t k_full[S::kSlots], k_empty[S::kSlots];
@@ -470,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Req req0;  // of this thread's first request (with up to kThreads requests, its only one)
   for (int r = r_lo; r < r_hi; ++r) {
     const Req q = load_req<kTree>(a, r, blockIdx.x == 0);
+    if (kTree && blockIdx.x == 0 && q.n > 32 * mask_of<kTree>(p).words) set_status(a.status, PE_ST_TREE);
     if (r == r_lo) req0 = q;
     mine += req_cost<kTree>(q, ov);
   }
@@ -743,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int b = 0; b < kKeys / 32; ++b)
               tree[b] = lim < 0 ? 0u
-                                : mask_bits(a.mask + static_cast<int64_t>(lim) * a.words, a.words,
+                                : mask_bits(p.mask.bits + static_cast<int64_t>(lim) * p.mask.words, p.mask.words,
                                             t0 + kKeys * hf + 32 * b - static_cast<int64_t>(lim0 + 1));
           } else {
 #pragma unroll
@@ -1171,7 +1182,7 @@ PE_DEV int join_row(int i, int warp) { return (blockIdx.y + i * gridDim.y) * kRo
 // so far as a key of the unit is past them.  (This and the next one are calls, not inlined:
 // their registers would be the join's.)
 template <bool kTree>
-__device__ __noinline__ void redo_unit(const TcArgs& p, int r, int g, int row0, uint32_t again,
+__device__ __noinline__ void redo_unit(const Args<kTree>& p, int r, int g, int row0, uint32_t again,
                                        RowScratch& scratch) {
   __shared__ uint32_t again_sh[kRowWarps];
   const ChunkArgs& a = p.c;
@@ -1199,7 +1210,7 @@ __device__ __noinline__ void redo_unit(const TcArgs& p, int r, int g, int row0, 
       if (!kTree && lim >= kend - 1) continue;
       row_query<bf16>(a, q.q0 + tok, head, scratch);
       __syncthreads();
-      attend_row<bf16, kTree>(a, r, q.q0 + tok, head, lim, q.L - q.n, scratch);
+      attend_row<bf16, kTree>(a, mask_of<kTree>(p), r, q.q0 + tok, head, lim, q.L - q.n, scratch);
       __syncthreads();
     }
   __syncthreads();
@@ -1208,7 +1219,7 @@ __device__ __noinline__ void redo_unit(const TcArgs& p, int r, int g, int row0, 
 // The whole units of this CTA's list up to the last that was noted, as the K warp of the
 // first kernel went through them.
 template <int HD, bool kTree>
-__device__ __noinline__ void redo_list(const TcArgs& p, RowScratch& scratch) {
+__device__ __noinline__ void redo_list(const Args<kTree>& p, RowScratch& scratch) {
   const ChunkArgs& a = p.c;
   const Rec& rec = p.rec[blockIdx.x];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, HG = a.H / a.G;
@@ -1246,7 +1257,7 @@ __device__ __noinline__ void redo_list(const TcArgs& p, RowScratch& scratch) {
 // first ones of the CTAs after c, up to the one that ends it.  One warp per row.  Then the
 // rows to compute again: of that unit, and of CTA c's whole units that have some.
 template <int HD, bool kTree>
-__global__ void __launch_bounds__(32 * kRowWarps) chunk_join_kernel(const __grid_constant__ TcArgs p) {
+__global__ void __launch_bounds__(32 * kRowWarps) chunk_join_kernel(const __grid_constant__ Args<kTree> p) {
   constexpr int V = HD / 32;
   __shared__ RowScratch scratch;
   pdl_trigger();
@@ -1351,7 +1362,7 @@ size_t rec_bytes() { return al256(kMaxGrid * sizeof(Rec)); }
 size_t ml_bytes(int part_rows) { return al256(size_t{kMaxGrid} * 2 * part_rows * 2 * sizeof(float)); }
 
 template <int HD, bool kTree>
-int launch(const TcArgs& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+int launch(const Args<kTree>& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
   // the function's shared-memory limit, once per device (a bit each; past 63 every time)
   static std::atomic<uint64_t> set{0};
   int dev = 0;
@@ -1393,8 +1404,9 @@ size_t chunk_tc_workspace(const pe_attn_plan* plan, int max_rows) {
          al256(size_t{kMaxGrid} * 2 * rows * plan->head_dim * sizeof(float));
 }
 
-int launch_chunk_tc(const ChunkArgs& a, char* ws, cudaStream_t st) {
-  TcArgs p = {};
+int launch_chunk_tc(const ChunkArgs& a, const TreeMask& mask, char* ws, cudaStream_t st) {
+  TcTreeArgs p = {};
+  p.mask = mask;
   p.c = a;
   p.box = 8;
   const int tile = a.hd == 64 ? Shape<64>::kTile : Shape<128>::kTile;
@@ -1422,7 +1434,7 @@ int launch_chunk_tc(const ChunkArgs& a, char* ws, cudaStream_t st) {
   auto* encode = a.hd == 64 ? encode_tmap_bf16 : encode_tmap_bf16_rows128;
   if (!encode(&km, a.k_cache, rows, a.hd, p.box) || !encode(&vm, a.v_cache, rows, a.hd, p.box))
     return PE_ERR_CUDA;
-  if (a.mask) return a.hd == 64 ? launch<64, true>(p, km, vm, st) : launch<128, true>(p, km, vm, st);
+  if (mask.bits) return a.hd == 64 ? launch<64, true>(p, km, vm, st) : launch<128, true>(p, km, vm, st);
   return a.hd == 64 ? launch<64, false>(p, km, vm, st) : launch<128, false>(p, km, vm, st);
 }
 

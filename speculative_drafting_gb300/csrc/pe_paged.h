@@ -42,15 +42,19 @@ struct ChunkArgs {
   void* out;
   int64_t ld_out;
   uint32_t* status;
-  const uint32_t* mask;  // pe_tree_attention: [T][words], else null
-  int words;
   int stall;  // pe_test_chunk_attention_stall's, else 0
+};
+// The masks of pe_tree_attention beside it (an argument of their own: in ChunkArgs they cost the
+// kernels without a tree half a microsecond of a small call, in registers).
+struct TreeMask {
+  const uint32_t* bits;  // [T][words], null: no tree
+  int words;
 };
 
 // The tensor-core kernels of the two (bf16, blocks of a multiple of 8 keys).
 bool chunk_tc_takes(const pe_attn_plan* plan);
 size_t chunk_tc_workspace(const pe_attn_plan* plan, int max_rows);
-int launch_chunk_tc(const ChunkArgs& a, char* ws, cudaStream_t st);
+int launch_chunk_tc(const ChunkArgs& a, const TreeMask& mask, char* ws, cudaStream_t st);
 
 // Rows [q0, q1) of request r, clamped to [0, T]; bad: qsl is not a
 // non-decreasing run from 0 to at most T.
