@@ -686,8 +686,12 @@ def pages_reserve(n, row, length, block_table, refs, block_size, ws, stream=None
 
 def pages_free(n, row, block_table, refs, ws, stream=None):
     """pe_pages_free: rows row[i] of block_table give their pages back.  All int32."""
-    rows, max_blocks = _pool(ws, n, block_table, refs, row=row)
-    rc = load().pe_pages_free(n, row.data_ptr(), block_table.data_ptr(), rows, max_blocks, refs.numel(),
+    i32, table = _types()[2], block_table.shape
+    if not (row.dtype is i32 and block_table.dtype is i32 and refs.dtype is i32 and row.is_contiguous()
+            and block_table.is_contiguous() and refs.is_contiguous() and row.numel() >= n and len(table) == 2
+            and ws.get_device() == row.get_device() == block_table.get_device() == refs.get_device()):
+        _pool(ws, n, block_table, refs, row=row)
+    rc = load().pe_pages_free(n, row.data_ptr(), block_table.data_ptr(), table[0], table[1], refs.numel(),
                               refs.data_ptr(), ws.data_ptr(), ws.numel(), _stream_handle(stream, ws))
     _check(rc, "pe_pages_free")
 
@@ -884,11 +888,16 @@ class PagedAttention:
     def fork(self, n_layers, n, parent, child, length, block_table, refs, k_cache, v_cache, ws, stream=None):
         """pe_pages_fork: rows child[i] of block_table share the first length[i] positions of rows
         parent[i]; refs counts the uses of each page (num_blocks of them).  All int32."""
-        num_blocks = refs.numel()
+        i32, num_blocks, table = self.i32, refs.numel(), block_table.shape
         self._layers(n_layers, num_blocks, k_cache, v_cache, ws)
-        rows, max_blocks = _pool(ws, n, block_table, refs, parent=parent, child=child, length=length)
+        if not (parent.dtype is i32 and child.dtype is i32 and length.dtype is i32 and block_table.dtype is i32
+                and refs.dtype is i32 and parent.is_contiguous() and child.is_contiguous() and length.is_contiguous()
+                and block_table.is_contiguous() and refs.is_contiguous() and parent.numel() >= n and child.numel() >= n
+                and length.numel() >= n and len(table) == 2 and ws.get_device() == parent.get_device()
+                == child.get_device() == length.get_device() == block_table.get_device() == refs.get_device()):
+            _pool(ws, n, block_table, refs, parent=parent, child=child, length=length)
         rc = self.lib.pe_pages_fork(self.addr, n_layers, n, parent.data_ptr(), child.data_ptr(), length.data_ptr(),
-                                    block_table.data_ptr(), rows, max_blocks, num_blocks, refs.data_ptr(),
+                                    block_table.data_ptr(), table[0], table[1], num_blocks, refs.data_ptr(),
                                     k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(), ws.numel(),
                                     _stream_handle(stream, ws))
         _check(rc, "pe_pages_fork")
