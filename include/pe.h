@@ -666,7 +666,7 @@ int pe_cache_compact(const pe_attn_plan* plan, int n_layers, int B, int T, const
  * token = argmax over the kept ones of (logit - largest) / temperature + gumbel, the lowest
  * index on ties: a draw from the kept tokens' probabilities.  Temperature 0: the largest
  * logit's, by pe_verify_greedy's rules.  Sums and weights are formed in fp32 or more: a
- * token whose sum before it, or w, is within 1e-6 of the bound may fall on either side;
+ * token whose sum before it, or w, is within 1e-5 of the bound may fall on either side;
  * two scores within a few fp32 roundings may trade places.
  * A logit of -inf is never kept.  A row with a NaN or +inf logit, with nothing but -inf, or
  * whose kept tokens all have noise of -inf or NaN gets token -1 and PE_ST_SAMPLING (at

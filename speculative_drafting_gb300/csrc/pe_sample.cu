@@ -21,8 +21,8 @@
 //                each in shared memory.  Top-p: all tokens race, and the weight before the
 //                winner tells whether it is kept (if not, the tokens before it race again).
 //                Top-k: a histogram of counts over the distance from the largest logit, finer
-//                ones inside the bin of the cut, then the race.  Weights are 31-bit integers there: their
-//                sums do not depend on an order.
+//                ones inside the bin of the cut, then the race.  Weights are 40-bit integers there:
+//                their sums do not depend on an order.
 //
 // The first kernel is bound by the logits' bytes.  (Every row by a cluster with the row in
 // shared memory: 512 bf16 rows of 201,088 with top-k 162 us; the barriers of a row are waited
@@ -747,7 +747,7 @@ PE_DEV void row_sync() {
 // held twice and taken in turn: whoever writes a place again has met all of them at a barrier
 // since the last one read it.
 struct __align__(16) WideShared {
-  uint2 bins[2][kBins];  // counts; or sums of weights' lower and upper bits
+  uint2 bins[2][kBins];  // counts; or sums of weights, their lower and upper word
   float m[kCluster], lo[kCluster];  // of every CTA: largest and least finite logit
   uint4 in[2][kCluster];  // ... of the cut's bin: tokens, least and greatest order
   unsigned long long best[2][kCluster], best_key[2][kCluster];  // ... of its best score, and which token
@@ -851,9 +851,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
       lo = fminf(lo, sh.lo[i]);
     }
     const float c = scale_of(st.temp), it = 1.f / st.temp;
-    auto weight_bits = [&](float x) { return static_cast<uint32_t>(ex2((x - M) * c) * 0x1p31f); };
-    // bits of a weight in a bin's lower sum: a slice of up to 2^16 tokens, or 2^21
-    const int low = per * kVec <= 65536 ? 16 : 11;
+    // 2^20 weights of at most 2^40 have a sum; what is cut off of them is below 2^-20 of it
+    auto as_weight = [](float w) { return static_cast<unsigned long long>(w * 0x1p40f); };
+    auto weight_of = [&](float x) { return as_weight(ex2((x - M) * c)); };
+    auto add_weight = [](uint2& bin, unsigned long long q) {  // (the lower word's carry goes to the upper one)
+      const uint32_t lo = static_cast<uint32_t>(q);
+      const uint32_t hi = static_cast<uint32_t>(q >> 32) + (lo && atomicAdd(&bin.x, lo) + lo < lo);
+      if (hi) atomicAdd(&bin.y, hi);
+    };
 
     const Noise<T> noise(a, row, s.shift);
     // whether a token comes no later than a key (argmax_key), or before it
@@ -1040,9 +1045,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
               for (int e = 0; e < kVec; ++e) {
                 const int d = linear(fminf((M - f[e]) * scale, kTop));
                 if (by_w) {
-                  const uint32_t q = weight_bits(f[e]), lower = q & ((1u << low) - 1u);
-                  if (lower) atomicAdd(&bins[d].x, lower);
-                  if (q >> low) atomicAdd(&bins[d].y, q >> low);
+                  add_weight(bins[d], weight_of(f[e]));
                 } else if (f[e] > -INFINITY) {
                   atomicAdd(&bins[d].x, 1u);
                 }
@@ -1075,9 +1078,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
                 }
                 if (level == levels) continue;
                 if (by_w) {
-                  const uint32_t q = weight_bits(l);
-                  atomicAdd(&bins[d].x, q & ((1u << low) - 1u));
-                  atomicAdd(&bins[d].y, q >> low);
+                  add_weight(bins[d], weight_of(l));
                 } else {
                   atomicAdd(&bins[d].x, 1u);
                 }
@@ -1114,7 +1115,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
             if (least == greatest) {
               // ---------------- all are equal: the first ones by index
               ++turn;
-              const uint32_t q = by_w ? weight_bits(logit_of(least)) : 1u;
+              const unsigned long long q = by_w ? weight_of(logit_of(least)) : 1ull;
               const unsigned long long t = q > 0 ? (most - before + q - 1) / q : n_in;  // (before < most)
               const unsigned long long key = static_cast<unsigned long long>(least) << 32;
               if (t >= n_in) return key;
@@ -1151,7 +1152,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
               row_sync();
               const unsigned long long key = tid < n_in ? sh.key[tid] : 0ull;
               unsigned long long ahead = before;
-              sh.mine[tid] = by_w ? weight_bits(logit_of(static_cast<uint32_t>(key >> 32))) : 1u;
+              sh.mine[tid] = by_w ? weight_of(logit_of(static_cast<uint32_t>(key >> 32))) : 1ull;
               __syncthreads();
               if ((tid & ~31) < n_in) {
                 for (uint32_t j = 0; j < n_in; ++j)
@@ -1180,8 +1181,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
           for (uint32_t i = 0; i < kCluster; ++i) w[i] = get128(&bins[2 * tid], i);
 #pragma unroll
           for (uint32_t i = 0; i < kCluster; ++i) {
-            x0 += w[i].x + (static_cast<unsigned long long>(w[i].y) << low);
-            x1 += w[i].z + (static_cast<unsigned long long>(w[i].w) << low);
+            x0 += w[i].x + (static_cast<unsigned long long>(w[i].y) << 32);
+            x1 += w[i].z + (static_cast<unsigned long long>(w[i].w) << 32);
           }
           ++turn;
           unsigned long long upto = x0 + x1;
@@ -1222,12 +1223,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
         float f[kVec];
         unpack16<T>(get(v), f);
         const int t0 = s.token(v);
+        float b = 0.f, w = 0.f;  // (a vector's in fp32: conversions to 64 bits are slow)
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-          const uint32_t q = weight_bits(f[e]);
-          before += comes_before(f[e], t0 + e, won) ? q : 0u;
-          if (attempt == 0) all += from(f[e], t0 + e, cut) ? q : 0u;
+          const float q = ex2((f[e] - M) * c);
+          b += comes_before(f[e], t0 + e, won) ? q : 0.f;
+          if (attempt == 0) w += from(f[e], t0 + e, cut) ? q : 0.f;
         }
+        before += as_weight(b);
+        if (attempt == 0) all += as_weight(w);
       }
       wide_sums(before, all);
       // (the first token is kept whatever top_p is: nothing is before it)

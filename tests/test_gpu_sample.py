@@ -123,6 +123,32 @@ def test_ties_at_the_cut_go_to_the_lowest_index():
     assert run(c)[0].tolist() == [1994]
 
 
+def test_the_largest_vocabulary_of_equal_logits():
+    """2^20 of them: every slice's sum of weights is 2^17 times the largest one's."""
+    V, k = 1 << 20, 5000
+    for dtype in ("f32", "bf16"):
+        c = case((1, 1), V, dtype, "equal", settings=[(1.0, k, 1.0, 0.0), (1.0, 0, (k - 0.5) / V, 0.0)])
+        c["g"][:] = np.arange(V, dtype=np.float32)
+        got, st = run(c)
+        assert st == 0 and got.tolist() == [k - 1, k - 1]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_tokens_of_little_weight(dtype):
+    """One token and 201,087 of 7.6e-10 of its weight: 1.5e-4 together.  0.9999 of all are the first and 69,240 of
+    those."""
+    V = 201088
+    c = case((1, 1, 1), V, dtype, settings=[(1.0, 0, 0.9999, 0.0)] * 3)
+    x = np.full((3, V), -21.0)
+    x[:, 0] = 0.0
+    c["logits"] = _bits(x, dtype)
+    c["g"][:] = 0.0
+    for row, t in enumerate((30000, 120000, V - 1)):
+        c["g"][row, t] = 60.0
+    got, _ = check(c, least_clear=1.0)
+    assert got.tolist() == [30000, 0, 0]
+
+
 def test_no_settings_is_a_draw_from_the_softmax():
     c = dict(case((3, 4), 700, "f32", seed=6), temp=None, k=None, p=None, m=None)
     check(c)
