@@ -698,7 +698,7 @@ size_t pe_pages_workspace_bytes(int max_entries, int num_blocks);
  * or above max_blocks * block_size.  Rows are served in order; the first whose pages are not
  * there, and all later ones that need some, are refused.  PE_ERR_ARG: negative n, rows or
  * num_blocks, max_blocks or block_size < 1, null or misaligned pointers, ws.
- * PE_ERR_UNSUPPORTED: n > 65535. */
+ * PE_ERR_UNSUPPORTED: n > 65535, max_blocks >= 2^22. */
 int pe_pages_reserve(int n, const int32_t* row, const int32_t* length, int32_t* block_table,
                      int rows, int max_blocks, int num_blocks, int block_size, int32_t* refs,
                      void* ws, size_t ws_bytes, void* stream);
@@ -710,16 +710,17 @@ int pe_pages_reserve(int n, const int32_t* row, const int32_t* length, int32_t* 
  * range, a child that is not empty, is named twice or is some entry's parent, a length as for
  * pe_pages_reserve, a parent without valid, counted pages for it; for want of a free page as
  * there.  PE_ERR_ARG as there, and a plan that pe_attn_plan_init did not fill, n_layers < 1,
- * caches null or not 16-byte aligned.  PE_ERR_UNSUPPORTED: n > 65535. */
+ * caches null or not 16-byte aligned.  PE_ERR_UNSUPPORTED as there. */
 int pe_pages_fork(const pe_attn_plan* plan, int n_layers, int n, const int32_t* parent,
                   const int32_t* child, const int32_t* length, int32_t* block_table, int rows,
                   int max_blocks, int num_blocks, int32_t* refs, void* k_cache, void* v_cache,
                   void* ws, size_t ws_bytes, void* stream);
 
 /* n rows give their pages back: every entry of the row becomes -1 and its page's count falls by
- * one (a row named twice gives them back once).  A row out of range is refused; an entry
- * outside [0, num_blocks) is dropped (PE_ST_BLOCK_RANGE), and a page whose count is 0 keeps it
- * (PE_ST_PAGES).  ws: 256 bytes or more serve.  PE_ERR_ARG as for pe_pages_reserve. */
+ * one (a row named twice gives them back once).  A row out of range is refused; an entry from
+ * num_blocks on is dropped (PE_ST_BLOCK_RANGE), and a page whose count is 0 keeps it
+ * (PE_ST_PAGES).  ws: 256 bytes or more serve.  PE_ERR_ARG as for pe_pages_reserve, n has no
+ * limit, PE_ERR_UNSUPPORTED: max_blocks >= 2^22. */
 int pe_pages_free(int n, const int32_t* row, int32_t* block_table, int rows, int max_blocks,
                   int num_blocks, int32_t* refs, void* ws, size_t ws_bytes, void* stream);
 

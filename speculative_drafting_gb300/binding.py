@@ -843,6 +843,7 @@ class PagedAttention:
                 == v_cache.get_device() == block_table.get_device() == out.get_device()
                 == (ws if sink is None else sink).get_device()):
             self._apart(ws, qsl, seq_len, q, k_cache, v_cache, block_table, out, sink)
+
     def _layers(self, n_layers, num_blocks, k_cache, v_cache, ws):
         """Caches of n_layers layers, back to back."""
         d, n = self.dtype, n_layers * num_blocks * self.block

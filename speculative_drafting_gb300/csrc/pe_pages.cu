@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kScanThreads = 512;  // of the kernel that checks and lists
+constexpr int kMaxRow = 1 << 22;   // entries of a row of the table: kScanThreads rows' have an int's sum
 constexpr int kBatch = 8;          // 16-byte loads in flight per thread
 
 struct CacheArgs {
@@ -466,8 +467,8 @@ __global__ void __launch_bounds__(kThreads) free_kernel(const PoolArgs a) {
     int32_t* at = a.table + static_cast<int64_t>(row) * a.max_blocks + b;
     if (__ldcg(at) == -1) continue;
     const int page = atomicExch(at, -1);
-    if (page == -1) continue;
-    if (page < 0 || page >= a.num_blocks) {
+    if (page < 0) continue;  // (there was none)
+    if (page >= a.num_blocks) {
       set_status(a.status, PE_ST_BLOCK_RANGE);
     } else if (atomicSub(a.refs + page, 1) <= 0) {
       atomicAdd(a.refs + page, 1);  // (it was free: its count stays)
@@ -609,7 +610,7 @@ extern "C" int pe_pages_reserve(int n, const int32_t* row, const int32_t* length
   if (n < 0 || rows < 0 || max_blocks < 1 || num_blocks < 0 || block_size < 1 ||
       !ws_ok(ws, ws_bytes, pe_pages_workspace_bytes(n, num_blocks)))
     return PE_ERR_ARG;
-  if (n > 65535) return PE_ERR_UNSUPPORTED;
+  if (n > 65535 || max_blocks >= kMaxRow) return PE_ERR_UNSUPPORTED;
   if (n == 0) return PE_OK;
   PoolArgs a = {};
   if (pool_args(a, n, row, rows, length, block_table, max_blocks, num_blocks, block_size, refs, ws) != PE_OK)
@@ -628,7 +629,7 @@ extern "C" int pe_pages_fork(const pe_attn_plan* plan, int n_layers, int n, cons
   if (!plan_ok(plan) || n_layers < 1 || n < 0 || rows < 0 || max_blocks < 1 || num_blocks < 0 ||
       !ws_ok(ws, ws_bytes, pe_pages_workspace_bytes(n, num_blocks)))
     return PE_ERR_ARG;
-  if (n > 65535) return PE_ERR_UNSUPPORTED;
+  if (n > 65535 || max_blocks >= kMaxRow) return PE_ERR_UNSUPPORTED;
   if (n == 0) return PE_OK;
   PoolArgs a = {};
   CacheArgs c = {};
@@ -650,6 +651,7 @@ extern "C" int pe_pages_free(int n, const int32_t* row, int32_t* block_table, in
                              int num_blocks, int32_t* refs, void* ws, size_t ws_bytes, void* stream) {
   NvtxRange nvtx("pe_pages_free");
   if (n < 0 || rows < 0 || max_blocks < 1 || num_blocks < 0 || !ws_ok(ws, ws_bytes, 256)) return PE_ERR_ARG;
+  if (max_blocks >= kMaxRow) return PE_ERR_UNSUPPORTED;
   if (n == 0) return PE_OK;
   PoolArgs a = {};
   if (!row || !block_table || !refs || !aligned(row, 4) || !aligned(block_table, 4) || !aligned(refs, 4))

@@ -233,6 +233,10 @@ def test_pool_refuses():
     st = binding.read_status_ws(d.ws)[0]
     assert st == binding.PE_ST_PAGES | binding.PE_ST_BLOCK_RANGE
     assert (host(d.table)[0] == -1).all() and (host(d.refs) == 0).all()
+    # every negative entry is none
+    d.table[0, :3] = i32([-5, -(1 << 31), -2])
+    binding.pages_free(1, i32([0]), d.table, d.refs, d.ws)
+    assert binding.read_status_ws(d.ws)[0] == 0 and (host(d.table)[0] == -1).all() and (host(d.refs) == 0).all()
 
 
 def test_pool_large():

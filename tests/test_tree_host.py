@@ -158,6 +158,9 @@ def test_pages(lib, plan):
     assert lib.pe_pages_free(*free(n=0)) == OK
     check(lib.pe_pages_free, free, [dict(n=-1), dict(rows=-1), dict(mb=0), dict(nb=-1), dict(wsb=255), dict(ws=WS + 64),
                                     *pointers("row", "table", "refs")])
+    for mb, code in (((1 << 22) - 1, OK), (1 << 22, UNSUP)):
+        assert lib.pe_pages_free(*free(n=0, mb=mb)) == code and lib.pe_pages_reserve(*reserve(n=0, mb=mb)) == code
+        assert lib.pe_pages_fork(*fork(plan, n=0, mb=mb)) == code
 
 
 def test_status_bits_match_the_header():
