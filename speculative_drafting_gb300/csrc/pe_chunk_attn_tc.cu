@@ -26,6 +26,13 @@
 // not finite though their l is a number, in units with a value that is not finite past
 // some row's last key, are computed again by the second kernel from the keys that they see.
 //
+// Trees.  Every unit goes over all of its request's keys.  Tiles of the context alone are as
+// without a tree; in the others a thread takes its row's bits of the tile's keys out of the mask
+// while the product runs.  64 requests of 1 to 64 nodes over 512 to 8192 keys, 8 query heads a KV
+// head of 64: 242 us, of which the bytes would take 86 and the operations 73.  Issue slots are used
+// 51 % of the time and the tensor pipe 35 %: the steps of a tile wait for one another, as in a
+// prompt.  Requests of more than 32 nodes read their keys once for each unit (826 MB for 581).
+//
 // Warps: 0-7 softmax of stream 0 (two warps to 32 rows, half the keys of a tile each),
 // 8-15 of stream 1, 16 K tiles and the unit list, 17 and 18 the products of either stream,
 // 19 V tiles.

@@ -9,7 +9,9 @@
 // Free pages are those whose count is 0.  They are handed out in ascending order, to the
 // calls' entries in order, so a call's outcome does not depend on how its CTAs run: one CTA
 // per entry checks it and counts what it needs, the last of them to finish adds up and lists
-// as many free pages, a second kernel fills in the rows and copies.
+// as many free pages, a second kernel fills in the rows and copies.  (64 forks of 8 prompts and the
+// free before them, 14 MB in 16 layers: 15 us for the two calls, 14 of it host time; launched cold 6
+// for the free, 9.3 for the check and the list, 9.4 for rows and copies.)
 #include <algorithm>
 #include <atomic>
 
@@ -152,7 +154,9 @@ struct CompactArgs {
 // Row d of a request's path goes from node path[d] to node d.  The path ascends, so
 // d <= path[d], and a thread that moves its 16 bytes of each row in order (kBatch loads, then
 // their stores) reads every node before it is written over: node e is written by row e, at or
-// after the row that comes from it.
+// after the row that comes from it.  (64 requests, 14 MB read and written in 16 layers: 7 us a
+// call, which is its host time; launched cold the kernel takes 9, of which the bytes are 2: a chain
+// of offsets, path and block table comes before the first of them.)
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) {
   constexpr int kRows = 256;  // of the path at a time
   __shared__ int64_t from_sh[kRows], to_sh[kRows];

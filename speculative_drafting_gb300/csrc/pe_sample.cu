@@ -24,9 +24,13 @@
 //                ones inside the bin of the cut, then the race.  Weights are 40-bit integers there:
 //                their sums do not depend on an order.
 //
-// The first kernel is bound by the logits' bytes.  (Every row by a cluster with the row in
-// shared memory: 512 bf16 rows of 201,088 with top-k 162 us; the barriers of a row are waited
-// for with its 400 KB held.)
+// The first kernel is bound by the logits' bytes, the others by the latency of a row's steps.
+// Launched cold, 512 bf16 rows of 201,088 of mixed settings (245 MB with the noise): 48 us at 5.1
+// TB/s, 26, and 39 for some 70 flat rows.  8 fp32 rows: 7, 12 and 4, 13.4 us a call.
+// Every row by a cluster with the row in shared memory took 162 us for 512 bf16 rows with top-k:
+// the barriers of a row are waited for with its 400 KB held.  The cut in the first kernel, by a
+// cluster of a row's CTAs, took 78 where the two take 72, the cut by the first CTA of the wide
+// kernel's cluster for few rows 14.6 where three kernels take 13.4.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -90,6 +94,7 @@ struct SampleArgs {
   uint32_t* todo_n;  // rows for the wide kernel
   int32_t* todo;     // [T]
   int resident;      // the wide kernel's slices fit in shared memory
+  int near;          // ... beside their noise
 };
 
 struct Settings {
@@ -343,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
       }
     }
     out.m = cta_max<kWarps>(m, warp_m);
-    // The threads whose best is within reach of the CTA's compare in 64 bits.
+    // The threads whose best is within reach of the CTA's: if there is more than one token, they
+    // compare in 64 bits (which is slow: the one that there mostly is does without).
     const float far = m == out.m ? 0.f : (m - out.m) * it;
     if (bs < INFINITY) bs += far;
     float top = warp_max(bs);
@@ -355,14 +361,20 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
     unsigned long long k = 0ull;
     int bi = 0x7fffffff;
     float bx = 0.f, bg = 0.f;
-    if (bv >= 0 && fabsf(out.m) < INFINITY && within_reach(bs, top, far)) {
+    const bool in = bv >= 0 && fabsf(out.m) < INFINITY && within_reach(bs, top, far);
+    const int n_in = __syncthreads_count(in);
+    if (in) {
       float f[kVec], g[kVec];
       unpack16<T>(s.load(v0 + bv), f);
       const int t0 = s.token(v0 + bv);
       noise.load(t0, a.V, g);
+      int left = 0;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) left += within_reach(fmaf(f[e] - m, it, g[e]) + far, top, far);
+      const bool alone = n_in == 1 && left == 1;
       for (int e = 0; e < kVec; ++e) {
         if (!within_reach(fmaf(f[e] - m, it, g[e]) + far, top, far)) continue;
-        const unsigned long long o = exact_score(f[e], g[e], out.m, st.temp);
+        const unsigned long long o = alone ? 1ull : exact_score(f[e], g[e], out.m, st.temp);
         if (o > k) {
           k = o;
           bi = t0 + e;
@@ -373,10 +385,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
     }
     unsigned long long best = k;
     int winner = bi;
-    cta_best<kWarps>(best, winner, warp_k, warp_i);
+    if (n_in > 1) cta_best<kWarps>(best, winner, warp_k, warp_i);
     out.idx = best ? winner : -1;
     // (its thread writes the part)
-    if (best ? bi == winner : tid == 0) {
+    if (n_in == 1 ? in : best ? bi == winner : tid == 0) {
       out.x = bx;
       out.g = bg;
       a.stat[static_cast<size_t>(row) * a.parts + part] = out;
@@ -530,9 +542,19 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
     answer(0ull, -1);
     return;
   }
+  // the best score among the threads': where one alone is within reach, that one
+  auto finish = [&](bool there, float l, float g, int t) {
+    const float score = there ? fmaf(l - M, 1.f / st.temp, g) : -INFINITY;
+    const float best = cta_max<kCutWarps>(score == score ? score : -INFINITY, sh.m);
+    const bool in = there && within_reach(score, best);
+    if (__syncthreads_count(in) != 1)
+      answer(in ? exact_score(l, g, M, st.temp) : 0ull, in ? t : 0x7fffffff);
+    else if (in)
+      a.token[row] = t;
+  };
   if (!cut) {
     const int t = tid < a.parts ? __ldcg(&stat[tid].idx) : -1;
-    answer(t < 0 ? 0ull : exact_score(__ldcg(&stat[tid].x), __ldcg(&stat[tid].g), M, st.temp), t < 0 ? 0x7fffffff : t);
+    finish(t >= 0, t < 0 ? 0.f : __ldcg(&stat[tid].x), t < 0 ? 0.f : __ldcg(&stat[tid].g), t);
     return;
   }
   const float c = scale_of(st.temp);
@@ -700,11 +722,7 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
       keep = there && (tid == 0 || upto - q < most);
     }
     if (done) {
-      keep = keep && (tid == 0 || w >= st.mp);
-      // in fp32, then those within reach of the best in 64 bits
-      const float score = keep ? fmaf(l - M, 1.f / st.temp, g) : -INFINITY;
-      const float best = cta_max<kCutWarps>(score == score ? score : -INFINITY, sh.m);
-      answer(keep && within_reach(score, best) ? exact_score(l, g, M, st.temp) : 0ull, t);
+      finish(keep && (tid == 0 || w >= st.mp), l, g, t);
       return;
     }
   }
@@ -804,8 +822,32 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
     const int row = __ldcg(a.todo + item);
     const Settings st = a.set[row];
     const Row<T> s(a, row);
+    const Noise<T> noise(a, row, s.shift);
+    const bool cut_k = st.k > 0, cut_p = st.p < 1.f;
     const int nv = s.vectors(), per = (nv + kCluster - 1) / kCluster;
     const int v0 = min(static_cast<int>(rank) * per, nv), v1 = min(v0 + per, nv);
+    // All tokens race if there is no k: their noise is on its way beside the logits.  (Vectors of
+    // it lie in kVec / 4 planes; each thread reads what it copied, here and of the logits.)
+    const bool near = a.near && noise.wide && !cut_k;
+    uint4* held_g = held + per;
+    auto inside = [&](int t0) { return t0 >= 0 && t0 + kVec <= a.V; };
+    if (near) {
+      for (int v = v0 + tid; v < v1; v += kWideThreads)
+        if (inside(s.token(v)))
+#pragma unroll
+          for (int e = 0; e < kVec / 4; ++e)
+            cp_async16(smem_u32(held_g + e * per + v - v0), noise.g + s.token(v) + 4 * e, true);
+      cp_async_commit();
+    }
+    auto get_noise = [&](int v, float* x) {
+      const int t0 = s.token(v);
+      if (near && inside(t0)) {
+#pragma unroll
+        for (int e = 0; e < kVec / 4; ++e) unpack16<float>(held_g[e * per + v - v0], x + 4 * e);
+      } else {
+        noise.load(t0, a.V, x);
+      }
+    };
     auto get = [&](int v) { return a.resident ? held[v - v0] : s.load(v); };
     __syncthreads();
     // ---------------- the slice, its largest and least logit
@@ -860,7 +902,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
       if (hi) atomicAdd(&bin.y, hi);
     };
 
-    const Noise<T> noise(a, row, s.shift);
     // whether a token comes no later than a key (argmax_key), or before it
     auto from = [&](float l, int t, unsigned long long key) {
       const float x = key ? logit_of(static_cast<uint32_t>(key >> 32)) : -INFINITY;
@@ -889,7 +930,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
             if (!kept(f[x][e], t0 + e)) f[x][e] = -INFINITY;
             any |= f[x][e] > -INFINITY;
           }
-          if (any) noise.load(t0, a.V, g[x]);
+          if (any) get_noise(vx, g[x]);
         }
 #pragma unroll
         for (int x = 0; x < kWideRace; ++x) {
@@ -903,29 +944,65 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
           }
         }
       }
-      // (as in the row kernel)
       const float wt = warp_max(bs);
       __syncthreads();
       if (lane == 0) sh.wm[warp] = wt;
       __syncthreads();
       float top = sh.wm[0];
       for (int w = 1; w < kWideWarps; ++w) top = fmaxf(top, sh.wm[w]);
+      // The tokens within reach of the best score (of this thread's best vector): how many, the
+      // key of the best one in 64 bits, or of the only one.
       unsigned long long best = 0ull, key = 0ull;
       int bi = 0x7fffffff;
-      if (bv >= 0 && within_reach(bs, top)) {
+      auto reach = [&](bool exact) {
         const uint4 u = get(bv);
+        int n = 0;
         for (int e = 0; e < kVec; ++e) {
           const float l = __uint_as_float(element<T>(u, e));
           const int t = s.token(bv) + e;
           if (!(l > -INFINITY) || !kept(l, t) || !within_reach(fmaf(l - M, it, noise.g[t]), top)) continue;
-          const unsigned long long o = exact_score(l, noise.g[t], M, st.temp);
+          ++n;
+          const unsigned long long o = exact ? exact_score(l, noise.g[t], M, st.temp) : 1ull;
           if (o > best) {
             best = o;
             bi = t;
             key = argmax_key(l, static_cast<uint32_t>(t));
           }
         }
+        return n;
+      };
+      // As a rule one token of the row is within reach: its key and fp32 score do.  (Key 0: there
+      // are more in this CTA.)
+      bool in = bv >= 0 && within_reach(bs, top);
+      const int n_in = __syncthreads_count(in);
+      const int left = in ? reach(false) : 0;
+      if (n_in == 1 ? in : tid == 0)
+        for (int to = 0; to < kCluster; ++to) {
+          put64(&sh.best[turn & 1][rank], to, __float_as_uint(top));
+          put64(&sh.best_key[turn & 1][rank], to, n_in == 1 && left == 1 ? key : 0ull);
+        }
+      row_sync();
+      float tops[kCluster];
+#pragma unroll
+      for (int i = 0; i < kCluster; ++i) {
+        tops[i] = __uint_as_float(static_cast<uint32_t>(sh.best[turn & 1][i]));
+        top = fmaxf(top, tops[i]);
       }
+      int ctas = 0;
+      unsigned long long only = 0ull;
+#pragma unroll
+      for (int i = 0; i < kCluster; ++i)
+        if (within_reach(tops[i], top)) {
+          ++ctas;
+          only = sh.best_key[turn & 1][i];
+        }
+      ++turn;
+      if (ctas == 0 || (ctas == 1 && only)) return only;
+      // ---------------- the others, in 64 bits (as in the row kernel)
+      in = bv >= 0 && within_reach(bs, top);
+      best = key = 0ull;
+      bi = 0x7fffffff;
+      if (in) reach(true);
       unsigned long long k = best;
       int i = bi;
       cta_best<kWideWarps>(k, i, sh.k, sh.i);
@@ -1212,7 +1289,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
     // is none); for top-p, is that token kept?  If it is not, none behind it is: the tokens before
     // it race again.  Few are rejected, by the noise of a Gumbel draw; after kTries the cut is
     // looked for.
-    const bool cut_k = st.k > 0, cut_p = st.p < 1.f;
+    cp_async_wait<0>();
     unsigned long long cut = cut_k ? find(st.k, false) : 0ull, won = 0ull, most = 0ull;
     for (int attempt = 0;; ++attempt) {
       won = race(cut);
@@ -1250,7 +1327,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
 
 size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
-constexpr int kSlice = 176 * 1024;   // of a row, in a CTA of the wide kernel
+constexpr int kSlice = 200 * 1024;   // of a row and of its noise, in a CTA of the wide kernel
 constexpr int kMaxParts = kGroups / (kThreads >> 5);  // (and trips, in all of a row's parts)
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kWave = 4;  // CTAs of the row kernel per SM
@@ -1275,6 +1352,9 @@ void plan(SampleArgs& a, int esize, int num_sms) {
   while (a.gshift < 5 && a.parts * a.trips * (kThreads >> a.gshift) > kGroups) ++a.gshift;
 }
 
+// the most vectors of a slice, whatever the row's place on the grid
+int64_t slice_vectors(int V, int esize) { return ((V + 7ll) * esize / 16 + kCluster) / kCluster + 1; }
+
 // the most parts and groups of a row for any number of rows
 size_t max_parts(int V) {
   return std::min<size_t>((static_cast<size_t>(V) + 6) / (4 * kThreads) + 1, kMaxParts);
@@ -1297,11 +1377,11 @@ cudaError_t launch(const SampleArgs& a, int num_sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_chained(sample_cut_kernel<T>, dim3(a.T), dim3(kCutThreads), 0, st, a);
   if (e != cudaSuccess || !(a.top_k || a.top_p || a.min_p)) return e;
-  const int64_t slice = ((a.V + 7ll) * sizeof(T) / 16 + kCluster) / kCluster * 16 + 16;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCluster * std::min(a.T, std::max(num_sms / kCluster, 1)));
   cfg.blockDim = dim3(kWideThreads);
-  cfg.dynamicSmemBytes = a.resident ? static_cast<size_t>(slice) : 0;
+  cfg.dynamicSmemBytes = static_cast<size_t>(a.near ? slice_vectors(a.V, sizeof(T)) * (16 + 64 / sizeof(T))
+                                             : a.resident ? slice_vectors(a.V, sizeof(T)) * 16 : 0);
   cfg.stream = st;
   cudaLaunchAttribute attr[3];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1368,7 +1448,8 @@ extern "C" int pe_sample(int B, int T, const int32_t* qsl, const void* logits, i
   a.token = token;
   plan(a, esize, sms);
   if (static_cast<int64_t>(T) * a.parts > 0x7fffffff) return PE_ERR_UNSUPPORTED;
-  a.resident = (static_cast<int64_t>(vocab) + 7) * esize / 16 + kCluster <= static_cast<int64_t>(kSlice) / 16 * kCluster - kCluster;
+  a.resident = slice_vectors(vocab, esize) * 16 <= kSlice;
+  a.near = slice_vectors(vocab, esize) * (16 + 64 / esize) <= kSlice;
   char* w = static_cast<char*>(ws);
   a.status = reinterpret_cast<uint32_t*>(w);
   a.todo_n = reinterpret_cast<uint32_t*>(w + 128);
