@@ -902,42 +902,53 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
       if (hi) atomicAdd(&bin.y, hi);
     };
 
-    // whether a token comes no later than a key (argmax_key), or before it
-    auto from = [&](float l, int t, unsigned long long key) {
-      const float x = key ? logit_of(static_cast<uint32_t>(key >> 32)) : -INFINITY;
-      return l > x || (l == x && static_cast<uint32_t>(t) <= ~static_cast<uint32_t>(key));
+    // A place in the order (an argmax_key, 0: the end), and whether a token comes no later.
+    // (Without branches: a few instructions a token are what the passes over a slice take.)
+    struct To {
+      float x;
+      int t;
     };
-    auto comes_before = [&](float l, int t, unsigned long long key) {
-      const float x = logit_of(static_cast<uint32_t>(key >> 32));
-      return l > x || (l == x && static_cast<uint32_t>(t) < ~static_cast<uint32_t>(key));
+    auto place_of = [](unsigned long long key) {
+      return To{key ? logit_of(static_cast<uint32_t>(key >> 32)) : -INFINITY,
+                static_cast<int>(~static_cast<uint32_t>(key) & 0x7fffffffu)};
     };
+    auto no_later = [](float l, int t, const To& to) { return (l > to.x) | ((l == to.x) & (t <= to.t)); };
     // The key of the best score among the tokens from a cut on, 0 if there is none.
     auto race = [&](unsigned long long cut) {
-      auto kept = [&](float l, int t) {
-        return from(l, t, cut) && !(st.mp > 0.f && l != M && ex2((l - M) * c) < st.mp);
+      const To to = place_of(cut);
+      // a vector's kept logits, -inf for the others; whether there are some
+      auto kept = [&](int v, float* f) {
+        const int t0 = s.token(v);
+        unpack16<T>(v < v1 ? get(v) : no_tokens<T>(), f);
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          f[e] = no_later(f[e], t0 + e, to) ? f[e] : -INFINITY;
+          any |= f[e] > -INFINITY;
+        }
+        if (st.mp > 0.f) {
+#pragma unroll
+          for (int e = 0; e < kVec; ++e)
+            if (f[e] != M && ex2((f[e] - M) * c) < st.mp) f[e] = -INFINITY;
+        }
+        return any;
       };
       float bs = -INFINITY;
       int bv = -1;  // the vector with this thread's
       for (int v = v0 + tid; v < v1; v += kWideRace * kWideThreads) {
         float f[kWideRace][kVec], g[kWideRace][kVec];
+        bool any[kWideRace];
 #pragma unroll
         for (int x = 0; x < kWideRace; ++x) {
-          const int vx = v + x * kWideThreads, t0 = s.token(vx);
-          unpack16<T>(vx < v1 ? get(vx) : no_tokens<T>(), f[x]);
-          bool any = false;
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            if (!kept(f[x][e], t0 + e)) f[x][e] = -INFINITY;
-            any |= f[x][e] > -INFINITY;
-          }
-          if (any) get_noise(vx, g[x]);
+          any[x] = kept(v + x * kWideThreads, f[x]);
+          if (any[x]) get_noise(v + x * kWideThreads, g[x]);
         }
 #pragma unroll
         for (int x = 0; x < kWideRace; ++x) {
+          if (!any[x]) continue;
           float top = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < kVec; ++e)
-            top = fmaxf(top, f[x][e] > -INFINITY ? fmaf(f[x][e] - M, it, g[x][e]) : -INFINITY);
+          for (int e = 0; e < kVec; ++e) top = fmaxf(top, fmaf(f[x][e] - M, it, g[x][e]));
           if (top > bs) {
             bs = top;
             bv = v + x * kWideThreads;
@@ -955,18 +966,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
       unsigned long long best = 0ull, key = 0ull;
       int bi = 0x7fffffff;
       auto reach = [&](bool exact) {
-        const uint4 u = get(bv);
+        float f[kVec], g[kVec];
+        kept(bv, f);
+        get_noise(bv, g);
         int n = 0;
+#pragma unroll
         for (int e = 0; e < kVec; ++e) {
-          const float l = __uint_as_float(element<T>(u, e));
-          const int t = s.token(bv) + e;
-          if (!(l > -INFINITY) || !kept(l, t) || !within_reach(fmaf(l - M, it, noise.g[t]), top)) continue;
+          if (!(f[e] > -INFINITY) || !within_reach(fmaf(f[e] - M, it, g[e]), top)) continue;
           ++n;
-          const unsigned long long o = exact ? exact_score(l, noise.g[t], M, st.temp) : 1ull;
+          const unsigned long long o = exact ? exact_score(f[e], g[e], M, st.temp) : 1ull;
           if (o > best) {
             best = o;
-            bi = t;
-            key = argmax_key(l, static_cast<uint32_t>(t));
+            bi = s.token(bv) + e;
+            key = argmax_key(f[e], static_cast<uint32_t>(bi));
           }
         }
         return n;
@@ -1296,6 +1308,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
       if (!cut_p || won == 0ull || attempt > kTries) break;
       // the weight before it, and (once) of all that top-p is a share of
       unsigned long long before = 0ull, all = 0ull;
+      const To last = place_of(cut);
+      To to = place_of(won);
+      --to.t;
       for (int v = v0 + tid; v < v1; v += kWideThreads) {
         float f[kVec];
         unpack16<T>(get(v), f);
@@ -1304,8 +1319,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
           const float q = ex2((f[e] - M) * c);
-          b += comes_before(f[e], t0 + e, won) ? q : 0.f;
-          if (attempt == 0) w += from(f[e], t0 + e, cut) ? q : 0.f;
+          b += no_later(f[e], t0 + e, to) ? q : 0.f;
+          if (attempt == 0) w += no_later(f[e], t0 + e, last) ? q : 0.f;
         }
         before += as_weight(b);
         if (attempt == 0) all += as_weight(w);
