@@ -34,6 +34,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "pe_paged.h"
 #include "pe_sampling.cuh"
@@ -766,14 +767,14 @@ PE_DEV void row_sync() {
 // since the last one read it.
 struct __align__(16) WideShared {
   uint2 bins[2][kBins];  // counts; or sums of weights, their lower and upper word
-  float m[kCluster], lo[kCluster];  // of every CTA: largest and least finite logit
+  float lo[kCluster];  // of every CTA: least finite logit
   uint4 in[2][kCluster];  // ... of the cut's bin: tokens, least and greatest order
   unsigned long long best[2][kCluster], best_key[2][kCluster];  // ... of its best score, and which token
   unsigned long long key[kList];  // the tokens of the cut's bin, of all CTAs
   int tie;
   // this CTA's own
   unsigned long long scan[kWideWarps], k[kWideWarps], mine[kList];
-  float wm[kWideWarps], wl[kWideWarps];
+  float wm[kWideWarps];
   uint32_t u[kWideWarps], v[kWideWarps];
   int i[kWideWarps];
   int digit;
@@ -826,71 +827,46 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
     const bool cut_k = st.k > 0, cut_p = st.p < 1.f;
     const int nv = s.vectors(), per = (nv + kCluster - 1) / kCluster;
     const int v0 = min(static_cast<int>(rank) * per, nv), v1 = min(v0 + per, nv);
-    // All tokens race if there is no k: their noise is on its way beside the logits.  (Vectors of
-    // it lie in kVec / 4 planes; each thread reads what it copied, here and of the logits.)
+    // The slice, and the noise of all of it if there is no k: then all tokens race.  (Vectors of
+    // the noise lie in kVec / 4 planes.  Each thread reads what it copied.)
     const bool near = a.near && noise.wide && !cut_k;
     uint4* held_g = held + per;
     auto inside = [&](int t0) { return t0 >= 0 && t0 + kVec <= a.V; };
-    if (near) {
-      for (int v = v0 + tid; v < v1; v += kWideThreads)
-        if (inside(s.token(v)))
+    // (no more parts than threads)
+    const float part_m = tid < a.parts ? __ldcg(&a.stat[static_cast<size_t>(row) * a.parts + tid].m) : -INFINITY;
+    if (a.resident) {
+      for (int v = v0 + tid; v < v1; v += kWideThreads) {
+        const int t0 = s.token(v);
+        if (!inside(t0)) {
+          held[v - v0] = s.load(v);
+          continue;
+        }
+        cp_async16(smem_u32(held + v - v0), s.row + t0, true);
+        if (near) {
 #pragma unroll
           for (int e = 0; e < kVec / 4; ++e)
-            cp_async16(smem_u32(held_g + e * per + v - v0), noise.g + s.token(v) + 4 * e, true);
+            cp_async16(smem_u32(held_g + e * per + v - v0), noise.g + t0 + 4 * e, true);
+        }
+      }
       cp_async_commit();
     }
-    auto get_noise = [&](int v, float* x) {
-      const int t0 = s.token(v);
-      if (near && inside(t0)) {
-#pragma unroll
-        for (int e = 0; e < kVec / 4; ++e) unpack16<float>(held_g[e * per + v - v0], x + 4 * e);
-      } else {
-        noise.load(t0, a.V, x);
-      }
-    };
     auto get = [&](int v) { return a.resident ? held[v - v0] : s.load(v); };
-    __syncthreads();
-    // ---------------- the slice, its largest and least logit
-    float m = -INFINITY, lo = INFINITY;
-    for (int v = v0 + tid; v < v1; v += kUnroll * kWideThreads) {
-      uint4 u[kUnroll];
+    const float M = cta_max<kWideWarps>(part_m, sh.wm);
+    cp_async_wait<0>();
+    // the row's least finite logit, for the bins of a k
+    float lo = -INFINITY;
+    if (cut_k) {
+      lo = INFINITY;
+      for (int v = v0 + tid; v < v1; v += kWideThreads) {
+        float f[kVec];
+        unpack16<T>(get(v), f);
 #pragma unroll
-      for (int x = 0; x < kUnroll; ++x)
-        if (v + x * kWideThreads < v1) u[x] = s.load(v + x * kWideThreads);
-#pragma unroll
-      for (int x = 0; x < kUnroll; ++x)
-        if (v + x * kWideThreads < v1) {
-          if (a.resident) held[v + x * kWideThreads - v0] = u[x];
-          float f[kVec];
-          unpack16<T>(u[x], f);
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            m = fmaxf(m, f[e]);
-            if (f[e] > -INFINITY) lo = fminf(lo, f[e]);
-          }
-        }
-    }
-    m = warp_max(m);
-    lo = -warp_max(-lo);
-    if (lane == 0) {
-      sh.wm[warp] = m;
-      sh.wl[warp] = lo;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      m = warp_max(lane < kWideWarps ? sh.wm[lane] : -INFINITY);
-      lo = -warp_max(lane < kWideWarps ? -sh.wl[lane] : -INFINITY);
-      if (lane < kCluster) {
-        put32(&sh.m[rank], lane, __float_as_uint(m));
-        put32(&sh.lo[rank], lane, __float_as_uint(lo));
+        for (int e = 0; e < kVec; ++e) lo = f[e] > -INFINITY ? fminf(lo, f[e]) : lo;
       }
-    }
-    row_sync();
-    float M = -INFINITY;
-    lo = INFINITY;
-    for (int i = 0; i < kCluster; ++i) {
-      M = fmaxf(M, sh.m[i]);
-      lo = fminf(lo, sh.lo[i]);
+      lo = -cta_max<kWideWarps>(-lo, sh.wm);
+      if (tid < kCluster) put32(&sh.lo[rank], tid, __float_as_uint(lo));
+      row_sync();
+      for (int i = 0; i < kCluster; ++i) lo = fminf(lo, sh.lo[i]);
     }
     const float c = scale_of(st.temp), it = 1.f / st.temp;
     // 2^20 weights of at most 2^40 have a sum; what is cut off of them is below 2^-20 of it
@@ -917,6 +893,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
     auto race = [&](unsigned long long cut) {
       const To to = place_of(cut);
       // a vector's kept logits, -inf for the others; whether there are some
+      auto light = [&](float l) { return l != M && ex2((l - M) * c) < st.mp; };
       auto kept = [&](int v, float* f) {
         const int t0 = s.token(v);
         unpack16<T>(v < v1 ? get(v) : no_tokens<T>(), f);
@@ -929,31 +906,46 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
         if (st.mp > 0.f) {
 #pragma unroll
           for (int e = 0; e < kVec; ++e)
-            if (f[e] != M && ex2((f[e] - M) * c) < st.mp) f[e] = -INFINITY;
+            if (light(f[e])) f[e] = -INFINITY;
         }
         return any;
       };
       float bs = -INFINITY;
       int bv = -1;  // the vector with this thread's
-      for (int v = v0 + tid; v < v1; v += kWideRace * kWideThreads) {
-        float f[kWideRace][kVec], g[kWideRace][kVec];
-        bool any[kWideRace];
+      auto pass = [&](auto vectors, auto&& load) {
+        constexpr int kV = decltype(vectors)::value;
+        for (int v = v0 + tid; v < v1; v += kV * kWideThreads) {
+          float f[kV][kVec], g[kV][kVec];
+          bool any[kV];
 #pragma unroll
-        for (int x = 0; x < kWideRace; ++x) {
-          any[x] = kept(v + x * kWideThreads, f[x]);
-          if (any[x]) get_noise(v + x * kWideThreads, g[x]);
-        }
+          for (int x = 0; x < kV; ++x) {
+            any[x] = kept(v + x * kWideThreads, f[x]);
+            if (any[x]) load(v + x * kWideThreads, g[x]);
+          }
 #pragma unroll
-        for (int x = 0; x < kWideRace; ++x) {
-          if (!any[x]) continue;
-          float top = -INFINITY;
+          for (int x = 0; x < kV; ++x) {
+            if (!any[x]) continue;
+            float top = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) top = fmaxf(top, fmaf(f[x][e] - M, it, g[x][e]));
-          if (top > bs) {
-            bs = top;
-            bv = v + x * kWideThreads;
+            for (int e = 0; e < kVec; ++e) top = fmaxf(top, fmaf(f[x][e] - M, it, g[x][e]));
+            if (top > bs) {
+              bs = top;
+              bv = v + x * kWideThreads;
+            }
           }
         }
+      };
+      if (near) {
+        pass(std::integral_constant<int, 1>(), [&](int v, float* g) {
+          if (inside(s.token(v))) {
+#pragma unroll
+            for (int e = 0; e < kVec / 4; ++e) unpack16<float>(held_g[e * per + v - v0], g + 4 * e);
+          } else {
+            noise.load(s.token(v), a.V, g);
+          }
+        });
+      } else {
+        pass(std::integral_constant<int, kWideRace>(), [&](int v, float* g) { noise.load(s.token(v), a.V, g); });
       }
       const float wt = warp_max(bs);
       __syncthreads();
@@ -961,82 +953,72 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
       __syncthreads();
       float top = sh.wm[0];
       for (int w = 1; w < kWideWarps; ++w) top = fmaxf(top, sh.wm[w]);
-      // The tokens within reach of the best score (of this thread's best vector): how many, the
-      // key of the best one in 64 bits, or of the only one.
-      unsigned long long best = 0ull, key = 0ull;
-      int bi = 0x7fffffff;
-      auto reach = [&](bool exact) {
-        float f[kVec], g[kVec];
-        kept(bv, f);
-        get_noise(bv, g);
-        int n = 0;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          if (!(f[e] > -INFINITY) || !within_reach(fmaf(f[e] - M, it, g[e]), top)) continue;
-          ++n;
-          const unsigned long long o = exact ? exact_score(f[e], g[e], M, st.temp) : 1ull;
-          if (o > best) {
-            best = o;
-            bi = s.token(bv) + e;
-            key = argmax_key(f[e], static_cast<uint32_t>(bi));
+      // The tokens within reach of the best score (of this thread's best vector).  As a rule it is
+      // one in the whole row: then its fp32 score and key do, else the scores are formed again, in
+      // 64 bits (as in the row kernel).
+      for (bool exact = false;; exact = true) {
+        const bool in = bv >= 0 && within_reach(bs, top);
+        const int n_in = __syncthreads_count(in);
+        unsigned long long best = 0ull, key = 0ull;
+        int left = 0, bi = 0x7fffffff;
+        if (in) {
+          const uint4 u = get(bv);
+          const int t0 = s.token(bv);
+#pragma unroll 1
+          for (int e = 0; e < kVec; ++e) {
+            const float l = __uint_as_float(element<T>(u, e));
+            if (!(l > -INFINITY) || !no_later(l, t0 + e, to) || (st.mp > 0.f && light(l))) continue;
+            const float g = near && inside(t0) ? reinterpret_cast<const float*>(held_g + (e >> 2) * per + bv - v0)[e & 3]
+                                               : noise.g[t0 + e];
+            if (!within_reach(fmaf(l - M, it, g), top)) continue;
+            ++left;
+            const unsigned long long o = exact ? exact_score(l, g, M, st.temp) : 1ull;
+            if (o > best) {
+              best = o;
+              bi = t0 + e;
+              key = argmax_key(l, static_cast<uint32_t>(bi));
+            }
           }
         }
-        return n;
-      };
-      // As a rule one token of the row is within reach: its key and fp32 score do.  (Key 0: there
-      // are more in this CTA.)
-      bool in = bv >= 0 && within_reach(bs, top);
-      const int n_in = __syncthreads_count(in);
-      const int left = in ? reach(false) : 0;
-      if (n_in == 1 ? in : tid == 0)
-        for (int to = 0; to < kCluster; ++to) {
-          put64(&sh.best[turn & 1][rank], to, __float_as_uint(top));
-          put64(&sh.best_key[turn & 1][rank], to, n_in == 1 && left == 1 ? key : 0ull);
+        // its thread, or the first where there is none (key 0: of several), tells the others
+        unsigned long long k = best;
+        int i = bi;
+        if (exact) cta_best<kWideWarps>(k, i, sh.k, sh.i);
+        if (exact ? (k ? bi == i && best == k : tid == 0) : (n_in == 1 ? in : tid == 0)) {
+          if (!exact) {
+            k = __float_as_uint(top);
+            if (n_in != 1 || left != 1) key = 0ull;
+          }
+          for (int to_cta = 0; to_cta < kCluster; ++to_cta) {
+            put64(&sh.best[turn & 1][rank], to_cta, k);
+            put64(&sh.best_key[turn & 1][rank], to_cta, key);
+          }
         }
-      row_sync();
-      float tops[kCluster];
-#pragma unroll
-      for (int i = 0; i < kCluster; ++i) {
-        tops[i] = __uint_as_float(static_cast<uint32_t>(sh.best[turn & 1][i]));
-        top = fmaxf(top, tops[i]);
-      }
-      int ctas = 0;
-      unsigned long long only = 0ull;
-#pragma unroll
-      for (int i = 0; i < kCluster; ++i)
-        if (within_reach(tops[i], top)) {
-          ++ctas;
-          only = sh.best_key[turn & 1][i];
-        }
-      ++turn;
-      if (ctas == 0 || (ctas == 1 && only)) return only;
-      // ---------------- the others, in 64 bits (as in the row kernel)
-      in = bv >= 0 && within_reach(bs, top);
-      best = key = 0ull;
-      bi = 0x7fffffff;
-      if (in) reach(true);
-      unsigned long long k = best;
-      int i = bi;
-      cta_best<kWideWarps>(k, i, sh.k, sh.i);
-      // (its thread, or the first where none has one, tells the others)
-      if (k ? bi == i && best == k : tid == 0)
-        for (int to = 0; to < kCluster; ++to) {
-          put64(&sh.best[turn & 1][rank], to, k);
-          put64(&sh.best_key[turn & 1][rank], to, key);
-        }
-      row_sync();
-      k = 0ull;
-      key = 0ull;
-      for (int from_cta = 0; from_cta < kCluster; ++from_cta) {
-        const unsigned long long o = sh.best[turn & 1][from_cta], x = sh.best_key[turn & 1][from_cta];
-        // (equal scores: the lowest index)
-        if (o > k || (o == k && o && static_cast<uint32_t>(x) > static_cast<uint32_t>(key))) {
-          k = o;
-          key = x;
+        row_sync();
+        const unsigned long long *scores = sh.best[turn & 1], *keys = sh.best_key[turn & 1];
+        ++turn;
+        key = 0ull;
+        if (!exact) {
+          int ctas = 0;
+          for (int c0 = 0; c0 < kCluster; ++c0) top = fmaxf(top, __uint_as_float(static_cast<uint32_t>(scores[c0])));
+          for (int c0 = 0; c0 < kCluster; ++c0)
+            if (within_reach(__uint_as_float(static_cast<uint32_t>(scores[c0])), top)) {
+              ++ctas;
+              key = keys[c0];
+            }
+          if (ctas == 0 || (ctas == 1 && key)) return key;
+        } else {
+          k = 0ull;
+          for (int c0 = 0; c0 < kCluster; ++c0)
+            // (equal scores: the lowest index)
+            if (scores[c0] > k ||
+                (scores[c0] == k && k && static_cast<uint32_t>(keys[c0]) > static_cast<uint32_t>(key))) {
+              k = scores[c0];
+              key = keys[c0];
+            }
+          return key;
         }
       }
-      ++turn;
-      return key;
     };
     // Sums of two over the row; all threads get them.
     auto wide_sums = [&](unsigned long long& x, unsigned long long& y) {
@@ -1301,7 +1283,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
     // is none); for top-p, is that token kept?  If it is not, none behind it is: the tokens before
     // it race again.  Few are rejected, by the noise of a Gumbel draw; after kTries the cut is
     // looked for.
-    cp_async_wait<0>();
     unsigned long long cut = cut_k ? find(st.k, false) : 0ull, won = 0ull, most = 0ull;
     for (int attempt = 0;; ++attempt) {
       won = race(cut);
@@ -1344,6 +1325,7 @@ size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
 constexpr int kSlice = 200 * 1024;   // of a row and of its noise, in a CTA of the wide kernel
 constexpr int kMaxParts = kGroups / (kThreads >> 5);  // (and trips, in all of a row's parts)
+static_assert(kMaxParts <= kCutThreads && kMaxParts <= kWideThreads, "");
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kWave = 4;  // CTAs of the row kernel per SM
 
