@@ -268,6 +268,14 @@ PE_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) 
 
 // ---------------------------------------------------------------- TMA
 
+// Untiled bulk load into shared memory, completing on `bar`: 16-byte boundaries and sizes.
+PE_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // 2-D tiled bulk-tensor load into shared memory, completing on `bar`.
 // x is the innermost coordinate (elements), y the row.
 PE_DEV void tma_load_2d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y,

@@ -34,13 +34,7 @@ struct CacheArgs {
   uint32_t* status;
 };
 
-// Untiled bulk copies: global memory to shared memory, completing on `bar`, and back.
-PE_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
+// Untiled bulk copies back to global memory.
 PE_DEV void bulk_store(void* dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(dst),
                "r"(smem_u32(src)), "r"(bytes)

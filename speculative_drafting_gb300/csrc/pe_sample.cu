@@ -465,6 +465,14 @@ struct __align__(16) CutShared {
   int vec[kGroupList];
 };
 
+// A weight, or a few together (at most 8), in units of 2^-40, truncated.  (Out of its bits: conversions
+// between floats and 64-bit integers are two a clock and SM.)
+PE_DEV unsigned long long as_weight(float w) {
+  const uint32_t u = __float_as_uint(w);
+  const unsigned long long m = static_cast<unsigned long long>((u & 0x7fffffu) | 0x800000u) << 20;
+  return m >> min(130u - (u >> 23), 63u);  // (below 2^-86: 0)
+}
+
 // Sums over the CTA up to and with this thread (cut kernel); no barrier after the last read.
 template <typename T>
 PE_DEV T sum_upto(T v, T* warps) {
@@ -713,7 +721,7 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
     const float w = ex2((l - M) * c);
     bool keep = there;
     if (cut_p) {
-      const unsigned long long q = there ? static_cast<unsigned long long>(w * kOne) : 0ull;
+      const unsigned long long q = there ? as_weight(w) >> 2 : 0ull;  // (kOne)
       const unsigned long long upto = sum_upto<unsigned long long>(q, sh.scan);
       if (tid == kCutThreads - 1) sh.sum = upto;
       __syncthreads();
@@ -773,6 +781,8 @@ struct __align__(16) WideShared {
   unsigned long long key[kList];  // the tokens of the cut's bin, of all CTAs
   int tie;
   // this CTA's own
+  uint64_t full;  // (barrier) the slice is there
+  int never;      // 0
   unsigned long long scan[kWideWarps], k[kWideWarps], mine[kList];
   float wm[kWideWarps];
   uint32_t u[kWideWarps], v[kWideWarps];
@@ -809,6 +819,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
   constexpr int kVec = 16 / sizeof(T), kWideRace = 16 / kVec;  // (16 tokens a thread and trip)
   extern __shared__ uint4 held[];
   __shared__ WideShared sh;
+  if (threadIdx.x == 0) {
+    mbar_init(&sh.full, 1);
+    sh.never = 0;
+    fence_barrier_init();
+  }
   pdl_trigger();
   // (every CTA of the cluster has to have begun before another one writes to it)
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -818,7 +833,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
   const int rows = static_cast<int>(__ldcg(a.todo_n)), step = gridDim.x / kCluster;
   __syncwarp();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  uint32_t turn = 0;
+  uint32_t turn = 0, fulls = 0;
   for (int item = blockIdx.x / kCluster; item < rows; item += step) {
     const int row = __ldcg(a.todo + item);
     const Settings st = a.set[row];
@@ -827,32 +842,39 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
     const bool cut_k = st.k > 0, cut_p = st.p < 1.f;
     const int nv = s.vectors(), per = (nv + kCluster - 1) / kCluster;
     const int v0 = min(static_cast<int>(rank) * per, nv), v1 = min(v0 + per, nv);
-    // The slice, and the noise of all of it if there is no k: then all tokens race.  (Vectors of
-    // the noise lie in kVec / 4 planes.  Each thread reads what it copied.)
+    // The slice, and the noise of all of it if there is no k: then all tokens race.  By bulk copies
+    // what lies in whole vectors (all but the row's ends), of which this CTA has those up to w1.
     const bool near = a.near && noise.wide && !cut_k;
     uint4* held_g = held + per;
     auto inside = [&](int t0) { return t0 >= 0 && t0 + kVec <= a.V; };
     // (no more parts than threads)
     const float part_m = tid < a.parts ? __ldcg(&a.stat[static_cast<size_t>(row) * a.parts + tid].m) : -INFINITY;
+    __syncthreads();
     if (a.resident) {
-      for (int v = v0 + tid; v < v1; v += kWideThreads) {
-        const int t0 = s.token(v);
-        if (!inside(t0)) {
-          held[v - v0] = s.load(v);
-          continue;
+      const int w0 = v0 + (v0 < v1 && !inside(s.token(v0))), w1 = max(w0, v1 - (v0 < v1 && !inside(s.token(v1 - 1))));
+      if (tid == 0) {
+        const uint32_t bytes = static_cast<uint32_t>(w1 - w0) * 16u;
+        fence_proxy_async();  // (the last row's slice has been read)
+        mbar_arrive_expect_tx(&sh.full, near ? bytes * (1u + kVec / 4) : bytes);
+        if (bytes) {
+          bulk_load(held + w0 - v0, s.row + s.token(w0), bytes, &sh.full);
+          if (near)
+            bulk_load(held_g + (w0 - v0) * (kVec / 4), noise.g + s.token(w0), bytes * (kVec / 4), &sh.full);
         }
-        cp_async16(smem_u32(held + v - v0), s.row + t0, true);
-        if (near) {
-#pragma unroll
-          for (int e = 0; e < kVec / 4; ++e)
-            cp_async16(smem_u32(held_g + e * per + v - v0), noise.g + t0 + 4 * e, true);
-        }
+      } else if (tid < 3) {
+        const int v = tid == 1 ? v0 : v1 - 1;
+        if (v0 < v1 && (v < w0 || v >= w1)) held[v - v0] = s.load(v);
       }
-      cp_async_commit();
     }
     auto get = [&](int v) { return a.resident ? held[v - v0] : s.load(v); };
     const float M = cta_max<kWideWarps>(part_m, sh.wm);
-    cp_async_wait<0>();
+    if (a.resident) {
+      if (!mbar_wait(&sh.full, fulls & 1, &sh.never)) {
+        set_status(a.status, PE_ST_TIMEOUT);
+        mbar_wait(&sh.full, fulls & 1, &sh.never);  // (no copy is in flight when the CTA leaves)
+      }
+      ++fulls;
+    }
     // the row's least finite logit, for the bins of a k
     float lo = -INFINITY;
     if (cut_k) {
@@ -870,7 +892,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
     }
     const float c = scale_of(st.temp), it = 1.f / st.temp;
     // 2^20 weights of at most 2^40 have a sum; what is cut off of them is below 2^-20 of it
-    auto as_weight = [](float w) { return static_cast<unsigned long long>(w * 0x1p40f); };
     auto weight_of = [&](float x) { return as_weight(ex2((x - M) * c)); };
     auto add_weight = [](uint2& bin, unsigned long long q) {  // (the lower word's carry goes to the upper one)
       const uint32_t lo = static_cast<uint32_t>(q);
@@ -892,11 +913,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
     // The key of the best score among the tokens from a cut on, 0 if there is none.
     auto race = [&](unsigned long long cut) {
       const To to = place_of(cut);
+      const bool all = cut == 0ull && !(st.mp > 0.f);
       // a vector's kept logits, -inf for the others; whether there are some
       auto light = [&](float l) { return l != M && ex2((l - M) * c) < st.mp; };
       auto kept = [&](int v, float* f) {
         const int t0 = s.token(v);
         unpack16<T>(v < v1 ? get(v) : no_tokens<T>(), f);
+        if (all) return true;
         bool any = false;
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
@@ -939,7 +962,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
         pass(std::integral_constant<int, 1>(), [&](int v, float* g) {
           if (inside(s.token(v))) {
 #pragma unroll
-            for (int e = 0; e < kVec / 4; ++e) unpack16<float>(held_g[e * per + v - v0], g + 4 * e);
+            for (int e = 0; e < kVec / 4; ++e) unpack16<float>(held_g[(v - v0) * (kVec / 4) + e], g + 4 * e);
           } else {
             noise.load(s.token(v), a.V, g);
           }
@@ -959,35 +982,34 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
       for (bool exact = false;; exact = true) {
         const bool in = bv >= 0 && within_reach(bs, top);
         const int n_in = __syncthreads_count(in);
+        // (a lane for each token of the vector)
         unsigned long long best = 0ull, key = 0ull;
-        int left = 0, bi = 0x7fffffff;
-        if (in) {
-          const uint4 u = get(bv);
-          const int t0 = s.token(bv);
-#pragma unroll 1
-          for (int e = 0; e < kVec; ++e) {
-            const float l = __uint_as_float(element<T>(u, e));
-            if (!(l > -INFINITY) || !no_later(l, t0 + e, to) || (st.mp > 0.f && light(l))) continue;
-            const float g = near && inside(t0) ? reinterpret_cast<const float*>(held_g + (e >> 2) * per + bv - v0)[e & 3]
-                                               : noise.g[t0 + e];
-            if (!within_reach(fmaf(l - M, it, g), top)) continue;
-            ++left;
-            const unsigned long long o = exact ? exact_score(l, g, M, st.temp) : 1ull;
-            if (o > best) {
-              best = o;
-              bi = t0 + e;
-              key = argmax_key(l, static_cast<uint32_t>(bi));
-            }
+        int bi = 0x7fffffff;
+        unsigned found = 0;
+        for (unsigned of = __ballot_sync(0xffffffffu, in); of; of &= of - 1) {
+          const int v = __shfl_sync(0xffffffffu, bv, __ffs(of) - 1), t0 = s.token(v), e = lane & (kVec - 1);
+          const float l = __uint_as_float(element<T>(get(v), e));
+          bool there = lane < kVec && l > -INFINITY && no_later(l, t0 + e, to) && !(st.mp > 0.f && light(l));
+          float g = 0.f;
+          if (there) g = near && inside(t0) ? reinterpret_cast<const float*>(held_g)[(v - v0) * kVec + e] : noise.g[t0 + e];
+          there = there && within_reach(fmaf(l - M, it, g), top);
+          found |= __ballot_sync(0xffffffffu, there);
+          const unsigned long long o = !there ? 0ull : exact ? exact_score(l, g, M, st.temp) : 1ull;
+          if (o > best) {
+            best = o;
+            bi = t0 + e;
+            key = argmax_key(l, static_cast<uint32_t>(bi));
           }
         }
         // its thread, or the first where there is none (key 0: of several), tells the others
         unsigned long long k = best;
         int i = bi;
         if (exact) cta_best<kWideWarps>(k, i, sh.k, sh.i);
-        if (exact ? (k ? bi == i && best == k : tid == 0) : (n_in == 1 ? in : tid == 0)) {
+        const bool alone = n_in == 1 && __popc(found) == 1;  // (of the warp with it)
+        if (__syncthreads_or(alone) ? alone && best : exact ? (k ? bi == i && best == k : tid == 0) : tid == 0) {
           if (!exact) {
             k = __float_as_uint(top);
-            if (n_in != 1 || left != 1) key = 0ull;
+            if (!alone) key = 0ull;
           }
           for (int to_cta = 0; to_cta < kCluster; ++to_cta) {
             put64(&sh.best[turn & 1][rank], to_cta, k);
