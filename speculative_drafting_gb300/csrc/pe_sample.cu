@@ -210,8 +210,9 @@ PE_DEV float cta_max(float v, float* warps) {  // NaN if there is one
   __syncthreads();
   if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = warps[0];
-  for (int w = 1; w < W; ++w) v = max_nan(v, warps[w]);
+  v = warps[threadIdx.x % W];
+#pragma unroll
+  for (int o = W / 2; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 // Sum over the CTA, in a fixed order; all threads get it.
@@ -888,7 +889,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
       lo = -cta_max<kWideWarps>(-lo, sh.wm);
       if (tid < kCluster) put32(&sh.lo[rank], tid, __float_as_uint(lo));
       row_sync();
-      for (int i = 0; i < kCluster; ++i) lo = fminf(lo, sh.lo[i]);
+      lo = -warp_max(-sh.lo[lane % kCluster]);
     }
     const float c = scale_of(st.temp), it = 1.f / st.temp;
     // 2^20 weights of at most 2^40 have a sum; what is cut off of them is below 2^-20 of it
@@ -920,11 +921,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
         const int t0 = s.token(v);
         unpack16<T>(v < v1 ? get(v) : no_tokens<T>(), f);
         if (all) return true;
-        bool any = false;
+        bool any = false, tie = false;
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-          f[e] = no_later(f[e], t0 + e, to) ? f[e] : -INFINITY;
+          tie |= f[e] == to.x;
+          f[e] = f[e] >= to.x ? f[e] : -INFINITY;
           any |= f[e] > -INFINITY;
+        }
+        if (tie) {
+#pragma unroll
+          for (int e = 0; e < kVec; ++e)
+            if (f[e] == to.x && t0 + e > to.t) f[e] = -INFINITY;
         }
         if (st.mp > 0.f) {
 #pragma unroll
@@ -974,8 +981,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
       __syncthreads();
       if (lane == 0) sh.wm[warp] = wt;
       __syncthreads();
-      float top = sh.wm[0];
-      for (int w = 1; w < kWideWarps; ++w) top = fmaxf(top, sh.wm[w]);
+      float top = warp_max(sh.wm[lane % kWideWarps]);
       // The tokens within reach of the best score (of this thread's best vector).  As a rule it is
       // one in the whole row: then its fp32 score and key do, else the scores are formed again, in
       // 64 bits (as in the row kernel).
@@ -1006,40 +1012,37 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
         int i = bi;
         if (exact) cta_best<kWideWarps>(k, i, sh.k, sh.i);
         const bool alone = n_in == 1 && __popc(found) == 1;  // (of the warp with it)
-        if (__syncthreads_or(alone) ? alone && best : exact ? (k ? bi == i && best == k : tid == 0) : tid == 0) {
+        const bool tells = __syncthreads_or(alone) ? alone && best : exact && k ? bi == i && best == k : tid == 0;
+        if (const unsigned teller = __ballot_sync(0xffffffffu, tells)) {
           if (!exact) {
             k = __float_as_uint(top);
             if (!alone) key = 0ull;
           }
-          for (int to_cta = 0; to_cta < kCluster; ++to_cta) {
-            put64(&sh.best[turn & 1][rank], to_cta, k);
-            put64(&sh.best_key[turn & 1][rank], to_cta, key);
+          k = __shfl_sync(0xffffffffu, k, __ffs(teller) - 1);
+          key = __shfl_sync(0xffffffffu, key, __ffs(teller) - 1);
+          if (lane < kCluster) {
+            put64(&sh.best[turn & 1][rank], lane, k);
+            put64(&sh.best_key[turn & 1][rank], lane, key);
           }
         }
         row_sync();
-        const unsigned long long *scores = sh.best[turn & 1], *keys = sh.best_key[turn & 1];
+        // (lane i: CTA i % kCluster's)
+        k = sh.best[turn & 1][lane % kCluster];
+        key = sh.best_key[turn & 1][lane % kCluster];
         ++turn;
-        key = 0ull;
-        if (!exact) {
-          int ctas = 0;
-          for (int c0 = 0; c0 < kCluster; ++c0) top = fmaxf(top, __uint_as_float(static_cast<uint32_t>(scores[c0])));
-          for (int c0 = 0; c0 < kCluster; ++c0)
-            if (within_reach(__uint_as_float(static_cast<uint32_t>(scores[c0])), top)) {
-              ++ctas;
-              key = keys[c0];
-            }
-          if (ctas == 0 || (ctas == 1 && key)) return key;
-        } else {
-          k = 0ull;
-          for (int c0 = 0; c0 < kCluster; ++c0)
-            // (equal scores: the lowest index)
-            if (scores[c0] > k ||
-                (scores[c0] == k && k && static_cast<uint32_t>(keys[c0]) > static_cast<uint32_t>(key))) {
-              k = scores[c0];
-              key = keys[c0];
-            }
-          return key;
+        if (exact) {  // (equal scores: the lowest index)
+          i = static_cast<int>(~static_cast<uint32_t>(key) & 0x7fffffffu);
+          const unsigned long long mine = k;
+          const int at = i;
+          warp_best(k, i);
+          return k ? __shfl_sync(0xffffffffu, key, __ffs(__ballot_sync(0xffffffffu, mine == k && at == i)) - 1) : 0ull;
         }
+        const float theirs = __uint_as_float(static_cast<uint32_t>(k));
+        top = warp_max(theirs);
+        const unsigned ctas = __ballot_sync(0xffffffffu, lane < kCluster && within_reach(theirs, top));
+        if (ctas == 0) return 0ull;
+        key = __shfl_sync(0xffffffffu, key, __ffs(ctas) - 1);
+        if ((ctas & (ctas - 1)) == 0 && key) return key;
       }
     };
     // Sums of two over the row; all threads get them.
@@ -1069,10 +1072,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
         }
       }
       row_sync();
-      x = y = 0ull;
-      for (int i = 0; i < kCluster; ++i) {
-        x += sh.best[turn & 1][i];
-        y += sh.best_key[turn & 1][i];
+      x = sh.best[turn & 1][lane % kCluster];
+      y = sh.best_key[turn & 1][lane % kCluster];
+#pragma unroll
+      for (int o = kCluster / 2; o; o >>= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+        y += __shfl_xor_sync(0xffffffffu, y, o);
       }
       ++turn;
     };
@@ -1317,16 +1322,28 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
       for (int v = v0 + tid; v < v1; v += kWideThreads) {
         float f[kVec];
         unpack16<T>(get(v), f);
-        const int t0 = s.token(v);
-        float b = 0.f, w = 0.f;  // (a vector's in fp32: conversions to 64 bits are slow)
+        // (a vector's in fp32; the ties at a place apart, which are few)
+        float q[kVec];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          const float q = ex2((f[e] - M) * c);
-          b += no_later(f[e], t0 + e, to) ? q : 0.f;
-          if (attempt == 0) w += no_later(f[e], t0 + e, last) ? q : 0.f;
-        }
-        before += as_weight(b);
-        if (attempt == 0) all += as_weight(w);
+        for (int e = 0; e < kVec; ++e) q[e] = ex2((f[e] - M) * c);
+        auto upto = [&](const To& to) {
+          float w = 0.f;
+          bool tie = false;
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) {
+            if (f[e] > to.x) w += q[e];
+            tie |= f[e] == to.x;
+          }
+          if (tie) {
+            const int t0 = s.token(v);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+              if (f[e] == to.x && t0 + e <= to.t) w += q[e];
+          }
+          return as_weight(w);
+        };
+        before += upto(to);
+        if (attempt == 0) all += upto(last);
       }
       wide_sums(before, all);
       // (the first token is kept whatever top_p is: nothing is before it)
