@@ -18,19 +18,23 @@
 //                    one, in order; sums of their weights, the cut, the best score.
 //   wide kernel  takes the rows for which that does not do (flat rows that keep thousands of
 //                tokens, a large k, many equal logits), a cluster of CTAs a row with a slice
-//                each in shared memory.  Top-p: all tokens race, and the weight before the
-//                winner tells whether it is kept (if not, the tokens before it race again).
+//                each in shared memory, beside its noise where that fits.  Top-p: all tokens race, and the
+//                weight before the winner tells whether it is kept (if not, the tokens before it
+//                race again).
 //                Top-k: a histogram of counts over the distance from the largest logit, finer
 //                ones inside the bin of the cut, then the race.  Weights are 40-bit integers there:
 //                their sums do not depend on an order.
 //
 // The first kernel is bound by the logits' bytes, the others by the latency of a row's steps.
-// Launched cold, 512 bf16 rows of 201,088 of mixed settings (245 MB with the noise): 48 us at 5.1
-// TB/s, 26, and 39 for some 70 flat rows.  8 fp32 rows: 7, 12 and 4, 13.4 us a call.
+// Launched cold, 512 bf16 rows of 201,088 of mixed settings (245 MB with the noise): 49 us at 5.0
+// TB/s, 23, and 26 for a dozen flat rows; 104 us a call.  8 fp32 rows: 7, 11 and 4, 12.5 us a
+// call.  512 flat bf16 rows: 297 us, some 9 a row and cluster.  A flat row alone takes 15: a third is
+// the first fetch of the code.
 // Every row by a cluster with the row in shared memory took 162 us for 512 bf16 rows with top-k:
 // the barriers of a row are waited for with its 400 KB held.  The cut in the first kernel, by a
-// cluster of a row's CTAs, took 78 where the two take 72, the cut by the first CTA of the wide
-// kernel's cluster for few rows 14.6 where three kernels take 13.4.
+// cluster of a row's CTAs, took 78 where the two took 72, the cut by the first CTA of the wide
+// kernel's cluster for few rows 14.6 where three kernels took 13.4.  Scores are compared in fp32,
+// and in 64 bits only where two are near: a comparison in doubles takes 5000 clocks.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -815,7 +819,8 @@ PE_DEV int wide_before(int v, int* warps, int& all) {
 }
 
 template <typename T>
-// (two CTAs an SM: 512 flat rows 850 us instead of 1170, 8 of them 66 instead of 52)
+// (two CTAs an SM, with half the registers: 512 mixed bf16 rows 159 us, 161 with one, 64 of them 91
+// and 72)
 __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const SampleArgs a) {
   constexpr int kVec = 16 / sizeof(T), kWideRace = 16 / kVec;  // (16 tokens a thread and trip)
   extern __shared__ uint4 held[];
