@@ -906,7 +906,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
     };
 
     // A place in the order (an argmax_key, 0: the end), and whether a token comes no later.
-    // (Without branches: a few instructions a token are what the passes over a slice take.)
     struct To {
       float x;
       int t;
@@ -926,6 +925,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
         const int t0 = s.token(v);
         unpack16<T>(v < v1 ? get(v) : no_tokens<T>(), f);
         if (all) return true;
+        // (ties with the place apart, which are few: instructions are what a pass takes)
         bool any = false, tie = false;
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
