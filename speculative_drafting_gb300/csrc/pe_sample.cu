@@ -53,10 +53,8 @@ constexpr int kRaceUnroll = 2;        // ... where the noise is streamed too
 constexpr int kMaxPartBytes = 65536;  // of a row, per CTA
 constexpr int kGroups = 4096;         // of a row, at most
 
-constexpr int kCutThreads = 512;      // cut kernel
-constexpr int kCutWarps = kCutThreads / 32;
-constexpr int kCutBins = kCutThreads;  // of the groups' largest logits
-constexpr int kList = kCutThreads;    // candidates of a row that are put in order
+constexpr int kCutBins = 512;         // cut kernel: of the groups' largest logits
+constexpr int kList = 512;            // candidates of a row that are put in order
 constexpr int kGroupList = 1024;      // groups that are read again, and vectors of theirs that matter
 
 constexpr int kWideThreads = 512;     // wide kernel
@@ -450,9 +448,9 @@ constexpr float kOne = 0x1p38f;
 
 // Shared memory of the cut kernel.
 struct __align__(16) CutShared {
-  float m[kCutWarps];
-  unsigned long long k[kCutWarps], scan[kCutWarps];
-  int i[kCutWarps], scan_n[kCutWarps];
+  float m[16];
+  unsigned long long k[16], scan[16];
+  int i[16], scan_n[16];
   int n, n_groups, n_vec, last, most, near;
   uint32_t bound;
   unsigned long long sum;
@@ -479,7 +477,7 @@ PE_DEV unsigned long long as_weight(float w) {
 }
 
 // Sums over the CTA up to and with this thread (cut kernel); no barrier after the last read.
-template <typename T>
+template <int W, typename T>
 PE_DEV T sum_upto(T v, T* warps) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -490,7 +488,7 @@ PE_DEV T sum_upto(T v, T* warps) {
   if (lane == 31) warps[warp] = v;
   __syncthreads();
   T before = 0;
-  for (int w = 0; w < kCutWarps; ++w)
+  for (int w = 0; w < W; ++w)
     if (w < warp) before += warps[w];
   return v + before;
 }
@@ -498,10 +496,13 @@ PE_DEV T sum_upto(T v, T* warps) {
 // (for the rounding of a sum that is compared with another)
 PE_DEV unsigned long long with_margin(unsigned long long x) { return x + (x >> 20); }
 
-// The answer of a row from its parts.
-template <typename T>
-__global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const SampleArgs a) {
-  constexpr int kVec = 16 / sizeof(T);
+// The answer of a row from its parts.  16 warps, or 8 (with two bins and two candidates a thread)
+// where the rows are more than the SMs hold of the former at once: 512 bf16 rows of 201,088 with top-k
+// 69 us, 77 with 16 warps; 8 rows 19 and 20.
+template <typename T, int W>
+__global__ void __launch_bounds__(32 * W, 32 / W) sample_cut_kernel(const SampleArgs a) {
+  constexpr int kVec = 16 / sizeof(T), kN = 32 * W, kE = kList / kN;
+  static_assert(kCutBins == kList && kE * kN == kList && W <= 16, "");
   __shared__ CutShared sh;
   pdl_trigger();
   pdl_wait();
@@ -511,16 +512,16 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
   // (what only some rows need is asked for with the settings; no more parts than threads)
   const int gpt = 8 - a.gshift, groups = a.parts * a.trips << gpt;  // log2 of a trip's groups; the row's
   const float* top = a.top + static_cast<size_t>(row) * groups;
-  float part_m = -INFINITY, part_s = 0.f, top_m[kGroups / kCutThreads];
+  float part_m = -INFINITY, part_s = 0.f, top_m[kGroups / kN];
   if (tid < a.parts) {
     part_m = __ldcg(&stat[tid].m);
     part_s = __ldcg(&stat[tid].s);
   }
 #pragma unroll
-  for (int x = 0; x < kGroups / kCutThreads; ++x)
-    top_m[x] = tid + x * kCutThreads < groups ? __ldcg(top + tid + x * kCutThreads) : -INFINITY;
+  for (int x = 0; x < kGroups / kN; ++x)
+    top_m[x] = tid + x * kN < groups ? __ldcg(top + tid + x * kN) : -INFINITY;
   auto answer = [&](unsigned long long k, int i) {
-    cta_best<kCutWarps>(k, i, sh.k, sh.i);
+    cta_best<W>(k, i, sh.k, sh.i);
     if (tid == 0) {
       a.token[row] = k ? i : -1;
       if (!k) set_status(a.status, PE_ST_SAMPLING);
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
   if (st.temp < 0.f) return;
   if (st.temp == 0.f) {
     unsigned long long k = 0ull;
-    for (int i = tid; i < a.parts; i += kCutThreads) k = max(k, __ldcg(&stat[i].key));
+    for (int i = tid; i < a.parts; i += kN) k = max(k, __ldcg(&stat[i].key));
     answer(k, static_cast<int>(~static_cast<uint32_t>(k)));
     return;
   }
@@ -537,13 +538,16 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
   float lo = INFINITY;
   if (cut) {
 #pragma unroll
-    for (int x = 0; x < kGroups / kCutThreads; ++x) {
-      if (tid + x * kCutThreads < groups) sh.top[tid + x * kCutThreads] = top_m[x];
+    for (int x = 0; x < kGroups / kN; ++x) {
+      if (tid + x * kN < groups) sh.top[tid + x * kN] = top_m[x];
       if (top_m[x] > -INFINITY) lo = fminf(lo, top_m[x]);
     }
-    sh.h.cnt[tid] = 0;
-    sh.h.least[tid] = 0xffffffffu;
-    sh.h.low[tid] = sh.h.high[tid] = 0;
+#pragma unroll
+    for (int x = 0; x < kE; ++x) {
+      sh.h.cnt[tid + x * kN] = 0;
+      sh.h.least[tid + x * kN] = 0xffffffffu;
+      sh.h.low[tid + x * kN] = sh.h.high[tid + x * kN] = 0;
+    }
     if (tid == 0) {
       sh.n = sh.n_groups = sh.n_vec = 0;
       sh.last = kCutBins;
@@ -551,24 +555,55 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
       sh.bound = 0xffffffffu;
     }
   }
-  const float M = cta_max<kCutWarps>(part_m, sh.m);
+  const float M = cta_max<W>(part_m, sh.m);
   if (!(fabsf(M) < INFINITY)) {  // no distribution
     answer(0ull, -1);
     return;
   }
   // the best score among the threads': where one alone is within reach, that one
-  auto finish = [&](bool there, float l, float g, int t) {
-    const float score = there ? fmaf(l - M, 1.f / st.temp, g) : -INFINITY;
-    const float best = cta_max<kCutWarps>(score == score ? score : -INFINITY, sh.m);
-    const bool in = there && within_reach(score, best);
-    if (__syncthreads_count(in) != 1)
-      answer(in ? exact_score(l, g, M, st.temp) : 0ull, in ? t : 0x7fffffff);
-    else if (in)
-      a.token[row] = t;
+  auto finish = [&](const bool* there, const float* l, const float* g, const int* t) {
+    float score[kE], top = -INFINITY;
+    bool in[kE];
+    int near = 0;
+#pragma unroll
+    for (int x = 0; x < kE; ++x) {
+      score[x] = there[x] ? fmaf(l[x] - M, 1.f / st.temp, g[x]) : -INFINITY;
+      top = fmaxf(top, score[x]);
+    }
+    top = cta_max<W>(top, sh.m);
+#pragma unroll
+    for (int x = 0; x < kE; ++x) {
+      in[x] = there[x] && within_reach(score[x], top);
+      near += __syncthreads_count(in[x]);
+    }
+    unsigned long long k = 0ull;
+    int i = 0x7fffffff;
+#pragma unroll
+    for (int x = 0; x < kE; ++x) {
+      if (!in[x]) continue;
+      const unsigned long long o = near == 1 ? 1ull : exact_score(l[x], g[x], M, st.temp);
+      if (o > k || (o == k && t[x] < i)) {
+        k = o;
+        i = t[x];
+      }
+    }
+    if (near != 1)
+      answer(k, i);
+    else if (k)
+      a.token[row] = i;
   };
+  bool keep[kE];
+  float l[kE], g[kE];
+  int t[kE];
   if (!cut) {
-    const int t = tid < a.parts ? __ldcg(&stat[tid].idx) : -1;
-    finish(t >= 0, t < 0 ? 0.f : __ldcg(&stat[tid].x), t < 0 ? 0.f : __ldcg(&stat[tid].g), t);
+#pragma unroll
+    for (int x = 0; x < kE; ++x) {
+      t[x] = x == 0 && tid < a.parts ? __ldcg(&stat[tid].idx) : -1;
+      keep[x] = t[x] >= 0;
+      l[x] = keep[x] ? __ldcg(&stat[tid].x) : 0.f;
+      g[x] = keep[x] ? __ldcg(&stat[tid].g) : 0.f;
+    }
+    finish(keep, l, g, t);
     return;
   }
   const float c = scale_of(st.temp);
@@ -577,13 +612,13 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
   unsigned long long z = 0;  // the weight of the whole row, where top-p alone asks for it
   if (cut_k || cut_p) {
     if (!cut_k)
-      z = cta_sum<kCutWarps>(
+      z = cta_sum<W>(
           part_m > -INFINITY ? static_cast<unsigned long long>(part_s * ex2((part_m - M) * c) * kOne) : 0ull, sh.k);
     // bins of the range that the groups' largest logits span
-    lo = -cta_max<kCutWarps>(-lo, sh.m);
+    lo = -cta_max<W>(-lo, sh.m);
     const float span = M - lo;
     const float scale = span > 0.f && span < INFINITY ? fminf(kCutBins / span, 1e30f) : 0.f;
-    for (int i = tid; i < groups; i += kCutThreads) {
+    for (int i = tid; i < groups; i += kN) {
       const float t = sh.top[i], w = ex2((t - M) * c) * 0x1p20f;
       const uint32_t high = static_cast<uint32_t>(w);
       // (top-p alone: those that weigh next to nothing are left out, as many fall into one bin)
@@ -600,23 +635,56 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
     __syncthreads();
     // The first bin with which there are k, or p of the weight (a margin for the rounding of
     // the sum); for want of the latter as many as are put in order: their weight tells, below.
-    const uint32_t least = sh.h.least[tid];
-    const int count = sum_upto<int>(sh.h.cnt[tid], sh.scan_n);
-    bool enough = count >= st.k;
+    // (bins kE tid and on)
+    uint32_t least[kE];
+    int cnt[kE], upto[kE], total = 0;
+    bool enough[kE];
+#pragma unroll
+    for (int x = 0; x < kE; ++x) {
+      least[x] = sh.h.least[kE * tid + x];
+      cnt[x] = sh.h.cnt[kE * tid + x];
+      total += cnt[x];
+    }
+    total = sum_upto<W, int>(total, sh.scan_n);
+#pragma unroll
+    for (int x = kE - 1; x >= 0; --x) {
+      upto[x] = total;
+      enough[x] = total >= st.k;
+      total -= cnt[x];
+    }
     if (!cut_k) {
-      const unsigned long long mass = sum_upto<unsigned long long>(
-          sh.h.low[tid] + (static_cast<unsigned long long>(sh.h.high[tid]) << 18), sh.scan);
+      unsigned long long w[kE], mass = 0;
+#pragma unroll
+      for (int x = 0; x < kE; ++x) {
+        w[x] = sh.h.low[kE * tid + x] + (static_cast<unsigned long long>(sh.h.high[kE * tid + x]) << 18);
+        mass += w[x];
+      }
+      mass = sum_upto<W, unsigned long long>(mass, sh.scan);
       const unsigned long long need = with_margin(share_of(st.p, z));
-      enough = mass >= need;
-      if (tid == kCutThreads - 1) sh.near = mass >= need - (need >> 2);
-      const int most = __reduce_max_sync(0xffffffffu, count <= kList / 2 ? tid : -1);
+      if (tid == kN - 1) sh.near = mass >= need - (need >> 2);
+      int most = -1;
+#pragma unroll
+      for (int x = kE - 1; x >= 0; --x) {
+        enough[x] = mass >= need;
+        mass -= w[x];
+        if (most < 0 && upto[x] <= kList / 2) most = kE * tid + x;
+      }
+      most = __reduce_max_sync(0xffffffffu, most);
       if (lane == 0) atomicMax(&sh.most, most);
     }
-    const int last = __reduce_min_sync(0xffffffffu, enough ? tid : kCutBins);
+    int last = kCutBins;
+#pragma unroll
+    for (int x = kE - 1; x >= 0; --x)
+      if (enough[x]) last = kE * tid + x;
+    last = __reduce_min_sync(0xffffffffu, last);
     if (lane == 0) atomicMin(&sh.last, last);
     __syncthreads();
     const int bin = sh.last < kCutBins || cut_k ? sh.last : sh.most;
-    const uint32_t o = __reduce_min_sync(0xffffffffu, tid <= bin ? least : 0xffffffffu);
+    uint32_t o = 0xffffffffu;
+#pragma unroll
+    for (int x = 0; x < kE; ++x)
+      if (kE * tid + x <= bin) o = min(o, least[x]);
+    o = __reduce_min_sync(0xffffffffu, o);
     if (lane == 0) atomicMin(&sh.bound, o);
     __syncthreads();
     // (where all groups' largest are far from enough, the tokens behind them weigh as much)
@@ -630,7 +698,7 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
     bound = fminf(M + (log2f(fminf(st.mp, 1.f)) * 1.00001f - 1e-5f) / c, M);
   }
   // ---------------- the groups that have a token from the bound on, and those tokens
-  for (int i = tid; i < groups; i += kCutThreads)
+  for (int i = tid; i < groups; i += kN)
     if (sh.top[i] > -INFINITY && sh.top[i] >= bound) {
       const int at = atomicAdd(&sh.n_groups, 1);
       if (at < kGroupList) sh.group[at] = static_cast<uint16_t>(i);
@@ -643,12 +711,12 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
     // loads), a thread to a vector.  Then those vectors' tokens.
     const int per = 2 + a.gshift, items = n_groups << per;  // log2 of a group's vectors
     static_assert(kUnroll == 4 && kThreads == 256, "");
-    for (int i0 = tid & ~31; i0 < items; i0 += kUnroll * kCutThreads) {
+    for (int i0 = tid & ~31; i0 < items; i0 += kUnroll * kN) {
       uint4 u[kUnroll];
       int v[kUnroll];
 #pragma unroll
       for (int x = 0; x < kUnroll; ++x) {
-        const int i = i0 + x * kCutThreads + lane;
+        const int i = i0 + x * kN + lane;
         const int g = sh.group[min(i, items - 1) >> per], j = i & ((1 << per) - 1);
         const int trip = g >> gpt, part = trip / a.trips;
         const int at = (trip - part * a.trips) * kUnroll * kThreads + (j >> a.gshift) * kThreads +
@@ -676,7 +744,7 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
     }
     __syncthreads();
     const int n_vec = sh.n_vec;
-    for (int i0 = 0; i0 < min(n_vec, kGroupList); i0 += kCutThreads) {
+    for (int i0 = 0; i0 < min(n_vec, kGroupList); i0 += kN) {
       const int v = i0 + tid < min(n_vec, kGroupList) ? sh.vec[i0 + tid] : -1;
       const uint4 u = v >= 0 ? s.load(v) : no_tokens<T>();
       float f[kVec];
@@ -708,35 +776,52 @@ __global__ void __launch_bounds__(kCutThreads, 2) sample_cut_kernel(const Sample
   bool done = n_groups <= kGroupList && sh.n_vec <= kGroupList && n <= kList;
   if (done) {
     // ---------------- in order: each counts those before it; then thread i has the i-th
-    {
-      const unsigned long long mine = tid < n ? sh.l.key[tid] : 0ull;
+#pragma unroll 1
+    for (int x = 0; x < kE; ++x) {
+      const int i = tid + x * kN;
+      const unsigned long long mine = i < n ? sh.l.key[i] : 0ull;
       int place = 0;
-      if ((tid & ~31) < n) {
+      if ((i & ~31) < n) {
 #pragma unroll 8
         for (int j = 0; j < n; ++j) place += sh.l.key[j] > mine;
       }
-      if (tid < n) sh.l.sorted[place] = mine;
+      if (i < n) sh.l.sorted[place] = mine;
     }
     __syncthreads();
-    const unsigned long long key = tid < n ? sh.l.sorted[tid] : 0ull;
-    const int t = static_cast<int>(~static_cast<uint32_t>(key));
-    const bool there = tid < n && (!cut_k || tid < st.k);
-    const float g = there ? a.gumbel[row * a.ld_g + t] : 0.f;
-    const float l = logit_of(static_cast<uint32_t>(key >> 32));
-    const float w = ex2((l - M) * c);
-    bool keep = there;
+    float w[kE];
+#pragma unroll
+    for (int x = 0; x < kE; ++x) {
+      const int i = kE * tid + x;
+      const unsigned long long key = i < n ? sh.l.sorted[i] : 0ull;
+      t[x] = static_cast<int>(~static_cast<uint32_t>(key));
+      keep[x] = i < n && (!cut_k || i < st.k);
+      g[x] = keep[x] ? a.gumbel[row * a.ld_g + t[x]] : 0.f;
+      l[x] = logit_of(static_cast<uint32_t>(key >> 32));
+      w[x] = ex2((l[x] - M) * c);
+    }
     if (cut_p) {
-      const unsigned long long q = there ? as_weight(w) >> 2 : 0ull;  // (kOne)
-      const unsigned long long upto = sum_upto<unsigned long long>(q, sh.scan);
-      if (tid == kCutThreads - 1) sh.sum = upto;
+      unsigned long long q[kE], mass = 0;
+#pragma unroll
+      for (int x = 0; x < kE; ++x) {
+        q[x] = keep[x] ? as_weight(w[x]) >> 2 : 0ull;  // (kOne)
+        mass += q[x];
+      }
+      mass = sum_upto<W, unsigned long long>(mass, sh.scan);
+      if (tid == kN - 1) sh.sum = mass;
       __syncthreads();
       // (top-p alone: of all tokens, and if these do not weigh enough the cut lies behind them)
       const unsigned long long most = share_of(st.p, cut_k ? sh.sum : z);
       done = cut_k || sh.sum >= with_margin(most);
-      keep = there && (tid == 0 || upto - q < most);
+#pragma unroll
+      for (int x = kE - 1; x >= 0; --x) {
+        mass -= q[x];  // (before it)
+        keep[x] = keep[x] && (kE * tid + x == 0 || mass < most);
+      }
     }
     if (done) {
-      finish(keep && (tid == 0 || w >= st.mp), l, g, t);
+#pragma unroll
+      for (int x = 0; x < kE; ++x) keep[x] = keep[x] && (kE * tid + x == 0 || w[x] >= st.mp);
+      finish(keep, l, g, t);
       return;
     }
   }
@@ -1369,7 +1454,7 @@ size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
 constexpr int kSlice = 200 * 1024;   // of a row and of its noise, in a CTA of the wide kernel
 constexpr int kMaxParts = kGroups / (kThreads >> 5);  // (and trips, in all of a row's parts)
-static_assert(kMaxParts <= kCutThreads && kMaxParts <= kWideThreads, "");
+static_assert(kMaxParts <= 512 && kMaxParts <= kWideThreads, "");
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kWave = 4;  // CTAs of the row kernel per SM
 
@@ -1416,7 +1501,9 @@ cudaError_t launch(const SampleArgs& a, int num_sms, cudaStream_t st) {
   }
   e = launch_chained(sample_row_kernel<T>, dim3(static_cast<unsigned>(a.T) * a.parts), dim3(kThreads), 0, st, a);
   if (e != cudaSuccess) return e;
-  e = launch_chained(sample_cut_kernel<T>, dim3(a.T), dim3(kCutThreads), 0, st, a);
+  const bool many = a.T > 2 * num_sms && a.parts <= 256;
+  e = launch_chained(many ? sample_cut_kernel<T, 8> : sample_cut_kernel<T, 16>, dim3(a.T), dim3(many ? 256 : 512), 0, st,
+                     a);
   if (e != cudaSuccess || !(a.top_k || a.top_p || a.min_p)) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCluster * std::min(a.T, std::max(num_sms / kCluster, 1)));

@@ -100,6 +100,15 @@ def test_odd_vocabulary_and_many_rows():
     check(case((9, 1, 4) * 3, 50257, "f32", seed=3, extra=1), least_clear=0.9)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["peaked", "flat", "ties"])
+def test_more_rows_than_fit_at_once(dtype, kind):
+    """640 rows: every setting in a batch of that size, candidates up to the most that are put in order."""
+    check(case((9, 1, 8, 0, 14) * 20, 3001, dtype, kind, seed=12, extra=1), least_clear=0.8, pad=(3, 2))
+    ks = [(1.0, k, p, 0.0) for k, p in ((500, 1.0), (512, 0.99), (513, 1.0), (300, 0.9), (0, 0.97))]
+    check(case((64,) * 5, 1500, dtype, kind, seed=13, settings=ks), least_clear=0.5)
+
+
 def test_large_vocabulary():
     """Slices that no shared memory holds: the rows are read again where they lie."""
     check(case((1,) * 3, 1_000_003, "f32", settings=[SETTINGS[i] for i in (2, 3, 9)], seed=4), least_clear=0.6)
