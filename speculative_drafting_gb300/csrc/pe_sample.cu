@@ -50,7 +50,9 @@ constexpr int kThreads = 256;         // row kernel (the cut kernel counts on 2^
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;            // 16-byte loads in flight per thread
 constexpr int kRaceUnroll = 2;        // ... where the noise is streamed too
-constexpr int kMaxPartBytes = 65536;  // of a row, per CTA
+// of a row, per CTA (768 greedy bf16 rows of 201,088 74 us, 82 with 64 KB, 79 with 112; 384 fp32
+// ones of 151,936 60, 62 and 61)
+constexpr int kMaxPartBytes = 80 * 1024;
 constexpr int kGroups = 4096;         // of a row, at most
 
 constexpr int kCutBins = 512;         // cut kernel: of the groups' largest logits
@@ -146,6 +148,14 @@ PE_DEV uint4 no_tokens() {
                         : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
 }
 
+// Half of a 32-byte sector whose other half is loaded next: by way of the L1 cache, past which every
+// sector would come twice (512 bf16 rows of 201,088 without a cut 179 us, 145 like this).
+PE_DEV uint4 ld_half16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // The noise of a row beside a vector of its logits; zeros outside the row.
 template <typename T>
 struct Noise {
@@ -159,7 +169,7 @@ struct Noise {
   PE_DEV void load(int t0, int V, float* x) const {
     if (wide && t0 >= 0 && t0 + kVec <= V) {
 #pragma unroll
-      for (int e = 0; e < kVec; e += 4) unpack16<float>(ld_stream16(g + t0 + e), x + e);
+      for (int e = 0; e < kVec; e += 4) unpack16<float>(kVec > 4 ? ld_half16(g + t0 + e) : ld_stream16(g + t0 + e), x + e);
     } else {
 #pragma unroll
       for (int e = 0; e < kVec; ++e) x[e] = t0 + e >= 0 && t0 + e < V ? g[t0 + e] : 0.f;
@@ -244,6 +254,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
   __shared__ unsigned long long warp_k[kWarps];
   __shared__ int warp_i[kWarps];
   __shared__ Settings set_sh;
+  __shared__ int request_sh;
+  __shared__ uint32_t status_sh;
   pdl_trigger();
   pdl_wait();
   const int row = blockIdx.x / a.parts, part = blockIdx.x - row * a.parts;
@@ -259,20 +271,20 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
     if (lane == 0) {
       uint32_t status = 0;
       Settings x{-1.f, 1.f, 0.f, 0};
-      if (r >= 0) {
-        x = settings_of(a, r, status);
-        if (request_rows(a.qsl, r, a.T).bad) status |= PE_ST_ROWS_RANGE;
-      }
+      if (r >= 0) x = settings_of(a, r, status);
       set_sh = x;
-      if (part == 0) {
-        a.set[row] = x;
-        if (status) set_status(a.status, status);
-        if (row == 0) *a.todo_n = 0u;
-      }
+      request_sh = r;
+      status_sh = status;
     }
   }
   __syncthreads();
   const Settings st = set_sh;
+  if (part == 0 && tid == 0) {
+    a.set[row] = st;
+    if (request_sh >= 0 && request_rows(a.qsl, request_sh, a.T).bad) status_sh |= PE_ST_ROWS_RANGE;
+    if (status_sh) set_status(a.status, status_sh);
+    if (row == 0) *a.todo_n = 0u;
+  }
   if (st.temp < 0.f) return;
   Part out{-INFINITY, 0.f, 0.f, 0.f, -1, 0, 0ull};
   const bool free = st.k == 0 && st.p >= 1.f && st.mp == 0.f;
