@@ -26,14 +26,15 @@
 //                their sums do not depend on an order.
 //
 // The first kernel is bound by the logits' bytes, the others by the latency of a row's steps.
-// Launched cold, 512 bf16 rows of 201,088 of mixed settings (245 MB with the noise): 49 us at 5.0
-// TB/s, 23, and 26 for a dozen flat rows; 104 us a call.  8 fp32 rows: 7, 11 and 4, 12.5 us a
+// Launched cold, 512 bf16 rows of 201,088 of mixed settings (245 MB with the noise): 46 us at 5.4
+// TB/s, 18, and 25 for a dozen flat rows; 94 us a call.  8 fp32 rows: 7, 11 and 4, 12.5 us a
 // call.  512 flat bf16 rows: 297 us, some 9 a row and cluster.  A flat row alone takes 15: a third is
 // the first fetch of the code.
 // Every row by a cluster with the row in shared memory took 162 us for 512 bf16 rows with top-k:
 // the barriers of a row are waited for with its 400 KB held.  The cut in the first kernel, by a
 // cluster of a row's CTAs, took 78 where the two took 72, the cut by the first CTA of the wide
-// kernel's cluster for few rows 14.6 where three kernels took 13.4.  Scores are compared in fp32,
+// kernel's cluster for few rows 14.6 where three kernels took 13.4, by the last CTA of a row to
+// finish 16.8 for 13.6.  Scores are compared in fp32,
 // and in 64 bits only where two are near: a comparison in doubles takes 5000 clocks.
 #include <algorithm>
 #include <atomic>
