@@ -310,8 +310,9 @@ PE_DEV void load_q(const TcArgs& p, const Unit& u, uint8_t* q_sm, bool to_l2) {
 // A unit's results: through its Q tiles (whole units), or as fp32 partials straight to the
 // workspace.  m and l are this thread's row's; those of a narrow unit's two streams join
 // here, in stream 0's warps.  A whole unit is noted in bad if a value is not finite though
-// its row's l is a number.
-template <int HD>
+// its row's l is a number.  (One for the kernels with a tree, one for those without: a call that both
+// share costs a prompt of 8192 573 us, 568 like this.)
+template <int HD, bool kTree>
 __device__ __noinline__ void finish_unit(const TcArgs& p, const Unit& u, int* bad, uint8_t* q_sm, uint32_t tmem,
                                          const float (*ml)[kRows][2], float m, float l) {
   constexpr int kLpr = Lines<HD>::kLpr, kRpi = Lines<HD>::kRpi;
@@ -922,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         failed = failed || !wait_warp(&x_bar[0], n_x & 1);
         tc_fence_after();
       }
-      if (!failed) finish_unit<HD>(p, items[slot], bad_sh, q_sm, tmem, ml_sh, m, l);
+      if (!failed) finish_unit<HD, kTree>(p, items[slot], bad_sh, q_sm, tmem, ml_sh, m, l);
       tc_fence_before();
       if (!wide) {
         // stream 1's O and ml_sh have been read
