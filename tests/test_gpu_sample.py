@@ -115,6 +115,14 @@ def test_large_vocabulary():
     check(case((1,) * 2, 1_000_003, "bf16", "flat", settings=[SETTINGS[i] for i in (1, 9)], seed=5), least_clear=0.5)
 
 
+@pytest.mark.parametrize("dtype,V", [("f32", 209001), ("f32", 300001), ("bf16", 278001), ("bf16", 600001)])
+def test_slices_with_and_without_their_noise(dtype, V):
+    """Vocabularies around the sizes up to which a slice and its noise, or the slice alone, fit in shared memory."""
+    ks = [(1.0, 0, 0.9, 0.0), (1.0, 0, 0.5, 0.02), (1.0, 5000, 0.9, 0.0), (1.0, 0, 0.01, 0.0)]
+    for kind in ("flat", "ties"):
+        check(case((1,) * 4, V, dtype, kind, settings=ks, seed=14), least_clear=0.5, pad=(1, 3))
+
+
 def test_ties_at_the_cut_go_to_the_lowest_index():
     """Many equal logits, noise that makes the last kept one win: the token shows the cut."""
     for V, k in ((1000, 700), (1000, 10), (60000, 30000), (201088, 7), (201088, 100003), (300, 299)):
