@@ -50,7 +50,6 @@ namespace {
 constexpr int kThreads = 256;         // row kernel (the cut kernel counts on 2^8)
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;            // 16-byte loads in flight per thread
-constexpr int kRaceUnroll = 2;        // ... where the noise is streamed too
 // of a row, per CTA (768 greedy bf16 rows of 201,088 74 us, 82 with 64 KB, 79 with 112; 384 fp32
 // ones of 151,936 60, 62 and 61)
 constexpr int kMaxPartBytes = 80 * 1024;
@@ -330,6 +329,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
     const float it = 1.f / st.temp;
     float bs = -INFINITY;
     int bv = -1;
+    // (16 tokens a thread and trip, as many as the registers hold: 512 fp32 rows of 201,088 164 us, 169
+    // with 8)
+    constexpr int kRaceUnroll = 16 / kVec;
     float g[kRaceUnroll][kVec];
     auto load_noise = [&](int j) {
 #pragma unroll
@@ -354,12 +356,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
           bs = fmaxf(bs, best);
           bv = j + x * kThreads;
         }
-        // the next trip's are on their way (the first two trips' logits were loaded above)
-        static_assert(kUnroll == 2 * kRaceUnroll, "");
-        u[x] = j == tid ? u[x + kRaceUnroll] : no_tokens<T>();
+        // the next trip's are on their way (the first kUnroll vectors of logits were loaded above)
+        constexpr bool kAbove = kUnroll > kRaceUnroll;
+        static_assert(kUnroll == kRaceUnroll || kUnroll == 2 * kRaceUnroll, "");
+        u[x] = kAbove && j == tid ? u[(x + kRaceUnroll) % kUnroll] : no_tokens<T>();
         const int jn = j + (x + kRaceUnroll) * kThreads;
         if (jn < n) {
-          if (j != tid) u[x] = s.load(v0 + jn);
+          if (!kAbove || j != tid) u[x] = s.load(v0 + jn);
           noise.load(s.token(v0 + jn), a.V, g[x]);
         }
       }
