@@ -650,7 +650,8 @@ int pe_cache_compact(const pe_attn_plan* plan, int n_layers, int B, int T, const
  *   top_k[B]    int32, nullable: the number of tokens kept; 0, negative or vocab and more: all
  *   top_p[B]    float, nullable: 1 and more: all; 0 and less: the first token; NaN: all,
  *               PE_ST_SAMPLING
- *   min_p[B]    float, nullable: 0 and less: all; NaN: all, PE_ST_SAMPLING
+ *   min_p[B]    float, nullable: 0 and less: all; above 1: the first token; NaN: all,
+ *               PE_ST_SAMPLING
  *   gumbel      [T][vocab] float standard Gumbel noise, rows ld_gumbel elements apart.  Only
  *               the noise of kept tokens is looked at
  *   token[T]    out

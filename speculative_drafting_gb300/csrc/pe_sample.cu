@@ -103,7 +103,7 @@ struct SampleArgs {
 };
 
 struct Settings {
-  float temp, p, mp;  // temperature (negative: a row of no request); top-p, 1: off; min-p, 0: off
+  float temp, p, mp;  // temperature (negative: a row of no request); top-p, 1: off; min-p, 0: off, at most 1
   int k;              // 0: off
 };
 PE_DEV Settings settings_of(const SampleArgs& a, int r, uint32_t& status) {
@@ -116,6 +116,11 @@ PE_DEV Settings settings_of(const SampleArgs& a, int r, uint32_t& status) {
   s.k = k <= 0 || k >= a.V ? 0 : k;
   s.p = p < 1.f ? p : 1.f;     // (NaN: 1)
   s.mp = mp > 0.f ? mp : 0.f;  // (NaN: 0)
+  if (s.mp > 1.f) {            // no weight reaches it: the first token, which is always kept
+    s.k = a.V > 1;
+    s.p = 1.f;
+    s.mp = 0.f;
+  }
   return s;
 }
 
@@ -711,7 +716,7 @@ __global__ void __launch_bounds__(32 * W, 32 / W) sample_cut_kernel(const Sample
     bound = logit_of(sh.bound);
   } else {
     // min-p alone: the logit that its weight stands for, a little less for the roundings
-    bound = fminf(M + (log2f(fminf(st.mp, 1.f)) * 1.00001f - 1e-5f) / c, M);
+    bound = fminf(M + (log2f(st.mp) * 1.00001f - 1e-5f) / c, M);
   }
   // ---------------- the groups that have a token from the bound on, and those tokens
   for (int i = tid; i < groups; i += kN)
