@@ -1460,7 +1460,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) sample_wide_kernel(const Samp
       // (the first token is kept whatever top_p is: nothing is before it)
       if (attempt == 0) most = max(share_of(st.p, all), 1ull);
       if (before < most) break;
-      cut = attempt == kTries ? find(most, true) : won + 1ull;
+      // (find adds up other roundings of the weights, of all tokens: no place behind the cut so far)
+      cut = won + 1ull;
+      if (attempt == kTries) cut = max(cut, find(most, true));
     }
     if (rank == 0 && tid == 0) {
       a.token[row] = won ? static_cast<int>(~static_cast<uint32_t>(won)) : -1;

@@ -33,3 +33,26 @@ def test_min_p_above_one_keeps_the_first_token(dtype, min_p):
     assert got.tolist() == [-1, 0] and st == binding.PE_ST_SAMPLING
     want = X.sample(c["qsl"], O.decode(c["logits"], dtype), c["temp"], c["k"], c["p"], c["m"], c["g"])[0]
     assert got.tolist() == want.tolist()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_no_more_than_top_k_where_top_p_is_almost_one(dtype):
+    """One token and 199,999 of 1.9 * 2^-40 of its weight, the first 100,000 kept by top_k, 65,000 or so of them by
+    top_p = 1 - 2^-24.  The noise lets tokens that top_p rejects win one after another, and is largest where top_k
+    has cut."""
+    V, k = 200000, 100000
+    x = np.full((3, V), np.float32(np.log(1.9) - 40 * np.log(2.0)))
+    x[:, 0] = 0.0
+    c = case((1, 1, 1), V, dtype, settings=[(1.0, k, float(np.float32(1 - 2.0 ** -24)), 0.0)] * 3)
+    c["logits"] = _bits(x, dtype)
+    c["g"][:] = 0.0
+    for row, n in enumerate((7, 8, 12)):        # as many winners that are rejected, the last ranks first
+        c["g"][row, k - 1 - np.arange(n)] = 200.0 - np.arange(n)
+        c["g"][row, 10] = 100.0
+        c["g"][row, k:] = 1000.0
+    got, st = run(c)
+    # The sum before any of the first k is in 1 + [0, 1e5 * 1.9 * 2^-40 = 1.73e-7], p of all is 1 + 1.73e-7 - 2^-24
+    # = 1 + 1.13e-7: all of them are within 1e-5 of the bound, so each may be kept.  Not those behind the k-th, and
+    # where as many winners as are raced for have been rejected, not those either.
+    assert st == 0 and (got < k).all()
+    assert got[0] == 10 and all(t == 10 or t < k - 7 for t in got)
