@@ -100,8 +100,9 @@ extern "C" {
 #define PE_ST_TOKEN_RANGE 0x4u    /* token id outside [0, V): embedding row 0 is used */
 #define PE_ST_ROWS_RANGE 0x8u     /* pe_verify_greedy: qsl is not a non-decreasing run
                                      from 0 to T_in (each request is clamped to
-                                     the rows in range); pe_verify_sampled and
-                                     pe_chunk_attention: from 0 to at most T;
+                                     the rows in range); pe_verify_sampled,
+                                     pe_chunk_attention, the tree calls and
+                                     pe_sample: from 0 to at most T;
                                      pe_draft_step with several layers: a request
                                      has more non-rejected rows than the layers
                                      carry */

@@ -259,7 +259,6 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
   __shared__ unsigned long long warp_k[kWarps];
   __shared__ int warp_i[kWarps];
   __shared__ Settings set_sh;
-  __shared__ int request_sh;
   __shared__ uint32_t status_sh;
   pdl_trigger();
   pdl_wait();
@@ -278,15 +277,17 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
       Settings x{-1.f, 1.f, 0.f, 0};
       if (r >= 0) x = settings_of(a, r, status);
       set_sh = x;
-      request_sh = r;
       status_sh = status;
     }
+  } else if (blockIdx.x == 0) {  // the offsets of every request, of those that no row is looked up in too
+    bool bad = false;
+    for (int r = tid - 32; r < a.B; r += kThreads - 32) bad |= request_rows(a.qsl, r, a.T).bad;
+    if (bad) set_status(a.status, PE_ST_ROWS_RANGE);
   }
   __syncthreads();
   const Settings st = set_sh;
   if (part == 0 && tid == 0) {
     a.set[row] = st;
-    if (request_sh >= 0 && request_rows(a.qsl, request_sh, a.T).bad) status_sh |= PE_ST_ROWS_RANGE;
     if (status_sh) set_status(a.status, status_sh);
     if (row == 0) *a.todo_n = 0u;
   }

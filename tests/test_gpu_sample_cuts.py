@@ -56,3 +56,24 @@ def test_no_more_than_top_k_where_top_p_is_almost_one(dtype):
     # where as many winners as are raced for have been rejected, not those either.
     assert st == 0 and (got < k).all()
     assert got[0] == 10 and all(t == 10 or t < k - 7 for t in got)
+
+
+@pytest.mark.parametrize("qsl,status", [((0, 2, 1, 4), True), ((0, 3, 3, 2, 5), True), ((1, 2), True), ((0, 0, 5), True),
+                                        ((0, 2, 2, 4), False), ((0, 0, 0, 0), False)])
+def test_bad_offsets_of_any_request_are_reported(qsl, status):
+    """Those of requests that no row is looked up in too."""
+    qsl = np.array(qsl, np.int32)
+    c = dict(case((1,) * (len(qsl) - 1), 300, "f32", settings=(1.0, 5, 0.9, 0.0)), qsl=qsl)
+    g = case((4,), 300, "f32")
+    c.update(logits=g["logits"], g=g["g"])
+    _, st = run(c)
+    assert st == (binding.PE_ST_ROWS_RANGE if status else 0)
+
+
+def test_bad_offsets_among_many_requests_are_reported():
+    B = 3000
+    qsl = np.concatenate([np.arange(B), [B]]).astype(np.int32)
+    c = dict(case((1,) * B, 40, "f32", settings=(1.0, 5, 0.9, 0.0)), qsl=qsl)
+    assert run(c)[1] == 0
+    qsl[1777] = B
+    assert run(c)[1] == binding.PE_ST_ROWS_RANGE
