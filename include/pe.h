@@ -691,7 +691,9 @@ int pe_sample(int B, int T, const int32_t* qsl, const void* logits, int64_t ld_l
  * captured loop may grow, share and drop requests.  Free pages are handed out in ascending order to the
  * entries of a call in order: the outcome does not depend on the run.
  *   ws          pe_pages_workspace_bytes(n, num_blocks) bytes or more, 256-byte aligned,
- *               zeroed once; its first word is the status word, which the calls do not clear
+ *               zeroed once; its first word is the status word, which the calls do not clear.
+ *               The workspace of other calls serves too, in turn: none of them writes to the
+ *               counter that the page calls keep in its first 256 bytes
  * An entry that is refused changes nothing and sets PE_ST_PAGES. */
 size_t pe_pages_workspace_bytes(int max_entries, int num_blocks);
 

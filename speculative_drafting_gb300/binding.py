@@ -650,7 +650,8 @@ def tree_accept(B, T, qsl, parent, tok, target, accepted, path, bonus, ws, strea
 
 
 def pages_workspace(max_entries: int, num_blocks: int, device="cuda"):
-    """A device workspace for the page calls (zeroed): at most max_entries entries a call."""
+    """A device workspace for the page calls (zeroed): at most max_entries entries a call.  Other
+    calls may use it in turn."""
     import torch
 
     n = int(load().pe_pages_workspace_bytes(int(max_entries), int(num_blocks)))

@@ -25,6 +25,10 @@ constexpr int kThreads = 256;
 constexpr int kScanThreads = 512;  // of the kernel that checks and lists
 constexpr int kMaxRow = 1 << 22;   // entries of a row of the table: kScanThreads rows' have an int's sum
 constexpr int kBatch = 8;          // 16-byte loads in flight per thread
+// The counter of finished CTAs: a place of its own among a workspace's first 256 bytes, where no other
+// call writes anything but zeros (0: the status word, 128: pe_sample's list length), so that one
+// workspace can serve several calls in turn.
+constexpr int kDone = 192;
 
 struct CacheArgs {
   int layers, num_blocks, G, bs;
@@ -228,7 +232,8 @@ struct PoolArgs {
   int32_t* table;
   int32_t* refs;
   uint32_t* status;
-  uint32_t* done;   // CTAs of the checking kernel that finished; 0 between calls
+  uint32_t* done;   // CTAs of the checking kernel that finished; 0 between calls (the last CTA leaves it
+                    // so, and the second kernel, whatever stood there before)
   int32_t* need;    // [n] pages that entry i needs, -1: it is refused
   int32_t* start;   // [n] its first one in list
   int32_t* list;    // [num_blocks] free pages
@@ -355,6 +360,7 @@ __global__ void __launch_bounds__(kScanThreads) reserve_fill_kernel(const PoolAr
   pdl_trigger();
   pdl_wait();
   const int i = blockIdx.x, tid = threadIdx.x;
+  if (i == 0 && tid == 0) *a.done = 0u;
   if (a.need[i] <= 0) return;
   const int e = entries_of(a, a.length[i]);
   int32_t* row = a.table + static_cast<int64_t>(a.row[i]) * a.max_blocks;
@@ -410,6 +416,7 @@ __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const PoolArgs a, 
   pdl_trigger();
   pdl_wait();
   const int i = blockIdx.y, tid = threadIdx.x;
+  if (i == 0 && blockIdx.x == 0 && tid == 0) *a.done = 0u;
   const int need = a.need[i];
   if (need < 0) return;
   const int len = a.length[i], full = len / a.bs, part = len % a.bs;
@@ -515,7 +522,7 @@ int pool_args(PoolArgs& a, int n, const int32_t* row, int rows, const int32_t* l
   a.refs = refs;
   char* w = static_cast<char*>(ws);
   a.status = reinterpret_cast<uint32_t*>(w);
-  a.done = reinterpret_cast<uint32_t*>(w + 128);
+  a.done = reinterpret_cast<uint32_t*>(w + kDone);
   w += 256;
   a.need = reinterpret_cast<int32_t*>(w);
   w += al256(n * sizeof(int32_t));
