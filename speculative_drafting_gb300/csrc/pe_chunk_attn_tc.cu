@@ -1385,15 +1385,20 @@ int launch(const Args<kTree>& p, const CUtensorMap& km, const CUtensorMap& vm, c
   if (launch_chained(chunk_tc_kernel<HD, kTree>, dim3(p.grid), dim3(kThreads), Shape<HD>::kSmem, st, km, vm, p) !=
       cudaSuccess)
     return PE_ERR_CUDA;
-  // Rows of a unit per warp of the join (it notes them in 32 bits): one where a unit has few
-  // (one token 18.6 -> 16.9 us); else the fewer rows there are in all, the fewer for each, whose
-  // reads wait for one another (16 nodes of one request over 2048 keys: 37.1 us with eight, 29.8
-  // with four, 27.1 with two, 27.5 with one; 8 x 16 nodes 41.8, 40.4, 41.3, 44.7; 64 x 8 rows
-  // 113, 114, 130, 121; graph replays).
+  // Rows of a unit per warp of the join (it notes them in 32 bits).  A warp's rows wait for one another; with
+  // fewer for each the grid has as many more CTAs, most of which find no cut unit.  So 8 CTAs of 4 warps to
+  // a unit of as many rows as one can have (one token 18.6 -> 16.9 us beside eight rows a warp), and more where
+  // few units can be cut: in calls of up to 8192 rows and 64 pairs of a request and a KV head four rows a warp,
+  // two for up to four requests or where a mean request has full units.  Graph replays with eight, four and two
+  // over 2048 keys: 64 query heads and 8 KV heads of 64, 1 x 8 rows 29.0 us, 22.7, 19.1; 4 x 16 30.5, 27.7, 27.8; 8 x
+  // 16 31.6, 30.2, 31.2; 64 x 1 61.5, 62.4, 65.3; 32 query heads and 4 KV heads of 128, 8 x 16 35.5, 32.6, 32.8; 64 x 1
+  // 55.0, 55.3, 57.8; 16 heads of 64 to query and KV, 64 x 1 110, 109, 106 (8 CTAs with two).
   const int rows = static_cast<int>(
       std::min<long long>(static_cast<long long>(p.c.T) * (p.c.H / p.c.G), p.part_rows));
-  const long long all = static_cast<long long>(p.c.T) * p.c.H;
-  const int per_warp = rows <= 32 ? 1 : all <= 4096 ? 2 : all <= 8192 ? 4 : 8;
+  const long long all = static_cast<long long>(p.c.T) * p.c.H, pairs = static_cast<long long>(p.c.B) * p.c.G;
+  int per_warp = rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 ? 4 : 8;
+  if (all <= 8192 && pairs <= 64)
+    per_warp = std::min(per_warp, (p.c.B <= 4 && pairs <= 32) || all / pairs >= kUnitRows ? 2 : 4);
   const int join = (rows + 4 * per_warp - 1) / (4 * per_warp);
   return launch_chained(chunk_join_kernel<HD, kTree>, dim3(p.grid, join), dim3(128), 0, st, p) == cudaSuccess
              ? PE_OK
