@@ -264,3 +264,57 @@ def sample(qsl, logits, temperature, top_k, top_p, min_p, gumbel):
                     for f in (1 - 2e-5, 1 + 2e-5) for g in (1 - 2e-5, 1 + 2e-5)] if p < 1 or 0 < m < 1 else []
             clear[row] = lead > 1e-4 and all(x == tok for x in near)
     return token, clear
+
+
+def _sample_holds(x, temp, k, p, min_p, g, tok):
+    """Whether a row's token may stand: it may be kept if the bounds of the weights move by 2e-5 of their size,
+    and no token that is kept wherever they lie has a score ahead of its by more than the fp32 forms of the two are
+    off: 1e-6 of their terms (a quotient and a sum, up to ten rescalings of a running score, 2^-24 each)."""
+    V = len(x)
+    top = x.max()
+    if temp == 0 or not np.isfinite(top):
+        return tok == _sample_row(x, temp, k, p, min_p, g)[0]
+    order = np.lexsort((np.arange(V), -x))
+    w = np.exp((x[order] - top) / temp)
+    first = np.arange(V) == 0
+    m = k if 0 < k < V else V
+    before = np.concatenate([[0.0], np.cumsum(w[:m])[:-1], np.full(V - m, np.inf)])
+
+    def kept(by):
+        keep = (np.arange(V) < m) & ~np.isneginf(x[order])
+        if p < 1:
+            keep &= (before < p * by * w[:m].sum()) | first
+        if min_p > 0:
+            keep &= (w >= (min_p / by if min_p <= 1 else min_p)) | first
+        return keep
+
+    with np.errstate(invalid="ignore"):
+        term, noise = (x[order] - top) / temp, g[order].astype(np.float64)
+        score = np.where(np.isneginf(term) | np.isnan(noise), -np.inf, term + noise)
+        off = np.where(np.isfinite(score), 1e-6 * (np.abs(term) + np.abs(noise)), 0.0)
+    low = np.where(kept(1 - 2e-5), score - off, -np.inf)
+    if tok == -1:
+        return bool(np.isneginf(low).all())
+    if not 0 <= tok < V:
+        return False
+    at = int(np.flatnonzero(order == tok)[0])
+    if not kept(1 + 2e-5)[at] or np.isneginf(score[at]):
+        return False
+    return bool(score[at] + off[at] >= low.max())
+
+
+def sample_holds(qsl, logits, temperature, top_k, top_p, min_p, gumbel, token):
+    """Of each row of a request: whether its token is one of those that the formulas allow (_sample_holds).
+    Rows of no request: whether it is -7."""
+    logits = np.asarray(logits, dtype=np.float64)
+    ok = np.asarray(token) == -7
+    for r in range(len(qsl) - 1):
+        t = 1.0 if temperature is None else float(temperature[r])
+        t = min(max(t, 1e-30), 1e30) if t > 0 else 0.0
+        k = 0 if top_k is None else int(top_k[r])
+        p = 1.0 if top_p is None else float(top_p[r])
+        m = 0.0 if min_p is None else float(min_p[r])
+        p, m = 1.0 if np.isnan(p) else p, 0.0 if np.isnan(m) else m
+        for row in range(int(qsl[r]), int(qsl[r + 1])):
+            ok[row] = _sample_holds(logits[row], t, k, p, m, gumbel[row], int(token[row]))
+    return ok
