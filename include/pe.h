@@ -669,7 +669,10 @@ int pe_cache_compact(const pe_attn_plan* plan, int n_layers, int B, int T, const
  * index on ties: a draw from the kept tokens' probabilities.  Temperature 0: the largest
  * logit's, by pe_verify_greedy's rules.  Sums and weights are formed in fp32 or more: a
  * token whose sum before it, or w, is within 1e-5 of the bound may fall on either side;
- * two scores within a few fp32 roundings may trade places.
+ * two scores within a few fp32 roundings may trade places, which then may differ between
+ * batches of other sizes.  A score below fp32's range counts as -inf (that of a logit of the
+ * type's lowest value at a temperature below 1, say); a token whose logit is farther from
+ * the largest than fp32's range may count as one of -inf.
  * A logit of -inf is never kept.  A row with a NaN or +inf logit, with nothing but -inf, or
  * whose kept tokens all have noise of -inf or NaN gets token -1 and PE_ST_SAMPLING (at
  * temperature 0 pe_verify_greedy's rules hold for such rows).  Rows from qsl[B] on are neither

@@ -213,6 +213,9 @@ class Pool:
             self.table[row] = -1
 
 
+FP32_MAX = float(np.finfo(np.float32).max)
+
+
 def _sample_row(x, temp, k, p, min_p, g):
     """(token, lead) of one row: the score's lead over the next kept token's."""
     V = len(x)
@@ -233,7 +236,7 @@ def _sample_row(x, temp, k, p, min_p, g):
     keep &= ~np.isneginf(x[order])
     with np.errstate(invalid="ignore"):
         s = np.where(keep, (x[order] - top) / temp + np.where(keep, g[order].astype(np.float64), 0.0), -np.inf)
-    s[np.isnan(s)] = -np.inf
+    s[np.isnan(s) | (s < -FP32_MAX)] = -np.inf
     if np.isneginf(s).all():
         return -1, np.inf
     best = s.max()
@@ -291,8 +294,10 @@ def _sample_holds(x, temp, k, p, min_p, g, tok):
     with np.errstate(invalid="ignore"):
         term, noise = (x[order] - top) / temp, g[order].astype(np.float64)
         score = np.where(np.isneginf(term) | np.isnan(noise), -np.inf, term + noise)
+        score[score < -FP32_MAX] = -np.inf
+        sure = x[order] - top > -FP32_MAX
         off = np.where(np.isfinite(score), 1e-6 * (np.abs(term) + np.abs(noise)), 0.0)
-    low = np.where(kept(1 - 2e-5), score - off, -np.inf)
+    low = np.where(kept(1 - 2e-5) & sure, score - off, -np.inf)
     if tok == -1:
         return bool(np.isneginf(low).all())
     if not 0 <= tok < V:

@@ -38,6 +38,7 @@
 // and in 64 bits only where two are near: a comparison in doubles takes 5000 clocks.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -376,8 +377,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
     out.m = cta_max<kWarps>(m, warp_m);
     // The threads whose best is within reach of the CTA's: if there is more than one token, they
     // compare in 64 bits (which is slow: the one that there mostly is does without).
-    const float far = m == out.m ? 0.f : (m - out.m) * it;
-    if (bs < INFINITY) bs += far;
+    // (`far` finite, so that infinite noise stays)
+    const float far = m == out.m ? 0.f : fmaxf((m - out.m) * it, -FLT_MAX);
+    bs += far;
     float top = warp_max(bs);
     __syncthreads();
     if (lane == 0) warp_m[warp] = top;
@@ -589,7 +591,7 @@ __global__ void __launch_bounds__(32 * W, 32 / W) sample_cut_kernel(const Sample
     int near = 0;
 #pragma unroll
     for (int x = 0; x < kE; ++x) {
-      score[x] = there[x] ? fmaf(l[x] - M, 1.f / st.temp, g[x]) : -INFINITY;
+      score[x] = !there[x] ? -INFINITY : g[x] < INFINITY ? fmaf(l[x] - M, 1.f / st.temp, g[x]) : g[x];
       top = fmaxf(top, score[x]);
     }
     top = cta_max<W>(top, sh.m);

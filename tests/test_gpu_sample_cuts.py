@@ -77,3 +77,35 @@ def test_bad_offsets_among_many_requests_are_reported():
     assert run(c)[1] == 0
     qsl[1777] = B
     assert run(c)[1] == binding.PE_ST_ROWS_RANGE
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [40, 3000, 201088])
+def test_logits_of_the_lowest_value(dtype, V):
+    """Tokens masked by the type's lowest value: quotients by temperatures below 1 are past fp32's range."""
+    low = {"f32": np.finfo(np.float32).max, "bf16": np.float32(2.0 ** 127 * (2 - 2.0 ** -7))}[dtype]
+    cuts = [(0, 1.0), (V - 1, 1.0), (5, 1.0), (0, 0.9)]
+    some = np.unique(np.array([1, 2, V // 3, V // 2, V - 2]))
+    for temp in (0.7, 1.0, 1e-30, 3.0):
+        c = case((1,) * len(cuts), V, dtype, "equal", seed=V, settings=[(temp, k, p, 0.0) for k, p in cuts])
+        x = np.full((len(cuts), V), -low, np.float64)
+        x[:, some] = np.arange(len(some)) * 1e-3
+        c["logits"] = _bits(x, dtype)
+        x = O.decode(c["logits"], dtype)
+        got, st = run(c)
+        assert st == 0 and X.sample_holds(c["qsl"], x, c["temp"], c["k"], c["p"], c["m"], c["g"], got).all()
+        assert np.isin(got, some).all()
+        # infinite noise wins where the token is kept: at the lowest index
+        c["g"][:, [0, 7, V - 1]] = np.inf
+        got, st = run(c)
+        assert st == 0 and got[:2].tolist() == [0, 0]
+        assert X.sample_holds(c["qsl"], x, c["temp"], c["k"], c["p"], c["m"], c["g"], got).all()
+        # nothing but lowest values can win
+        c["g"][:, [0, 7, V - 1]] = 0.0
+        c["g"][:, some] = -np.inf
+        got, st = run(c)
+        if temp < 1.0:
+            assert got[:2].tolist() == [-1, -1] and st == binding.PE_ST_SAMPLING
+        else:
+            assert got[:2].tolist() == [0, 0]   # (scores of the same 64-bit number)
+        assert X.sample_holds(c["qsl"], x, c["temp"], c["k"], c["p"], c["m"], c["g"], got).all()
