@@ -109,3 +109,21 @@ def test_logits_of_the_lowest_value(dtype, V):
         else:
             assert got[:2].tolist() == [0, 0]   # (scores of the same 64-bit number)
         assert X.sample_holds(c["qsl"], x, c["temp"], c["k"], c["p"], c["m"], c["g"], got).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [400, 3000, 201088])
+def test_infinite_noise_among_logits_of_the_lowest_value(dtype, V):
+    """A masked token that its noise lets win, away from the tokens that are not masked: no thread that holds it has
+    another logit, and its distance to the largest is past fp32's range."""
+    low = {"f32": np.finfo(np.float32).max, "bf16": np.float32(2.0 ** 127 * (2 - 2.0 ** -7))}[dtype]
+    at = V // 5
+    for temp in (0.7, 1e-30, 1.0):
+        c = case((1, 1, 1), V, dtype, "equal", seed=V, settings=[(temp, 0, 1.0, 0.0), (temp, V - 1, 1.0, 0.0), (temp, 5, 1.0, 0.0)])
+        x = np.full((3, V), -low, np.float64)
+        x[:, [V - 9, V - 1]] = 1.0
+        c["logits"] = _bits(x, dtype)
+        c["g"][:, at] = np.inf
+        got, st = run(c)
+        # (five tokens: the two and the first three masked ones)
+        assert st == 0 and got[:2].tolist() == [at, at] and got[2] in (V - 9, V - 1, 0, 1, 2)
