@@ -50,6 +50,7 @@ namespace {
 
 constexpr int kThreads = 256;         // row kernel (the cut kernel counts on 2^8)
 constexpr int kWarps = kThreads / 32;
+constexpr int kChecked = kThreads - 32;  // requests whose offsets a CTA of the row kernel checks at a time
 constexpr int kUnroll = 4;            // 16-byte loads in flight per thread
 // of a row, per CTA (768 greedy bf16 rows of 201,088 74 us, 82 with 64 KB, 79 with 112; 384 fp32
 // ones of 151,936 60, 62 and 61)
@@ -105,6 +106,7 @@ struct SampleArgs {
   int32_t* todo;     // [T]
   int resident;      // the wide kernel's slices fit in shared memory
   int near;          // ... beside their noise
+  int checks, checked;  // CTAs of the row kernel that look at the requests' offsets, requests of each
 };
 
 struct Settings {
@@ -284,9 +286,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_row_kernel(const SampleArg
       set_sh = x;
       status_sh = status;
     }
-  } else if (blockIdx.x == 0) {  // the offsets of every request, of those that no row is looked up in too
+  } else if (blockIdx.x < a.checks) {  // the offsets of every request, of those that no row is looked up in too
     bool bad = false;
-    for (int r = tid - 32; r < a.B; r += kThreads - 32) bad |= request_rows(a.qsl, r, a.T).bad;
+    const int r0 = static_cast<int>(blockIdx.x) * a.checked, r1 = min(r0 + a.checked, a.B);
+    for (int r = r0 + tid - 32; r < r1; r += kChecked) bad |= request_rows(a.qsl, r, a.T).bad;
     if (bad) set_status(a.status, PE_ST_ROWS_RANGE);
   }
   __syncthreads();
@@ -1606,6 +1609,8 @@ extern "C" int pe_sample(int B, int T, const int32_t* qsl, const void* logits, i
   a.token = token;
   plan(a, esize, sms);
   if (static_cast<int64_t>(T) * a.parts > 0x7fffffff) return PE_ERR_UNSUPPORTED;
+  a.checked = std::max(kChecked, (B - 1) / (T * a.parts) + 1);
+  a.checks = (B + a.checked - 1) / a.checked;
   a.resident = slice_vectors(vocab, esize) * 16 <= kSlice;
   a.near = slice_vectors(vocab, esize) * (16 + 64 / esize) <= kSlice;
   char* w = static_cast<char*>(ws);

@@ -127,3 +127,18 @@ def test_infinite_noise_among_logits_of_the_lowest_value(dtype, V):
         got, st = run(c)
         # (five tokens: the two and the first three masked ones)
         assert st == 0 and got[:2].tolist() == [at, at] and got[2] in (V - 9, V - 1, 0, 1, 2)
+
+
+@pytest.mark.parametrize("V,T", [(40, 1), (40, 3), (9001, 3)])
+def test_bad_offsets_among_more_requests_than_rows_are_reported(V, T):
+    B = 65535
+    qsl = np.minimum(np.arange(B + 1), T).astype(np.int32)
+    g = case((T,), V, "f32")
+    one = lambda v, ty: np.full(B, v, ty)  # noqa: E731
+    c = dict(qsl=qsl, dtype="f32", V=V, logits=g["logits"], g=g["g"], temp=one(1.0, np.float32), k=one(5, np.int32),
+             p=one(0.9, np.float32), m=one(0.0, np.float32))
+    assert run(c)[1] == 0
+    for at in (5, 300, 40000, B - 1):
+        c["qsl"] = qsl.copy()
+        c["qsl"][at] = T + 1
+        assert run(c)[1] == binding.PE_ST_ROWS_RANGE, at
