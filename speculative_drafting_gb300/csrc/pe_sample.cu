@@ -65,10 +65,10 @@ constexpr int kWideThreads = 512;     // wide kernel
 constexpr int kWideWarps = kWideThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kBins = 1024;           // two per thread
-// Races of a top-p row that may be lost before its cut is looked for.  Each lost one leaves the weight before the
-// winner, half of the rest on average, so that top_p = 0.1 is reached in some three (512 flat bf16 rows of
-// 201,088: 2390 us with 1, 1491 with 4, 1367 with 6, 1327 with 12; top_p = 0.5 1170, 799, 787, 786; 0.9 606 with any).
-// Only for top_p near 0.01 is looking for it at once faster (1527 us with 0, 1946 with 6).
+// The cut of a top-p row is looked for once kTries + 1 races are lost.  Each lost one leaves the weight before its
+// winner, half of the rest on average, so top_p = 0.1 is reached in some three (512 flat bf16 rows of 201,088:
+// 2390 us with kTries = 1, 1491 with 4, 1367 with 6, 1327 with 12; top_p = 0.5 1170, 799, 787, 786; 0.9 606 with
+// any).  Near top_p = 0.01 alone fewer are faster (1527 us with 0, 1946 with 6).
 constexpr int kTries = 6;
 
 // What a CTA of the row kernel leaves of its part.
